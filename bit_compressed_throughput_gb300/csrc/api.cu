@@ -15,6 +15,7 @@
 
 #include "../../include/fg.h"
 #include "fg_internal.h"
+#include "ragged.cuh"
 
 namespace fg {
 namespace {
@@ -30,6 +31,7 @@ int set_cuda_error(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // ---------------------------------------------------------------- device facts
 struct DevInfo {
@@ -433,10 +435,20 @@ int fg_check_device_error(void* stream) {
   flag |= sflag;
   e = attn_read_error(&aflag);
   if (e != cudaSuccess) return set_cuda_error(e);
+  unsigned int wflag = 0;              // kernels that check extents on the device
+  for (auto* read : {ragged_read_error, decode_window_read_error, prefill_window_read_error}) {
+    if ((e = read(&sflag)) != cudaSuccess) return set_cuda_error(e);
+    wflag |= sflag;
+  }
+  flag |= wflag & ~kErrExtent;
   if (flag || aflag) {
     t_last_error = "bounded device wait timed out (GEMM flag " + std::to_string(flag) +
                    ", decode attention flag " + std::to_string(aflag) + ")";
     return FG_ERR_TIMEOUT;
+  }
+  if (wflag & kErrExtent) {
+    t_last_error = "a length, position or row offset in a device array does not fit its buffers";
+    return FG_ERR_CAPACITY;
   }
   return FG_OK;
 }
@@ -558,6 +570,53 @@ int fg_kv_append_q4(const uint16_t* k_new, const uint16_t* v_new, int64_t row_st
   return run_kv_append(k_new, v_new, row_stride, T, pos, *kv, static_cast<cudaStream_t>(stream));
 }
 
+// Arguments shared by the two ragged cache calls; *nothing_to_do when there are no rows.
+static int check_ragged(const fg_kvcache* kv, int64_t row_stride, int32_t rows,
+                        const int32_t* row_off, const int32_t* pos, bool* nothing_to_do) {
+  *nothing_to_do = false;
+  int rc = check_kv(kv);
+  if (rc) return rc;
+  if (rows < 0 || row_stride < kv->h || row_stride % 8 != 0) return FG_ERR_SHAPE;
+  if (rows == 0 || kv->B == 0) {
+    *nothing_to_do = true;
+    return FG_OK;
+  }
+  if (!row_off || !pos || !aligned4(row_off) || !aligned4(pos)) return FG_ERR_ARG;
+  return FG_OK;
+}
+
+int fg_kv_append_q4_ragged(const uint16_t* k_new, const uint16_t* v_new, int64_t row_stride,
+                           int32_t rows, const int32_t* row_off, const int32_t* pos,
+                           const fg_kvcache* kv, void* stream) {
+  bool noop = false;
+  int rc = check_ragged(kv, row_stride, rows, row_off, pos, &noop);
+  if (rc || noop) return rc;
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return FG_ERR_ARG;
+  if ((rc = check_device(nullptr))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  cudaError_t e = launch_kv_append_ragged(k_new, v_new, row_stride, rows, row_off, pos, *kv, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_KV_APPEND, work_quantize(2.0 * rows * kv->h));
+  return FG_OK;
+}
+
+int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int32_t* pos,
+                         int32_t rows, uint16_t* k_out, uint16_t* v_out, int64_t row_stride,
+                         void* stream) {
+  bool noop = false;
+  int rc = check_ragged(kv, row_stride, rows, row_off, pos, &noop);
+  if (rc || noop) return rc;
+  if ((!k_out && !v_out) || !aligned16(k_out) || !aligned16(v_out)) return FG_ERR_ARG;
+  if ((rc = check_device(nullptr))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  cudaError_t e = launch_kv_read_ragged(*kv, row_off, pos, rows, k_out, v_out, row_stride, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_KV_READ, work_dequant((double)((k_out != nullptr) + (v_out != nullptr)) * rows * kv->h));
+  return FG_OK;
+}
+
 size_t fg_decode_attn_workspace_bytes(const fg_kvcache* kv, int32_t len) {
   if (!kv || check_kv(kv) != FG_OK || len <= 0) return 0;
   return decode_attn_ws_bytes(*kv, len, kMaxSms);
@@ -618,6 +677,76 @@ int fg_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, int32_t H, int
   int rc = check_device(&sms);
   if (rc) return rc;
   return run_prefill_attn(qkv, nseq, s, H, d, scale, out, sms, static_cast<cudaStream_t>(stream));
+}
+
+// Window, sinks and scale of the windowed calls.
+static int check_window(int32_t window, int32_t sinks, float scale) {
+  if (window < 0 || sinks < 0) return FG_ERR_SHAPE;
+  if (!(scale > 0.0f) || !isfinite(scale)) return FG_ERR_ARG;
+  return FG_OK;
+}
+
+size_t fg_decode_attn_window_workspace_bytes(const fg_kvcache* kv, int32_t Hq) {
+  if (check_kv(kv) != FG_OK || Hq <= 0 || Hq % kv->H != 0 || kv->B == 0) return 0;
+  return decode_attn_window_ws_bytes(*kv, Hq);
+}
+
+int fg_decode_attn_q4kv_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
+                               const fg_kvcache* kv, const int32_t* lens, int32_t window,
+                               int32_t sinks, float scale, uint16_t* out, int64_t out_stride,
+                               void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_kv(kv);
+  if (rc || (rc = check_window(window, sinks, scale))) return rc;
+  const int64_t width = (int64_t)Hq * (kv->h / kv->H);
+  if (Hq <= 0 || Hq % kv->H != 0 || q_stride < width || q_stride % 8 != 0 || out_stride < width ||
+      out_stride % 8 != 0 || (int64_t)kv->B * Hq > (1ll << 31) - 1)
+    return FG_ERR_SHAPE;
+  if (kv->B == 0) return FG_OK;
+  if (!q || !out || !lens || !aligned16(q) || !aligned16(out) || !aligned4(lens)) return FG_ERR_ARG;
+  const size_t need = fg_decode_attn_window_workspace_bytes(kv, Hq);
+  if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return FG_ERR_WORKSPACE;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  cudaError_t e = launch_decode_attn_window(q, q_stride, Hq, *kv, lens, window, sinks, scale, out,
+                                            out_stride, ws, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_DECODE_ATTN_WINDOW,
+          2.0 * kv->B * kv->cap * kv->h * 0.5625 + 4.0 * kv->B * width);
+  return FG_OK;
+}
+
+int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,
+                           const int32_t* q_off, const uint16_t* k, const uint16_t* v,
+                           int64_t kv_stride, int32_t kv_rows, const int32_t* kv_off, int32_t nseq,
+                           int32_t Hq, int32_t Hkv, int32_t d, int32_t window, int32_t sinks,
+                           float scale, uint16_t* out, int64_t out_stride, void* stream) {
+  int rc = check_window(window, sinks, scale);
+  if (rc) return rc;
+  if (nseq < 0 || q_rows < 0 || kv_rows < 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 ||
+      (d != 64 && d != 128))
+    return FG_ERR_SHAPE;
+  const int64_t wq = (int64_t)Hq * d, wk = (int64_t)Hkv * d;
+  if (wq > (1 << 30) || q_stride < wq || q_stride % 8 != 0 || out_stride < wq ||
+      out_stride % 8 != 0 || kv_stride < wk || kv_stride % 8 != 0)
+    return FG_ERR_SHAPE;
+  if (nseq == 0 || q_rows == 0) return FG_OK;
+  if (!q || !out || !q_off || !kv_off || !aligned16(q) || !aligned16(out) || !aligned4(q_off) ||
+      !aligned4(kv_off))
+    return FG_ERR_ARG;
+  if (kv_rows > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return FG_ERR_ARG;
+  if (out == q || out == k || out == v) return FG_ERR_ARG;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  const PrefillWindow a{q,      k,       v,    out, q_off, kv_off, q_stride, kv_stride, out_stride,
+                        q_rows, kv_rows, nseq, Hq,  Hkv,   window, sinks,    scale};
+  cudaError_t e = launch_prefill_attn_window(a, d, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_PREFILL_ATTN_WINDOW, 4.0 * q_rows * wq + 4.0 * kv_rows * wk);
+  return FG_OK;
 }
 
 int fg_layernorm(const uint16_t* x, int64_t rows, int32_t h, const uint16_t* gamma,
@@ -814,7 +943,7 @@ const char* fg_kernel_name(int kind) {
       "q4g64_quantize", "q4g64_dequant", "q4_dequant_gemm_tc", "gemm_splitk_reduce",
       "q4kv_append", "q4kv_decode_attn", "decode_attn_combine", "prefill_attn",
       "layernorm", "q4_dequant_gemm_stream", "q4kv_decode_attn_topk", "q4_dequant_gemm_pair",
-      "gemm_f16w_pair"};
+      "gemm_f16w_pair", "q4kv_read", "q4kv_decode_attn_window", "prefill_attn_window"};
   return (kind >= 0 && kind < FG_K_COUNT) ? names[kind] : "unknown";
 }
 

@@ -30,6 +30,34 @@ cudaError_t launch_layernorm(const uint16_t* x, int64_t rows, int32_t h, const u
 cudaError_t launch_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, int32_t H,
                                 int32_t d, float scale, uint16_t* out, int nsm, cudaStream_t st);
 
+// Ragged append and read-back (kv_ragged.cu): rows row_off[b] .. row_off[b+1]-1 are positions
+// pos[b] .. of sequence b.
+cudaError_t launch_kv_append_ragged(const uint16_t* k_new, const uint16_t* v_new,
+                                    int64_t row_stride, int32_t rows, const int32_t* row_off,
+                                    const int32_t* pos, const fg_kvcache& kv, cudaStream_t st);
+cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, const int32_t* pos,
+                                  int32_t rows, uint16_t* k_out, uint16_t* v_out,
+                                  int64_t row_stride, cudaStream_t st);
+
+// Windowed decode attention (attn_decode_window.cu): workspace bytes for any lengths and any SM
+// count up to kMaxSms.
+size_t decode_attn_window_ws_bytes(const fg_kvcache& kv, int32_t Hq);
+cudaError_t launch_decode_attn_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
+                                      const fg_kvcache& kv, const int32_t* lens, int32_t window,
+                                      int32_t sinks, float scale, uint16_t* out,
+                                      int64_t out_stride, void* ws, int nsm, cudaStream_t st);
+
+// Windowed prefill attention (attn_prefill_window.cu).
+struct PrefillWindow {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  const int32_t *q_off, *kv_off;
+  int64_t q_stride, kv_stride, out_stride;
+  int32_t q_rows, kv_rows, nseq, Hq, Hkv, window, sinks;
+  float scale;
+};
+cudaError_t launch_prefill_attn_window(const PrefillWindow& a, int d, int nsm, cudaStream_t st);
+
 // Launch with programmatic stream serialisation (see pdl_wait in fg_common.cuh).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
@@ -146,6 +174,11 @@ cudaError_t gemm_stream_read_error(unsigned int* out);
 cudaError_t gemm_pair_read_error(unsigned int* out);
 cudaError_t prefill_read_error(unsigned int* out);
 cudaError_t attn_read_error(unsigned int* out);
+// The same for the kernels that read extents from device arrays (bit kErrExtent of ragged.cuh:
+// an extent that does not fit its buffers).
+cudaError_t ragged_read_error(unsigned int* out);
+cudaError_t decode_window_read_error(unsigned int* out);
+cudaError_t prefill_window_read_error(unsigned int* out);
 
 // Algorithmic work of one launch (bytes for memory-bound kernels, flops for the GEMM and
 // prefill attention): 4-bit storage costs 0.5 byte per element plus one (a, b) fp16 pair

@@ -25,10 +25,10 @@ FG_EPI_NONE, FG_EPI_RELU, FG_EPI_RESIDUAL = 0, 1, 2
 KINDS = ["q4g64_quantize", "q4g64_dequant", "q4_dequant_gemm_tc", "gemm_splitk_reduce",
          "q4kv_append", "q4kv_decode_attn", "decode_attn_combine", "prefill_attn", "layernorm",
          "q4_dequant_gemm_stream", "q4kv_decode_attn_topk", "q4_dequant_gemm_pair",
-         "gemm_f16w_pair"]
+         "gemm_f16w_pair", "q4kv_read", "q4kv_decode_attn_window", "prefill_attn_window"]
 K_QUANT, K_DEQUANT, K_GEMM, K_GEMM_REDUCE, K_KV_APPEND, K_DECODE_ATTN, K_DECODE_COMBINE, \
     K_PREFILL_ATTN, K_LAYERNORM, K_GEMM_STREAM, K_DECODE_ATTN_TOPK, K_GEMM_PAIR, \
-    K_GEMM_PAIR_F16W = range(13)
+    K_GEMM_PAIR_F16W, K_KV_READ, K_DECODE_ATTN_WINDOW, K_PREFILL_ATTN_WINDOW = range(16)
 
 
 class fg_q4mat(C.Structure):
@@ -73,6 +73,13 @@ _SIGS = {
                                   _SZ, _P], C.c_int),
     "fg_decode_attn_topk_workspace_bytes": ([C.POINTER(fg_kvcache), _I32], _SZ),
     "fg_prefill_attn": ([_P, _I32, _I32, _I32, _I32, _F, _P, _P], C.c_int),
+    "fg_kv_append_q4_ragged": ([_P, _P, _I64, _I32, _P, _P, C.POINTER(fg_kvcache), _P], C.c_int),
+    "fg_kv_read_q4_ragged": ([C.POINTER(fg_kvcache), _P, _P, _I32, _P, _P, _I64, _P], C.c_int),
+    "fg_decode_attn_q4kv_window": ([_P, _I64, _I32, C.POINTER(fg_kvcache), _P, _I32, _I32, _F, _P,
+                                    _I64, _P, _SZ, _P], C.c_int),
+    "fg_decode_attn_window_workspace_bytes": ([C.POINTER(fg_kvcache), _I32], _SZ),
+    "fg_prefill_attn_window": ([_P, _I64, _I32, _P, _P, _P, _I64, _I32, _P, _I32, _I32, _I32, _I32,
+                                _I32, _I32, _F, _P, _I64, _P], C.c_int),
     "fg_layernorm": ([_P, _I64, _I32, _P, _P, _F, _P, _P], C.c_int),
     "fg_layer_prefill": ([C.POINTER(fg_dims), C.POINTER(fg_layer), C.POINTER(fg_kvcache), _P, _P,
                           _I32, _I32, _I32, _P, _SZ, _P], C.c_int),
@@ -300,6 +307,118 @@ def fg_decode_attn_q4kv_static(q, q_stride: int, cache: KVCacheQ4, length: int, 
 def fg_prefill_attn(qkv, nseq: int, s: int, H: int, d: int, scale: float, out, stream=None):
     _check("fg_prefill_attn", lib.fg_prefill_attn(_ptr(qkv), nseq, s, H, d, scale, _ptr(out),
                                                   _stream(stream)))
+
+
+# The ragged calls take their row counts and strides from the tensors, and the kernels rely on
+# them, so these are checked here (ValueError) before they become bare pointers.
+
+
+def _rows(name: str, t, width: int):
+    """(rows, row stride) of a 2-D fp16 tensor of rows of `width` contiguous values."""
+    import torch
+    if t.dim() != 2 or t.dtype != torch.float16 or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{name}: fp16 [rows][{width}] with contiguous rows expected, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    # the stride of a dimension of one row (or none) is arbitrary and never used
+    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8)
+
+
+def _extents(name: str, t, n: int):
+    import torch
+    if t.dim() != 1 or t.dtype != torch.int32 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: contiguous int32 [{n}] expected, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _one_device(stream, *tensors):
+    """Every tensor on the device that the call launches on: the current one, and the stream's."""
+    import torch
+    here = torch.device("cuda", torch.cuda.current_device())
+    bad = [t.device for t in tensors if t is not None and t.device != here]
+    if stream is not None and stream.device != here:
+        bad.append(stream.device)
+    if bad:
+        raise ValueError(f"tensor or stream on {bad[0]}, but the current device is {here}")
+
+
+def fg_kv_append_q4_ragged(k_new, v_new, row_off, pos, cache: KVCacheQ4, stream=None):
+    """Rows row_off[b] .. row_off[b+1]-1 of ``k_new`` and ``v_new`` (fp16 [rows][h], one row
+    stride) quantised into positions pos[b] .. of sequence b; ``row_off`` int32 [B+1] and ``pos``
+    int32 [B] on the device."""
+    rows, stride = _rows("k_new", k_new, cache.h)
+    if _rows("v_new", v_new, cache.h) != (rows, stride):
+        raise ValueError("k_new and v_new differ in rows or row stride")
+    _extents("row_off", row_off, cache.B + 1)
+    _extents("pos", pos, cache.B)
+    _one_device(stream, k_new, v_new, row_off, pos, cache.k_codes)
+    st = cache.struct()
+    _check("fg_kv_append_q4_ragged",
+           lib.fg_kv_append_q4_ragged(_ptr(k_new), _ptr(v_new), stride, rows, _ptr(row_off),
+                                      _ptr(pos), C.byref(st), _stream(stream)))
+
+
+def fg_kv_read_q4_ragged(cache: KVCacheQ4, row_off, pos, k_out, v_out, stream=None):
+    """Positions pos[b] .. of sequence b restored to fp16 rows row_off[b] .. row_off[b+1]-1 of
+    ``k_out`` and ``v_out`` (fp16 [rows][h], one row stride; either may be None)."""
+    outs = [_rows(n, t, cache.h) for n, t in (("k_out", k_out), ("v_out", v_out)) if t is not None]
+    if not outs or outs[0] != outs[-1]:
+        raise ValueError("k_out and v_out differ in rows or row stride, or both are None")
+    rows, stride = outs[0]
+    _extents("row_off", row_off, cache.B + 1)
+    _extents("pos", pos, cache.B)
+    _one_device(stream, k_out, v_out, row_off, pos, cache.k_codes)
+    st = cache.struct()
+    _check("fg_kv_read_q4_ragged",
+           lib.fg_kv_read_q4_ragged(C.byref(st), _ptr(row_off), _ptr(pos), rows, _ptr(k_out),
+                                    _ptr(v_out), stride, _stream(stream)))
+
+
+def fg_decode_attn_window_workspace_bytes(cache: KVCacheQ4, Hq: int) -> int:
+    st = cache.struct()
+    return int(lib.fg_decode_attn_window_workspace_bytes(C.byref(st), Hq))
+
+
+def fg_decode_attn_q4kv_window(q, Hq: int, cache: KVCacheQ4, lens, scale: float, out, ws=None,
+                               window: int = 0, sinks: int = 0, stream=None):
+    """Decode attention of the newest position of every sequence (``lens`` int32 [B] on the
+    device) over its last ``window`` positions (0: all) and its first ``sinks``; ``q`` and ``out``
+    fp16 [B][Hq*d], Hq a multiple of the cache's heads."""
+    nq, q_stride = _rows("q", q, Hq * cache.d)
+    no, o_stride = _rows("out", out, Hq * cache.d)
+    if nq != cache.B or no != cache.B:
+        raise ValueError(f"q and out need {cache.B} rows, got {nq} and {no}")
+    _extents("lens", lens, cache.B)
+    _one_device(stream, q, out, lens, ws, cache.k_codes)
+    st = cache.struct()
+    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    _check("fg_decode_attn_q4kv_window",
+           lib.fg_decode_attn_q4kv_window(_ptr(q), q_stride, Hq, C.byref(st), _ptr(lens), window,
+                                          sinks, scale, _ptr(out), o_stride, _ptr(ws), wsb,
+                                          _stream(stream)))
+
+
+def fg_prefill_attn_window(q, q_off, k, v, kv_off, Hq: int, Hkv: int, scale: float, out,
+                           window: int = 0, sinks: int = 0, stream=None):
+    """Attention of the newest positions of every sequence over its fp16 K/V rows: ``q`` and
+    ``out`` [q_rows][Hq*d], ``k`` and ``v`` [kv_rows][Hkv*d] with one row stride, ``q_off`` and
+    ``kv_off`` int32 [nseq+1] on the device; window and sinks as in
+    ``fg_decode_attn_q4kv_window``."""
+    if Hq <= 0 or Hkv <= 0 or q.dim() != 2 or q.shape[1] % Hq:
+        raise ValueError(f"q: [rows][Hq*d] expected, got {tuple(q.shape)} for {Hq} heads")
+    d = q.shape[1] // Hq
+    q_rows, q_stride = _rows("q", q, Hq * d)
+    o_rows, o_stride = _rows("out", out, Hq * d)
+    kv_rows, kv_stride = _rows("k", k, Hkv * d)
+    if _rows("v", v, Hkv * d) != (kv_rows, kv_stride) or o_rows != q_rows:
+        raise ValueError("k and v, or q and out, differ in rows, or k and v in row stride")
+    nseq = q_off.shape[0] - 1
+    _extents("q_off", q_off, nseq + 1)
+    _extents("kv_off", kv_off, nseq + 1)
+    _one_device(stream, q, out, k, v, q_off, kv_off)
+    _check("fg_prefill_attn_window",
+           lib.fg_prefill_attn_window(_ptr(q), q_stride, q_rows, _ptr(q_off), _ptr(k), _ptr(v),
+                                      kv_stride, kv_rows, _ptr(kv_off), nseq, Hq, Hkv, d, window,
+                                      sinks, scale, _ptr(out), o_stride, _stream(stream)))
 
 
 def fg_layernorm(x, gamma, beta, eps: float, y, stream=None):

@@ -186,6 +186,31 @@ int fg_dequant_gemm_q4_ln(const uint16_t* X, int64_t M, const fg_q4mat* W, const
 int fg_kv_append_q4(const uint16_t* k_new, const uint16_t* v_new, int64_t row_stride,
                     int32_t T, int32_t pos, const fg_kvcache* kv, void* stream);
 
+/* Ragged append: sequences of different lengths, each at a position of its own.  Rows
+ * row_off[b] .. row_off[b+1]-1 of k_new and v_new (h contiguous values per row, rows row_stride
+ * elements apart: >= h, a multiple of 8) are quantised into positions pos[b], pos[b]+1, .. of
+ * sequence b, with the codes and statistics fg_kv_append_q4 gives for those rows; everything
+ * else in the cache stays as it was.  `rows`: the rows k_new and v_new hold; rows before
+ * row_off[0] or from row_off[B] on are not read.  row_off: device int32 [B+1], 0 <= row_off[b]
+ * <= row_off[b+1] <= rows; pos: device int32 [B], 0 <= pos[b], pos[b] + (rows of b) <= cap.  The
+ * host never reads the two arrays, so their values are checked on the device: a row that does
+ * not fit is not written, and fg_check_device_error() returns FG_ERR_CAPACITY.
+ * rows == 0 or kv->B == 0 is a no-op.  The pages process blocks of equal prompts and have no
+ * counterpart. */
+int fg_kv_append_q4_ragged(const uint16_t* k_new, const uint16_t* v_new, int64_t row_stride,
+                           int32_t rows, const int32_t* row_off, const int32_t* pos,
+                           const fg_kvcache* kv, void* stream);
+
+/* The inverse: positions pos[b], pos[b]+1, .. of sequence b restored to fp16 (the values of
+ * fg_dequant_g64) into rows row_off[b] .. row_off[b+1]-1 of k_out and v_out, for prefill
+ * attention over what the cache holds.  Arguments as fg_kv_append_q4_ragged; k_out or v_out may
+ * be NULL (that half is not read).  Rows outside every sequence, and rows that do not fit, stay
+ * as they were.  [FlexGen review (jaehun.me), "4-bit 압축은 정수 연산 가속과 같은가": values
+ * are restored to FP16 before compute] */
+int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int32_t* pos,
+                         int32_t rows, uint16_t* k_out, uint16_t* v_out, int64_t row_stride,
+                         void* stream);
+
 /* ---------------------------------------------------------------------- attention */
 
 /* Decode attention of one new token per sequence over cache positions 0 .. len-1:
@@ -243,6 +268,52 @@ size_t fg_decode_attn_topk_workspace_bytes(const fg_kvcache* kv, int32_t len);
 int fg_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, int32_t H, int32_t d,
                     float scale, uint16_t* out, void* stream);
 
+/* What a query sees in the two windowed calls: position i sees position t of its sequence when
+ *   t <= i  and  (window == 0  or  t > i - window  or  t < sinks),
+ * i.e. the newest `window` positions up to its own (0: all of them) and the first `sinks`
+ * positions, which stay visible however far the window has moved.
+ *
+ * Decode attention over the 4-bit cache for sequences of different lengths: the query of
+ * sequence b is its newest cached position i = lens[b] - 1, and
+ *   out[b][hq*d + j] = sum_t softmax_t(scale * q_b,hq . K^_b,hk,t) V^_b,hk,t,j   over the visible t,
+ * query head hq reading K/V head hk = hq / (Hq / H): Hq query heads, a multiple of the cache's H.
+ * A sequence of length 0 sees nothing: its output is 0.  q: device fp16, row b at b*q_stride; out:
+ * device fp16, row b at b*out_stride (both strides >= Hq*d, multiples of 8).  lens: device int32
+ * [B], 0 <= lens[b] <= cap, checked on the device (a length that does not fit counts as 0, and
+ * fg_check_device_error() returns FG_ERR_CAPACITY).  window, sinks >= 0.  ws: device scratch of
+ * at least fg_decode_attn_window_workspace_bytes(kv, Hq) bytes, whatever the lengths and the
+ * window; it needs no initialisation.  Two calls in flight at once need workspaces of their own.
+ * Reads the sequences' visible 16-position tiles only.  The pages attend over whole caches
+ * of one length and have no counterpart. */
+int fg_decode_attn_q4kv_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
+                               const fg_kvcache* kv, const int32_t* lens, int32_t window,
+                               int32_t sinks, float scale, uint16_t* out, int64_t out_stride,
+                               void* ws, size_t ws_bytes, void* stream);
+/* Scratch bytes of fg_decode_attn_q4kv_window (planned for up to 192 SMs).  Host computation
+ * only; 0 for invalid arguments. */
+size_t fg_decode_attn_window_workspace_bytes(const fg_kvcache* kv, int32_t Hq);
+
+/* Prefill attention over fp16 rows for sequences of different lengths: sequence b has query rows
+ * q_off[b] .. q_off[b+1]-1 and K/V rows kv_off[b] .. kv_off[b+1]-1 (nq and nk of them); its query
+ * rows are its newest positions, row r of them being position i = nk - nq + r, and
+ *   out[row][hq*d + j] = sum_t softmax_t(scale * q_row,hq . k_hk,t) v_hk,t,j   over the visible t,
+ * hk = hq / (Hq / Hkv).  A row that sees nothing (nk < nq) gets 0.  With nq == nk this is a whole
+ * prompt (q, k and v may be column blocks of one QKV buffer), with nq < nk a piece of one against
+ * what was before it (fg_kv_read_q4_ragged).  q, out: device fp16, q_rows rows, q_stride and
+ * out_stride elements apart (>= Hq*d, multiples of 8); k, v: device fp16, kv_rows rows, kv_stride
+ * elements apart (>= Hkv*d, a multiple of 8).  q_off, kv_off: device int32 [nseq+1], not
+ * decreasing, within 0 .. q_rows and 0 .. kv_rows; checked on the device (the output of a sequence
+ * that does not fit stays as it was, and fg_check_device_error() returns FG_ERR_CAPACITY).  Rows
+ * of out outside every sequence stay as they were.  d in {64, 128}; Hq a multiple of Hkv; out
+ * must not alias q, k or v.  Values of keys that a row does not see never reach it, not even
+ * infinities and NaN.  nseq == 0 or q_rows == 0 is a no-op; with kv_rows == 0, k and v may be
+ * NULL.  The pages' prompts have one length and no window; no counterpart. */
+int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,
+                           const int32_t* q_off, const uint16_t* k, const uint16_t* v,
+                           int64_t kv_stride, int32_t kv_rows, const int32_t* kv_off, int32_t nseq,
+                           int32_t Hq, int32_t Hkv, int32_t d, int32_t window, int32_t sinks,
+                           float scale, uint16_t* out, int64_t out_stride, void* stream);
+
 /* ---------------------------------------------------------------------- LayerNorm */
 
 /* y[rows][h] = (x - mean) / sqrt(var + eps) * gamma + beta, fp32 statistics (population
@@ -296,7 +367,9 @@ size_t fg_layer_workspace_bytes(const fg_dims* dims, int32_t g, int32_t m, int32
 
 const char* fg_status_string(int status);
 const char* fg_last_error(void);
-/* Synchronise `stream`, read and clear the device error word: FG_OK or FG_ERR_TIMEOUT. */
+/* Synchronise `stream`, read and clear the device error words: FG_OK, FG_ERR_TIMEOUT, or
+ * FG_ERR_CAPACITY when a call met lengths, positions or offsets in a device array that do not
+ * fit its buffers. */
 int fg_check_device_error(void* stream);
 
 /* Per-kernel timing with CUDA events recorded around every launch on its stream.
@@ -312,7 +385,12 @@ enum {
   FG_K_GEMM_PAIR = 11,   /* the tiled GEMM on CTA pairs (many tokens): flops */
   FG_K_GEMM_PAIR_F16W = 12,   /* the CTA-pair GEMM on weights restored to fp16 (layer
                                  prefill): flops */
-  FG_K_COUNT = 13
+  /* work of the calls whose extents the host does not see is counted for the most that their
+   * host arguments allow: every row of the buffers, full cache, no window */
+  FG_K_KV_READ = 13,             /* fg_kv_read_q4_ragged: bytes */
+  FG_K_DECODE_ATTN_WINDOW = 14,  /* fg_decode_attn_q4kv_window, all its kernels: bytes */
+  FG_K_PREFILL_ATTN_WINDOW = 15, /* fg_prefill_attn_window: bytes of its rows */
+  FG_K_COUNT = 16
 };
 int fg_prof_enable(int on);
 int fg_prof_reset(void);

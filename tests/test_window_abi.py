@@ -1,0 +1,168 @@
+"""Host-side refusals of the ragged cache calls and the windowed attention (no GPU needed), and
+the device's index arithmetic compiled for the host."""
+import ctypes as C
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE, MISALIGNED = 0x10000, 0x10008        # never dereferenced: validation fails before any use
+
+
+@pytest.fixture(scope="module")
+def fg():
+    import __graft_entry__ as g
+    g.build()
+    from bit_compressed_throughput_gb300 import fg as mod
+    return mod
+
+
+def kvs(fg, B=2, cap=32, h=256, H=2, k=FAKE):
+    return fg.fg_kvcache(k, FAKE, FAKE, FAKE, B, cap, h, H)
+
+
+def test_ragged_cache_validation(fg):
+    L = fg.lib
+
+    def append(k=FAKE, v=FAKE, stride=256, rows=4, off=FAKE, pos=FAKE, kv=None):
+        return L.fg_kv_append_q4_ragged(k, v, stride, rows, off, pos,
+                                        C.byref(kv or kvs(fg)), None)
+
+    def read(k=FAKE, v=FAKE, stride=256, rows=4, off=FAKE, pos=FAKE, kv=None):
+        return L.fg_kv_read_q4_ragged(C.byref(kv or kvs(fg)), off, pos, rows, k, v, stride, None)
+
+    for call in (append, read):
+        assert call(stride=248) == fg.FG_ERR_SHAPE
+        assert call(stride=260) == fg.FG_ERR_SHAPE
+        assert call(rows=-1) == fg.FG_ERR_SHAPE
+        assert call(kv=kvs(fg, cap=20)) == fg.FG_ERR_SHAPE
+        assert call(kv=kvs(fg, H=8)) == fg.FG_ERR_SHAPE               # d = 32
+        assert call(kv=kvs(fg, k=None)) == fg.FG_ERR_ARG
+        assert call(k=MISALIGNED) == fg.FG_ERR_ARG
+        assert call(off=None) == fg.FG_ERR_ARG
+        assert call(pos=None) == fg.FG_ERR_ARG
+        assert call(off=FAKE + 2) == fg.FG_ERR_ARG
+        assert call(rows=0, k=None, v=None, off=None, pos=None) == fg.FG_OK
+        assert call(kv=kvs(fg, B=0), k=None, v=None, off=None, pos=None) == fg.FG_OK
+    assert append(k=None) == fg.FG_ERR_ARG and append(v=None) == fg.FG_ERR_ARG
+    assert read(k=None, v=None) == fg.FG_ERR_ARG
+
+
+def test_decode_window_validation(fg):
+    L = fg.lib
+    wsb = 1 << 30
+
+    def call(q=FAKE, qs=512, Hq=4, kv=None, lens=FAKE, window=8, sinks=2, scale=0.1, out=FAKE,
+             os_=512, ws=FAKE, n=wsb):
+        return L.fg_decode_attn_q4kv_window(q, qs, Hq, C.byref(kv or kvs(fg)), lens, window, sinks,
+                                            scale, out, os_, ws, n, None)
+
+    assert call(Hq=3) == fg.FG_ERR_SHAPE and call(Hq=0) == fg.FG_ERR_SHAPE
+    assert call(qs=504) == fg.FG_ERR_SHAPE and call(qs=516) == fg.FG_ERR_SHAPE
+    assert call(os_=504) == fg.FG_ERR_SHAPE
+    assert call(window=-1) == fg.FG_ERR_SHAPE and call(sinks=-1) == fg.FG_ERR_SHAPE
+    for s in (0.0, -1.0, float("inf"), float("nan")):
+        assert call(scale=s) == fg.FG_ERR_ARG
+    assert call(q=None) == fg.FG_ERR_ARG and call(out=MISALIGNED) == fg.FG_ERR_ARG
+    assert call(lens=None) == fg.FG_ERR_ARG and call(lens=FAKE + 1) == fg.FG_ERR_ARG
+    assert call(kv=kvs(fg, B=0), q=None, out=None, lens=None) == fg.FG_OK
+    need = L.fg_decode_attn_window_workspace_bytes(C.byref(kvs(fg)), 4)
+    if need:
+        assert call(n=need - 1) == fg.FG_ERR_WORKSPACE
+        assert call(ws=None) == fg.FG_ERR_WORKSPACE and call(ws=MISALIGNED) == fg.FG_ERR_WORKSPACE
+    assert L.fg_decode_attn_window_workspace_bytes(C.byref(kvs(fg, cap=20)), 4) == 0
+    assert L.fg_decode_attn_window_workspace_bytes(C.byref(kvs(fg)), 3) == 0
+    assert L.fg_decode_attn_window_workspace_bytes(None, 4) == 0
+
+
+def test_prefill_window_validation(fg):
+    L = fg.lib
+
+    def call(q=FAKE, qs=256, qr=8, qo=FAKE, k=FAKE, v=FAKE, ks=128, kr=8, ko=FAKE, nseq=2, Hq=4,
+             Hkv=2, d=64, window=0, sinks=0, scale=0.1, out=0x90000, os_=256):
+        return L.fg_prefill_attn_window(q, qs, qr, qo, k, v, ks, kr, ko, nseq, Hq, Hkv, d, window,
+                                        sinks, scale, out, os_, None)
+
+    assert call(Hkv=3) == fg.FG_ERR_SHAPE and call(d=32) == fg.FG_ERR_SHAPE
+    assert call(Hq=0) == fg.FG_ERR_SHAPE and call(Hkv=0) == fg.FG_ERR_SHAPE
+    assert call(nseq=-1) == fg.FG_ERR_SHAPE and call(qr=-1) == fg.FG_ERR_SHAPE
+    assert call(kr=-1) == fg.FG_ERR_SHAPE
+    assert call(qs=248) == fg.FG_ERR_SHAPE and call(ks=132) == fg.FG_ERR_SHAPE
+    assert call(os_=260) == fg.FG_ERR_SHAPE and call(ks=120) == fg.FG_ERR_SHAPE
+    assert call(window=-1) == fg.FG_ERR_SHAPE and call(sinks=-5) == fg.FG_ERR_SHAPE
+    assert call(scale=0.0) == fg.FG_ERR_ARG
+    assert call(q=None) == fg.FG_ERR_ARG and call(k=None) == fg.FG_ERR_ARG
+    assert call(v=MISALIGNED) == fg.FG_ERR_ARG and call(qo=None) == fg.FG_ERR_ARG
+    assert call(ko=FAKE + 2) == fg.FG_ERR_ARG
+    for alias in ("q", "k", "v"):
+        assert call(**{alias: 0x90000}) == fg.FG_ERR_ARG
+    assert call(nseq=0, q=None, out=None, qo=None, ko=None) == fg.FG_OK
+    assert call(qr=0, q=None, out=None, k=None, v=None) == fg.FG_OK
+
+
+HOST_SRC = r"""
+#include "ragged.cuh"
+using namespace fg;
+extern "C" {
+int h_sequence_of_row(const int32_t* off, int n, int r) { return sequence_of_row(off, n, r); }
+int h_offsets_ok(const int32_t* off, int n, int rows) { return offsets_ok(off, n, rows, 0, 1); }
+int h_visible(int t, int i, int window, int sinks) { return visible(t, i, window, sinks); }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    d = tmp_path_factory.mktemp("ragged")
+    src, lib = d / "h.cpp", d / "h.so"
+    src.write_text(HOST_SRC)
+    inc = os.path.join(ROOT, "bit_compressed_throughput_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(src), "-o",
+                    str(lib)], check=True)
+    return C.CDLL(str(lib))
+
+
+def arr(x):
+    a = np.asarray(x, np.int32)
+    return a, a.ctypes.data_as(C.POINTER(C.c_int32))
+
+
+def test_sequence_of_row(host):
+    rng = np.random.default_rng(1)
+    for _ in range(200):
+        n = int(rng.integers(1, 20))
+        lens = rng.integers(0, 4, n)
+        off = np.concatenate([[0], np.cumsum(lens)]) + int(rng.integers(0, 3))
+        keep, p = arr(off)
+        for r in range(-1, int(off[-1]) + 3):
+            want = [b for b in range(n) if off[b] <= r < off[b + 1]]
+            assert host.h_sequence_of_row(p, n, r) == (want[0] if want else -1)
+
+
+def test_sequence_of_row_stays_inside_for_any_offsets(host):
+    """Offsets that fall, repeat or overflow: the answer is a sequence or -1."""
+    rng = np.random.default_rng(2)
+    for _ in range(500):
+        n = int(rng.integers(1, 9))
+        keep, p = arr(rng.choice([-2 ** 31, -5, 0, 1, 3, 7, 2 ** 31 - 1], n + 1))
+        for r in (0, 1, 3, 6, 2 ** 31 - 1):
+            assert -1 <= host.h_sequence_of_row(p, n, r) < n
+
+
+def test_offsets_ok(host):
+    for off, rows, ok in (([0, 2, 2, 5], 5, 1), ([1, 2, 2, 5], 9, 1), ([0, 3, 2, 5], 5, 0),
+                          ([0, 2, 2, 6], 5, 0), ([-1, 2, 2, 5], 5, 0), ([0, 0], 0, 1)):
+        keep, p = arr(off)
+        assert host.h_offsets_ok(p, len(off) - 1, rows) == ok, off
+
+
+def test_visible(host):
+    from oracle import window as OW
+    for n in (1, 7, 20):
+        for window in (0, 1, 5, 2 ** 31 - 1):
+            for sinks in (0, 2, 2 ** 31 - 1):
+                for i in range(n):
+                    got = [t for t in range(n) if host.h_visible(t, i, window, sinks)]
+                    assert got == OW.visible(i, n, window, sinks).tolist()
