@@ -576,7 +576,7 @@ static int check_ragged(const fg_kvcache* kv, int64_t row_stride, int32_t rows,
   *nothing_to_do = false;
   int rc = check_kv(kv);
   if (rc) return rc;
-  if (rows < 0 || row_stride < kv->h || row_stride % 8 != 0) return FG_ERR_SHAPE;
+  if (rows < 0 || rows > 0x7FFFFFFF - 64 || row_stride < kv->h || row_stride % 8 != 0) return FG_ERR_SHAPE;
   if (rows == 0 || kv->B == 0) {
     *nothing_to_do = true;
     return FG_OK;
@@ -589,13 +589,15 @@ int fg_kv_append_q4_ragged(const uint16_t* k_new, const uint16_t* v_new, int64_t
                            int32_t rows, const int32_t* row_off, const int32_t* pos,
                            const fg_kvcache* kv, void* stream) {
   bool noop = false;
+  int sms = 0;
   int rc = check_ragged(kv, row_stride, rows, row_off, pos, &noop);
   if (rc || noop) return rc;
   if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return FG_ERR_ARG;
-  if ((rc = check_device(nullptr))) return rc;
+  if ((rc = check_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Span sp(st);
-  cudaError_t e = launch_kv_append_ragged(k_new, v_new, row_stride, rows, row_off, pos, *kv, st);
+  cudaError_t e = launch_kv_append_ragged(k_new, v_new, row_stride, rows, row_off, pos, *kv, sms,
+                                          st);
   if (e != cudaSuccess) return set_cuda_error(e);
   sp.stop(FG_K_KV_APPEND, work_quantize(2.0 * rows * kv->h));
   return FG_OK;
@@ -605,13 +607,15 @@ int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int
                          int32_t rows, uint16_t* k_out, uint16_t* v_out, int64_t row_stride,
                          void* stream) {
   bool noop = false;
+  int sms = 0;
   int rc = check_ragged(kv, row_stride, rows, row_off, pos, &noop);
   if (rc || noop) return rc;
   if ((!k_out && !v_out) || !aligned16(k_out) || !aligned16(v_out)) return FG_ERR_ARG;
-  if ((rc = check_device(nullptr))) return rc;
+  if ((rc = check_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Span sp(st);
-  cudaError_t e = launch_kv_read_ragged(*kv, row_off, pos, rows, k_out, v_out, row_stride, st);
+  cudaError_t e = launch_kv_read_ragged(*kv, row_off, pos, rows, k_out, v_out, row_stride, sms,
+                                        st);
   if (e != cudaSuccess) return set_cuda_error(e);
   sp.stop(FG_K_KV_READ, work_dequant((double)((k_out != nullptr) + (v_out != nullptr)) * rows * kv->h));
   return FG_OK;

@@ -34,10 +34,11 @@ cudaError_t launch_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, in
 // pos[b] .. of sequence b.
 cudaError_t launch_kv_append_ragged(const uint16_t* k_new, const uint16_t* v_new,
                                     int64_t row_stride, int32_t rows, const int32_t* row_off,
-                                    const int32_t* pos, const fg_kvcache& kv, cudaStream_t st);
+                                    const int32_t* pos, const fg_kvcache& kv, int nsm,
+                                    cudaStream_t st);
 cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, const int32_t* pos,
                                   int32_t rows, uint16_t* k_out, uint16_t* v_out,
-                                  int64_t row_stride, cudaStream_t st);
+                                  int64_t row_stride, int nsm, cudaStream_t st);
 
 // Windowed decode attention (attn_decode_window.cu): workspace bytes for any lengths and any SM
 // count up to kMaxSms.

@@ -6,7 +6,12 @@
 // q = rint((x - a) 15 / (b - a)) in binary32, restored as fp16(a + q ((b - a) / 15)).
 //
 // Both are bound by HBM: 2 bytes of fp16 and 0.5625 bytes of codes and statistics per element.
-// Work split: 8 lanes per group of 64, in row order.
+// A CTA takes a tile of rows of K and V and some heads.  For one head the tile's codes are then
+// one contiguous run of the head-major cache (per sequence), and its rows d contiguous values.
+// The tile's sequences are looked up once, then the CTA walks its heads with the next head's loads
+// in flight.
+#include <algorithm>
+
 #include "fg_common.cuh"
 #include "fg_internal.h"
 #include "ragged.cuh"
@@ -18,116 +23,304 @@ __device__ unsigned int g_ragged_error = 0;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroupsPerCta = kThreads / 8;
 
 struct RaggedArgs {
   const int32_t* row_off;
   const int32_t* pos;
-  int rows, B, H, d, cap;
+  int rows, B, H, cap;
+  int heads, hblocks;  // heads per CTA; CTAs per tile of rows
   int64_t stride;      // elements between the fp16 rows
 };
 
-// Cache slot ((b*H + head)*cap + position) of row `row` and head `head`, or -1.
-__device__ __forceinline__ int64_t slot_of(const RaggedArgs& a, int row, int head) {
-  const int b = sequence_of_row(a.row_off, a.B, row);
-  if (b < 0) return -1;
-  const int64_t t = (int64_t)row - a.row_off[b];
-  const int64_t p = a.pos[b] + t;
-  if (t < 0 || row >= a.row_off[b + 1]) return -1;
-  if (a.pos[b] < 0 || p >= a.cap) {
-    atomicOr(&g_ragged_error, kErrExtent);
-    return -1;
+// The sequence holding row r, found by a whole warp, 32 offsets at a time (the answers of
+// sequence_of_row).
+__device__ __forceinline__ int warp_sequence_of_row(const int32_t* off, int n, int r, int lane) {
+  if (r < off[0] || r >= off[n]) return -1;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int i = lo + lane * step;
+    const unsigned le = __ballot_sync(0xFFFFFFFFu, i < hi && off[i] <= r);
+    lo += max(__popc(le) - 1, 0) * step;
+    hi = min(hi, lo + step);
   }
-  return ((int64_t)b * a.H + head) * a.cap + p;
+  return lo;
 }
 
-__global__ void __launch_bounds__(kThreads)
-append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
-              const uint16_t* __restrict__ v_new, const fg_kvcache kv) {
-  pdl_launch_dependents();
-  pdl_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 &&
+// Slots (b*H)*cap + position of the tile's ROWS rows from r0 on, -1 for rows that no sequence
+// holds or that do not fit.  Every thread of the CTA calls it.
+template <int ROWS>
+__device__ __forceinline__ void tile_slots(const RaggedArgs& a, int r0, int64_t* slots) {
+  const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 &&
       !offsets_ok(a.row_off, a.B, a.rows, threadIdx.x, kThreads))
     atomicOr(&g_ragged_error, kErrExtent);
-  const int gpr = a.H * (a.d >> 6), gph = a.d >> 6;
-  const int64_t grp = (int64_t)blockIdx.x * kGroupsPerCta + (threadIdx.x >> 3);
-  const int sub = threadIdx.x & 7;
-  const int row = (int)(grp / gpr), gi = (int)(grp - (int64_t)row * gpr);
-  const int64_t slot = (row < a.rows) ? slot_of(a, row, gi / gph) : -1;
-  const uint16_t* src = blockIdx.y ? v_new : k_new;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (slot >= 0) v = ldg_nc_v4(src + (int64_t)row * a.stride + gi * 64 + sub * 8);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t mm = q4_minmax8(w);
+  if (threadIdx.x < ROWS) {
+    static_assert(ROWS % 32 == 0 && ROWS <= kThreads, "whole warps look rows up");
+    const int row = r0 + threadIdx.x;
+    // the warp's first row gives the sequence of most of its rows; the others search from there
+    int b = warp_sequence_of_row(a.row_off, a.B, row - lane, lane);
+    if (b < 0 || row >= a.row_off[b + 1])
+      b = row < a.rows ? sequence_of_row(a.row_off, a.B, row) : -1;
+    int64_t slot = -1;
+    if (b >= 0 && row < a.rows) {
+      const int64_t t = (int64_t)row - a.row_off[b];
+      if (t >= 0 && row < a.row_off[b + 1]) {
+        const int64_t p = a.pos[b] + t;
+        if (a.pos[b] >= 0 && p < a.cap)
+          slot = (int64_t)b * a.H * a.cap + p;
+        else
+          atomicOr(&g_ragged_error, kErrExtent);
+      }
+    }
+    slots[threadIdx.x] = slot;
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------------------- append
+
+__device__ __forceinline__ uint32_t hmin2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t q4_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A group's 16 values per lane (8 words), 4 lanes per group, by the exact formulas: order keys for
+// the minimum and maximum (signed zeros, NaN), the division for the codes.  The lanes of a group
+// come here together.
+__device__ __noinline__ uint2 quantize16_exact(uint4 v0, uint4 v1, unsigned group_lanes,
+                                               uint32_t* ab_out) {
+  const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+  uint32_t mm = __vminu2(q4_minmax8(w0), q4_minmax8(w1));
+  mm = __vminu2(mm, __shfl_xor_sync(group_lanes, mm, 1));
+  mm = __vminu2(mm, __shfl_xor_sync(group_lanes, mm, 2));
+  *ab_out = q4_ab_word(mm);
+  const Q4Group g = q4_group(*ab_out);
+  if (g.bma == 0.0f) return make_uint2(0u, 0u);
+  return make_uint2(q4_codes8_exact(v0, g.af, g.bma), q4_codes8_exact(v1, g.af, g.bma));
+}
+
+// Codes of 8 values in fixed point: with c15 = 15 / (b - a) and K = 192.5 + 2^-15 - a c15 held
+// in [128, 256), one fused multiply-add gives x c15 + K = 192.5 + y + 2^-15 with a unit of 2^-16:
+// bits 16-19 hold floor(y + 1/2) and the low 16 bits its fraction.  Errors, in that unit: 1/2 for
+// rounding K, 1/2 for the fused sum, and 15 * 2^-22 relative (the reciprocal's 2^-23, two roundings
+// of 2^-24) = 0.24 for c15, which multiplies x - a exactly; the defined code's own three roundings
+// move it by at most 15 * 3 * 2^-24 = 0.18.  So the code is the defined one unless y lies within
+// 1.42 units of a half-integer, when the fraction is 2 +- 1.42: below 4.  `frac` gathers the smallest
+// fraction (16-bit lanes).
+__device__ __forceinline__ uint32_t codes8_fixed(const uint32_t (&w)[4], uint64_t c2, uint64_t k2,
+                                                 uint32_t& frac) {
+  uint32_t t[8];
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) mm = __vminu2(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-  const uint32_t abw = q4_ab_word(mm);
-  const uint32_t c = q4_codes8_checked_x2(w, q4_group(abw));
-  if (slot >= 0) {
-    const int gs = gi % gph;
-    uint8_t* codes = blockIdx.y ? kv.v_codes : kv.k_codes;
-    uint32_t* ab = blockIdx.y ? kv.v_ab : kv.k_ab;
-    reinterpret_cast<uint32_t*>(codes + slot * (a.d >> 1) + gs * 32)[sub] = c;
-    if (sub == 0) ab[slot * gph + gs] = abw;
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack_h2(w[i]);
+    float lo, hi;
+    q4_unpack2(q4_fma2(q4_pack2(x.x, x.y), c2, k2), lo, hi);
+    t[2 * i] = __float_as_uint(lo);
+    t[2 * i + 1] = __float_as_uint(hi);
+    frac = __vminu2(frac, __byte_perm(t[2 * i], t[2 * i + 1], 0x5410));
+  }
+  const uint32_t ev = __byte_perm(__byte_perm(t[0], t[2], 0x0062), __byte_perm(t[4], t[6], 0x0062),
+                                  0x5410);
+  const uint32_t od = __byte_perm(__byte_perm(t[1], t[3], 0x0062), __byte_perm(t[5], t[7], 0x0062),
+                                  0x5410);
+  return (ev & 0x0F0F0F0Fu) | ((od & 0x0F0F0F0Fu) << 4);
+}
+
+// Quantises the 16 values of this lane (4 lanes per group of 64): codes, and the group's (a, b).
+// The fast path takes minimum and maximum as fp16 pairs and the codes in fixed point; a group with
+// a NaN, an infinity, a zero at either end (their order is by sign), a constant one, one whose K leaves
+// [128, 256) (its offset is more than four times its width) or with a code near a tie goes the
+// exact way (about 1 warp in 8 on normal data, for exact ties of fp16 values).
+__device__ __forceinline__ uint2 quantize16(const uint4 v0, const uint4 v1, int lane,
+                                            uint32_t* ab_out) {
+  const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+  uint32_t mn = hmin2_nan(w0[0], w0[1]), mx = hmax2_nan(w0[0], w0[1]);
+  mn = hmin2_nan(mn, hmin2_nan(w0[2], w0[3]));
+  mx = hmax2_nan(mx, hmax2_nan(w0[2], w0[3]));
+  mn = hmin2_nan(mn, hmin2_nan(hmin2_nan(w1[0], w1[1]), hmin2_nan(w1[2], w1[3])));
+  mx = hmax2_nan(mx, hmax2_nan(hmax2_nan(w1[0], w1[1]), hmax2_nan(w1[2], w1[3])));
+  // (min, -max) in one word: a minimum merges both
+  uint32_t mm = hmin2_nan(__byte_perm(mn, mx ^ 0x80008000u, 0x5410),
+                          __byte_perm(mn, mx ^ 0x80008000u, 0x7632));
+  mm = hmin2_nan(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 1));
+  mm = hmin2_nan(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 2));
+  const uint32_t abw = mm ^ 0x80000000u;
+  const float2 ab = unpack_h2(abw);
+  const float c15 = 15.0f * rcp_approx(__fsub_rn(ab.y, ab.x));
+  const float K = fmaf(-ab.x, c15, 192.5f + 0x1p-15f);
+  const uint64_t c2 = q4_pack2(c15, c15), k2 = q4_pack2(K, K);
+  uint32_t frac = 0xFFFFFFFFu;
+  uint2 codes;
+  codes.x = codes8_fixed(w0, c2, k2, frac);
+  codes.y = codes8_fixed(w1, c2, k2, frac);
+  // every comparison is false for NaN; c15 is 0 where b - a is infinite
+  const bool fast = K >= 128.0f && K < 256.0f && c15 > 0.0f && c15 < INFINITY && ab.x != 0.0f && ab.y != 0.0f &&
+                    min(frac & 0xFFFFu, frac >> 16) >= 4u;
+  *ab_out = abw;
+  const unsigned slow = __ballot_sync(0xFFFFFFFFu, !fast);
+  if (slow) {
+    const int g = lane & ~3;
+    if ((slow >> g) & 0xFu) codes = quantize16_exact(v0, v1, 0xFu << g, ab_out);
+  }
+  return codes;
+}
+
+// 4 lanes per group of 64, 16 values each: 16 * 256 / D rows per CTA.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 4)
+append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
+              const uint16_t* __restrict__ v_new, const fg_kvcache kv) {
+  constexpr int ROWS = 16 * kThreads / D, LPR = D / 16, NG = D / 64;
+  __shared__ int64_t slots[ROWS];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, r = threadIdx.x / LPR, c = threadIdx.x % LPR;
+  const unsigned tile = blockIdx.x / a.hblocks;
+  const int64_t r0 = (int64_t)tile * ROWS;
+  tile_slots<ROWS>(a, (int)r0, slots);
+  const int64_t slot0 = slots[r];
+  const bool live = slot0 >= 0;
+  const int h0 = (int)(blockIdx.x - tile * a.hblocks) * a.heads, h1 = min(a.H, h0 + a.heads);
+  const int64_t at = live ? (r0 + r) * a.stride + c * 16 : 0;
+  const uint16_t *ks = k_new + at, *vs = v_new + at;
+  uint4 x[4];
+  auto load = [&](int head) {
+    if (live) {
+      x[0] = ldg_nc_v4(ks + head * D);
+      x[1] = ldg_nc_v4(ks + head * D + 8);
+      x[2] = ldg_nc_v4(vs + head * D);
+      x[3] = ldg_nc_v4(vs + head * D + 8);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+  load(h0);
+  for (int head = h0; head < h1; ++head) {
+    const uint4 k0 = x[0], k1 = x[1], v0 = x[2], v1 = x[3];
+    if (head + 1 < h1) load(head + 1);
+    uint32_t kab, vab;
+    const uint2 kc = quantize16(k0, k1, lane, &kab);
+    const uint2 vc = quantize16(v0, v1, lane, &vab);
+    if (live) {
+      const int64_t slot = slot0 + (int64_t)head * a.cap;
+      *reinterpret_cast<uint2*>(kv.k_codes + slot * (D / 2) + c * 8) = kc;
+      *reinterpret_cast<uint2*>(kv.v_codes + slot * (D / 2) + c * 8) = vc;
+      if ((c & 3) == 0) {
+        kv.k_ab[slot * NG + (c >> 2)] = kab;
+        kv.v_ab[slot * NG + (c >> 2)] = vab;
+      }
+    }
   }
 }
 
+// ---------------------------------------------------------------------------- read-back
+
+// The 8 values of a code word: each code to binary32 exactly (its bits under the exponent of
+// 2^23, less 2^23), then the format's product, sum and rounding to fp16.
+__device__ __forceinline__ uint4 restore8(uint32_t codes, uint32_t abw) {
+  const float2 ab = unpack_h2(abw);
+  const float s = __fdiv_rn(__fsub_rn(ab.y, ab.x), 15.0f);
+  const uint32_t ev = codes & 0x0F0F0F0Fu, od = (codes >> 4) & 0x0F0F0F0Fu;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = __uint_as_float(__byte_perm(ev, 0x4B000000u, 0x7440 + i)) - 8388608.0f;
+    const float hi = __uint_as_float(__byte_perm(od, 0x4B000000u, 0x7440 + i)) - 8388608.0f;
+    o[i] = pack_h2(__fadd_rn(ab.x, __fmul_rn(lo, s)), __fadd_rn(ab.x, __fmul_rn(hi, s)));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 8 lanes per group of 64, 8 values each (a warp's stores are whole 32-byte sectors), two rows
+// per thread.
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 read_kernel(const RaggedArgs a, const fg_kvcache kv, uint16_t* __restrict__ k_out,
             uint16_t* __restrict__ v_out) {
+  constexpr int ROWS = 16 * kThreads / D, LPR = D / 8, NG = D / 64, STEP = kThreads / LPR;
+  __shared__ int64_t slots[ROWS];
   pdl_launch_dependents();
   pdl_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 &&
-      !offsets_ok(a.row_off, a.B, a.rows, threadIdx.x, kThreads))
-    atomicOr(&g_ragged_error, kErrExtent);
-  uint16_t* out = blockIdx.y ? v_out : k_out;
-  if (!out) return;
-  const int gpr = a.H * (a.d >> 6), gph = a.d >> 6;
-  const int64_t grp = (int64_t)blockIdx.x * kGroupsPerCta + (threadIdx.x >> 3);
-  const int sub = threadIdx.x & 7;
-  const int row = (int)(grp / gpr), gi = (int)(grp - (int64_t)row * gpr);
-  if (row >= a.rows) return;
-  const int64_t slot = slot_of(a, row, gi / gph);
-  if (slot < 0) return;
-  const int gs = gi % gph;
-  const uint8_t* codes = blockIdx.y ? kv.v_codes : kv.k_codes;
-  const uint32_t* ab = blockIdx.y ? kv.v_ab : kv.k_ab;
-  const uint32_t c = reinterpret_cast<const uint32_t*>(codes + slot * (a.d >> 1) + gs * 32)[sub];
-  const uint32_t abw = ab[slot * gph + gs];
-  const float af = h2f((uint16_t)(abw & 0xFFFFu)), bf = h2f((uint16_t)(abw >> 16));
-  const float s = __fdiv_rn(__fsub_rn(bf, af), 15.0f);
-  uint32_t o[4];
+  const int r = threadIdx.x / LPR, c = threadIdx.x % LPR;
+  const unsigned tile = blockIdx.x / a.hblocks;
+  const int64_t r0 = (int64_t)tile * ROWS;
+  tile_slots<ROWS>(a, (int)r0, slots);
+  const int h0 = (int)(blockIdx.x - tile * a.hblocks) * a.heads, h1 = min(a.H, h0 + a.heads);
+  for (int head = h0; head < h1; ++head) {
+    uint32_t code[2][2], ab[2][2];
+    int64_t slot[2];
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
-    o[n] = pack_h2(__fadd_rn(af, __fmul_rn((float)((c >> (8 * n)) & 0xF), s)),
-                   __fadd_rn(af, __fmul_rn((float)((c >> (8 * n + 4)) & 0xF), s)));
-  reinterpret_cast<uint4*>(out + (int64_t)row * a.stride + gi * 64)[sub] =
-      make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < 2; ++j) {
+      slot[j] = slots[r + j * STEP];
+      if (slot[j] < 0) continue;
+      slot[j] += (int64_t)head * a.cap;
+      if (k_out) {
+        code[j][0] = *reinterpret_cast<const uint32_t*>(kv.k_codes + slot[j] * (D / 2) + c * 4);
+        ab[j][0] = kv.k_ab[slot[j] * NG + (c >> 3)];
+      }
+      if (v_out) {
+        code[j][1] = *reinterpret_cast<const uint32_t*>(kv.v_codes + slot[j] * (D / 2) + c * 4);
+        ab[j][1] = kv.v_ab[slot[j] * NG + (c >> 3)];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (slot[j] < 0) continue;
+      const int64_t at = (r0 + r + j * STEP) * a.stride + (int64_t)head * D + c * 8;
+      if (k_out) *reinterpret_cast<uint4*>(k_out + at) = restore8(code[j][0], ab[j][0]);
+      if (v_out) *reinterpret_cast<uint4*>(v_out + at) = restore8(code[j][1], ab[j][1]);
+    }
+  }
 }
 
-RaggedArgs args_of(const int32_t* row_off, const int32_t* pos, int32_t rows, int64_t stride,
-                   const fg_kvcache& kv) {
-  return RaggedArgs{row_off, pos, rows, kv.B, kv.H, kv.h / kv.H, kv.cap, stride};
+// Heads per CTA: as many as leave the grid kCtasPerSm CTAs per SM, at most 8, so that the lookup
+// of a tile's rows is shared; one when there are few tiles.
+constexpr int kCtasPerSm = 16;
+template <typename Kernel, typename... Args>
+cudaError_t launch(Kernel* kernel, const int32_t* row_off, const int32_t* pos, int32_t rows,
+                   int64_t stride, const fg_kvcache& kv, int nsm, cudaStream_t st, Args... args) {
+  const int per = 16 * kThreads / (kv.h / kv.H);
+  const int64_t tiles = ((int64_t)rows + per - 1) / per;
+  const int heads =
+      (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * kv.H / ((int64_t)nsm * kCtasPerSm)));
+  const int hblocks = (kv.H + heads - 1) / heads;
+  if (tiles * hblocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const RaggedArgs a{row_off, pos, rows, kv.B, kv.H, kv.cap, heads, hblocks, stride};
+  return launch_pdl(kernel, dim3((unsigned)(tiles * hblocks)), dim3(kThreads), 0, st, a, args...);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_ragged(const uint16_t* k_new, const uint16_t* v_new,
                                     int64_t row_stride, int32_t rows, const int32_t* row_off,
-                                    const int32_t* pos, const fg_kvcache& kv, cudaStream_t st) {
-  const int64_t ng = (int64_t)rows * (kv.h / 64);
-  const dim3 grid((unsigned)((ng + kGroupsPerCta - 1) / kGroupsPerCta), 2);
-  return launch_pdl(append_kernel, grid, dim3(kThreads), 0, st,
-                    args_of(row_off, pos, rows, row_stride, kv), k_new, v_new, kv);
+                                    const int32_t* pos, const fg_kvcache& kv, int nsm,
+                                    cudaStream_t st) {
+  return launch(kv.h / kv.H == 128 ? append_kernel<128> : append_kernel<64>, row_off, pos, rows,
+                row_stride, kv, nsm, st, k_new, v_new, kv);
 }
 
 cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, const int32_t* pos,
                                   int32_t rows, uint16_t* k_out, uint16_t* v_out,
-                                  int64_t row_stride, cudaStream_t st) {
-  const int64_t ng = (int64_t)rows * (kv.h / 64);
-  const dim3 grid((unsigned)((ng + kGroupsPerCta - 1) / kGroupsPerCta), 2);
-  return launch_pdl(read_kernel, grid, dim3(kThreads), 0, st,
-                    args_of(row_off, pos, rows, row_stride, kv), kv, k_out, v_out);
+                                  int64_t row_stride, int nsm, cudaStream_t st) {
+  return launch(kv.h / kv.H == 128 ? read_kernel<128> : read_kernel<64>, row_off, pos, rows,
+                row_stride, kv, nsm, st, kv, k_out, v_out);
 }
 
 cudaError_t ragged_read_error(unsigned int* out) {
