@@ -47,4 +47,49 @@ FG_HD bool visible(int t, int i, int window, int sinks) {
   return t <= i && (window == 0 || t > i - window || t < sinks);
 }
 
+// ---- decode: the 16-position tiles of a sequence that its newest position sees
+//
+// Tiles 0 .. ns-1 hold the first positions, tiles tw .. te-1 the window; where they touch or
+// overlap ns is 0 and tw is 0 (one run of tiles).  Each of the nt tiles holds a visible position.
+constexpr int kTilePos = 16;
+struct SeqTiles {
+  int len, wstart;     // length; first position of the window
+  int nt, ns, tw;      // tiles; of them first-position tiles; first tile of the window
+};
+FG_HD SeqTiles seq_tiles(int len, int window, int sinks) {
+  SeqTiles s;
+  s.len = len;
+  s.wstart = (window == 0 || window >= len) ? 0 : len - window;
+  const int te = (int)(((int64_t)len + kTilePos - 1) / kTilePos);
+  const int seen = sinks < len ? sinks : len;
+  s.ns = (int)(((int64_t)seen + kTilePos - 1) / kTilePos);
+  s.tw = s.wstart / kTilePos;
+  if (s.ns >= s.tw) s.ns = s.tw = 0;
+  s.nt = s.ns + te - s.tw;
+  return s;
+}
+// Position of the first row of tile u (0 <= u < nt), and the tiles of a slot of at most `most`
+// that starts there: one run of positions inside tiles u .. u1-1.
+FG_HD int tile_pos(const SeqTiles& s, int u) {
+  return (u < s.ns ? u : u - s.ns + s.tw) * kTilePos;
+}
+FG_HD int slot_tiles(const SeqTiles& s, int u, int u1, int most) {
+  const int end = (u < s.ns && s.ns < u1) ? s.ns : u1;
+  return end - u < most ? end - u : most;
+}
+
+// The tiles of a call in one order, cut evenly among nw workers: worker w takes tiles
+// first_tile(w) .. first_tile(w + 1) - 1 of `total`; worker_of_tile is the inverse.
+FG_HD int64_t first_tile(int64_t total, int nw, int w) {
+  return (total / nw) * w + (total % nw) * w / nw;
+}
+FG_HD int worker_of_tile(int64_t total, int nw, int64_t x) {
+  // (a guess within one, then the definition: total * nw may pass 64 bits)
+  int w = (int)((double)x / (double)total * nw);
+  w = w < 0 ? 0 : (w >= nw ? nw - 1 : w);
+  while (w > 0 && first_tile(total, nw, w) > x) --w;
+  while (w + 1 < nw && first_tile(total, nw, w + 1) <= x) ++w;
+  return w;
+}
+
 }  // namespace fg
