@@ -10,17 +10,22 @@
 // so the products run on mma.sync m16n8k16 over the codes (exact fp16 subnormals, attn_q4.cuh) with
 // fp32 sums.  The work is bound by reading the visible part of the cache once.
 //
-// Heads: the 8 columns of a product are (query head, group) pairs -- 4 heads of one K/V head (for
-// d = 64 the second column of a pair repeats the first) -- so lane (gid, tig) ends up with the
-// scores, weights and outputs of head tig for the rows and channels of gid: up to 4 heads cost
-// what one does.  More than 4 heads per K/V head are further row sets over the same positions,
-// adjacent in the work order, which find them in L2.
+// Columns: the 8 columns of a product are (part, query head, group) with NP parts of HEADS = 4 / NP
+// query heads of one K/V head (for d = 64 the second column of a group pair repeats the first), so
+// lane (gid, tig) ends up with scores of head tig % HEADS.  A slot of 32 positions has four
+// 8-row halves of tiles; part tig / HEADS takes 4 / NP of them, so the softmax and the statistics of
+// a position are computed once per head: with one head per K/V head (NP = 4) a lane has one
+// position of the slot, with four (NP = 1) all four of its rows.  The weights meet the values as a
+// B operand that is zero outside the part's columns, so the parts add up in separate columns, summed
+// at the end.  More than 4 heads per K/V head are further row sets over the same positions, adjacent
+// in the work order, which find them in L2.
 //
-// Work split: the visible 16-position tiles of all row sets (sequence, K/V head, 4 query heads) stand
-// in one order, cut evenly among the warps of the grid, whatever the lengths.  A warp's range crosses
-// row sets; a row set that lies within one range is finished there, one that is cut leaves softmax
-// partials (m, l, unnormalised o), merged by a second kernel in a fixed order.  So the scratch is
-// two partials per warp, whatever the call.
+// Work split: the visible 16-position tiles of all row sets (sequence, K/V head, HEADS query heads)
+// stand
+// in one order, cut into even chunks whatever the lengths (Chunks, ragged.cuh): one CTA of 16 warps
+// per SM, whose warps take the CTA's chunks.  A chunk crosses row sets; a row set that lies within
+// one chunk is finished there, one that is cut leaves softmax partials (m, l, unnormalised o), merged
+// by a second kernel in a fixed order.  So the scratch is two partials per chunk, whatever the call.
 //
 // Memory pipeline, as in the dense decode attention: per warp a ring of slots (3 tiles of K and V
 // codes and statistics), filled by bulk async copies that run ahead across row sets.  Every wait is
@@ -46,18 +51,19 @@ namespace {
 using q4attn::mma16816;
 using q4attn::movtrans;
 
-constexpr int kWarps = 4;                 // per CTA
-constexpr int kCtasPerSm = 4;
-constexpr int kHeads = 4;                 // query heads of a row set
-constexpr int kSub = 3;                   // tiles per ring slot
+constexpr int kSub = 2;                   // tiles per ring slot
 constexpr int kSlotPos = kSub * kTilePos;
-constexpr int kRing = 2;                  // slots per warp
-constexpr int kMinTiles = 3;              // per warp of a small call: one slot
+constexpr int kMinTiles = 4;              // per warp of a small call: two slots
 constexpr long long kWaitCycles = 1ll << 32;
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 
+// One CTA per SM.  Its rings hold about 110 KB, what the memory system needs in flight (152 x 110 KB
+// = 17 MB, 2.4 us of its rate); with twice as much the SMs advance less evenly and the last ones
+// finish later (128 sequences of 784 positions, 56 heads: 173 us with 16 warps x 3 slots, 152 us with
+// 12 x 2; 64-channel heads, whose slots are half as large, 72 us with 16 x 3, 81 us with 12 x 2).
 template <int D>
 struct Ring {
+  static constexpr int WARPS = (D == 128) ? 12 : 16, DEPTH = (D == 128) ? 2 : 3;
   static constexpr int NG = D / 64;
   static constexpr int ROW_CODE = D / 2;                // code bytes of one position
   static constexpr int ROW_AB = NG * 4;                 // statistics bytes of one position
@@ -65,11 +71,12 @@ struct Ring {
   static constexpr int KAB_OFF = 2 * V_OFF;
   static constexpr int VAB_OFF = KAB_OFF + kSlotPos * ROW_AB;
   static constexpr int SLOT = VAB_OFF + kSlotPos * ROW_AB;
-  static constexpr int CTA_BYTES = kWarps * kRing * (SLOT + 8);
+  static constexpr int CTA_BYTES = WARPS * DEPTH * (SLOT + 8);
 };
+static_assert(Ring<128>::CTA_BYTES + 1024 <= 227 * 1024, "shared memory per CTA");
 
-// What a warp leaves of its first row set when an earlier warp began it: the warp before the first
-// such cut merges `pieces` partials, from its own on.
+// What is to be merged at the cut before a warp's share: the pieces of the row set that it begins
+// inside of, when the share before holds that row set's first tile.
 struct Cut {
   int pieces;          // 0: nothing to merge here
   int b, hq, heads;
@@ -84,8 +91,9 @@ struct Args {
   int G, nhb;          // query heads per K/V head; row sets per K/V head
   int window, sinks;
   float scale_log2;
-  Cut* cuts;           // [warps]
-  float* partial;      // [2 * warps][kHeads][D + 2]
+  int ncuts;           // the grid's warps
+  Cut* cuts;           // [ncuts]
+  float* partial;      // [2 * ncuts][HEADS][D + 2]
 };
 
 // 2^x on the special-function unit (x <= 2 here; results below 2^-126 flush to zero)
@@ -158,24 +166,24 @@ __device__ __forceinline__ void next_row_set(Cursor& c, const Args& a, const fg_
   } while (c.s.nt == 0);
 }
 
-// The query heads of a row set as B fragments (column n = gid: head gid / 2, group gid & 1; indexes
-// permuted as the lanes hold the codes), the group sums of head tig and the code-scale factor, in
-// the base-2 score scale.
+// The query heads of a row set as B fragments (column n = gid: head (gid / 2) % HEADS, group gid & 1;
+// indexes permuted as the lanes hold the codes), the group sums of head tig % HEADS, in the base-2
+// score scale.
 template <int D>
 struct QFrag {
   uint32_t bq[2 * (D / 32)][2];
   float Q[D / 64];
 };
-template <int D>
+template <int D, int HEADS>
 __device__ __forceinline__ void load_q(const uint16_t* q_heads, int heads, int lane,
                                        float scale_log2, QFrag<D>& f) {
   constexpr int NW = D / 32, NG = D / 64;
-  const int gid = lane >> 2, tig = lane & 3;
+  const int gid = lane >> 2, tig = lane & 3, col_head = (gid >> 1) % HEADS;
   uint32_t qw[NW * 4];
 #pragma unroll
   for (int c = 0; c < NW; ++c) {
     uint4 u = make_uint4(0, 0, 0, 0);
-    if ((gid >> 1) < heads) u = ldg_nc_v4(q_heads + (gid >> 1) * D + tig * 8 * NW + 8 * c);
+    if (col_head < heads) u = ldg_nc_v4(q_heads + col_head * D + tig * 8 * NW + 8 * c);
     qw[4 * c] = u.x; qw[4 * c + 1] = u.y; qw[4 * c + 2] = u.z; qw[4 * c + 3] = u.w;
   }
   const bool mine = NG == 1 || (gid & 1) == (tig >> 1);
@@ -199,19 +207,42 @@ __device__ __forceinline__ void load_q(const uint16_t* q_heads, int heads, int l
   qsum += __shfl_xor_sync(0xFFFFFFFFu, qsum, 1);
   if (NG == 1) qsum += __shfl_xor_sync(0xFFFFFFFFu, qsum, 2);
 #pragma unroll
-  for (int g = 0; g < NG; ++g)              // head tig: lanes gid = 2 tig, tig = 2 g
-    f.Q[g] = __shfl_sync(0xFFFFFFFFu, qsum, 8 * tig + 2 * g) * scale_log2;
+  for (int g = 0; g < NG; ++g)              // lanes gid = 2 head, tig = 2 g
+    f.Q[g] = __shfl_sync(0xFFFFFFFFu, qsum, 8 * (tig % HEADS) + 2 * g) * scale_log2;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+// Moves a place dx tiles on in the order.
+__device__ __forceinline__ void skip_tiles(Cursor& c, int64_t dx, const Args& a,
+                                           const fg_kvcache& kv) {
+  const int rsets = kv.H * a.nhb;
+  int64_t at = (int64_t)c.rs * c.s.nt + c.u + dx;        // within sequence b
+  while (at >= (int64_t)rsets * c.s.nt) {
+    at -= (int64_t)rsets * c.s.nt;
+    if (++c.b >= kv.B) {                   // the end of the order: never asked for
+      c.b = kv.B - 1;
+      return;
+    }
+    c.s = seq_tiles(length_of(a, kv, c.b), a.window, a.sinks);
+  }
+  c.rs = at < 0x7FFFFFFF ? (int)((unsigned)at / (unsigned)c.s.nt) : (int)(at / c.s.nt);
+  c.u = (int)(at - (int64_t)c.rs * c.s.nt);
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(Ring<D>::WARPS * 32, 1)
 decode_window_kernel(const Args a, const fg_kvcache kv) {
   using R = Ring<D>;
+  constexpr int kWarps = R::WARPS, kRing = R::DEPTH;
   constexpr int NW = D / 32, NG = D / 64;
+  constexpr int HEADS = 4 / NP, RPL = 4 / NP;   // heads of a row set; rows of a slot per lane
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ unsigned warp_nt[kWarps];
+  __shared__ int first_b;                  // the sequence of the CTA's first tile,
+  __shared__ int64_t first_before;         // and the tiles of the sequences before it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gid = lane >> 2, tig = lane & 3;
+  const int gid = lane >> 2, tig = lane & 3, part = tig / HEADS;
   uint8_t* ring = smem + warp * kRing * R::SLOT;
+  const uint32_t ring0 = smem_u32(ring);
   const uint32_t bar0 = smem_u32(smem + kWarps * kRing * R::SLOT) + warp * kRing * 8;
   if (lane == 0) {
     for (int i = 0; i < kRing; ++i) mbar_init(bar0 + 8 * i, 1);
@@ -221,119 +252,148 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- the order of the work: tiles of all sequences, and this warp's share.  Neighbouring
-  // warps of the order sit on different SMs, so a small call spreads over the GPU.
-  const int nwarps = gridDim.x * kWarps, w = warp * gridDim.x + blockIdx.x;
+  // ---- the order of the work: how many tiles, and where this CTA's begin
   const int rsets = kv.H * a.nhb;          // row sets of one sequence
-  int64_t tiles = 0;
-  for (int b0 = 0; b0 < kv.B; b0 += 32) {
-    const int b = b0 + lane;
-    const unsigned nt = b < kv.B ? seq_tiles(length_of(a, kv, b), a.window, a.sinks).nt : 0;
-    tiles += __reduce_add_sync(0xFFFFFFFFu, nt);
-  }
-  for (int b = w; b < kv.B; b += nwarps) {  // sequences that see nothing
-    const int len = a.lens[b];
-    if (lane == 0 && (len < 0 || len > kv.cap)) atomicOr(&g_decode_window_error, kErrExtent);
-    if (length_of(a, kv, b) == 0)
-      for (int i = lane; i < rsets / a.nhb * a.G * (D / 8); i += 32)
-        reinterpret_cast<uint4*>(a.out + b * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
-  }
-  const int64_t total = tiles * rsets;
-  const int nw = (int)max((int64_t)1, min((int64_t)nwarps, total / kMinTiles));
-  Cut cut{};
-  if (w >= nw || total == 0) {
-    if (lane == 0) a.cuts[w] = cut;
-    return;
-  }
-  const int64_t x0 = first_tile(total, nw, w), x1 = first_tile(total, nw, w + 1);
-  Cursor cc{};                              // compute cursor
-  {
-    int64_t before = 0;                     // tiles of earlier sequences, once per row set
-    for (int b0 = 0;; b0 += 32) {
-      const int b = b0 + lane;
-      const unsigned nt = b < kv.B ? seq_tiles(length_of(a, kv, b), a.window, a.sinks).nt : 0;
-      unsigned incl = nt;
+  int64_t tiles = 0, before = 0;           // of one row set: all sequences; those of earlier rounds
+  unsigned incl = 0, mine = 0;
+  auto scan_round = [&](int b0) {          // a sequence per thread: its tiles, those up to it
+    const int b = b0 + threadIdx.x;
+    mine = b < kv.B ? seq_tiles(length_of(a, kv, b), a.window, a.sinks).nt : 0;
+    incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      const unsigned past = __ballot_sync(0xFFFFFFFFu, (before + incl) * rsets > x0);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        cc.b = b0 + l;
-        before += __shfl_sync(0xFFFFFFFFu, incl - nt, l);
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) warp_nt[warp] = incl;
+    __syncthreads();
+    unsigned round = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const unsigned n = warp_nt[i];
+      if (i < warp) incl += n;
+      round += n;
+    }
+    __syncthreads();
+    return round;
+  };
+  for (int b0 = 0; b0 < kv.B; b0 += kWarps * 32) tiles += scan_round(b0);
+  const int64_t total = tiles * rsets;
+  // Neighbours of the order sit on one SM (they read neighbouring memory); a call with less than
+  // kMinTiles for every warp has fewer shares of about that, the same few on every SM.
+  const int64_t most_shares = max((int64_t)1, total / kMinTiles);
+  const int per_cta = (int)min((int64_t)kWarps, (most_shares - 1) / gridDim.x + 1);
+  const int n = (int)min(most_shares, (int64_t)gridDim.x * per_cta);
+  const Shares shares(total, n);
+  const int w = blockIdx.x * per_cta + warp;
+  const bool busy = total > 0 && (int)blockIdx.x * per_cta < n;
+  const int64_t cta_x = busy ? shares.first(blockIdx.x * per_cta) : 0;
+  if (busy) {
+    for (int b0 = 0; b0 < kv.B; b0 += kWarps * 32) {
+      const unsigned round = kv.B > kWarps * 32 ? scan_round(b0) : (unsigned)tiles;
+      if ((before + round) * rsets > cta_x) {
+        if ((before + incl) * rsets > cta_x && (before + incl - mine) * rsets <= cta_x) {
+          first_b = b0 + threadIdx.x;
+          first_before = before + incl - mine;
+        }
         break;
       }
-      before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if (b0 + 32 >= kv.B) return;          // not reached: x0 < total
+      before += round;
     }
-    cc.s = seq_tiles(length_of(a, kv, cc.b), a.window, a.sinks);
-    const int64_t rel = x0 - before * rsets;
-    cc.rs = (int)(rel / cc.s.nt);
-    cc.u = (int)(rel - (int64_t)cc.rs * cc.s.nt);
-    // what has to be merged: this warp speaks for the row set it begins inside of, when the warp
-    // before holds that row set's first tile
-    const int64_t r0 = x0 - cc.u;
-    if (cc.u > 0) {
-      const int64_t xp = first_tile(total, nw, w - 1);
-      if (xp <= r0) {
-        const int hk = cc.rs / a.nhb, hb = cc.rs - hk * a.nhb;
-        cut.pieces = worker_of_tile(total, nw, r0 + cc.s.nt - 1) - (w - 1) + 1;
-        cut.b = cc.b;
-        cut.hq = hk * a.G + hb * kHeads;
-        cut.heads = min(kHeads, a.G - hb * kHeads);
-        cut.prev_slot = 2 * (w - 1) + (xp == r0 ? 0 : 1);
-      }
-    }
-    if (lane == 0) a.cuts[w] = cut;
   }
+  __syncthreads();
 
-  // ---- the issue cursor, kRing slots ahead of the compute cursor
-  Cursor ic = cc;
-  int ileft = (int)(x1 - x0);              // the scratch and the cache bound it far below 2^31
-  int is = 0, issued = 0;
+  // ---- issue: fills the ring kRing slots ahead of the computation, one run of positions (the first
+  // ones or the window of a row set) after the other
+  int ileft = 0, irun = 0, is = 0, issued = 0;         // tiles left, of them in the run; slot
+  int64_t irow = 0;                        // the run's next position, as a row of the cache
+  Cursor ic{};
+  const bool has_share = busy && warp < per_cta && w < n;
+  if (has_share) {
+    const int64_t x0 = shares.first(w);
+    ileft = (int)(shares.first(w + 1) - x0);           // the cache's size bounds it far below 2^31
+    ic.b = first_b;
+    ic.s = seq_tiles(length_of(a, kv, ic.b), a.window, a.sinks);
+    skip_tiles(ic, x0 - first_before * rsets, a, kv);
+  }
+  Cursor cc = ic;                          // the computation's cursor
+  int left = ileft;
   auto issue = [&]() {
-    if (ileft <= 0) return;
-    const int u1 = min(ic.s.nt, ic.u + ileft);
-    const int cnt = slot_tiles(ic.s, ic.u, u1, kSub);
+    if (irun == 0) {
+      if (ileft == 0) return;
+      if (ic.u == ic.s.nt) {
+        next_row_set(ic, a, kv);
+        // its queries, needed kRing slots from here
+        const int hk = ic.rs / a.nhb;
+        const int hq = hk * a.G + (ic.rs - hk * a.nhb) * HEADS + (lane >> 3);
+        if ((lane >> 3) < HEADS && hq < hk * a.G + a.G && (lane & 7) * 16 < D)
+          prefetch_l2(a.q + ic.b * a.q_stride + (int64_t)hq * D + (lane & 7) * 16);
+      }
+      irun = run_tiles(ic.s, ic.u, min(ic.s.nt, ic.u + ileft));
+      irow = ((int64_t)ic.b * kv.H + ic.rs / a.nhb) * kv.cap + tile_pos(ic.s, ic.u);
+      ic.u += irun;
+      ileft -= irun;
+    }
+    const int cnt = min(kSub, irun);
     if (lane == 0) {
-      const uint32_t bar = bar0 + 8 * is;
-      uint8_t* slot = ring + is * R::SLOT;
-      const uint32_t rows = cnt * kTilePos;          // whole tiles: never past cap
-      const int64_t row0 =
-          ((int64_t)ic.b * kv.H + ic.rs / a.nhb) * kv.cap + tile_pos(ic.s, ic.u);
+      const uint32_t bar = bar0 + 8 * is, rows = cnt * kTilePos;   // whole tiles: never past cap
+      const uint32_t slot = ring0 + is * R::SLOT;
       // the slot was last read through the generic proxy; order that before the copy
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_expect_tx(bar, rows * 2 * (R::ROW_CODE + R::ROW_AB));
-      bulk_copy(smem_u32(slot), kv.k_codes + row0 * R::ROW_CODE, rows * R::ROW_CODE, bar);
-      bulk_copy(smem_u32(slot + R::KAB_OFF), kv.k_ab + row0 * NG, rows * R::ROW_AB, bar);
-      bulk_copy(smem_u32(slot + R::V_OFF), kv.v_codes + row0 * R::ROW_CODE, rows * R::ROW_CODE, bar);
-      bulk_copy(smem_u32(slot + R::VAB_OFF), kv.v_ab + row0 * NG, rows * R::ROW_AB, bar);
+      bulk_copy(slot, kv.k_codes + irow * R::ROW_CODE, rows * R::ROW_CODE, bar);
+      bulk_copy(slot + R::KAB_OFF, kv.k_ab + irow * NG, rows * R::ROW_AB, bar);
+      bulk_copy(slot + R::V_OFF, kv.v_codes + irow * R::ROW_CODE, rows * R::ROW_CODE, bar);
+      bulk_copy(slot + R::VAB_OFF, kv.v_ab + irow * NG, rows * R::ROW_AB, bar);
     }
+    irow += cnt * kTilePos;
+    irun -= cnt;
     ++issued;
     if (++is == kRing) is = 0;
-    ileft -= cnt;
-    ic.u += cnt;
-    if (ic.u == ic.s.nt && ileft > 0) next_row_set(ic, a, kv);
   };
   for (int i = 0; i < kRing; ++i) issue();
+
+  // ---- what is to be merged at this warp's cut
+  Cut cut{};
+  if (has_share && cc.u > 0) {
+    const int64_t r0 = shares.first(w) - cc.u, xp = shares.first(w - 1);
+    if (xp <= r0) {
+      const int hk = cc.rs / a.nhb, hb = cc.rs - hk * a.nhb;
+      cut.pieces = shares.share_of(r0 + cc.s.nt - 1) - (w - 1) + 1;
+      cut.b = cc.b;
+      cut.hq = hk * a.G + hb * HEADS;
+      cut.heads = min(HEADS, a.G - hb * HEADS);
+      cut.prev_slot = 2 * (w - 1) + (xp == r0 ? 0 : 1);
+    }
+  }
+  if (has_share && lane == 0) a.cuts[w] = cut;
+
+  // ---- sequences that see nothing, and cuts of warps without a share
+  for (int64_t b = (int64_t)blockIdx.x * kWarps + warp; b < kv.B; b += (int64_t)gridDim.x * kWarps) {
+    const int len = a.lens[b];
+    if (lane == 0 && (len < 0 || len > kv.cap)) atomicOr(&g_decode_window_error, kErrExtent);
+    if (length_of(a, kv, (int)b) == 0)
+      for (int i = lane; i < kv.H * a.G * (D / 8); i += 32)
+        reinterpret_cast<uint4*>(a.out + b * a.out_stride)[i] = make_uint4(0, 0, 0, 0);
+  }
+  for (int c = (total > 0 ? n : 0) + blockIdx.x * kWarps * 32 + threadIdx.x; c < a.ncuts;
+       c += gridDim.x * kWarps * 32)
+    a.cuts[c].pieces = 0;
 
   const float ck = (16777216.0f / 15.0f) * a.scale_log2;
   int cs = 0, consumed = 0;
   uint32_t cph = 0;
-  int left = (int)(x1 - x0);
   bool ok = true;
   for (int seg_no = 0; left > 0 && ok; ++seg_no) {
     const int u1 = min(cc.s.nt, cc.u + left);
     const bool whole = cc.u == 0 && u1 == cc.s.nt;
     const int seg = u1 - cc.u;
     const int hk = cc.rs / a.nhb, hb = cc.rs - hk * a.nhb;
-    const int hq = hk * a.G + hb * kHeads, heads = min(kHeads, a.G - hb * kHeads);
+    const int hq = hk * a.G + hb * HEADS, heads = min(HEADS, a.G - hb * HEADS);
     QFrag<D> qf;
-    load_q<D>(a.q + cc.b * a.q_stride + (int64_t)hq * D, heads, lane, a.scale_log2, qf);
+    load_q<D, HEADS>(a.q + cc.b * a.q_stride + (int64_t)hq * D, heads, lane, a.scale_log2, qf);
 
-    // head tig, the lane's rows (l, asum) and channels (acc)
+    // head tig % HEADS: the part's rows (l, asum) and columns (acc)
     float m_run = -INFINITY, l_run = 0.0f;
     float acc[2 * NW][4], asum[NG];
 #pragma unroll
@@ -348,150 +408,184 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
     // weight 0 by selects on the score and on the statistics.
     auto process = [&](const uint8_t* slot, int ts, int cnt, auto mask_tag) {
       constexpr bool MASK = decltype(mask_tag)::value;
-      auto valid = [&](int sub, int r) {
-        const int t = ts + sub * kTilePos + gid + 8 * r;
-        return !MASK || (sub < cnt && t < cc.s.len && (t >= cc.s.wstart || t < a.sinks));
-      };
-      float sc[kSub][2];
+      float dk[kSub][4];
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
-        uint32_t kw[2][NW], ka[2][NG];
+        uint32_t kw[2][NW];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = sub * kTilePos + gid + 8 * r;
-          load_words<NW>(slot + row * R::ROW_CODE + tig * 4 * NW, kw[r]);
-          load_words<NG>(slot + R::KAB_OFF + row * R::ROW_AB, ka[r]);
-        }
-        float dk[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 2; ++r)
+          load_words<NW>(slot + (sub * kTilePos + gid + 8 * r) * R::ROW_CODE + tig * 4 * NW, kw[r]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dk[sub][c] = 0.0f;
 #pragma unroll
         for (int wd = 0; wd < NW; ++wd) {
           uint32_t c0[4], c1[4];
           q4attn::code_pairs(kw[0][wd], c0);
           q4attn::code_pairs(kw[1][wd], c1);
-          mma16816(dk, c0[0], c1[0], c0[1], c1[1], qf.bq[2 * wd][0], qf.bq[2 * wd][1]);
-          mma16816(dk, c0[2], c1[2], c0[3], c1[3], qf.bq[2 * wd + 1][0], qf.bq[2 * wd + 1][1]);
+          mma16816(dk[sub], c0[0], c1[0], c0[1], c1[1], qf.bq[2 * wd][0], qf.bq[2 * wd][1]);
+          mma16816(dk[sub], c0[2], c1[2], c0[3], c1[3], qf.bq[2 * wd + 1][0],
+                   qf.bq[2 * wd + 1][1]);
         }
-        // dk[2r], dk[2r + 1]: row gid + 8r, head tig, groups 0 and 1
+      }
+      // dk[sub][2r + g]: row 16 sub + 8r + gid, the lane's head, group g.  The part's rows are
+      // 8 rh + gid, rh = part * RPL + j.
+      float sc[RPL];
+      bool valid[RPL];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float dot = 0.0f, off = 0.0f;
+      for (int j = 0; j < RPL; ++j) {
+        const int row = 8 * (part * RPL + j) + gid, t = ts + row;
+        valid[j] = !MASK || (row < cnt * kTilePos && t < cc.s.len &&
+                             (t >= cc.s.wstart || t < a.sinks));
+        uint32_t ka[NG];
+        load_words<NG>(slot + R::KAB_OFF + row * R::ROW_AB, ka);
+        float dot = 0.0f, off = 0.0f;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float2 ab = unpack_h2(ka[r][g]);
-            dot = fmaf(ab.y - ab.x, dk[2 * r + g], dot);
-            off = fmaf(ab.x, qf.Q[g], off);
-          }
-          const float s = fmaf(dot, ck, off);
-          sc[sub][r] = valid(sub, r) ? s : -INFINITY;
+        for (int g = 0; g < NG; ++g) {
+          float x;
+          if (NP == 4)
+            x = (part & 2) ? ((part & 1) ? dk[1][2 + g] : dk[1][g])
+                           : ((part & 1) ? dk[0][2 + g] : dk[0][g]);
+          else if (NP == 2)
+            x = part ? dk[1][2 * j + g] : dk[0][2 * j + g];
+          else
+            x = dk[j >> 1][2 * (j & 1) + g];
+          const float2 ab = unpack_h2(ka[g]);
+          dot = fmaf(ab.y - ab.x, x, dot);
+          off = fmaf(ab.x, qf.Q[g], off);
         }
+        const float s = fmaf(dot, ck, off);
+        sc[j] = valid[j] ? s : -INFINITY;
       }
       // The reference maximum moves only when a score exceeds it by more than 2^2, so that p <= 4
       // and the fp16 weight p (b - a) / 15 cannot overflow (131008 / 15 * 4 < 65504).
-      float mloc = fmaxf(sc[0][0], sc[0][1]);
+      float mloc = sc[0];
 #pragma unroll
-      for (int sub = 1; sub < kSub; ++sub) mloc = fmaxf(mloc, fmaxf(sc[sub][0], sc[sub][1]));
+      for (int j = 1; j < RPL; ++j) mloc = fmaxf(mloc, sc[j]);
       if (__any_sync(0xFFFFFFFFu, mloc > m_run + 2.0f)) {
         float mx = fmaxf(mloc, m_run);
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+#pragma unroll
+        for (int o = HEADS; o < 32; o <<= 1)            // over parts and gid
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
         const float corr = (m_run == -INFINITY) ? 0.0f : ex2(m_run - mx);
         l_run *= corr;
 #pragma unroll
         for (int g = 0; g < NG; ++g) asum[g] *= corr;
-        // acc column 2 tig + g belongs to head tig as well
 #pragma unroll
-        for (int u = 0; u < 2 * NW; ++u)
+        for (int u = 0; u < 2 * NW; ++u)                // columns 2 tig, 2 tig + 1: the same head
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[u][c] *= corr;
         m_run = mx;
       }
       const float m_ref = (m_run == -INFINITY) ? 0.0f : m_run;
-      float p[kSub][2];
+      uint32_t wt[RPL];                     // weights p (b - a) / 15 of both groups, transposed:
+#pragma unroll                              // column (part, head, group) x the half's 8 rows
+      for (int j = 0; j < RPL; ++j) {
+        const int row = 8 * (part * RPL + j) + gid;
+        uint32_t va[NG];
+        load_words<NG>(slot + R::VAB_OFF + row * R::ROW_AB, va);
+        const float p = ex2(sc[j] - m_ref);
+        l_run += p;
+        const float p15 = p * (1.0f / 15.0f);
+        float w[2];
 #pragma unroll
-      for (int sub = 0; sub < kSub; ++sub) {
-        p[sub][0] = ex2(sc[sub][0] - m_ref);
-        p[sub][1] = ex2(sc[sub][1] - m_ref);
-        l_run += p[sub][0] + p[sub][1];
+        for (int g = 0; g < NG; ++g) {
+          const float2 ab = unpack_h2(valid[j] ? va[g] : 0u);
+          w[g] = p15 * (ab.y - ab.x);
+          asum[g] = fmaf(p, ab.x, asum[g]);
+        }
+        wt[j] = movtrans(pack_h2(w[0], NG == 2 ? w[NG - 1] : w[0]));
       }
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
-        uint32_t vw[2][NW], wrow[2];
+        uint32_t vw[2][NW], bv[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = sub * kTilePos + gid + 8 * r;
-          uint32_t va[NG];
-          load_words<NW>(slot + R::V_OFF + row * R::ROW_CODE + tig * 4 * NW, vw[r]);
-          load_words<NG>(slot + R::VAB_OFF + row * R::ROW_AB, va);
-          const float p15 = p[sub][r] * (1.0f / 15.0f);
-          float wt[2];
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float2 ab = unpack_h2(valid(sub, r) ? va[g] : 0u);
-            wt[g] = p15 * (ab.y - ab.x);
-            asum[g] = fmaf(p[sub][r], ab.x, asum[g]);
-          }
-          wrow[r] = pack_h2(wt[0], NG == 2 ? wt[NG - 1] : wt[0]);
+          const int rh = 2 * sub + r;
+          load_words<NW>(slot + R::V_OFF + (8 * rh + gid) * R::ROW_CODE + tig * 4 * NW, vw[r]);
+          bv[r] = (NP == 1 || (gid >> 1) / HEADS == rh / RPL) ? wt[rh % RPL] : 0u;
         }
-        // rows x (head, group) -> the B operand: (head, group) x rows
-        const uint32_t bv0 = movtrans(wrow[0]), bv1 = movtrans(wrow[1]);
 #pragma unroll
         for (int wd = 0; wd < NW; ++wd) {
           uint32_t c0[4], c1[4];
           q4attn::code_pairs(movtrans(vw[0][wd]), c0);
           q4attn::code_pairs(movtrans(vw[1][wd]), c1);
-          mma16816(acc[2 * wd], c0[0], c0[1], c1[0], c1[1], bv0, bv1);
-          mma16816(acc[2 * wd + 1], c0[2], c0[3], c1[2], c1[3], bv0, bv1);
+          mma16816(acc[2 * wd], c0[0], c0[1], c1[0], c1[1], bv[0], bv[1]);
+          mma16816(acc[2 * wd + 1], c0[2], c0[3], c1[2], c1[3], bv[0], bv[1]);
         }
       }
     };
 
-    while (cc.u < u1) {
-      const int cnt = slot_tiles(cc.s, cc.u, u1, kSub), ts = tile_pos(cc.s, cc.u);
-      ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar0 + 8 * cs, cph, kErrWait));
-      if (!ok) break;
-      const uint8_t* slot = ring + cs * R::SLOT;
-      const int te = ts + kSlotPos;
-      if (cnt == kSub && te <= cc.s.len && (ts >= cc.s.wstart || te <= a.sinks))
-        process(slot, ts, cnt, std::false_type{});
-      else
-        process(slot, ts, cnt, std::true_type{});
-      __syncwarp();                         // every lane has read the slot: refill it
-      issue();
-      ++consumed;
-      if (++cs == kRing) {
-        cs = 0;
-        cph ^= 1u;
+    while (cc.u < u1 && ok) {
+      int run = run_tiles(cc.s, cc.u, u1), ts = tile_pos(cc.s, cc.u);
+      cc.u += run;
+      for (; run > 0; run -= kSub, ts += kSlotPos) {
+        ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar0 + 8 * cs, cph, kErrWait));
+        if (!ok) break;
+        const uint8_t* slot = ring + cs * R::SLOT;
+        const int te = ts + kSlotPos;
+        if (run >= kSub && te <= cc.s.len && (ts >= cc.s.wstart || te <= a.sinks))
+          process(slot, ts, kSub, std::false_type{});
+        else
+          process(slot, ts, min(run, kSub), std::true_type{});
+        __syncwarp();                       // every lane has read the slot: refill it
+        issue();
+        ++consumed;
+        if (++cs == kRing) {
+          cs = 0;
+          cph ^= 1u;
+        }
       }
-      cc.u += cnt;
     }
     if (!ok) break;
 
-    // ---- end of the segment
+    // ---- end of the segment: sums over the rows' lanes and the parts
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
+    for (int o = HEADS; o < 32; o <<= 1) {
       l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, o);
 #pragma unroll
       for (int g = 0; g < NG; ++g) asum[g] += __shfl_xor_sync(0xFFFFFFFFu, asum[g], o);
     }
-    if (tig < heads) {
-      const int g = (NG == 2) ? (gid >> 2) : 0;        // group of the lane's channels
-      const float A = (NG == 2 && g) ? asum[NG - 1] : asum[0];
-      const int cbase = 8 * NW * (gid >> 1) + 4 * (gid & 1);
-      const float inv = (l_run == 0.0f) ? 0.0f : 1.0f / l_run;
-      uint16_t* o = a.out + cc.b * a.out_stride + (int64_t)(hq + tig) * D;
-      float* pp = a.partial + ((int64_t)(2 * w + (seg_no > 0)) * kHeads + tig) * (D + 2);
+    // the lane's channels are those of group gid / 4 (d = 128): pair u holds channels cbase + 8 (u /
+    // 2) + 2 (u % 2) and the next
+    const int g = (NG == 2) ? (gid >> 2) : 0;
+    const float A = (NG == 2 && g) ? asum[NG - 1] : asum[0];
+    const int cbase = 8 * NW * (gid >> 1) + 4 * (gid & 1);
+    float2 y[2 * NW];
 #pragma unroll
-      for (int u = 0; u < 2 * NW; ++u) {
-        const int ch = cbase + 8 * (u >> 1) + 2 * (u & 1);
-        const float y0 = fmaf(g ? acc[u][1] : acc[u][0], 16777216.0f, A);
-        const float y1 = fmaf(g ? acc[u][3] : acc[u][2], 1048576.0f, A);
+    for (int u = 0; u < 2 * NW; ++u)
+      y[u] = make_float2((g ? acc[u][1] : acc[u][0]) * 16777216.0f,
+                         (g ? acc[u][3] : acc[u][2]) * 1048576.0f);
+    // each halving of the parts leaves half of the pairs to a lane: pairs u0 .. u0 + NY - 1
+    constexpr int NY = 2 * NW / NP;
+    int u0 = 0;
+#pragma unroll
+    for (int n = NW, o = 2; o >= HEADS; n >>= 1, o >>= 1) {
+      const bool up = tig & o;
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+        const float2 keep = up ? y[u + n] : y[u], send = up ? y[u] : y[u + n];
+        y[u].x = keep.x + __shfl_xor_sync(0xFFFFFFFFu, send.x, o);
+        y[u].y = keep.y + __shfl_xor_sync(0xFFFFFFFFu, send.y, o);
+      }
+      u0 += up ? n : 0;
+    }
+    const int head = tig % HEADS;
+    if (head < heads) {
+      const float inv = (l_run == 0.0f) ? 0.0f : 1.0f / l_run;
+      uint16_t* o = a.out + cc.b * a.out_stride + (int64_t)(hq + head) * D;
+      float* pp = a.partial + ((int64_t)(2 * w + (seg_no > 0)) * HEADS + head) * (D + 2);
+#pragma unroll
+      for (int i = 0; i < NY; ++i) {
+        const int ch = cbase + 8 * ((u0 + i) >> 1) + 2 * ((u0 + i) & 1);
+        const float y0 = y[i].x + A, y1 = y[i].y + A;
         if (whole)
-          *reinterpret_cast<uint32_t*>(o + ch) = pack_h2(in_range(y0 * inv), in_range(y1 * inv));
+          *reinterpret_cast<uint32_t*>(o + ch) =
+              pack_h2(in_range(y0 * inv), in_range(y1 * inv));
         else
           *reinterpret_cast<float2*>(pp + ch) = make_float2(y0, y1);
       }
-      if (!whole && gid == 0) *reinterpret_cast<float2*>(pp + D) = make_float2(m_run, l_run);
+      if (!whole && gid == 0 && part == 0)
+        *reinterpret_cast<float2*>(pp + D) = make_float2(m_run, l_run);
     }
     __syncwarp();
     left -= seg;
@@ -503,35 +597,48 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
     bounded_wait(bar0 + 8 * (uint32_t)(i % kRing), (uint32_t)((i / kRing) & 1), kErrDrain);
 }
 
-// One warp per (cut, head of its row set): merges the pieces (m, l, unnormalised o) in order.
-template <int D>
-__global__ void __launch_bounds__(kHeads * 32)
+// One warp per (cut, head of its row set): merges the pieces (m, l, unnormalised o) in order,
+// 32 at a time: a lane takes one piece's m and l, then all lanes that piece's channels.
+template <int D, int HEADS>
+__global__ void __launch_bounds__(HEADS * 32)
 merge_kernel(const Args a) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int C = D / 32;
   const Cut cut = a.cuts[blockIdx.x];
   const int head = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (cut.pieces == 0 || head >= cut.heads) return;
   auto piece = [&](int i) {
     const int slot = i == 0 ? cut.prev_slot : 2 * ((int)blockIdx.x + i - 1);
-    return a.partial + ((int64_t)slot * kHeads + head) * (D + 2);
+    return a.partial + ((int64_t)slot * HEADS + head) * (D + 2);
   };
-  float M = -INFINITY;
-  for (int i = lane; i < cut.pieces; i += 32) M = fmaxf(M, piece(i)[D]);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  if (M == -INFINITY) M = 0.0f;
-  constexpr int C = D / 32;
-  float L = 0.0f, o[C];
+  float M = -INFINITY, L = 0.0f, o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < cut.pieces; ++i) {
-    const float* pp = piece(i);
-    const float wgt = exp2f(pp[D] - M);
-    L = fmaf(wgt, pp[D + 1], L);
+  for (int i0 = 0; i0 < cut.pieces; i0 += 32) {
+    const int n = min(32, cut.pieces - i0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (lane < n) ml = *reinterpret_cast<const float2*>(piece(i0 + lane) + D);
+    float mx = ml.x;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(wgt, pp[c * 32 + lane], o[c]);
+    for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+    mx = fmaxf(mx, M);
+    const float ref = (mx == -INFINITY) ? 0.0f : mx;
+    const float corr = exp2f(M - ref), wgt = exp2f(ml.x - ref);
+    float l = wgt * ml.y;                   // 0 * NaN where a piece is NaN: as it should be
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
+    L = fmaf(L, corr, l);
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= corr;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float* pp = piece(i0 + i);
+      const float wi = __shfl_sync(0xFFFFFFFFu, wgt, i);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = fmaf(wi, pp[c * 32 + lane], o[c]);
+    }
+    M = mx;
   }
   const float inv = (L == 0.0f) ? 0.0f : 1.0f / L;
   uint16_t* op = a.out + cut.b * a.out_stride + (int64_t)(cut.hq + head) * D;
@@ -544,14 +651,13 @@ int64_t most_tiles(const fg_kvcache& kv, int nhb, int window, int sinks) {
   const SeqTiles s = seq_tiles(kv.cap, window, sinks);
   return (int64_t)kv.B * kv.H * nhb * (s.nt + 2);
 }
-int grid_ctas(const fg_kvcache& kv, int nhb, int window, int sinks, int nsm) {
-  const int64_t want = most_tiles(kv, nhb, window, sinks) / (kMinTiles * kWarps) + 1;
-  return (int)std::min<int64_t>(want, (int64_t)nsm * kCtasPerSm);
+int grid_ctas(int64_t most, int nsm) {
+  return (int)std::min<int64_t>(most / kMinTiles + 1, std::max(nsm, 1));
 }
-size_t cut_bytes(int ctas) { return ((size_t)ctas * kWarps * sizeof(Cut) + 255) / 256 * 256; }
+size_t cut_bytes(int64_t ncuts) { return ((size_t)ncuts * sizeof(Cut) + 255) / 256 * 256; }
 
 // Shared memory and carveout of the kernel on the current device, set once per device.
-template <int D>
+template <int D, int NP>
 cudaError_t prepare() {
   static std::mutex mu;
   static bool done[64] = {};
@@ -560,54 +666,65 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(mu);
   if (dev < 0 || dev >= 64 || done[dev]) return cudaSuccess;
-  if ((e = cudaFuncSetAttribute(decode_window_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto* kernel = decode_window_kernel<D, NP>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Ring<D>::CTA_BYTES)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(decode_window_kernel<D>,
-                                cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) !=
+          cudaSuccess)
     return e;
   done[dev] = true;
   return cudaSuccess;
 }
 
-template <int D>
+template <int D, int NP>
 cudaError_t launch_d(const Args& a, const fg_kvcache& kv, int ctas, cudaStream_t st) {
-  cudaError_t e = prepare<D>();
+  cudaError_t e = prepare<D, NP>();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_window_kernel<D>, dim3(ctas), dim3(kWarps * 32), Ring<D>::CTA_BYTES, st, a,
-                 kv);
+  e = launch_pdl(decode_window_kernel<D, NP>, dim3(ctas), dim3(Ring<D>::WARPS * 32),
+                 Ring<D>::CTA_BYTES, st, a, kv);
   if (e != cudaSuccess) return e;
-  return launch_pdl(merge_kernel<D>, dim3(ctas * kWarps), dim3(kHeads * 32), 0, st, a);
+  return launch_pdl(merge_kernel<D, 4 / NP>, dim3(a.ncuts), dim3(4 / NP * 32), 0, st, a);
 }
 
-int head_blocks(int G) { return (G + kHeads - 1) / kHeads; }
+int warps_of(int d) { return d == 128 ? Ring<128>::WARPS : Ring<64>::WARPS; }
+// Query heads of a row set: 1, 2 or 4.
+int set_heads(int G) { return G < 3 ? G : 4; }
 
 }  // namespace
 
 size_t decode_attn_window_ws_bytes(const fg_kvcache& kv, int32_t Hq) {
-  const int ctas = grid_ctas(kv, head_blocks(Hq / kv.H), 0, 0, kMaxSms);
-  return cut_bytes(ctas) + (size_t)ctas * kWarps * 2 * kHeads * (kv.h / kv.H + 2) * sizeof(float);
+  const int G = Hq / kv.H, heads = set_heads(G);
+  const int64_t n = (int64_t)grid_ctas(most_tiles(kv, (G + heads - 1) / heads, 0, 0), kMaxSms) *
+                    warps_of(kv.h / kv.H);
+  return cut_bytes(n) + (size_t)n * 2 * heads * (kv.h / kv.H + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_attn_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
                                       const fg_kvcache& kv, const int32_t* lens, int32_t window,
                                       int32_t sinks, float scale, uint16_t* out,
                                       int64_t out_stride, void* ws, int nsm, cudaStream_t st) {
+  const int G = Hq / kv.H, heads = set_heads(G);
   Args a;
   a.q = q;
   a.lens = lens;
   a.out = out;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  a.G = Hq / kv.H;
-  a.nhb = head_blocks(a.G);
+  a.G = G;
+  a.nhb = (G + heads - 1) / heads;
   a.window = window;
   a.sinks = sinks;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const int ctas = std::min(grid_ctas(kv, a.nhb, window, sinks, nsm),
-                            grid_ctas(kv, a.nhb, 0, 0, kMaxSms));
+  const int64_t most = std::min(most_tiles(kv, a.nhb, window, sinks), most_tiles(kv, a.nhb, 0, 0));
+  const int ctas = grid_ctas(most, nsm);
+  a.ncuts = ctas * warps_of(kv.h / kv.H);
   a.cuts = static_cast<Cut*>(ws);
-  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + cut_bytes(ctas));
-  return kv.h / kv.H == 128 ? launch_d<128>(a, kv, ctas, st) : launch_d<64>(a, kv, ctas, st);
+  a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + cut_bytes(a.ncuts));
+  const bool wide = kv.h / kv.H == 128;
+  auto* launch = heads == 1   ? (wide ? launch_d<128, 4> : launch_d<64, 4>)
+                 : heads == 2 ? (wide ? launch_d<128, 2> : launch_d<64, 2>)
+                              : (wide ? launch_d<128, 1> : launch_d<64, 1>);
+  return launch(a, kv, ctas, st);
 }
 
 cudaError_t decode_window_read_error(unsigned int* out) {

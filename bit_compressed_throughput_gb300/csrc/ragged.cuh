@@ -68,28 +68,38 @@ FG_HD SeqTiles seq_tiles(int len, int window, int sinks) {
   s.nt = s.ns + te - s.tw;
   return s;
 }
-// Position of the first row of tile u (0 <= u < nt), and the tiles of a slot of at most `most`
-// that starts there: one run of positions inside tiles u .. u1-1.
+// Position of the first row of tile u (0 <= u < nt), and the tiles from there to u1 that are one run
+// of positions (either the first positions' or the window's).
 FG_HD int tile_pos(const SeqTiles& s, int u) {
   return (u < s.ns ? u : u - s.ns + s.tw) * kTilePos;
 }
-FG_HD int slot_tiles(const SeqTiles& s, int u, int u1, int most) {
-  const int end = (u < s.ns && s.ns < u1) ? s.ns : u1;
-  return end - u < most ? end - u : most;
+FG_HD int run_tiles(const SeqTiles& s, int u, int u1) {
+  return ((u < s.ns && s.ns < u1) ? s.ns : u1) - u;
 }
 
-// The tiles of a call in one order, cut evenly among nw workers: worker w takes tiles
-// first_tile(w) .. first_tile(w + 1) - 1 of `total`; worker_of_tile is the inverse.
-FG_HD int64_t first_tile(int64_t total, int nw, int w) {
-  return (total / nw) * w + (total % nw) * w / nw;
-}
-FG_HD int worker_of_tile(int64_t total, int nw, int64_t x) {
-  // (a guess within one, then the definition: total * nw may pass 64 bits)
-  int w = (int)((double)x / (double)total * nw);
-  w = w < 0 ? 0 : (w >= nw ? nw - 1 : w);
-  while (w > 0 && first_tile(total, nw, w) > x) --w;
-  while (w + 1 < nw && first_tile(total, nw, w + 1) <= x) ++w;
-  return w;
-}
+// `total` tiles in one order, cut evenly into n shares (n < 2^16): share i is tiles first(i) ..
+// first(i + 1) - 1; share_of is the inverse.
+struct Shares {
+  int64_t each;        // tiles per share, rounded down
+  int n, rest;         // shares; tiles left over
+  FG_HD Shares(int64_t total, int shares) : n(shares) {
+    if (total < (1ll << 32)) {             // a 32-bit division takes a fraction of the time
+      each = (uint32_t)total / (uint32_t)n;
+      rest = (int)((uint32_t)total % (uint32_t)n);
+    } else {
+      each = total / n;
+      rest = (int)(total % n);
+    }
+  }
+  FG_HD int64_t first(int i) const { return each * i + (unsigned)rest * (unsigned)i / (unsigned)n; }
+  FG_HD int share_of(int64_t x) const {
+    // a guess in binary32, then the definition
+    int i = (int)((float)x / ((float)each + (float)rest / (float)n));
+    i = i < 0 ? 0 : (i >= n ? n - 1 : i);
+    while (i > 0 && first(i) > x) --i;
+    while (i + 1 < n && first(i + 1) <= x) ++i;
+    return i;
+  }
+};
 
 }  // namespace fg

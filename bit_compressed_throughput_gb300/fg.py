@@ -121,8 +121,10 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream=None) -> Optional[int]:
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle of torch.cuda.current_stream(), without building a Stream object each call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # ----------------------------------------------------------------------------- containers
@@ -333,12 +335,12 @@ def _extents(name: str, t, n: int):
 def _one_device(stream, *tensors):
     """Every tensor on the device that the call launches on: the current one, and the stream's."""
     import torch
-    here = torch.device("cuda", torch.cuda.current_device())
-    bad = [t.device for t in tensors if t is not None and t.device != here]
-    if stream is not None and stream.device != here:
-        bad.append(stream.device)
-    if bad:
-        raise ValueError(f"tensor or stream on {bad[0]}, but the current device is {here}")
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
+    if stream is not None and stream.device.index != here:
+        raise ValueError(f"stream on {stream.device}, but the current device is cuda:{here}")
 
 
 def fg_kv_append_q4_ragged(k_new, v_new, row_off, pos, cache: KVCacheQ4, stream=None):

@@ -115,11 +115,11 @@ void h_seq_tiles(int len, int window, int sinks, int32_t* o) {
 int h_tile_pos(int len, int window, int sinks, int u) {
   return tile_pos(seq_tiles(len, window, sinks), u);
 }
-int h_slot_tiles(int len, int window, int sinks, int u, int u1, int most) {
-  return slot_tiles(seq_tiles(len, window, sinks), u, u1, most);
+int h_run_tiles(int len, int window, int sinks, int u, int u1) {
+  return run_tiles(seq_tiles(len, window, sinks), u, u1);
 }
-int64_t h_first_tile(int64_t total, int nw, int w) { return first_tile(total, nw, w); }
-int h_worker_of_tile(int64_t total, int nw, int64_t x) { return worker_of_tile(total, nw, x); }
+int64_t h_first_tile(int64_t total, int nw, int w) { return Shares(total, nw).first(w); }
+int h_share_of(int64_t total, int nw, int64_t x) { return Shares(total, nw).share_of(x); }
 int h_visible(int t, int i, int window, int sinks) { return visible(t, i, window, sinks); }
 }
 """
@@ -136,7 +136,7 @@ def host(tmp_path_factory):
     dll = C.CDLL(str(lib))
     dll.h_first_tile.argtypes = [C.c_int64, C.c_int, C.c_int]
     dll.h_first_tile.restype = C.c_int64
-    dll.h_worker_of_tile.argtypes = [C.c_int64, C.c_int, C.c_int64]
+    dll.h_share_of.argtypes = [C.c_int64, C.c_int, C.c_int64]
     return dll
 
 
@@ -185,8 +185,8 @@ def test_visible(host):
 
 
 def test_decode_tiles_are_the_visible_ones(host):
-    """The tiles of a sequence are those that hold a visible position, each once and in order; a
-    slot is one run of positions."""
+    """The tiles of a sequence are those that hold a visible position, each once and in order, in
+    at most two runs of positions."""
     from oracle import window as OW
     for n in (1, 15, 16, 17, 47, 48, 100, 161):
         for window in (0, 1, 2, 15, 16, 17, 40, 160, 2 ** 31 - 1):
@@ -198,12 +198,14 @@ def test_decode_tiles_are_the_visible_ones(host):
                 assert pos == [16 * t for t in want], (n, window, sinks)
                 assert o[1] == (max(0, n - window) if window else 0)
                 for u1 in range(1, len(pos) + 1):
-                    u = 0
+                    u = runs = 0
                     while u < u1:
-                        c = host.h_slot_tiles(n, window, sinks, u, u1, 3)
-                        assert 1 <= c <= 3 and u + c <= u1
+                        c = host.h_run_tiles(n, window, sinks, u, u1)
+                        assert 1 <= c and u + c <= u1
                         assert pos[u + c - 1] == pos[u] + 16 * (c - 1)
                         u += c
+                        runs += 1
+                    assert runs <= 2
     o = np.zeros(5, np.int32)
     for n in (0, 2 ** 31 - 16):                            # nothing, and the longest
         host.h_seq_tiles(n, 0, 0, o.ctypes.data_as(C.POINTER(C.c_int32)))
@@ -211,14 +213,14 @@ def test_decode_tiles_are_the_visible_ones(host):
 
 
 def test_worker_ranges(host):
-    """The ranges cover the order without gaps, differ by one tile at most, and worker_of_tile is
+    """The ranges cover the order without gaps, differ by one tile at most, and share_of is
     their inverse, for small and for very large totals."""
     for total, nw in ((1, 1), (7, 3), (576, 192), (5000, 2432), (2 ** 40 + 12345, 2432),
-                      (2 ** 55 + 1, 3072)):
+                      (2 ** 55 + 1, 24576)):
         first = [host.h_first_tile(total, nw, w) for w in range(nw + 1)]
         assert first[0] == 0 and first[-1] == total
         size = np.diff(np.array(first, dtype=object))
         assert min(size) >= total // nw and max(size) <= total // nw + 1
         for w in list(range(0, nw, max(1, nw // 50))) + [nw - 1]:
             for x in {first[w], first[w + 1] - 1}:
-                assert host.h_worker_of_tile(total, nw, x) == w, (total, nw, w)
+                assert host.h_share_of(total, nw, x) == w, (total, nw, w)
