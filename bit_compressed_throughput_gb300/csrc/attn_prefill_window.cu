@@ -1,16 +1,48 @@
 // Prefill attention over fp16 K/V rows of sequences of different lengths, with a sliding window,
-// first positions that stay visible, and query heads that share K/V heads (sm_103a).
+// first positions that stay visible, and query heads that share K/V heads, on the 5th-generation
+// tensor cores (sm_103a).
 //
 // Sequence b has nq = q_off[b+1] - q_off[b] query rows and nk = kv_off[b+1] - kv_off[b] K/V rows;
 // query row r is position i = nk - nq + r (the newest positions), and
 //   out_r,hq = sum_t softmax_t(scale * q_r,hq . k_t) v_t   over the t that i sees,
 // K/V head hq / G of G = Hq / Hkv query heads each; a row that sees nothing gets zeros.
 //
-// One warp per (query row, query head): a lane holds d/32 channels, one key at a time.
+// A CTA owns a block of 256 query rows of one (sequence, query head): two Q tiles of 128 rows that
+// share the K/V tiles of 128 keys.  The key tiles of a block are those that one of its rows sees
+// (first positions, then the window; key_tiles in ragged.cuh): a window costs what it shows, not the
+// sequence.  Q, K and V are read in place by TMA (boxes of 64 columns x 128 rows, 128B swizzle) at
+// the sequence's own rows, so a box may end in another sequence's rows or past the buffer (zeros);
+// such rows are masked or not stored.
+//   S = Q K^T     tcgen05.mma kind::f16, S (fp32) in TMEM
+//   softmax       two threads per query row, each over one half of the 128 key columns: base-2
+//                 online softmax with a lazily moved reference maximum (by more than 2^8),
+//                 P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that every row of the
+//                 Q tile sees in full are not masked; the others take a bit mask per row.
+//   O += P V      tcgen05.mma with P from TMEM
+// The warps' roles, the ring, TMEM and the ping-pong of the two Q tiles are those of the prefill
+// attention over equal prompts (attn_prefill_tc.cu); here a Q tile takes part only in the key tiles
+// that it sees, so "the next product" of a Q tile is looked up per key tile.
+//
+// Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it would
+// reach the rows of the Q tile that do not see it.  The output warps therefore test their rows of
+// O: a row with an infinity or a NaN is computed again on its own, over its visible keys alone
+// (attend_row), so that only what it sees can reach it.  Finite inputs never take that path.
+//
+// The work order: blocks by descending index, for each the sequences that have one (longest first),
+// for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read and
+// checked on the device, kMaxSeqs sequences per launch.
+//
+// Every mbarrier wait is bounded; on timeout the CTA sets the device error word (read by
+// fg_check_device_error), drains its copies and MMAs and frees TMEM.
 #include <math.h>
 
+#include <algorithm>
+#include <mutex>
+
+#include "attn_tc.cuh"
 #include "fg_common.cuh"
 #include "fg_internal.h"
+#include "gemm_tc.cuh"
 #include "ragged.cuh"
 
 namespace fg {
@@ -19,63 +51,768 @@ __device__ unsigned int g_prefill_window_error = 0;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int QB = 2 * QT;                  // query rows per block
+constexpr int STAGES = 2;                   // K/V ring
+constexpr int THREADS = 22 * 32;
+constexpr int W_SM = 2;                     // softmax warps 2..17: Q tile (w - 2) / 8, key half
+                                            // ((w - 2) / 4) & 1, TMEM lane quarter w % 4
+constexpr int W_OUT = 18;                   // first output warp (18..21)
+constexpr uint32_t TMEM_COLS = 512;
+constexpr long long kWaitCycles = 1ll << 34;   // attend_row may keep the other warps waiting
+constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
+constexpr int BOX = QT * 128;               // bytes of one 64-column x 128-row box
+constexpr int kMaxSeqs = 384;               // sequences per launch
+static_assert(kMaxSeqs <= THREADS, "one thread per sequence reads its offsets");
+
+struct Seq {
+  int q0, nq, k0, nk;                       // first query row, rows, first K/V row, rows
+};
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
-prefill_window_kernel(const PrefillWindow a) {
-  pdl_launch_dependents();
-  pdl_wait();
+struct PSmem {
+  static constexpr int TILE = (D / 64) * BOX;          // one Q, K or V tile
+  static constexpr int Q_OFF = 0;                      // Q_A, Q_B
+  static constexpr int K_OFF = 2 * TILE;               // K stages
+  static constexpr int V_OFF = K_OFF + STAGES * TILE;  // V stages
+  static constexpr int O_OFF = V_OFF + STAGES * TILE;  // one output box
+  static constexpr int L_OFF = O_OFF + BOX;            // row sums l [tile][key half][row]
+  static constexpr int MX_OFF = L_OFF + 2 * 2 * QT * 4;  // row maxima [parity][tile][half][row]
+  static constexpr int BAR_OFF = MX_OFF + 2 * 2 * 2 * QT * 4;
+  static constexpr int SEQ_OFF = BAR_OFF + 256;        // sequences, longest first
+  static constexpr int BYTES = SEQ_OFF + kMaxSeqs * (int)sizeof(Seq) + 1024;   // 1024: alignment
+};
+static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
+
+// barriers: q_full, q_free, kv_full[2], kv_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
+// l_full[2], o_staged, o_stage_free, drain, mx_ready[tile][quarter] (the two key halves of a
+// row have written their maxima)
+constexpr int B_QFULL = 0, B_QFREE = 1, B_KVFULL = 2, B_KVFREE = 4, B_SFULL = 6, B_PFULL = 8,
+              B_ODONE = 10, B_OFREE = 12, B_LFULL = 14, B_OSTAGED = 16, B_OSFREE = 17,
+              B_DRAIN = 18, B_MX = 19, NBARS = 27;
+static_assert(NBARS * 8 + 16 <= 256, "barrier space");
+
+__device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      atomicOr(&g_prefill_window_error, kErrWait);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (clock64() - t0 > kWaitCycles) {
+      atomicOr(&g_prefill_window_error, kErrDrain);
+      return;
+    }
+  }
+}
+
+// An output is a mean of values within fp16's range: what rounding carries past its end is put
+// back; infinities stay.
+__device__ __forceinline__ float in_range(float y) {
+  return fabsf(y) < 66000.0f ? fminf(fmaxf(y, -65504.0f), 65504.0f) : y;
+}
+
+// One row on its own, by a whole warp: position i of a sequence whose K/V rows start at k0; lane
+// l returns channels l D/32 ..  Scores are computed a key per lane, values a channel group per
+// lane; only visible keys are read.
+template <int D>
+__device__ __noinline__ void attend_row(const PrefillWindow& a, int64_t qrow, int hq, int k0, int i,
+                                        float (&o)[D / 32]) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && (!offsets_ok(a.q_off, a.nseq, a.q_rows, threadIdx.x, kThreads) ||
-                          !offsets_ok(a.kv_off, a.nseq, a.kv_rows, threadIdx.x, kThreads)))
-    atomicOr(&g_prefill_window_error, kErrExtent);
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (item >= (int64_t)a.q_rows * a.Hq) return;
-  const int row = (int)(item / a.Hq), hq = (int)(item - (int64_t)row * a.Hq);
-  const int b = sequence_of_row(a.q_off, a.nseq, row);
-  if (b < 0) return;
-  const int q0 = a.q_off[b], nq = a.q_off[b + 1] - q0;
-  const int k0 = a.kv_off[b], nk = a.kv_off[b + 1] - k0;
-  if (row < q0 || row >= q0 + nq || k0 < 0 || nk < 0 || k0 + nk > a.kv_rows) return;
-  const int i = nk - nq + (row - q0), hk = hq / (a.Hq / a.Hkv);
-  float qv[C], acc[C], m = -INFINITY, l = 0.0f;
+  const int64_t kcol = (int64_t)(hq / (a.Hq / a.Hkv)) * D;
+  const uint16_t* q = a.q + qrow * a.q_stride + (int64_t)hq * D;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  float m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    qv[c] = h2f(a.q[(int64_t)row * a.q_stride + hq * D + lane * C + c]) * a.scale;
-    acc[c] = 0.0f;
-  }
-  const int w0 = (a.window == 0) ? 0 : max(0, i + 1 - a.window);
-  for (int t = 0; t <= i; ++t) {
-    if (t < w0 && t >= a.sinks) {
-      t = w0 - 1;
-      continue;
+  for (int c = 0; c < C; ++c) o[c] = 0.0f;
+  if (i < 0) return;
+  const int w0 = (a.window == 0 || i < a.window) ? 0 : i - a.window + 1;
+  const int first = min(a.sinks, w0), n = first + (i + 1 - w0);   // visible keys
+  auto key_row = [&](int u) { return (int64_t)k0 + (u < first ? u : u - first + w0); };
+  for (int u0 = 0; u0 < n; u0 += 32) {
+    const int cnt = min(32, n - u0);
+    float s = -INFINITY;
+    if (lane < cnt) {
+      const uint16_t* k = a.k + key_row(u0 + lane) * a.kv_stride + kcol;
+      s = 0.0f;
+      for (int c = 0; c < D; c += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(q + c), y = ldg_nc_v4(k + c);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 xf = unpack_h2(xw[e]), yf = unpack_h2(yw[e]);
+          s = fmaf(xf.x, yf.x, fmaf(xf.y, yf.y, s));
+        }
+      }
+      s *= sl2;
     }
-    const int64_t at = (int64_t)(k0 + t) * a.kv_stride + hk * D + lane * C;
-    float s = 0.0f;
+    float mx = s;
 #pragma unroll
-    for (int c = 0; c < C; ++c) s = fmaf(qv[c], h2f(a.k[at + c]), s);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const float mn = fmaxf(m, s);
-    const float corr = (m == -INFINITY) ? 0.0f : expf(m - mn), p = expf(s - mn);
+    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+    mx = fmaxf(mx, m);
+    const float ref = (mx == -INFINITY) ? 0.0f : mx;
+    const float corr = exp2f(m - ref), p = lane < cnt ? exp2f(s - ref) : 0.0f;
     l = l * corr + p;
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = fmaf(acc[c], corr, p * h2f(a.v[at + c]));
-    m = mn;
+    for (int c = 0; c < C; ++c) o[c] *= corr;
+    for (int j = 0; j < cnt; ++j) {
+      const float pj = __shfl_sync(0xFFFFFFFFu, p, j);
+      const uint16_t* v = a.v + key_row(u0 + j) * a.kv_stride + kcol + lane * C;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = fmaf(pj, h2f(v[c]), o[c]);
+    }
+    m = mx;
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    a.out[(int64_t)row * a.out_stride + hq * D + lane * C + c] = f2h(i >= 0 ? acc[c] / l : 0.0f);
+  for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = in_range(o[c] / l);
+}
+
+struct PArgs {
+  PrefillWindow w;
+  int s0, ns;                               // sequences s0 .. s0 + ns - 1 of the call
+  float scale_log2;
+};
+
+// The place of an item in the work order, and the item: block qb of sequence `seq` (an index into
+// the sequences in shared memory, longest first) and query head hq.
+struct Cursor {
+  int level, cnt, i;                        // block index; sequences that have it; item within it
+};
+struct Item {
+  Seq s;
+  int hq, q0;
+  KeyTiles t[2], u;                         // the Q tiles' key tiles, and their union
+};
+__device__ __forceinline__ int blocks_of(int nq) { return (nq + QB - 1) / QB; }
+// How many of the sequences (longest first) have a block `level`.
+__device__ __forceinline__ int level_count(const Seq* seqs, int n, int level) {
+  int lo = 0, hi = n;                       // seqs[lo - 1] has it, seqs[hi] does not
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (blocks_of(seqs[mid].nq) > level) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+// Moves n items on; false past the last.
+__device__ __forceinline__ bool advance(Cursor& c, int n, const Seq* seqs, int nseq, int Hq) {
+  int64_t i = (int64_t)c.i + n;
+  while (c.level >= 0 && i >= (int64_t)c.cnt * Hq) {
+    i -= (int64_t)c.cnt * Hq;
+    if (--c.level >= 0) c.cnt = level_count(seqs, nseq, c.level);
+  }
+  c.i = (int)i;
+  return c.level >= 0;
+}
+__device__ __forceinline__ Cursor first_item(const Seq* seqs, int nseq) {
+  Cursor c;
+  c.level = nseq > 0 ? blocks_of(seqs[0].nq) - 1 : -1;
+  c.cnt = c.level >= 0 ? level_count(seqs, nseq, c.level) : 0;
+  c.i = 0;
+  return c;
+}
+__device__ __forceinline__ Item item_at(const Cursor& c, const Seq* seqs, const PrefillWindow& w) {
+  Item it;
+  const int b = c.i / w.Hq;
+  it.hq = c.i - b * w.Hq;
+  it.s = seqs[b];
+  it.q0 = c.level * QB;
+  it.t[0] = key_tiles(it.q0, it.s.nq, it.s.nk, w.window, w.sinks);
+  it.t[1] = key_tiles(it.q0 + QT, it.s.nq, it.s.nk, w.window, w.sinks);
+  it.u = either(it.t[0], it.t[1]);
+  return it;
+}
+
+// Persistent: CTA c takes items c, c + gridDim, ...  The producer loads the next item's Q as
+// soon as the current item's last S product is done and streams K/V through the ring across
+// items; the MMA issuer starts the next item's S products while the current item's last P V
+// products run, and the output warps store an item's O while the softmax warps work on the next.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmO, const __grid_constant__ PArgs pa) {
+  using L = PSmem<D>;
+  constexpr int NB = D / 64;                           // 64-column boxes per tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* live = reinterpret_cast<int*>(tmem_slot + 2);   // sequences with rows
+  Seq* seqs = reinterpret_cast<Seq*>(smem + L::SEQ_OFF);
+  float* l_buf = reinterpret_cast<float*>(smem + L::L_OFF);
+  float* mx_buf = reinterpret_cast<float*>(smem + L::MX_OFF);
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PrefillWindow& w = pa.w;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_QFULL), 1);
+    mbar_init(bar(B_QFREE), 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(bar(B_KVFULL + i), 1);
+      mbar_init(bar(B_KVFREE + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(B_SFULL + t), 1);
+      mbar_init(bar(B_PFULL + t), 8);                  // one arrival per softmax warp
+      mbar_init(bar(B_ODONE + t), 1);
+      mbar_init(bar(B_OFREE + t), 4);                  // one arrival per output warp
+      mbar_init(bar(B_LFULL + t), 8);                  // one arrival per softmax warp
+      for (int q = 0; q < 4; ++q) mbar_init(bar(B_MX + 4 * t + q), 2);   // both key halves
+    }
+    mbar_init(bar(B_OSTAGED), 4);                      // one arrival per output warp
+    mbar_init(bar(B_OSFREE), 1);
+    mbar_init(bar(B_DRAIN), 1);
+    *abort_flag = 0;
+    *live = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- the sequences, longest first (by query rows, then by index).  The ones whose offsets do
+  // not fit their buffers count as empty.  l_buf and mx_buf hold the unsorted rows meanwhile.
+  Seq me{0, 0, 0, 0};
+  int* nq_all = reinterpret_cast<int*>(l_buf);         // kMaxSeqs ints: within l_buf
+  static_assert(kMaxSeqs * 4 <= 2 * 2 * QT * 4, "the row sums' buffer holds the lengths");
+  if (threadIdx.x < kMaxSeqs) {
+    if ((int)threadIdx.x < pa.ns) {
+      const int b = pa.s0 + threadIdx.x;
+      const int q0 = w.q_off[b], q1 = w.q_off[b + 1], k0 = w.kv_off[b], k1 = w.kv_off[b + 1];
+      if (q0 >= 0 && q0 <= q1 && q1 <= w.q_rows && k0 >= 0 && k0 <= k1 && k1 <= w.kv_rows)
+        me = Seq{q0, q1 - q0, k0, k1 - k0};
+      else if (blockIdx.x == 0)
+        atomicOr(&g_prefill_window_error, kErrExtent);
+    }
+    nq_all[threadIdx.x] = me.nq;
+  }
+  __syncthreads();
+  if (me.nq > 0) {
+    int rank = 0;
+    for (int b = 0; b < pa.ns; ++b)
+      rank += nq_all[b] > me.nq || (nq_all[b] == me.nq && b < (int)threadIdx.x);
+    seqs[rank] = me;
+    atomicAdd(live, 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int nseq = *live;
+  // TMEM columns: S_A 0..127, S_B 128..255, O_A 256.., O_B 256 + D..
+  auto s_col = [&](int t) { return (uint32_t)(t * KT); };
+  auto o_col = [&](int t) { return (uint32_t)(2 * KT + t * D); };
+  Cursor cur = first_item(seqs, nseq);
+  bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
+  auto next = [&]() { have = advance(cur, gridDim.x, seqs, nseq, w.Hq); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int kvg = 0, qn = 0;                             // K/V tiles, Q pairs issued
+      bool ok = true;
+      for (; have && ok; next()) {
+        const Item it = item_at(cur, seqs, w);
+        const int nkv = it.u.count();
+        if (nkv == 0) continue;
+        const int hk = it.hq / (w.Hq / w.Hkv);
+        // the previous item's S products are done with the Q tiles
+        if (qn > 0 && !bwait(bar(B_QFREE), (uint32_t)((qn - 1) & 1), abort_flag)) break;
+        mbar_expect_tx(bar(B_QFULL), (uint32_t)(2 * L::TILE));
+        for (int t = 0; t < 2; ++t)
+          for (int c = 0; c < NB; ++c)
+            tma_load_2d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ,
+                        it.hq * D + 64 * c, it.s.q0 + it.q0 + t * QT, bar(B_QFULL));
+        ++qn;
+        for (int j = 0; j < nkv; ++j, ++kvg) {
+          const int st = kvg % STAGES;
+          if (kvg >= STAGES &&
+              !bwait(bar(B_KVFREE + st), (uint32_t)(((kvg / STAGES) & 1) ^ 1), abort_flag)) {
+            ok = false;
+            break;
+          }
+          const int row = it.s.k0 + it.u.tile(j) * KT;
+          mbar_expect_tx(bar(B_KVFULL + st), (uint32_t)(2 * L::TILE));
+          for (int c = 0; c < NB; ++c) {
+            tma_load_2d(smem_u32(smem + L::K_OFF + st * L::TILE + c * BOX), &tmK,
+                        hk * D + 64 * c, row, bar(B_KVFULL + st));
+            tma_load_2d(smem_u32(smem + L::V_OFF + st * L::TILE + c * BOX), &tmV,
+                        hk * D + 64 * c, row, bar(B_KVFULL + st));
+          }
+        }
+      }
+      // every issued copy has landed before the CTA exits
+      if (qn > 0) drain_wait(bar(B_QFULL), (uint32_t)((qn - 1) & 1));
+      for (int i = max(0, kvg - STAGES); i < kvg; ++i)
+        drain_wait(bar(B_KVFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t qbase = smem_u32(smem + L::Q_OFF), kbase = smem_u32(smem + L::K_OFF),
+                     vbase = smem_u32(smem + L::V_OFF);
+      const uint32_t idesc_o = idesc_pv(D);
+      bool ok = true, issued = false;
+      int kvg = 0, qn = 0;                             // K/V tiles, items consumed
+      int pc[2] = {0, 0}, uses[2] = {0, 0};            // P V products; items, per Q tile
+      // S_t = Q_t K^T of K/V tile g over K = D: k-step i reads 16 columns, 32 bytes into box
+      // i / 4
+      auto issue_s = [&](int t, int g) {
+        const int st = g % STAGES;
+        const uint64_t qd = smem_desc(qbase + t * L::TILE, 16, 1024);
+        const uint64_t kd = smem_desc(kbase + st * L::TILE, 16, 1024);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
+          umma_f16(tmem + s_col(t), qd + off, kd + off, kIdescS, i > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(B_SFULL + t));
+      };
+      // O_t (+)= P_t V of K/V tile g over K = 128 keys: k-step i reads the 8 TMEM columns of
+      // P of keys 16i.. (key half i / 4 keeps its P in the first 32 of its 64 S columns) and
+      // rows 16i.. of V (2048 bytes per step in its MN-major 128B-swizzled layout)
+      auto issue_pv = [&](int t, int g, bool first) {
+        const int st = g % STAGES;
+        const uint64_t vd = smem_desc(vbase + st * L::TILE, BOX, 1024);
+#pragma unroll
+        for (int i = 0; i < KT / 16; ++i)
+          umma_ts(tmem + o_col(t), tmem + s_col(t) + 64 * (i >> 2) + 8 * (i & 3),
+                  vd + (uint64_t)(i * 128), idesc_o, (!first || i > 0) ? 1u : 0u);
+        umma_commit(bar(B_ODONE + t));
+      };
+      auto wait_kv = [&](int g) {
+        if (!bwait(bar(B_KVFULL + g % STAGES), (uint32_t)((g / STAGES) & 1), abort_flag))
+          return false;
+        tc_fence_after();
+        return true;
+      };
+      for (; have && ok; next()) {
+        const Item it = item_at(cur, seqs, w);
+        const int nkv = it.u.count();
+        if (nkv == 0) continue;
+        if (!bwait(bar(B_QFULL), (uint32_t)(qn & 1), abort_flag) || !wait_kv(kvg)) break;
+        ++qn;
+        bool begun[2] = {false, false};                // Q tile t has a P V product of this item
+        for (int t = 0; t < 2; ++t)
+          if (it.t[t].has(it.u.tile(0))) issue_s(t, kvg);
+        issued = true;
+        if (nkv == 1) umma_commit(bar(B_QFREE));       // every S product of the item issued
+        for (int j = 0; j < nkv && ok; ++j) {
+          const int g = kvg + j, tile = it.u.tile(j), tile_n = j + 1 < nkv ? it.u.tile(j + 1) : -1;
+          bool next_ready = false;                     // K/V of tile j + 1 waited for
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (it.t[t].has(tile)) {
+              if (!bwait(bar(B_PFULL + t), (uint32_t)(pc[t] & 1), abort_flag)) {
+                ok = false;
+                break;
+              }
+              // the first product of an item overwrites O_t: the output warps have read it
+              if (!begun[t] && uses[t] > 0 &&
+                  !bwait(bar(B_OFREE + t), (uint32_t)((uses[t] - 1) & 1), abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_pv(t, g, !begun[t]);
+              if (!begun[t]) ++uses[t];
+              begun[t] = true;
+              ++pc[t];
+            }
+            // S_t of the next key tile: its columns hold no P that is still to be read (this Q
+            // tile's earlier products were issued before)
+            if (tile_n >= 0 && it.t[t].has(tile_n)) {
+              if (!next_ready && !wait_kv(g + 1)) {
+                ok = false;
+                break;
+              }
+              next_ready = true;
+              issue_s(t, g + 1);
+            }
+          }
+          if (!ok) break;
+          if (j == nkv - 2) umma_commit(bar(B_QFREE));      // the item's last S products
+          umma_commit(bar(B_KVFREE + g % STAGES));     // K/V tile g read by every MMA above
+        }
+        kvg += nkv;
+      }
+      // the CTA frees TMEM only after every MMA issued here has completed
+      if (issued) {
+        umma_commit(bar(B_DRAIN));
+        drain_wait(bar(B_DRAIN), 0u);
+      }
+    }
+  } else if (warp >= W_SM && warp < W_OUT) {
+    // ------------------------------------------------------------ softmax: one key half of
+    // one Q tile's rows.  Two threads per row: half c takes key columns 64c .. 64c + 63 of each
+    // S tile, the row maximum is exchanged through shared memory (mx_ready barrier of the two
+    // warps of a lane quarter), and half c writes its P over the first 32 of its own S columns
+    // and rescales O columns c d/2 ..
+    const int t = (warp - W_SM) >> 3, c = ((warp - W_SM) >> 2) & 1;
+    const int quarter = warp & 3;                      // TMEM lanes 32 quarter ..
+    const int m = 32 * quarter + lane;                 // row within the Q tile
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t srow = lane_addr + s_col(t) + 64 * c;
+    const uint32_t mxb = bar(B_MX + 4 * t + quarter);
+    const float sl2 = pa.scale_log2;
+    int sc = 0, uses = 0;                              // S products consumed, items finished
+    bool ok = true;
+    // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them is
+    // decided for the whole warp, waits included (a lane that gave up takes its warp along);
+    // both halves of a row take the same decisions (the same maximum)
+    for (; have && ok; next()) {
+      const Item it = item_at(cur, seqs, w);
+      const KeyTiles kt = t ? it.t[1] : it.t[0];
+      const int nt = kt.count();
+      if (nt == 0) continue;
+      // positions: this row's, and those of the Q tile's first and last row with one
+      const int base = it.s.nk - it.s.nq + it.q0 + t * QT;
+      const int pos = min(base + m, it.s.nk - 1);
+      const int plo = base, phi = min(base + QT, it.s.nk) - 1;
+      float m_ref = -INFINITY, l_sum = 0.0f;           // l over this half's keys
+      for (int j = 0; j < nt; ++j, ++sc) {
+        const bool got = bwait(bar(B_SFULL + t), (uint32_t)(sc & 1), abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // masked: some row of the Q tile does not see every key of the tile (warp-uniform)
+        const int k0 = kt.tile(j) * KT;
+        const bool masked = k0 + KT - 1 > plo ||
+                            (w.window != 0 && phi >= w.window && k0 <= phi - w.window &&
+                             k0 + KT > w.sinks);
+        uint32_t vis[2] = {~0u, ~0u};
+        if (masked) {
+          vis[0] = visible_bits(k0 + 64 * c, pos, w.window, w.sinks);
+          vis[1] = visible_bits(k0 + 64 * c + 32, pos, w.window, w.sinks);
+        }
+        // pass 1: this half's maximum, 32 columns at a time (the second load in flight)
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto max_chunk = [&](float (&v)[32], int c2) {
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (vis[c2] >> e & 1u) ? v[e] : -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], v[e], v[e + 1]);
+        };
+        {
+          float va[32], vb[32];
+          tmem_ld32(srow, va);
+          tmem_wait_ld_dep(va);
+          tmem_ld32(srow + 32, vb);
+          max_chunk(va, 0);
+          tmem_wait_ld_dep(vb);
+          max_chunk(vb, 1);
+        }
+        // the row maximum over both halves (slot of this tile's parity: the other half reads
+        // it before either can write the slot again two tiles on)
+        float* mx_slot = mx_buf + (((sc & 1) * 2 + t) * 2) * QT;
+        mx_slot[c * QT + m] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mxb);
+        const bool ex = bwait(mxb, (uint32_t)(sc & 1), abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, ex)) {
+          ok = false;
+          break;
+        }
+        // in base 2 (scale > 0, so scaling after the maximum is the same); -inf for a row that
+        // has seen no key yet
+        const float mx = fmaxf(mx_slot[m], mx_slot[QT + m]) * sl2;
+        if (__any_sync(0xFFFFFFFFu, mx > m_ref + 8.0f)) {
+          // move the reference maximum of every row of the warp to max(m_ref, mx): O and l
+          // scale by 2^(m_ref - m_new) (1 for rows whose maximum did not grow); O holds P V of
+          // the item's earlier tiles once their MMAs are done; this half rescales its d/2
+          // columns of O
+          const float m_new = fmaxf(m_ref, mx);
+          const float alpha = (m_ref == -INFINITY) ? 0.0f : ex2(m_ref - m_new);
+          if (j > 0) {
+            const bool done = bwait(bar(B_ODONE + t), (uint32_t)((sc - 1) & 1), abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, done)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int c16 = 0; c16 < D / 32; ++c16) {
+              uint32_t wv[16];
+              const uint32_t oa = lane_addr + o_col(t) + (uint32_t)(c * (D / 2) + 16 * c16);
+              tmem_ld16(oa, wv);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                wv[e] = __float_as_uint(__uint_as_float(wv[e]) * alpha);
+              tmem_st16(oa, wv);
+            }
+            tmem_wait_st();
+          }
+          l_sum *= alpha;
+          m_ref = m_new;
+        }
+        // pass 2: p = 2^(s * scale - m_ref), 32 columns at a time (the scaling and the row sums
+        // two elements per instruction), packed to fp16 over columns 16 c2 .. of this half's S
+        // (S columns that have been read)
+        const float ref = (m_ref == -INFINITY) ? 0.0f : m_ref;
+        const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-ref, -ref);
+        uint64_t ls2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
+        auto p_chunk = [&](float (&v)[32], int c2) {
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (vis[c2] >> e & 1u) ? v[e] : -INFINITY;
+          }
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = f2unpack(ffma2(f2pack(v[e], v[e + 1]), sl2x2, negm2));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            ls2[(e >> 1) & 1] = fadd2(ls2[(e >> 1) & 1], f2pack(p0, p1));
+            pw[e / 2] = pack_h2(p0, p1);
+          }
+          tmem_st16(srow + 16 * c2, pw);
+        };
+        {
+          float va[32], vb[32];
+          tmem_ld32(srow, va);
+          tmem_wait_ld_dep(va);
+          tmem_ld32(srow + 32, vb);
+          p_chunk(va, 0);
+          tmem_wait_ld_dep(vb);
+          p_chunk(vb, 1);
+        }
+        tmem_wait_st();
+        const float2 la = f2unpack(fadd2(ls2[0], ls2[1]));
+        l_sum += la.x + la.y;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL + t));
+      }
+      if (!ok) break;
+      // this half's row sums for the output warps, once they have taken the previous item's
+      if (uses > 0) {
+        const bool fr = bwait(bar(B_OFREE + t), (uint32_t)((uses - 1) & 1), abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, fr)) {
+          ok = false;
+          break;
+        }
+      }
+      l_buf[(t * 2 + c) * QT + m] = l_sum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_LFULL + t));
+      ++uses;
+    }
+  } else if (warp >= W_OUT) {
+    // ------------------------------------------------------------ output of both Q tiles
+    const int quarter = warp & 3;
+    const int m = 32 * quarter + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16);
+    const bool leader = (warp == W_OUT) && lane == 0;  // issues the stores
+    int cum[2] = {0, 0}, uses[2] = {0, 0}, nbox = 0;   // P V products, items, boxes stored
+    bool ok = true;
+    for (; have && ok; next()) {
+      const Item it = item_at(cur, seqs, w);
+      for (int t = 0; t < 2 && ok; ++t) {
+        const int r0 = it.q0 + t * QT, rows = min(QT, it.s.nq - r0);   // valid rows
+        if (rows <= 0) continue;
+        const int nt = (t ? it.t[1] : it.t[0]).count();
+        const int64_t row = (int64_t)it.s.q0 + r0 + m;
+        uint16_t* out = w.out + row * w.out_stride + (int64_t)it.hq * D;
+        if (nt == 0) {                                 // no row of the tile sees a key
+          if (m < rows)
+            for (int c = 0; c < D / 8; ++c)
+              reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        cum[t] += nt;
+        // the row sums, then the item's last P V product into O_t
+        bool got = bwait(bar(B_LFULL + t), (uint32_t)(uses[t] & 1), abort_flag);
+        got = got && bwait(bar(B_ODONE + t), (uint32_t)((cum[t] - 1) & 1), abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        ++uses[t];
+        const int pos = it.s.nk - it.s.nq + r0 + m;
+        const float l = l_buf[(t * 2) * QT + m] + l_buf[(t * 2 + 1) * QT + m];
+        const bool sees = pos >= 0;
+        const float inv = sees ? 1.0f / l : 0.0f;
+        // rows with an infinity or a NaN: x * 0 is 0 for finite x only
+        float zero = inv * 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(lane_addr + o_col(t) + 32 * c, o);
+          tmem_wait_ld_dep(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) zero = fmaf(o[e], 0.0f, zero);
+        }
+        const unsigned redo = __ballot_sync(0xFFFFFFFFu, m < rows && sees && zero != 0.0f);
+        // O / l in 64-column boxes.  A full tile: staged in shared memory (the 128B-swizzled layout of
+        // the output map: 16-byte chunk k of row m at chunk k ^ (m % 8)) and stored by TMA.  The
+        // last tile of a sequence: each thread stores its own row.
+        const bool full = rows == QT;
+#pragma unroll 1
+        for (int hb = 0; hb < NB; ++hb) {
+          const uint32_t stage = smem_u32(smem + L::O_OFF);
+          if (full && nbox >= 1) {
+            // the box is free once the previous store has read it
+            if (leader) {
+              bulk_wait_read();
+              mbar_arrive(bar(B_OSFREE));
+            }
+            const bool fr = bwait(bar(B_OSFREE), (uint32_t)((nbox - 1) & 1), abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, fr)) {
+              ok = false;
+              break;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float o[32];
+            tmem_ld32(lane_addr + o_col(t) + 64 * hb + 32 * c, o);
+            tmem_wait_ld_dep(o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 4 * c + i;
+              uint32_t p[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x = sees ? o[8 * i + 2 * e] * inv : 0.0f;
+                const float y = sees ? o[8 * i + 2 * e + 1] * inv : 0.0f;
+                p[e] = pack_h2(in_range(x), in_range(y));
+              }
+              if (full)
+                st_shared_v4(stage + 128 * m + ((k ^ (m & 7)) << 4), p[0], p[1], p[2], p[3]);
+              else if (m < rows)
+                reinterpret_cast<uint4*>(out + 64 * hb)[k] = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          }
+          if (hb == NB - 1) {
+            // O_t has been read: the next item's first P V product may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_OFREE + t));
+          }
+          if (redo) {
+            __syncwarp();                              // over what the row's own thread stored
+            for (unsigned left = redo; left; left &= left - 1) {
+              constexpr int C = D / 32;
+              const int rr = 32 * quarter + __ffs(left) - 1;
+              float x[C];
+              attend_row<D>(w, (int64_t)it.s.q0 + r0 + rr, it.hq, it.s.k0,
+                            it.s.nk - it.s.nq + r0 + rr, x);
+              const int ch = lane * C - 64 * hb;       // within this box
+              if (ch < 0 || ch >= 64) continue;
+              uint16_t* dst = full ? reinterpret_cast<uint16_t*>(
+                                         smem + L::O_OFF + 128 * rr +
+                                         (((ch >> 3) ^ (rr & 7)) << 4) + (ch & 7) * 2)
+                                   : w.out + ((int64_t)it.s.q0 + r0 + rr) * w.out_stride +
+                                         (int64_t)it.hq * D + lane * C;
+#pragma unroll
+              for (int e = 0; e < C; ++e) dst[e] = f2h(x[e]);
+            }
+          }
+          if (full) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_OSTAGED));
+            if (leader && bwait(bar(B_OSTAGED), (uint32_t)(nbox & 1), abort_flag)) {
+              tma_store_2d(&tmO, stage, it.hq * D + 64 * hb, it.s.q0 + r0);
+              bulk_commit();
+            }
+            ++nbox;
+          }
+          __syncwarp();
+        }
+      }
+    }
+    // the CTA's shared memory stays valid until its stores have completed
+    if (leader) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// Shared memory of the kernel on the current device, set once per device.
+template <int D>
+cudaError_t prepare() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 0 || dev >= 64 || done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(prefill_window_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PSmem<D>::BYTES);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+template <int D>
+cudaError_t launch_d(const PrefillWindow& a, int nsm, cudaStream_t st) {
+  cudaError_t e = prepare<D>();
+  if (e != cudaSuccess || (e = get_encode()) != cudaSuccess) return e;
+  CUtensorMap tq, tk, tv, to;
+  auto map = [](CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int64_t stride) {
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, (uint64_t)cols, (uint64_t)rows,
+                       (uint64_t)stride * 2, 64, QT, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  const int64_t wq = (int64_t)a.Hq * D, wk = (int64_t)a.Hkv * D;
+  if ((e = map(&tq, a.q, wq, a.q_rows, a.q_stride)) != cudaSuccess ||
+      (e = map(&to, a.out, wq, a.q_rows, a.out_stride)) != cudaSuccess)
+    return e;
+  tk = tv = tq;                             // without K/V rows no key tile is loaded
+  if (a.kv_rows > 0 && ((e = map(&tk, a.k, wk, a.kv_rows, a.kv_stride)) != cudaSuccess ||
+                        (e = map(&tv, a.v, wk, a.kv_rows, a.kv_stride)) != cudaSuccess))
+    return e;
+  for (int s0 = 0; s0 < a.nseq; s0 += kMaxSeqs) {
+    const int ns = std::min(kMaxSeqs, a.nseq - s0);
+    const PArgs pa{a, s0, ns, a.scale * 1.4426950408889634f};
+    // the blocks of ns sequences of q_rows rows in all are at most this many
+    const int64_t items = ((int64_t)a.q_rows / QB + ns) * a.Hq;
+    const int64_t grid = std::min<int64_t>(items, std::max(1, nsm));   // one CTA per SM
+    e = launch_pdl(prefill_window_kernel<D>, dim3((unsigned)grid), dim3(THREADS), PSmem<D>::BYTES,
+                   st, tq, tk, tv, to, pa);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_attn_window(const PrefillWindow& a, int d, int, cudaStream_t st) {
-  const unsigned grid = (unsigned)(((int64_t)a.q_rows * a.Hq + kThreads / 32 - 1) / (kThreads / 32));
-  return launch_pdl(d == 128 ? prefill_window_kernel<128> : prefill_window_kernel<64>, dim3(grid),
-                    dim3(kThreads), 0, st, a);
+cudaError_t launch_prefill_attn_window(const PrefillWindow& a, int d, int nsm, cudaStream_t st) {
+  return d == 128 ? launch_d<128>(a, nsm, st) : launch_d<64>(a, nsm, st);
 }
 
 cudaError_t prefill_window_read_error(unsigned int* out) {

@@ -77,6 +77,49 @@ FG_HD int run_tiles(const SeqTiles& s, int u, int u1) {
   return ((u < s.ns && s.ns < u1) ? s.ns : u1) - u;
 }
 
+// ---- prefill: the 128-key tiles that a tile of 128 query rows sees
+//
+// Key tiles 0 .. ns-1 hold first positions, tw .. te-1 the rows' windows (ns and tw 0 where the two
+// touch).  Row r of a sequence with nq query rows and nk keys is position nk - nq + r.
+constexpr int kKeyTile = 128, kQueryTile = 128;
+struct KeyTiles {
+  int ns, tw, te;
+  FG_HD int count() const { return ns + te - tw; }
+  FG_HD bool has(int tile) const { return tile < ns || (tile >= tw && tile < te); }
+  FG_HD int tile(int j) const { return j < ns ? j : j - ns + tw; }
+};
+FG_HD KeyTiles key_tiles(int r0, int nq, int nk, int window, int sinks) {
+  KeyTiles k{0, 0, 0};
+  const int last = r0 < nq - kQueryTile ? r0 + kQueryTile - 1 : nq - 1;
+  const int hi = nk - nq + last;           // the last row's position
+  if (r0 >= nq || hi < 0) return k;
+  const int lo = nk - nq + r0 > 0 ? nk - nq + r0 : 0;     // the first row's that has one
+  k.te = hi / kKeyTile + 1;
+  k.tw = (window == 0 || lo < window) ? 0 : (lo - window + 1) / kKeyTile;
+  const int seen = sinks <= hi ? sinks : hi + 1;
+  k.ns = seen > 0 ? (seen - 1) / kKeyTile + 1 : 0;
+  if (k.ns >= k.tw) k.ns = k.tw = 0;
+  return k;
+}
+// The tiles that either of two neighbouring query tiles sees.
+FG_HD KeyTiles either(const KeyTiles& a, const KeyTiles& b) {
+  if (a.count() == 0) return b;
+  if (b.count() == 0) return a;
+  KeyTiles k;
+  k.te = a.te > b.te ? a.te : b.te;
+  k.tw = a.tw < b.tw ? a.tw : b.tw;
+  k.ns = a.ns > b.ns ? a.ns : b.ns;
+  if (k.ns >= k.tw) k.ns = k.tw = 0;
+  return k;
+}
+// Bits e of 32 columns (keys c0 + e of the sequence) that position i sees, i < nk.
+FG_HD uint32_t bits_below(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
+FG_HD uint32_t visible_bits(int c0, int i, int window, int sinks) {
+  const uint32_t past = bits_below(i - c0 < 32 ? i - c0 + 1 : 32);
+  const int w0 = (window == 0 || i < window) ? 0 : i - window + 1;    // the window's first key
+  return past & (~bits_below(w0 - c0) | bits_below(sinks > c0 ? sinks - c0 : 0));
+}
+
 // `total` tiles in one order, cut evenly into n shares (n < 2^16): share i is tiles first(i) ..
 // first(i + 1) - 1; share_of is the inverse.
 struct Shares {

@@ -120,6 +120,17 @@ int h_run_tiles(int len, int window, int sinks, int u, int u1) {
 }
 int64_t h_first_tile(int64_t total, int nw, int w) { return Shares(total, nw).first(w); }
 int h_share_of(int64_t total, int nw, int64_t x) { return Shares(total, nw).share_of(x); }
+void h_key_tiles(int r0, int nq, int nk, int window, int sinks, int32_t* o) {
+  const KeyTiles k = key_tiles(r0, nq, nk, window, sinks);
+  o[0] = k.ns; o[1] = k.tw; o[2] = k.te;
+}
+void h_either(const int32_t* a, const int32_t* b, int32_t* o) {
+  const KeyTiles k = either(KeyTiles{a[0], a[1], a[2]}, KeyTiles{b[0], b[1], b[2]});
+  o[0] = k.ns; o[1] = k.tw; o[2] = k.te;
+}
+unsigned h_visible_bits(int c0, int i, int window, int sinks) {
+  return visible_bits(c0, i, window, sinks);
+}
 int h_visible(int t, int i, int window, int sinks) { return visible(t, i, window, sinks); }
 }
 """
@@ -136,6 +147,7 @@ def host(tmp_path_factory):
     dll = C.CDLL(str(lib))
     dll.h_first_tile.argtypes = [C.c_int64, C.c_int, C.c_int]
     dll.h_first_tile.restype = C.c_int64
+    dll.h_visible_bits.restype = C.c_uint32
     dll.h_share_of.argtypes = [C.c_int64, C.c_int, C.c_int64]
     return dll
 
@@ -224,3 +236,49 @@ def test_worker_ranges(host):
         for w in list(range(0, nw, max(1, nw // 50))) + [nw - 1]:
             for x in {first[w], first[w + 1] - 1}:
                 assert host.h_share_of(total, nw, x) == w, (total, nw, w)
+
+
+def tiles(host, *args):
+    o = np.zeros(3, np.int32)
+    host.h_key_tiles(*args, o.ctypes.data_as(C.POINTER(C.c_int32)))
+    ns, tw, te = (int(x) for x in o)
+    return o, set(range(ns)) | set(range(tw, te)), ns + te - tw
+
+
+def test_prefill_key_tiles(host):
+    """The key tiles of a query tile hold every key that one of its rows sees, each once, and no
+    tile without one except between two rows' windows; the tiles of a pair are the union."""
+    from oracle import window as OW
+    rng = np.random.default_rng(5)
+    cases = [(nq, nk, w, s) for nq in (1, 100, 128, 129, 300) for nk in (0, 1, 99, 128, 257, 700)
+             for w, s in ((0, 0), (1, 0), (2, 130), (64, 4), (128, 128), (129, 300), (500, 1),
+                          (2 ** 31 - 1, 2 ** 31 - 1))]
+    cases += [tuple(int(x) for x in rng.integers(1, 900, 4)) for _ in range(60)]
+    for nq, nk, w, s in cases:
+        for r0 in range(0, nq + 128, 128):
+            o, got, n = tiles(host, r0, nq, nk, w, s)
+            assert n == len(got)
+            want = set()
+            for r in range(r0, min(nq, r0 + 128)):
+                if nk - nq + r >= 0:
+                    want |= set((OW.visible(nk - nq + r, nk, w, s) // 128).tolist())
+            assert want == got, (nq, nk, w, s, r0, want, got)
+            assert not got or max(got) * 128 < nk
+            o2, got2, _ = tiles(host, r0 + 128, nq, nk, w, s)
+            u = np.zeros(3, np.int32)
+            ptr = [x.ctypes.data_as(C.POINTER(C.c_int32)) for x in (o, o2, u)]
+            host.h_either(*ptr)
+            union = set(range(u[0])) | set(range(u[1], u[2]))
+            assert got | got2 <= union and len(union) == u[0] + u[2] - u[1]
+            assert union == got | got2, (nq, nk, w, s, r0)
+
+
+def test_visible_bits(host):
+    for c0 in (0, 32, 64, 96, 1024):
+        for i in (0, 1, 31, 32, 40, 95, 96, 1023, 1030, 1055, 5000):
+            for w in (0, 1, 3, 31, 32, 33, 1000, 2 ** 31 - 1):
+                for s in (0, 1, 31, 33, 70, 1040, 2 ** 31 - 1):
+                    got = host.h_visible_bits(c0, i, w, s)
+                    want = sum(1 << e for e in range(32)
+                               if c0 + e <= i and (w == 0 or c0 + e > i - w or c0 + e < s))
+                    assert got == want, (c0, i, w, s)
