@@ -24,13 +24,15 @@
 // that it sees, so "the next product" of a Q tile is looked up per key tile.
 //
 // Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it would
-// reach the rows of the Q tile that do not see it.  The output warps therefore test their rows of
-// O: a row with an infinity or a NaN is computed again on its own, over its visible keys alone
+// reach the rows of the Q tile that do not see it.  The output warps therefore test their rows: a
+// row with an infinity or a NaN is computed again on its own, over its visible keys alone
 // (attend_row), so that only what it sees can reach it.  Finite inputs never take that path.
 //
 // The work order: blocks by descending index, for each the sequences that have one (longest first),
 // for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read and
-// checked on the device, kMaxSeqs sequences per launch.
+// checked on the device, kMaxSeqs sequences per launch.  The producer works the items out and hands
+// them to the other warps through a ring in shared memory, ahead of the loads: the softmax warps
+// have no registers to spare for it.
 //
 // Every mbarrier wait is bounded; on timeout the CTA sets the device error word (read by
 // fg_check_device_error), drains its copies and MMAs and frees TMEM.
@@ -64,6 +66,8 @@ constexpr int BOX = QT * 128;               // bytes of one 64-column x 128-row 
 constexpr int kMaxSeqs = 384;               // sequences per launch
 static_assert(kMaxSeqs <= THREADS, "one thread per sequence reads its offsets");
 
+constexpr int ITEMS = 4;                    // ring of work items
+
 struct Seq {
   int q0, nq, k0, nk;                       // first query row, rows, first K/V row, rows
 };
@@ -78,18 +82,20 @@ struct PSmem {
   static constexpr int L_OFF = O_OFF + BOX;            // row sums l [tile][key half][row]
   static constexpr int MX_OFF = L_OFF + 2 * 2 * QT * 4;  // row maxima [parity][tile][half][row]
   static constexpr int BAR_OFF = MX_OFF + 2 * 2 * 2 * QT * 4;
-  static constexpr int SEQ_OFF = BAR_OFF + 256;        // sequences, longest first
+  static constexpr int ITEM_OFF = BAR_OFF + 512;
+  static constexpr int SEQ_OFF = ITEM_OFF + ITEMS * 64;  // sequences, longest first
   static constexpr int BYTES = SEQ_OFF + kMaxSeqs * (int)sizeof(Seq) + 1024;   // 1024: alignment
 };
 static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 
 // barriers: q_full, q_free, kv_full[2], kv_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
 // l_full[2], o_staged, o_stage_free, drain, mx_ready[tile][quarter] (the two key halves of a
-// row have written their maxima)
+// row have written their maxima), item_full[4], item_free[4]
 constexpr int B_QFULL = 0, B_QFREE = 1, B_KVFULL = 2, B_KVFREE = 4, B_SFULL = 6, B_PFULL = 8,
               B_ODONE = 10, B_OFREE = 12, B_LFULL = 14, B_OSTAGED = 16, B_OSFREE = 17,
-              B_DRAIN = 18, B_MX = 19, NBARS = 27;
-static_assert(NBARS * 8 + 16 <= 256, "barrier space");
+              B_DRAIN = 18, B_MX = 19, B_IFULL = 27, B_IFREE = B_IFULL + ITEMS,
+              NBARS = B_IFREE + ITEMS;
+static_assert(NBARS * 8 + 16 <= 512, "barrier space");
 
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_test(bar, parity)) return true;
@@ -184,15 +190,18 @@ struct PArgs {
   float scale_log2;
 };
 
-// The place of an item in the work order, and the item: block qb of sequence `seq` (an index into
-// the sequences in shared memory, longest first) and query head hq.
+// A work item: a block of 256 query rows of one (sequence, query head).
+struct Item {
+  int hq;                                   // query head; -1: no more items
+  int qrow, rows;                           // the block's first row in q and out; rows from there on
+  int krow;                                 // the sequence's first K/V row
+  int pos;                                  // position of the block's first row (may be negative)
+  KeyTiles t[2], u;                         // the Q tiles' key tiles, and their union
+};
+static_assert(sizeof(Item) <= 64, "item ring");
+// The place of an item in the work order.
 struct Cursor {
   int level, cnt, i;                        // block index; sequences that have it; item within it
-};
-struct Item {
-  Seq s;
-  int hq, q0;
-  KeyTiles t[2], u;                         // the Q tiles' key tiles, and their union
 };
 __device__ __forceinline__ int blocks_of(int nq) { return (nq + QB - 1) / QB; }
 // How many of the sequences (longest first) have a block `level`.
@@ -223,12 +232,15 @@ __device__ __forceinline__ Cursor first_item(const Seq* seqs, int nseq) {
 }
 __device__ __forceinline__ Item item_at(const Cursor& c, const Seq* seqs, const PrefillWindow& w) {
   Item it;
-  const int b = c.i / w.Hq;
+  const int b = c.i / w.Hq, q0 = c.level * QB;
+  const Seq s = seqs[b];
   it.hq = c.i - b * w.Hq;
-  it.s = seqs[b];
-  it.q0 = c.level * QB;
-  it.t[0] = key_tiles(it.q0, it.s.nq, it.s.nk, w.window, w.sinks);
-  it.t[1] = key_tiles(it.q0 + QT, it.s.nq, it.s.nk, w.window, w.sinks);
+  it.qrow = s.q0 + q0;
+  it.rows = s.nq - q0;
+  it.krow = s.k0;
+  it.pos = s.nk - s.nq + q0;
+  it.t[0] = key_tiles(q0, s.nq, s.nk, w.window, w.sinks);
+  it.t[1] = key_tiles(q0 + QT, s.nq, s.nk, w.window, w.sinks);
   it.u = either(it.t[0], it.t[1]);
   return it;
 }
@@ -253,6 +265,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* live = reinterpret_cast<int*>(tmem_slot + 2);   // sequences with rows
   Seq* seqs = reinterpret_cast<Seq*>(smem + L::SEQ_OFF);
+  auto item_slot = [&](int n) { return reinterpret_cast<Item*>(smem + L::ITEM_OFF + 64 * (n % ITEMS)); };
   float* l_buf = reinterpret_cast<float*>(smem + L::L_OFF);
   float* mx_buf = reinterpret_cast<float*>(smem + L::MX_OFF);
   const uint32_t bar0 = smem_u32(bars);
@@ -279,6 +292,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     mbar_init(bar(B_OSTAGED), 4);                      // one arrival per output warp
     mbar_init(bar(B_OSFREE), 1);
     mbar_init(bar(B_DRAIN), 1);
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(bar(B_IFULL + i), 1);
+      mbar_init(bar(B_IFREE + i), 1 + 16 + 4);         // the MMA issuer, softmax and output warps
+    }
     *abort_flag = 0;
     *live = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -325,17 +342,31 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   // TMEM columns: S_A 0..127, S_B 128..255, O_A 256.., O_B 256 + D..
   auto s_col = [&](int t) { return (uint32_t)(t * KT); };
   auto o_col = [&](int t) { return (uint32_t)(2 * KT + t * D); };
-  Cursor cur = first_item(seqs, nseq);
-  bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
-  auto next = [&]() { have = advance(cur, gridDim.x, seqs, nseq, w.Hq); };
+  // Item n of this CTA for a consuming thread (null: a wait ran out), and the end of its use.
+  auto item_wait = [&](int n) -> const Item* {
+    return bwait(bar(B_IFULL + n % ITEMS), (uint32_t)((n / ITEMS) & 1), abort_flag) ? item_slot(n)
+                                                                                    : nullptr;
+  };
+  auto item_done = [&](int n) { mbar_arrive(bar(B_IFREE + n % ITEMS)); };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ items and TMA producer
     if (lane == 0) {
       int kvg = 0, qn = 0;                             // K/V tiles, Q pairs issued
       bool ok = true;
-      for (; have && ok; next()) {
-        const Item it = item_at(cur, seqs, w);
+      Cursor cur = first_item(seqs, nseq);
+      bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
+      for (int n = 0; ok; ++n) {
+        if (n >= ITEMS &&
+            !bwait(bar(B_IFREE + n % ITEMS), (uint32_t)((n / ITEMS - 1) & 1), abort_flag))
+          break;
+        Item it;
+        it.hq = -1;
+        if (have) it = item_at(cur, seqs, w);
+        *item_slot(n) = it;
+        mbar_arrive(bar(B_IFULL + n % ITEMS));
+        if (!have) break;
+        have = advance(cur, gridDim.x, seqs, nseq, w.Hq);
         const int nkv = it.u.count();
         if (nkv == 0) continue;
         const int hk = it.hq / (w.Hq / w.Hkv);
@@ -345,7 +376,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int t = 0; t < 2; ++t)
           for (int c = 0; c < NB; ++c)
             tma_load_2d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ,
-                        it.hq * D + 64 * c, it.s.q0 + it.q0 + t * QT, bar(B_QFULL));
+                        it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL));
         ++qn;
         for (int j = 0; j < nkv; ++j, ++kvg) {
           const int st = kvg % STAGES;
@@ -354,7 +385,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
             ok = false;
             break;
           }
-          const int row = it.s.k0 + it.u.tile(j) * KT;
+          const int row = it.krow + it.u.tile(j) * KT;
           mbar_expect_tx(bar(B_KVFULL + st), (uint32_t)(2 * L::TILE));
           for (int c = 0; c < NB; ++c) {
             tma_load_2d(smem_u32(smem + L::K_OFF + st * L::TILE + c * BOX), &tmK,
@@ -378,29 +409,31 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool ok = true, issued = false;
       int kvg = 0, qn = 0;                             // K/V tiles, items consumed
       int pc[2] = {0, 0}, uses[2] = {0, 0};            // P V products; items, per Q tile
-      // S_t = Q_t K^T of K/V tile g over K = D: k-step i reads 16 columns, 32 bytes into box
-      // i / 4
-      auto issue_s = [&](int t, int g) {
+      // S_t = Q_t K^T of the key steps [s0, s1) of K/V tile g over K = D: k-step i reads 16
+      // columns, 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
+      auto issue_s = [&](int t, int g, const KeySteps& ks) {
         const int st = g % STAGES;
         const uint64_t qd = smem_desc(qbase + t * L::TILE, 16, 1024);
-        const uint64_t kd = smem_desc(kbase + st * L::TILE, 16, 1024);
+        const uint64_t kd = smem_desc(kbase + st * L::TILE, 16, 1024) + (uint64_t)(ks.s0 * 128);
+        const uint32_t idesc = idesc_qk(16 * (ks.s1 - ks.s0)), col = tmem + s_col(t) + 16 * ks.s0;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
-          umma_f16(tmem + s_col(t), qd + off, kd + off, kIdescS, i > 0 ? 1u : 0u);
+          umma_f16(col, qd + off, kd + off, idesc, i > 0 ? 1u : 0u);
         }
         umma_commit(bar(B_SFULL + t));
       };
-      // O_t (+)= P_t V of K/V tile g over K = 128 keys: k-step i reads the 8 TMEM columns of
-      // P of keys 16i.. (key half i / 4 keeps its P in the first 32 of its 64 S columns) and
-      // rows 16i.. of V (2048 bytes per step in its MN-major 128B-swizzled layout)
-      auto issue_pv = [&](int t, int g, bool first) {
+      // O_t (+)= P_t V of the same key steps: step i reads the 8 TMEM columns of P of keys 16i..
+      // (key half i / 4 keeps its P in the first 32 of its 64 S columns) and rows 16i.. of V (2048
+      // bytes per step in its MN-major 128B-swizzled layout)
+      auto issue_pv = [&](int t, int g, const KeySteps& ks, bool first) {
         const int st = g % STAGES;
         const uint64_t vd = smem_desc(vbase + st * L::TILE, BOX, 1024);
 #pragma unroll
         for (int i = 0; i < KT / 16; ++i)
-          umma_ts(tmem + o_col(t), tmem + s_col(t) + 64 * (i >> 2) + 8 * (i & 3),
-                  vd + (uint64_t)(i * 128), idesc_o, (!first || i > 0) ? 1u : 0u);
+          if (i >= ks.s0 && i < ks.s1)
+            umma_ts(tmem + o_col(t), tmem + s_col(t) + 64 * (i >> 2) + 8 * (i & 3),
+                    vd + (uint64_t)(i * 128), idesc_o, (!first || i > ks.s0) ? 1u : 0u);
         umma_commit(bar(B_ODONE + t));
       };
       auto wait_kv = [&](int g) {
@@ -409,22 +442,37 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_after();
         return true;
       };
-      for (; have && ok; next()) {
-        const Item it = item_at(cur, seqs, w);
-        const int nkv = it.u.count();
+      for (int n = 0; ok; ++n) {
+        const Item* slot = item_wait(n);
+        if (!slot || slot->hq < 0) break;
+        const KeyTiles kt[2] = {slot->t[0], slot->t[1]}, u = slot->u;
+        const int pos = slot->pos, rows = slot->rows;
+        item_done(n);
+        const int nkv = u.count();
         if (nkv == 0) continue;
+        auto steps = [&](int t, int tile) {
+          return key_steps(tile, pos + t * QT, pos + min(t * QT + QT, rows) - 1, w.window, w.sinks);
+        };
+        int tile = u.tile(0);
+        bool sees[2] = {kt[0].has(tile), kt[1].has(tile)};
+        KeySteps ks[2] = {steps(0, tile), steps(1, tile)};
         if (!bwait(bar(B_QFULL), (uint32_t)(qn & 1), abort_flag) || !wait_kv(kvg)) break;
         ++qn;
         bool begun[2] = {false, false};                // Q tile t has a P V product of this item
         for (int t = 0; t < 2; ++t)
-          if (it.t[t].has(it.u.tile(0))) issue_s(t, kvg);
+          if (sees[t]) issue_s(t, kvg, ks[t]);
         issued = true;
         if (nkv == 1) umma_commit(bar(B_QFREE));       // every S product of the item issued
         for (int j = 0; j < nkv && ok; ++j) {
-          const int g = kvg + j, tile = it.u.tile(j), tile_n = j + 1 < nkv ? it.u.tile(j + 1) : -1;
+          const int g = kvg + j;
+          // the next key tile, worked out while the softmax runs
+          const bool more = j + 1 < nkv;
+          tile = more ? u.tile(j + 1) : 0;
+          const bool sees_n[2] = {more && kt[0].has(tile), more && kt[1].has(tile)};
+          const KeySteps ks_n[2] = {steps(0, tile), steps(1, tile)};
           bool next_ready = false;                     // K/V of tile j + 1 waited for
           for (int t = 0; t < 2 && ok; ++t) {
-            if (it.t[t].has(tile)) {
+            if (sees[t]) {
               if (!bwait(bar(B_PFULL + t), (uint32_t)(pc[t] & 1), abort_flag)) {
                 ok = false;
                 break;
@@ -436,21 +484,23 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                 break;
               }
               tc_fence_after();
-              issue_pv(t, g, !begun[t]);
+              issue_pv(t, g, ks[t], !begun[t]);
               if (!begun[t]) ++uses[t];
               begun[t] = true;
               ++pc[t];
             }
             // S_t of the next key tile: its columns hold no P that is still to be read (this Q
             // tile's earlier products were issued before)
-            if (tile_n >= 0 && it.t[t].has(tile_n)) {
+            if (sees_n[t]) {
               if (!next_ready && !wait_kv(g + 1)) {
                 ok = false;
                 break;
               }
               next_ready = true;
-              issue_s(t, g + 1);
+              issue_s(t, g + 1, ks_n[t]);
             }
+            sees[t] = sees_n[t];
+            ks[t] = ks_n[t];
           }
           if (!ok) break;
           if (j == nkv - 2) umma_commit(bar(B_QFREE));      // the item's last S products
@@ -482,45 +532,67 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them is
     // decided for the whole warp, waits included (a lane that gave up takes its warp along);
     // both halves of a row take the same decisions (the same maximum)
-    for (; have && ok; next()) {
-      const Item it = item_at(cur, seqs, w);
-      const KeyTiles kt = t ? it.t[1] : it.t[0];
-      const int nt = kt.count();
-      if (nt == 0) continue;
-      // positions: this row's, and those of the Q tile's first and last row with one
-      const int base = it.s.nk - it.s.nq + it.q0 + t * QT;
-      const int pos = min(base + m, it.s.nk - 1);
-      const int plo = base, phi = min(base + QT, it.s.nk) - 1;
+    for (int n = 0; ok; ++n) {
+      const volatile Item* it = item_wait(n);          // read again where needed: no registers for it
+      if (!__all_sync(0xFFFFFFFFu, it != nullptr) || it->hq < 0) break;
+      const int nt = it->t[t].ns + it->t[t].te - it->t[t].tw;
+      if (nt == 0) {
+        if (lane == 0) item_done(n);
+        continue;
+      }
       float m_ref = -INFINITY, l_sum = 0.0f;           // l over this half's keys
       for (int j = 0; j < nt; ++j, ++sc) {
+        // masked: some row of the Q tile does not see every key of the tile (warp-uniform); ahead:
+        // the position of the Q tile's first row less the key tile's first position
+        const int ns = it->t[t].ns;
+        const int k0 = (j < ns ? j : j - ns + it->t[t].tw) * KT, ahead = it->pos + t * QT - k0;
+        const bool masked = ahead < KT - 1 ||
+                            (w.window != 0 && k0 + KT > w.sinks &&
+                             ahead + min(QT, it->rows - t * QT) > w.window);
+        // what each row sees of this half, 32 columns at a time: all of them (2) or none (0) for
+        // the whole warp, or some (1)
+        uint32_t vis[2] = {~0u, ~0u};
+        int mode[2] = {2, 2};
+        if (masked) {
+#pragma unroll
+          for (int c2 = 0; c2 < 2; ++c2) {
+            vis[c2] = visible_bits(k0 + 64 * c + 32 * c2, k0 + ahead + m, w.window, w.sinks);
+            mode[c2] = !__any_sync(0xFFFFFFFFu, vis[c2] != 0u)    ? 0
+                       : __all_sync(0xFFFFFFFFu, vis[c2] == ~0u) ? 2
+                                                                 : 1;
+          }
+        }
         const bool got = bwait(bar(B_SFULL + t), (uint32_t)(sc & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // masked: some row of the Q tile does not see every key of the tile (warp-uniform)
-        const int k0 = kt.tile(j) * KT;
-        const bool masked = k0 + KT - 1 > plo ||
-                            (w.window != 0 && phi >= w.window && k0 <= phi - w.window &&
-                             k0 + KT > w.sinks);
-        uint32_t vis[2] = {~0u, ~0u};
-        if (masked) {
-          vis[0] = visible_bits(k0 + 64 * c, pos, w.window, w.sinks);
-          vis[1] = visible_bits(k0 + 64 * c + 32, pos, w.window, w.sinks);
-        }
-        // pass 1: this half's maximum, 32 columns at a time (the second load in flight)
+        // pass 1: this half's maximum, 32 columns at a time (the second load in flight).  Columns that
+        // a row does not see are set to -inf, in TMEM too: pass 2 reads them there.
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         auto max_chunk = [&](float (&v)[32], int c2) {
-          if (masked) {
+          if (mode[c2] == 1) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = (vis[c2] >> e & 1u) ? v[e] : -INFINITY;
+            tmem_st16(srow + 32 * c2, reinterpret_cast<const uint32_t*>(v));
+            tmem_st16(srow + 32 * c2 + 16, reinterpret_cast<const uint32_t*>(v) + 16);
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], v[e], v[e + 1]);
         };
-        {
+        if (masked) {
+          float v[32];
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            if (mode[c2] == 0) continue;
+            tmem_ld32(srow + 32 * c2, v);
+            tmem_wait_ld_dep(v);
+            max_chunk(v, c2);
+          }
+          tmem_wait_st();
+        } else {
           float va[32], vb[32];
           tmem_ld32(srow, va);
           tmem_wait_ld_dep(va);
@@ -580,10 +652,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-ref, -ref);
         uint64_t ls2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
         auto p_chunk = [&](float (&v)[32], int c2) {
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (vis[c2] >> e & 1u) ? v[e] : -INFINITY;
-          }
           uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -594,7 +662,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           tmem_st16(srow + 16 * c2, pw);
         };
-        {
+        if (mode[0] != 0 && mode[1] != 0) {
           float va[32], vb[32];
           tmem_ld32(srow, va);
           tmem_wait_ld_dep(va);
@@ -602,6 +670,19 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           p_chunk(va, 0);
           tmem_wait_ld_dep(vb);
           p_chunk(vb, 1);
+        } else {
+#pragma unroll 1
+          for (int c2 = 0; c2 < 2; ++c2) {
+            if (mode[c2] != 0) {
+              float v[32];
+              tmem_ld32(srow + 32 * c2, v);
+              tmem_wait_ld_dep(v);
+              p_chunk(v, c2);
+            } else {
+              const uint32_t none[16] = {};
+              tmem_st16(srow + 16 * c2, none);
+            }
+          }
         }
         tmem_wait_st();
         const float2 la = f2unpack(fadd2(ls2[0], ls2[1]));
@@ -621,7 +702,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       l_buf[(t * 2 + c) * QT + m] = l_sum;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_LFULL + t));
+      if (lane == 0) {
+        mbar_arrive(bar(B_LFULL + t));
+        item_done(n);
+      }
       ++uses;
     }
   } else if (warp >= W_OUT) {
@@ -632,14 +716,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     const bool leader = (warp == W_OUT) && lane == 0;  // issues the stores
     int cum[2] = {0, 0}, uses[2] = {0, 0}, nbox = 0;   // P V products, items, boxes stored
     bool ok = true;
-    for (; have && ok; next()) {
-      const Item it = item_at(cur, seqs, w);
+    for (int n = 0; ok; ++n) {
+      const Item* it = item_wait(n);
+      if (!__all_sync(0xFFFFFFFFu, it != nullptr) || it->hq < 0) break;
       for (int t = 0; t < 2 && ok; ++t) {
-        const int r0 = it.q0 + t * QT, rows = min(QT, it.s.nq - r0);   // valid rows
+        const int rows = min(QT, it->rows - t * QT);   // valid rows
         if (rows <= 0) continue;
-        const int nt = (t ? it.t[1] : it.t[0]).count();
-        const int64_t row = (int64_t)it.s.q0 + r0 + m;
-        uint16_t* out = w.out + row * w.out_stride + (int64_t)it.hq * D;
+        const int nt = it->t[t].count(), qrow = it->qrow + t * QT, pos = it->pos + t * QT;
+        uint16_t* out = w.out + (int64_t)(qrow + m) * w.out_stride + (int64_t)it->hq * D;
         if (nt == 0) {                                 // no row of the tile sees a key
           if (m < rows)
             for (int c = 0; c < D / 8; ++c)
@@ -656,21 +740,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         tc_fence_after();
         ++uses[t];
-        const int pos = it.s.nk - it.s.nq + r0 + m;
-        const float l = l_buf[(t * 2) * QT + m] + l_buf[(t * 2 + 1) * QT + m];
-        const bool sees = pos >= 0;
-        const float inv = sees ? 1.0f / l : 0.0f;
-        // rows with an infinity or a NaN: x * 0 is 0 for finite x only
-        float zero = inv * 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tmem_ld32(lane_addr + o_col(t) + 32 * c, o);
-          tmem_wait_ld_dep(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) zero = fmaf(o[e], 0.0f, zero);
-        }
-        const unsigned redo = __ballot_sync(0xFFFFFFFFu, m < rows && sees && zero != 0.0f);
+        // (a row that sees nothing: O 0, or NaN, which is mended below)
+        const float inv = pos + m >= 0
+                              ? 1.0f / (l_buf[(t * 2) * QT + m] + l_buf[(t * 2 + 1) * QT + m])
+                              : 0.0f;
         // O / l in 64-column boxes.  A full tile: staged in shared memory (the 128B-swizzled layout of
         // the output map: 16-byte chunk k of row m at chunk k ^ (m % 8)) and stored by TMA.  The
         // last tile of a sequence: each thread stores its own row.
@@ -690,7 +763,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
               break;
             }
           }
-#pragma unroll
+          __half2 zero = __float2half2_rn(0.0f);       // x * 0: NaN for an infinity or a NaN
+#pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             float o[32];
             tmem_ld32(lane_addr + o_col(t) + 64 * hb + 32 * c, o);
@@ -701,9 +775,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
               uint32_t p[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float x = sees ? o[8 * i + 2 * e] * inv : 0.0f;
-                const float y = sees ? o[8 * i + 2 * e + 1] * inv : 0.0f;
-                p[e] = pack_h2(in_range(x), in_range(y));
+                p[e] = pack_h2(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
+                zero = __hfma2(*reinterpret_cast<const __half2*>(&p[e]), __float2half2_rn(0.0f),
+                               zero);
               }
               if (full)
                 st_shared_v4(stage + 128 * m + ((k ^ (m & 7)) << 4), p[0], p[1], p[2], p[3]);
@@ -711,6 +785,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                 reinterpret_cast<uint4*>(out + 64 * hb)[k] = make_uint4(p[0], p[1], p[2], p[3]);
             }
           }
+          const unsigned redo = __ballot_sync(
+              0xFFFFFFFFu, m < rows && (__hisnan(__low2half(zero)) || __hisnan(__high2half(zero))));
           if (hb == NB - 1) {
             // O_t has been read: the next item's first P V product may overwrite it
             tc_fence_before();
@@ -723,15 +799,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
               constexpr int C = D / 32;
               const int rr = 32 * quarter + __ffs(left) - 1;
               float x[C];
-              attend_row<D>(w, (int64_t)it.s.q0 + r0 + rr, it.hq, it.s.k0,
-                            it.s.nk - it.s.nq + r0 + rr, x);
+              attend_row<D>(w, (int64_t)qrow + rr, it->hq, it->krow, pos + rr, x);
               const int ch = lane * C - 64 * hb;       // within this box
               if (ch < 0 || ch >= 64) continue;
               uint16_t* dst = full ? reinterpret_cast<uint16_t*>(
                                          smem + L::O_OFF + 128 * rr +
                                          (((ch >> 3) ^ (rr & 7)) << 4) + (ch & 7) * 2)
-                                   : w.out + ((int64_t)it.s.q0 + r0 + rr) * w.out_stride +
-                                         (int64_t)it.hq * D + lane * C;
+                                   : w.out + (int64_t)(qrow + rr) * w.out_stride +
+                                         (int64_t)it->hq * D + lane * C;
 #pragma unroll
               for (int e = 0; e < C; ++e) dst[e] = f2h(x[e]);
             }
@@ -741,7 +816,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_OSTAGED));
             if (leader && bwait(bar(B_OSTAGED), (uint32_t)(nbox & 1), abort_flag)) {
-              tma_store_2d(&tmO, stage, it.hq * D + 64 * hb, it.s.q0 + r0);
+              tma_store_2d(&tmO, stage, it->hq * D + 64 * hb, qrow);
               bulk_commit();
             }
             ++nbox;
@@ -749,6 +824,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           __syncwarp();
         }
       }
+      __syncwarp();
+      if (lane == 0) item_done(n);
     }
     // the CTA's shared memory stays valid until its stores have completed
     if (leader) bulk_wait_all();

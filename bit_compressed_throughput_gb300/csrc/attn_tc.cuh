@@ -136,6 +136,9 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
 
 // instruction descriptors: D f32, A and B f16, M = 128.  S = Q K^T: both operands K-major,
 // N = 128 keys.  O += P V: A (P, in TMEM) K-major, B (V) MN-major, N = d.
+__host__ __device__ constexpr uint32_t idesc_qk(int keys) {
+  return (1u << 4) | ((uint32_t)(keys >> 3) << 17) | ((uint32_t)(QT >> 4) << 24);
+}
 constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(QT >> 4) << 24);
 __host__ __device__ constexpr uint32_t idesc_pv(int d) {
   return (1u << 4) | (1u << 16) | ((uint32_t)(d >> 3) << 17) | ((uint32_t)(QT >> 4) << 24);

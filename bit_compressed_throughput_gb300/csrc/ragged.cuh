@@ -112,6 +112,19 @@ FG_HD KeyTiles either(const KeyTiles& a, const KeyTiles& b) {
   if (k.ns >= k.tw) k.ns = k.tw = 0;
   return k;
 }
+// The 16-key steps s0 .. s1-1 of key tile `tile` that hold what rows at positions lo .. hi (lo may
+// be negative) see of it; not empty for a tile that the query tile has.
+struct KeySteps {
+  int s0, s1;
+};
+FG_HD KeySteps key_steps(int tile, int lo, int hi, int window, int sinks) {
+  const int k0 = tile * kKeyTile;
+  const int w0 = (window == 0 || lo < window) ? 0 : lo - window + 1;     // the windows' first key
+  const int first = k0 < sinks || w0 <= k0 ? 0 : w0 - k0;
+  int end = hi - k0 < kKeyTile ? hi - k0 + 1 : kKeyTile;
+  if (w0 >= k0 + kKeyTile && sinks - k0 < end) end = sinks - k0;         // first positions only
+  return KeySteps{first / 16, (end + 15) / 16};
+}
 // Bits e of 32 columns (keys c0 + e of the sequence) that position i sees, i < nk.
 FG_HD uint32_t bits_below(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
 FG_HD uint32_t visible_bits(int c0, int i, int window, int sinks) {

@@ -128,6 +128,10 @@ void h_either(const int32_t* a, const int32_t* b, int32_t* o) {
   const KeyTiles k = either(KeyTiles{a[0], a[1], a[2]}, KeyTiles{b[0], b[1], b[2]});
   o[0] = k.ns; o[1] = k.tw; o[2] = k.te;
 }
+void h_key_steps(int tile, int lo, int hi, int window, int sinks, int32_t* o) {
+  const KeySteps k = key_steps(tile, lo, hi, window, sinks);
+  o[0] = k.s0; o[1] = k.s1;
+}
 unsigned h_visible_bits(int c0, int i, int window, int sinks) {
   return visible_bits(c0, i, window, sinks);
 }
@@ -263,7 +267,16 @@ def test_prefill_key_tiles(host):
                 if nk - nq + r >= 0:
                     want |= set((OW.visible(nk - nq + r, nk, w, s) // 128).tolist())
             assert want == got, (nq, nk, w, s, r0, want, got)
+            for tile in got:
+                seen = set()
+                for r in range(r0, min(nq, r0 + 128)):
+                    v = OW.visible(nk - nq + r, nk, w, s) if nk - nq + r >= 0 else np.zeros(0, int)
+                    seen |= set(((v[v // 128 == tile] - 128 * tile) // 16).tolist())
+                host.h_key_steps(tile, nk - nq + r0, nk - nq + min(r0 + 128, nq) - 1, w, s, o.ctypes.data_as(C.POINTER(C.c_int32)))
+                assert 0 <= o[0] < o[1] <= 8
+                assert min(seen) == o[0] and max(seen) == o[1] - 1, (nq, nk, w, s, r0, tile)
             assert not got or max(got) * 128 < nk
+            o, _, _ = tiles(host, r0, nq, nk, w, s)
             o2, got2, _ = tiles(host, r0 + 128, nq, nk, w, s)
             u = np.zeros(3, np.int32)
             ptr = [x.ctypes.data_as(C.POINTER(C.c_int32)) for x in (o, o2, u)]
