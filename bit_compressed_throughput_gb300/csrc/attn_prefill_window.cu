@@ -14,10 +14,10 @@
 // the sequence's own rows, so a box may end in another sequence's rows or past the buffer (zeros);
 // such rows are masked or not stored.
 //   S = Q K^T     tcgen05.mma kind::f16, S (fp32) in TMEM
-//   softmax       two threads per query row, each over one half of the 128 key columns: base-2
-//                 online softmax with a lazily moved reference maximum (by more than 2^8),
-//                 P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that every row of the
-//                 Q tile sees in full are not masked; the others take a bit mask per row.
+//   softmax       one thread per query row, two passes over its 128 key columns in TMEM (the maximum,
+//                 then P): base-2 online softmax with a lazily moved reference maximum (by more
+//                 than 2^8), P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that every row
+//                 of the Q tile sees in full are not masked; the others take a bit mask per row.
 //   O += P V      tcgen05.mma with P from TMEM
 // The warps' roles, the ring, TMEM and the ping-pong of the two Q tiles are those of the prefill
 // attention over equal prompts (attn_prefill_tc.cu); here a Q tile takes part only in the key tiles
@@ -55,10 +55,10 @@ namespace {
 
 constexpr int QB = 2 * QT;                  // query rows per block
 constexpr int STAGES = 2;                   // K/V ring
-constexpr int THREADS = 22 * 32;
-constexpr int W_SM = 2;                     // softmax warps 2..17: Q tile (w - 2) / 8, key half
-                                            // ((w - 2) / 4) & 1, TMEM lane quarter w % 4
-constexpr int W_OUT = 18;                   // first output warp (18..21)
+constexpr int THREADS = 14 * 32;
+constexpr int W_SM = 2;                     // softmax warps 2..9: Q tile (w - 2) / 4, TMEM lane
+                                            // quarter w % 4
+constexpr int W_OUT = 10;                   // first output warp (10..13)
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long kWaitCycles = 1ll << 34;   // attend_row may keep the other warps waiting
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
@@ -79,9 +79,9 @@ struct PSmem {
   static constexpr int K_OFF = 2 * TILE;               // K stages
   static constexpr int V_OFF = K_OFF + STAGES * TILE;  // V stages
   static constexpr int O_OFF = V_OFF + STAGES * TILE;  // one output box
-  static constexpr int L_OFF = O_OFF + BOX;            // row sums l [tile][key half][row]
-  static constexpr int MX_OFF = L_OFF + 2 * 2 * QT * 4;  // row maxima [parity][tile][half][row]
-  static constexpr int BAR_OFF = MX_OFF + 2 * 2 * 2 * QT * 4;
+  static constexpr int L_OFF = O_OFF + BOX;            // row sums l [tile][row]
+  static constexpr int NQ_OFF = L_OFF + 2 * QT * 4;    // the sequences' query rows (start only)
+  static constexpr int BAR_OFF = NQ_OFF + kMaxSeqs * 4;
   static constexpr int ITEM_OFF = BAR_OFF + 512;
   static constexpr int SEQ_OFF = ITEM_OFF + ITEMS * 64;  // sequences, longest first
   static constexpr int BYTES = SEQ_OFF + kMaxSeqs * (int)sizeof(Seq) + 1024;   // 1024: alignment
@@ -89,11 +89,10 @@ struct PSmem {
 static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 
 // barriers: q_full, q_free, kv_full[2], kv_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
-// l_full[2], o_staged, o_stage_free, drain, mx_ready[tile][quarter] (the two key halves of a
-// row have written their maxima), item_full[4], item_free[4]
+// l_full[2], o_staged, o_stage_free, drain, item_full[4], item_free[4]
 constexpr int B_QFULL = 0, B_QFREE = 1, B_KVFULL = 2, B_KVFREE = 4, B_SFULL = 6, B_PFULL = 8,
               B_ODONE = 10, B_OFREE = 12, B_LFULL = 14, B_OSTAGED = 16, B_OSFREE = 17,
-              B_DRAIN = 18, B_MX = 19, B_IFULL = 27, B_IFREE = B_IFULL + ITEMS,
+              B_DRAIN = 18, B_IFULL = 19, B_IFREE = B_IFULL + ITEMS,
               NBARS = B_IFREE + ITEMS;
 static_assert(NBARS * 8 + 16 <= 512, "barrier space");
 
@@ -267,7 +266,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   Seq* seqs = reinterpret_cast<Seq*>(smem + L::SEQ_OFF);
   auto item_slot = [&](int n) { return reinterpret_cast<Item*>(smem + L::ITEM_OFF + 64 * (n % ITEMS)); };
   float* l_buf = reinterpret_cast<float*>(smem + L::L_OFF);
-  float* mx_buf = reinterpret_cast<float*>(smem + L::MX_OFF);
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
 
@@ -283,18 +281,17 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(B_SFULL + t), 1);
-      mbar_init(bar(B_PFULL + t), 8);                  // one arrival per softmax warp
+      mbar_init(bar(B_PFULL + t), 4);                  // one arrival per softmax warp
       mbar_init(bar(B_ODONE + t), 1);
       mbar_init(bar(B_OFREE + t), 4);                  // one arrival per output warp
-      mbar_init(bar(B_LFULL + t), 8);                  // one arrival per softmax warp
-      for (int q = 0; q < 4; ++q) mbar_init(bar(B_MX + 4 * t + q), 2);   // both key halves
+      mbar_init(bar(B_LFULL + t), 4);                  // one arrival per softmax warp
     }
     mbar_init(bar(B_OSTAGED), 4);                      // one arrival per output warp
     mbar_init(bar(B_OSFREE), 1);
     mbar_init(bar(B_DRAIN), 1);
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(bar(B_IFULL + i), 1);
-      mbar_init(bar(B_IFREE + i), 1 + 16 + 4);         // the MMA issuer, softmax and output warps
+      mbar_init(bar(B_IFREE + i), 1 + 8 + 4);         // the MMA issuer, softmax and output warps
     }
     *abort_flag = 0;
     *live = 0;
@@ -311,10 +308,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   pdl_wait();
 
   // ---- the sequences, longest first (by query rows, then by index).  The ones whose offsets do
-  // not fit their buffers count as empty.  l_buf and mx_buf hold the unsorted rows meanwhile.
+  // not fit their buffers count as empty.
   Seq me{0, 0, 0, 0};
-  int* nq_all = reinterpret_cast<int*>(l_buf);         // kMaxSeqs ints: within l_buf
-  static_assert(kMaxSeqs * 4 <= 2 * 2 * QT * 4, "the row sums' buffer holds the lengths");
+  int* nq_all = reinterpret_cast<int*>(smem + L::NQ_OFF);
   if (threadIdx.x < kMaxSeqs) {
     if ((int)threadIdx.x < pa.ns) {
       const int b = pa.s0 + threadIdx.x;
@@ -424,15 +420,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         umma_commit(bar(B_SFULL + t));
       };
       // O_t (+)= P_t V of the same key steps: step i reads the 8 TMEM columns of P of keys 16i..
-      // (key half i / 4 keeps its P in the first 32 of its 64 S columns) and rows 16i.. of V (2048
-      // bytes per step in its MN-major 128B-swizzled layout)
+      // (32 keys keep their P in the first 16 of their S columns) and rows 16i.. of V (2048 bytes per
+      // step in its MN-major 128B-swizzled layout)
       auto issue_pv = [&](int t, int g, const KeySteps& ks, bool first) {
         const int st = g % STAGES;
         const uint64_t vd = smem_desc(vbase + st * L::TILE, BOX, 1024);
 #pragma unroll
         for (int i = 0; i < KT / 16; ++i)
           if (i >= ks.s0 && i < ks.s1)
-            umma_ts(tmem + o_col(t), tmem + s_col(t) + 64 * (i >> 2) + 8 * (i & 3),
+            umma_ts(tmem + o_col(t), tmem + s_col(t) + 32 * (i >> 1) + 8 * (i & 1),
                     vd + (uint64_t)(i * 128), idesc_o, (!first || i > ks.s0) ? 1u : 0u);
         umma_commit(bar(B_ODONE + t));
       };
@@ -515,23 +511,17 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
     }
   } else if (warp >= W_SM && warp < W_OUT) {
-    // ------------------------------------------------------------ softmax: one key half of
-    // one Q tile's rows.  Two threads per row: half c takes key columns 64c .. 64c + 63 of each
-    // S tile, the row maximum is exchanged through shared memory (mx_ready barrier of the two
-    // warps of a lane quarter), and half c writes its P over the first 32 of its own S columns
-    // and rescales O columns c d/2 ..
-    const int t = (warp - W_SM) >> 3, c = ((warp - W_SM) >> 2) & 1;
+    // ------------------------------------------------------------ softmax of one Q tile's rows
+    const int t = (warp - W_SM) >> 2;
     const int quarter = warp & 3;                      // TMEM lanes 32 quarter ..
     const int m = 32 * quarter + lane;                 // row within the Q tile
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t srow = lane_addr + s_col(t) + 64 * c;
-    const uint32_t mxb = bar(B_MX + 4 * t + quarter);
+    const uint32_t srow = lane_addr + s_col(t);
     const float sl2 = pa.scale_log2;
     int sc = 0, uses = 0;                              // S products consumed, items finished
     bool ok = true;
     // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them is
-    // decided for the whole warp, waits included (a lane that gave up takes its warp along);
-    // both halves of a row take the same decisions (the same maximum)
+    // decided for the whole warp, waits included (a lane that gave up takes its warp along)
     for (int n = 0; ok; ++n) {
       const volatile Item* it = item_wait(n);          // read again where needed: no registers for it
       if (!__all_sync(0xFFFFFFFFu, it != nullptr) || it->hq < 0) break;
@@ -540,7 +530,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (lane == 0) item_done(n);
         continue;
       }
-      float m_ref = -INFINITY, l_sum = 0.0f;           // l over this half's keys
+      float m_ref = -INFINITY, l_sum = 0.0f;
       for (int j = 0; j < nt; ++j, ++sc) {
         // masked: some row of the Q tile does not see every key of the tile (warp-uniform); ahead:
         // the position of the Q tile's first row less the key tile's first position
@@ -549,77 +539,62 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const bool masked = ahead < KT - 1 ||
                             (w.window != 0 && k0 + KT > w.sinks &&
                              ahead + min(QT, it->rows - t * QT) > w.window);
-        // what each row sees of this half, 32 columns at a time: all of them (2) or none (0) for
-        // the whole warp, or some (1)
-        uint32_t vis[2] = {~0u, ~0u};
-        int mode[2] = {2, 2};
-        if (masked) {
-#pragma unroll
-          for (int c2 = 0; c2 < 2; ++c2) {
-            vis[c2] = visible_bits(k0 + 64 * c + 32 * c2, k0 + ahead + m, w.window, w.sinks);
-            mode[c2] = !__any_sync(0xFFFFFFFFu, vis[c2] != 0u)    ? 0
-                       : __all_sync(0xFFFFFFFFu, vis[c2] == ~0u) ? 2
-                                                                 : 1;
-          }
-        }
         const bool got = bwait(bar(B_SFULL + t), (uint32_t)(sc & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // pass 1: this half's maximum, 32 columns at a time (the second load in flight).  Columns that
-        // a row does not see are set to -inf, in TMEM too: pass 2 reads them there.
+        // pass 1: the row's maximum, 32 columns at a time (the next load in flight)
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto max_chunk = [&](float (&v)[32], int c2) {
-          if (mode[c2] == 1) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (vis[c2] >> e & 1u) ? v[e] : -INFINITY;
-            tmem_st16(srow + 32 * c2, reinterpret_cast<const uint32_t*>(v));
-            tmem_st16(srow + 32 * c2 + 16, reinterpret_cast<const uint32_t*>(v) + 16);
-          }
+        auto max_chunk = [&](const float (&v)[32]) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2)
             m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], v[e], v[e + 1]);
         };
+        float va[32], vb[32];
+        unsigned none = 0;                             // chunks that no row of the warp sees
         if (masked) {
-          float v[32];
+          // keys that a row does not see are set to -inf, in TMEM too: pass 2 reads them there
 #pragma unroll 1
-          for (int c2 = 0; c2 < 2; ++c2) {
-            if (mode[c2] == 0) continue;
-            tmem_ld32(srow + 32 * c2, v);
-            tmem_wait_ld_dep(v);
-            max_chunk(v, c2);
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t vis = visible_bits(k0 + 32 * c, k0 + ahead + m, w.window, w.sinks);
+            if (!__any_sync(0xFFFFFFFFu, vis != 0u)) {
+              none |= 1u << c;
+              continue;
+            }
+            tmem_ld32(srow + 32 * c, va);
+            tmem_wait_ld_dep(va);
+            if (!__all_sync(0xFFFFFFFFu, vis == ~0u)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) va[e] = (vis >> e & 1u) ? va[e] : -INFINITY;
+              tmem_st16(srow + 32 * c, reinterpret_cast<const uint32_t*>(va));
+              tmem_st16(srow + 32 * c + 16, reinterpret_cast<const uint32_t*>(va) + 16);
+            }
+            max_chunk(va);
           }
           tmem_wait_st();
         } else {
-          float va[32], vb[32];
           tmem_ld32(srow, va);
           tmem_wait_ld_dep(va);
           tmem_ld32(srow + 32, vb);
-          max_chunk(va, 0);
+          max_chunk(va);
           tmem_wait_ld_dep(vb);
-          max_chunk(vb, 1);
-        }
-        // the row maximum over both halves (slot of this tile's parity: the other half reads
-        // it before either can write the slot again two tiles on)
-        float* mx_slot = mx_buf + (((sc & 1) * 2 + t) * 2) * QT;
-        mx_slot[c * QT + m] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(mxb);
-        const bool ex = bwait(mxb, (uint32_t)(sc & 1), abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, ex)) {
-          ok = false;
-          break;
+          tmem_ld32(srow + 64, va);
+          max_chunk(vb);
+          tmem_wait_ld_dep(va);
+          tmem_ld32(srow + 96, vb);
+          max_chunk(va);
+          tmem_wait_ld_dep(vb);
+          max_chunk(vb);
         }
         // in base 2 (scale > 0, so scaling after the maximum is the same); -inf for a row that
         // has seen no key yet
-        const float mx = fmaxf(mx_slot[m], mx_slot[QT + m]) * sl2;
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
         if (__any_sync(0xFFFFFFFFu, mx > m_ref + 8.0f)) {
           // move the reference maximum of every row of the warp to max(m_ref, mx): O and l
           // scale by 2^(m_ref - m_new) (1 for rows whose maximum did not grow); O holds P V of
-          // the item's earlier tiles once their MMAs are done; this half rescales its d/2
-          // columns of O
+          // the item's earlier tiles once their MMAs are done
           const float m_new = fmaxf(m_ref, mx);
           const float alpha = (m_ref == -INFINITY) ? 0.0f : ex2(m_ref - m_new);
           if (j > 0) {
@@ -629,10 +604,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
               break;
             }
             tc_fence_after();
-#pragma unroll
-            for (int c16 = 0; c16 < D / 32; ++c16) {
+#pragma unroll 1
+            for (int c16 = 0; c16 < D / 16; ++c16) {
               uint32_t wv[16];
-              const uint32_t oa = lane_addr + o_col(t) + (uint32_t)(c * (D / 2) + 16 * c16);
+              const uint32_t oa = lane_addr + o_col(t) + (uint32_t)(16 * c16);
               tmem_ld16(oa, wv);
               tmem_wait_ld();
 #pragma unroll
@@ -646,12 +621,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           m_ref = m_new;
         }
         // pass 2: p = 2^(s * scale - m_ref), 32 columns at a time (the scaling and the row sums
-        // two elements per instruction), packed to fp16 over columns 16 c2 .. of this half's S
-        // (S columns that have been read)
+        // two elements per instruction), packed to fp16 over the first 16 of the 32 S columns
         const float ref = (m_ref == -INFINITY) ? 0.0f : m_ref;
         const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-ref, -ref);
         uint64_t ls2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
-        auto p_chunk = [&](float (&v)[32], int c2) {
+        auto p_chunk = [&](const float (&v)[32], int c) {
           uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -660,27 +634,30 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
             ls2[(e >> 1) & 1] = fadd2(ls2[(e >> 1) & 1], f2pack(p0, p1));
             pw[e / 2] = pack_h2(p0, p1);
           }
-          tmem_st16(srow + 16 * c2, pw);
+          tmem_st16(srow + 32 * c, pw);
         };
-        if (mode[0] != 0 && mode[1] != 0) {
-          float va[32], vb[32];
+        if (!masked) {
+          // the last chunk is still in registers
           tmem_ld32(srow, va);
+          p_chunk(vb, 3);
           tmem_wait_ld_dep(va);
           tmem_ld32(srow + 32, vb);
           p_chunk(va, 0);
           tmem_wait_ld_dep(vb);
+          tmem_ld32(srow + 64, va);
           p_chunk(vb, 1);
+          tmem_wait_ld_dep(va);
+          p_chunk(va, 2);
         } else {
 #pragma unroll 1
-          for (int c2 = 0; c2 < 2; ++c2) {
-            if (mode[c2] != 0) {
-              float v[32];
-              tmem_ld32(srow + 32 * c2, v);
-              tmem_wait_ld_dep(v);
-              p_chunk(v, c2);
+          for (int c = 0; c < 4; ++c) {
+            if (none >> c & 1u) {
+              const uint32_t zeros[16] = {};
+              tmem_st16(srow + 32 * c, zeros);
             } else {
-              const uint32_t none[16] = {};
-              tmem_st16(srow + 16 * c2, none);
+              tmem_ld32(srow + 32 * c, va);
+              tmem_wait_ld_dep(va);
+              p_chunk(va, c);
             }
           }
         }
@@ -692,7 +669,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (lane == 0) mbar_arrive(bar(B_PFULL + t));
       }
       if (!ok) break;
-      // this half's row sums for the output warps, once they have taken the previous item's
+      // the row sums for the output warps, once they have taken the previous item's
       if (uses > 0) {
         const bool fr = bwait(bar(B_OFREE + t), (uint32_t)((uses - 1) & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, fr)) {
@@ -700,7 +677,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           break;
         }
       }
-      l_buf[(t * 2 + c) * QT + m] = l_sum;
+      l_buf[t * QT + m] = l_sum;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(B_LFULL + t));
@@ -742,7 +719,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         ++uses[t];
         // (a row that sees nothing: O 0, or NaN, which is mended below)
         const float inv = pos + m >= 0
-                              ? 1.0f / (l_buf[(t * 2) * QT + m] + l_buf[(t * 2 + 1) * QT + m])
+                              ? 1.0f / l_buf[t * QT + m]
                               : 0.0f;
         // O / l in 64-column boxes.  A full tile: staged in shared memory (the 128B-swizzled layout of
         // the output map: 16-byte chunk k of row m at chunk k ^ (m % 8)) and stored by TMA.  The
