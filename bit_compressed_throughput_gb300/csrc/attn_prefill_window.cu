@@ -88,11 +88,11 @@ struct PSmem {
 };
 static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 
-// barriers: q_full, q_free, kv_full[2], kv_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
+// barriers: q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
 // l_full[2], o_staged, o_stage_free, drain, item_full[4], item_free[4]
-constexpr int B_QFULL = 0, B_QFREE = 1, B_KVFULL = 2, B_KVFREE = 4, B_SFULL = 6, B_PFULL = 8,
-              B_ODONE = 10, B_OFREE = 12, B_LFULL = 14, B_OSTAGED = 16, B_OSFREE = 17,
-              B_DRAIN = 18, B_IFULL = 19, B_IFREE = B_IFULL + ITEMS,
+constexpr int B_QFULL = 0, B_QFREE = 1, B_KFULL = 2, B_KFREE = 4, B_VFULL = 6, B_VFREE = 8,
+              B_SFULL = 10, B_PFULL = 12, B_ODONE = 14, B_OFREE = 16, B_LFULL = 18, B_OSTAGED = 20,
+              B_OSFREE = 21, B_DRAIN = 22, B_IFULL = 23, B_IFREE = B_IFULL + ITEMS,
               NBARS = B_IFREE + ITEMS;
 static_assert(NBARS * 8 + 16 <= 512, "barrier space");
 
@@ -276,8 +276,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     mbar_init(bar(B_QFULL), 1);
     mbar_init(bar(B_QFREE), 1);
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(bar(B_KVFULL + i), 1);
-      mbar_init(bar(B_KVFREE + i), 1);
+      for (int r : {B_KFULL, B_KFREE, B_VFULL, B_VFREE}) mbar_init(bar(r + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(B_SFULL + t), 1);
@@ -348,7 +347,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (warp == 0) {
     // ------------------------------------------------------------ items and TMA producer
     if (lane == 0) {
-      int kvg = 0, qn = 0;                             // K/V tiles, Q pairs issued
+      int kvg = 0, qn = 0, kn = 0, vn = 0;             // key tiles, Q pairs, K and V tiles issued
       bool ok = true;
       Cursor cur = first_item(seqs, nseq);
       bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
@@ -366,35 +365,51 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int nkv = it.u.count();
         if (nkv == 0) continue;
         const int hk = it.hq / (w.Hq / w.Hkv);
-        // the previous item's S products are done with the Q tiles
-        if (qn > 0 && !bwait(bar(B_QFREE), (uint32_t)((qn - 1) & 1), abort_flag)) break;
-        mbar_expect_tx(bar(B_QFULL), (uint32_t)(2 * L::TILE));
-        for (int t = 0; t < 2; ++t)
-          for (int c = 0; c < NB; ++c)
-            tma_load_2d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ,
-                        it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL));
-        ++qn;
         for (int j = 0; j < nkv; ++j, ++kvg) {
-          const int st = kvg % STAGES;
-          if (kvg >= STAGES &&
-              !bwait(bar(B_KVFREE + st), (uint32_t)(((kvg / STAGES) & 1) ^ 1), abort_flag)) {
+          // K and V have rings of their own: a K stage is free once both Q tiles' S products
+          // have read it, a whole softmax before the V stage of the same tile
+          const int st = kvg % STAGES, row = it.krow + it.u.tile(j) * KT;
+          auto load = [&](const CUtensorMap* tm, int off, int full, int free) {
+            if (kvg >= STAGES &&
+                !bwait(bar(free + st), (uint32_t)(((kvg / STAGES) & 1) ^ 1), abort_flag))
+              return false;
+            mbar_expect_tx(bar(full + st), (uint32_t)L::TILE);
+            for (int c = 0; c < NB; ++c)
+              tma_load_2d(smem_u32(smem + off + st * L::TILE + c * BOX), tm, hk * D + 64 * c, row,
+                          bar(full + st));
+            return true;
+          };
+          if (!load(&tmK, L::K_OFF, B_KFULL, B_KFREE)) {
             ok = false;
             break;
           }
-          const int row = it.krow + it.u.tile(j) * KT;
-          mbar_expect_tx(bar(B_KVFULL + st), (uint32_t)(2 * L::TILE));
-          for (int c = 0; c < NB; ++c) {
-            tma_load_2d(smem_u32(smem + L::K_OFF + st * L::TILE + c * BOX), &tmK,
-                        hk * D + 64 * c, row, bar(B_KVFULL + st));
-            tma_load_2d(smem_u32(smem + L::V_OFF + st * L::TILE + c * BOX), &tmV,
-                        hk * D + 64 * c, row, bar(B_KVFULL + st));
+          kn = kvg + 1;
+          if (j == 0) {
+            // Q, when the previous item's S products are done with it
+            if (qn > 0 && !bwait(bar(B_QFREE), (uint32_t)((qn - 1) & 1), abort_flag)) {
+              ok = false;
+              break;
+            }
+            mbar_expect_tx(bar(B_QFULL), (uint32_t)(2 * L::TILE));
+            for (int t = 0; t < 2; ++t)
+              for (int c = 0; c < NB; ++c)
+                tma_load_2d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ,
+                            it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL));
+            ++qn;
           }
+          if (!load(&tmV, L::V_OFF, B_VFULL, B_VFREE)) {
+            ok = false;
+            break;
+          }
+          vn = kvg + 1;
         }
       }
       // every issued copy has landed before the CTA exits
       if (qn > 0) drain_wait(bar(B_QFULL), (uint32_t)((qn - 1) & 1));
-      for (int i = max(0, kvg - STAGES); i < kvg; ++i)
-        drain_wait(bar(B_KVFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
+      for (int i = max(0, kn - STAGES); i < kn; ++i)
+        drain_wait(bar(B_KFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
+      for (int i = max(0, vn - STAGES); i < vn; ++i)
+        drain_wait(bar(B_VFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -432,9 +447,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                     vd + (uint64_t)(i * 128), idesc_o, (!first || i > ks.s0) ? 1u : 0u);
         umma_commit(bar(B_ODONE + t));
       };
-      auto wait_kv = [&](int g) {
-        if (!bwait(bar(B_KVFULL + g % STAGES), (uint32_t)((g / STAGES) & 1), abort_flag))
-          return false;
+      auto wait_tile = [&](int full, int g) {
+        if (!bwait(bar(full + g % STAGES), (uint32_t)((g / STAGES) & 1), abort_flag)) return false;
         tc_fence_after();
         return true;
       };
@@ -452,12 +466,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         int tile = u.tile(0);
         bool sees[2] = {kt[0].has(tile), kt[1].has(tile)};
         KeySteps ks[2] = {steps(0, tile), steps(1, tile)};
-        if (!bwait(bar(B_QFULL), (uint32_t)(qn & 1), abort_flag) || !wait_kv(kvg)) break;
+        if (!bwait(bar(B_QFULL), (uint32_t)(qn & 1), abort_flag) || !wait_tile(B_KFULL, kvg))
+          break;
         ++qn;
         bool begun[2] = {false, false};                // Q tile t has a P V product of this item
         for (int t = 0; t < 2; ++t)
           if (sees[t]) issue_s(t, kvg, ks[t]);
         issued = true;
+        umma_commit(bar(B_KFREE + kvg % STAGES));      // K of the tile read by the S products above
         if (nkv == 1) umma_commit(bar(B_QFREE));       // every S product of the item issued
         for (int j = 0; j < nkv && ok; ++j) {
           const int g = kvg + j;
@@ -466,7 +482,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           tile = more ? u.tile(j + 1) : 0;
           const bool sees_n[2] = {more && kt[0].has(tile), more && kt[1].has(tile)};
           const KeySteps ks_n[2] = {steps(0, tile), steps(1, tile)};
-          bool next_ready = false;                     // K/V of tile j + 1 waited for
+          bool next_ready = false, v_ready = false;    // K of tile j + 1, V of tile j waited for
           for (int t = 0; t < 2 && ok; ++t) {
             if (sees[t]) {
               if (!bwait(bar(B_PFULL + t), (uint32_t)(pc[t] & 1), abort_flag)) {
@@ -479,6 +495,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                 ok = false;
                 break;
               }
+              if (!v_ready && !wait_tile(B_VFULL, g)) {
+                ok = false;
+                break;
+              }
+              v_ready = true;
               tc_fence_after();
               issue_pv(t, g, ks[t], !begun[t]);
               if (!begun[t]) ++uses[t];
@@ -488,7 +509,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
             // S_t of the next key tile: its columns hold no P that is still to be read (this Q
             // tile's earlier products were issued before)
             if (sees_n[t]) {
-              if (!next_ready && !wait_kv(g + 1)) {
+              if (!next_ready && !wait_tile(B_KFULL, g + 1)) {
                 ok = false;
                 break;
               }
@@ -500,7 +521,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           if (!ok) break;
           if (j == nkv - 2) umma_commit(bar(B_QFREE));      // the item's last S products
-          umma_commit(bar(B_KVFREE + g % STAGES));     // K/V tile g read by every MMA above
+          if (more) umma_commit(bar(B_KFREE + (g + 1) % STAGES));
+          umma_commit(bar(B_VFREE + g % STAGES));      // V of tile g read by every MMA above
         }
         kvg += nkv;
       }
