@@ -67,6 +67,7 @@ constexpr int kMaxSeqs = 384;               // sequences per launch
 static_assert(kMaxSeqs <= THREADS, "one thread per sequence reads its offsets");
 
 constexpr int ITEMS = 4;                    // ring of work items
+constexpr unsigned kAllSteps = (KT / 16) << 4;   // every 16-key step of a tile (s0 | s1 << 4)
 
 struct Seq {
   int q0, nq, k0, nk;                       // first query row, rows, first K/V row, rows
@@ -94,7 +95,7 @@ constexpr int B_QFULL = 0, B_QFREE = 1, B_KFULL = 2, B_KFREE = 4, B_VFULL = 6, B
               B_SFULL = 10, B_PFULL = 12, B_ODONE = 14, B_OFREE = 16, B_LFULL = 18, B_OSTAGED = 20,
               B_OSFREE = 21, B_DRAIN = 22, B_IFULL = 23, B_IFREE = B_IFULL + ITEMS,
               NBARS = B_IFREE + ITEMS;
-static_assert(NBARS * 8 + 16 <= 512, "barrier space");
+static_assert(NBARS * 8 + 12 + STAGES * 4 <= 512, "barrier space");
 
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_test(bar, parity)) return true;
@@ -263,6 +264,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* live = reinterpret_cast<int*>(tmem_slot + 2);   // sequences with rows
+  unsigned* steps_of = tmem_slot + 3;                  // [STAGES]: key steps of the K tile
   Seq* seqs = reinterpret_cast<Seq*>(smem + L::SEQ_OFF);
   auto item_slot = [&](int n) { return reinterpret_cast<Item*>(smem + L::ITEM_OFF + 64 * (n % ITEMS)); };
   float* l_buf = reinterpret_cast<float*>(smem + L::L_OFF);
@@ -369,17 +371,26 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           // K and V have rings of their own: a K stage is free once both Q tiles' S products
           // have read it, a whole softmax before the V stage of the same tile
           const int st = kvg % STAGES, row = it.krow + it.u.tile(j) * KT;
-          auto load = [&](const CUtensorMap* tm, int off, int full, int free) {
+          auto load = [&](const CUtensorMap* tm, int off, int full, int free, unsigned steps) {
             if (kvg >= STAGES &&
                 !bwait(bar(free + st), (uint32_t)(((kvg / STAGES) & 1) ^ 1), abort_flag))
               return false;
+            if (full == B_KFULL) steps_of[st] = steps;  // handed on by the barrier
             mbar_expect_tx(bar(full + st), (uint32_t)L::TILE);
             for (int c = 0; c < NB; ++c)
               tma_load_2d(smem_u32(smem + off + st * L::TILE + c * BOX), tm, hk * D + 64 * c, row,
                           bar(full + st));
             return true;
           };
-          if (!load(&tmK, L::K_OFF, B_KFULL, B_KFREE)) {
+          // the 16-key steps that the Q tiles take of the tile, a byte each (s0 | s1 << 4; 0: none)
+          auto steps = [&](int t) -> unsigned {
+            if (!it.t[t].has(it.u.tile(j))) return 0u;
+            const KeySteps k = key_steps(it.u.tile(j), it.pos + t * QT,
+                                         it.pos + min(t * QT + QT, it.rows) - 1, w.window, w.sinks);
+            return (unsigned)(k.s0 | k.s1 << 4);
+          };
+          const unsigned both = steps(0) | steps(1) << 8;
+          if (!load(&tmK, L::K_OFF, B_KFULL, B_KFREE, both)) {
             ok = false;
             break;
           }
@@ -397,7 +408,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                             it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL));
             ++qn;
           }
-          if (!load(&tmV, L::V_OFF, B_VFULL, B_VFREE)) {
+          if (!load(&tmV, L::V_OFF, B_VFULL, B_VFREE, 0u)) {
             ok = false;
             break;
           }
@@ -412,7 +423,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         drain_wait(bar(B_VFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer.  Its own arithmetic
+    // is kept short (one thread's dependent instructions take longer than the tensor core's queue
+    // lasts): which key steps each Q tile takes of a key tile comes from the producer with the tile.
     if (lane == 0) {
       const uint32_t qbase = smem_u32(smem + L::Q_OFF), kbase = smem_u32(smem + L::K_OFF),
                      vbase = smem_u32(smem + L::V_OFF);
@@ -420,13 +433,18 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       bool ok = true, issued = false;
       int kvg = 0, qn = 0;                             // K/V tiles, items consumed
       int pc[2] = {0, 0}, uses[2] = {0, 0};            // P V products; items, per Q tile
-      // S_t = Q_t K^T of the key steps [s0, s1) of K/V tile g over K = D: k-step i reads 16
-      // columns, 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
-      auto issue_s = [&](int t, int g, const KeySteps& ks) {
-        const int st = g % STAGES;
+      // S_t = Q_t K^T of the key steps `ks` of K/V tile g over K = D: k-step i reads 16 columns,
+      // 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
+      auto issue_s = [&](int t, int g, unsigned ks) {
+        uint64_t kd = smem_desc(kbase + (g % STAGES) * L::TILE, 16, 1024);
         const uint64_t qd = smem_desc(qbase + t * L::TILE, 16, 1024);
-        const uint64_t kd = smem_desc(kbase + st * L::TILE, 16, 1024) + (uint64_t)(ks.s0 * 128);
-        const uint32_t idesc = idesc_qk(16 * (ks.s1 - ks.s0)), col = tmem + s_col(t) + 16 * ks.s0;
+        uint32_t idesc = kIdescS, col = tmem + s_col(t);
+        if (ks != kAllSteps) {
+          const int s0 = ks & 15, s1 = ks >> 4;
+          kd += (uint64_t)(s0 * 128);
+          idesc = idesc_qk(16 * (s1 - s0));
+          col += 16 * s0;
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
@@ -435,94 +453,88 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         umma_commit(bar(B_SFULL + t));
       };
       // O_t (+)= P_t V of the same key steps: step i reads the 8 TMEM columns of P of keys 16i..
-      // (32 keys keep their P in the first 16 of their S columns) and rows 16i.. of V (2048 bytes per
-      // step in its MN-major 128B-swizzled layout)
-      auto issue_pv = [&](int t, int g, const KeySteps& ks, bool first) {
-        const int st = g % STAGES;
-        const uint64_t vd = smem_desc(vbase + st * L::TILE, BOX, 1024);
+      // (32 keys keep their P in the first 16 of their S columns) and rows 16i.. of V (2048 bytes
+      // per step in its MN-major 128B-swizzled layout)
+      auto issue_pv = [&](int t, int g, unsigned ks, bool first) {
+        const uint64_t vd = smem_desc(vbase + (g % STAGES) * L::TILE, BOX, 1024);
+        const uint32_t od = tmem + o_col(t), pa0 = tmem + s_col(t);
+        if (ks == kAllSteps) {
+          // no branch between the steps: they issue back to back
+          umma_ts(od, pa0, vd, idesc_o, first ? 0u : 1u);
 #pragma unroll
-        for (int i = 0; i < KT / 16; ++i)
-          if (i >= ks.s0 && i < ks.s1)
-            umma_ts(tmem + o_col(t), tmem + s_col(t) + 32 * (i >> 1) + 8 * (i & 1),
-                    vd + (uint64_t)(i * 128), idesc_o, (!first || i > ks.s0) ? 1u : 0u);
+          for (int i = 1; i < KT / 16; ++i)
+            umma_ts(od, pa0 + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, 1u);
+        } else {
+          const int s0 = ks & 15, s1 = ks >> 4;
+          for (int i = s0; i < s1; ++i)
+            umma_ts(od, pa0 + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o,
+                    (!first || i > s0) ? 1u : 0u);
+        }
         umma_commit(bar(B_ODONE + t));
       };
-      auto wait_tile = [&](int full, int g) {
-        if (!bwait(bar(full + g % STAGES), (uint32_t)((g / STAGES) & 1), abort_flag)) return false;
-        tc_fence_after();
-        return true;
+      auto wait = [&](int b, int parity) {
+        if (!bwait(bar(b), (uint32_t)parity, abort_flag)) ok = false;
+      };
+      // waits for K of tile g; the steps of it that the Q tiles take
+      auto wait_k = [&](int g) -> unsigned {
+        wait(B_KFULL + g % STAGES, (g / STAGES) & 1);
+        return steps_of[g % STAGES];
       };
       for (int n = 0; ok; ++n) {
         const Item* slot = item_wait(n);
         if (!slot || slot->hq < 0) break;
-        const KeyTiles kt[2] = {slot->t[0], slot->t[1]}, u = slot->u;
-        const int pos = slot->pos, rows = slot->rows;
+        const int nkv = slot->u.count();
         item_done(n);
-        const int nkv = u.count();
         if (nkv == 0) continue;
-        auto steps = [&](int t, int tile) {
-          return key_steps(tile, pos + t * QT, pos + min(t * QT + QT, rows) - 1, w.window, w.sinks);
-        };
-        int tile = u.tile(0);
-        bool sees[2] = {kt[0].has(tile), kt[1].has(tile)};
-        KeySteps ks[2] = {steps(0, tile), steps(1, tile)};
-        if (!bwait(bar(B_QFULL), (uint32_t)(qn & 1), abort_flag) || !wait_tile(B_KFULL, kvg))
-          break;
+        wait(B_QFULL, qn & 1);
+        unsigned cur = wait_k(kvg);
+        if (!ok) break;
+        tc_fence_after();
         ++qn;
-        bool begun[2] = {false, false};                // Q tile t has a P V product of this item
-        for (int t = 0; t < 2; ++t)
-          if (sees[t]) issue_s(t, kvg, ks[t]);
         issued = true;
+        bool begun[2] = {false, false};                // Q tile t has a P V product of this item
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (cur >> (8 * t) & 0xFFu) issue_s(t, kvg, cur >> (8 * t) & 0xFFu);
         umma_commit(bar(B_KFREE + kvg % STAGES));      // K of the tile read by the S products above
         if (nkv == 1) umma_commit(bar(B_QFREE));       // every S product of the item issued
         for (int j = 0; j < nkv && ok; ++j) {
           const int g = kvg + j;
-          // the next key tile, worked out while the softmax runs
           const bool more = j + 1 < nkv;
-          tile = more ? u.tile(j + 1) : 0;
-          const bool sees_n[2] = {more && kt[0].has(tile), more && kt[1].has(tile)};
-          const KeySteps ks_n[2] = {steps(0, tile), steps(1, tile)};
-          bool next_ready = false, v_ready = false;    // K of tile j + 1, V of tile j waited for
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (sees[t]) {
-              if (!bwait(bar(B_PFULL + t), (uint32_t)(pc[t] & 1), abort_flag)) {
-                ok = false;
-                break;
-              }
+          unsigned next = 0;
+          bool v_ready = false, k_ready = !more;       // V of tile j, K of tile j + 1 waited for
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const unsigned ks = cur >> (8 * t) & 0xFFu;
+            if (ks) {
+              wait(B_PFULL + t, pc[t] & 1);
               // the first product of an item overwrites O_t: the output warps have read it
-              if (!begun[t] && uses[t] > 0 &&
-                  !bwait(bar(B_OFREE + t), (uint32_t)((uses[t] - 1) & 1), abort_flag)) {
-                ok = false;
-                break;
-              }
-              if (!v_ready && !wait_tile(B_VFULL, g)) {
-                ok = false;
-                break;
-              }
+              if (!begun[t] && uses[t] > 0) wait(B_OFREE + t, (uses[t] - 1) & 1);
+              if (!v_ready) wait(B_VFULL + g % STAGES, (g / STAGES) & 1);
               v_ready = true;
+              if (!ok) break;
               tc_fence_after();
-              issue_pv(t, g, ks[t], !begun[t]);
+              issue_pv(t, g, ks, !begun[t]);
               if (!begun[t]) ++uses[t];
               begun[t] = true;
               ++pc[t];
             }
             // S_t of the next key tile: its columns hold no P that is still to be read (this Q
             // tile's earlier products were issued before)
-            if (sees_n[t]) {
-              if (!next_ready && !wait_tile(B_KFULL, g + 1)) {
-                ok = false;
-                break;
-              }
-              next_ready = true;
-              issue_s(t, g + 1, ks_n[t]);
+            if (!k_ready) {
+              next = wait_k(g + 1);
+              if (!ok) break;
+              tc_fence_after();
+              k_ready = true;
             }
-            sees[t] = sees_n[t];
-            ks[t] = ks_n[t];
+            const unsigned ks_n = next >> (8 * t) & 0xFFu;
+            if (ks_n) issue_s(t, g + 1, ks_n);
           }
           if (!ok) break;
           if (j == nkv - 2) umma_commit(bar(B_QFREE));      // the item's last S products
           if (more) umma_commit(bar(B_KFREE + (g + 1) % STAGES));
           umma_commit(bar(B_VFREE + g % STAGES));      // V of tile g read by every MMA above
+          cur = next;
         }
         kvg += nkv;
       }
