@@ -7,7 +7,7 @@
 //   out_r,hq = sum_t softmax_t(scale * q_r,hq . k_t) v_t   over the t that i sees,
 // K/V head hq / G of G = Hq / Hkv query heads each; a row that sees nothing gets zeros.
 //
-// A CTA owns a block of 256 query rows of one (sequence, query head): two Q tiles of 128 rows that
+// A CTA owns a block of 256 query rows of one (sequence, query head): two Q tiles (A, B) of 128 rows that
 // share the K/V tiles of 128 keys.  The key tiles of a block are those that one of its rows sees
 // (first positions, then the window; key_tiles in ragged.cuh): a window costs what it shows, not the
 // sequence.  Q, K and V are read in place by TMA (boxes of 64 columns x 128 rows, 128B swizzle) at
@@ -19,9 +19,12 @@
 //                 than 2^8), P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that every row
 //                 of the Q tile sees in full are not masked; the others take a bit mask per row.
 //   O += P V      tcgen05.mma with P from TMEM
-// The warps' roles, the ring, TMEM and the ping-pong of the two Q tiles are those of the prefill
-// attention over equal prompts (attn_prefill_tc.cu); here a Q tile takes part only in the key tiles
-// that it sees, so "the next product" of a Q tile is looked up per key tile.
+// TMEM: S of A and B (128 columns each), O of A and B (d columns each).  A Q tile takes part only in
+// the key tiles that it sees, and in the 16-key steps of them that it sees.
+//   warp 0       the work items and TMA producer: K tiles, V tiles and Q, rings of two each
+//   warps 1, 2   MMA issuers of Q tiles A and B: S_t(0); then per key tile P_t(j) V_j, S_t(j + 1)
+//   warps 3-10   softmax of A and B (TMEM lanes 32 (w % 4) ..)
+//   warps 11-14  output: O_t / l of a finished block, staged in shared memory, stored by TMA
 //
 // Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it would
 // reach the rows of the Q tile that do not see it.  The output warps therefore test their rows: a
@@ -55,10 +58,11 @@ namespace {
 
 constexpr int QB = 2 * QT;                  // query rows per block
 constexpr int STAGES = 2;                   // K/V ring
-constexpr int THREADS = 14 * 32;
-constexpr int W_SM = 2;                     // softmax warps 2..9: Q tile (w - 2) / 4, TMEM lane
+constexpr int THREADS = 15 * 32;
+constexpr int W_MMA = 1;                    // MMA issuers: warps 1 and 2, one per Q tile
+constexpr int W_SM = 3;                     // softmax warps 3..10: Q tile (w - 3) / 4, TMEM lane
                                             // quarter w % 4
-constexpr int W_OUT = 10;                   // first output warp (10..13)
+constexpr int W_OUT = 11;                   // first output warp (11..14)
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long kWaitCycles = 1ll << 34;   // attend_row may keep the other warps waiting
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
@@ -93,7 +97,7 @@ static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 // l_full[2], o_staged, o_stage_free, drain, item_full[4], item_free[4]
 constexpr int B_QFULL = 0, B_QFREE = 1, B_KFULL = 2, B_KFREE = 4, B_VFULL = 6, B_VFREE = 8,
               B_SFULL = 10, B_PFULL = 12, B_ODONE = 14, B_OFREE = 16, B_LFULL = 18, B_OSTAGED = 20,
-              B_OSFREE = 21, B_DRAIN = 22, B_IFULL = 23, B_IFREE = B_IFULL + ITEMS,
+              B_OSFREE = 21, B_DRAIN = 22, B_IFULL = 24, B_IFREE = B_IFULL + ITEMS,
               NBARS = B_IFREE + ITEMS;
 static_assert(NBARS * 8 + 12 + STAGES * 4 <= 512, "barrier space");
 
@@ -276,9 +280,12 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   if (threadIdx.x == 0) {
     mbar_init(bar(B_QFULL), 1);
-    mbar_init(bar(B_QFREE), 1);
+    mbar_init(bar(B_QFREE), 2);                        // one arrival per MMA issuer
     for (int i = 0; i < STAGES; ++i) {
-      for (int r : {B_KFULL, B_KFREE, B_VFULL, B_VFREE}) mbar_init(bar(r + i), 1);
+      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_KFREE + i), 2);
+      mbar_init(bar(B_VFREE + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(B_SFULL + t), 1);
@@ -290,9 +297,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     mbar_init(bar(B_OSTAGED), 4);                      // one arrival per output warp
     mbar_init(bar(B_OSFREE), 1);
     mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN + 1), 1);
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(bar(B_IFULL + i), 1);
-      mbar_init(bar(B_IFREE + i), 1 + 8 + 4);         // the MMA issuer, softmax and output warps
+      mbar_init(bar(B_IFREE + i), 2 + 8 + 4);         // the MMA issuers, softmax and output warps
     }
     *abort_flag = 0;
     *live = 0;
@@ -422,22 +430,27 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       for (int i = max(0, vn - STAGES); i < vn; ++i)
         drain_wait(bar(B_VFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer.  Its own arithmetic
-    // is kept short (one thread's dependent instructions take longer than the tensor core's queue
-    // lasts): which key steps each Q tile takes of a key tile comes from the producer with the tile.
+  } else if (warp < W_SM) {
+    // ------------------------------------------------------------ MMA issuer of Q tile t.  One
+    // thread takes about 80 cycles per MMA it issues (650 for S's eight, 700 for P V's), more than
+    // the tensor core takes for them (64 each), so each Q tile has a thread of its own: the
+    // order that matters is within a Q tile (S_t(j + 1) overwrites the columns of P_t(j) only
+    // after P_t(j) V_j has read them), and the rings count an arrival of each.  Its own arithmetic
+    // is kept short: which key steps the Q tiles take of a key tile comes from the producer with
+    // the tile.
     if (lane == 0) {
-      const uint32_t qbase = smem_u32(smem + L::Q_OFF), kbase = smem_u32(smem + L::K_OFF),
-                     vbase = smem_u32(smem + L::V_OFF);
+      const int t = warp - W_MMA;
+      const uint32_t qbase = smem_u32(smem + L::Q_OFF + t * L::TILE),
+                     kbase = smem_u32(smem + L::K_OFF), vbase = smem_u32(smem + L::V_OFF);
       const uint32_t idesc_o = idesc_pv(D);
-      bool ok = true, issued = false;
+      bool ok = true;
       int kvg = 0, qn = 0;                             // K/V tiles, items consumed
-      int pc[2] = {0, 0}, uses[2] = {0, 0};            // P V products; items, per Q tile
+      int pc = 0, uses = 0;                            // P V products; items of this Q tile
       // S_t = Q_t K^T of the key steps `ks` of K/V tile g over K = D: k-step i reads 16 columns,
       // 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
-      auto issue_s = [&](int t, int g, unsigned ks) {
+      auto issue_s = [&](int g, unsigned ks) {
         uint64_t kd = smem_desc(kbase + (g % STAGES) * L::TILE, 16, 1024);
-        const uint64_t qd = smem_desc(qbase + t * L::TILE, 16, 1024);
+        const uint64_t qd = smem_desc(qbase, 16, 1024);
         uint32_t idesc = kIdescS, col = tmem + s_col(t);
         if (ks != kAllSteps) {
           const int s0 = ks & 15, s1 = ks >> 4;
@@ -455,7 +468,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       // O_t (+)= P_t V of the same key steps: step i reads the 8 TMEM columns of P of keys 16i..
       // (32 keys keep their P in the first 16 of their S columns) and rows 16i.. of V (2048 bytes
       // per step in its MN-major 128B-swizzled layout)
-      auto issue_pv = [&](int t, int g, unsigned ks, bool first) {
+      auto issue_pv = [&](int g, unsigned ks, bool first) {
         const uint64_t vd = smem_desc(vbase + (g % STAGES) * L::TILE, BOX, 1024);
         const uint32_t od = tmem + o_col(t), pa0 = tmem + s_col(t);
         if (ks == kAllSteps) {
@@ -475,10 +488,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       auto wait = [&](int b, int parity) {
         if (!bwait(bar(b), (uint32_t)parity, abort_flag)) ok = false;
       };
-      // waits for K of tile g; the steps of it that the Q tiles take
+      // waits for K of tile g; the steps of it that this Q tile takes (0: none)
       auto wait_k = [&](int g) -> unsigned {
         wait(B_KFULL + g % STAGES, (g / STAGES) & 1);
-        return steps_of[g % STAGES];
+        return steps_of[g % STAGES] >> (8 * t) & 0xFFu;
       };
       for (int n = 0; ok; ++n) {
         const Item* slot = item_wait(n);
@@ -491,58 +504,47 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (!ok) break;
         tc_fence_after();
         ++qn;
-        issued = true;
-        bool begun[2] = {false, false};                // Q tile t has a P V product of this item
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (cur >> (8 * t) & 0xFFu) issue_s(t, kvg, cur >> (8 * t) & 0xFFu);
-        umma_commit(bar(B_KFREE + kvg % STAGES));      // K of the tile read by the S products above
+        bool begun = false;                            // there is a P V product of this item
+        if (cur) issue_s(kvg, cur);
+        umma_commit(bar(B_KFREE + kvg % STAGES));      // K of the tile read by the product above
         if (nkv == 1) umma_commit(bar(B_QFREE));       // every S product of the item issued
-        for (int j = 0; j < nkv && ok; ++j) {
+        for (int j = 0; j < nkv; ++j) {
           const int g = kvg + j;
-          const bool more = j + 1 < nkv;
           unsigned next = 0;
-          bool v_ready = false, k_ready = !more;       // V of tile j, K of tile j + 1 waited for
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const unsigned ks = cur >> (8 * t) & 0xFFu;
-            if (ks) {
-              wait(B_PFULL + t, pc[t] & 1);
-              // the first product of an item overwrites O_t: the output warps have read it
-              if (!begun[t] && uses[t] > 0) wait(B_OFREE + t, (uses[t] - 1) & 1);
-              if (!v_ready) wait(B_VFULL + g % STAGES, (g / STAGES) & 1);
-              v_ready = true;
-              if (!ok) break;
-              tc_fence_after();
-              issue_pv(t, g, ks, !begun[t]);
-              if (!begun[t]) ++uses[t];
-              begun[t] = true;
-              ++pc[t];
-            }
+          if (cur) {
+            wait(B_PFULL + t, pc & 1);
+            // the first product of an item overwrites O_t: the output warps have read it
+            if (!begun && uses > 0) wait(B_OFREE + t, (uses - 1) & 1);
+          }
+          // waited for in any case: an issuer that ran ahead of the other would arrive twice in one
+          // phase of V's free barrier
+          wait(B_VFULL + g % STAGES, (g / STAGES) & 1);
+          if (!ok) break;
+          if (cur) {
+            tc_fence_after();
+            issue_pv(g, cur, !begun);
+            if (!begun) ++uses;
+            begun = true;
+            ++pc;
+          }
+          umma_commit(bar(B_VFREE + g % STAGES));      // V of tile g read by the product above
+          if (j + 1 < nkv) {
             // S_t of the next key tile: its columns hold no P that is still to be read (this Q
             // tile's earlier products were issued before)
-            if (!k_ready) {
-              next = wait_k(g + 1);
-              if (!ok) break;
-              tc_fence_after();
-              k_ready = true;
-            }
-            const unsigned ks_n = next >> (8 * t) & 0xFFu;
-            if (ks_n) issue_s(t, g + 1, ks_n);
+            next = wait_k(g + 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (next) issue_s(g + 1, next);
+            umma_commit(bar(B_KFREE + (g + 1) % STAGES));
+            if (j + 2 == nkv) umma_commit(bar(B_QFREE));    // the item's last S product
           }
-          if (!ok) break;
-          if (j == nkv - 2) umma_commit(bar(B_QFREE));      // the item's last S products
-          if (more) umma_commit(bar(B_KFREE + (g + 1) % STAGES));
-          umma_commit(bar(B_VFREE + g % STAGES));      // V of tile g read by every MMA above
           cur = next;
         }
         kvg += nkv;
       }
       // the CTA frees TMEM only after every MMA issued here has completed
-      if (issued) {
-        umma_commit(bar(B_DRAIN));
-        drain_wait(bar(B_DRAIN), 0u);
-      }
+      umma_commit(bar(B_DRAIN + t));
+      drain_wait(bar(B_DRAIN + t), 0u);
     }
   } else if (warp >= W_SM && warp < W_OUT) {
     // ------------------------------------------------------------ softmax of one Q tile's rows
