@@ -431,121 +431,118 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         drain_wait(bar(B_VFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
     }
   } else if (warp < W_SM) {
-    // ------------------------------------------------------------ MMA issuer of Q tile t.  One
-    // thread takes about 80 cycles per MMA it issues (650 for S's eight, 700 for P V's), more than
-    // the tensor core takes for them (64 each), so each Q tile has a thread of its own: the
-    // order that matters is within a Q tile (S_t(j + 1) overwrites the columns of P_t(j) only
-    // after P_t(j) V_j has read them), and the rings count an arrival of each.  Its own arithmetic
-    // is kept short: which key steps the Q tiles take of a key tile comes from the producer with
-    // the tile.
-    if (lane == 0) {
-      const int t = warp - W_MMA;
-      const uint32_t qbase = smem_u32(smem + L::Q_OFF + t * L::TILE),
-                     kbase = smem_u32(smem + L::K_OFF), vbase = smem_u32(smem + L::V_OFF);
-      const uint32_t idesc_o = idesc_pv(D);
-      bool ok = true;
-      int kvg = 0, qn = 0;                             // K/V tiles, items consumed
-      int pc = 0, uses = 0;                            // P V products; items of this Q tile
-      // S_t = Q_t K^T of the key steps `ks` of K/V tile g over K = D: k-step i reads 16 columns,
-      // 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
-      auto issue_s = [&](int g, unsigned ks) {
-        uint64_t kd = smem_desc(kbase + (g % STAGES) * L::TILE, 16, 1024);
-        const uint64_t qd = smem_desc(qbase, 16, 1024);
-        uint32_t idesc = kIdescS, col = tmem + s_col(t);
-        if (ks != kAllSteps) {
-          const int s0 = ks & 15, s1 = ks >> 4;
-          kd += (uint64_t)(s0 * 128);
-          idesc = idesc_qk(16 * (s1 - s0));
-          col += 16 * s0;
-        }
+    // ------------------------------------------------------------ MMA issuer of Q tile t.  Each
+    // Q tile has a warp of its own: the order that matters is within a Q tile (S_t(j + 1)
+    // overwrites the columns of P_t(j) only after P_t(j) V_j has read them), and the rings count an
+    // arrival of each.  What is between a P and the next S is on the critical path (softmax and
+    // products of one Q tile take turns), so everything else is done before P is waited for or
+    // after S is issued, and which key steps the Q tiles take of a key tile comes from the producer
+    // with the tile.  The whole warp runs the loop on values that are the same in every lane, and
+    // one lane's predicate issues: descriptors stay in uniform registers.
+    const int t = __shfl_sync(0xFFFFFFFFu, warp - W_MMA, 0);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), sbase = smem_u32(smem);
+    const uint32_t one = elect_one();
+    const uint32_t od = tm + o_col(t), scol = tm + s_col(t);
+    const uint64_t qd = smem_desc(sbase + L::Q_OFF + t * L::TILE, 16, 1024);
+    const uint32_t idesc_o = idesc_pv(D);
+    int kvg = 0, qn = 0;                               // K/V tiles, items consumed
+    int pc = 0, uses = 0;                              // P V products; items of this Q tile
+    bool ok = true;
+    auto wait = [&](int b, int parity) {
+      ok = ok && __all_sync(0xFFFFFFFFu, bwait(bar(b), (uint32_t)parity, abort_flag));
+    };
+    auto commit = [&](int b) { umma_commit_if(bar(b), one); };
+    // S_t = Q_t K^T of the key steps `ks` of K/V tile g over K = D: k-step i reads 16 columns,
+    // 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
+    auto issue_s = [&](int g, unsigned ks) {
+      const int s0 = ks & 15, s1 = ks >> 4;
+      const uint64_t kd = smem_desc(sbase + L::K_OFF + (g % STAGES) * L::TILE, 16, 1024) +
+                          (uint64_t)(s0 * 128);
+      const uint32_t idesc = idesc_qk(16 * (s1 - s0)), col = scol + 16 * s0;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
-          umma_f16(col, qd + off, kd + off, idesc, i > 0 ? 1u : 0u);
-        }
-        umma_commit(bar(B_SFULL + t));
-      };
-      // O_t (+)= P_t V of the same key steps: step i reads the 8 TMEM columns of P of keys 16i..
-      // (32 keys keep their P in the first 16 of their S columns) and rows 16i.. of V (2048 bytes
-      // per step in its MN-major 128B-swizzled layout)
-      auto issue_pv = [&](int g, unsigned ks, bool first) {
-        const uint64_t vd = smem_desc(vbase + (g % STAGES) * L::TILE, BOX, 1024);
-        const uint32_t od = tmem + o_col(t), pa0 = tmem + s_col(t);
-        if (ks == kAllSteps) {
-          // no branch between the steps: they issue back to back
-          umma_ts(od, pa0, vd, idesc_o, first ? 0u : 1u);
+      for (int i = 0; i < D / 16; ++i) {
+        const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
+        umma_f16_if(col, qd + off, kd + off, idesc, i > 0, one);
+      }
+      commit(B_SFULL + t);
+    };
+    // O_t (+)= P_t V of the same key steps: step i reads the 8 TMEM columns of P of keys 16i..
+    // (32 keys keep their P in the first 16 of their S columns) and rows 16i.. of V (2048 bytes
+    // per step in its MN-major 128B-swizzled layout)
+    auto issue_pv = [&](int g, unsigned ks, uint32_t add) {
+      const uint64_t vd = smem_desc(sbase + L::V_OFF + (g % STAGES) * L::TILE, BOX, 1024);
+      if (ks == kAllSteps) {
+        umma_ts_if(od, scol, vd, idesc_o, add, one);
 #pragma unroll
-          for (int i = 1; i < KT / 16; ++i)
-            umma_ts(od, pa0 + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, 1u);
-        } else {
-          const int s0 = ks & 15, s1 = ks >> 4;
-          for (int i = s0; i < s1; ++i)
-            umma_ts(od, pa0 + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o,
-                    (!first || i > s0) ? 1u : 0u);
+        for (int i = 1; i < KT / 16; ++i)
+          umma_ts_if(od, scol + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, 1u,
+                     one);
+      } else {
+        for (int i = ks & 15; i < (int)(ks >> 4); ++i, add = 1u)
+          umma_ts_if(od, scol + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, add,
+                     one);
+      }
+    };
+    // waits for K of tile g; the steps of it that this Q tile takes (0: none)
+    auto wait_k = [&](int g) -> unsigned {
+      wait(B_KFULL + g % STAGES, (g / STAGES) & 1);
+      return __shfl_sync(0xFFFFFFFFu, steps_of[g % STAGES], 0) >> (8 * t) & 0xFFu;
+    };
+    for (int n = 0; ok; ++n) {
+      const Item* slot = item_wait(n);
+      if (!__all_sync(0xFFFFFFFFu, slot != nullptr)) break;
+      const int hq = __shfl_sync(0xFFFFFFFFu, slot->hq, 0);
+      if (hq < 0) break;
+      const int nkv = __shfl_sync(0xFFFFFFFFu, slot->u.count(), 0);
+      if (lane == 0) item_done(n);
+      if (nkv == 0) continue;
+      wait(B_QFULL, qn & 1);
+      unsigned cur = wait_k(kvg);
+      if (!ok) break;
+      tc_fence_after();
+      ++qn;
+      uint32_t add = 0;                                // there is a P V product of this item
+      if (cur) issue_s(kvg, cur);
+      commit(B_KFREE + kvg % STAGES);                  // K of the tile read by the product above
+      if (nkv == 1) commit(B_QFREE);                   // every S product of the item issued
+      for (int j = 0; j < nkv; ++j) {
+        const int g = kvg + j;
+        const bool more = j + 1 < nkv;
+        // both tiles first: P is the last to come.  (V is waited for in any case: an issuer
+        // that ran ahead of the other would arrive twice in one phase of its free barrier.)
+        wait(B_VFULL + g % STAGES, (g / STAGES) & 1);
+        const unsigned next = more ? wait_k(g + 1) : 0u;
+        if (cur) {
+          // the first product of an item overwrites O_t: the output warps have read it
+          if (!add && uses > 0) wait(B_OFREE + t, (uses - 1) & 1);
+          wait(B_PFULL + t, pc & 1);
         }
-        umma_commit(bar(B_ODONE + t));
-      };
-      auto wait = [&](int b, int parity) {
-        if (!bwait(bar(b), (uint32_t)parity, abort_flag)) ok = false;
-      };
-      // waits for K of tile g; the steps of it that this Q tile takes (0: none)
-      auto wait_k = [&](int g) -> unsigned {
-        wait(B_KFULL + g % STAGES, (g / STAGES) & 1);
-        return steps_of[g % STAGES] >> (8 * t) & 0xFFu;
-      };
-      for (int n = 0; ok; ++n) {
-        const Item* slot = item_wait(n);
-        if (!slot || slot->hq < 0) break;
-        const int nkv = slot->u.count();
-        item_done(n);
-        if (nkv == 0) continue;
-        wait(B_QFULL, qn & 1);
-        unsigned cur = wait_k(kvg);
         if (!ok) break;
         tc_fence_after();
-        ++qn;
-        bool begun = false;                            // there is a P V product of this item
-        if (cur) issue_s(kvg, cur);
-        umma_commit(bar(B_KFREE + kvg % STAGES));      // K of the tile read by the product above
-        if (nkv == 1) umma_commit(bar(B_QFREE));       // every S product of the item issued
-        for (int j = 0; j < nkv; ++j) {
-          const int g = kvg + j;
-          unsigned next = 0;
-          if (cur) {
-            wait(B_PFULL + t, pc & 1);
-            // the first product of an item overwrites O_t: the output warps have read it
-            if (!begun && uses > 0) wait(B_OFREE + t, (uses - 1) & 1);
-          }
-          // waited for in any case: an issuer that ran ahead of the other would arrive twice in one
-          // phase of V's free barrier
-          wait(B_VFULL + g % STAGES, (g / STAGES) & 1);
-          if (!ok) break;
-          if (cur) {
-            tc_fence_after();
-            issue_pv(g, cur, !begun);
-            if (!begun) ++uses;
-            begun = true;
-            ++pc;
-          }
-          umma_commit(bar(B_VFREE + g % STAGES));      // V of tile g read by the product above
-          if (j + 1 < nkv) {
-            // S_t of the next key tile: its columns hold no P that is still to be read (this Q
-            // tile's earlier products were issued before)
-            next = wait_k(g + 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (next) issue_s(g + 1, next);
-            umma_commit(bar(B_KFREE + (g + 1) % STAGES));
-            if (j + 2 == nkv) umma_commit(bar(B_QFREE));    // the item's last S product
-          }
-          cur = next;
+        if (cur) {
+          issue_pv(g, cur, add);
+          if (!add) ++uses;
+          add = 1;
+          ++pc;
         }
-        kvg += nkv;
+        // S_t of the next key tile: its columns hold no P that is still to be read (this Q
+        // tile's earlier products were issued before)
+        if (next) issue_s(g + 1, next);
+        commit(B_VFREE + g % STAGES);                  // V of tile g read by the product above
+        if (more) {
+          commit(B_KFREE + (g + 1) % STAGES);
+          if (j + 2 == nkv) commit(B_QFREE);           // the item's last S product
+        }
+        cur = next;
       }
-      // the CTA frees TMEM only after every MMA issued here has completed
-      umma_commit(bar(B_DRAIN + t));
-      drain_wait(bar(B_DRAIN + t), 0u);
+      if (!ok) break;
+      if (add) commit(B_ODONE + t);                    // the item's P V products
+      kvg += nkv;
     }
+    // the CTA frees TMEM only after every MMA issued here has completed
+    commit(B_DRAIN + t);
+    if (one) drain_wait(bar(B_DRAIN + t), 0u);
+    __syncwarp();
   } else if (warp >= W_SM && warp < W_OUT) {
     // ------------------------------------------------------------ softmax of one Q tile's rows
     const int t = (warp - W_SM) >> 2;
@@ -629,17 +626,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
         if (__any_sync(0xFFFFFFFFu, mx > m_ref + 8.0f)) {
           // move the reference maximum of every row of the warp to max(m_ref, mx): O and l
-          // scale by 2^(m_ref - m_new) (1 for rows whose maximum did not grow); O holds P V of
-          // the item's earlier tiles once their MMAs are done
+          // scale by 2^(m_ref - m_new) (1 for rows whose maximum did not grow).  O holds P V of the
+          // item's earlier tiles: those MMAs were issued, and so are done, before this S
           const float m_new = fmaxf(m_ref, mx);
           const float alpha = (m_ref == -INFINITY) ? 0.0f : ex2(m_ref - m_new);
           if (j > 0) {
-            const bool done = bwait(bar(B_ODONE + t), (uint32_t)((sc - 1) & 1), abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, done)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
 #pragma unroll 1
             for (int c16 = 0; c16 < D / 16; ++c16) {
               uint32_t wv[16];
@@ -727,7 +718,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int m = 32 * quarter + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16);
     const bool leader = (warp == W_OUT) && lane == 0;  // issues the stores
-    int cum[2] = {0, 0}, uses[2] = {0, 0}, nbox = 0;   // P V products, items, boxes stored
+    int uses[2] = {0, 0}, nbox = 0;                    // items per Q tile, boxes stored
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const Item* it = item_wait(n);
@@ -743,10 +734,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
               reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
           continue;
         }
-        cum[t] += nt;
-        // the row sums, then the item's last P V product into O_t
+        // the row sums, then the item's P V products into O_t
         bool got = bwait(bar(B_LFULL + t), (uint32_t)(uses[t] & 1), abort_flag);
-        got = got && bwait(bar(B_ODONE + t), (uint32_t)((cum[t] - 1) & 1), abort_flag);
+        got = got && bwait(bar(B_ODONE + t), (uint32_t)(uses[t] & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
           break;
