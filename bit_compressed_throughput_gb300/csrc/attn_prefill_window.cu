@@ -72,6 +72,7 @@ static_assert(kMaxSeqs <= THREADS, "one thread per sequence reads its offsets");
 
 constexpr int ITEMS = 4;                    // ring of work items
 constexpr unsigned kAllSteps = (KT / 16) << 4;   // every 16-key step of a tile (s0 | s1 << 4)
+constexpr unsigned kLastTile = 8u;               // the Q tile's last key tile (s0 < 8)
 
 struct Seq {
   int q0, nq, k0, nk;                       // first query row, rows, first K/V row, rows
@@ -93,11 +94,11 @@ struct PSmem {
 };
 static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 
-// barriers: q_full, q_free, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
-// l_full[2], o_staged, o_stage_free, drain, item_full[4], item_free[4]
-constexpr int B_QFULL = 0, B_QFREE = 1, B_KFULL = 2, B_KFREE = 4, B_VFULL = 6, B_VFREE = 8,
-              B_SFULL = 10, B_PFULL = 12, B_ODONE = 14, B_OFREE = 16, B_LFULL = 18, B_OSTAGED = 20,
-              B_OSFREE = 21, B_DRAIN = 22, B_IFULL = 24, B_IFREE = B_IFULL + ITEMS,
+// barriers: q_full[2], q_free[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
+// l_full[2], o_staged, o_stage_free, drain[2], item_full[4], item_free[4]
+constexpr int B_QFULL = 0, B_QFREE = 2, B_KFULL = 4, B_KFREE = 6, B_VFULL = 8, B_VFREE = 10,
+              B_SFULL = 12, B_PFULL = 14, B_ODONE = 16, B_OFREE = 18, B_LFULL = 20, B_OSTAGED = 22,
+              B_OSFREE = 23, B_DRAIN = 24, B_IFULL = 26, B_IFREE = B_IFULL + ITEMS,
               NBARS = B_IFREE + ITEMS;
 static_assert(NBARS * 8 + 12 + STAGES * 4 <= 512, "barrier space");
 
@@ -279,15 +280,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   const PrefillWindow& w = pa.w;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_QFULL), 1);
-    mbar_init(bar(B_QFREE), 2);                        // one arrival per MMA issuer
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(bar(B_KFULL + i), 1);
       mbar_init(bar(B_VFULL + i), 1);
-      mbar_init(bar(B_KFREE + i), 2);
+      mbar_init(bar(B_KFREE + i), 2);                  // one arrival per MMA issuer
       mbar_init(bar(B_VFREE + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(B_QFULL + t), 1);
+      mbar_init(bar(B_QFREE + t), 1);
       mbar_init(bar(B_SFULL + t), 1);
       mbar_init(bar(B_PFULL + t), 4);                  // one arrival per softmax warp
       mbar_init(bar(B_ODONE + t), 1);
@@ -358,6 +359,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     // ------------------------------------------------------------ items and TMA producer
     if (lane == 0) {
       int kvg = 0, qn = 0, kn = 0, vn = 0;             // key tiles, Q pairs, K and V tiles issued
+      int qt[2] = {0, 0};                              // Q tiles A and B issued
       bool ok = true;
       Cursor cur = first_item(seqs, nseq);
       bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
@@ -390,12 +392,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                           bar(full + st));
             return true;
           };
-          // the 16-key steps that the Q tiles take of the tile, a byte each (s0 | s1 << 4; 0: none)
+          // the 16-key steps that the Q tiles take of the tile, a byte each: s0 | s1 << 4 (s1 0:
+          // none), and kLastTile when they take none of a later one
           auto steps = [&](int t) -> unsigned {
-            if (!it.t[t].has(it.u.tile(j))) return 0u;
-            const KeySteps k = key_steps(it.u.tile(j), it.pos + t * QT,
-                                         it.pos + min(t * QT + QT, it.rows) - 1, w.window, w.sinks);
-            return (unsigned)(k.s0 | k.s1 << 4);
+            const int tile = it.u.tile(j), lo = it.pos + t * QT;
+            const unsigned last = (it.t[t].count() == 0 || tile >= it.t[t].te - 1) ? kLastTile : 0u;
+            if (!it.t[t].has(tile)) return last;
+            const KeySteps k = key_steps(tile, lo, it.pos + min(t * QT + QT, it.rows) - 1, w.window,
+                                         w.sinks);
+            return (unsigned)(k.s0 | k.s1 << 4) | last;
           };
           const unsigned both = steps(0) | steps(1) << 8;
           if (!load(&tmK, L::K_OFF, B_KFULL, B_KFREE, both)) {
@@ -404,16 +409,19 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           kn = kvg + 1;
           if (j == 0) {
-            // Q, when the previous item's S products are done with it
-            if (qn > 0 && !bwait(bar(B_QFREE), (uint32_t)((qn - 1) & 1), abort_flag)) {
-              ok = false;
-              break;
-            }
-            mbar_expect_tx(bar(B_QFULL), (uint32_t)(2 * L::TILE));
-            for (int t = 0; t < 2; ++t)
+            // each Q tile, when its last S product of the previous item is done with it
+            for (int t = 0; t < 2 && ok; ++t) {
+              if (qn > 0 && !bwait(bar(B_QFREE + t), (uint32_t)((qn - 1) & 1), abort_flag)) {
+                ok = false;
+                break;
+              }
+              mbar_expect_tx(bar(B_QFULL + t), (uint32_t)L::TILE);
               for (int c = 0; c < NB; ++c)
                 tma_load_2d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ,
-                            it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL));
+                            it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL + t));
+              qt[t] = qn + 1;
+            }
+            if (!ok) break;
             ++qn;
           }
           if (!load(&tmV, L::V_OFF, B_VFULL, B_VFREE, 0u)) {
@@ -424,7 +432,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
       }
       // every issued copy has landed before the CTA exits
-      if (qn > 0) drain_wait(bar(B_QFULL), (uint32_t)((qn - 1) & 1));
+      for (int t = 0; t < 2; ++t)
+        if (qt[t] > 0) drain_wait(bar(B_QFULL + t), (uint32_t)((qt[t] - 1) & 1));
       for (int i = max(0, kn - STAGES); i < kn; ++i)
         drain_wait(bar(B_KFULL + i % STAGES), (uint32_t)((i / STAGES) & 1));
       for (int i = max(0, vn - STAGES); i < vn; ++i)
@@ -455,7 +464,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     // S_t = Q_t K^T of the key steps `ks` of K/V tile g over K = D: k-step i reads 16 columns,
     // 32 bytes into box i / 4; 16 keys are 2048 bytes of each box
     auto issue_s = [&](int g, unsigned ks) {
-      const int s0 = ks & 15, s1 = ks >> 4;
+      const int s0 = ks & 7, s1 = ks >> 4;
       const uint64_t kd = smem_desc(sbase + L::K_OFF + (g % STAGES) * L::TILE, 16, 1024) +
                           (uint64_t)(s0 * 128);
       const uint32_t idesc = idesc_qk(16 * (s1 - s0)), col = scol + 16 * s0;
@@ -471,19 +480,19 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     // per step in its MN-major 128B-swizzled layout)
     auto issue_pv = [&](int g, unsigned ks, uint32_t add) {
       const uint64_t vd = smem_desc(sbase + L::V_OFF + (g % STAGES) * L::TILE, BOX, 1024);
-      if (ks == kAllSteps) {
+      if ((ks & ~kLastTile) == kAllSteps) {
         umma_ts_if(od, scol, vd, idesc_o, add, one);
 #pragma unroll
         for (int i = 1; i < KT / 16; ++i)
           umma_ts_if(od, scol + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, 1u,
                      one);
       } else {
-        for (int i = ks & 15; i < (int)(ks >> 4); ++i, add = 1u)
+        for (int i = ks & 7; i < (int)(ks >> 4); ++i, add = 1u)
           umma_ts_if(od, scol + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, add,
                      one);
       }
     };
-    // waits for K of tile g; the steps of it that this Q tile takes (0: none)
+    // waits for K of tile g; the steps of it that this Q tile takes
     auto wait_k = [&](int g) -> unsigned {
       wait(B_KFULL + g % STAGES, (g / STAGES) & 1);
       return __shfl_sync(0xFFFFFFFFu, steps_of[g % STAGES], 0) >> (8 * t) & 0xFFu;
@@ -496,15 +505,22 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int nkv = __shfl_sync(0xFFFFFFFFu, slot->u.count(), 0);
       if (lane == 0) item_done(n);
       if (nkv == 0) continue;
-      wait(B_QFULL, qn & 1);
+      wait(B_QFULL + t, qn & 1);
       unsigned cur = wait_k(kvg);
       if (!ok) break;
       tc_fence_after();
       ++qn;
       uint32_t add = 0;                                // there is a P V product of this item
-      if (cur) issue_s(kvg, cur);
-      commit(B_KFREE + kvg % STAGES);                  // K of the tile read by the product above
-      if (nkv == 1) commit(B_QFREE);                   // every S product of the item issued
+      bool q_free = false;                             // every S product of the item issued
+      auto after_s = [&](int g, unsigned ks) {
+        commit(B_KFREE + g % STAGES);                  // K of the tile read by the product before
+        if ((ks & kLastTile) && !q_free) {
+          commit(B_QFREE + t);
+          q_free = true;
+        }
+      };
+      if (cur & ~kLastTile) issue_s(kvg, cur);
+      after_s(kvg, cur);
       for (int j = 0; j < nkv; ++j) {
         const int g = kvg + j;
         const bool more = j + 1 < nkv;
@@ -512,14 +528,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         // that ran ahead of the other would arrive twice in one phase of its free barrier.)
         wait(B_VFULL + g % STAGES, (g / STAGES) & 1);
         const unsigned next = more ? wait_k(g + 1) : 0u;
-        if (cur) {
+        const bool pv = cur & ~kLastTile;
+        if (pv) {
           // the first product of an item overwrites O_t: the output warps have read it
           if (!add && uses > 0) wait(B_OFREE + t, (uses - 1) & 1);
           wait(B_PFULL + t, pc & 1);
         }
         if (!ok) break;
         tc_fence_after();
-        if (cur) {
+        if (pv) {
           issue_pv(g, cur, add);
           if (!add) ++uses;
           add = 1;
@@ -527,12 +544,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         // S_t of the next key tile: its columns hold no P that is still to be read (this Q
         // tile's earlier products were issued before)
-        if (next) issue_s(g + 1, next);
+        if (next & ~kLastTile) issue_s(g + 1, next);
         commit(B_VFREE + g % STAGES);                  // V of tile g read by the product above
-        if (more) {
-          commit(B_KFREE + (g + 1) % STAGES);
-          if (j + 2 == nkv) commit(B_QFREE);           // the item's last S product
-        }
+        if (more) after_s(g + 1, next);
         cur = next;
       }
       if (!ok) break;
