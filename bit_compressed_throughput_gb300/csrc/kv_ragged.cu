@@ -60,8 +60,14 @@ __device__ __forceinline__ void tile_slots(const RaggedArgs& a, int r0, int64_t*
     const int row = r0 + threadIdx.x;
     // the warp's first row gives the sequence of most of its rows; the others search from there
     int b = warp_sequence_of_row(a.row_off, a.B, row - lane, lane);
-    if (b < 0 || row >= a.row_off[b + 1])
-      b = row < a.rows ? sequence_of_row(a.row_off, a.B, row) : -1;
+    if (b < 0 || row >= a.row_off[b + 1]) {
+      // one row a sequence (single tokens) puts this row `lane` sequences on
+      const int c = b < 0 ? -1 : min(b + lane, a.B - 1);
+      if (c >= 0 && a.row_off[c] <= row && row < a.row_off[c + 1])
+        b = c;
+      else
+        b = row < a.rows ? sequence_of_row(a.row_off, a.B, row) : -1;
+    }
     int64_t slot = -1;
     if (b >= 0 && row < a.rows) {
       const int64_t t = (int64_t)row - a.row_off[b];
@@ -194,15 +200,13 @@ append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
   const int lane = threadIdx.x & 31, r = threadIdx.x / LPR, c = threadIdx.x % LPR;
   const unsigned tile = blockIdx.x / a.hblocks;
   const int64_t r0 = (int64_t)tile * ROWS;
-  tile_slots<ROWS>(a, (int)r0, slots);
-  const int64_t slot0 = slots[r];
-  const bool live = slot0 >= 0;
   const int h0 = (int)(blockIdx.x - tile * a.hblocks) * a.heads, h1 = min(a.H, h0 + a.heads);
-  const int64_t at = live ? (r0 + r) * a.stride + c * 16 : 0;
+  const bool held = r0 + r < a.rows;
+  const int64_t at = held ? (r0 + r) * a.stride + c * 16 : 0;
   const uint16_t *ks = k_new + at, *vs = v_new + at;
   uint4 x[4];
   auto load = [&](int head) {
-    if (live) {
+    if (held) {
       x[0] = ldg_nc_v4(ks + head * D);
       x[1] = ldg_nc_v4(ks + head * D + 8);
       x[2] = ldg_nc_v4(vs + head * D);
@@ -211,7 +215,10 @@ append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
-  load(h0);
+  load(h0);                                // in flight while the rows' sequences are looked up
+  tile_slots<ROWS>(a, (int)r0, slots);
+  const int64_t slot0 = slots[r];
+  const bool live = slot0 >= 0;
   for (int head = h0; head < h1; ++head) {
     const uint4 k0 = x[0], k1 = x[1], v0 = x[2], v1 = x[3];
     if (head + 1 < h1) load(head + 1);

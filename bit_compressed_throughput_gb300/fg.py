@@ -318,16 +318,17 @@ def fg_prefill_attn(qkv, nseq: int, s: int, H: int, d: int, scale: float, out, s
 def _rows(name: str, t, width: int):
     """(rows, row stride) of a 2-D fp16 tensor of rows of `width` contiguous values."""
     import torch
-    if t.dim() != 2 or t.dtype != torch.float16 or t.shape[1] != width or t.stride(1) != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width or stride[1] != 1 or t.dtype is not torch.float16:
         raise ValueError(f"{name}: fp16 [rows][{width}] with contiguous rows expected, got "
-                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+                         f"{t.dtype} {tuple(shape)} with strides {stride}")
     # the stride of a dimension of one row (or none) is arbitrary and never used
-    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else (width + 7) // 8 * 8)
+    return shape[0], (stride[0] if shape[0] > 1 else (width + 7) // 8 * 8)
 
 
 def _extents(name: str, t, n: int):
     import torch
-    if t.dim() != 1 or t.dtype != torch.int32 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 [{n}] expected, got {t.dtype} "
                          f"{tuple(t.shape)}")
 

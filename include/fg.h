@@ -191,7 +191,7 @@ int fg_kv_append_q4(const uint16_t* k_new, const uint16_t* v_new, int64_t row_st
  * elements apart: >= h, a multiple of 8) are quantised into positions pos[b], pos[b]+1, .. of
  * sequence b, with the codes and statistics fg_kv_append_q4 gives for those rows; everything
  * else in the cache stays as it was.  `rows`: the rows k_new and v_new hold (< 2^31 - 64); rows
- * before row_off[0] or from row_off[B] on are not read.  row_off: device int32 [B+1], 0 <= row_off[b]
+ * before row_off[0] or from row_off[B] on are not used.  row_off: device int32 [B+1], 0 <= row_off[b]
  * <= row_off[b+1] <= rows; pos: device int32 [B], 0 <= pos[b], pos[b] + (rows of b) <= cap.  The
  * host never reads the two arrays, so their values are checked on the device: a row that does
  * not fit is not written, and fg_check_device_error() returns FG_ERR_CAPACITY.
