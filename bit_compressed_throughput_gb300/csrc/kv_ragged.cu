@@ -130,30 +130,56 @@ __device__ __noinline__ uint2 quantize16_exact(uint4 v0, uint4 v1, unsigned grou
 // move it by at most 15 * 3 * 2^-24 = 0.18.  So the code is the defined one unless y lies within
 // 1.42 units of a half-integer, when the fraction is 2 +- 1.42: below 4.  `frac` gathers the smallest
 // fraction (16-bit lanes).
+__device__ __forceinline__ void fixed2(uint32_t w, uint64_t c2, uint64_t k2, uint32_t (&t)[2]) {
+  const float2 x = unpack_h2(w);
+  float lo, hi;
+  q4_unpack2(q4_fma2(q4_pack2(x.x, x.y), c2, k2), lo, hi);
+  t[0] = __float_as_uint(lo);
+  t[1] = __float_as_uint(hi);
+}
 __device__ __forceinline__ uint32_t codes8_fixed(const uint32_t (&w)[4], uint64_t c2, uint64_t k2,
                                                  uint32_t& frac) {
-  uint32_t t[8];
+  uint32_t t[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = unpack_h2(w[i]);
-    float lo, hi;
-    q4_unpack2(q4_fma2(q4_pack2(x.x, x.y), c2, k2), lo, hi);
-    t[2 * i] = __float_as_uint(lo);
-    t[2 * i + 1] = __float_as_uint(hi);
-    frac = __vminu2(frac, __byte_perm(t[2 * i], t[2 * i + 1], 0x5410));
+    fixed2(w[i], c2, k2, t[i]);
+    frac = __vminu2(frac, __byte_perm(t[i][0], t[i][1], 0x5410));
   }
-  const uint32_t ev = __byte_perm(__byte_perm(t[0], t[2], 0x0062), __byte_perm(t[4], t[6], 0x0062),
-                                  0x5410);
-  const uint32_t od = __byte_perm(__byte_perm(t[1], t[3], 0x0062), __byte_perm(t[5], t[7], 0x0062),
-                                  0x5410);
+  const uint32_t ev = __byte_perm(__byte_perm(t[0][0], t[1][0], 0x0062),
+                                  __byte_perm(t[2][0], t[3][0], 0x0062), 0x5410);
+  const uint32_t od = __byte_perm(__byte_perm(t[0][1], t[1][1], 0x0062),
+                                  __byte_perm(t[2][1], t[3][1], 0x0062), 0x5410);
   return (ev & 0x0F0F0F0Fu) | ((od & 0x0F0F0F0Fu) << 4);
+}
+// The codes of 8 values with those near a half-integer taken by the division (a called function, out of
+// the way of the code that calls it rarely).
+__device__ __noinline__ uint32_t codes8_near(uint4 v, float c15, float K, float2 ab,
+                                             uint32_t codes) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint64_t c2 = q4_pack2(c15, c15), k2 = q4_pack2(K, K);
+  const float width = __fsub_rn(ab.y, ab.x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t t[2];
+    fixed2(w[i], c2, k2, t);
+    const bool near0 = (t[0] & 0xFFFFu) < 4u, near1 = (t[1] & 0xFFFFu) < 4u;
+    if (near0 || near1) {
+      const float2 x = unpack_h2(w[i]);
+      const int at = near0 ? 8 * i : 8 * i + 4;
+      codes = (codes & ~(0xFu << at)) | (q4_code(near0 ? x.x : x.y, ab.x, width) << at);
+      if (near0 && near1)
+        codes = (codes & ~(0xF0u << at)) | (q4_code(x.y, ab.x, width) << (at + 4));
+    }
+  }
+  return codes;
 }
 
 // Quantises the 16 values of this lane (4 lanes per group of 64): codes, and the group's (a, b).
-// The fast path takes minimum and maximum as fp16 pairs and the codes in fixed point; a group with
-// a NaN, an infinity, a zero at either end (their order is by sign), a constant one, one whose K leaves
-// [128, 256) (its offset is more than four times its width) or with a code near a tie goes the
-// exact way (about 1 warp in 8 on normal data, for exact ties of fp16 values).
+// The fast path takes minimum and maximum as fp16 pairs and the codes in fixed point.  A group with
+// a NaN, an infinity, a zero at either end (their order is by sign), a constant one, or one whose K
+// leaves [128, 256) (its offset is more than four times its width) goes the exact way as a whole;
+// codes near a tie do so alone (1 value in 4000 of normal data, exact ties of fp16 values; a lane of
+// 1 warp in 8 has one).
 __device__ __forceinline__ uint2 quantize16(const uint4 v0, const uint4 v1, int lane,
                                             uint32_t* ab_out) {
   const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
@@ -177,13 +203,17 @@ __device__ __forceinline__ uint2 quantize16(const uint4 v0, const uint4 v1, int 
   codes.x = codes8_fixed(w0, c2, k2, frac);
   codes.y = codes8_fixed(w1, c2, k2, frac);
   // every comparison is false for NaN; c15 is 0 where b - a is infinite
-  const bool fast = K >= 128.0f && K < 256.0f && c15 > 0.0f && c15 < INFINITY && ab.x != 0.0f && ab.y != 0.0f &&
-                    min(frac & 0xFFFFu, frac >> 16) >= 4u;
+  const bool plain = K >= 128.0f && K < 256.0f && c15 > 0.0f && c15 < INFINITY && ab.x != 0.0f &&
+                     ab.y != 0.0f;
+  const bool near = min(frac & 0xFFFFu, frac >> 16) < 4u;
   *ab_out = abw;
-  const unsigned slow = __ballot_sync(0xFFFFFFFFu, !fast);
-  if (slow) {
-    const int g = lane & ~3;
-    if ((slow >> g) & 0xFu) codes = quantize16_exact(v0, v1, 0xFu << g, ab_out);
+  if (__any_sync(0xFFFFFFFFu, !plain || near)) {
+    if (!plain) {                          // the group's lanes agree
+      codes = quantize16_exact(v0, v1, 0xFu << (lane & ~3), ab_out);
+    } else if (near) {
+      codes.x = codes8_near(v0, c15, K, ab, codes.x);
+      codes.y = codes8_near(v1, c15, K, ab, codes.y);
+    }
   }
   return codes;
 }
@@ -239,18 +269,40 @@ append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
 
 // ---------------------------------------------------------------------------- read-back
 
-// The 8 values of a code word: each code to binary32 exactly (its bits under the exponent of
-// 2^23, less 2^23), then the format's product, sum and rounding to fp16.
+// w / 15 rounded once (w finite and normal): the product with the rounded reciprocal, corrected by
+// its remainder, which is exact (Markstein, 1990).  It equals the quotient for each of the 2^23
+// mantissas of w (scaling by powers of two changes nothing).
+__device__ __forceinline__ float div15(float w) {
+  const float r = 1.0f / 15.0f, q = __fmul_rn(w, r);
+  return __fmaf_rn(__fmaf_rn(-15.0f, q, w), r, q);
+}
+// The same values by the format's operations one by one (infinite or NaN statistics).
+__device__ __noinline__ uint4 restore8_exact(uint32_t codes, float af, float s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_h2(__fadd_rn(af, __fmul_rn((float)((codes >> (8 * i)) & 0xFu), s)),
+                   __fadd_rn(af, __fmul_rn((float)((codes >> (8 * i + 4)) & 0xFu), s)));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// The 8 values fp16(a + fl(q s)), s = fl((b - a) / 15), of a code word.  A code's bits under the
+// exponent of 2^23 are the binary32 number 2^23 + q, and (2^23 + q) s - 2^23 s = q s exactly, so one
+// fused multiply-add with the exact -2^23 s gives fl(q s); two values per instruction.
 __device__ __forceinline__ uint4 restore8(uint32_t codes, uint32_t abw) {
   const float2 ab = unpack_h2(abw);
-  const float s = __fdiv_rn(__fsub_rn(ab.y, ab.x), 15.0f);
+  const float s = div15(__fsub_rn(ab.y, ab.x)), c = -8388608.0f * s;
+  if (!(s < INFINITY))                     // fp16 infinities or NaN
+    return restore8_exact(codes, ab.x, __fdiv_rn(__fsub_rn(ab.y, ab.x), 15.0f));
   const uint32_t ev = codes & 0x0F0F0F0Fu, od = (codes >> 4) & 0x0F0F0F0Fu;
+  const uint64_t a2 = q4_pack2(ab.x, ab.x), s2 = q4_pack2(s, s), c2 = q4_pack2(c, c);
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(__byte_perm(ev, 0x4B000000u, 0x7440 + i)) - 8388608.0f;
-    const float hi = __uint_as_float(__byte_perm(od, 0x4B000000u, 0x7440 + i)) - 8388608.0f;
-    o[i] = pack_h2(__fadd_rn(ab.x, __fmul_rn(lo, s)), __fadd_rn(ab.x, __fmul_rn(hi, s)));
+    const float lo = __uint_as_float(__byte_perm(ev, 0x4B000000u, 0x7440 + i));
+    const float hi = __uint_as_float(__byte_perm(od, 0x4B000000u, 0x7440 + i));
+    float x, y;
+    q4_unpack2(q4_add2(a2, q4_fma2(q4_pack2(lo, hi), s2, c2)), x, y);
+    o[i] = pack_h2(x, y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
