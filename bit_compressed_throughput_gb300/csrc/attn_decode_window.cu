@@ -53,7 +53,8 @@ using q4attn::movtrans;
 
 constexpr int kSub = 2;                   // tiles per ring slot
 constexpr int kSlotPos = kSub * kTilePos;
-constexpr int kMinTiles = 4;              // per warp of a small call: two slots
+constexpr int kMinTiles = 2;              // per warp of a small call: one slot (32 heads x 260
+                                          // positions: 7.8 us; with 4 9.3, with 6 8.8)
 constexpr long long kWaitCycles = 1ll << 32;
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 
@@ -615,10 +616,23 @@ merge_kernel(const Args a) {
   float M = -INFINITY, L = 0.0f, o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.0f;
+  // 8 pieces' channels at a time, the first 8 in flight before their weights are known
+  constexpr int BATCH = 8;
+  float v[BATCH][C];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (i0 + i < cut.pieces) {
+        const float* pp = piece(i0 + i);
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[i][c] = pp[c * 32 + lane];
+      }
+  };
   for (int i0 = 0; i0 < cut.pieces; i0 += 32) {
     const int n = min(32, cut.pieces - i0);
     float2 ml = make_float2(-INFINITY, 0.0f);
     if (lane < n) ml = *reinterpret_cast<const float2*>(piece(i0 + lane) + D);
+    load(i0);
     float mx = ml.x;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
@@ -631,12 +645,16 @@ merge_kernel(const Args a) {
     L = fmaf(L, corr, l);
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] *= corr;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float* pp = piece(i0 + i);
-      const float wi = __shfl_sync(0xFFFFFFFFu, wgt, i);
+    for (int j = 0; j < n; j += BATCH) {
+      if (j > 0) load(i0 + j);
 #pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = fmaf(wi, pp[c * 32 + lane], o[c]);
+      for (int i = 0; i < BATCH; ++i) {
+        const float wi = __shfl_sync(0xFFFFFFFFu, wgt, j + i);
+        if (j + i < n) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) o[c] = fmaf(wi, v[i][c], o[c]);
+        }
+      }
     }
     M = mx;
   }
@@ -687,6 +705,10 @@ cudaError_t launch_d(const Args& a, const fg_kvcache& kv, int ctas, cudaStream_t
 }
 
 int warps_of(int d) { return d == 128 ? Ring<128>::WARPS : Ring<64>::WARPS; }
+// Shares that a call of at most `most` tiles can have.
+int64_t most_cuts(int64_t most, int nsm, int d) {
+  return std::min<int64_t>(most / kMinTiles + 1, (int64_t)grid_ctas(most, nsm) * warps_of(d));
+}
 // Query heads of a row set: 1, 2 or 4.
 int set_heads(int G) { return G < 3 ? G : 4; }
 
@@ -694,8 +716,7 @@ int set_heads(int G) { return G < 3 ? G : 4; }
 
 size_t decode_attn_window_ws_bytes(const fg_kvcache& kv, int32_t Hq) {
   const int G = Hq / kv.H, heads = set_heads(G);
-  const int64_t n = (int64_t)grid_ctas(most_tiles(kv, (G + heads - 1) / heads, 0, 0), kMaxSms) *
-                    warps_of(kv.h / kv.H);
+  const int64_t n = most_cuts(most_tiles(kv, (G + heads - 1) / heads, 0, 0), kMaxSms, kv.h / kv.H);
   return cut_bytes(n) + (size_t)n * 2 * heads * (kv.h / kv.H + 2) * sizeof(float);
 }
 
@@ -717,7 +738,7 @@ cudaError_t launch_decode_attn_window(const uint16_t* q, int64_t q_stride, int32
   a.scale_log2 = scale * 1.4426950408889634f;
   const int64_t most = std::min(most_tiles(kv, a.nhb, window, sinks), most_tiles(kv, a.nhb, 0, 0));
   const int ctas = grid_ctas(most, nsm);
-  a.ncuts = ctas * warps_of(kv.h / kv.H);
+  a.ncuts = (int)most_cuts(most, nsm, kv.h / kv.H);
   a.cuts = static_cast<Cut*>(ws);
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + cut_bytes(a.ncuts));
   const bool wide = kv.h / kv.H == 128;
