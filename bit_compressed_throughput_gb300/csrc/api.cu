@@ -732,7 +732,7 @@ int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,
       (d != 64 && d != 128))
     return FG_ERR_SHAPE;
   const int64_t wq = (int64_t)Hq * d, wk = (int64_t)Hkv * d;
-  if (wq > (1 << 30) || q_stride < wq || q_stride % 8 != 0 || out_stride < wq ||
+  if (Hq > 65536 || q_stride < wq || q_stride % 8 != 0 || out_stride < wq ||
       out_stride % 8 != 0 || kv_stride < wk || kv_stride % 8 != 0)
     return FG_ERR_SHAPE;
   if (nseq == 0 || q_rows == 0) return FG_OK;

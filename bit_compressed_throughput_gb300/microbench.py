@@ -8,6 +8,7 @@ tests check the results; this only times them).
     python -m bit_compressed_throughput_gb300.microbench gemm      # GEMMs, fused K/V append
     python -m bit_compressed_throughput_gb300.microbench attn      # dense and Top-K decode
     python -m bit_compressed_throughput_gb300.microbench prefill   # causal prefill attention
+    python -m bit_compressed_throughput_gb300.microbench window    # ragged cache, windowed attention
 """
 from __future__ import annotations
 
@@ -133,13 +134,60 @@ def prefill_cases(fg, torch):
         print(f"prefill {nseq}x{H}x{s:<5d} {us:9.1f} us  {fl / us / 1e6:7.1f} TFLOP/s", flush=True)
 
 
+def window_cases(fg, torch):
+    """The ragged cache calls and the windowed attention: sequences of different lengths, a sliding
+    window with 4 first positions, one and four query heads per K/V head."""
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    for B, Hq, H, d, n, window in ((64, 32, 32, 128, 1024, 512), (16, 32, 8, 128, 8192, 4096)):
+        lens = [n - (i * 37) % (n // 2) for i in range(B)]
+        off = [0]
+        for x in lens:
+            off.append(off[-1] + x)
+        rows, h = off[-1], H * d
+        cache = fg.KVCacheQ4(B, n, h, H)
+        kv = torch.randn((rows, 2 * h), device="cuda").half()
+        k, v = kv[:, :h], kv[:, h:]
+        offs, zero, ln = i32(off), i32([0] * B), i32(lens)
+        out = torch.empty((rows, 2 * h), dtype=torch.float16, device="cuda")
+        q = torch.randn((B, Hq * d), device="cuda").half()
+        o = torch.empty_like(q)
+        qp = torch.randn((rows, Hq * d), device="cuda").half()
+        op = torch.empty_like(qp)
+        ws = torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, Hq), dtype=torch.uint8,
+                         device="cuda")
+        scale = 1.0 / math.sqrt(d)
+        seen = sum(min(x, window + min(4, max(0, x - window))) for x in lens)
+        pairs = sum(min(i + 1, window + min(4, max(0, i + 1 - window))) for x in lens
+                    for i in range(x))
+        for name, fn, byts, flops in (
+                ("append", lambda: fg.fg_kv_append_q4_ragged(k, v, offs, zero, cache),
+                 2 * rows * h * 2.5625, 0),
+                ("read", lambda: fg.fg_kv_read_q4_ragged(cache, offs, zero, out[:, :h], out[:, h:]),
+                 2 * rows * h * 2.5625, 0),
+                ("decode", lambda: fg.fg_decode_attn_q4kv_window(q, Hq, cache, ln, scale, o, ws,
+                                                                 window=window, sinks=4),
+                 2 * seen * h * 0.5625 + 4.0 * B * Hq * d, 0),
+                ("prefill", lambda: fg.fg_prefill_attn_window(qp, offs, k, v, offs, Hq, H, scale, op,
+                                                              window=window, sinks=4),
+                 0, 4.0 * pairs * Hq * d)):
+            us = time_graph(fn)
+            fg.fg_check_device_error()
+            rate = (f"{flops / us / 1e6:7.1f} TFLOP/s" if flops else f"{byts / us / 1e3:7.1f} GB/s")
+            print(f"window {B}x{Hq}/{H}x{n:<5d} window {window:<5d} {name:8s} {us:9.1f} us  {rate}",
+                  flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("cases", nargs="*", help="gemm, attn, prefill (default: all)")
+    ap.add_argument("cases", nargs="*", help="gemm, attn, prefill, window (default: all)")
     a = ap.parse_args()
-    cases = a.cases or ["gemm", "attn", "prefill"]
+    run = {"gemm": gemm_cases, "attn": attn_cases, "prefill": prefill_cases,
+           "window": window_cases}
+    cases = a.cases or list(run)
     for c in cases:
-        if c not in ("gemm", "attn", "prefill"):
+        if c not in run:
             ap.error(f"unknown case {c!r}")
     import torch
     import __graft_entry__
@@ -147,7 +195,7 @@ def main():
     from bit_compressed_throughput_gb300 import fg
     time_graph.flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
     for c in cases:
-        {"gemm": gemm_cases, "attn": attn_cases, "prefill": prefill_cases}[c](fg, torch)
+        run[c](fg, torch)
 
 
 if __name__ == "__main__":

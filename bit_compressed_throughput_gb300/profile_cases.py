@@ -84,6 +84,38 @@ def prefill_case(nseq, s, H, d, reps):
     fg.fg_check_device_error()
 
 
+def window_case(op, B, Hq, H, d, lens, window, reps):
+    """One ragged cache call or windowed attention over B sequences of lengths between lens[0] and
+    lens[1], a window (0: none) and 4 first positions."""
+    import torch
+    from bit_compressed_throughput_gb300 import fg
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    n = [lens[0] + (lens[1] - lens[0]) * i // max(1, B - 1) for i in range(B)]
+    off = torch.tensor([0] + n, device="cuda").cumsum(0).int()
+    pos, ln = torch.zeros(B, dtype=torch.int32, device="cuda"), off[1:] - off[:-1]
+    rows, h, scale = sum(n), H * d, 1.0 / math.sqrt(d)
+    kv = torch.randn((rows, 2 * h), generator=g, device="cuda").half()
+    k, v = kv[:, :h], kv[:, h:]
+    cache = fg.KVCacheQ4(B, lens[1], h, H)
+    fg.fg_kv_append_q4_ragged(k, v, off, pos, cache)
+    q = torch.randn((B if op == "decode" else rows, Hq * d), generator=g, device="cuda").half()
+    out = torch.empty_like(q)
+    back = torch.empty_like(kv)
+    ws = torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, Hq), dtype=torch.uint8,
+                     device="cuda")
+    for _ in range(1 + reps):
+        if op == "append":
+            fg.fg_kv_append_q4_ragged(k, v, off, pos, cache)
+        elif op == "read":
+            fg.fg_kv_read_q4_ragged(cache, off, pos, back[:, :h], back[:, h:])
+        elif op == "decode":
+            fg.fg_decode_attn_q4kv_window(q, Hq, cache, ln, scale, out, ws, window=window, sinks=4)
+        else:
+            fg.fg_prefill_attn_window(q, off, k, v, off, Hq, H, scale, out, window=window, sinks=4)
+    fg.fg_check_device_error()
+
+
 def layer_prefill_case(h, H, f, g, s, reps):
     """One decoder layer's prefill over one GPU batch (g sequences of s tokens): the layer
     restores its weights to fp16 once, then runs LN, the four projections (the CTA-pair GEMM
@@ -139,6 +171,17 @@ CASES = {
     "prefill-attn-opt67b": lambda r: prefill_case(16, 512, 32, 128, r),
     # KV-workload prefill attention, a quarter of one GPU batch: 32 x 56 heads x 1024 (1.3 GB)
     "prefill-attn-kv-quarter": lambda r: prefill_case(32, 1024, 56, 128, r),
+    # ragged cache calls over 36 prompts of 400 .. 512 tokens, 96 heads (0.8 GB of fp16 K/V)
+    "kv-append-ragged": lambda r: window_case("append", 36, 96, 96, 128, (400, 512), 0, r),
+    "kv-read-ragged": lambda r: window_case("read", 36, 96, 96, 128, (400, 512), 0, r),
+    # windowed decode attention: 128 sequences x 56 heads of 512 .. 1055 positions, all visible
+    # (0.8 GB of cache), and 4 query heads per K/V head over long contexts
+    "decode-window-full": lambda r: window_case("decode", 128, 56, 56, 128, (512, 1055), 0, r),
+    "decode-window-grouped": lambda r: window_case("decode", 16, 32, 8, 128, (9000, 32760), 16384,
+                                                   r),
+    # windowed prefill attention: long documents with grouped heads, and prompts
+    "prefill-window-long": lambda r: window_case("prefill", 2, 32, 8, 128, (7001, 8191), 1024, r),
+    "prefill-window-prompts": lambda r: window_case("prefill", 16, 32, 32, 128, (300, 512), 0, r),
     # top-K on the full KV workload (launch lists only: 4.3 GB of cache)
     "decode-attn-topk-kv": lambda r: attn_case(512, 56, 128, 1056, r, topk=106),
 }

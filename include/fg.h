@@ -304,8 +304,8 @@ size_t fg_decode_attn_window_workspace_bytes(const fg_kvcache* kv, int32_t Hq);
  * elements apart (>= Hkv*d, a multiple of 8).  q_off, kv_off: device int32 [nseq+1], not
  * decreasing, within 0 .. q_rows and 0 .. kv_rows; checked on the device (the output of a sequence
  * that does not fit stays as it was, and fg_check_device_error() returns FG_ERR_CAPACITY).  Rows
- * of out outside every sequence stay as they were.  d in {64, 128}; Hq a multiple of Hkv; out
- * must not alias q, k or v.  Values of keys that a row does not see never reach it, not even
+ * of out outside every sequence stay as they were.  d in {64, 128}; Hq a multiple of Hkv, at most
+ * 65536; out must not overlap q, k or v.  Values of keys that a row does not see never reach it, not even
  * infinities and NaN.  nseq == 0 or q_rows == 0 is a no-op; with kv_rows == 0, k and v may be
  * NULL.  The pages' prompts have one length and no window; no counterpart. */
 int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,

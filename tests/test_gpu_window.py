@@ -348,6 +348,42 @@ def test_decode_window_repeats_bit_identical(fg):
         assert torch.equal(a, run_decode(fg, q, Hq, cache, lens, 0.09, 300, 4))
 
 
+@pytest.mark.parametrize("B", [384, 385, 1700])
+def test_decode_window_many_sequences(fg, B):
+    """More sequences than the threads of a CTA (which plans the work in rounds of them), most of
+    them short or empty, one long."""
+    d, cap = 128, 208
+    lens = [(i * 11) % 23 for i in range(B)]
+    lens[B - 2] = 207
+    cache, k, v, km, vm = fill_cache(fg, B, 1, d, cap, seed=17)
+    q16 = fg_synth.random_fp16((B, d), 4)
+    out = run_decode(fg, dev(q16), 1, cache, i32(lens), 0.1, 100, 3)
+    want = OW.decode(q16, k, v, lens, 1, 100, 3, np.float32(0.1), km, vm)
+    check_rows(out, dict(enumerate(want)), d, True, "many sequences")
+
+
+def test_append_many_sequences(fg):
+    """Sequences of none to two rows each: every lookup path of a row's sequence."""
+    B, H, d = 3000, 1, 64
+    rng = np.random.default_rng(8)
+    for lens in ([1] * B, rng.integers(0, 3, B).tolist(), [0] * (B - 1) + [70]):
+        pos = rng.integers(0, 10, B).tolist()
+        buf, t, cache, off, ps = ragged_case(fg, B, H, d, lens, pos, 80, 1, 2, seed=B)
+        fg.fg_kv_append_q4_ragged(t[:, :d], t[:, d:2 * d], off, ps, cache)
+        fg.fg_check_device_error()
+        q, a, b = OQ.quantize_g64(np.ascontiguousarray(buf[:, d:2 * d]))
+        codes, o = OQ.pack_nibbles(q), offsets(lens, 1)
+        want = np.full((B, 1, 80, d // 2), 0xA5, np.uint8)
+        for s in range(B):
+            want[s, 0, pos[s]:pos[s] + lens[s]] = codes[o[s]:o[s + 1]]
+        assert np.array_equal(host(cache.v_codes), want)
+        out = torch.full((t.shape[0], d), 7.0, dtype=torch.float16, device="cuda")
+        fg.fg_kv_read_q4_ragged(cache, off, ps, None, out)
+        want = np.full((t.shape[0], d), 7.0, np.float16)
+        want[1:o[-1]] = OQ.dequant_g64(q, a, b)[1:o[-1]]
+        assert np.array_equal(host(out), want)
+
+
 # ------------------------------------------------------------------------------- prefill
 
 
@@ -403,6 +439,36 @@ def test_prefill_window(fg, Hq, Hkv, d, nq, nk, window, sinks):
     rest = host(out)
     assert (rest[:, Hq * d:] == 7.0).all() and (rest[:3] == 7.0).all()
     assert (rest[qo[-1]:] == 7.0).all()                    # rows behind the last sequence
+
+
+def test_prefill_window_without_keys(fg):
+    """Sequences that hold no K/V row at all, and no K/V buffer: zeros."""
+    d, nq = 64, [3, 0, 140]
+    q16, _ = prefill_inputs(1, 1, d, nq, [0], seed=2)
+    none = torch.empty((0, d), dtype=torch.float16, device="cuda")
+    out = run_prefill(fg, dev(q16), i32(offsets(nq)), none, none, i32([0, 0, 0, 0]), 1, 1, 0.1, 8, 2)
+    fg.fg_check_device_error()
+    assert not host(out)[:, :d].any() and (host(out)[:, d:] == 7.0).all()
+
+
+def test_prefill_window_extreme_values(fg):
+    """Values at the end of fp16's range: the mean does not pass it by rounding."""
+    d, n = 128, 200
+    q16 = np.zeros((n, d), np.float16)
+    kv = dev(np.full((n, 2 * d), 65504.0, np.float16))
+    out = run_prefill(fg, dev(q16), i32([0, n]), kv[:, :d], kv[:, d:], i32([0, n]), 1, 1, 0.1, 0, 0)
+    assert np.abs(host(out)[:, :d].astype(np.float64) - 65504.0).max() <= 65504.0 * 2 * H16
+
+
+def test_prefill_window_repeats_bit_identical(fg):
+    Hq, Hkv, d, nq, past = 4, 2, 128, [300, 17, 260], 90
+    q16, kv16 = prefill_inputs(Hq, Hkv, d, nq, [n + past for n in nq], seed=40)
+    kv, w = dev(kv16), Hkv * d
+    args = (dev(q16), i32(offsets(nq)), kv[:, :w], kv[:, w:2 * w],
+            i32(offsets([n + past for n in nq])), Hq, Hkv, 0.09, 70, 5)
+    a = run_prefill(fg, *args)
+    for _ in range(5):
+        assert torch.equal(a, run_prefill(fg, *args))
 
 
 def test_prefill_window_large_scores(fg):

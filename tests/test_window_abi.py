@@ -87,6 +87,7 @@ def test_prefill_window_validation(fg):
 
     assert call(Hkv=3) == fg.FG_ERR_SHAPE and call(d=32) == fg.FG_ERR_SHAPE
     assert call(Hq=0) == fg.FG_ERR_SHAPE and call(Hkv=0) == fg.FG_ERR_SHAPE
+    assert call(Hq=1 << 17, Hkv=1 << 17, qs=1 << 23, os_=1 << 23, ks=1 << 23) == fg.FG_ERR_SHAPE
     assert call(nseq=-1) == fg.FG_ERR_SHAPE and call(qr=-1) == fg.FG_ERR_SHAPE
     assert call(kr=-1) == fg.FG_ERR_SHAPE
     assert call(qs=248) == fg.FG_ERR_SHAPE and call(ks=132) == fg.FG_ERR_SHAPE
