@@ -13,23 +13,29 @@
 // Columns: the 8 columns of a product are (part, query head, group) with NP parts of HEADS = 4 / NP
 // query heads of one K/V head (for d = 64 the second column of a group pair repeats the first), so
 // lane (gid, tig) ends up with scores of head tig % HEADS.  A slot of 32 positions has four
-// 8-row halves of tiles; part tig / HEADS takes 4 / NP of them, so the softmax and the statistics of
-// a position are computed once per head: with one head per K/V head (NP = 4) a lane has one
+// 8-row halves of tiles; part tig / HEADS takes 4 / NP of them, so the softmax and the statistics
+// of a position are computed once per head: with one head per K/V head (NP = 4) a lane has one
 // position of the slot, with four (NP = 1) all four of its rows.  The weights meet the values as a
-// B operand that is zero outside the part's columns, so the parts add up in separate columns, summed
-// at the end.  More than 4 heads per K/V head are further row sets over the same positions, adjacent
-// in the work order, which find them in L2.
+// B operand that is zero outside the part's columns, so the parts add up in separate columns,
+// summed at the end.  More than 4 heads per K/V head are further row sets over the same positions,
+// adjacent in the work order, which find them in L2.
 //
 // Work split: the visible 16-position tiles of all row sets (sequence, K/V head, HEADS query heads)
-// stand
-// in one order, cut into even chunks whatever the lengths (Chunks, ragged.cuh): one CTA of 16 warps
-// per SM, whose warps take the CTA's chunks.  A chunk crosses row sets; a row set that lies within
-// one chunk is finished there, one that is cut leaves softmax partials (m, l, unnormalised o), merged
-// by a second kernel in a fixed order.  So the scratch is two partials per chunk, whatever the call.
+// stand in one order, cut evenly among the warps of the grid (one CTA per SM), whatever the
+// lengths.  A warp's share crosses row sets; a row set that lies within one share is finished
+// there, one that is cut leaves softmax partials (m, l, unnormalised o), merged by a second kernel
+// in a fixed order.  So the scratch is two partials per warp, whatever the call, and results do not
+// depend on the order in which warps run.
 //
-// Memory pipeline, as in the dense decode attention: per warp a ring of slots (3 tiles of K and V
+// Memory pipeline, as in the dense decode attention: per warp a ring of slots (2 tiles of K and V
 // codes and statistics), filled by bulk async copies that run ahead across row sets.  Every wait is
 // bounded; on timeout the warp sets the device error word, drains its copies and stops.
+//
+// Measured (GB300, HBM copy 6.78 TB/s; bytes of the visible 4-bit K/V): 128 sequences x 56 heads of
+// 512 .. 1055 positions 132 us, 0.91 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
+// window of 1024, 52 us, 0.70 (248 MB: 9 us until the first slots are there and 5 us of uneven ends
+// beside 38 us of streaming, 5 us to merge); 4 heads per K/V head over 16 contexts of 9000 .. 32760
+// 57 us, 0.72.
 #include <math.h>
 
 #include <algorithm>
@@ -58,10 +64,11 @@ constexpr int kMinTiles = 2;              // per warp of a small call: one slot 
 constexpr long long kWaitCycles = 1ll << 32;
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 
-// One CTA per SM.  Its rings hold about 110 KB, what the memory system needs in flight (152 x 110 KB
-// = 17 MB, 2.4 us of its rate); with twice as much the SMs advance less evenly and the last ones
-// finish later (128 sequences of 784 positions, 56 heads: 173 us with 16 warps x 3 slots, 152 us with
-// 12 x 2; 64-channel heads, whose slots are half as large, 72 us with 16 x 3, 81 us with 12 x 2).
+// One CTA per SM.  Its rings hold about 110 KB, what the memory system needs in flight (152 x 110
+// KB = 17 MB, 2.4 us of its rate); with twice as much the SMs advance less evenly and the last ones
+// finish later (128 sequences of 784 positions, 56 heads: 173 us with 16 warps x 3 slots, 152 us
+// with 12 x 2; 64-channel heads, whose slots are half as large, 72 us with 16 x 3, 81 us with 12 x
+// 2).
 template <int D>
 struct Ring {
   static constexpr int WARPS = (D == 128) ? 12 : 16, DEPTH = (D == 128) ? 2 : 3;
@@ -167,9 +174,9 @@ __device__ __forceinline__ void next_row_set(Cursor& c, const Args& a, const fg_
   } while (c.s.nt == 0);
 }
 
-// The query heads of a row set as B fragments (column n = gid: head (gid / 2) % HEADS, group gid & 1;
-// indexes permuted as the lanes hold the codes), the group sums of head tig % HEADS, in the base-2
-// score scale.
+// The query heads of a row set as B fragments (column n = gid: head (gid / 2) % HEADS, group gid &
+// 1; indexes permuted as the lanes hold the codes), the group sums of head tig % HEADS, in the
+// base-2 score scale.
 template <int D>
 struct QFrag {
   uint32_t bq[2 * (D / 32)][2];
@@ -304,8 +311,8 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
   }
   __syncthreads();
 
-  // ---- issue: fills the ring kRing slots ahead of the computation, one run of positions (the first
-  // ones or the window of a row set) after the other
+  // ---- issue: fills the ring kRing slots ahead of the computation, one run of positions (the
+  // first ones or the window of a row set) after the other
   int ileft = 0, irun = 0, is = 0, issued = 0;         // tiles left, of them in the run; slot
   int64_t irow = 0;                        // the run's next position, as a row of the cache
   Cursor ic{};
@@ -370,7 +377,8 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
   if (has_share && lane == 0) a.cuts[w] = cut;
 
   // ---- sequences that see nothing, and cuts of warps without a share
-  for (int64_t b = (int64_t)blockIdx.x * kWarps + warp; b < kv.B; b += (int64_t)gridDim.x * kWarps) {
+  for (int64_t b = (int64_t)blockIdx.x * kWarps + warp; b < kv.B;
+       b += (int64_t)gridDim.x * kWarps) {
     const int len = a.lens[b];
     if (lane == 0 && (len < 0 || len > kv.cap)) atomicOr(&g_decode_window_error, kErrExtent);
     if (length_of(a, kv, (int)b) == 0)
@@ -478,8 +486,10 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         m_run = mx;
       }
       const float m_ref = (m_run == -INFINITY) ? 0.0f : m_run;
-      uint32_t wt[RPL];                     // weights p (b - a) / 15 of both groups, transposed:
-#pragma unroll                              // column (part, head, group) x the half's 8 rows
+      // weights p (b - a) / 15 of both groups, transposed: column (part, head, group) x the half's
+      // 8 rows; and their second terms
+      uint32_t wt[RPL], lt[RPL];
+#pragma unroll
       for (int j = 0; j < RPL; ++j) {
         const int row = 8 * (part * RPL + j) + gid;
         uint32_t va[NG];
@@ -494,7 +504,21 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
           w[g] = p15 * (ab.y - ab.x);
           asum[g] = fmaf(p, ab.x, asum[g]);
         }
-        wt[j] = movtrans(pack_h2(w[0], NG == 2 ? w[NG - 1] : w[0]));
+        // Outputs are means, near 0, of values a + s c with a < 0, and show an fp16 weight's error
+        // several times over (relative error of the outputs 6.6e-4).  So the weight's remainder
+        // goes along: as a second fp16 term in the columns of another part, which are zero in this
+        // half's products (3.3e-4); with one part, where it would take products of its own (4%
+        // of the call's time), times the codes' middle, in the sums of the minima (5e-4).
+        const uint32_t wh = pack_h2(w[0], NG == 2 ? w[NG - 1] : w[0]);
+        const float2 wr = unpack_h2(wh);
+        if (NP == 1) {
+          asum[0] = fmaf(7.5f, w[0] - wr.x, asum[0]);
+          if (NG == 2) asum[NG - 1] = fmaf(7.5f, w[NG - 1] - wr.y, asum[NG - 1]);
+        } else {
+          const uint32_t wl = pack_h2(w[0] - wr.x, NG == 2 ? w[NG - 1] - wr.y : w[0] - wr.x);
+          lt[j] = movtrans(__shfl_xor_sync(0xFFFFFFFFu, wl, 2));
+        }
+        wt[j] = movtrans(wh);
       }
 #pragma unroll
       for (int sub = 0; sub < kSub; ++sub) {
@@ -503,7 +527,10 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         for (int r = 0; r < 2; ++r) {
           const int rh = 2 * sub + r;
           load_words<NW>(slot + R::V_OFF + (8 * rh + gid) * R::ROW_CODE + tig * 4 * NW, vw[r]);
-          bv[r] = (NP == 1 || (gid >> 1) / HEADS == rh / RPL) ? wt[rh % RPL] : 0u;
+          const int col = (gid >> 1) / HEADS;            // the part of the lane's column
+          bv[r] = (NP == 1 || col == rh / RPL)         ? wt[rh % RPL]
+                  : ((col ^ (NP / 2)) == rh / RPL) ? lt[rh % RPL]
+                                                   : 0u;
         }
 #pragma unroll
         for (int wd = 0; wd < NW; ++wd) {
@@ -546,8 +573,8 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) asum[g] += __shfl_xor_sync(0xFFFFFFFFu, asum[g], o);
     }
-    // the lane's channels are those of group gid / 4 (d = 128): pair u holds channels cbase + 8 (u /
-    // 2) + 2 (u % 2) and the next
+    // the lane's channels are those of group gid / 4 (d = 128): pair u holds channels cbase + 8 (u
+    // / 2) + 2 (u % 2) and the next
     const int g = (NG == 2) ? (gid >> 2) : 0;
     const float A = (NG == 2 && g) ? asum[NG - 1] : asum[0];
     const int cbase = 8 * NW * (gid >> 1) + 4 * (gid & 1);

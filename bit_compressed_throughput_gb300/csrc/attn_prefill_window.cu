@@ -7,35 +7,51 @@
 //   out_r,hq = sum_t softmax_t(scale * q_r,hq . k_t) v_t   over the t that i sees,
 // K/V head hq / G of G = Hq / Hkv query heads each; a row that sees nothing gets zeros.
 //
-// A CTA owns a block of 256 query rows of one (sequence, query head): two Q tiles (A, B) of 128 rows that
-// share the K/V tiles of 128 keys.  The key tiles of a block are those that one of its rows sees
-// (first positions, then the window; key_tiles in ragged.cuh): a window costs what it shows, not the
-// sequence.  Q, K and V are read in place by TMA (boxes of 64 columns x 128 rows, 128B swizzle) at
-// the sequence's own rows, so a box may end in another sequence's rows or past the buffer (zeros);
-// such rows are masked or not stored.
+// A CTA owns a block of 256 query rows of one (sequence, query head): two Q tiles (A, B) of 128
+// rows that share the K/V tiles of 128 keys.  The key tiles of a block are those that one of its
+// rows sees (first positions, then the window; key_tiles in ragged.cuh): a window costs what it
+// shows, not the sequence.  Q, K and V are read in place by TMA (boxes of 64 columns x 128 rows,
+// 128B swizzle) at the sequence's own rows, so a box may end in another sequence's rows or past the
+// buffer (zeros); such rows are masked or not stored.
 //   S = Q K^T     tcgen05.mma kind::f16, S (fp32) in TMEM
-//   softmax       one thread per query row, two passes over its 128 key columns in TMEM (the maximum,
-//                 then P): base-2 online softmax with a lazily moved reference maximum (by more
-//                 than 2^8), P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that every row
-//                 of the Q tile sees in full are not masked; the others take a bit mask per row.
+//   softmax       one thread per query row, two passes over its 128 key columns in TMEM (the
+//                 maximum, then P): base-2 online softmax with a lazily moved reference maximum
+//                 (by more than 2^8), P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that
+//                 every row of the Q tile sees in full are not masked; the others take a bit mask
+//                 per row.
 //   O += P V      tcgen05.mma with P from TMEM
-// TMEM: S of A and B (128 columns each), O of A and B (d columns each).  A Q tile takes part only in
-// the key tiles that it sees, and in the 16-key steps of them that it sees.
+// TMEM: S of A and B (128 columns each), O of A and B (d columns each).  A Q tile takes part only
+// in the key tiles that it sees, and in the 16-key steps of them that it sees.
 //   warp 0       the work items and TMA producer: K tiles, V tiles and Q, rings of two each
 //   warps 1, 2   MMA issuers of Q tiles A and B: S_t(0); then per key tile P_t(j) V_j, S_t(j + 1)
 //   warps 3-10   softmax of A and B (TMEM lanes 32 (w % 4) ..)
 //   warps 11-14  output: O_t / l of a finished block, staged in shared memory, stored by TMA
 //
-// Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it would
-// reach the rows of the Q tile that do not see it.  The output warps therefore test their rows: a
-// row with an infinity or a NaN is computed again on its own, over its visible keys alone
-// (attend_row), so that only what it sees can reach it.  Finite inputs never take that path.
+// Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it
+// would reach the rows of the Q tile that do not see it.  The output warps therefore test their
+// rows: a row with an infinity or a NaN is computed again on its own, over its visible keys alone
+// (attend_row), so that only what it sees can reach it.  Finite inputs take that path only where
+// rounding carries an output past fp16's range.
 //
 // The work order: blocks by descending index, for each the sequences that have one (longest first),
-// for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read and
-// checked on the device, kMaxSeqs sequences per launch.  The producer works the items out and hands
-// them to the other warps through a ring in shared memory, ahead of the loads: the softmax warps
-// have no registers to spare for it.
+// for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read
+// and checked on the device, kMaxSeqs sequences per launch.  The producer works the items out and
+// hands them to the other warps through a ring in shared memory, ahead of the loads: the softmax
+// warps have no registers to spare for it.
+//
+// What bounds it: the turn that a Q tile takes -- P V and S (16 MMAs, 1024 cycles of tensor work),
+// the softmax (about 400 cycles for the maximum, 900 for P: 128 exponentials a thread, 512 cycles
+// of the special-function unit), and the barriers between -- with two Q tiles taking turns: 3200
+// cycles for a pair of key tiles of both, of which the tensor core works 2050.  Two sequences of
+// 8192, 32 heads, no window: 800 us, 1376 TFLOP/s (0.72 of the measured burst rate); a window of
+// 1024 with 4 first positions over two documents of 8k, grouped heads: 254 us, 935 TFLOP/s of
+// visible pairs; ragged prompts of 300 .. 512: 64 us, where the first loads and the turns of short
+// blocks count.  Steps that brought it there, on the 8k window: one thread per row instead of two
+// that exchange maxima 345 -> 318 us, an issuer warp per Q tile and key steps from the producer 318
+// -> 307, MMAs issued under one lane's predicate on warp-uniform values 307 -> 254.  Not kept: one
+// pass instead of two (a chunk's maximum checked before its exponentials: 254 -> 277 us, the
+// exponentials stand still meanwhile); prefetching the next Q and K/V tiles into L2 (64 -> 72 us on
+// the prompts).
 //
 // Every mbarrier wait is bounded; on timeout the CTA sets the device error word (read by
 // fg_check_device_error), drains its copies and MMAs and frees TMEM.
@@ -94,8 +110,8 @@ struct PSmem {
 };
 static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 
-// barriers: q_full[2], q_free[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_done[2], o_free[2],
-// l_full[2], o_staged, o_stage_free, drain[2], item_full[4], item_free[4]
+// barriers: q_full[2], q_free[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2],
+// o_done[2], o_free[2], l_full[2], o_staged, o_stage_free, drain[2], item_full[4], item_free[4]
 constexpr int B_QFULL = 0, B_QFREE = 2, B_KFULL = 4, B_KFREE = 6, B_VFULL = 8, B_VFREE = 10,
               B_SFULL = 12, B_PFULL = 14, B_ODONE = 16, B_OFREE = 18, B_LFULL = 20, B_OSTAGED = 22,
               B_OSFREE = 23, B_DRAIN = 24, B_IFULL = 26, B_IFREE = B_IFULL + ITEMS,
@@ -198,7 +214,7 @@ struct PArgs {
 // A work item: a block of 256 query rows of one (sequence, query head).
 struct Item {
   int hq;                                   // query head; -1: no more items
-  int qrow, rows;                           // the block's first row in q and out; rows from there on
+  int qrow, rows;                           // the block's first row in q and out; how many
   int krow;                                 // the sequence's first K/V row
   int pos;                                  // position of the block's first row (may be negative)
   KeyTiles t[2], u;                         // the Q tiles' key tiles, and their union
@@ -271,7 +287,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   int* live = reinterpret_cast<int*>(tmem_slot + 2);   // sequences with rows
   unsigned* steps_of = tmem_slot + 3;                  // [STAGES]: key steps of the K tile
   Seq* seqs = reinterpret_cast<Seq*>(smem + L::SEQ_OFF);
-  auto item_slot = [&](int n) { return reinterpret_cast<Item*>(smem + L::ITEM_OFF + 64 * (n % ITEMS)); };
+  auto item_slot = [&](int n) {
+    return reinterpret_cast<Item*>(smem + L::ITEM_OFF + 64 * (n % ITEMS));
+  };
   float* l_buf = reinterpret_cast<float*>(smem + L::L_OFF);
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
@@ -570,7 +588,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them is
     // decided for the whole warp, waits included (a lane that gave up takes its warp along)
     for (int n = 0; ok; ++n) {
-      const volatile Item* it = item_wait(n);          // read again where needed: no registers for it
+      const volatile Item* it = item_wait(n);          // read where needed: no registers for it
       if (!__all_sync(0xFFFFFFFFu, it != nullptr) || it->hq < 0) break;
       const int nt = it->t[t].ns + it->t[t].te - it->t[t].tw;
       if (nt == 0) {
@@ -761,8 +779,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const float inv = pos + m >= 0
                               ? 1.0f / l_buf[t * QT + m]
                               : 0.0f;
-        // O / l in 64-column boxes.  A full tile: staged in shared memory (the 128B-swizzled layout of
-        // the output map: 16-byte chunk k of row m at chunk k ^ (m % 8)) and stored by TMA.  The
+        // O / l in 64-column boxes.  A full tile: staged in shared memory (the 128B-swizzled layout
+        // of the output map: 16-byte chunk k of row m at chunk k ^ (m % 8)) and stored by TMA.  The
         // last tile of a sequence: each thread stores its own row.
         const bool full = rows == QT;
 #pragma unroll 1

@@ -68,8 +68,8 @@ FG_HD SeqTiles seq_tiles(int len, int window, int sinks) {
   s.nt = s.ns + te - s.tw;
   return s;
 }
-// Position of the first row of tile u (0 <= u < nt), and the tiles from there to u1 that are one run
-// of positions (either the first positions' or the window's).
+// Position of the first row of tile u (0 <= u < nt), and the tiles from there to u1 that are one
+// run of positions (either the first positions' or the window's).
 FG_HD int tile_pos(const SeqTiles& s, int u) {
   return (u < s.ns ? u : u - s.ns + s.tw) * kTilePos;
 }

@@ -191,10 +191,10 @@ int fg_kv_append_q4(const uint16_t* k_new, const uint16_t* v_new, int64_t row_st
  * elements apart: >= h, a multiple of 8) are quantised into positions pos[b], pos[b]+1, .. of
  * sequence b, with the codes and statistics fg_kv_append_q4 gives for those rows; everything
  * else in the cache stays as it was.  `rows`: the rows k_new and v_new hold (< 2^31 - 64); rows
- * before row_off[0] or from row_off[B] on are not used.  row_off: device int32 [B+1], 0 <= row_off[b]
- * <= row_off[b+1] <= rows; pos: device int32 [B], 0 <= pos[b], pos[b] + (rows of b) <= cap.  The
- * host never reads the two arrays, so their values are checked on the device: a row that does
- * not fit is not written, and fg_check_device_error() returns FG_ERR_CAPACITY.
+ * before row_off[0] or from row_off[B] on are not used.  row_off: device int32 [B+1], 0 <=
+ * row_off[b] <= row_off[b+1] <= rows; pos: device int32 [B], 0 <= pos[b], pos[b] + (rows of b) <=
+ * cap.  The host never reads the two arrays, so their values are checked on the device: a row that
+ * does not fit is not written, and fg_check_device_error() returns FG_ERR_CAPACITY.
  * rows == 0 or kv->B == 0 is a no-op.  The pages process blocks of equal prompts and have no
  * counterpart. */
 int fg_kv_append_q4_ragged(const uint16_t* k_new, const uint16_t* v_new, int64_t row_stride,
@@ -277,9 +277,10 @@ int fg_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, int32_t H, int
  * sequence b is its newest cached position i = lens[b] - 1, and
  *   out[b][hq*d + j] = sum_t softmax_t(scale * q_b,hq . K^_b,hk,t) V^_b,hk,t,j   over the visible t,
  * query head hq reading K/V head hk = hq / (Hq / H): Hq query heads, a multiple of the cache's H.
- * A sequence of length 0 sees nothing: its output is 0.  q: device fp16, row b at b*q_stride; out:
- * device fp16, row b at b*out_stride (both strides >= Hq*d, multiples of 8).  lens: device int32
- * [B], 0 <= lens[b] <= cap, checked on the device (a length that does not fit counts as 0, and
+ * K^ and V^ enter the sums as a + q*((b-a)/15), not rounded to fp16 first.  A sequence of length
+ * 0 sees nothing: its output is 0.  q: device fp16, row b at b*q_stride; out: device fp16, row b
+ * at b*out_stride (both strides >= Hq*d, multiples of 8).  lens: device int32 [B], 0 <= lens[b]
+ * <= cap, checked on the device (a length that does not fit counts as 0, and
  * fg_check_device_error() returns FG_ERR_CAPACITY).  window, sinks >= 0.  ws: device scratch of
  * at least fg_decode_attn_window_workspace_bytes(kv, Hq) bytes, whatever the lengths and the
  * window; it needs no initialisation.  Two calls in flight at once need workspaces of their own.
@@ -305,9 +306,9 @@ size_t fg_decode_attn_window_workspace_bytes(const fg_kvcache* kv, int32_t Hq);
  * decreasing, within 0 .. q_rows and 0 .. kv_rows; checked on the device (the output of a sequence
  * that does not fit stays as it was, and fg_check_device_error() returns FG_ERR_CAPACITY).  Rows
  * of out outside every sequence stay as they were.  d in {64, 128}; Hq a multiple of Hkv, at most
- * 65536; out must not overlap q, k or v.  Values of keys that a row does not see never reach it, not even
- * infinities and NaN.  nseq == 0 or q_rows == 0 is a no-op; with kv_rows == 0, k and v may be
- * NULL.  The pages' prompts have one length and no window; no counterpart. */
+ * 65536; out must not overlap q, k or v.  Values of keys that a row does not see never reach it,
+ * not even infinities and NaN.  nseq == 0 or q_rows == 0 is a no-op; with kv_rows == 0, k and v may
+ * be NULL.  The pages' prompts have one length and no window; no counterpart. */
 int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,
                            const int32_t* q_off, const uint16_t* k, const uint16_t* v,
                            int64_t kv_stride, int32_t kv_rows, const int32_t* kv_off, int32_t nseq,
