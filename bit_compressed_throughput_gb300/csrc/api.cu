@@ -610,7 +610,7 @@ int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int
   int sms = 0;
   int rc = check_ragged(kv, row_stride, rows, row_off, pos, &noop);
   if (rc || noop) return rc;
-  if ((!k_out && !v_out) || !aligned16(k_out) || !aligned16(v_out)) return FG_ERR_ARG;
+  if (k_out == v_out || !aligned16(k_out) || !aligned16(v_out)) return FG_ERR_ARG;
   if ((rc = check_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Span sp(st);
@@ -690,8 +690,15 @@ static int check_window(int32_t window, int32_t sinks, float scale) {
   return FG_OK;
 }
 
+// Query heads that share the cache's heads; the kernel numbers a call's tiles, and a warp's share
+// of them, with room for 2^40 tiles.
+static bool window_heads_ok(const fg_kvcache& kv, int32_t Hq) {
+  return Hq > 0 && Hq <= 65536 && Hq % kv.H == 0 &&
+         (int64_t)kv.B * Hq <= (1ll << 40) / (kv.cap / 16 + 2);
+}
+
 size_t fg_decode_attn_window_workspace_bytes(const fg_kvcache* kv, int32_t Hq) {
-  if (check_kv(kv) != FG_OK || Hq <= 0 || Hq % kv->H != 0 || kv->B == 0) return 0;
+  if (check_kv(kv) != FG_OK || !window_heads_ok(*kv, Hq) || kv->B == 0) return 0;
   return decode_attn_window_ws_bytes(*kv, Hq);
 }
 
@@ -702,8 +709,8 @@ int fg_decode_attn_q4kv_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
   int rc = check_kv(kv);
   if (rc || (rc = check_window(window, sinks, scale))) return rc;
   const int64_t width = (int64_t)Hq * (kv->h / kv->H);
-  if (Hq <= 0 || Hq % kv->H != 0 || q_stride < width || q_stride % 8 != 0 || out_stride < width ||
-      out_stride % 8 != 0 || (int64_t)kv->B * Hq > (1ll << 31) - 1)
+  if (!window_heads_ok(*kv, Hq) || q_stride < width || q_stride % 8 != 0 || out_stride < width ||
+      out_stride % 8 != 0)
     return FG_ERR_SHAPE;
   if (kv->B == 0) return FG_OK;
   if (!q || !out || !lens || !aligned16(q) || !aligned16(out) || !aligned4(lens)) return FG_ERR_ARG;

@@ -161,17 +161,27 @@ struct Cursor {
   int b, rs, u;
   SeqTiles s;
 };
+// Moves to the next sequence that sees something, found by the whole warp 32 at a time (a batch
+// may have many empty places).
+__device__ __forceinline__ bool next_sequence(Cursor& c, const Args& a, const fg_kvcache& kv) {
+  const int lane = threadIdx.x & 31;
+  for (int b = c.b + 1; b < kv.B; b += 32) {
+    const int len = b + lane < kv.B ? length_of(a, kv, b + lane) : 0;
+    const unsigned busy = __ballot_sync(0xFFFFFFFFu, len > 0);
+    if (busy) {
+      const int i = __ffs(busy) - 1;
+      c.b = b + i;
+      c.s = seq_tiles(__shfl_sync(0xFFFFFFFFu, len, i), a.window, a.sinks);
+      return true;
+    }
+  }
+  return false;                            // the end of the order: never asked for
+}
 __device__ __forceinline__ void next_row_set(Cursor& c, const Args& a, const fg_kvcache& kv) {
   c.u = 0;
   if (++c.rs < kv.H * a.nhb) return;
   c.rs = 0;
-  do {
-    if (++c.b >= kv.B) {                   // the end of the order: never asked for
-      c.b = kv.B - 1;
-      return;
-    }
-    c.s = seq_tiles(length_of(a, kv, c.b), a.window, a.sinks);
-  } while (c.s.nt == 0);
+  next_sequence(c, a, kv);
 }
 
 // The query heads of a row set as B fragments (column n = gid: head (gid / 2) % HEADS, group gid &
@@ -226,11 +236,7 @@ __device__ __forceinline__ void skip_tiles(Cursor& c, int64_t dx, const Args& a,
   int64_t at = (int64_t)c.rs * c.s.nt + c.u + dx;        // within sequence b
   while (at >= (int64_t)rsets * c.s.nt) {
     at -= (int64_t)rsets * c.s.nt;
-    if (++c.b >= kv.B) {                   // the end of the order: never asked for
-      c.b = kv.B - 1;
-      return;
-    }
-    c.s = seq_tiles(length_of(a, kv, c.b), a.window, a.sinks);
+    if (!next_sequence(c, a, kv)) return;
   }
   c.rs = at < 0x7FFFFFFF ? (int)((unsigned)at / (unsigned)c.s.nt) : (int)(at / c.s.nt);
   c.u = (int)(at - (int64_t)c.rs * c.s.nt);
@@ -319,7 +325,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
   const bool has_share = busy && warp < per_cta && w < n;
   if (has_share) {
     const int64_t x0 = shares.first(w);
-    ileft = (int)(shares.first(w + 1) - x0);           // the cache's size bounds it far below 2^31
+    ileft = (int)(shares.first(w + 1) - x0);           // the host bounds the call's tiles by 2^40
     ic.b = first_b;
     ic.s = seq_tiles(length_of(a, kv, ic.b), a.window, a.sinks);
     skip_tiles(ic, x0 - first_before * rsets, a, kv);

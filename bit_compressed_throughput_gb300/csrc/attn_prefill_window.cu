@@ -30,8 +30,9 @@
 // Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it
 // would reach the rows of the Q tile that do not see it.  The output warps therefore test their
 // rows: a row with an infinity or a NaN is computed again on its own, over its visible keys alone
-// (attend_row), so that only what it sees can reach it.  Finite inputs take that path only where
-// rounding carries an output past fp16's range.
+// (attend_rows), so that only what it sees can reach it.  Finite inputs take that path only where
+// rounding carries an output past fp16's range.  The rows behind a sequence in its last 16-key
+// step, which may hold anything, are zeroed in shared memory first.
 //
 // The work order: blocks by descending index, for each the sequences that have one (longest first),
 // for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read
@@ -80,7 +81,7 @@ constexpr int W_SM = 3;                     // softmax warps 3..10: Q tile (w - 
                                             // quarter w % 4
 constexpr int W_OUT = 11;                   // first output warp (11..14)
 constexpr uint32_t TMEM_COLS = 512;
-constexpr long long kWaitCycles = 1ll << 34;   // attend_row may keep the other warps waiting
+constexpr long long kWaitCycles = 1ll << 36;   // attend_rows may keep the other warps waiting
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 constexpr int BOX = QT * 128;               // bytes of one 64-column x 128-row box
 constexpr int kMaxSeqs = 384;               // sequences per launch
@@ -116,7 +117,7 @@ constexpr int B_QFULL = 0, B_QFREE = 2, B_KFULL = 4, B_KFREE = 6, B_VFULL = 8, B
               B_SFULL = 12, B_PFULL = 14, B_ODONE = 16, B_OFREE = 18, B_LFULL = 20, B_OSTAGED = 22,
               B_OSFREE = 23, B_DRAIN = 24, B_IFULL = 26, B_IFREE = B_IFULL + ITEMS,
               NBARS = B_IFREE + ITEMS;
-static_assert(NBARS * 8 + 12 + STAGES * 4 <= 512, "barrier space");
+static_assert(NBARS * 8 + 12 + STAGES * 8 <= 512, "barrier space");
 
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_test(bar, parity)) return true;
@@ -147,62 +148,100 @@ __device__ __forceinline__ float in_range(float y) {
   return fabsf(y) < 66000.0f ? fminf(fmaxf(y, -65504.0f), 65504.0f) : y;
 }
 
-// One row on its own, by a whole warp: position i of a sequence whose K/V rows start at k0; lane
-// l returns channels l D/32 ..  Scores are computed a key per lane, values a channel group per
-// lane; only visible keys are read.
+// Rows on their own, by a whole warp: up to kRowsAtOnce of its 32 (the bits of `rows`), the first of
+// which is row qrow at position pos of a sequence whose K/V rows start at k0; lane l returns
+// channels 64 box + 2l and the next.  Scores are computed a key per lane, values a channel pair per
+// lane; what a row does not see takes no part in it.  (4 rows of 16384 keys: 3 ms.)
+constexpr int kRowsAtOnce = 4;
 template <int D>
-__device__ __noinline__ void attend_row(const PrefillWindow& a, int64_t qrow, int hq, int k0, int i,
-                                        float (&o)[D / 32]) {
-  constexpr int C = D / 32;
+__device__ __noinline__ void attend_rows(const PrefillWindow& a, int qrow, int hq, int k0, int pos,
+                                         unsigned rows, int box, float2 (&out)[kRowsAtOnce]) {
+  constexpr int R = kRowsAtOnce;
   const int lane = threadIdx.x & 31;
   const int64_t kcol = (int64_t)(hq / (a.Hq / a.Hkv)) * D;
-  const uint16_t* q = a.q + qrow * a.q_stride + (int64_t)hq * D;
   const float sl2 = a.scale * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.0f;
+  const uint16_t* q[R];
+  int i[R];                                 // the rows' positions, ascending (the last repeats)
+  float m[R], l[R];
 #pragma unroll
-  for (int c = 0; c < C; ++c) o[c] = 0.0f;
-  if (i < 0) return;
-  const int w0 = (a.window == 0 || i < a.window) ? 0 : i - a.window + 1;
-  const int first = min(a.sinks, w0), n = first + (i + 1 - w0);   // visible keys
-  auto key_row = [&](int u) { return (int64_t)k0 + (u < first ? u : u - first + w0); };
+  for (int r = 0; r < R; ++r) {
+    const int row = __ffs(rows) - 1;
+    if (rows & (rows - 1)) rows &= rows - 1;
+    q[r] = a.q + (int64_t)(qrow + row) * a.q_stride + (int64_t)hq * D;
+    i[r] = pos + row;
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+    out[r] = make_float2(0.0f, 0.0f);
+  }
+  const int w0 = (a.window == 0 || i[0] < a.window) ? 0 : i[0] - a.window + 1;
+  const int first = min(a.sinks, w0), n = first + (i[R - 1] + 1 - w0);   // keys that a row sees
+  auto key = [&](int u) { return u < first ? u : u - first + w0; };
+#pragma unroll 1
   for (int u0 = 0; u0 < n; u0 += 32) {
-    const int cnt = min(32, n - u0);
-    float s = -INFINITY;
-    if (lane < cnt) {
-      const uint16_t* k = a.k + key_row(u0 + lane) * a.kv_stride + kcol;
-      s = 0.0f;
-      for (int c = 0; c < D; c += 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(q + c), y = ldg_nc_v4(k + c);
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+    const int cnt = min(32, n - u0), t = key(u0 + min(lane, cnt - 1));
+    const uint16_t* k = a.k + (int64_t)(k0 + t) * a.kv_stride + kcol;
+    float s[R] = {};
+#pragma unroll 4
+    for (int c = 0; c < D; c += 8) {
+      const uint4 y = ldg_nc_v4(k + c);
+      const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 x = ldg_nc_v4(q[r] + c);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 xf = unpack_h2(xw[e]), yf = unpack_h2(yw[e]);
-          s = fmaf(xf.x, yf.x, fmaf(xf.y, yf.y, s));
+          s[r] = fmaf(xf.x, yf.x, fmaf(xf.y, yf.y, s[r]));
         }
       }
-      s *= sl2;
     }
-    float mx = s;
+    unsigned sees[R];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-    mx = fmaxf(mx, m);
-    const float ref = (mx == -INFINITY) ? 0.0f : mx;
-    const float corr = exp2f(m - ref), p = lane < cnt ? exp2f(s - ref) : 0.0f;
-    l = l * corr + p;
+    for (int r = 0; r < R; ++r) {
+      const bool vis = lane < cnt && visible(t, i[r], a.window, a.sinks);
+      sees[r] = __ballot_sync(0xFFFFFFFFu, vis);
+      const float x = vis ? s[r] * sl2 : -INFINITY;
+      float mx = x;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] *= corr;
-    for (int j = 0; j < cnt; ++j) {
-      const float pj = __shfl_sync(0xFFFFFFFFu, p, j);
-      const uint16_t* v = a.v + key_row(u0 + j) * a.kv_stride + kcol + lane * C;
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = fmaf(pj, h2f(v[c]), o[c]);
+      for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+      mx = fmaxf(mx, m[r]);
+      const float ref = (mx == -INFINITY) ? 0.0f : mx, corr = exp2f(m[r] - ref);
+      s[r] = vis ? exp2f(x - ref) : 0.0f;
+      l[r] = l[r] * corr + s[r];
+      out[r].x *= corr;
+      out[r].y *= corr;
+      m[r] = mx;
     }
-    m = mx;
+    constexpr int BATCH = 8;                // values in flight
+#pragma unroll 1
+    for (int j0 = 0; j0 < cnt; j0 += BATCH) {
+      uint32_t v[BATCH];
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        v[j] = *reinterpret_cast<const uint32_t*>(
+            a.v + (int64_t)(k0 + key(u0 + min(j0 + j, cnt - 1))) * a.kv_stride + kcol + 64 * box +
+            2 * lane);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const float2 x = unpack_h2(v[j]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const bool vis = sees[r] >> (j0 + j) & 1u;
+          const float pj = __shfl_sync(0xFFFFFFFFu, s[r], j0 + j);
+          out[r].x = fmaf(pj, vis ? x.x : 0.0f, out[r].x);
+          out[r].y = fmaf(pj, vis ? x.y : 0.0f, out[r].y);
+        }
+      }
+    }
   }
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+  for (int r = 0; r < R; ++r) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) o[c] = in_range(o[c] / l);
+    for (int d = 1; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], d);
+    out[r].x = i[r] < 0 ? 0.0f : in_range(out[r].x / l[r]);
+    out[r].y = i[r] < 0 ? 0.0f : in_range(out[r].y / l[r]);
+  }
 }
 
 struct PArgs {
@@ -210,6 +249,20 @@ struct PArgs {
   int s0, ns;                               // sequences s0 .. s0 + ns - 1 of the call
   float scale_log2;
 };
+
+// Rows `tail` .. of a V tile in their 16-key step become 0, written by a whole warp (a called
+// function: in line it takes registers that the other warps' loops need, 1.5% of an 8k window's
+// time).  Both MMA issuers may write (the same zeros); each does before its own products read them
+// and before its part of V's release.
+__device__ __noinline__ void clear_rows(uint8_t* v, int tail, int boxes) {
+  const int chunks = 8 * (((tail + 15) & ~15) - tail);
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < boxes * chunks; i += 32)
+    *reinterpret_cast<uint4*>(v + 128 * tail + (i < chunks ? 16 * i : BOX + 16 * (i - chunks))) =
+        make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
 
 // A work item: a block of 256 query rows of one (sequence, query head).
 struct Item {
@@ -286,6 +339,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* live = reinterpret_cast<int*>(tmem_slot + 2);   // sequences with rows
   unsigned* steps_of = tmem_slot + 3;                  // [STAGES]: key steps of the K tile
+  unsigned* tail_of = steps_of + STAGES;               // [STAGES]: where rows of a V tile that are
+                                                       // not the sequence's begin in a step, or 0
   Seq* seqs = reinterpret_cast<Seq*>(smem + L::SEQ_OFF);
   auto item_slot = [&](int n) {
     return reinterpret_cast<Item*>(smem + L::ITEM_OFF + 64 * (n % ITEMS));
@@ -399,11 +454,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           // K and V have rings of their own: a K stage is free once both Q tiles' S products
           // have read it, a whole softmax before the V stage of the same tile
           const int st = kvg % STAGES, row = it.krow + it.u.tile(j) * KT;
-          auto load = [&](const CUtensorMap* tm, int off, int full, int free, unsigned steps) {
+          auto load = [&](const CUtensorMap* tm, int off, int full, int free, unsigned note) {
             if (kvg >= STAGES &&
                 !bwait(bar(free + st), (uint32_t)(((kvg / STAGES) & 1) ^ 1), abort_flag))
               return false;
-            if (full == B_KFULL) steps_of[st] = steps;  // handed on by the barrier
+            (full == B_KFULL ? steps_of : tail_of)[st] = note;   // handed on by the barrier
             mbar_expect_tx(bar(full + st), (uint32_t)L::TILE);
             for (int c = 0; c < NB; ++c)
               tma_load_2d(smem_u32(smem + off + st * L::TILE + c * BOX), tm, hk * D + 64 * c, row,
@@ -420,8 +475,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                                          w.sinks);
             return (unsigned)(k.s0 | k.s1 << 4) | last;
           };
-          const unsigned both = steps(0) | steps(1) << 8;
-          if (!load(&tmK, L::K_OFF, B_KFULL, B_KFREE, both)) {
+          if (!load(&tmK, L::K_OFF, B_KFULL, B_KFREE, steps(0) | steps(1) << 8)) {
             ok = false;
             break;
           }
@@ -442,7 +496,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (!ok) break;
             ++qn;
           }
-          if (!load(&tmV, L::V_OFF, B_VFULL, B_VFREE, 0u)) {
+          // the sequence may end inside a 16-key step
+          const int valid = min(KT, it.pos + it.rows - it.u.tile(j) * KT);
+          if (!load(&tmV, L::V_OFF, B_VFULL, B_VFREE, valid % 16 ? valid : 0)) {
             ok = false;
             break;
           }
@@ -513,8 +569,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     // waits for K of tile g; the steps of it that this Q tile takes
     auto wait_k = [&](int g) -> unsigned {
       wait(B_KFULL + g % STAGES, (g / STAGES) & 1);
-      return __shfl_sync(0xFFFFFFFFu, steps_of[g % STAGES], 0) >> (8 * t) & 0xFFu;
+      const unsigned all = __shfl_sync(0xFFFFFFFFu, steps_of[g % STAGES], 0);
+      return all >> (8 * t) & 0xFFu;
     };
+    // Rows `tail` .. of V in their 16-key step become 0.  Both issuers may write (the same zeros);
+    // each does before its own products read them and before its part of V's release.
     for (int n = 0; ok; ++n) {
       const Item* slot = item_wait(n);
       if (!__all_sync(0xFFFFFFFFu, slot != nullptr)) break;
@@ -548,6 +607,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const unsigned next = more ? wait_k(g + 1) : 0u;
         const bool pv = cur & ~kLastTile;
         if (pv) {
+          const unsigned tail = __shfl_sync(0xFFFFFFFFu, tail_of[g % STAGES], 0);
+          if (tail && ok) clear_rows(smem + L::V_OFF + (g % STAGES) * L::TILE, tail, NB);
           // the first product of an item overwrites O_t: the output warps have read it
           if (!add && uses > 0) wait(B_OFREE + t, (uses - 1) & 1);
           wait(B_PFULL + t, pc & 1);
@@ -595,7 +656,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (lane == 0) item_done(n);
         continue;
       }
-      float m_ref = -INFINITY, l_sum = 0.0f;
+      // (rows behind the sequence: no score of theirs moves the reference of the warp's rows)
+      float m_ref = t * QT + m < it->rows ? -INFINITY : INFINITY, l_sum = 0.0f;
       for (int j = 0; j < nt; ++j, ++sc) {
         // masked: some row of the Q tile does not see every key of the tile (warp-uniform); ahead:
         // the position of the Q tile's first row less the key tile's first position
@@ -830,20 +892,21 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           if (redo) {
             __syncwarp();                              // over what the row's own thread stored
-            for (unsigned left = redo; left; left &= left - 1) {
-              constexpr int C = D / 32;
-              const int rr = 32 * quarter + __ffs(left) - 1;
-              float x[C];
-              attend_row<D>(w, (int64_t)qrow + rr, it->hq, it->krow, pos + rr, x);
-              const int ch = lane * C - 64 * hb;       // within this box
-              if (ch < 0 || ch >= 64) continue;
-              uint16_t* dst = full ? reinterpret_cast<uint16_t*>(
-                                         smem + L::O_OFF + 128 * rr +
-                                         (((ch >> 3) ^ (rr & 7)) << 4) + (ch & 7) * 2)
-                                   : w.out + (int64_t)(qrow + rr) * w.out_stride +
-                                         (int64_t)it->hq * D + lane * C;
+            for (unsigned left = redo; left;) {
+              float2 x[kRowsAtOnce];
+              attend_rows<D>(w, qrow + 32 * quarter, it->hq, it->krow, pos + 32 * quarter, left, hb,
+                             x);
 #pragma unroll
-              for (int e = 0; e < C; ++e) dst[e] = f2h(x[e]);
+              for (int r = 0; r < kRowsAtOnce; ++r) {
+                if (!left) break;
+                const int rr = 32 * quarter + __ffs(left) - 1, ch = 2 * lane;
+                left &= left - 1;
+                uint8_t* dst =
+                    full ? smem + L::O_OFF + 128 * rr + (((ch >> 3) ^ (rr & 7)) << 4) + (ch & 7) * 2
+                         : reinterpret_cast<uint8_t*>(w.out + (int64_t)(qrow + rr) * w.out_stride +
+                                                      (int64_t)it->hq * D + 64 * hb + ch);
+                *reinterpret_cast<uint32_t*>(dst) = pack_h2(x[r].x, x[r].y);
+              }
             }
           }
           if (full) {

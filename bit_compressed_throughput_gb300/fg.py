@@ -393,6 +393,8 @@ def fg_decode_attn_q4kv_window(q, Hq: int, cache: KVCacheQ4, lens, scale: float,
     _extents("lens", lens, cache.B)
     _one_device(stream, q, out, lens, ws, cache.k_codes)
     st = cache.struct()
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor expected")
     wsb = 0 if ws is None else ws.numel() * ws.element_size()
     _check("fg_decode_attn_q4kv_window",
            lib.fg_decode_attn_q4kv_window(_ptr(q), q_stride, Hq, C.byref(st), _ptr(lens), window,

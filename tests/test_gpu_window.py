@@ -362,6 +362,31 @@ def test_decode_window_many_sequences(fg, B):
     check_rows(out, dict(enumerate(want)), d, True, "many sequences")
 
 
+@pytest.mark.parametrize("B,G", [(40, 1), (700, 4)])
+def test_decode_window_mostly_empty_batch(fg, B, G):
+    """A few sequences among many empty places, with runs of more than 32 of those."""
+    H, d, cap = 2, 64, 96
+    lens = [0] * B
+    for i, n in zip((1, 2, 35, B - 1), (96, 17, 50, 33)):
+        lens[i] = n
+    cache, k, v, km, vm = fill_cache(fg, B, H, d, cap, seed=27)
+    q16 = fg_synth.random_fp16((B, H * G * d), 5)
+    out = run_decode(fg, dev(q16), H * G, cache, i32(lens), 0.1, 40, 3)
+    want = OW.decode(q16, k, v, lens, H * G, 40, 3, np.float32(0.1), km, vm)
+    check_rows(out, dict(enumerate(want)), d, True, "mostly empty")
+
+
+@pytest.mark.parametrize("Hq,H", [(4, 4), (8, 2)])
+def test_decode_window_in_place(fg, Hq, H):
+    """The output over the queries: the bits of an output of its own."""
+    B, d = 9, 128
+    lens = i32([0, 600, 1, 33, 250, 599, 16, 17, 420])
+    cache, *_ = fill_cache(fg, B, H, d, 600, seed=14)
+    q = dev(fg_synth.random_fp16((B, Hq * d), seed=2))
+    want = run_decode(fg, q, Hq, cache, lens, 0.09, 0, 0)
+    assert torch.equal(want, run_decode(fg, q, Hq, cache, lens, 0.09, 0, 0, out=q))
+
+
 def test_append_many_sequences(fg):
     """Sequences of none to two rows each: every lookup path of a row's sequence."""
     B, H, d = 3000, 1, 64
@@ -515,6 +540,24 @@ def test_prefill_window_masked_positions_may_hold_anything(fg, d, window, sinks,
                 err = np.abs(o[row, :d] - c[row, :d]).max()
                 assert err <= 2 * H16 * np.abs(c[row, :d]).max(), (b, r, err)
     assert (o[qo[-1]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("d,window", [(64, 0), (128, 90)])
+@pytest.mark.parametrize("nk", [[1, 130, 127, 300], [17, 255, 33, 129]])
+def test_prefill_window_rows_behind_hold_anything(fg, d, window, nk):
+    """What stands in the rows behind the last sequence changes no bit of the outputs."""
+    q16, kv16 = prefill_inputs(2, 1, d, nk, nk, seed=d + window, spare=70)
+    off = offsets(nk)
+    outs = []
+    for tail in (0.0, np.nan, np.inf, -65504.0):
+        q, kv = q16.copy(), kv16.copy()
+        q[off[-1]:], kv[off[-1]:] = tail, tail
+        t = dev(kv)
+        outs.append(run_prefill(fg, dev(q), i32(off), t[:, :d], t[:, d:2 * d], i32(off), 2, 1, 0.1,
+                                window, 3))
+        assert torch.equal(outs[0], outs[-1]), tail
+    fg.fg_check_device_error()
+    assert bool(torch.isfinite(outs[0]).all())
 
 
 @pytest.mark.parametrize("q_off,kv_off", [
@@ -727,6 +770,7 @@ def test_binding_refuses(fg):
         lambda: fg.fg_kv_read_q4_ragged(cache, off, pos, None, None),
         lambda: fg.fg_decode_attn_q4kv_window(x, 1, cache, pos, 0.1, x[:2]),
         lambda: fg.fg_decode_attn_q4kv_window(x[:2], 1, cache, off, 0.1, x[2:]),
+        lambda: fg.fg_decode_attn_q4kv_window(x[:2], 1, cache, pos, 0.1, x[2:], x[:1].expand(64, 128)),
         lambda: fg.fg_prefill_attn_window(x, off, x, x[:3], off, 1, 1, 0.1, x.clone()),
         lambda: fg.fg_prefill_attn_window(x, off, x, x, off[:2], 1, 1, 0.1, x.clone()),
         lambda: fg.fg_prefill_attn_window(x, off, x.t(), x, off, 1, 1, 0.1, x.clone()),

@@ -48,6 +48,7 @@ def test_ragged_cache_validation(fg):
         assert call(kv=kvs(fg, B=0), k=None, v=None, off=None, pos=None) == fg.FG_OK
     assert append(k=None) == fg.FG_ERR_ARG and append(v=None) == fg.FG_ERR_ARG
     assert read(k=None, v=None) == fg.FG_ERR_ARG
+    assert read(k=FAKE, v=FAKE) == fg.FG_ERR_ARG                      # one output over the other
 
 
 def test_decode_window_validation(fg):
@@ -75,6 +76,14 @@ def test_decode_window_validation(fg):
     assert L.fg_decode_attn_window_workspace_bytes(C.byref(kvs(fg, cap=20)), 4) == 0
     assert L.fg_decode_attn_window_workspace_bytes(C.byref(kvs(fg)), 3) == 0
     assert L.fg_decode_attn_window_workspace_bytes(None, 4) == 0
+    # more heads, or more tiles of row sets, than the kernel can number
+    many = kvs(fg, h=64, H=1)
+    assert call(kv=many, Hq=65537, qs=65537 * 64, os_=65537 * 64) == fg.FG_ERR_SHAPE
+    assert L.fg_decode_attn_window_workspace_bytes(C.byref(many), 65536) > 0
+    assert L.fg_decode_attn_window_workspace_bytes(C.byref(many), 65537) == 0
+    long = kvs(fg, B=64, cap=1 << 26, h=64, H=1)
+    assert call(kv=long, Hq=8192, qs=8192 * 64, os_=8192 * 64) == fg.FG_ERR_SHAPE
+    assert L.fg_decode_attn_window_workspace_bytes(C.byref(long), 8192) == 0
 
 
 def test_prefill_window_validation(fg):
