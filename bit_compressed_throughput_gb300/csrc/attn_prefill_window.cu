@@ -25,7 +25,8 @@
 //   warp 0       the work items and TMA producer: K tiles, V tiles and Q, rings of two each
 //   warps 1, 2   MMA issuers of Q tiles A and B: S_t(0); then per key tile P_t(j) V_j, S_t(j + 1)
 //   warps 3-10   softmax of A and B (TMEM lanes 32 (w % 4) ..)
-//   warps 11-14  output: O_t / l of a finished block, staged in shared memory, stored by TMA
+//   warps 11-14  output: O_t / l of a finished block, 32 rows a warp, staged in shared memory and
+//                stored by TMA
 //
 // Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it
 // would reach the rows of the Q tile that do not see it.  The output warps therefore test their
@@ -45,14 +46,17 @@
 // of the special-function unit), and the barriers between -- with two Q tiles taking turns: 3200
 // cycles for a pair of key tiles of both, of which the tensor core works 2050.  Two sequences of
 // 8192, 32 heads, no window: 800 us, 1376 TFLOP/s (0.72 of the measured burst rate); a window of
-// 1024 with 4 first positions over two documents of 8k, grouped heads: 254 us, 935 TFLOP/s of
-// visible pairs; ragged prompts of 300 .. 512: 64 us, where the first loads and the turns of short
-// blocks count.  Steps that brought it there, on the 8k window: one thread per row instead of two
-// that exchange maxima 345 -> 318 us, an issuer warp per Q tile and key steps from the producer 318
-// -> 307, MMAs issued under one lane's predicate on warp-uniform values 307 -> 254.  Not kept: one
-// pass instead of two (a chunk's maximum checked before its exponentials: 254 -> 277 us, the
-// exponentials stand still meanwhile); prefetching the next Q and K/V tiles into L2 (64 -> 72 us on
-// the prompts).
+// 1024 with 4 first positions over two documents of 8k, grouped heads: 252 us, 940 TFLOP/s of
+// visible pairs; ragged prompts of 300 .. 512: 62 us, where the first loads (10000 cycles to the
+// first S), the masked tiles and the turns of short blocks count.  A masked tile's softmax takes
+// 2700 cycles instead of 1250.  Steps that brought it there, on the 8k window: one thread per row
+// instead of two that exchange maxima 345 -> 318 us, an issuer warp per Q tile and key steps from
+// the producer 318 -> 307, MMAs issued under one lane's predicate on warp-uniform values
+// 307 -> 254.  Not kept: one pass instead of two (a chunk's maximum checked before its
+// exponentials: 254 -> 277 us, the exponentials stand still meanwhile); the next load in flight in
+// masked tiles too (249 -> 259 us: registers), or masks in the code of the unmasked ones
+// (249 -> 276 us); more registers for the softmax warps (setmaxnreg, 16 warps: 252 -> 262 us);
+// prefetching the next Q and K/V tiles into L2 (prompts 62 -> 66 us).
 //
 // Every mbarrier wait is bounded; on timeout the CTA sets the device error word (read by
 // fg_check_device_error), drains its copies and MMAs and frees TMEM.
@@ -112,11 +116,10 @@ struct PSmem {
 static_assert(PSmem<128>::BYTES <= 227 * 1024, "shared memory per CTA");
 
 // barriers: q_full[2], q_free[2], k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2],
-// o_done[2], o_free[2], l_full[2], o_staged, o_stage_free, drain[2], item_full[4], item_free[4]
+// o_done[2], o_free[2], l_full[2], drain[2], item_full[4], item_free[4]
 constexpr int B_QFULL = 0, B_QFREE = 2, B_KFULL = 4, B_KFREE = 6, B_VFULL = 8, B_VFREE = 10,
-              B_SFULL = 12, B_PFULL = 14, B_ODONE = 16, B_OFREE = 18, B_LFULL = 20, B_OSTAGED = 22,
-              B_OSFREE = 23, B_DRAIN = 24, B_IFULL = 26, B_IFREE = B_IFULL + ITEMS,
-              NBARS = B_IFREE + ITEMS;
+              B_SFULL = 12, B_PFULL = 14, B_ODONE = 16, B_OFREE = 18, B_LFULL = 20, B_DRAIN = 22,
+              B_IFULL = 24, B_IFREE = B_IFULL + ITEMS, NBARS = B_IFREE + ITEMS;
 static_assert(NBARS * 8 + 12 + STAGES * 8 <= 512, "barrier space");
 
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -368,8 +371,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       mbar_init(bar(B_OFREE + t), 4);                  // one arrival per output warp
       mbar_init(bar(B_LFULL + t), 4);                  // one arrival per softmax warp
     }
-    mbar_init(bar(B_OSTAGED), 4);                      // one arrival per output warp
-    mbar_init(bar(B_OSFREE), 1);
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_DRAIN + 1), 1);
     for (int i = 0; i < ITEMS; ++i) {
@@ -811,8 +812,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int quarter = warp & 3;
     const int m = 32 * quarter + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16);
-    const bool leader = (warp == W_OUT) && lane == 0;  // issues the stores
-    int uses[2] = {0, 0}, nbox = 0;                    // items per Q tile, boxes stored
+    int uses[2] = {0, 0};                              // items per Q tile
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const Item* it = item_wait(n);
@@ -841,25 +841,17 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         const float inv = pos + m >= 0
                               ? 1.0f / l_buf[t * QT + m]
                               : 0.0f;
-        // O / l in 64-column boxes.  A full tile: staged in shared memory (the 128B-swizzled layout
-        // of the output map: 16-byte chunk k of row m at chunk k ^ (m % 8)) and stored by TMA.  The
-        // last tile of a sequence: each thread stores its own row.
-        const bool full = rows == QT;
+        // O / l in boxes of 64 columns x the warp's 32 rows, staged in shared memory (the
+        // 128B-swizzled layout of the output map: 16-byte chunk k of row m at chunk k ^ (m % 8))
+        // and stored by TMA, each warp by itself (one box of the tile's 128 rows, with the four
+        // warps waiting for one another: ragged prompts 62 -> 65 us).  Where a sequence ends, each
+        // thread stores its own row.
+        const bool full = rows >= 32 * quarter + 32;   // the warp's rows
 #pragma unroll 1
         for (int hb = 0; hb < NB; ++hb) {
           const uint32_t stage = smem_u32(smem + L::O_OFF);
-          if (full && nbox >= 1) {
-            // the box is free once the previous store has read it
-            if (leader) {
-              bulk_wait_read();
-              mbar_arrive(bar(B_OSFREE));
-            }
-            const bool fr = bwait(bar(B_OSFREE), (uint32_t)((nbox - 1) & 1), abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, fr)) {
-              ok = false;
-              break;
-            }
-          }
+          if (lane == 0) bulk_wait_read();              // the previous store has read the box
+          __syncwarp();
           __half2 zero = __float2half2_rn(0.0f);       // x * 0: NaN for an infinity or a NaN
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
@@ -912,12 +904,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (full) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_OSTAGED));
-            if (leader && bwait(bar(B_OSTAGED), (uint32_t)(nbox & 1), abort_flag)) {
-              tma_store_2d(&tmO, stage, it->hq * D + 64 * hb, qrow);
+            if (lane == 0) {
+              tma_store_2d(&tmO, stage + 4096 * quarter, it->hq * D + 64 * hb, qrow + 32 * quarter);
               bulk_commit();
             }
-            ++nbox;
           }
           __syncwarp();
         }
@@ -926,7 +916,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       if (lane == 0) item_done(n);
     }
     // the CTA's shared memory stays valid until its stores have completed
-    if (leader) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -959,13 +949,14 @@ cudaError_t launch_d(const PrefillWindow& a, int nsm, cudaStream_t st) {
   cudaError_t e = prepare<D>();
   if (e != cudaSuccess || (e = get_encode()) != cudaSuccess) return e;
   CUtensorMap tq, tk, tv, to;
-  auto map = [](CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int64_t stride) {
+  auto map = [](CUtensorMap* m, const uint16_t* p, int64_t cols, int64_t rows, int64_t stride,
+                int box = QT) {
     return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, (uint64_t)cols, (uint64_t)rows,
-                       (uint64_t)stride * 2, 64, QT, CU_TENSOR_MAP_SWIZZLE_128B);
+                       (uint64_t)stride * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   const int64_t wq = (int64_t)a.Hq * D, wk = (int64_t)a.Hkv * D;
   if ((e = map(&tq, a.q, wq, a.q_rows, a.q_stride)) != cudaSuccess ||
-      (e = map(&to, a.out, wq, a.q_rows, a.out_stride)) != cudaSuccess)
+      (e = map(&to, a.out, wq, a.q_rows, a.out_stride, 32)) != cudaSuccess)
     return e;
   tk = tv = tq;                             // without K/V rows no key tile is loaded
   if (a.kv_rows > 0 && ((e = map(&tk, a.k, wk, a.kv_rows, a.kv_stride)) != cudaSuccess ||
