@@ -32,10 +32,10 @@
 // bounded; on timeout the warp sets the device error word, drains its copies and stops.
 //
 // Measured (GB300, HBM copy 6.78 TB/s; bytes of the visible 4-bit K/V): 128 sequences x 56 heads of
-// 512 .. 1055 positions 132 us, 0.91 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
-// window of 1024, 52 us, 0.70 (248 MB: 9 us until the first slots are there and 5 us of uneven ends
-// beside 38 us of streaming, 5 us to merge); 4 heads per K/V head over 16 contexts of 9000 .. 32760
-// 57 us, 0.72.
+// 512 .. 1055 positions 134 us, 0.90 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
+// window of 1024, 52 us, 0.70 (248 MB: 2.5 us of planning, 4 us until the first slots are there and
+// 5 us of uneven ends beside 37 us of streaming, 4 us to merge); 4 heads per K/V head over 16
+// contexts of 9000 .. 32760 58 us, 0.71.  Warps end up to 12% behind the mean, in no fixed order.
 #include <math.h>
 
 #include <algorithm>
