@@ -32,10 +32,11 @@
 // bounded; on timeout the warp sets the device error word, drains its copies and stops.
 //
 // Measured (GB300, HBM copy 6.78 TB/s; bytes of the visible 4-bit K/V): 128 sequences x 56 heads of
-// 512 .. 1055 positions 134 us, 0.90 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
-// window of 1024, 52 us, 0.70 (248 MB: 2.5 us of planning, 4 us until the first slots are there and
-// 5 us of uneven ends beside 37 us of streaming, 4 us to merge); 4 heads per K/V head over 16
-// contexts of 9000 .. 32760 58 us, 0.71.  Warps end up to 12% behind the mean, in no fixed order.
+// 512 .. 1055 positions 132 us, 0.91 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
+// window of 1024, 51 us, 0.72 (248 MB: 2 us of planning, 4 us until the first slots are there and
+// 5 us of uneven ends beside 37 us of streaming, 4 us to merge; a plan with 64-bit divisions and
+// one per share boundary took 0.7 us more); 4 heads per K/V head over 16 contexts of 9000 .. 32760
+// 56 us, 0.73.  Warps end up to 12% behind the mean, in no fixed order.
 #include <math.h>
 
 #include <algorithm>
@@ -161,6 +162,10 @@ struct Cursor {
   int b, rs, u;
   SeqTiles s;
 };
+// The K/V head of a row set (most calls have one row set each: no division for them).
+__device__ __forceinline__ int kv_head(int rs, const Args& a) {
+  return a.nhb == 1 ? rs : rs / a.nhb;
+}
 // Moves to the next sequence that sees something, found by the whole warp 32 at a time (a batch
 // may have many empty places).
 __device__ __forceinline__ bool next_sequence(Cursor& c, const Args& a, const fg_kvcache& kv) {
@@ -296,7 +301,9 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
   // Neighbours of the order sit on one SM (they read neighbouring memory); a call with less than
   // kMinTiles for every warp has fewer shares of about that, the same few on every SM.
   const int64_t most_shares = max((int64_t)1, total / kMinTiles);
-  const int per_cta = (int)min((int64_t)kWarps, (most_shares - 1) / gridDim.x + 1);
+  const int per_cta = most_shares >= (int64_t)kWarps * gridDim.x
+                          ? kWarps
+                          : ((int)most_shares - 1) / (int)gridDim.x + 1;
   const int n = (int)min(most_shares, (int64_t)gridDim.x * per_cta);
   const Shares shares(total, n);
   const int w = blockIdx.x * per_cta + warp;
@@ -338,13 +345,13 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
       if (ic.u == ic.s.nt) {
         next_row_set(ic, a, kv);
         // its queries, needed kRing slots from here
-        const int hk = ic.rs / a.nhb;
+        const int hk = kv_head(ic.rs, a);
         const int hq = hk * a.G + (ic.rs - hk * a.nhb) * HEADS + (lane >> 3);
         if ((lane >> 3) < HEADS && hq < hk * a.G + a.G && (lane & 7) * 16 < D)
           prefetch_l2(a.q + ic.b * a.q_stride + (int64_t)hq * D + (lane & 7) * 16);
       }
       irun = run_tiles(ic.s, ic.u, min(ic.s.nt, ic.u + ileft));
-      irow = ((int64_t)ic.b * kv.H + ic.rs / a.nhb) * kv.cap + tile_pos(ic.s, ic.u);
+      irow = ((int64_t)ic.b * kv.H + kv_head(ic.rs, a)) * kv.cap + tile_pos(ic.s, ic.u);
       ic.u += irun;
       ileft -= irun;
     }
@@ -372,7 +379,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
   if (has_share && cc.u > 0) {
     const int64_t r0 = shares.first(w) - cc.u, xp = shares.first(w - 1);
     if (xp <= r0) {
-      const int hk = cc.rs / a.nhb, hb = cc.rs - hk * a.nhb;
+      const int hk = kv_head(cc.rs, a), hb = cc.rs - hk * a.nhb;
       cut.pieces = shares.share_of(r0 + cc.s.nt - 1) - (w - 1) + 1;
       cut.b = cc.b;
       cut.hq = hk * a.G + hb * HEADS;
@@ -403,7 +410,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
     const int u1 = min(cc.s.nt, cc.u + left);
     const bool whole = cc.u == 0 && u1 == cc.s.nt;
     const int seg = u1 - cc.u;
-    const int hk = cc.rs / a.nhb, hb = cc.rs - hk * a.nhb;
+    const int hk = kv_head(cc.rs, a), hb = cc.rs - hk * a.nhb;
     const int hq = hk * a.G + hb * HEADS, heads = min(HEADS, a.G - hb * HEADS);
     QFrag<D> qf;
     load_q<D, HEADS>(a.q + cc.b * a.q_stride + (int64_t)hq * D, heads, lane, a.scale_log2, qf);

@@ -137,20 +137,28 @@ FG_HD uint32_t visible_bits(int c0, int i, int window, int sinks) {
 // first(i + 1) - 1; share_of is the inverse.
 struct Shares {
   int64_t each;        // tiles per share, rounded down
-  int n, rest;         // shares; tiles left over
+  uint32_t more;       // the tiles left over, per share, times 2^32, rounded up
+  int n;               // shares
   FG_HD Shares(int64_t total, int shares) : n(shares) {
+    uint32_t rest;
     if (total < (1ll << 32)) {             // a 32-bit division takes a fraction of the time
       each = (uint32_t)total / (uint32_t)n;
-      rest = (int)((uint32_t)total % (uint32_t)n);
+      rest = (uint32_t)total - (uint32_t)each * (uint32_t)n;
     } else {
       each = total / n;
-      rest = (int)(total % n);
+      rest = (uint32_t)(total - each * n);
     }
+    // (rest 2^32 + n - 1) / n in two digits of 16 bits, as n < 2^16
+    const uint32_t hi = (rest << 16) / (uint32_t)n, left = (rest << 16) - hi * (uint32_t)n;
+    more = (hi << 16) + ((left << 16) + (uint32_t)n - 1) / (uint32_t)n;
   }
-  FG_HD int64_t first(int i) const { return each * i + (unsigned)rest * (unsigned)i / (unsigned)n; }
+  // (first(n) = total: n more lies within n of rest 2^32)
+  FG_HD int64_t first(int i) const {
+    return each * i + (int64_t)(((uint64_t)more * (uint32_t)i) >> 32);
+  }
   FG_HD int share_of(int64_t x) const {
     // a guess in binary32, then the definition
-    int i = (int)((float)x / ((float)each + (float)rest / (float)n));
+    int i = (int)((float)x / ((float)each + (float)more * 0x1p-32f));
     i = i < 0 ? 0 : (i >= n ? n - 1 : i);
     while (i > 0 && first(i) > x) --i;
     while (i + 1 < n && first(i + 1) <= x) ++i;

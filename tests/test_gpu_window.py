@@ -755,6 +755,99 @@ def test_captured_steps_replay(fg):
     assert torch.equal(cache.k_codes, eager_cache.k_codes)
 
 
+def test_offsets_past_32_bits(fg):
+    """A cache of more than 2^32 bytes of codes, written, read and attended at its far end; and fp16
+    rows more than 2^31 elements apart, which give the bits of packed ones."""
+    B, H, d, cap, n, window = 2, 2, 64, 1 << 25, 40, 33
+    h = H * d
+    x16 = fg_synth.random_fp16((n + 3, 3 * h), seed=41)
+    x = dev(x16)
+    cache = fg.KVCacheQ4(B, cap, h, H)
+    off, pos = i32([0, 3, n + 3]), i32([0, cap - n])
+    fg.fg_kv_append_q4_ragged(x[:, h:2 * h], x[:, 2 * h:], off, pos, cache)
+    back = torch.zeros((n + 3, 2 * h), dtype=torch.float16, device="cuda")
+    fg.fg_kv_read_q4_ragged(cache, off, pos, back[:, :h], back[:, h:])
+    q = x[[2, n + 2], :h].contiguous()
+    out = run_decode(fg, q, H, cache, i32([3, cap]), 0.1, window, 0)
+    fg.fg_check_device_error()
+    del cache
+    vals, mags = [], []
+    for j in (1, 2):
+        qc, a, b = OQ.quantize_g64(np.ascontiguousarray(x16[:, j * h:(j + 1) * h]))
+        vals.append(OQ.dequant_g64(qc, a, b))
+        mags.append(np.repeat(np.abs(a.astype(np.float64)) +
+                              (b.astype(np.float64) - a.astype(np.float64)), 64, axis=1))
+    assert np.array_equal(host(back), np.concatenate(vals, axis=1))
+    for row, rows in ((0, slice(0, 3)), (1, slice(3, n + 3))):
+        kk, vv, km, vm = (z[rows].reshape(-1, H, d).transpose(1, 0, 2)[None] for z in vals + mags)
+        want = OW.decode(host(q)[row:row + 1], kk, vv, [kk.shape[2]], H, window, 0,
+                         np.float32(0.1), km, vm)
+        check_rows(out[row:row + 1], dict(enumerate(want)), d, True, f"far end {row}")
+    # 20 rows 2^27 elements apart
+    wide = torch.empty((20, 1 << 27), dtype=torch.float16, device="cuda")
+    far = wide[:, :4 * h]
+    far[:, :3 * h] = x[:20]
+    o20 = i32([0, 7, 20])
+    near = torch.empty((20, h), dtype=torch.float16, device="cuda")
+    for a, o in ((x[:20], near), (far, far[:, 3 * h:])):
+        fg.fg_prefill_attn_window(a[:, :h], o20, a[:, h:2 * h], a[:, 2 * h:3 * h], o20, H, H, 0.1, o,
+                                  window=5, sinks=1)
+    assert torch.equal(near, far[:, 3 * h:])
+    caches = [fg.KVCacheQ4(2, 16, h, H) for _ in range(2)]
+    for a, c in zip((x, far), caches):
+        fg.fg_kv_append_q4_ragged(a[:20, h:2 * h], a[:20, 2 * h:3 * h], o20, i32([0, 2]), c)
+    for name in ("k_codes", "v_codes", "k_ab", "v_ab"):
+        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name)), name
+    fg.fg_check_device_error()
+
+
+def test_two_streams_at_once(fg):
+    """The calls on two streams with nothing between them, each with a cache and a workspace of its
+    own, give what they give one after another."""
+    sets = []
+    for seed, (B, Hq, H, d, lens) in enumerate(((6, 4, 4, 128, [900, 30, 1, 512, 700, 64]),
+                                                (3, 8, 2, 64, [1500, 0, 333]))):
+        cache, *_ = fill_cache(fg, B, H, d, max(lens), seed=60 + seed)
+        q16, kv16 = prefill_inputs(Hq, H, d, lens, lens, seed=70 + seed)
+        sets.append(dict(B=B, Hq=Hq, H=H, d=d, cache=cache, lens=i32(lens), off=i32(offsets(lens)),
+                         zero=i32([0] * B), q=dev(q16), kv=dev(kv16), st=torch.cuda.Stream(),
+                         ws=torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, Hq),
+                                        dtype=torch.uint8, device="cuda")))
+
+    def run(c, stream):
+        w, dv = c["H"] * c["d"], c["kv"].device
+        k, v = c["kv"][:, :w], c["kv"][:, w:2 * w]
+        res = [torch.zeros((c["B"], c["Hq"] * c["d"]), dtype=torch.float16, device=dv),
+               torch.zeros_like(c["q"]), torch.zeros_like(c["kv"])]
+        torch.cuda.synchronize()
+        yield res
+        for _ in range(4):
+            fg.fg_kv_append_q4_ragged(k, v, c["off"], c["zero"], c["cache"], stream)
+            fg.fg_decode_attn_q4kv_window(c["q"][:c["B"]], c["Hq"], c["cache"], c["lens"], 0.1,
+                                          res[0], c["ws"], 200, 3, stream)
+            fg.fg_prefill_attn_window(c["q"], c["off"], k, v, c["off"], c["Hq"], c["H"], 0.1, res[1],
+                                      200, 3, stream)
+            fg.fg_kv_read_q4_ragged(c["cache"], c["off"], c["zero"], res[2][:, :w],
+                                    res[2][:, w:2 * w], stream)
+            yield res
+
+    alone = []
+    for c in sets:
+        for res in run(c, None):
+            torch.cuda.synchronize()
+        alone.append(res)
+    both = [run(c, c["st"]) for c in sets]
+    together = [next(r) for r in both]
+    for _ in range(4):
+        for r in both:
+            next(r)
+    torch.cuda.synchronize()
+    fg.fg_check_device_error()
+    for a, b in zip(alone, together):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 def test_binding_refuses(fg):
     """What the binding refuses before a pointer is taken."""
     cache = fg.KVCacheQ4(2, 16, 128, 1)
@@ -770,7 +863,8 @@ def test_binding_refuses(fg):
         lambda: fg.fg_kv_read_q4_ragged(cache, off, pos, None, None),
         lambda: fg.fg_decode_attn_q4kv_window(x, 1, cache, pos, 0.1, x[:2]),
         lambda: fg.fg_decode_attn_q4kv_window(x[:2], 1, cache, off, 0.1, x[2:]),
-        lambda: fg.fg_decode_attn_q4kv_window(x[:2], 1, cache, pos, 0.1, x[2:], x[:1].expand(64, 128)),
+        lambda: fg.fg_decode_attn_q4kv_window(x[:2], 1, cache, pos, 0.1, x[2:],
+                                              x[:1].expand(64, 128)),
         lambda: fg.fg_prefill_attn_window(x, off, x, x[:3], off, 1, 1, 0.1, x.clone()),
         lambda: fg.fg_prefill_attn_window(x, off, x, x, off[:2], 1, 1, 0.1, x.clone()),
         lambda: fg.fg_prefill_attn_window(x, off, x.t(), x, off, 1, 1, 0.1, x.clone()),
