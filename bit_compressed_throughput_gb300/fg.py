@@ -333,15 +333,19 @@ def _extents(name: str, t, n: int):
                          f"{tuple(t.shape)}")
 
 
-def _one_device(stream, *tensors):
-    """Every tensor on the device that the call launches on: the current one, and the stream's."""
+def _stream_for(stream, *tensors) -> int:
+    """The handle to launch on, for tensors that are all on the device that the call launches on:
+    the current one, and the stream's."""
     import torch
     here = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
-    if stream is not None and stream.device.index != here:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
+    if stream.device.index != here:
         raise ValueError(f"stream on {stream.device}, but the current device is cuda:{here}")
+    return stream.cuda_stream
 
 
 def fg_kv_append_q4_ragged(k_new, v_new, row_off, pos, cache: KVCacheQ4, stream=None):
@@ -353,11 +357,11 @@ def fg_kv_append_q4_ragged(k_new, v_new, row_off, pos, cache: KVCacheQ4, stream=
         raise ValueError("k_new and v_new differ in rows or row stride")
     _extents("row_off", row_off, cache.B + 1)
     _extents("pos", pos, cache.B)
-    _one_device(stream, k_new, v_new, row_off, pos, cache.k_codes)
+    handle = _stream_for(stream, k_new, v_new, row_off, pos, cache.k_codes)
     st = cache.struct()
     _check("fg_kv_append_q4_ragged",
            lib.fg_kv_append_q4_ragged(_ptr(k_new), _ptr(v_new), stride, rows, _ptr(row_off),
-                                      _ptr(pos), C.byref(st), _stream(stream)))
+                                      _ptr(pos), C.byref(st), handle))
 
 
 def fg_kv_read_q4_ragged(cache: KVCacheQ4, row_off, pos, k_out, v_out, stream=None):
@@ -369,11 +373,11 @@ def fg_kv_read_q4_ragged(cache: KVCacheQ4, row_off, pos, k_out, v_out, stream=No
     rows, stride = outs[0]
     _extents("row_off", row_off, cache.B + 1)
     _extents("pos", pos, cache.B)
-    _one_device(stream, k_out, v_out, row_off, pos, cache.k_codes)
+    handle = _stream_for(stream, k_out, v_out, row_off, pos, cache.k_codes)
     st = cache.struct()
     _check("fg_kv_read_q4_ragged",
            lib.fg_kv_read_q4_ragged(C.byref(st), _ptr(row_off), _ptr(pos), rows, _ptr(k_out),
-                                    _ptr(v_out), stride, _stream(stream)))
+                                    _ptr(v_out), stride, handle))
 
 
 def fg_decode_attn_window_workspace_bytes(cache: KVCacheQ4, Hq: int) -> int:
@@ -391,7 +395,7 @@ def fg_decode_attn_q4kv_window(q, Hq: int, cache: KVCacheQ4, lens, scale: float,
     if nq != cache.B or no != cache.B:
         raise ValueError(f"q and out need {cache.B} rows, got {nq} and {no}")
     _extents("lens", lens, cache.B)
-    _one_device(stream, q, out, lens, ws, cache.k_codes)
+    handle = _stream_for(stream, q, out, lens, ws, cache.k_codes)
     st = cache.struct()
     if ws is not None and not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor expected")
@@ -399,7 +403,7 @@ def fg_decode_attn_q4kv_window(q, Hq: int, cache: KVCacheQ4, lens, scale: float,
     _check("fg_decode_attn_q4kv_window",
            lib.fg_decode_attn_q4kv_window(_ptr(q), q_stride, Hq, C.byref(st), _ptr(lens), window,
                                           sinks, scale, _ptr(out), o_stride, _ptr(ws), wsb,
-                                          _stream(stream)))
+                                          handle))
 
 
 def fg_prefill_attn_window(q, q_off, k, v, kv_off, Hq: int, Hkv: int, scale: float, out,
@@ -419,11 +423,11 @@ def fg_prefill_attn_window(q, q_off, k, v, kv_off, Hq: int, Hkv: int, scale: flo
     nseq = q_off.shape[0] - 1
     _extents("q_off", q_off, nseq + 1)
     _extents("kv_off", kv_off, nseq + 1)
-    _one_device(stream, q, out, k, v, q_off, kv_off)
+    handle = _stream_for(stream, q, out, k, v, q_off, kv_off)
     _check("fg_prefill_attn_window",
            lib.fg_prefill_attn_window(_ptr(q), q_stride, q_rows, _ptr(q_off), _ptr(k), _ptr(v),
                                       kv_stride, kv_rows, _ptr(kv_off), nseq, Hq, Hkv, d, window,
-                                      sinks, scale, _ptr(out), o_stride, _stream(stream)))
+                                      sinks, scale, _ptr(out), o_stride, handle))
 
 
 def fg_layernorm(x, gamma, beta, eps: float, y, stream=None):
