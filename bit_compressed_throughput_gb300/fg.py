@@ -11,6 +11,8 @@ import ctypes as C
 import os
 from typing import Optional
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfg.so")
 
@@ -120,7 +122,6 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream=None) -> Optional[int]:
-    import torch
     if stream is not None:
         return stream.cuda_stream
     # the handle of torch.cuda.current_stream(), without building a Stream object each call
@@ -139,7 +140,6 @@ class Q4Weight:
 
     @classmethod
     def from_fp16(cls, w, stream=None) -> "Q4Weight":
-        import torch
         K, N = w.shape
         codes = torch.empty((K, N // 2), dtype=torch.uint8, device=w.device)
         ab = torch.empty((K, N // 64), dtype=torch.int32, device=w.device)
@@ -155,7 +155,6 @@ class KVCacheQ4:
     int32, for K and V.  ``cap`` is rounded up to a multiple of 16 positions."""
 
     def __init__(self, B: int, cap: int, h: int, H: int, device="cuda"):
-        import torch
         cap = (int(cap) + 15) // 16 * 16
         d = h // H
         self.B, self.cap, self.h, self.H, self.d = B, cap, h, H, d
@@ -180,8 +179,6 @@ class LayerQ4:
     @classmethod
     def from_fp16(cls, params: dict, H: int, ln_eps=1e-5, device="cuda", stream=None):
         """Quantise fp16 parameters (numpy or torch, W[K][N] layout) on the device."""
-        import torch
-
         def dev(a):
             t = a if isinstance(a, torch.Tensor) else torch.from_numpy(a)
             return t.to(device=device, dtype=torch.float16).contiguous()
@@ -317,7 +314,6 @@ def fg_prefill_attn(qkv, nseq: int, s: int, H: int, d: int, scale: float, out, s
 
 def _rows(name: str, t, width: int):
     """(rows, row stride) of a 2-D fp16 tensor of rows of `width` contiguous values."""
-    import torch
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[1] != width or stride[1] != 1 or t.dtype is not torch.float16:
         raise ValueError(f"{name}: fp16 [rows][{width}] with contiguous rows expected, got "
@@ -327,7 +323,6 @@ def _rows(name: str, t, width: int):
 
 
 def _extents(name: str, t, n: int):
-    import torch
     if t.shape != (n,) or t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 [{n}] expected, got {t.dtype} "
                          f"{tuple(t.shape)}")
@@ -336,7 +331,6 @@ def _extents(name: str, t, n: int):
 def _stream_for(stream, *tensors) -> int:
     """The handle to launch on, for tensors that are all on the device that the call launches on:
     the current one, and the stream's."""
-    import torch
     here = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
@@ -489,7 +483,6 @@ class StackEngine:
     (the block schedule).  Orchestration only -- each layer step is one C call."""
 
     def __init__(self, layers, g: int, m: int, cap: int, s_max: int, device="cuda"):
-        import torch
         self.layers, self.g, self.m, self.cap = layers, g, m, cap
         L0 = layers[0]
         self.B = g * m
