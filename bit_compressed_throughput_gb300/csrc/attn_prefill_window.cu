@@ -22,11 +22,18 @@
 //   O += P V      tcgen05.mma with P from TMEM
 // TMEM: S of A and B (128 columns each), O of A and B (d columns each).  A Q tile takes part only
 // in the key tiles that it sees, and in the 16-key steps of them that it sees.
-//   warp 0       the work items and TMA producer: K tiles, V tiles and Q, rings of two each
+//   warp 0       TMA producer: K tiles, V tiles and Q, rings of two each
 //   warps 1, 2   MMA issuers of Q tiles A and B: S_t(0); then per key tile P_t(j) V_j, S_t(j + 1)
 //   warps 3-10   softmax of A and B (TMEM lanes 32 (w % 4) ..)
 //   warps 11-14  output: O_t / l of a finished block, 32 rows a warp, staged in shared memory and
 //                stored by TMA
+//   warp 15      the work items
+//
+// A sequence of up to 128 query rows has no second Q tile.  Both tiles then hold its rows, take
+// every other of its key tiles, and are joined at the output (a piece of 100 rows behind 4000 x 32
+// heads 50 -> 38 us, 64 of them behind 300 with 64 channels 92 -> 84 us, behind 30 59 -> 58 us).
+// The last block of a longer sequence is left to one tile: the other one works on the next item
+// meanwhile (ragged prompts 61 us; 63 us with such blocks split).
 //
 // Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it
 // would reach the rows of the Q tile that do not see it.  The output warps therefore test their
@@ -37,17 +44,17 @@
 //
 // The work order: blocks by descending index, for each the sequences that have one (longest first),
 // for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read
-// and checked on the device, kMaxSeqs sequences per launch.  The producer works the items out and
-// hands them to the other warps through a ring in shared memory, ahead of the loads: the softmax
-// warps have no registers to spare for it.
+// and checked on the device, kMaxSeqs sequences per launch.  A warp of its own works the items out
+// and hands them to the others through a ring in shared memory (by the producer, between its loads:
+// the 8k window 249 us instead of 246).
 //
 // What bounds it: the turn that a Q tile takes -- P V and S (16 MMAs, 1024 cycles of tensor work),
 // the softmax (about 400 cycles for the maximum, 900 for P: 128 exponentials a thread, 512 cycles
 // of the special-function unit), and the barriers between -- with two Q tiles taking turns: 3200
 // cycles for a pair of key tiles of both, of which the tensor core works 2050.  Two sequences of
 // 8192, 32 heads, no window: 800 us, 1376 TFLOP/s (0.72 of the measured burst rate); a window of
-// 1024 with 4 first positions over two documents of 8k, grouped heads: 252 us, 940 TFLOP/s of
-// visible pairs; ragged prompts of 300 .. 512: 62 us, where the first loads (10000 cycles to the
+// 1024 with 4 first positions over two documents of 8k, grouped heads: 247 us, 960 TFLOP/s of
+// visible pairs; ragged prompts of 300 .. 512: 61 us, where the first loads (10000 cycles to the
 // first S), the masked tiles and the turns of short blocks count.  A masked tile's softmax takes
 // 2700 cycles instead of 1250.  Steps that brought it there, on the 8k window: one thread per row
 // instead of two that exchange maxima 345 -> 318 us, an issuer warp per Q tile and key steps from
@@ -79,11 +86,12 @@ namespace {
 
 constexpr int QB = 2 * QT;                  // query rows per block
 constexpr int STAGES = 2;                   // K/V ring
-constexpr int THREADS = 15 * 32;
+constexpr int THREADS = 16 * 32;
 constexpr int W_MMA = 1;                    // MMA issuers: warps 1 and 2, one per Q tile
 constexpr int W_SM = 3;                     // softmax warps 3..10: Q tile (w - 3) / 4, TMEM lane
                                             // quarter w % 4
 constexpr int W_OUT = 11;                   // first output warp (11..14)
+constexpr int W_ITEM = 15;                  // work items
 constexpr uint32_t TMEM_COLS = 512;
 constexpr long long kWaitCycles = 1ll << 36;   // attend_rows may keep the other warps waiting
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
@@ -106,8 +114,8 @@ struct PSmem {
   static constexpr int K_OFF = 2 * TILE;               // K stages
   static constexpr int V_OFF = K_OFF + STAGES * TILE;  // V stages
   static constexpr int O_OFF = V_OFF + STAGES * TILE;  // one output box
-  static constexpr int L_OFF = O_OFF + BOX;            // row sums l [tile][row]
-  static constexpr int NQ_OFF = L_OFF + 2 * QT * 4;    // the sequences' query rows (start only)
+  static constexpr int L_OFF = O_OFF + BOX;            // row sums l [tile][row], maxima the same
+  static constexpr int NQ_OFF = L_OFF + 4 * QT * 4;    // the sequences' query rows (start only)
   static constexpr int BAR_OFF = NQ_OFF + kMaxSeqs * 4;
   static constexpr int ITEM_OFF = BAR_OFF + 512;
   static constexpr int SEQ_OFF = ITEM_OFF + ITEMS * 64;  // sequences, longest first
@@ -151,8 +159,8 @@ __device__ __forceinline__ float in_range(float y) {
   return fabsf(y) < 66000.0f ? fminf(fmaxf(y, -65504.0f), 65504.0f) : y;
 }
 
-// Rows on their own, by a whole warp: up to kRowsAtOnce of its 32 (the bits of `rows`), the first of
-// which is row qrow at position pos of a sequence whose K/V rows start at k0; lane l returns
+// Rows on their own, by a whole warp: up to kRowsAtOnce of its 32 (the bits of `rows`), the first
+// of which is row qrow at position pos of a sequence whose K/V rows start at k0; lane l returns
 // channels 64 box + 2l and the next.  Scores are computed a key per lane, values a channel pair per
 // lane; what a row does not see takes no part in it.  (4 rows of 16384 keys: 3 ms.)
 constexpr int kRowsAtOnce = 4;
@@ -247,6 +255,66 @@ __device__ __noinline__ void attend_rows(const PrefillWindow& a, int qrow, int h
   }
 }
 
+// The rows of an item whose key tiles both Q tiles worked on, 32 by a warp: `rows` of them are the
+// sequence's, lane r has row qrow + r in O of A and B (D columns each from o_addr on) and their
+// sums and maxima in l.  (O_A 2^(m_A - m) + O_B 2^(m_B - m)) / l, l joined alike.  A called
+// function: the output of unsplit items keeps its registers.
+template <int D>
+__device__ __noinline__ void store_split(const PrefillWindow& w, int qrow, int rows, int hq, int k0,
+                                         int pos, uint32_t o_addr, const float* l,
+                                         uint32_t o_free) {
+  const int lane = threadIdx.x & 31;
+  const float ma = l[2 * QT + lane], mb = l[3 * QT + lane], mx = fmaxf(ma, mb);
+  const float wa = ex2(ma - mx), wb = ex2(mb - mx);
+  const float sum = l[lane] * wa + l[QT + lane] * wb;
+  const bool sees = pos + lane >= 0;
+  const float fa = sees ? wa / sum : 0.0f, fb = sees ? wb / sum : 0.0f;
+  uint16_t* out = w.out + (int64_t)(qrow + lane) * w.out_stride + (int64_t)hq * D;
+  unsigned redo[2] = {0, 0};
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float a[32], b[32];
+    tmem_ld32(o_addr + 32 * c, a);
+    tmem_ld32(o_addr + D + 32 * c, b);
+    tmem_wait_ld_dep(a);
+    tmem_wait_ld_dep(b);
+    __half2 zero = __float2half2_rn(0.0f);  // x * 0: NaN for an infinity or a NaN
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 8 * k + 2 * e;
+        p[e] = pack_h2(fmaf(b[i], fb, a[i] * fa), fmaf(b[i + 1], fb, a[i + 1] * fa));
+        zero = __hfma2(*reinterpret_cast<const __half2*>(&p[e]), __float2half2_rn(0.0f), zero);
+      }
+      if (lane < rows)
+        reinterpret_cast<uint4*>(out + 32 * c)[k] = make_uint4(p[0], p[1], p[2], p[3]);
+    }
+    redo[c >> 1] |= __ballot_sync(0xFFFFFFFFu, lane < rows && (__hisnan(__low2half(zero)) ||
+                                                               __hisnan(__high2half(zero))));
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane < 2) mbar_arrive(o_free + 8 * lane);        // of A and of B
+#pragma unroll 1
+  for (int box = 0; box < D / 64; ++box) {
+    for (unsigned left = box ? redo[1] : redo[0]; left;) {
+      float2 x[kRowsAtOnce];
+      attend_rows<D>(w, qrow, hq, k0, pos, left, box, x);
+#pragma unroll
+      for (int r = 0; r < kRowsAtOnce; ++r) {
+        if (!left) break;
+        *reinterpret_cast<uint32_t*>(w.out + (int64_t)(qrow + __ffs(left) - 1) * w.out_stride +
+                                     (int64_t)hq * D + 64 * box + 2 * lane) =
+            pack_h2(x[r].x, x[r].y);
+        left &= left - 1;
+      }
+    }
+  }
+  __syncwarp();
+}
+
 struct PArgs {
   PrefillWindow w;
   int s0, ns;                               // sequences s0 .. s0 + ns - 1 of the call
@@ -274,6 +342,8 @@ struct Item {
   int krow;                                 // the sequence's first K/V row
   int pos;                                  // position of the block's first row (may be negative)
   KeyTiles t[2], u;                         // the Q tiles' key tiles, and their union
+  int split;                                // the Q tiles hold the same rows, and tile t works on
+                                            // the key tiles number t, t + 2, .. of them
 };
 static_assert(sizeof(Item) <= 64, "item ring");
 // The place of an item in the work order.
@@ -319,6 +389,8 @@ __device__ __forceinline__ Item item_at(const Cursor& c, const Seq* seqs, const 
   it.t[0] = key_tiles(q0, s.nq, s.nk, w.window, w.sinks);
   it.t[1] = key_tiles(q0 + QT, s.nq, s.nk, w.window, w.sinks);
   it.u = either(it.t[0], it.t[1]);
+  it.split = s.nq <= QT && it.u.count() >= 2;   // (what it gains: at the top)
+  if (it.split) it.t[1] = it.t[0];
   return it;
 }
 
@@ -375,7 +447,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
     mbar_init(bar(B_DRAIN + 1), 1);
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(bar(B_IFULL + i), 1);
-      mbar_init(bar(B_IFREE + i), 2 + 8 + 4);         // the MMA issuers, softmax and output warps
+      mbar_init(bar(B_IFREE + i), 1 + 2 + 8 + 4);     // every other warp
     }
     *abort_flag = 0;
     *live = 0;
@@ -430,24 +502,16 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
   auto item_done = [&](int n) { mbar_arrive(bar(B_IFREE + n % ITEMS)); };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ items and TMA producer
+    // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       int kvg = 0, qn = 0, kn = 0, vn = 0;             // key tiles, Q pairs, K and V tiles issued
       int qt[2] = {0, 0};                              // Q tiles A and B issued
       bool ok = true;
-      Cursor cur = first_item(seqs, nseq);
-      bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
       for (int n = 0; ok; ++n) {
-        if (n >= ITEMS &&
-            !bwait(bar(B_IFREE + n % ITEMS), (uint32_t)((n / ITEMS - 1) & 1), abort_flag))
-          break;
-        Item it;
-        it.hq = -1;
-        if (have) it = item_at(cur, seqs, w);
-        *item_slot(n) = it;
-        mbar_arrive(bar(B_IFULL + n % ITEMS));
-        if (!have) break;
-        have = advance(cur, gridDim.x, seqs, nseq, w.Hq);
+        const Item* slot = item_wait(n);
+        if (slot == nullptr || slot->hq < 0) break;
+        const Item it = *slot;
+        item_done(n);
         const int nkv = it.u.count();
         if (nkv == 0) continue;
         const int hk = it.hq / (w.Hq / w.Hkv);
@@ -469,6 +533,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           // the 16-key steps that the Q tiles take of the tile, a byte each: s0 | s1 << 4 (s1 0:
           // none), and kLastTile when they take none of a later one
           auto steps = [&](int t) -> unsigned {
+            if (it.split) {
+              const bool now = (j & 1) == t;
+              const unsigned last = j + 1 + now < nkv ? 0u : kLastTile;
+              if (!now) return last;
+              const KeySteps k = key_steps(it.u.tile(j), it.pos, it.pos + it.rows - 1, w.window,
+                                           w.sinks);
+              return (unsigned)(k.s0 | k.s1 << 4) | last;
+            }
             const int tile = it.u.tile(j), lo = it.pos + t * QT;
             const unsigned last = (it.t[t].count() == 0 || tile >= it.t[t].te - 1) ? kLastTile : 0u;
             if (!it.t[t].has(tile)) return last;
@@ -491,7 +563,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
               mbar_expect_tx(bar(B_QFULL + t), (uint32_t)L::TILE);
               for (int c = 0; c < NB; ++c)
                 tma_load_2d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ,
-                            it.hq * D + 64 * c, it.qrow + t * QT, bar(B_QFULL + t));
+                            it.hq * D + 64 * c, it.qrow + (it.split ? 0 : t * QT),
+                            bar(B_QFULL + t));
               qt[t] = qn + 1;
             }
             if (!ok) break;
@@ -653,20 +726,21 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       const volatile Item* it = item_wait(n);          // read where needed: no registers for it
       if (!__all_sync(0xFFFFFFFFu, it != nullptr) || it->hq < 0) break;
       const int nt = it->t[t].ns + it->t[t].te - it->t[t].tw;
+      const int step = 1 + it->split, row0 = step == 1 ? t * QT : 0;
       if (nt == 0) {
         if (lane == 0) item_done(n);
         continue;
       }
       // (rows behind the sequence: no score of theirs moves the reference of the warp's rows)
-      float m_ref = t * QT + m < it->rows ? -INFINITY : INFINITY, l_sum = 0.0f;
-      for (int j = 0; j < nt; ++j, ++sc) {
+      float m_ref = row0 + m < it->rows ? -INFINITY : INFINITY, l_sum = 0.0f;
+      for (int j = step == 1 ? 0 : t; j < nt; j += step, ++sc) {
         // masked: some row of the Q tile does not see every key of the tile (warp-uniform); ahead:
         // the position of the Q tile's first row less the key tile's first position
         const int ns = it->t[t].ns;
-        const int k0 = (j < ns ? j : j - ns + it->t[t].tw) * KT, ahead = it->pos + t * QT - k0;
+        const int k0 = (j < ns ? j : j - ns + it->t[t].tw) * KT, ahead = it->pos + row0 - k0;
         const bool masked = ahead < KT - 1 ||
                             (w.window != 0 && k0 + KT > w.sinks &&
-                             ahead + min(QT, it->rows - t * QT) > w.window);
+                             ahead + min(QT, it->rows - row0) > w.window);
         const bool got = bwait(bar(B_SFULL + t), (uint32_t)(sc & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
@@ -725,7 +799,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           // item's earlier tiles: those MMAs were issued, and so are done, before this S
           const float m_new = fmaxf(m_ref, mx);
           const float alpha = (m_ref == -INFINITY) ? 0.0f : ex2(m_ref - m_new);
-          if (j > 0) {
+          if (j >= step) {
 #pragma unroll 1
             for (int c16 = 0; c16 < D / 16; ++c16) {
               uint32_t wv[16];
@@ -800,12 +874,31 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
       }
       l_buf[t * QT + m] = l_sum;
+      if (it->split) l_buf[(2 + t) * QT + m] = m_ref;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(B_LFULL + t));
         item_done(n);
       }
       ++uses;
+    }
+  } else if (warp == W_ITEM) {
+    // ------------------------------------------------------------ work items
+    if (lane == 0) {
+      Cursor cur = first_item(seqs, nseq);
+      bool have = advance(cur, blockIdx.x, seqs, nseq, w.Hq);
+      for (int n = 0;; ++n) {
+        if (n >= ITEMS &&
+            !bwait(bar(B_IFREE + n % ITEMS), (uint32_t)((n / ITEMS - 1) & 1), abort_flag))
+          break;
+        Item it;
+        it.hq = -1;
+        if (have) it = item_at(cur, seqs, w);
+        *item_slot(n) = it;
+        mbar_arrive(bar(B_IFULL + n % ITEMS));
+        if (!have) break;
+        have = advance(cur, gridDim.x, seqs, nseq, w.Hq);
+      }
     }
   } else if (warp >= W_OUT) {
     // ------------------------------------------------------------ output of both Q tiles
@@ -833,6 +926,21 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         got = got && bwait(bar(B_ODONE + t), (uint32_t)(uses[t] & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
+          break;
+        }
+        if (it->split) {
+          got = bwait(bar(B_LFULL + 1), (uint32_t)(uses[1] & 1), abort_flag);
+          got = got && bwait(bar(B_ODONE + 1), (uint32_t)(uses[1] & 1), abort_flag);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          ++uses[0];
+          ++uses[1];
+          store_split<D>(w, qrow + 32 * quarter, rows - 32 * quarter, it->hq, it->krow,
+                         pos + 32 * quarter, lane_addr + o_col(0), l_buf + 32 * quarter,
+                         bar(B_OFREE));
           break;
         }
         tc_fence_after();

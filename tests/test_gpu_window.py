@@ -542,6 +542,31 @@ def test_prefill_window_masked_positions_may_hold_anything(fg, d, window, sinks,
     assert (o[qo[-1]:] == 7.0).all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(2, 1, 64), (3, 3, 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 40), (1, 0), (129, 400)])
+def test_prefill_window_few_queries(fg, Hq, Hkv, d, window, sinks):
+    """Up to 128 query rows behind many keys, whose tiles two halves of the kernel share; beside
+    them a longer sequence, an empty one and one of a single tile."""
+    nq, nk = [1, 128, 127, 33, 0, 300, 100, 60], [1000, 257, 129, 700, 50, 500, 1157, 90]
+    w = Hkv * d
+    q16, kv16 = prefill_inputs(Hq, Hkv, d, nq, nk, seed=d + window, spare=9)
+    qo, ko = offsets(nq), offsets(nk)
+    kv = dev(kv16)
+    scale = 1.0 / np.sqrt(d)
+    out = run_prefill(fg, dev(q16), i32(qo), kv[:, :w], kv[:, w:2 * w], i32(ko), Hq, Hkv, scale,
+                      window, sinks)
+    fg.fg_check_device_error()
+    want = OW.prefill(q16, kv16[:, :w], kv16[:, w:2 * w], qo, ko, Hq, Hkv, window, sinks,
+                      np.float32(scale))
+    check_rows(out[:, :Hq * d], want, d, False, "few queries")
+    assert (host(out)[qo[-1]:] == 7.0).all() and (host(out)[:, Hq * d:] == 7.0).all()
+
+
+@pytest.mark.parametrize("d,window,sinks,past", [(64, 0, 0, 300), (128, 200, 30, 800)])
+def test_prefill_window_few_queries_masked_positions(fg, d, window, sinks, past):
+    test_prefill_window_masked_positions_may_hold_anything(fg, d, window, sinks, past)
+
+
 @pytest.mark.parametrize("d,window", [(64, 0), (128, 90)])
 @pytest.mark.parametrize("nk", [[1, 130, 127, 300], [17, 255, 33, 129]])
 def test_prefill_window_rows_behind_hold_anything(fg, d, window, nk):
