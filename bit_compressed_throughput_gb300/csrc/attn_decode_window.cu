@@ -32,11 +32,11 @@
 // bounded; on timeout the warp sets the device error word, drains its copies and stops.
 //
 // Measured (GB300, HBM copy 6.78 TB/s; bytes of the visible 4-bit K/V): 128 sequences x 56 heads of
-// 512 .. 1055 positions 132 us, 0.91 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
+// 512 .. 1055 positions 134 us, 0.90 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
 // window of 1024, 51 us, 0.72 (248 MB: 2 us of planning, 4 us until the first slots are there and
 // 5 us of uneven ends beside 37 us of streaming, 4 us to merge; a plan with 64-bit divisions and
 // one per share boundary took 0.7 us more); 4 heads per K/V head over 16 contexts of 9000 .. 32760
-// 56 us, 0.73.  Warps end up to 12% behind the mean, in no fixed order.
+// 57 us, 0.72.  Warps end up to 12% behind the mean, in no fixed order.
 #include <math.h>
 
 #include <algorithm>
@@ -60,6 +60,7 @@ using q4attn::movtrans;
 
 constexpr int kSub = 2;                   // tiles per ring slot
 constexpr int kSlotPos = kSub * kTilePos;
+constexpr int kRecentre = 8;              // slots between corrections of the sums (a power of 2)
 constexpr int kMinTiles = 2;              // per warp of a small call: one slot (32 heads x 260
                                           // positions: 7.8 us; with 4 9.3, with 6 8.8)
 constexpr long long kWaitCycles = 1ll << 32;
@@ -417,13 +418,14 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
 
     // head tig % HEADS: the part's rows (l, asum) and columns (acc)
     float m_run = -INFINITY, l_run = 0.0f;
-    float acc[2 * NW][4], asum[NG];
+    float acc[2 * NW][4], asum[NG], wsum[NG];
 #pragma unroll
     for (int u = 0; u < 2 * NW; ++u)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[u][c] = 0.0f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) asum[g] = 0.0f;
+    for (int g = 0; g < NG; ++g) asum[g] = wsum[g] = 0.0f;
+    int slots = 0;
 
     // One slot: scores of every tile, one softmax step, the values of every tile.  MASK: positions
     // that are not visible, and tiles the copy left out (whose stale bytes are still codes), get
@@ -491,7 +493,10 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         const float corr = (m_run == -INFINITY) ? 0.0f : ex2(m_run - mx);
         l_run *= corr;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) asum[g] *= corr;
+        for (int g = 0; g < NG; ++g) {
+          asum[g] *= corr;
+          wsum[g] *= corr;
+        }
 #pragma unroll
         for (int u = 0; u < 2 * NW; ++u)                // columns 2 tig, 2 tig + 1: the same head
 #pragma unroll
@@ -516,6 +521,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
           const float2 ab = unpack_h2(valid[j] ? va[g] : 0u);
           w[g] = p15 * (ab.y - ab.x);
           asum[g] = fmaf(p, ab.x, asum[g]);
+          wsum[g] += w[g];
         }
         // Outputs are means, near 0, of values a + s c with a < 0, and show an fp16 weight's error
         // several times over (relative error of the outputs 6.6e-4).  So the weight's remainder
@@ -556,6 +562,29 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
       }
     };
 
+    // Codes are not negative: sums of them grow with the positions, while the output, a mean of
+    // values of both signs, gets smaller, and the products' additions truncate.  So every kRecentre
+    // slots the codes' middle times the weights since then moves from these sums to those of the
+    // minima, binary32 additions of a lane's own.  Relative error of outputs over 65536 positions a
+    // warp: 3.5e-4 (without it 6e-2); 1% of the time.
+    auto recentre = [&]() {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        asum[g] = fmaf(7.5f, wsum[g], asum[g]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)               // the rows of the part
+          wsum[g] += __shfl_xor_sync(0xFFFFFFFFu, wsum[g], o);
+      }
+#pragma unroll
+      for (int u = 0; u < 2 * NW; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)                    // column 2 tig + (c & 1): the lane's head
+          acc[u][c] = fmaf(c < 2 ? -7.5f / 16777216.0f : -7.5f / 1048576.0f,
+                           wsum[NG == 2 ? c & 1 : 0], acc[u][c]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) wsum[g] = 0.0f;
+    };
+
     while (cc.u < u1 && ok) {
       int run = run_tiles(cc.s, cc.u, u1), ts = tile_pos(cc.s, cc.u);
       cc.u += run;
@@ -570,6 +599,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
           process(slot, ts, min(run, kSub), std::true_type{});
         __syncwarp();                       // every lane has read the slot: refill it
         issue();
+        if ((++slots & (kRecentre - 1)) == 0) recentre();
         ++consumed;
         if (++cs == kRing) {
           cs = 0;

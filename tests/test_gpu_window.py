@@ -362,6 +362,46 @@ def test_decode_window_many_sequences(fg, B):
     check_rows(out, dict(enumerate(want)), d, True, "many sequences")
 
 
+@pytest.mark.parametrize("G", [1, 4])
+def test_decode_window_long_shares(fg, G):
+    """65536 positions a warp: what the sums lose does not grow with the length.
+
+    Against the values a + q (b - a)/15 that the kernel sums, the relative error of a row has the
+    output's rounding (uniform within half a step of 2^-11 .. 2^-10 relative: 2.1e-4), with G = 4
+    that of the fp16 weights (they stand at random before values that sum to the output as the
+    rounded ones do: 2^-11/sqrt(3) = 2.8e-4), and the truncation of the 16 additions between two
+    corrections, half of 2^-24 a step on average, times the ratio of the uncorrected sums (7.5/15
+    of the width, 2.3) to the output's size (0.009): 16 * 2^-25 * 255 / 2 = 6e-5.  Together 3.6e-4;
+    the bound is three times that.  Sums that truncate all the way lose 1.5e-2 and more."""
+    B, H, d, n = 58, 32, 128, 65536
+    g = torch.Generator(device="cuda")
+    g.manual_seed(19)
+    cache = fg.KVCacheQ4(B, n, H * d, H)
+    some = torch.randn(1 << 20, 2, generator=g, device="cuda").abs() * 0.3 + 2.0
+    some = (some * torch.tensor([-1.0, 1.0], device="cuda")).half().view(torch.int32).view(-1)
+    for c in (cache.k_codes, cache.v_codes):
+        c.random_(0, 256, generator=g)
+    for t in (cache.k_ab, cache.v_ab):
+        t.copy_(some[torch.randint(0, 1 << 20, t.shape, generator=g, device="cuda")])
+    q = torch.randn(B, H * G * d, generator=g, device="cuda").half()
+    out = run_decode(fg, q, H * G, cache, i32([n] * B), d ** -0.5, 0, 0)
+    fg.fg_check_device_error()
+
+    def restored(codes, ab):
+        x = torch.stack([codes & 15, codes >> 4], -1).view(n, d // 64, 64).double()
+        lo, hi = ab.contiguous().view(torch.float16).view(n, d // 64, 2).double().split(1, -1)
+        return (lo + x * ((hi - lo) / 15)).view(n, d)
+
+    for b, h in ((0, 0), (17, 5), (B - 1, H - 1)):
+        k = restored(cache.k_codes[b, h], cache.k_ab[b, h])
+        v = restored(cache.v_codes[b, h], cache.v_ab[b, h])
+        for hq in range(h * G, h * G + G):
+            at = slice(hq * d, hq * d + d)
+            want = torch.softmax(k @ q[b, at].double() * d ** -0.5, 0) @ v
+            rel = ((out[b, at].double() - want).norm() / want.norm()).item()
+            assert rel <= 1.1e-3, (b, hq, rel)
+
+
 @pytest.mark.parametrize("B,G", [(40, 1), (700, 4)])
 def test_decode_window_mostly_empty_batch(fg, B, G):
     """A few sequences among many empty places, with runs of more than 32 of those."""
@@ -815,8 +855,8 @@ def test_offsets_past_32_bits(fg):
     o20 = i32([0, 7, 20])
     near = torch.empty((20, h), dtype=torch.float16, device="cuda")
     for a, o in ((x[:20], near), (far, far[:, 3 * h:])):
-        fg.fg_prefill_attn_window(a[:, :h], o20, a[:, h:2 * h], a[:, 2 * h:3 * h], o20, H, H, 0.1, o,
-                                  window=5, sinks=1)
+        fg.fg_prefill_attn_window(a[:, :h], o20, a[:, h:2 * h], a[:, 2 * h:3 * h], o20, H, H, 0.1,
+                                  o, window=5, sinks=1)
     assert torch.equal(near, far[:, 3 * h:])
     caches = [fg.KVCacheQ4(2, 16, h, H) for _ in range(2)]
     for a, c in zip((x, far), caches):
@@ -850,8 +890,8 @@ def test_two_streams_at_once(fg):
             fg.fg_kv_append_q4_ragged(k, v, c["off"], c["zero"], c["cache"], stream)
             fg.fg_decode_attn_q4kv_window(c["q"][:c["B"]], c["Hq"], c["cache"], c["lens"], 0.1,
                                           res[0], c["ws"], 200, 3, stream)
-            fg.fg_prefill_attn_window(c["q"], c["off"], k, v, c["off"], c["Hq"], c["H"], 0.1, res[1],
-                                      200, 3, stream)
+            fg.fg_prefill_attn_window(c["q"], c["off"], k, v, c["off"], c["Hq"], c["H"], 0.1,
+                                      res[1], 200, 3, stream)
             fg.fg_kv_read_q4_ragged(c["cache"], c["off"], c["zero"], res[2][:, :w],
                                     res[2][:, w:2 * w], stream)
             yield res
