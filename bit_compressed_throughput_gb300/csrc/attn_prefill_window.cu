@@ -93,7 +93,9 @@ constexpr int W_SM = 3;                     // softmax warps 3..10: Q tile (w - 
 constexpr int W_OUT = 11;                   // first output warp (11..14)
 constexpr int W_ITEM = 15;                  // work items
 constexpr uint32_t TMEM_COLS = 512;
-constexpr long long kWaitCycles = 1ll << 36;   // attend_rows may keep the other warps waiting
+constexpr long long kWaitCycles = 1ll << 36;   // attend_rows may keep the other warps waiting (64
+                                               // rows of 10^6 keys: 3 s)
+constexpr long long kDrainCycles = 1ll << 32;  // for copies and products in flight
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 constexpr int BOX = QT * 128;               // bytes of one 64-column x 128-row box
 constexpr int kMaxSeqs = 384;               // sequences per launch
@@ -146,7 +148,7 @@ __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile in
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity)) {
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > kDrainCycles) {
       atomicOr(&g_prefill_window_error, kErrDrain);
       return;
     }
