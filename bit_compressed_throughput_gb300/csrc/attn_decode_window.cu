@@ -67,6 +67,24 @@ constexpr int kMinTiles = 2;              // per warp of a small call: one slot 
 constexpr long long kWaitCycles = 1ll << 32;
 constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 
+// The weights p (b - a) / 15 of the values are rounded to fp16, so they are taken times a power of
+// two f per (head, group), which leaves the sums again at their end.  t = (b - a) f is at most
+// kWide: with p <= 4 a weight is at most 2^15.  A wider position sets f anew, to t < 2^14, so that
+// a 7 times wider one still fits; f starts where the narrowest group's t is past kWide.  Weights
+// down to 2^-23 of the widest position's are then normal numbers.  (Unscaled, the weights of a position 12
+// nats below the largest score, or of values near 0.003, were subnormal or 0, and their codes' part
+// of the values lost, all with one sign: 8192 positions 14 nats below a first one, values of 0.05:
+// relative error 2.0e-2, now below 1.2e-3; 1 to 2% of the time.)
+constexpr float kWide = 122880.0f, kFirstF = 0x1p60f;
+__device__ __forceinline__ float inverse_f(float f) {    // of a power of two
+  return __uint_as_float(0x7F000000u - __float_as_uint(f));
+}
+// The power of two that brings t, above kWide and finite, into 2^13 .. 2^14; 1 for any other t.
+__device__ __forceinline__ float narrow(float t) {
+  return t > kWide && t < INFINITY ? __uint_as_float((267u - (__float_as_uint(t) >> 23)) << 23)
+                                   : 1.0f;
+}
+
 // One CTA per SM.  Its rings hold about 110 KB, what the memory system needs in flight (152 x 110
 // KB = 17 MB, 2.4 us of its rate); with twice as much the SMs advance less evenly and the last ones
 // finish later (128 sequences of 784 positions, 56 heads: 173 us with 16 warps x 3 slots, 152 us
@@ -419,13 +437,16 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
 
     // head tig % HEADS: the part's rows (l, asum) and columns (acc)
     float m_run = -INFINITY, l_run = 0.0f;
-    float acc[2 * NW][4], asum[NG], wsum[NG];
+    float acc[2 * NW][4], asum[NG], wsum[NG], f[NG];   // acc and wsum: times f
 #pragma unroll
     for (int u = 0; u < 2 * NW; ++u)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[u][c] = 0.0f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) asum[g] = wsum[g] = 0.0f;
+    for (int g = 0; g < NG; ++g) {
+      asum[g] = wsum[g] = 0.0f;
+      f[g] = kFirstF;
+    }
     int slots = 0;
 
     // One slot: scores of every tile, one softmax step, the values of every tile.  MASK: positions
@@ -481,32 +502,50 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         const float s = fmaf(dot, ck, off);
         sc[j] = valid[j] ? s : -INFINITY;
       }
-      // The reference maximum moves only when a score exceeds it by more than 2^2, so that p <= 4
-      // and the fp16 weight p (b - a) / 15 cannot overflow (131008 / 15 * 4 < 65504).
-      float mloc = sc[0];
+      // The reference maximum moves only when a score exceeds it by more than 2^2, so that p <= 4;
+      // the weights' scale only for a position wider than kWide.
+      float mloc = sc[0], tloc[NG] = {};
 #pragma unroll
       for (int j = 1; j < RPL; ++j) mloc = fmaxf(mloc, sc[j]);
-      if (__any_sync(0xFFFFFFFFu, mloc > m_run + 2.0f)) {
-        float mx = fmaxf(mloc, m_run);
 #pragma unroll
-        for (int o = HEADS; o < 32; o <<= 1)            // over parts and gid
+      for (int j = 0; j < RPL; ++j) {
+        uint32_t va[NG];
+        load_words<NG>(slot + R::VAB_OFF + (8 * (part * RPL + j) + gid) * R::ROW_AB, va);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 ab = unpack_h2(valid[j] ? va[g] : 0u);
+          tloc[g] = fmaxf(tloc[g], (ab.y - ab.x) * f[g]);
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu,
+                     mloc > m_run + 2.0f || fmaxf(tloc[0], tloc[NG - 1]) > kWide)) {
+        float mx = fmaxf(mloc, m_run), r[NG];
+#pragma unroll
+        for (int o = HEADS; o < 32; o <<= 1) {          // over parts and gid
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            tloc[g] = fmaxf(tloc[g], __shfl_xor_sync(0xFFFFFFFFu, tloc[g], o));
+        }
         const float corr = (m_run == -INFINITY) ? 0.0f : ex2(m_run - mx);
         l_run *= corr;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
+          const float n = narrow(tloc[g]);
+          f[g] *= n;
+          r[g] = corr * n;
           asum[g] *= corr;
-          wsum[g] *= corr;
+          wsum[g] *= r[g];
         }
 #pragma unroll
         for (int u = 0; u < 2 * NW; ++u)                // columns 2 tig, 2 tig + 1: the same head
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[u][c] *= corr;
+          for (int c = 0; c < 4; ++c) acc[u][c] *= r[NG == 2 ? c & 1 : 0];
         m_run = mx;
       }
       const float m_ref = (m_run == -INFINITY) ? 0.0f : m_run;
-      // weights p (b - a) / 15 of both groups, transposed: column (part, head, group) x the half's
-      // 8 rows; and their second terms
+      // weights p (b - a) / 15 of both groups, times f, transposed: column (part, head, group) x
+      // the half's 8 rows; and their second terms
       uint32_t wt[RPL], lt[RPL];
 #pragma unroll
       for (int j = 0; j < RPL; ++j) {
@@ -520,7 +559,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           const float2 ab = unpack_h2(valid[j] ? va[g] : 0u);
-          w[g] = p15 * (ab.y - ab.x);
+          w[g] = p15 * ((ab.y - ab.x) * f[g]);
           asum[g] = fmaf(p, ab.x, asum[g]);
           wsum[g] += w[g];
         }
@@ -532,8 +571,9 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         const uint32_t wh = pack_h2(w[0], NG == 2 ? w[NG - 1] : w[0]);
         const float2 wr = unpack_h2(wh);
         if (NP == 1) {
-          asum[0] = fmaf(7.5f, w[0] - wr.x, asum[0]);
-          if (NG == 2) asum[NG - 1] = fmaf(7.5f, w[NG - 1] - wr.y, asum[NG - 1]);
+          asum[0] = fmaf(7.5f * inverse_f(f[0]), w[0] - wr.x, asum[0]);
+          if (NG == 2)
+            asum[NG - 1] = fmaf(7.5f * inverse_f(f[NG - 1]), w[NG - 1] - wr.y, asum[NG - 1]);
         } else {
           const uint32_t wl = pack_h2(w[0] - wr.x, NG == 2 ? w[NG - 1] - wr.y : w[0] - wr.x);
           lt[j] = movtrans(__shfl_xor_sync(0xFFFFFFFFu, wl, 2));
@@ -571,7 +611,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
     auto recentre = [&]() {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        asum[g] = fmaf(7.5f, wsum[g], asum[g]);
+        asum[g] = fmaf(7.5f * inverse_f(f[g]), wsum[g], asum[g]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)               // the rows of the part
           wsum[g] += __shfl_xor_sync(0xFFFFFFFFu, wsum[g], o);
@@ -622,11 +662,12 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
     const int g = (NG == 2) ? (gid >> 2) : 0;
     const float A = (NG == 2 && g) ? asum[NG - 1] : asum[0];
     const int cbase = 8 * NW * (gid >> 1) + 4 * (gid & 1);
+    const float unit = inverse_f(g ? f[NG - 1] : f[0]);
     float2 y[2 * NW];
 #pragma unroll
     for (int u = 0; u < 2 * NW; ++u)
-      y[u] = make_float2((g ? acc[u][1] : acc[u][0]) * 16777216.0f,
-                         (g ? acc[u][3] : acc[u][2]) * 1048576.0f);
+      y[u] = make_float2((g ? acc[u][1] : acc[u][0]) * (16777216.0f * unit),
+                         (g ? acc[u][3] : acc[u][2]) * (1048576.0f * unit));
     // each halving of the parts leaves half of the pairs to a lane: pairs u0 .. u0 + NY - 1
     constexpr int NY = 2 * NW / NP;
     int u0 = 0;

@@ -1,0 +1,68 @@
+"""The windowed attention over the whole range of softmax weights and of values: what a few large
+weights must not take away from many small ones."""
+import pytest
+import torch
+
+from parity_util import lib
+from test_gpu_window import i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fg():
+    return lib()
+
+
+def restored(codes, ab, d):
+    """64-bit a + q (b - a)/15 of cached positions [..][n][d]."""
+    q = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).unflatten(-1, (d // 64, 64)).double()
+    lo, hi = ab.contiguous().view(torch.float16).unflatten(-1, (-1, 2)).double().split(1, -1)
+    return (lo + q * ((hi - lo) / 15)).flatten(-2)
+
+
+def relative(got, want):
+    return ((got.double() - want).norm(dim=-1) / want.norm(dim=-1)).max().item()
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 7])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sigma,gap,n", [(0.01, 12, 2048), (0.05, 14, 8192), (0.01, 12, 8192),
+                                         (1.0, 13, 2048), (0.0005, 0, 2048)])
+def test_decode_window_one_large_weight(fg, G, d, sigma, gap, n):
+    """A first position `gap` nats above thousands of others, as attention sinks are, and small
+    values; 4000 row sets or more, so that most lie within one warp's share.
+
+    Relative error of a row: the output's rounding, at most 2^-11, and for the smallest values (near
+    0.0005 / sqrt(2048) = 1e-5 without a gap) half of fp16's smallest step, 2^-25 = 3e-8 an element
+    of 1e-5: 3e-3; the weights' rounding where one fp16 term is kept (G > 2), at most 2^-11 of each
+    (c - 7.5) (b - a)/15, which are 1.2 times the values at most (their middle is not their mean);
+    the truncated sums between corrections (6e-5, as for long shares); scores of up to 14 from d +
+    40 operations: 14 (d + 40) 2^-23 = 2.8e-4 of the small weights together, which are a twentieth
+    of the sum: 1.4e-5.  Together 4.9e-4 + 5.9e-4 + 8e-5 = 1.2e-3."""
+    H, B = 8, 500
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    x = torch.randn(n, 2, H * d, generator=g, device="cuda")
+    k, v = (0.3 * x[:, 0]).half(), (sigma * x[:, 1]).half()
+    q = (1.0 + 0.3 * torch.randn(H * G * d, generator=g, device="cuda")).half()
+    if gap:
+        k[0] = gap / d ** 0.5
+    one = fg.KVCacheQ4(1, n, H * d, H)
+    fg.fg_kv_append_q4_ragged(k, v, i32([0, n]), i32([0]), one)
+    cache = fg.KVCacheQ4(B, n, H * d, H)
+    for name in ("k_codes", "k_ab", "v_codes", "v_ab"):
+        getattr(cache, name).copy_(getattr(one, name).expand_as(getattr(cache, name)))
+    qs = q.expand(B, -1).contiguous()
+    out = torch.empty_like(qs)
+    ws = torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, H * G), dtype=torch.uint8,
+                     device="cuda")
+    fg.fg_decode_attn_q4kv_window(qs, H * G, cache, i32([n] * B), d ** -0.5, out, ws)
+    fg.fg_check_device_error()
+    kk, vv = (restored(getattr(one, c + "_codes")[0], getattr(one, c + "_ab")[0], d) for c in "kv")
+    p = torch.softmax(torch.einsum("hgd,hnd->hgn", q.view(H, G, d).double(), kk) * d ** -0.5, -1)
+    want = torch.einsum("hgn,hnd->hgd", p, vv)
+    if gap:
+        assert p[:, :, 0].min() > 0.5 and p[:, :, 1:].max() < 1e-2     # one large, the rest small
+    got = out.view(B, H, G, d)
+    assert relative(got, want) <= 1.2e-3 + (3e-3 if sigma < 0.001 else 0.0)
