@@ -16,7 +16,8 @@
 //   S = Q K^T     tcgen05.mma kind::f16, S (fp32) in TMEM
 //   softmax       one thread per query row, two passes over its 128 key columns in TMEM (the
 //                 maximum, then P): base-2 online softmax with a lazily moved reference maximum
-//                 (by more than 2^8), P = 2^(s - m) rounded to fp16 over S's columns.  Tiles that
+//                 (by more than 2^8), P = 2^(s - m + 7) rounded to fp16 over S's columns (at most
+//                 2^15: what is 14 nats below the maximum is still a normal number).  Tiles that
 //                 every row of the Q tile sees in full are not masked; the others take a bit mask
 //                 per row.
 //   O += P V      tcgen05.mma with P from TMEM
@@ -101,6 +102,10 @@ constexpr int BOX = QT * 128;               // bytes of one 64-column x 128-row 
 constexpr int kMaxSeqs = 384;               // sequences per launch
 static_assert(kMaxSeqs <= THREADS, "one thread per sequence reads its offsets");
 
+constexpr float kLag = 8.0f;                // base-2 score by which a row may pass its reference
+constexpr float kPExp = 7.0f;               // P is scaled by 2^7, as its row sum is: with a lag of 8
+                                            // P <= 2^15, and down to 2^-21 of the reference's P a
+                                            // weight is a normal fp16 number, to 2^-31 not zero
 constexpr int ITEMS = 4;                    // ring of work items
 constexpr unsigned kAllSteps = (KT / 16) << 4;   // every 16-key step of a tile (s0 | s1 << 4)
 constexpr unsigned kLastTile = 8u;               // the Q tile's last key tile (s0 < 8)
@@ -795,7 +800,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
         // in base 2 (scale > 0, so scaling after the maximum is the same); -inf for a row that
         // has seen no key yet
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
-        if (__any_sync(0xFFFFFFFFu, mx > m_ref + 8.0f)) {
+        if (__any_sync(0xFFFFFFFFu, mx > m_ref + kLag)) {
           // move the reference maximum of every row of the warp to max(m_ref, mx): O and l
           // scale by 2^(m_ref - m_new) (1 for rows whose maximum did not grow).  O holds P V of the
           // item's earlier tiles: those MMAs were issued, and so are done, before this S
@@ -818,10 +823,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
           l_sum *= alpha;
           m_ref = m_new;
         }
-        // pass 2: p = 2^(s * scale - m_ref), 32 columns at a time (the scaling and the row sums
+        // pass 2: p = 2^(s * scale - m_ref + 7), 32 columns at a time (the scaling and the row sums
         // two elements per instruction), packed to fp16 over the first 16 of the 32 S columns
         const float ref = (m_ref == -INFINITY) ? 0.0f : m_ref;
-        const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-ref, -ref);
+        const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(kPExp - ref, kPExp - ref);
         uint64_t ls2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
         auto p_chunk = [&](const float (&v)[32], int c) {
           uint32_t pw[16];

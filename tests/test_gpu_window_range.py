@@ -66,3 +66,29 @@ def test_decode_window_one_large_weight(fg, G, d, sigma, gap, n):
         assert p[:, :, 0].min() > 0.5 and p[:, :, 1:].max() < 1e-2     # one large, the rest small
     got = out.view(B, H, G, d)
     assert relative(got, want) <= 1.2e-3 + (3e-3 if sigma < 0.001 else 0.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [300, 64])          # an item per Q tile, and one that both share
+def test_prefill_window_one_large_weight(fg, d, nq):
+    """A first key 14.2 nats above 16384 equal ones, with a value of 0: the output is the small
+    weights' (2^-20.5 of the first).
+
+    Relative error of a row: the output's rounding and the weights', at most 2^-11 each (the
+    weights are all alike, so their errors have one sign); scores of 14.2 from d + 40 operations:
+    14.2 (d + 40) 2^-23 = 2.9e-4; the exponential's 2^-21.  Together 1.3e-3."""
+    n = 16384
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    k = torch.zeros(n, d, dtype=torch.float16, device="cuda")
+    k[0] = 14.2 / d ** 0.5
+    v = (1.0 + 0.3 * torch.randn(n, d, generator=g, device="cuda")).half()
+    v[0] = 0
+    q = torch.ones(nq, d, dtype=torch.float16, device="cuda")
+    out = torch.empty_like(q)
+    fg.fg_prefill_attn_window(q, i32([0, nq]), k, v, i32([0, n]), 1, 1, d ** -0.5, out)
+    fg.fg_check_device_error()
+    s = (q.double() @ k.double().T) * d ** -0.5
+    t = torch.arange(n, device="cuda")
+    s = s.masked_fill(t > torch.arange(n - nq, n, device="cuda")[:, None], -torch.inf)
+    assert relative(out, torch.softmax(s, -1) @ v.double()) <= 1.3e-3
