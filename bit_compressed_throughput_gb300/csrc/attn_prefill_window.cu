@@ -39,8 +39,9 @@
 // Masked keys.  A masked key has P = 0, but 0 times an infinity or a NaN in its V row is NaN: it
 // would reach the rows of the Q tile that do not see it.  The output warps therefore test their
 // rows: a row with an infinity or a NaN is computed again on its own, over its visible keys alone
-// (attend_rows), so that only what it sees can reach it.  Finite inputs take that path only where
-// rounding carries an output past fp16's range.  The rows behind a sequence in its last 16-key
+// (attend_rows), so that only what it sees can reach it.  A row whose sum of weights is NaN has its
+// answer: masked scores take no part in that sum, so one that it sees is NaN or infinite.  Finite
+// inputs take the path only where rounding carries an output past fp16's range.  The rows behind a sequence in its last 16-key
 // step, which may hold anything, are zeroed in shared memory first.
 //
 // The work order: blocks by descending index, for each the sequences that have one (longest first),
@@ -169,7 +170,8 @@ __device__ __forceinline__ float in_range(float y) {
 // Rows on their own, by a whole warp: up to kRowsAtOnce of its 32 (the bits of `rows`), the first
 // of which is row qrow at position pos of a sequence whose K/V rows start at k0; lane l returns
 // channels 64 box + 2l and the next.  Scores are computed a key per lane, values a channel pair per
-// lane; what a row does not see takes no part in it.  (4 rows of 16384 keys: 3 ms.)
+// lane; what a row does not see takes no part in it, and once all of the rows' channels are NaN
+// nothing changes them.  (4 rows of 16384 keys: 3 ms.)
 constexpr int kRowsAtOnce = 4;
 template <int D>
 __device__ __noinline__ void attend_rows(const PrefillWindow& a, int qrow, int hq, int k0, int pos,
@@ -252,6 +254,11 @@ __device__ __noinline__ void attend_rows(const PrefillWindow& a, int qrow, int h
         }
       }
     }
+    bool settled = true;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      settled = settled && (i[r] < 0 || (isnan(out[r].x) && isnan(out[r].y)));
+    if (__all_sync(0xFFFFFFFFu, settled)) break;
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -298,8 +305,9 @@ __device__ __noinline__ void store_split(const PrefillWindow& w, int qrow, int r
       if (lane < rows)
         reinterpret_cast<uint4*>(out + 32 * c)[k] = make_uint4(p[0], p[1], p[2], p[3]);
     }
-    redo[c >> 1] |= __ballot_sync(0xFFFFFFFFu, lane < rows && (__hisnan(__low2half(zero)) ||
-                                                               __hisnan(__high2half(zero))));
+    redo[c >> 1] |= __ballot_sync(0xFFFFFFFFu, lane < rows && !(sees && isnan(sum)) &&
+                                                   (__hisnan(__low2half(zero)) ||
+                                                    __hisnan(__high2half(zero))));
   }
   tc_fence_before();
   __syncwarp();
@@ -989,8 +997,9 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
                 reinterpret_cast<uint4*>(out + 64 * hb)[k] = make_uint4(p[0], p[1], p[2], p[3]);
             }
           }
-          const unsigned redo = __ballot_sync(
-              0xFFFFFFFFu, m < rows && (__hisnan(__low2half(zero)) || __hisnan(__high2half(zero))));
+          const unsigned redo =
+              __ballot_sync(0xFFFFFFFFu, m < rows && !isnan(inv) && (__hisnan(__low2half(zero)) ||
+                                                                     __hisnan(__high2half(zero))));
           if (hb == NB - 1) {
             // O_t has been read: the next item's first P V product may overwrite it
             tc_fence_before();

@@ -92,3 +92,45 @@ def test_prefill_window_one_large_weight(fg, d, nq):
     t = torch.arange(n, device="cuda")
     s = s.masked_fill(t > torch.arange(n - nq, n, device="cuda")[:, None], -torch.inf)
     assert relative(out, torch.softmax(s, -1) @ v.double()) <= 1.3e-3
+
+
+@pytest.mark.parametrize("nq", [256, 100])
+def test_prefill_window_visible_nan_costs_little(fg, nq):
+    """Rows that see a NaN in a key or in a whole value row have their answer without their keys
+    being gone over again (which takes 500 times as long); a NaN in one channel stays in it."""
+    d, n, H = 128, 16384, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    q, k, v = (torch.randn(r, H * d, generator=g, device="cuda").half() for r in (nq, n, n))
+    qo, ko = i32([0, nq]), i32([0, n])
+
+    def timed(k, v):
+        best = 1e9
+        for _ in range(4):
+            out = torch.empty_like(q)
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            fg.fg_prefill_attn_window(q, qo, k, v, ko, H, H, d ** -0.5, out)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        fg.fg_check_device_error()
+        return out, best
+
+    clean, t0 = timed(k, v)
+    assert bool(torch.isfinite(clean).all())
+    for t, bad_k, bad_v in ((5, True, True), (5, False, True), (n - nq, True, False)):
+        kk, vv = k.clone(), v.clone()
+        if bad_k:
+            kk[t] = torch.nan
+        if bad_v:
+            vv[t] = torch.nan
+        out, dt = timed(kk, vv)
+        assert bool(torch.isnan(out).all()), (t, bad_k, bad_v)
+        assert dt <= 10 * t0, (dt, t0)
+    vv = v.clone()
+    vv[7, 3], vv[9, d + 5] = torch.nan, torch.inf
+    out, _ = timed(k, vv)
+    assert bool(torch.isnan(out[:, 3]).all()) and bool((out[:, d + 5] == torch.inf).all())
+    rest = [c for c in range(H * d) if c not in (3, d + 5)]
+    assert (out[:, rest].float() - clean[:, rest].float()).abs().max() <= 2e-3 * clean.abs().max()
