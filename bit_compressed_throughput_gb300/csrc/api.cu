@@ -14,8 +14,8 @@
 #include <vector>
 
 #include "../../include/fg.h"
+#include "device_error.h"
 #include "fg_internal.h"
-#include "ragged.cuh"
 
 namespace fg {
 namespace {
@@ -421,36 +421,24 @@ const char* fg_last_error(void) { return t_last_error.c_str(); }
 int fg_check_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_cuda_error(e);
-  unsigned int flag = 0, sflag = 0, aflag = 0;
-  e = gemm_read_error(&flag);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  e = gemm_stream_read_error(&sflag);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  flag |= sflag;
-  e = gemm_pair_read_error(&sflag);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  flag |= sflag;
-  e = prefill_read_error(&sflag);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  flag |= sflag;
-  e = attn_read_error(&aflag);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  unsigned int wflag = 0;              // kernels that check extents on the device
-  for (auto* read : {ragged_read_error, decode_window_read_error, prefill_window_read_error}) {
-    if ((e = read(&sflag)) != cudaSuccess) return set_cuda_error(e);
-    wflag |= sflag;
+  const struct {
+    const char* family;
+    cudaError_t (*read)(unsigned int*);
+  } families[] = {{"GEMM", gemm_read_error},
+                  {"streaming GEMM", gemm_stream_read_error},
+                  {"CTA-pair GEMM", gemm_pair_read_error},
+                  {"prefill attention", prefill_read_error},
+                  {"decode attention", attn_read_error},
+                  {"ragged cache", ragged_read_error},
+                  {"windowed decode attention", decode_window_read_error},
+                  {"windowed prefill attention", prefill_window_read_error}};
+  constexpr int n = sizeof(families) / sizeof(families[0]);
+  DeviceErrorWord words[n];
+  for (int i = 0; i < n; ++i) {
+    words[i].family = families[i].family;
+    if ((e = families[i].read(&words[i].bits)) != cudaSuccess) return set_cuda_error(e);
   }
-  flag |= wflag & ~kErrExtent;
-  if (flag || aflag) {
-    t_last_error = "bounded device wait timed out (GEMM flag " + std::to_string(flag) +
-                   ", decode attention flag " + std::to_string(aflag) + ")";
-    return FG_ERR_TIMEOUT;
-  }
-  if (wflag & kErrExtent) {
-    t_last_error = "a length, position or row offset in a device array does not fit its buffers";
-    return FG_ERR_CAPACITY;
-  }
-  return FG_OK;
+  return device_error_status(words, n, &t_last_error);
 }
 
 int fg_quantize_g64(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, uint32_t* ab,

@@ -563,11 +563,6 @@ cudaError_t launch_decode_attn_scores(const uint16_t* q, int64_t q_stride, const
                     (float*)nullptr, keys, ml);
 }
 
-cudaError_t attn_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(unsigned int));
-}
+cudaError_t attn_read_error(unsigned int* out) { return read_and_clear(g_attn_error, out); }
 
 }  // namespace fg

@@ -861,11 +861,6 @@ cudaError_t launch_decode_attn_window(const uint16_t* q, int64_t q_stride, int32
   return launch(a, kv, ctas, st);
 }
 
-cudaError_t decode_window_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_decode_window_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_decode_window_error, &zero, sizeof(unsigned int));
-}
+cudaError_t decode_window_read_error(unsigned int* out) { return read_and_clear(g_decode_window_error, out); }
 
 }  // namespace fg

@@ -606,11 +606,6 @@ cudaError_t launch_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, in
                   : launch_d<64>(qkv, nseq, s, H, scale, out, nsm, st);
 }
 
-cudaError_t prefill_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_prefill_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_prefill_error, &zero, sizeof(unsigned int));
-}
+cudaError_t prefill_read_error(unsigned int* out) { return read_and_clear(g_prefill_error, out); }
 
 }  // namespace fg

@@ -1105,11 +1105,6 @@ cudaError_t launch_prefill_attn_window(const PrefillWindow& a, int d, int nsm, c
   return d == 128 ? launch_d<128>(a, nsm, st) : launch_d<64>(a, nsm, st);
 }
 
-cudaError_t prefill_window_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_prefill_window_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_prefill_window_error, &zero, sizeof(unsigned int));
-}
+cudaError_t prefill_window_read_error(unsigned int* out) { return read_and_clear(g_prefill_window_error, out); }
 
 }  // namespace fg

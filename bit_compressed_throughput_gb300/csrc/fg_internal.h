@@ -169,6 +169,14 @@ cudaError_t launch_gemm(const GemmPlan& p, const uint16_t* X, const fg_q4mat& W,
                         void* ws, cudaStream_t st, cudaEvent_t mid_event,
                         const KvOut* kv = nullptr, const LnOut* ln = nullptr,
                         const uint16_t* w16 = nullptr);
+// A device error word into *out; a word that is not 0 is cleared (one blocking copy for a word that
+// is, as nearly always).
+inline cudaError_t read_and_clear(const unsigned int& word, unsigned int* out) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, word, sizeof(unsigned int));
+  if (e != cudaSuccess || *out == 0) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(word, &zero, sizeof(unsigned int));
+}
 // Device error words of the bounded waits (GEMM, decode attention): read-and-clear.
 cudaError_t gemm_read_error(unsigned int* out);
 cudaError_t gemm_stream_read_error(unsigned int* out);

@@ -1044,11 +1044,6 @@ cudaError_t launch_gemm(const GemmPlan& p, const uint16_t* X, const fg_q4mat& W,
   return launch_reduce(p, ws, final_ea, ln, st);
 }
 
-cudaError_t gemm_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_gemm_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(unsigned int));
-}
+cudaError_t gemm_read_error(unsigned int* out) { return read_and_clear(g_gemm_error, out); }
 
 }  // namespace fg

@@ -825,11 +825,6 @@ cudaError_t launch_gemm_pair(const GemmPlan& p, const fg_q4mat& W, const uint16_
   return cudaLaunchKernelEx(&cfg, gemm_q4_pair_kernel, tmX, tmC, tmS, tmA, ka, ea);
 }
 
-cudaError_t gemm_pair_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_gemm_pair_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_gemm_pair_error, &zero, sizeof(unsigned int));
-}
+cudaError_t gemm_pair_read_error(unsigned int* out) { return read_and_clear(g_gemm_pair_error, out); }
 
 }  // namespace fg

@@ -594,11 +594,6 @@ cudaError_t launch_gemm_stream(const GemmPlan& p, const fg_q4mat& W, const CUten
                     tmX, tmC4, tmS4, ka, ea);
 }
 
-cudaError_t gemm_stream_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_gemm_stream_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_gemm_stream_error, &zero, sizeof(unsigned int));
-}
+cudaError_t gemm_stream_read_error(unsigned int* out) { return read_and_clear(g_gemm_stream_error, out); }
 
 }  // namespace fg

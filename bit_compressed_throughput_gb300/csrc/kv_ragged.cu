@@ -388,11 +388,6 @@ cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, 
                 row_stride, kv, nsm, st, kv, k_out, v_out);
 }
 
-cudaError_t ragged_read_error(unsigned int* out) {
-  unsigned int zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(out, g_ragged_error, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_ragged_error, &zero, sizeof(unsigned int));
-}
+cudaError_t ragged_read_error(unsigned int* out) { return read_and_clear(g_ragged_error, out); }
 
 }  // namespace fg

@@ -16,7 +16,8 @@
 
 namespace fg {
 
-constexpr unsigned int kErrExtent = 4u;    // bit of a device error word: an extent does not fit
+constexpr unsigned int kErrExtent = 1u << 16;    // bit of a device error word: an extent does not
+                                                 // fit (the low bits: a bounded wait ran out)
 
 // The sequence holding row r: the last b of 0 .. n-1 with off[b] <= r, or -1 when r lies before
 // the first or behind the last sequence.  For offsets that do not grow the answer may not hold

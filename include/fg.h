@@ -371,7 +371,8 @@ const char* fg_status_string(int status);
 const char* fg_last_error(void);
 /* Synchronise `stream`, read and clear the device error words: FG_OK, FG_ERR_TIMEOUT, or
  * FG_ERR_CAPACITY when a call met lengths, positions or offsets in a device array that do not
- * fit its buffers. */
+ * fit its buffers.  fg_last_error() names the kernels of either kind; FG_ERR_TIMEOUT is the status
+ * when both happened. */
 int fg_check_device_error(void* stream);
 
 /* Per-kernel timing with CUDA events recorded around every launch on its stream.
