@@ -11,7 +11,18 @@ import ctypes as C
 import os
 from typing import Optional
 
-import torch
+
+class _LazyTorch:
+    """Stands for torch until its first use, which imports it and puts it in this object's place:
+    the library's host-side calls work where torch is not installed."""
+
+    def __getattr__(self, name):
+        import torch as module
+        globals()["torch"] = module
+        return getattr(module, name)
+
+
+torch = _LazyTorch()
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfg.so")
