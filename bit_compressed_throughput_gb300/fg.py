@@ -174,6 +174,30 @@ class KVCacheQ4:
         self.k_ab = torch.zeros((B, H, cap, d // 64), dtype=torch.int32, device=device)
         self.v_ab = torch.zeros_like(self.k_ab)
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_fits", False)
+
+    def check(self):
+        """ValueError unless the four tensors have the shapes that B, cap, h and H say, on one
+        device.  Done once after an attribute was set; the ragged and windowed calls ask for it."""
+        if self._fits:
+            return
+        if self.H <= 0 or self.h != self.H * self.d or self.d % 64:
+            raise ValueError(f"cache: h = {self.h}, H = {self.H} and d = {self.d} do not fit")
+        device = self.k_codes.device
+        for name, dtype, width in (("k_codes", torch.uint8, self.d // 2),
+                                   ("v_codes", torch.uint8, self.d // 2),
+                                   ("k_ab", torch.int32, self.d // 64),
+                                   ("v_ab", torch.int32, self.d // 64)):
+            t, shape = getattr(self, name), (self.B, self.H, self.cap, width)
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError(f"cache.{name}: contiguous {dtype} {shape} expected, got {t.dtype} "
+                                 f"{tuple(t.shape)}")
+            if t.device != device:
+                raise ValueError(f"cache.{name} on {t.device}, cache.k_codes on {device}")
+        object.__setattr__(self, "_fits", True)
+
     def struct(self) -> fg_kvcache:
         return fg_kvcache(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_ab),
                           _ptr(self.v_ab), self.B, self.cap, self.h, self.H)
@@ -362,6 +386,7 @@ def fg_kv_append_q4_ragged(k_new, v_new, row_off, pos, cache: KVCacheQ4, stream=
         raise ValueError("k_new and v_new differ in rows or row stride")
     _extents("row_off", row_off, cache.B + 1)
     _extents("pos", pos, cache.B)
+    cache.check()
     handle = _stream_for(stream, k_new, v_new, row_off, pos, cache.k_codes)
     st = cache.struct()
     _check("fg_kv_append_q4_ragged",
@@ -378,6 +403,7 @@ def fg_kv_read_q4_ragged(cache: KVCacheQ4, row_off, pos, k_out, v_out, stream=No
     rows, stride = outs[0]
     _extents("row_off", row_off, cache.B + 1)
     _extents("pos", pos, cache.B)
+    cache.check()
     handle = _stream_for(stream, k_out, v_out, row_off, pos, cache.k_codes)
     st = cache.struct()
     _check("fg_kv_read_q4_ragged",
@@ -400,6 +426,7 @@ def fg_decode_attn_q4kv_window(q, Hq: int, cache: KVCacheQ4, lens, scale: float,
     if nq != cache.B or no != cache.B:
         raise ValueError(f"q and out need {cache.B} rows, got {nq} and {no}")
     _extents("lens", lens, cache.B)
+    cache.check()
     handle = _stream_for(stream, q, out, lens, ws, cache.k_codes)
     st = cache.struct()
     if ws is not None and not ws.is_contiguous():
