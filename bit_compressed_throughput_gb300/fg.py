@@ -363,6 +363,12 @@ def _extents(name: str, t, n: int):
                          f"{tuple(t.shape)}")
 
 
+def _window(window: int, sinks: int):
+    # what does not fit 32 bits would reach the library as another number
+    if not (-1 << 31) <= window < 1 << 31 or not (-1 << 31) <= sinks < 1 << 31:
+        raise ValueError(f"window and sinks are 32-bit integers, got {window} and {sinks}")
+
+
 def _stream_for(stream, *tensors) -> int:
     """The handle to launch on, for tensors that are all on the device that the call launches on:
     the current one, and the stream's."""
@@ -421,6 +427,7 @@ def fg_decode_attn_q4kv_window(q, Hq: int, cache: KVCacheQ4, lens, scale: float,
     """Decode attention of the newest position of every sequence (``lens`` int32 [B] on the
     device) over its last ``window`` positions (0: all) and its first ``sinks``; ``q`` and ``out``
     fp16 [B][Hq*d], Hq a multiple of the cache's heads."""
+    _window(window, sinks)
     nq, q_stride = _rows("q", q, Hq * cache.d)
     no, o_stride = _rows("out", out, Hq * cache.d)
     if nq != cache.B or no != cache.B:
@@ -444,6 +451,7 @@ def fg_prefill_attn_window(q, q_off, k, v, kv_off, Hq: int, Hkv: int, scale: flo
     ``out`` [q_rows][Hq*d], ``k`` and ``v`` [kv_rows][Hkv*d] with one row stride, ``q_off`` and
     ``kv_off`` int32 [nseq+1] on the device; window and sinks as in
     ``fg_decode_attn_q4kv_window``."""
+    _window(window, sinks)
     if Hq <= 0 or Hkv <= 0 or q.dim() != 2 or q.shape[1] % Hq:
         raise ValueError(f"q: [rows][Hq*d] expected, got {tuple(q.shape)} for {Hq} heads")
     d = q.shape[1] // Hq

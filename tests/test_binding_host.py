@@ -76,3 +76,16 @@ def test_cache_tensors_set_anew(fg):
     cache.k_ab = torch.zeros((2, 1, 48, 2), dtype=torch.int32)
     cache.v_ab = torch.zeros_like(cache.k_ab)
     cache.check()
+
+
+@pytest.mark.parametrize("name", ["window", "sinks"])
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 5, 1 << 62, -(1 << 32)])
+def test_window_of_more_than_32_bits(fg, name, value):
+    """2^32 + 5 is not a window of 5, and 2^32 not none at all."""
+    cache = fg.KVCacheQ4(2, 16, 128, 1, device="cpu")
+    q = torch.zeros((2, 128), dtype=torch.float16)
+    off, lens = torch.tensor([0, 1, 2], dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="32-bit"):
+        fg.fg_decode_attn_q4kv_window(q, 1, cache, lens, 0.1, q, **{name: value})
+    with pytest.raises(ValueError, match="32-bit"):
+        fg.fg_prefill_attn_window(q, off, q, q, off, 1, 1, 0.1, q.clone(), **{name: value})
