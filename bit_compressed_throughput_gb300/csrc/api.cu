@@ -16,6 +16,7 @@
 #include "../../include/fg.h"
 #include "device_error.h"
 #include "fg_internal.h"
+#include "overlap.h"
 
 namespace fg {
 namespace {
@@ -599,6 +600,10 @@ int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int
   int rc = check_ragged(kv, row_stride, rows, row_off, pos, &noop);
   if (rc || noop) return rc;
   if (k_out == v_out || !aligned16(k_out) || !aligned16(v_out)) return FG_ERR_ARG;
+  if (k_out && v_out &&
+      rows_overlap(fp16_rows(k_out, rows, row_stride, kv->h),
+                   fp16_rows(v_out, rows, row_stride, kv->h)))
+    return FG_ERR_ARG;
   if ((rc = check_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Span sp(st);
@@ -702,6 +707,9 @@ int fg_decode_attn_q4kv_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
     return FG_ERR_SHAPE;
   if (kv->B == 0) return FG_OK;
   if (!q || !out || !lens || !aligned16(q) || !aligned16(out) || !aligned4(lens)) return FG_ERR_ARG;
+  if (!(out == q && (q_stride == out_stride || kv->B == 1)) &&       // in place
+      rows_overlap(fp16_rows(q, kv->B, q_stride, width), fp16_rows(out, kv->B, out_stride, width)))
+    return FG_ERR_ARG;
   const size_t need = fg_decode_attn_window_workspace_bytes(kv, Hq);
   if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return FG_ERR_WORKSPACE;
   int sms = 0;
@@ -735,7 +743,11 @@ int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,
       !aligned4(kv_off))
     return FG_ERR_ARG;
   if (kv_rows > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return FG_ERR_ARG;
-  if (out == q || out == k || out == v) return FG_ERR_ARG;
+  const RowSet o = fp16_rows(out, q_rows, out_stride, wq);
+  if (rows_overlap(o, fp16_rows(q, q_rows, q_stride, wq)) ||
+      rows_overlap(o, fp16_rows(k, kv_rows, kv_stride, wk)) ||
+      rows_overlap(o, fp16_rows(v, kv_rows, kv_stride, wk)))
+    return FG_ERR_ARG;
   int sms = 0;
   if ((rc = check_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
