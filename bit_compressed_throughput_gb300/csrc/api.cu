@@ -719,8 +719,9 @@ int fg_decode_attn_q4kv_window(const uint16_t* q, int64_t q_stride, int32_t Hq,
   cudaError_t e = launch_decode_attn_window(q, q_stride, Hq, *kv, lens, window, sinks, scale, out,
                                             out_stride, ws, sms, st);
   if (e != cudaSuccess) return set_cuda_error(e);
+  const int64_t seen = window ? std::min<int64_t>(kv->cap, (int64_t)window + sinks) : kv->cap;
   sp.stop(FG_K_DECODE_ATTN_WINDOW,
-          2.0 * kv->B * kv->cap * kv->h * 0.5625 + 4.0 * kv->B * width);
+          2.0 * kv->B * seen * kv->h * 0.5625 + 4.0 * kv->B * width);
   return FG_OK;
 }
 

@@ -389,10 +389,13 @@ enum {
   FG_K_GEMM_PAIR_F16W = 12,   /* the CTA-pair GEMM on weights restored to fp16 (layer
                                  prefill): flops */
   /* work of the calls whose extents the host does not see is counted for the most that their
-   * host arguments allow: every row of the buffers, full cache, no window */
+   * host arguments allow: every row of the buffers, sequences that fill the cache (of which
+   * decode attention counts the window and the first positions).  A rate made from it is an upper
+   * bound, near the truth for full buffers only */
   FG_K_KV_READ = 13,             /* fg_kv_read_q4_ragged: bytes */
   FG_K_DECODE_ATTN_WINDOW = 14,  /* fg_decode_attn_q4kv_window, all its kernels: bytes */
-  FG_K_PREFILL_ATTN_WINDOW = 15, /* fg_prefill_attn_window: bytes of its rows */
+  FG_K_PREFILL_ATTN_WINDOW = 15, /* fg_prefill_attn_window: bytes of its rows (not its flops: how
+                                    many pairs are visible stands in the device arrays) */
   FG_K_COUNT = 16
 };
 int fg_prof_enable(int on);

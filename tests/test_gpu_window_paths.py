@@ -287,3 +287,27 @@ def test_launch_stream_is_the_current_one(fg):
             assert fg._stream() == torch.cuda.current_stream().cuda_stream
             assert fg._stream_for(None, torch.empty(1, device="cuda")) == s.cuda_stream
     assert fg._stream(st) == st.cuda_stream
+
+
+@pytest.mark.parametrize("window,sinks,seen", [(0, 0, 64), (0, 9, 64), (10, 3, 13), (60, 40, 64),
+                                               (2 ** 31 - 1, 2 ** 31 - 1, 64)])
+def test_profiled_work_of_windowed_decode(fg, window, sinks, seen):
+    """The profiler counts what full sequences see, not the whole cache."""
+    B, Hq, H, d = 3, 4, 2, 64
+    cache = fg.KVCacheQ4(B, 64, H * d, H)
+    q = torch.zeros((B, Hq * d), dtype=torch.float16, device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, Hq), dtype=torch.uint8,
+                     device="cuda")
+    fg.fg_prof_reset()
+    fg.fg_prof_enable()
+    try:
+        fg.fg_decode_attn_q4kv_window(q, Hq, cache, i32([64, 5, 0]), 0.1, out, ws, window=window,
+                                      sinks=sinks)
+        torch.cuda.synchronize()
+        r = fg.fg_prof_query(fg.K_DECODE_ATTN_WINDOW)
+    finally:
+        fg.fg_prof_enable(False)
+        fg.fg_prof_reset()
+    assert r["launches"] == 1
+    assert r["work"] == 2 * B * seen * H * d * 0.5625 + 4 * B * Hq * d
