@@ -69,20 +69,22 @@ constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 
 // The weights p (b - a) / 15 of the values are rounded to fp16, so they are taken times a power of
 // two f per (head, group), which leaves the sums again at their end.  t = (b - a) f is at most
-// kWide: with p <= 4 a weight is at most 2^15.  A wider position sets f anew, to t < 2^14, so that
-// a 7 times wider one still fits; f starts where the narrowest group's t is past kWide.  Weights
-// down to 2^-23 of the widest position's are then normal numbers.  (Unscaled, the weights of a position 12
-// nats below the largest score, or of values near 0.003, were subnormal or 0, and their codes' part
-// of the values lost, all with one sign: 8192 positions 14 nats below a first one, values of 0.05:
-// relative error 2.0e-2, now below 1.2e-3; 1 to 2% of the time.)
+// kWide: with p <= 4 a weight is at most 2^15.  A wider position, or a new reference maximum, sets
+// f anew, to t of 2^13 .. 2^14 for the widest position of its slot, so that a 7 times wider one
+// still fits; f starts where the narrowest group's t is past kWide.  Weights down to 2^-23 of the
+// widest position's are then normal numbers.  (Unscaled, the weights of a position 12 nats below
+// the largest score, or of values near 0.003, were subnormal or 0, and their codes' part of the
+// values lost, all with one sign: 8192 positions 14 nats below a first one, values of 0.05:
+// relative error 2.0e-2, now 2.3e-4 with one head, 5.0e-4 with four; 1 to 2% of the time.)
 constexpr float kWide = 122880.0f, kFirstF = 0x1p60f;
 __device__ __forceinline__ float inverse_f(float f) {    // of a power of two
   return __uint_as_float(0x7F000000u - __float_as_uint(f));
 }
-// The power of two that brings t, above kWide and finite, into 2^13 .. 2^14; 1 for any other t.
-__device__ __forceinline__ float narrow(float t) {
-  return t > kWide && t < INFINITY ? __uint_as_float((267u - (__float_as_uint(t) >> 23)) << 23)
-                                   : 1.0f;
+// The power of two that brings t into 2^13 .. 2^14; 1 for 0, infinities and NaN.  (Widths of 2^-24
+// .. 131008 keep f within 2^-4 .. 2^60, t and the factor within binary32's normal range.)
+__device__ __forceinline__ float to_scale(float t) {
+  return t > 0.0f && t < INFINITY ? __uint_as_float((267u - (__float_as_uint(t) >> 23)) << 23)
+                                  : 1.0f;
 }
 
 // One CTA per SM.  Its rings hold about 110 KB, what the memory system needs in flight (152 x 110
@@ -503,7 +505,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         sc[j] = valid[j] ? s : -INFINITY;
       }
       // The reference maximum moves only when a score exceeds it by more than 2^2, so that p <= 4;
-      // the weights' scale only for a position wider than kWide.
+      // the weights' scale then and for a position wider than kWide.
       float mloc = sc[0], tloc[NG] = {};
 #pragma unroll
       for (int j = 1; j < RPL; ++j) mloc = fmaxf(mloc, sc[j]);
@@ -531,7 +533,7 @@ decode_window_kernel(const Args a, const fg_kvcache kv) {
         l_run *= corr;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float n = narrow(tloc[g]);
+          const float n = to_scale(tloc[g]);
           f[g] *= n;
           r[g] = corr * n;
           asum[g] *= corr;

@@ -14,6 +14,12 @@ def fg():
     return lib()
 
 
+def generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
 def restored(codes, ab, d):
     """64-bit a + q (b - a)/15 of cached positions [..][n][d]."""
     q = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).unflatten(-1, (d // 64, 64)).double()
@@ -134,3 +140,44 @@ def test_prefill_window_visible_nan_costs_little(fg, nq):
     assert bool(torch.isnan(out[:, 3]).all()) and bool((out[:, d + 5] == torch.inf).all())
     rest = [c for c in range(H * d) if c not in (3, d + 5)]
     assert (out[:, rest].float() - clean[:, rest].float()).abs().max() <= 2e-3 * clean.abs().max()
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 7])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("decades", [5, -5, 8, -8])
+def test_decode_window_values_of_growing_size(fg, G, d, decades):
+    """Values that grow (or shrink) by many orders along a sequence while the scores fall (or rise)
+    alike, so that every part of it contributes as much: widths and scores move all along.
+
+    Relative error of a row: the output's rounding, at most 2^-11 = 4.9e-4, and for outputs near
+    4.5e-5 (8 decades) half of fp16's smallest step, 2^-25: 6.6e-4; the weights' rounding where one
+    fp16 term is kept (G > 2), at most 2^-11 of each (c - 7.5) (b - a)/15, at random before values
+    that sum up at random, 1.2 times these: 5.9e-4; the truncated sums, 6e-5; scores of up to 18.4
+    from d + 40 operations: 18.4 (d + 40) 2^-23 = 3.7e-4 of the weights.  Together 1.6e-3, and 7e-4
+    more for 8 decades."""
+    H, B, n = 8, 500, 2048
+    g = generator(37)
+    up = torch.arange(n, device="cuda") / n * abs(decades)
+    size = up + 4 - abs(decades)                            # powers of ten, at most 10^4
+    if decades < 0:
+        size, up = size.flip(0), up.flip(0)
+    v = (torch.randn(n, H * d, generator=g, device="cuda") * 10 ** size[:, None]).half()
+    k = (-up * 2.302585 / d ** 0.5).half()[:, None].expand(n, H * d).contiguous()
+    q = torch.ones(H * G * d, dtype=torch.float16, device="cuda")
+    one = fg.KVCacheQ4(1, n, H * d, H)
+    fg.fg_kv_append_q4_ragged(k, v, i32([0, n]), i32([0]), one)
+    cache = fg.KVCacheQ4(B, n, H * d, H)
+    for name in ("k_codes", "k_ab", "v_codes", "v_ab"):
+        getattr(cache, name).copy_(getattr(one, name).expand_as(getattr(cache, name)))
+    qs = q.expand(B, -1).contiguous()
+    out = torch.empty_like(qs)
+    ws = torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, H * G), dtype=torch.uint8,
+                     device="cuda")
+    fg.fg_decode_attn_q4kv_window(qs, H * G, cache, i32([n] * B), d ** -0.5, out, ws)
+    fg.fg_check_device_error()
+    kk, vv = (restored(getattr(one, c + "_codes")[0], getattr(one, c + "_ab")[0], d) for c in "kv")
+    p = torch.softmax(torch.einsum("hgd,hnd->hgn", q.view(H, G, d).double(), kk) * d ** -0.5, -1)
+    want = torch.einsum("hgn,hnd->hgd", p, vv)
+    parts = (p[0, 0, :, None] * vv[0]).norm(dim=-1).view(4, -1).norm(dim=-1)
+    assert parts.max() < 8 * parts.min()                   # every quarter of the sequence counts
+    assert relative(out.view(B, H, G, d), want) <= (1.6e-3 if abs(decades) == 5 else 2.3e-3)
