@@ -83,14 +83,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 }
 
 
-// 2^x on the special-function unit; inputs are <= 8 (lazy rescaling) or -inf, results that
-// would be subnormal flush to zero, which only drops terms below 2^-126 of the largest.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void bar_init(uint32_t bar) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
 }

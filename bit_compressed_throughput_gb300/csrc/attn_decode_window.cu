@@ -31,12 +31,16 @@
 // codes and statistics), filled by bulk async copies that run ahead across row sets.  Every wait is
 // bounded; on timeout the warp sets the device error word, drains its copies and stops.
 //
-// Measured (GB300, HBM copy 6.78 TB/s; bytes of the visible 4-bit K/V): 128 sequences x 56 heads of
-// 512 .. 1055 positions 134 us, 0.90 of the copy rate; 64 x 32 heads, lengths 200 .. 2048 under a
-// window of 1024, 51 us, 0.72 (248 MB: 2 us of planning, 4 us until the first slots are there and
-// 5 us of uneven ends beside 37 us of streaming, 4 us to merge; a plan with 64-bit divisions and
-// one per share boundary took 0.7 us more); 4 heads per K/V head over 16 contexts of 9000 .. 32760
-// 57 us, 0.72.  Warps end up to 12% behind the mean, in no fixed order.
+// Measured (GB300, HBM copy 6.78 TB/s; calls one after another, bytes of the visible 4-bit K/V):
+//   128 sequences x 56 heads, 512 .. 1055 positions: 135 us, 0.89 of the copy rate.
+//   64 x 32 heads, 200 .. 2048 positions, a window of 1024: 52 us, 0.70.  Of that 2 us plan (with
+//   64-bit divisions, and one of them per share boundary, 2.7 us), 4 us pass until the first slots
+//   are there, 37 us stream the 248 MB, 5 us are uneven ends (warps end up to 12% behind the mean,
+//   in no fixed order) and 4 us merge.
+//   16 contexts of 9000 .. 32760, 4 heads per K/V head, a window of 16384: 59 us, 0.70.
+// A further row set over the same positions costs most of what the first does: 16 contexts of about
+// 32,000, 8 K/V heads, window 16384: 73 us with 1, 2 or 4 heads per K/V head, 118 with 5, 120 with
+// 7 or 8 (caches cold).
 #include <math.h>
 
 #include <algorithm>
@@ -126,13 +130,6 @@ struct Args {
   Cut* cuts;           // [ncuts]
   float* partial;      // [2 * ncuts][HEADS][D + 2]
 };
-
-// 2^x on the special-function unit (x <= 2 here; results below 2^-126 flush to zero)
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, unsigned int err) {
   if (mbar_test(bar, parity)) return true;

@@ -41,8 +41,8 @@
 // rows: a row with an infinity or a NaN is computed again on its own, over its visible keys alone
 // (attend_rows), so that only what it sees can reach it.  A row whose sum of weights is NaN has its
 // answer: masked scores take no part in that sum, so one that it sees is NaN or infinite.  Finite
-// inputs take the path only where rounding carries an output past fp16's range.  The rows behind a sequence in its last 16-key
-// step, which may hold anything, are zeroed in shared memory first.
+// inputs take the path only where rounding carries an output past fp16's range.  The rows behind a
+// sequence in its last 16-key step, which may hold anything, are zeroed in shared memory first.
 //
 // The work order: blocks by descending index, for each the sequences that have one (longest first),
 // for each the query heads (which share K/V in L2).  One persistent CTA per SM; offsets are read
@@ -53,12 +53,12 @@
 // What bounds it: the turn that a Q tile takes -- P V and S (16 MMAs, 1024 cycles of tensor work),
 // the softmax (about 400 cycles for the maximum, 900 for P: 128 exponentials a thread, 512 cycles
 // of the special-function unit), and the barriers between -- with two Q tiles taking turns: 3200
-// cycles for a pair of key tiles of both, of which the tensor core works 2050.  Two sequences of
-// 8192, 32 heads, no window: 800 us, 1376 TFLOP/s (0.72 of the measured burst rate); a window of
-// 1024 with 4 first positions over two documents of 8k, grouped heads: 247 us, 960 TFLOP/s of
-// visible pairs; ragged prompts of 300 .. 512: 61 us, where the first loads (10000 cycles to the
-// first S), the masked tiles and the turns of short blocks count.  A masked tile's softmax takes
-// 2700 cycles instead of 1250.  Steps that brought it there, on the 8k window: one thread per row
+// cycles for a pair of key tiles of both, of which the tensor core works 2050.  Calls one after
+// another: two sequences of 8192, 32 heads, no window: 815 us, 1350 TFLOP/s (0.71 of the measured
+// burst rate); a window of 1024 with 4 first positions over two documents of 8k, grouped heads: 254
+// us, 939 TFLOP/s of visible pairs (captured in a graph 247 us, 966); ragged prompts of 300 .. 512:
+// 62 us, where the first loads (10000 cycles to the first S), the masked tiles and the turns of
+// short blocks count.  A masked tile's softmax takes 2700 cycles instead of 1250.  Steps that brought it there, on the 8k window: one thread per row
 // instead of two that exchange maxima 345 -> 318 us, an issuer warp per Q tile and key steps from
 // the producer 318 -> 307, MMAs issued under one lane's predicate on warp-uniform values
 // 307 -> 254.  Not kept: one pass instead of two (a chunk's maximum checked before its
@@ -410,9 +410,9 @@ __device__ __forceinline__ Item item_at(const Cursor& c, const Seq* seqs, const 
 }
 
 // Persistent: CTA c takes items c, c + gridDim, ...  The producer loads the next item's Q as
-// soon as the current item's last S product is done and streams K/V through the ring across
-// items; the MMA issuer starts the next item's S products while the current item's last P V
-// products run, and the output warps store an item's O while the softmax warps work on the next.
+// soon as the current item's last S product is done and streams K/V through the rings across
+// items; each Q tile's MMA issuer starts the next item's S products while the current item's last
+// P V products run, and the output warps store an item's O while the softmax warps work on the next.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -661,8 +661,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
       const unsigned all = __shfl_sync(0xFFFFFFFFu, steps_of[g % STAGES], 0);
       return all >> (8 * t) & 0xFFu;
     };
-    // Rows `tail` .. of V in their 16-key step become 0.  Both issuers may write (the same zeros);
-    // each does before its own products read them and before its part of V's release.
     for (int n = 0; ok; ++n) {
       const Item* slot = item_wait(n);
       if (!__all_sync(0xFFFFFFFFu, slot != nullptr)) break;

@@ -129,14 +129,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 2^x on the special-function unit (x <= 0 here; results below 2^-126 flush to zero, far
-// below the fp16 P fed to the P V product).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Blackwell's three-input maximum and packed two-lane fp32 arithmetic (one instruction for two
 // elements).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {

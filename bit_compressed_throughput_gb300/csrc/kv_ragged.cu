@@ -11,11 +11,12 @@
 // The tile's sequences are looked up once (while the first rows load), then the CTA walks its heads
 // with the next head's loads in flight.
 //
-// Measured (GB300, HBM copy 6.78 TB/s): 36 prompts of 400 .. 512 tokens, 96 heads: append 171 us
-// (6.06 TB/s, 0.89), read-back 167 us (0.91); 16 prompts of 300 .. 512, 32 heads: 35 us and 29 us
-// (0.57 and 0.68: 136 MB each, 5 us of launch and first loads).  The append was bound by
-// instructions before the codes were taken in fixed point and near ties fixed one by one (290 us
-// with the packed-pair quantiser of the plain append on the same split).
+// Measured (GB300, HBM copy 6.78 TB/s; calls one after another on other rows): 36 prompts of 400 ..
+// 512 tokens, 96 heads, 1033 MB each: append 162 us (0.94), read-back 162 us (0.94); 16 prompts of
+// 300 .. 512, 32 heads, 136 MB each: 28.5 us and 26.0 us (0.70 and 0.77; alone with cold caches,
+// launch included, 36 and 30).  The append was bound by instructions before the codes were taken
+// in fixed point and near ties fixed one by one (290 us at 96 heads with the packed-pair quantiser
+// of the plain append on the same split).
 #include <algorithm>
 
 #include "fg_common.cuh"

@@ -135,7 +135,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream=None) -> Optional[int]:
     if stream is not None:
         return stream.cuda_stream
-    # the handle of torch.cuda.current_stream(), without building a Stream object each call
+    # the handle of torch.cuda.current_stream(), without building a Stream object each call (0.3
+    # instead of 2.9 us of a call's host time; torch 2.9 and 2.11 have it)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 

@@ -136,11 +136,16 @@ def prefill_cases(fg, torch):
 
 def window_cases(fg, torch):
     """The ragged cache calls and the windowed attention: sequences of different lengths, a sliding
-    window with 4 first positions, one and four query heads per K/V head."""
+    window with 4 first positions, one and four query heads per K/V head; decode attention with two,
+    five, seven and eight of them, and with heads of 64 channels."""
     def i32(x):
         return torch.tensor(x, dtype=torch.int32, device="cuda")
 
-    for B, Hq, H, d, n, window in ((64, 32, 32, 128, 1024, 512), (16, 32, 8, 128, 8192, 4096)):
+    every = ("append", "read", "decode", "prefill")
+    shapes = [(64, 32, 32, 128, 1024, 512, every), (16, 32, 8, 128, 8192, 4096, every)]
+    shapes += [(16, 8 * G, 8, 128, 32768, 16384, ("decode",)) for G in (1, 2, 4, 5, 7, 8)]
+    shapes += [(64, 32, 32, 64, 2048, 1024, ("decode",)), (64, 32, 8, 64, 8192, 4096, ("decode",))]
+    for B, Hq, H, d, n, window, ops in shapes:
         lens = [n - (i * 37) % (n // 2) for i in range(B)]
         off = [0]
         for x in lens:
@@ -172,10 +177,12 @@ def window_cases(fg, torch):
                 ("prefill", lambda: fg.fg_prefill_attn_window(qp, offs, k, v, offs, Hq, H, scale, op,
                                                               window=window, sinks=4),
                  0, 4.0 * pairs * Hq * d)):
+            if name not in ops:
+                continue
             us = time_graph(fn)
             fg.fg_check_device_error()
             rate = (f"{flops / us / 1e6:7.1f} TFLOP/s" if flops else f"{byts / us / 1e3:7.1f} GB/s")
-            print(f"window {B}x{Hq}/{H}x{n:<5d} window {window:<5d} {name:8s} {us:9.1f} us  {rate}",
+            print(f"window {B}x{Hq}/{H}x{n:<5d} d {d:<3d} window {window:<5d} {name:8s} {us:9.1f} us  {rate}",
                   flush=True)
 
 
