@@ -555,6 +555,8 @@ cudaError_t launch_decode_attn_scores(const uint16_t* q, int64_t q_stride, const
                     (float*)nullptr, keys, ml);
 }
 
-cudaError_t attn_read_error(unsigned int* out) { return read_and_clear(g_attn_error, out); }
+cudaError_t attn_read_error(unsigned int* out) {
+  return read_and_clear(g_attn_error, out);
+}
 
 }  // namespace fg

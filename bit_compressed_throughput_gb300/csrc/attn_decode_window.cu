@@ -39,8 +39,8 @@
 //   in no fixed order) and 4 us merge.
 //   16 contexts of 9000 .. 32760, 4 heads per K/V head, a window of 16384: 59 us, 0.70.
 // A further row set over the same positions costs most of what the first does: 16 contexts of about
-// 32,000, 8 K/V heads, window 16384: 73 us with 1, 2 or 4 heads per K/V head, 118 with 5, 120 with
-// 7 or 8 (caches cold).
+// 32,000, 8 K/V heads, window 16384: 73 us with 1 or 2 heads per K/V head, 75 with 4, 118 with 5, 7
+// or 8 (caches cold).
 #include <math.h>
 
 #include <algorithm>
@@ -860,6 +860,8 @@ cudaError_t launch_decode_attn_window(const uint16_t* q, int64_t q_stride, int32
   return launch(a, kv, ctas, st);
 }
 
-cudaError_t decode_window_read_error(unsigned int* out) { return read_and_clear(g_decode_window_error, out); }
+cudaError_t decode_window_read_error(unsigned int* out) {
+  return read_and_clear(g_decode_window_error, out);
+}
 
 }  // namespace fg

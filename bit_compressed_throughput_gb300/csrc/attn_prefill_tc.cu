@@ -606,6 +606,8 @@ cudaError_t launch_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, in
                   : launch_d<64>(qkv, nseq, s, H, scale, out, nsm, st);
 }
 
-cudaError_t prefill_read_error(unsigned int* out) { return read_and_clear(g_prefill_error, out); }
+cudaError_t prefill_read_error(unsigned int* out) {
+  return read_and_clear(g_prefill_error, out);
+}
 
 }  // namespace fg

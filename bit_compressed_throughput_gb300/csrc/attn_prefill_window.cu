@@ -58,10 +58,10 @@
 // burst rate); a window of 1024 with 4 first positions over two documents of 8k, grouped heads: 254
 // us, 939 TFLOP/s of visible pairs (captured in a graph 247 us, 966); ragged prompts of 300 .. 512:
 // 62 us, where the first loads (10000 cycles to the first S), the masked tiles and the turns of
-// short blocks count.  A masked tile's softmax takes 2700 cycles instead of 1250.  Steps that brought it there, on the 8k window: one thread per row
-// instead of two that exchange maxima 345 -> 318 us, an issuer warp per Q tile and key steps from
-// the producer 318 -> 307, MMAs issued under one lane's predicate on warp-uniform values
-// 307 -> 254.  Not kept: one pass instead of two (a chunk's maximum checked before its
+// short blocks count.  A masked tile's softmax takes 2700 cycles instead of 1250.  Steps that
+// brought it there, on the 8k window: one thread per row instead of two that exchange maxima
+// 345 -> 318 us, an issuer warp per Q tile and key steps from the producer 318 -> 307, MMAs issued
+// under one lane's predicate on warp-uniform values 307 -> 254.  Not kept: one pass instead of two (a chunk's maximum checked before its
 // exponentials: 254 -> 277 us, the exponentials stand still meanwhile); the next load in flight in
 // masked tiles too (249 -> 259 us: registers), or masks in the code of the unmasked ones
 // (249 -> 276 us); more registers for the softmax warps (setmaxnreg, 16 warps: 252 -> 262 us);
@@ -104,7 +104,7 @@ constexpr int kMaxSeqs = 384;               // sequences per launch
 static_assert(kMaxSeqs <= THREADS, "one thread per sequence reads its offsets");
 
 constexpr float kLag = 8.0f;                // base-2 score by which a row may pass its reference
-constexpr float kPExp = 7.0f;               // P is scaled by 2^7, as its row sum is: with a lag of 8
+constexpr float kPExp = 7.0f;               // P is scaled by 2^7, as its row sum is: with that lag
                                             // P <= 2^15, and down to 2^-21 of the reference's P a
                                             // weight is a normal fp16 number, to 2^-31 not zero
 constexpr int ITEMS = 4;                    // ring of work items
@@ -412,7 +412,8 @@ __device__ __forceinline__ Item item_at(const Cursor& c, const Seq* seqs, const 
 // Persistent: CTA c takes items c, c + gridDim, ...  The producer loads the next item's Q as
 // soon as the current item's last S product is done and streams K/V through the rings across
 // items; each Q tile's MMA issuer starts the next item's S products while the current item's last
-// P V products run, and the output warps store an item's O while the softmax warps work on the next.
+// P V products run, and the output warps store an item's O while the softmax warps work on the
+// next.
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -1103,6 +1104,8 @@ cudaError_t launch_prefill_attn_window(const PrefillWindow& a, int d, int nsm, c
   return d == 128 ? launch_d<128>(a, nsm, st) : launch_d<64>(a, nsm, st);
 }
 
-cudaError_t prefill_window_read_error(unsigned int* out) { return read_and_clear(g_prefill_window_error, out); }
+cudaError_t prefill_window_read_error(unsigned int* out) {
+  return read_and_clear(g_prefill_window_error, out);
+}
 
 }  // namespace fg

@@ -1044,6 +1044,8 @@ cudaError_t launch_gemm(const GemmPlan& p, const uint16_t* X, const fg_q4mat& W,
   return launch_reduce(p, ws, final_ea, ln, st);
 }
 
-cudaError_t gemm_read_error(unsigned int* out) { return read_and_clear(g_gemm_error, out); }
+cudaError_t gemm_read_error(unsigned int* out) {
+  return read_and_clear(g_gemm_error, out);
+}
 
 }  // namespace fg

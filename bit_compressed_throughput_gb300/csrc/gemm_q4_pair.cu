@@ -825,6 +825,8 @@ cudaError_t launch_gemm_pair(const GemmPlan& p, const fg_q4mat& W, const uint16_
   return cudaLaunchKernelEx(&cfg, gemm_q4_pair_kernel, tmX, tmC, tmS, tmA, ka, ea);
 }
 
-cudaError_t gemm_pair_read_error(unsigned int* out) { return read_and_clear(g_gemm_pair_error, out); }
+cudaError_t gemm_pair_read_error(unsigned int* out) {
+  return read_and_clear(g_gemm_pair_error, out);
+}
 
 }  // namespace fg

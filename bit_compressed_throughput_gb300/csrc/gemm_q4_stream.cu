@@ -594,6 +594,8 @@ cudaError_t launch_gemm_stream(const GemmPlan& p, const fg_q4mat& W, const CUten
                     tmX, tmC4, tmS4, ka, ea);
 }
 
-cudaError_t gemm_stream_read_error(unsigned int* out) { return read_and_clear(g_gemm_stream_error, out); }
+cudaError_t gemm_stream_read_error(unsigned int* out) {
+  return read_and_clear(g_gemm_stream_error, out);
+}
 
 }  // namespace fg

@@ -389,6 +389,8 @@ cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, 
                 row_stride, kv, nsm, st, kv, k_out, v_out);
 }
 
-cudaError_t ragged_read_error(unsigned int* out) { return read_and_clear(g_ragged_error, out); }
+cudaError_t ragged_read_error(unsigned int* out) {
+  return read_and_clear(g_ragged_error, out);
+}
 
 }  // namespace fg

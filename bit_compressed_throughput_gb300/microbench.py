@@ -8,7 +8,7 @@ tests check the results; this only times them).
     python -m bit_compressed_throughput_gb300.microbench gemm      # GEMMs, fused K/V append
     python -m bit_compressed_throughput_gb300.microbench attn      # dense and Top-K decode
     python -m bit_compressed_throughput_gb300.microbench prefill   # causal prefill attention
-    python -m bit_compressed_throughput_gb300.microbench window    # ragged cache, windowed attention
+    python -m bit_compressed_throughput_gb300.microbench window    # ragged, windowed attention
 """
 from __future__ import annotations
 
@@ -158,11 +158,13 @@ def window_cases(fg, torch):
         out = torch.empty((rows, 2 * h), dtype=torch.float16, device="cuda")
         q = torch.randn((B, Hq * d), device="cuda").half()
         o = torch.empty_like(q)
-        qp = torch.randn((rows, Hq * d), device="cuda").half()
+        qp = torch.randn((rows if "prefill" in ops else 0, Hq * d), device="cuda").half()
         op = torch.empty_like(qp)
         ws = torch.empty(fg.fg_decode_attn_window_workspace_bytes(cache, Hq), dtype=torch.uint8,
                          device="cuda")
         scale = 1.0 / math.sqrt(d)
+        fg.fg_kv_append_q4_ragged(k, v, offs, zero, cache)
+        torch.cuda.synchronize()
         seen = sum(min(x, window + min(4, max(0, x - window))) for x in lens)
         pairs = sum(min(i + 1, window + min(4, max(0, i + 1 - window))) for x in lens
                     for i in range(x))
@@ -174,16 +176,16 @@ def window_cases(fg, torch):
                 ("decode", lambda: fg.fg_decode_attn_q4kv_window(q, Hq, cache, ln, scale, o, ws,
                                                                  window=window, sinks=4),
                  2 * seen * h * 0.5625 + 4.0 * B * Hq * d, 0),
-                ("prefill", lambda: fg.fg_prefill_attn_window(qp, offs, k, v, offs, Hq, H, scale, op,
-                                                              window=window, sinks=4),
+                ("prefill", lambda: fg.fg_prefill_attn_window(qp, offs, k, v, offs, Hq, H, scale,
+                                                              op, window=window, sinks=4),
                  0, 4.0 * pairs * Hq * d)):
             if name not in ops:
                 continue
             us = time_graph(fn)
             fg.fg_check_device_error()
             rate = (f"{flops / us / 1e6:7.1f} TFLOP/s" if flops else f"{byts / us / 1e3:7.1f} GB/s")
-            print(f"window {B}x{Hq}/{H}x{n:<5d} d {d:<3d} window {window:<5d} {name:8s} {us:9.1f} us  {rate}",
-                  flush=True)
+            print(f"window {B}x{Hq}/{H}x{n:<5d} d {d:<3d} window {window:<5d} {name:8s} "
+                  f"{us:9.1f} us  {rate}", flush=True)
 
 
 def main():

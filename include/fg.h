@@ -205,8 +205,9 @@ int fg_kv_append_q4_ragged(const uint16_t* k_new, const uint16_t* v_new, int64_t
  * fg_dequant_g64) into rows row_off[b] .. row_off[b+1]-1 of k_out and v_out, for prefill
  * attention over what the cache holds.  Arguments as fg_kv_append_q4_ragged; k_out or v_out may
  * be NULL (that half is not read); rows that overlap are refused (column blocks of one buffer do
- * not).  Rows outside every sequence, and rows that do not fit, stay as they were.  [FlexGen review (jaehun.me), "4-bit 압축은 정수 연산 가속과 같은가": values
- * are restored to FP16 before compute] */
+ * not).  Rows outside every sequence, and rows that do not fit, stay as they were.  [FlexGen
+ * review (jaehun.me), "4-bit 압축은 정수 연산 가속과 같은가": values are restored to FP16 before
+ * compute] */
 int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int32_t* pos,
                          int32_t rows, uint16_t* k_out, uint16_t* v_out, int64_t row_stride,
                          void* stream);
@@ -280,8 +281,8 @@ int fg_prefill_attn(const uint16_t* qkv, int32_t nseq, int32_t s, int32_t H, int
  * K^ and V^ enter the sums as a + q*((b-a)/15), not rounded to fp16 first.  A sequence of length
  * 0 sees nothing: its output is 0.  q: device fp16, row b at b*q_stride; out: device fp16, row b
  * at b*out_stride (both strides >= Hq*d, multiples of 8); out may be q itself, with the same
- * stride; any other overlap of their rows is refused.  Hq <= 65536, B*Hq*(cap/16 + 2) <= 2^40.  lens:
- * device int32 [B], 0 <= lens[b] <= cap, checked on the device (a length that does not fit counts
+ * stride; any other overlap of their rows is refused.  Hq <= 65536, B*Hq*(cap/16 + 2) <= 2^40.
+ * lens: device int32 [B], 0 <= lens[b] <= cap, checked on the device (a length that does not fit counts
  * as 0, and fg_check_device_error() returns FG_ERR_CAPACITY).  window, sinks >= 0.  ws: device
  * scratch of at least fg_decode_attn_window_workspace_bytes(kv, Hq) bytes, whatever the lengths
  * and the window; it needs no initialisation.  Two calls in flight at once need workspaces of
