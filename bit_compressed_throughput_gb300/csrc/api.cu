@@ -432,7 +432,9 @@ int fg_check_device_error(void* stream) {
                   {"decode attention", attn_read_error},
                   {"ragged cache", ragged_read_error},
                   {"windowed decode attention", decode_window_read_error},
-                  {"windowed prefill attention", prefill_window_read_error}};
+                  {"windowed prefill attention", prefill_window_read_error},
+                  {"paged attention", paged_attn_read_error},
+                  {"eviction", evict_read_error}};
   constexpr int n = sizeof(families) / sizeof(families[0]);
   DeviceErrorWord words[n];
   for (int i = 0; i < n; ++i) {
@@ -761,6 +763,308 @@ int fg_prefill_attn_window(const uint16_t* q, int64_t q_stride, int32_t q_rows,
   return FG_OK;
 }
 
+// ---------------------------------------------------------------------- paged cache
+
+// The cache as the kernels see it; `sequences` rows of the page table.
+static int check_pages(const fg_kvpages* kv, int32_t nseq, int64_t table_stride) {
+  if (!kv || kv->H <= 0 || kv->h <= 0 || kv->pages < 0 || nseq < 0 || nseq > 65535 ||
+      table_stride < 0)
+    return kv ? FG_ERR_SHAPE : FG_ERR_ARG;
+  const int d = kv->h / kv->H;
+  if (d * kv->H != kv->h || (d != 64 && d != 128) || kv->H > 65535) return FG_ERR_SHAPE;
+  if (kv->page < 16 || kv->page > 1024 || (kv->page & (kv->page - 1)) != 0) return FG_ERR_SHAPE;
+  // positions and the tiles behind them are 32-bit numbers
+  if (table_stride > (0x7FFFFFFF - 65536) / kv->page) return FG_ERR_SHAPE;
+  return FG_OK;
+}
+static bool pages_ok(const fg_kvpages* kv, const int32_t* table) {
+  return kv->blocks && aligned16(kv->blocks) && table && aligned4(table);
+}
+static PagedCache paged_cache(const fg_kvpages& kv, const int32_t* table, int64_t table_stride,
+                              int32_t nseq) {
+  int lg = 0;
+  while ((1 << lg) < kv.page) ++lg;
+  return PagedCache{kv.blocks, table, table_stride, kv.pages, lg, kv.H, nseq};
+}
+static int check_rope(const fg_rope_rows* r, int d) {
+  if (r->rot <= 0 || r->rot > d || r->rot % 16 != 0 || r->positions <= 0) return FG_ERR_SHAPE;
+  if (!r->angles || !aligned16(r->angles) || !aligned4(r->pos) ||
+      (r->interleaved != 0 && r->interleaved != 1))
+    return FG_ERR_ARG;
+  return FG_OK;
+}
+static RopeRows rope_rows(const fg_rope_rows& r) {
+  return RopeRows{r.angles, r.pos, r.positions, r.rot, r.interleaved != 0};
+}
+
+int fg_rope_table(float* angles, int32_t positions, int32_t rot, double base, double factor,
+                  int32_t original, double low, double high, double gain, void* stream) {
+  if (positions < 0 || rot <= 0 || rot % 2 != 0 || rot > 65536 || original < 0)
+    return FG_ERR_SHAPE;
+  if (!(base > 0.0) || !isfinite(base) || !(factor > 0.0) || !isfinite(factor) || !isfinite(gain) ||
+      (original > 0 && !(low >= 0.0 && low <= high && isfinite(high))))
+    return FG_ERR_ARG;
+  if (positions == 0) return FG_OK;
+  if (!angles || !aligned16(angles)) return FG_ERR_ARG;
+  int sms = 0;
+  int rc = check_device(&sms);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const RopeScale sc{base, factor, low, high, gain, original};
+  cudaError_t e = launch_rope_table(angles, positions, rot, sc, sms, st);
+  return e == cudaSuccess ? FG_OK : set_cuda_error(e);
+}
+
+int fg_rope(const uint16_t* x, int64_t x_stride, int32_t rows, int32_t heads, int32_t d,
+            const int32_t* row_off, int32_t nseq, const fg_rope_rows* rope, int32_t transpose,
+            uint16_t* y, int64_t y_stride, void* stream) {
+  if (!rope) return FG_ERR_ARG;
+  if (rows < 0 || rows > 0x7FFFFFFF - 64 || heads <= 0 || heads > 65536 || nseq < 0 ||
+      (d != 64 && d != 128))
+    return FG_ERR_SHAPE;
+  const int64_t width = (int64_t)heads * d;
+  if (x_stride < width || x_stride % 8 != 0 || y_stride < width || y_stride % 8 != 0)
+    return FG_ERR_SHAPE;
+  int rc = check_rope(rope, d);
+  if (rc) return rc;
+  if (transpose != 0 && transpose != 1) return FG_ERR_ARG;
+  if (rows == 0 || nseq == 0) return FG_OK;
+  if (!x || !y || !aligned16(x) || !aligned16(y) || !row_off || !aligned4(row_off) || !rope->pos)
+    return FG_ERR_ARG;
+  if (!(y == x && (x_stride == y_stride || rows == 1)) &&            // in place
+      rows_overlap(fp16_rows(x, rows, x_stride, width), fp16_rows(y, rows, y_stride, width)))
+    return FG_ERR_ARG;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  cudaError_t e = launch_rope(x, x_stride, rows, heads, d, row_off, nseq, rope_rows(*rope),
+                              transpose != 0, y, y_stride, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_ROPE, 4.0 * rows * width);
+  return FG_OK;
+}
+
+// Arguments shared by the two paged cache calls; *nothing_to_do when there are no rows.
+static int check_paged_rows(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
+                            int32_t nseq, int64_t row_stride, int32_t rows, const int32_t* row_off,
+                            const int32_t* pos, bool* nothing_to_do) {
+  *nothing_to_do = false;
+  int rc = check_pages(kv, nseq, table_stride);
+  if (rc) return rc;
+  if (rows < 0 || rows > 0x7FFFFFFF - 64 || row_stride < kv->h || row_stride % 8 != 0)
+    return FG_ERR_SHAPE;
+  if (rows == 0 || nseq == 0) {
+    *nothing_to_do = true;
+    return FG_OK;
+  }
+  if (!pages_ok(kv, table) || !row_off || !pos || !aligned4(row_off) || !aligned4(pos))
+    return FG_ERR_ARG;
+  return FG_OK;
+}
+
+int fg_kv_append_q4_paged(const uint16_t* k_new, const uint16_t* v_new, int64_t row_stride,
+                          int32_t rows, const int32_t* row_off, const int32_t* pos,
+                          const fg_rope_rows* rope, const fg_kvpages* kv, const int32_t* table,
+                          int64_t table_stride, int32_t nseq, void* stream) {
+  bool noop = false;
+  int sms = 0;
+  int rc = check_paged_rows(kv, table, table_stride, nseq, row_stride, rows, row_off, pos, &noop);
+  if (rc) return rc;
+  if (rope && (rc = check_rope(rope, kv->h / kv->H))) return rc;
+  if (noop) return FG_OK;
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return FG_ERR_ARG;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  RopeRows rr{};
+  if (rope) rr = rope_rows(*rope);
+  cudaError_t e = launch_kv_append_paged(k_new, v_new, row_stride, rows, row_off, pos,
+                                         paged_cache(*kv, table, table_stride, nseq),
+                                         kv->h / kv->H, rope ? &rr : nullptr, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_KV_APPEND, work_quantize(2.0 * rows * kv->h));
+  return FG_OK;
+}
+
+int fg_kv_read_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
+                        int32_t nseq, const int32_t* row_off, const int32_t* pos, int32_t rows,
+                        uint16_t* k_out, uint16_t* v_out, int64_t row_stride, void* stream) {
+  bool noop = false;
+  int sms = 0;
+  int rc = check_paged_rows(kv, table, table_stride, nseq, row_stride, rows, row_off, pos, &noop);
+  if (rc || noop) return rc;
+  if (k_out == v_out || !aligned16(k_out) || !aligned16(v_out)) return FG_ERR_ARG;
+  if (k_out && v_out &&
+      rows_overlap(fp16_rows(k_out, rows, row_stride, kv->h),
+                   fp16_rows(v_out, rows, row_stride, kv->h)))
+    return FG_ERR_ARG;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  cudaError_t e = launch_kv_read_paged(paged_cache(*kv, table, table_stride, nseq), kv->h / kv->H,
+                                       row_off, pos, rows, k_out, v_out, row_stride, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  sp.stop(FG_K_KV_READ,
+          work_dequant((double)((k_out != nullptr) + (v_out != nullptr)) * rows * kv->h));
+  return FG_OK;
+}
+
+// Query heads that share the cache's heads, in row tiles of 128: at most 128 of them each.
+static bool paged_heads_ok(const fg_kvpages& kv, int32_t Hq) {
+  return Hq > 0 && Hq <= 65536 && Hq % kv.H == 0 && Hq / kv.H <= 128;
+}
+
+size_t fg_attn_paged_workspace_bytes(const fg_kvpages* kv, int32_t Hq, int32_t max_q) {
+  if (check_pages(kv, 0, 0) != FG_OK || !paged_heads_ok(*kv, Hq) || max_q <= 0) return 0;
+  return attn_paged_ws_bytes(*kv, Hq, max_q);
+}
+
+// Arguments shared by the two paged attention calls.
+static int check_paged_attn(const uint16_t* q, int64_t q_stride, int32_t q_rows,
+                            const int32_t* q_off, int32_t max_q, int32_t Hq, const fg_kvpages* kv,
+                            const int32_t* table, int64_t table_stride, const int32_t* lens,
+                            int32_t nseq, int32_t window, int32_t sinks, float scale,
+                            bool* nothing_to_do) {
+  *nothing_to_do = false;
+  int rc = check_pages(kv, nseq, table_stride);
+  if (rc || (rc = check_window(window, sinks, scale))) return rc;
+  if (!paged_heads_ok(*kv, Hq) || q_rows < 0 || max_q < 0 || q_rows > 0x7FFFFFFF - 65536)
+    return FG_ERR_SHAPE;
+  if (q_stride < (int64_t)Hq * (kv->h / kv->H) || q_stride % 8 != 0) return FG_ERR_SHAPE;
+  if (nseq == 0) {
+    *nothing_to_do = true;
+    return FG_OK;
+  }
+  if (!pages_ok(kv, table) || !lens || !aligned4(lens) || !q_off || !aligned4(q_off))
+    return FG_ERR_ARG;
+  if (q_rows > 0 && (!q || !aligned16(q))) return FG_ERR_ARG;
+  return FG_OK;
+}
+
+int fg_attn_q4kv_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows, const int32_t* q_off,
+                       int32_t max_q, int32_t Hq, const fg_kvpages* kv, const int32_t* table,
+                       int64_t table_stride, const int32_t* lens, int32_t nseq, int32_t window,
+                       int32_t sinks, float scale, uint16_t* out, int64_t out_stride, float* lse,
+                       void* ws, size_t ws_bytes, void* stream) {
+  bool noop = false;
+  int rc = check_paged_attn(q, q_stride, q_rows, q_off, max_q, Hq, kv, table, table_stride, lens,
+                            nseq, window, sinks, scale, &noop);
+  if (rc) return rc;
+  const int d = kv->h / kv->H;
+  const int64_t width = (int64_t)Hq * d;
+  if (out_stride < width || out_stride % 8 != 0) return FG_ERR_SHAPE;
+  if (noop || q_rows == 0 || max_q == 0) return FG_OK;
+  if (!out || !aligned16(out) || !aligned4(lse)) return FG_ERR_ARG;
+  if (!(out == q && (q_stride == out_stride || q_rows == 1)) &&      // in place
+      rows_overlap(fp16_rows(q, q_rows, q_stride, width), fp16_rows(out, q_rows, out_stride, width)))
+    return FG_ERR_ARG;
+  const size_t need = fg_attn_paged_workspace_bytes(kv, Hq, max_q);
+  if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return FG_ERR_WORKSPACE;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  PagedAttn a{};
+  a.cache = paged_cache(*kv, table, table_stride, nseq);
+  a.q = q;
+  a.q_off = q_off;
+  a.lens = lens;
+  a.q_stride = q_stride;
+  a.q_rows = q_rows;
+  a.max_q = max_q;
+  a.Hq = Hq;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = scale;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  cudaError_t e = launch_attn_paged(a, d, ws, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  const int64_t cap = table_stride * kv->page;
+  const int64_t seen = window ? std::min<int64_t>(cap, (int64_t)window + sinks + max_q) : cap;
+  sp.stop(FG_K_ATTN_PAGED, 2.0 * nseq * seen * kv->h * 0.5625 + 4.0 * q_rows * width);
+  return FG_OK;
+}
+
+int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows,
+                             const int32_t* q_off, int32_t max_q, int32_t Hq, const fg_kvpages* kv,
+                             const int32_t* table, int64_t table_stride, const int32_t* lens,
+                             int32_t nseq, int32_t window, int32_t sinks, float scale,
+                             const float* lse, const float* acc, float* acc_out,
+                             int64_t acc_stride, void* stream) {
+  bool noop = false;
+  int rc = check_paged_attn(q, q_stride, q_rows, q_off, max_q, Hq, kv, table, table_stride, lens,
+                            nseq, window, sinks, scale, &noop);
+  if (rc) return rc;
+  if (acc_stride < 0) return FG_ERR_SHAPE;
+  if (noop) return FG_OK;
+  if ((q_rows > 0 && (!lse || !aligned4(lse))) || !acc_out || !aligned4(acc_out) || !aligned4(acc))
+    return FG_ERR_ARG;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  PagedAttn a{};
+  a.cache = paged_cache(*kv, table, table_stride, nseq);
+  a.q = q;
+  a.q_off = q_off;
+  a.lens = lens;
+  a.q_stride = q_stride;
+  a.q_rows = q_rows;
+  a.max_q = max_q;
+  a.Hq = Hq;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = scale;
+  a.lse_in = lse;
+  a.acc = acc;
+  a.acc_out = acc_out;
+  a.acc_stride = acc_stride;
+  cudaError_t e = launch_attn_weights_paged(a, kv->h / kv->H, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  const int64_t cap = std::min<int64_t>(table_stride * kv->page, acc_stride);
+  sp.stop(FG_K_ATTN_WEIGHTS, nseq * cap * (kv->h * 0.5625 + 8.0 * kv->H) +
+                                 (2.0 * (kv->h / kv->H) + 4.0) * q_rows * Hq);
+  return FG_OK;
+}
+
+int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
+                         int32_t nseq, const int32_t* lens, const float* acc, int64_t acc_stride,
+                         int32_t keep, int32_t recent, const int32_t* dst_table,
+                         int64_t dst_stride, int32_t* kept, float* acc_out, int32_t* dst_lens,
+                         void* stream) {
+  int rc = check_pages(kv, nseq, table_stride);
+  if (rc || (rc = check_pages(kv, nseq, dst_stride))) return rc;
+  if (keep <= 0 || recent < 0 || recent > keep || acc_stride < 0) return FG_ERR_SHAPE;
+  if (keep > dst_stride * kv->page) return FG_ERR_CAPACITY;
+  if (nseq == 0) return FG_OK;
+  if (!pages_ok(kv, table) || !dst_table || !aligned4(dst_table) || !lens || !aligned4(lens) ||
+      !acc || !aligned4(acc) || !kept || !aligned4(kept) || !acc_out || !aligned4(acc_out) ||
+      !dst_lens || !aligned4(dst_lens) || dst_lens == lens || dst_table == table)
+    return FG_ERR_ARG;
+  const RowSet out{reinterpret_cast<uint64_t>(acc_out), (int64_t)nseq * kv->H, 4ll * keep,
+                   4ll * keep};
+  if (acc_stride > 0 &&
+      rows_overlap(out, RowSet{reinterpret_cast<uint64_t>(acc), (int64_t)nseq * kv->H,
+                               4 * acc_stride, 4 * acc_stride}))
+    return FG_ERR_ARG;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Span sp(st);
+  const Evict a{paged_cache(*kv, table, table_stride, nseq),
+                paged_cache(*kv, dst_table, dst_stride, nseq),
+                lens, acc, acc_stride, keep, recent, kept, acc_out, dst_lens};
+  cudaError_t e = launch_kv_evict(a, kv->h / kv->H, sms, st);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  const int64_t n = std::min<int64_t>(table_stride * kv->page, acc_stride);
+  sp.stop(FG_K_KV_EVICT, 4.0 * nseq * kv->H * n +
+                             (double)nseq * keep * (2 * 2 * 0.5625 * kv->h + 12.0 * kv->H));
+  return FG_OK;
+}
+
 int fg_layernorm(const uint16_t* x, int64_t rows, int32_t h, const uint16_t* gamma,
                  const uint16_t* beta, float eps, uint16_t* y, void* stream) {
   if (rows < 0 || h <= 0 || h % 64 != 0 || h > 16384) return FG_ERR_SHAPE;
@@ -955,7 +1259,8 @@ const char* fg_kernel_name(int kind) {
       "q4g64_quantize", "q4g64_dequant", "q4_dequant_gemm_tc", "gemm_splitk_reduce",
       "q4kv_append", "q4kv_decode_attn", "decode_attn_combine", "prefill_attn",
       "layernorm", "q4_dequant_gemm_stream", "q4kv_decode_attn_topk", "q4_dequant_gemm_pair",
-      "gemm_f16w_pair", "q4kv_read", "q4kv_decode_attn_window", "prefill_attn_window"};
+      "gemm_f16w_pair", "q4kv_read", "q4kv_decode_attn_window", "prefill_attn_window",
+      "rope", "q4kv_attn_paged", "q4kv_attn_weights", "q4kv_evict"};
   return (kind >= 0 && kind < FG_K_COUNT) ? names[kind] : "unknown";
 }
 

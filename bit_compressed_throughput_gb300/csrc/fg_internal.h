@@ -8,6 +8,8 @@
 #include <utility>
 
 #include "../../include/fg.h"
+#include "paged.cuh"
+#include "rope.h"
 
 namespace fg {
 
@@ -39,6 +41,59 @@ cudaError_t launch_kv_append_ragged(const uint16_t* k_new, const uint16_t* v_new
 cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, const int32_t* pos,
                                   int32_t rows, uint16_t* k_out, uint16_t* v_out,
                                   int64_t row_stride, int nsm, cudaStream_t st);
+
+// Rotary positions and the paged cache (kv_ragged.cu).  pos: the position of each sequence's first
+// row (null: the cache position it goes to).
+struct RopeRows {
+  const float* angles;
+  const int32_t* pos;
+  int32_t positions, rot;
+  bool interleaved;
+};
+cudaError_t launch_rope(const uint16_t* x, int64_t x_stride, int32_t rows, int32_t heads, int d,
+                        const int32_t* row_off, int32_t nseq, const RopeRows& rope, bool transpose,
+                        uint16_t* y, int64_t y_stride, int nsm, cudaStream_t st);
+cudaError_t launch_rope_table(float* angles, int32_t positions, int32_t rot, const RopeScale& sc,
+                              int nsm, cudaStream_t st);
+cudaError_t launch_kv_append_paged(const uint16_t* k_new, const uint16_t* v_new,
+                                   int64_t row_stride, int32_t rows, const int32_t* row_off,
+                                   const int32_t* pos, const PagedCache& pc, int d,
+                                   const RopeRows* rope, int nsm, cudaStream_t st);
+cudaError_t launch_kv_read_paged(const PagedCache& pc, int d, const int32_t* row_off,
+                                 const int32_t* pos, int32_t rows, uint16_t* k_out,
+                                 uint16_t* v_out, int64_t row_stride, int nsm, cudaStream_t st);
+
+// Attention over the paged cache, and the weights that its positions receive (attn_paged.cu).
+struct PagedAttn {
+  PagedCache cache;
+  const uint16_t* q;
+  const int32_t *q_off, *lens;
+  int64_t q_stride;
+  int32_t q_rows, max_q, Hq, window, sinks;
+  float scale;
+  uint16_t* out;             // attention
+  int64_t out_stride;
+  float* lse;                // [q_rows][Hq], may be null
+  const float *lse_in, *acc; // weights; acc may be null
+  float* acc_out;
+  int64_t acc_stride;
+};
+size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q);
+cudaError_t launch_attn_paged(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st);
+cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st);
+
+// Eviction (kv_evict.cu): src and dst are the same blocks under two page tables.
+struct Evict {
+  PagedCache src, dst;
+  const int32_t* lens;
+  const float* acc;
+  int64_t acc_stride;
+  int32_t keep, recent;
+  int32_t* kept;
+  float* acc_out;
+  int32_t* dst_lens;
+};
+cudaError_t launch_kv_evict(const Evict& a, int d, int nsm, cudaStream_t st);
 
 // Windowed decode attention (attn_decode_window.cu): workspace bytes for any lengths and any SM
 // count up to kMaxSms.
@@ -188,6 +243,8 @@ cudaError_t attn_read_error(unsigned int* out);
 cudaError_t ragged_read_error(unsigned int* out);
 cudaError_t decode_window_read_error(unsigned int* out);
 cudaError_t prefill_window_read_error(unsigned int* out);
+cudaError_t paged_attn_read_error(unsigned int* out);
+cudaError_t evict_read_error(unsigned int* out);
 
 // Algorithmic work of one launch (bytes for memory-bound kernels, flops for the GEMM and
 // prefill attention): 4-bit storage costs 0.5 byte per element plus one (a, b) fp16 pair

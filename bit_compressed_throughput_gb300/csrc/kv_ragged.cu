@@ -21,7 +21,10 @@
 
 #include "fg_common.cuh"
 #include "fg_internal.h"
+#include "paged.cuh"
+#include "q4_restore.cuh"
 #include "ragged.cuh"
+#include "rope.h"
 
 namespace fg {
 
@@ -34,9 +37,42 @@ constexpr int kThreads = 256;
 struct RaggedArgs {
   const int32_t* row_off;
   const int32_t* pos;
-  int rows, B, H, cap;
+  int rows, B, H;
   int heads, hblocks;  // heads per CTA; CTAs per tile of rows
   int64_t stride;      // elements between the fp16 rows
+};
+
+// Where the 4-bit rows of a position lie: slot(b, p) numbers position p of sequence b (-1: it does
+// not fit), cell(slot, head) is that head's part of it.
+struct Cell {
+  uint8_t *k_codes, *v_codes;
+  uint32_t *k_ab, *v_ab;
+};
+struct Regions {                           // one region per (sequence, head)
+  fg_kvcache kv;
+  __device__ __forceinline__ int64_t slot(int b, int64_t p) const {
+    return p < kv.cap ? (int64_t)b * kv.H * kv.cap + p : -1;
+  }
+  template <int D>
+  __device__ __forceinline__ Cell cell(int64_t slot, int head) const {
+    const int64_t s = slot + (int64_t)head * kv.cap;
+    return Cell{kv.k_codes + s * (D / 2), kv.v_codes + s * (D / 2), kv.k_ab + s * (D / 64),
+                kv.v_ab + s * (D / 64)};
+  }
+};
+struct Pages {
+  PagedCache pc;
+  __device__ __forceinline__ int64_t slot(int b, int64_t p) const {
+    return p < pc.cap() ? pc.slot(b, p) : -1;
+  }
+  template <int D>
+  __device__ __forceinline__ Cell cell(int64_t slot, int head) const {
+    uint8_t *k = pc.block(slot, head, D), *v = k + pc.half_bytes(D);
+    const int64_t at = slot & ((1 << pc.lg) - 1), ab = (int64_t)(D / 2) << pc.lg;
+    return Cell{k + at * (D / 2), v + at * (D / 2),
+                reinterpret_cast<uint32_t*>(k + ab) + at * (D / 64),
+                reinterpret_cast<uint32_t*>(v + ab) + at * (D / 64)};
+  }
 };
 
 // The sequence holding row r, found by a whole warp, 32 offsets at a time (the answers of
@@ -54,10 +90,11 @@ __device__ __forceinline__ int warp_sequence_of_row(const int32_t* off, int n, i
   return lo;
 }
 
-// Slots (b*H)*cap + position of the tile's ROWS rows from r0 on, -1 for rows that no sequence
-// holds or that do not fit.  Every thread of the CTA calls it.
-template <int ROWS>
-__device__ __forceinline__ void tile_slots(const RaggedArgs& a, int r0, int64_t* slots) {
+// place(b, t) of the tile's ROWS rows from r0 on, row t of sequence b, into slots; -1 for rows that
+// no sequence holds or that do not fit (place < 0).  Every thread of the CTA calls it.
+template <int ROWS, typename Place>
+__device__ __forceinline__ void tile_slots(const RaggedArgs& a, int r0, int64_t* slots,
+                                           Place place) {
   const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0 &&
       !offsets_ok(a.row_off, a.B, a.rows, threadIdx.x, kThreads))
@@ -79,16 +116,130 @@ __device__ __forceinline__ void tile_slots(const RaggedArgs& a, int r0, int64_t*
     if (b >= 0 && row < a.rows) {
       const int64_t t = (int64_t)row - a.row_off[b];
       if (t >= 0 && row < a.row_off[b + 1]) {
-        const int64_t p = a.pos[b] + t;
-        if (a.pos[b] >= 0 && p < a.cap)
-          slot = (int64_t)b * a.H * a.cap + p;
-        else
-          atomicOr(&g_ragged_error, kErrExtent);
+        slot = place(b, t);
+        if (slot < 0) atomicOr(&g_ragged_error, kErrExtent);
       }
     }
     slots[threadIdx.x] = slot;
   }
   __syncthreads();
+}
+
+// ---------------------------------------------------------------------------- rotary positions
+//
+// A row at position p turns pairs of a head's first `rot` channels, (j, j + rot/2) or (2j, 2j + 1),
+// by the angle of (c, s) = angles[p][j]:  y0 = x0 c - x1 s, y1 = x0 s + x1 c, each product and sum
+// rounded to binary32, the result to fp16.
+struct Turn {
+  const float2* angles;
+  const int32_t* pos;  // position of each sequence's first row
+  int positions, rot;
+};
+__device__ __forceinline__ float turn0(float x0, float x1, float2 cs) {
+  return __fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y));
+}
+__device__ __forceinline__ float turn1(float x0, float x1, float2 cs) {
+  return __fadd_rn(__fmul_rn(x0, cs.y), __fmul_rn(x1, cs.x));
+}
+template <int N>
+__device__ __forceinline__ void load_angles(const float2* p, float2* cs) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+    cs[i] = make_float2(v.x, v.y);
+    cs[i + 1] = make_float2(v.z, v.w);
+  }
+}
+// 8 channels with their partners' 8: the lower or the upper half of the pairs.
+__device__ __forceinline__ uint4 turn_half(uint4 x, uint4 partner, const float2* cs, bool upper) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, pw[4] = {partner.x, partner.y, partner.z, partner.w};
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack_h2(xw[i]), b = unpack_h2(pw[i]);
+    y[i] = upper ? pack_h2(turn1(b.x, a.x, cs[2 * i]), turn1(b.y, a.y, cs[2 * i + 1]))
+                 : pack_h2(turn0(a.x, b.x, cs[2 * i]), turn0(a.y, b.y, cs[2 * i + 1]));
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+// 8 channels as 4 neighbouring pairs.
+__device__ __forceinline__ uint4 turn_pairs(uint4 x, const float2* cs) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack_h2(xw[i]);
+    y[i] = pack_h2(turn0(a.x, a.y, cs[i]), turn1(a.x, a.y, cs[i]));
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// d/16 lanes per row, 16 channels each: 8 of either half of the pairs, or 8 neighbouring pairs;
+// channels behind the first `rot` are copied.  A lane's angles serve all heads that its CTA walks.
+template <int D, bool PAIRS>
+__global__ void __launch_bounds__(kThreads)
+rope_kernel(const RaggedArgs a, const Turn turn, float sign, const uint16_t* x, uint16_t* y,
+            int64_t y_stride) {
+  constexpr int ROWS = 16 * kThreads / D, LPR = D / 16;
+  __shared__ int64_t slots[ROWS];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int r = threadIdx.x / LPR, u = threadIdx.x % LPR;
+  const unsigned tile = blockIdx.x / a.hblocks;
+  const int64_t r0 = (int64_t)tile * ROWS;
+  const int h0 = (int)(blockIdx.x - tile * a.hblocks) * a.heads, h1 = min(a.H, h0 + a.heads);
+  const bool turned = 16 * u < turn.rot;
+  const int c0 = turned && !PAIRS ? 8 * u : 16 * u;
+  const int c1 = turned && !PAIRS ? turn.rot / 2 + 8 * u : 16 * u + 8;
+  const bool held = r0 + r < a.rows;
+  const uint16_t* xs = x + (held ? (r0 + r) * a.stride : 0);
+  uint4 v[2] = {};
+  auto load = [&](int head) {
+    if (held) {                            // (y may be x: not through the read-only path)
+      v[0] = *reinterpret_cast<const uint4*>(xs + (int64_t)head * D + c0);
+      v[1] = *reinterpret_cast<const uint4*>(xs + (int64_t)head * D + c1);
+    }
+  };
+  load(h0);
+  tile_slots<ROWS>(a, (int)r0, slots, [&](int b, int64_t t) -> int64_t {
+    const int64_t p = turn.pos[b] + t;
+    return turn.pos[b] >= 0 && p < turn.positions ? p : -1;
+  });
+  const int64_t p = slots[r];
+  if (p < 0) return;
+  float2 cs[8];
+  if (turned) {
+    load_angles<8>(turn.angles + p * (turn.rot / 2) + 8 * u, cs);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i].y *= sign;
+  }
+  uint16_t* ys = y + (r0 + r) * y_stride;
+  for (int head = h0; head < h1; ++head) {
+    uint4 o[2] = {v[0], v[1]};
+    if (head + 1 < h1) load(head + 1);
+    if (turned) {
+      const uint4 w0 = o[0], w1 = o[1];
+      o[0] = PAIRS ? turn_pairs(w0, cs) : turn_half(w0, w1, cs, false);
+      o[1] = PAIRS ? turn_pairs(w1, cs + 4) : turn_half(w1, w0, cs, true);
+    }
+    *reinterpret_cast<uint4*>(ys + (int64_t)head * D + c0) = o[0];
+    *reinterpret_cast<uint4*>(ys + (int64_t)head * D + c1) = o[1];
+  }
+}
+
+// angles[p][j] = gain (cos, sin)(p w_j), in 64 bits, rounded once.
+__global__ void __launch_bounds__(kThreads)
+rope_table_kernel(float2* angles, int32_t positions, int32_t half, RopeScale sc) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t n = (int64_t)positions * half;
+  const int64_t step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int j = (int)(i % half);
+    double s, c;
+    sincos((double)(i / half) * rope_frequency(sc, j, half), &s, &c);
+    angles[i] = make_float2((float)(sc.gain * c), (float)(sc.gain * s));
+  }
 }
 
 // ---------------------------------------------------------------------------- append
@@ -101,11 +252,6 @@ __device__ __forceinline__ uint32_t hmin2_nan(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t q4_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -225,13 +371,15 @@ __device__ __forceinline__ uint2 quantize16(const uint4 v0, const uint4 v1, int 
   return codes;
 }
 
-// 4 lanes per group of 64, 16 values each: 16 * 256 / D rows per CTA.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4)
+// 4 lanes per group of 64, 16 values each: 16 * 256 / D rows per CTA.  ROPE: K is turned first (1:
+// pairs in halves, 2: neighbouring pairs), as rope_kernel does.
+template <int D, typename Cache, int ROPE>
+__global__ void __launch_bounds__(kThreads, ROPE == 0 ? 4 : 2)
 append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
-              const uint16_t* __restrict__ v_new, const fg_kvcache kv) {
-  constexpr int ROWS = 16 * kThreads / D, LPR = D / 16, NG = D / 64;
+              const uint16_t* __restrict__ v_new, const Cache cache, const Turn turn) {
+  constexpr int ROWS = 16 * kThreads / D, LPR = D / 16;
   __shared__ int64_t slots[ROWS];
+  __shared__ int turn_at[ROPE ? ROWS : 1];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, r = threadIdx.x / LPR, c = threadIdx.x % LPR;
@@ -241,34 +389,69 @@ append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
   const bool held = r0 + r < a.rows;
   const int64_t at = held ? (r0 + r) * a.stride + c * 16 : 0;
   const uint16_t *ks = k_new + at, *vs = v_new + at;
-  uint4 x[4];
+  // the lane's two chunks of 8 channels are both turned or neither (rot is a multiple of 16), and
+  // their partners lie half of rot before or behind
+  const bool turned = ROPE != 0 && 16 * c < turn.rot;
+  const int half = turn.rot / 2;
+  const bool upper[2] = {16 * c >= half, 16 * c + 8 >= half};
+  uint4 x[4], mate[2];
   auto load = [&](int head) {
     if (held) {
       x[0] = ldg_nc_v4(ks + head * D);
       x[1] = ldg_nc_v4(ks + head * D + 8);
       x[2] = ldg_nc_v4(vs + head * D);
       x[3] = ldg_nc_v4(vs + head * D + 8);
+      if (ROPE == 1 && turned) {
+        mate[0] = ldg_nc_v4(ks + head * D + (upper[0] ? -half : half));
+        mate[1] = ldg_nc_v4(ks + head * D + 8 + (upper[1] ? -half : half));
+      }
     }
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+  mate[0] = mate[1] = make_uint4(0, 0, 0, 0);
   load(h0);                                // in flight while the rows' sequences are looked up
-  tile_slots<ROWS>(a, (int)r0, slots);
+  tile_slots<ROWS>(a, (int)r0, slots, [&](int b, int64_t t) -> int64_t {
+    if (a.pos[b] < 0) return -1;
+    if constexpr (ROPE != 0) {
+      const int64_t p = turn.pos[b] + t;
+      if (turn.pos[b] < 0 || p >= turn.positions) return -1;
+      turn_at[threadIdx.x] = (int)p;
+    }
+    return cache.slot(b, a.pos[b] + t);
+  });
   const int64_t slot0 = slots[r];
   const bool live = slot0 >= 0;
+  float2 cs[ROPE == 1 ? 16 : 8];
+  if (ROPE != 0 && turned && live) {
+    const float2* row = turn.angles + (int64_t)turn_at[r] * half;
+    if constexpr (ROPE == 1) {
+      load_angles<8>(row + 16 * c - (upper[0] ? half : 0), cs);
+      load_angles<8>(row + 16 * c + 8 - (upper[1] ? half : 0), cs + 8);
+    } else {
+      load_angles<8>(row + 8 * c, cs);
+    }
+  }
   for (int head = h0; head < h1; ++head) {
-    const uint4 k0 = x[0], k1 = x[1], v0 = x[2], v1 = x[3];
+    uint4 k0 = x[0], k1 = x[1];
+    const uint4 v0 = x[2], v1 = x[3];
+    if constexpr (ROPE != 0) {
+      if (turned && live) {
+        k0 = ROPE == 1 ? turn_half(k0, mate[0], cs, upper[0]) : turn_pairs(k0, cs);
+        k1 = ROPE == 1 ? turn_half(k1, mate[1], cs + 8, upper[1]) : turn_pairs(k1, cs + 4);
+      }
+    }
     if (head + 1 < h1) load(head + 1);
     uint32_t kab, vab;
     const uint2 kc = quantize16(k0, k1, lane, &kab);
     const uint2 vc = quantize16(v0, v1, lane, &vab);
     if (live) {
-      const int64_t slot = slot0 + (int64_t)head * a.cap;
-      *reinterpret_cast<uint2*>(kv.k_codes + slot * (D / 2) + c * 8) = kc;
-      *reinterpret_cast<uint2*>(kv.v_codes + slot * (D / 2) + c * 8) = vc;
+      const Cell cell = cache.template cell<D>(slot0, head);
+      *reinterpret_cast<uint2*>(cell.k_codes + c * 8) = kc;
+      *reinterpret_cast<uint2*>(cell.v_codes + c * 8) = vc;
       if ((c & 3) == 0) {
-        kv.k_ab[slot * NG + (c >> 2)] = kab;
-        kv.v_ab[slot * NG + (c >> 2)] = vab;
+        cell.k_ab[c >> 2] = kab;
+        cell.v_ab[c >> 2] = vab;
       }
     }
   }
@@ -276,58 +459,22 @@ append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
 
 // ---------------------------------------------------------------------------- read-back
 
-// w / 15 rounded once (w finite and normal): the product with the rounded reciprocal, corrected by
-// its remainder, which is exact (Markstein, 1990).  It equals the quotient for each of the 2^23
-// mantissas of w (scaling by powers of two changes nothing).
-__device__ __forceinline__ float div15(float w) {
-  const float r = 1.0f / 15.0f, q = __fmul_rn(w, r);
-  return __fmaf_rn(__fmaf_rn(-15.0f, q, w), r, q);
-}
-// The same values by the format's operations one by one (infinite or NaN statistics).
-__device__ __noinline__ uint4 restore8_exact(uint32_t codes, float af, float s) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = pack_h2(__fadd_rn(af, __fmul_rn((float)((codes >> (8 * i)) & 0xFu), s)),
-                   __fadd_rn(af, __fmul_rn((float)((codes >> (8 * i + 4)) & 0xFu), s)));
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-// The 8 values fp16(a + fl(q s)), s = fl((b - a) / 15), of a code word.  A code's bits under the
-// exponent of 2^23 are the binary32 number 2^23 + q, and (2^23 + q) s - 2^23 s = q s exactly, so
-// one fused multiply-add with the exact -2^23 s gives fl(q s); two values per instruction.
-__device__ __forceinline__ uint4 restore8(uint32_t codes, uint32_t abw) {
-  const float2 ab = unpack_h2(abw);
-  const float s = div15(__fsub_rn(ab.y, ab.x)), c = -8388608.0f * s;
-  if (!(s < INFINITY))                     // fp16 infinities or NaN
-    return restore8_exact(codes, ab.x, __fdiv_rn(__fsub_rn(ab.y, ab.x), 15.0f));
-  const uint32_t ev = codes & 0x0F0F0F0Fu, od = (codes >> 4) & 0x0F0F0F0Fu;
-  const uint64_t a2 = q4_pack2(ab.x, ab.x), s2 = q4_pack2(s, s), c2 = q4_pack2(c, c);
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(__byte_perm(ev, 0x4B000000u, 0x7440 + i));
-    const float hi = __uint_as_float(__byte_perm(od, 0x4B000000u, 0x7440 + i));
-    float x, y;
-    q4_unpack2(q4_add2(a2, q4_fma2(q4_pack2(lo, hi), s2, c2)), x, y);
-    o[i] = pack_h2(x, y);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // 8 lanes per group of 64, 8 values each (a warp's stores are whole 32-byte sectors), two rows
 // per thread.
-template <int D>
+template <int D, typename Cache>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(const RaggedArgs a, const fg_kvcache kv, uint16_t* __restrict__ k_out,
+read_kernel(const RaggedArgs a, const Cache cache, uint16_t* __restrict__ k_out,
             uint16_t* __restrict__ v_out) {
-  constexpr int ROWS = 16 * kThreads / D, LPR = D / 8, NG = D / 64, STEP = kThreads / LPR;
+  constexpr int ROWS = 16 * kThreads / D, LPR = D / 8, STEP = kThreads / LPR;
   __shared__ int64_t slots[ROWS];
   pdl_launch_dependents();
   pdl_wait();
   const int r = threadIdx.x / LPR, c = threadIdx.x % LPR;
   const unsigned tile = blockIdx.x / a.hblocks;
   const int64_t r0 = (int64_t)tile * ROWS;
-  tile_slots<ROWS>(a, (int)r0, slots);
+  tile_slots<ROWS>(a, (int)r0, slots, [&](int b, int64_t t) -> int64_t {
+    return a.pos[b] < 0 ? -1 : cache.slot(b, a.pos[b] + t);
+  });
   const int h0 = (int)(blockIdx.x - tile * a.hblocks) * a.heads, h1 = min(a.H, h0 + a.heads);
   for (int head = h0; head < h1; ++head) {
     uint32_t code[2][2], ab[2][2];
@@ -336,22 +483,22 @@ read_kernel(const RaggedArgs a, const fg_kvcache kv, uint16_t* __restrict__ k_ou
     for (int j = 0; j < 2; ++j) {
       slot[j] = slots[r + j * STEP];
       if (slot[j] < 0) continue;
-      slot[j] += (int64_t)head * a.cap;
+      const Cell cell = cache.template cell<D>(slot[j], head);
       if (k_out) {
-        code[j][0] = *reinterpret_cast<const uint32_t*>(kv.k_codes + slot[j] * (D / 2) + c * 4);
-        ab[j][0] = kv.k_ab[slot[j] * NG + (c >> 3)];
+        code[j][0] = *reinterpret_cast<const uint32_t*>(cell.k_codes + c * 4);
+        ab[j][0] = cell.k_ab[c >> 3];
       }
       if (v_out) {
-        code[j][1] = *reinterpret_cast<const uint32_t*>(kv.v_codes + slot[j] * (D / 2) + c * 4);
-        ab[j][1] = kv.v_ab[slot[j] * NG + (c >> 3)];
+        code[j][1] = *reinterpret_cast<const uint32_t*>(cell.v_codes + c * 4);
+        ab[j][1] = cell.v_ab[c >> 3];
       }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (slot[j] < 0) continue;
       const int64_t at = (r0 + r + j * STEP) * a.stride + (int64_t)head * D + c * 8;
-      if (k_out) *reinterpret_cast<uint4*>(k_out + at) = restore8(code[j][0], ab[j][0]);
-      if (v_out) *reinterpret_cast<uint4*>(v_out + at) = restore8(code[j][1], ab[j][1]);
+      if (k_out) *reinterpret_cast<uint4*>(k_out + at) = restore8_fp16(code[j][0], ab[j][0]);
+      if (v_out) *reinterpret_cast<uint4*>(v_out + at) = restore8_fp16(code[j][1], ab[j][1]);
     }
   }
 }
@@ -361,14 +508,14 @@ read_kernel(const RaggedArgs a, const fg_kvcache kv, uint16_t* __restrict__ k_ou
 constexpr int kCtasPerSm = 16;
 template <typename Kernel, typename... Args>
 cudaError_t launch(Kernel* kernel, const int32_t* row_off, const int32_t* pos, int32_t rows,
-                   int64_t stride, const fg_kvcache& kv, int nsm, cudaStream_t st, Args... args) {
-  const int per = 16 * kThreads / (kv.h / kv.H);
+                   int64_t stride, int B, int H, int d, int nsm, cudaStream_t st, Args... args) {
+  const int per = 16 * kThreads / d;
   const int64_t tiles = ((int64_t)rows + per - 1) / per;
   const int heads =
-      (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * kv.H / ((int64_t)nsm * kCtasPerSm)));
-  const int hblocks = (kv.H + heads - 1) / heads;
+      (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * H / ((int64_t)nsm * kCtasPerSm)));
+  const int hblocks = (H + heads - 1) / heads;
   if (tiles * hblocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  const RaggedArgs a{row_off, pos, rows, kv.B, kv.H, kv.cap, heads, hblocks, stride};
+  const RaggedArgs a{row_off, pos, rows, B, H, heads, hblocks, stride};
   return launch_pdl(kernel, dim3((unsigned)(tiles * hblocks)), dim3(kThreads), 0, st, a, args...);
 }
 
@@ -378,15 +525,60 @@ cudaError_t launch_kv_append_ragged(const uint16_t* k_new, const uint16_t* v_new
                                     int64_t row_stride, int32_t rows, const int32_t* row_off,
                                     const int32_t* pos, const fg_kvcache& kv, int nsm,
                                     cudaStream_t st) {
-  return launch(kv.h / kv.H == 128 ? append_kernel<128> : append_kernel<64>, row_off, pos, rows,
-                row_stride, kv, nsm, st, k_new, v_new, kv);
+  const int d = kv.h / kv.H;
+  return launch(d == 128 ? append_kernel<128, Regions, 0> : append_kernel<64, Regions, 0>, row_off,
+                pos, rows, row_stride, kv.B, kv.H, d, nsm, st, k_new, v_new, Regions{kv}, Turn{});
 }
 
 cudaError_t launch_kv_read_ragged(const fg_kvcache& kv, const int32_t* row_off, const int32_t* pos,
                                   int32_t rows, uint16_t* k_out, uint16_t* v_out,
                                   int64_t row_stride, int nsm, cudaStream_t st) {
-  return launch(kv.h / kv.H == 128 ? read_kernel<128> : read_kernel<64>, row_off, pos, rows,
-                row_stride, kv, nsm, st, kv, k_out, v_out);
+  const int d = kv.h / kv.H;
+  return launch(d == 128 ? read_kernel<128, Regions> : read_kernel<64, Regions>, row_off, pos, rows,
+                row_stride, kv.B, kv.H, d, nsm, st, Regions{kv}, k_out, v_out);
+}
+
+cudaError_t launch_kv_append_paged(const uint16_t* k_new, const uint16_t* v_new,
+                                   int64_t row_stride, int32_t rows, const int32_t* row_off,
+                                   const int32_t* pos, const PagedCache& pc, int d,
+                                   const RopeRows* rope, int nsm, cudaStream_t st) {
+  auto* kernel = d == 128 ? append_kernel<128, Pages, 0> : append_kernel<64, Pages, 0>;
+  Turn turn{};
+  if (rope) {
+    turn = Turn{reinterpret_cast<const float2*>(rope->angles), rope->pos ? rope->pos : pos,
+                rope->positions, rope->rot};
+    if (rope->interleaved)
+      kernel = d == 128 ? append_kernel<128, Pages, 2> : append_kernel<64, Pages, 2>;
+    else
+      kernel = d == 128 ? append_kernel<128, Pages, 1> : append_kernel<64, Pages, 1>;
+  }
+  return launch(kernel, row_off, pos, rows, row_stride, pc.B, pc.H, d, nsm, st, k_new, v_new,
+                Pages{pc}, turn);
+}
+
+cudaError_t launch_kv_read_paged(const PagedCache& pc, int d, const int32_t* row_off,
+                                 const int32_t* pos, int32_t rows, uint16_t* k_out,
+                                 uint16_t* v_out, int64_t row_stride, int nsm, cudaStream_t st) {
+  return launch(d == 128 ? read_kernel<128, Pages> : read_kernel<64, Pages>, row_off, pos, rows,
+                row_stride, pc.B, pc.H, d, nsm, st, Pages{pc}, k_out, v_out);
+}
+
+cudaError_t launch_rope(const uint16_t* x, int64_t x_stride, int32_t rows, int32_t heads, int d,
+                        const int32_t* row_off, int32_t nseq, const RopeRows& rope, bool transpose,
+                        uint16_t* y, int64_t y_stride, int nsm, cudaStream_t st) {
+  auto* kernel = rope.interleaved ? (d == 128 ? rope_kernel<128, true> : rope_kernel<64, true>)
+                                  : (d == 128 ? rope_kernel<128, false> : rope_kernel<64, false>);
+  const Turn turn{reinterpret_cast<const float2*>(rope.angles), rope.pos, rope.positions, rope.rot};
+  return launch(kernel, row_off, rope.pos, rows, x_stride, nseq, heads, d, nsm, st, turn,
+                transpose ? -1.0f : 1.0f, x, y, y_stride);
+}
+
+cudaError_t launch_rope_table(float* angles, int32_t positions, int32_t rot, const RopeScale& sc,
+                              int nsm, cudaStream_t st) {
+  const int64_t n = (int64_t)positions * (rot / 2);
+  const int64_t ctas = std::min<int64_t>((n + kThreads - 1) / kThreads, (int64_t)nsm * 8);
+  return launch_pdl(rope_table_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, st,
+                    reinterpret_cast<float2*>(angles), positions, rot / 2, sc);
 }
 
 cudaError_t ragged_read_error(unsigned int* out) {

@@ -38,10 +38,12 @@ FG_EPI_NONE, FG_EPI_RELU, FG_EPI_RESIDUAL = 0, 1, 2
 KINDS = ["q4g64_quantize", "q4g64_dequant", "q4_dequant_gemm_tc", "gemm_splitk_reduce",
          "q4kv_append", "q4kv_decode_attn", "decode_attn_combine", "prefill_attn", "layernorm",
          "q4_dequant_gemm_stream", "q4kv_decode_attn_topk", "q4_dequant_gemm_pair",
-         "gemm_f16w_pair", "q4kv_read", "q4kv_decode_attn_window", "prefill_attn_window"]
+         "gemm_f16w_pair", "q4kv_read", "q4kv_decode_attn_window", "prefill_attn_window", "rope",
+         "q4kv_attn_paged", "q4kv_attn_weights", "q4kv_evict"]
 K_QUANT, K_DEQUANT, K_GEMM, K_GEMM_REDUCE, K_KV_APPEND, K_DECODE_ATTN, K_DECODE_COMBINE, \
     K_PREFILL_ATTN, K_LAYERNORM, K_GEMM_STREAM, K_DECODE_ATTN_TOPK, K_GEMM_PAIR, \
-    K_GEMM_PAIR_F16W, K_KV_READ, K_DECODE_ATTN_WINDOW, K_PREFILL_ATTN_WINDOW = range(16)
+    K_GEMM_PAIR_F16W, K_KV_READ, K_DECODE_ATTN_WINDOW, K_PREFILL_ATTN_WINDOW, K_ROPE, \
+    K_ATTN_PAGED, K_ATTN_WEIGHTS, K_KV_EVICT = range(20)
 
 
 class fg_q4mat(C.Structure):
@@ -52,6 +54,16 @@ class fg_kvcache(C.Structure):
     _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_ab", C.c_void_p),
                 ("v_ab", C.c_void_p), ("B", C.c_int32), ("cap", C.c_int32), ("h", C.c_int32),
                 ("H", C.c_int32)]
+
+
+class fg_kvpages(C.Structure):
+    _fields_ = [("blocks", C.c_void_p), ("pages", C.c_int32), ("page", C.c_int32),
+                ("h", C.c_int32), ("H", C.c_int32)]
+
+
+class fg_rope_rows(C.Structure):
+    _fields_ = [("angles", C.c_void_p), ("pos", C.c_void_p), ("positions", C.c_int32),
+                ("rot", C.c_int32), ("interleaved", C.c_int32)]
 
 
 class fg_dims(C.Structure):
@@ -93,6 +105,21 @@ _SIGS = {
     "fg_decode_attn_window_workspace_bytes": ([C.POINTER(fg_kvcache), _I32], _SZ),
     "fg_prefill_attn_window": ([_P, _I64, _I32, _P, _P, _P, _I64, _I32, _P, _I32, _I32, _I32, _I32,
                                 _I32, _I32, _F, _P, _I64, _P], C.c_int),
+    "fg_rope_table": ([_P, _I32, _I32, C.c_double, C.c_double, _I32, C.c_double, C.c_double,
+                       C.c_double, _P], C.c_int),
+    "fg_rope": ([_P, _I64, _I32, _I32, _I32, _P, _I32, C.POINTER(fg_rope_rows), _I32, _P, _I64, _P],
+                C.c_int),
+    "fg_kv_append_q4_paged": ([_P, _P, _I64, _I32, _P, _P, C.POINTER(fg_rope_rows),
+                               C.POINTER(fg_kvpages), _P, _I64, _I32, _P], C.c_int),
+    "fg_kv_read_q4_paged": ([C.POINTER(fg_kvpages), _P, _I64, _I32, _P, _P, _I32, _P, _P, _I64,
+                             _P], C.c_int),
+    "fg_attn_paged_workspace_bytes": ([C.POINTER(fg_kvpages), _I32, _I32], _SZ),
+    "fg_attn_q4kv_paged": ([_P, _I64, _I32, _P, _I32, _I32, C.POINTER(fg_kvpages), _P, _I64, _P,
+                            _I32, _I32, _I32, _F, _P, _I64, _P, _P, _SZ, _P], C.c_int),
+    "fg_attn_weights_q4_paged": ([_P, _I64, _I32, _P, _I32, _I32, C.POINTER(fg_kvpages), _P, _I64,
+                                  _P, _I32, _I32, _I32, _F, _P, _P, _P, _I64, _P], C.c_int),
+    "fg_kv_evict_q4_paged": ([C.POINTER(fg_kvpages), _P, _I64, _I32, _P, _P, _I64, _I32, _I32, _P,
+                              _I64, _P, _P, _P, _P], C.c_int),
     "fg_layernorm": ([_P, _I64, _I32, _P, _P, _F, _P, _P], C.c_int),
     "fg_layer_prefill": ([C.POINTER(fg_dims), C.POINTER(fg_layer), C.POINTER(fg_kvcache), _P, _P,
                           _I32, _I32, _I32, _P, _SZ, _P], C.c_int),
@@ -202,6 +229,52 @@ class KVCacheQ4:
     def struct(self) -> fg_kvcache:
         return fg_kvcache(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_ab),
                           _ptr(self.v_ab), self.B, self.cap, self.h, self.H)
+
+
+class KVPagesQ4:
+    """One layer's 4-bit KV cache in pages of ``page`` positions (a power of two, 16 .. 1024):
+    ``blocks`` uint8 [pages][H][page*9*d/8], per page and head K codes [page][d/2], K statistics
+    [page][d/64] (int32), V codes, V statistics.  Which pages a sequence has is the caller's
+    affair: calls take a page table, int32 [nseq][n] on the device."""
+
+    def __init__(self, pages: int, page: int, h: int, H: int, device="cuda"):
+        self._set(torch.zeros((pages, H, page * 9 * (h // H) // 8), dtype=torch.uint8,
+                              device=device), h // H)
+        if self.page != page or self.h != h:
+            raise ValueError(f"pages of {page} positions with h = {h} and H = {H} do not fit")
+
+    @classmethod
+    def of(cls, blocks, d: int) -> "KVPagesQ4":
+        """The cache that a tensor of blocks holds, heads of ``d`` channels."""
+        self = cls.__new__(cls)
+        self._set(blocks, d)
+        return self
+
+    def _set(self, blocks, d: int):
+        if d not in (64, 128) or blocks.dim() != 3 or blocks.dtype is not torch.uint8 or \
+                not blocks.is_contiguous() or blocks.shape[2] % (9 * d // 8):
+            raise ValueError(f"blocks: contiguous uint8 [pages][H][page*9*d/8] expected, got "
+                             f"{blocks.dtype} {tuple(blocks.shape)} for d = {d}")
+        self.blocks, self.d = blocks, d
+        self.pages, self.H = blocks.shape[0], blocks.shape[1]
+        self.page, self.h = blocks.shape[2] * 8 // (9 * d), self.H * d
+        if self.page < 16 or self.page > 1024 or self.page & (self.page - 1):
+            raise ValueError(f"pages of {self.page} positions: a power of two, 16 .. 1024, expected")
+        self._struct = fg_kvpages(_ptr(blocks), self.pages, self.page, self.h, self.H)
+
+    def parts(self):
+        """Views of the blocks: K codes [pages][H][page][d/2] and statistics [..][page][d/64] (fp16
+        pairs a, b in a last dimension), V codes and statistics."""
+        nc, na = self.page * self.d // 2, self.page * self.d // 16
+        out = []
+        for at in (0, nc + na):
+            out.append(self.blocks[..., at:at + nc].unflatten(-1, (self.page, self.d // 2)))
+            out.append(self.blocks[..., at + nc:at + nc + na].view(torch.float16)
+                       .unflatten(-1, (self.page, self.d // 64, 2)))
+        return out
+
+    def struct(self) -> fg_kvpages:
+        return self._struct
 
 
 class LayerQ4:
@@ -469,6 +542,193 @@ def fg_prefill_attn_window(q, q_off, k, v, kv_off, Hq: int, Hkv: int, scale: flo
            lib.fg_prefill_attn_window(_ptr(q), q_stride, q_rows, _ptr(q_off), _ptr(k), _ptr(v),
                                       kv_stride, kv_rows, _ptr(kv_off), nseq, Hq, Hkv, d, window,
                                       sinks, scale, _ptr(out), o_stride, handle))
+
+
+def _table(name: str, t):
+    """(sequences, entries each) of a page table."""
+    if t.dim() != 2 or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 [sequences][pages] expected, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.shape
+
+
+def _angles(t):
+    """(positions, rotated channels) of a table of angles."""
+    if t.dim() != 3 or t.shape[2] != 2 or t.dtype is not torch.float32 or not t.is_contiguous():
+        raise ValueError(f"angles: contiguous fp32 [positions][rot/2][2] expected, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.shape[0], 2 * t.shape[1]
+
+
+def fg_rope_table(angles, base: float = 10000.0, factor: float = 1.0, original: int = 0,
+                  low: float = 1.0, high: float = 4.0, gain: float = 1.0, stream=None):
+    """Fills ``angles`` (fp32 [positions][rot/2][2]) with gain * (cos, sin) of every position's
+    angles; ``factor`` stretches them for contexts longer than ``original`` positions (0: all of
+    them, see include/fg.h)."""
+    positions, rot = _angles(angles)
+    _check("fg_rope_table",
+           lib.fg_rope_table(_ptr(angles), positions, rot, base, factor, original, low, high, gain,
+                             _stream_for(stream, angles)))
+
+
+def fg_rope(x, d: int, row_off, pos, angles, y, interleaved: bool = False, transpose: bool = False,
+            stream=None):
+    """Rotary positions: rows row_off[b] .. row_off[b+1]-1 of ``x`` (fp16 [rows][heads*d]) turned as
+    positions pos[b] .. into ``y`` (may be ``x``); ``transpose``: the gradient's (and, with a gain
+    of 1, the inverse) turn."""
+    if d <= 0 or x.dim() != 2 or x.shape[1] % d:
+        raise ValueError(f"x: [rows][heads*{d}] expected, got {tuple(x.shape)}")
+    rows, x_stride = _rows("x", x, x.shape[1])
+    y_rows, y_stride = _rows("y", y, x.shape[1])
+    if y_rows != rows:
+        raise ValueError(f"x has {rows} rows, y {y_rows}")
+    positions, rot = _angles(angles)
+    nseq = pos.shape[0]
+    _extents("row_off", row_off, nseq + 1)
+    _extents("pos", pos, nseq)
+    handle = _stream_for(stream, x, y, row_off, pos, angles)
+    st = fg_rope_rows(_ptr(angles), _ptr(pos), positions, rot, int(interleaved))
+    _check("fg_rope", lib.fg_rope(_ptr(x), x_stride, rows, x.shape[1] // d, d, _ptr(row_off), nseq,
+                                  C.byref(st), int(transpose), _ptr(y), y_stride, handle))
+
+
+def fg_kv_append_q4_paged(k_new, v_new, row_off, pos, pages: KVPagesQ4, table, angles=None,
+                          rope_pos=None, interleaved: bool = False, stream=None):
+    """Rows row_off[b] .. row_off[b+1]-1 of ``k_new`` and ``v_new`` (fp16 [rows][h], one row stride)
+    quantised into positions pos[b] .. of sequence b's pages (``table`` int32 [nseq][n]).  With
+    ``angles`` K is turned first, as positions rope_pos[b] .. (default: pos[b] ..)."""
+    rows, stride = _rows("k_new", k_new, pages.h)
+    if _rows("v_new", v_new, pages.h) != (rows, stride):
+        raise ValueError("k_new and v_new differ in rows or row stride")
+    nseq, n = _table("table", table)
+    _extents("row_off", row_off, nseq + 1)
+    _extents("pos", pos, nseq)
+    rope = None
+    if angles is not None:
+        positions, rot = _angles(angles)
+        if rope_pos is not None:
+            _extents("rope_pos", rope_pos, nseq)
+        rope = C.byref(fg_rope_rows(_ptr(angles), _ptr(rope_pos), positions, rot,
+                                    int(interleaved)))
+    elif rope_pos is not None:
+        raise ValueError("rope_pos without angles")
+    handle = _stream_for(stream, k_new, v_new, row_off, pos, table, angles, rope_pos, pages.blocks)
+    _check("fg_kv_append_q4_paged",
+           lib.fg_kv_append_q4_paged(_ptr(k_new), _ptr(v_new), stride, rows, _ptr(row_off),
+                                     _ptr(pos), rope, C.byref(pages.struct()), _ptr(table), n, nseq,
+                                     handle))
+
+
+def fg_kv_read_q4_paged(pages: KVPagesQ4, table, row_off, pos, k_out, v_out, stream=None):
+    """Positions pos[b] .. of sequence b's pages restored to fp16 rows row_off[b] .. row_off[b+1]-1
+    of ``k_out`` and ``v_out`` (fp16 [rows][h], one row stride; either may be None)."""
+    outs = [_rows(n, t, pages.h) for n, t in (("k_out", k_out), ("v_out", v_out)) if t is not None]
+    if not outs or outs[0] != outs[-1]:
+        raise ValueError("k_out and v_out differ in rows or row stride, or both are None")
+    rows, stride = outs[0]
+    nseq, n = _table("table", table)
+    _extents("row_off", row_off, nseq + 1)
+    _extents("pos", pos, nseq)
+    handle = _stream_for(stream, k_out, v_out, row_off, pos, table, pages.blocks)
+    _check("fg_kv_read_q4_paged",
+           lib.fg_kv_read_q4_paged(C.byref(pages.struct()), _ptr(table), n, nseq, _ptr(row_off),
+                                   _ptr(pos), rows, _ptr(k_out), _ptr(v_out), stride, handle))
+
+
+def fg_attn_paged_workspace_bytes(pages: KVPagesQ4, Hq: int, max_q: int) -> int:
+    return int(lib.fg_attn_paged_workspace_bytes(C.byref(pages.struct()), Hq, max_q))
+
+
+def _paged_queries(q, q_off, Hq: int, pages: KVPagesQ4, table, lens, max_q, window, sinks):
+    """What the two paged attention calls say of their queries: (rows, row stride, max_q, sequences,
+    page table entries)."""
+    _window(window, sinks)
+    rows, stride = _rows("q", q, Hq * pages.d)
+    nseq, n = _table("table", table)
+    _extents("q_off", q_off, nseq + 1)
+    _extents("lens", lens, nseq)
+    return rows, stride, rows if max_q is None else max_q, nseq, n
+
+
+def _scores(name: str, t, shape):
+    if t.shape != shape or t.dtype is not torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous fp32 {tuple(shape)} expected, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def fg_attn_q4kv_paged(q, q_off, Hq: int, pages: KVPagesQ4, table, lens, scale: float, out, ws,
+                       max_q: Optional[int] = None, window: int = 0, sinks: int = 0, lse=None,
+                       stream=None):
+    """Attention of the newest tokens of every sequence (rows q_off[b] .. q_off[b+1]-1 of ``q`` and
+    ``out``, fp16 [rows][Hq*d]; at most ``max_q`` each, default all rows) over its ``lens[b]``
+    cached positions; ``lse`` (optional fp32 [rows][Hq]) receives the scores' log-sum-exp; window
+    and sinks as in ``fg_decode_attn_q4kv_window``."""
+    rows, q_stride, max_q, nseq, n = _paged_queries(q, q_off, Hq, pages, table, lens, max_q, window,
+                                                    sinks)
+    o_rows, o_stride = _rows("out", out, Hq * pages.d)
+    if o_rows != rows:
+        raise ValueError(f"q has {rows} rows, out {o_rows}")
+    if lse is not None:
+        _scores("lse", lse, (rows, Hq))
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor expected")
+    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    handle = _stream_for(stream, q, out, q_off, table, lens, lse, ws, pages.blocks)
+    _check("fg_attn_q4kv_paged",
+           lib.fg_attn_q4kv_paged(_ptr(q), q_stride, rows, _ptr(q_off), max_q, Hq,
+                                  C.byref(pages.struct()), _ptr(table), n, _ptr(lens), nseq, window,
+                                  sinks, scale, _ptr(out), o_stride, _ptr(lse), _ptr(ws), wsb,
+                                  handle))
+
+
+def fg_attn_weights_q4_paged(q, q_off, Hq: int, pages: KVPagesQ4, table, lens, scale: float, lse,
+                             acc, acc_out, max_q: Optional[int] = None, window: int = 0,
+                             sinks: int = 0, stream=None):
+    """The softmax weights that cached positions receive from the given queries, added to ``acc``
+    (fp32 [nseq][H][n], or None for zeros) into ``acc_out`` (may be ``acc``); ``lse`` as
+    ``fg_attn_q4kv_paged`` gives it."""
+    rows, q_stride, max_q, nseq, n = _paged_queries(q, q_off, Hq, pages, table, lens, max_q, window,
+                                                    sinks)
+    _scores("lse", lse, (rows, Hq))
+    if acc_out.dim() != 3:
+        raise ValueError(f"acc_out: [nseq][H][positions] expected, got {tuple(acc_out.shape)}")
+    shape = (nseq, pages.H, acc_out.shape[2])
+    _scores("acc_out", acc_out, shape)
+    if acc is not None:
+        _scores("acc", acc, shape)
+    handle = _stream_for(stream, q, q_off, table, lens, lse, acc, acc_out, pages.blocks)
+    _check("fg_attn_weights_q4_paged",
+           lib.fg_attn_weights_q4_paged(_ptr(q), q_stride, rows, _ptr(q_off), max_q, Hq,
+                                        C.byref(pages.struct()), _ptr(table), n, _ptr(lens), nseq,
+                                        window, sinks, scale, _ptr(lse), _ptr(acc), _ptr(acc_out),
+                                        shape[2], handle))
+
+
+def fg_kv_evict_q4_paged(pages: KVPagesQ4, table, lens, acc, recent: int, dst_table, kept, acc_out,
+                         dst_lens, stream=None):
+    """Every head of sequence b keeps its last ``recent`` positions and the heaviest others (``acc``
+    fp32 [nseq][H][n]), as many as ``kept`` (int32 [nseq][H][keep]) has room for, moved into the
+    pages of ``dst_table``; ``acc_out`` (fp32 as ``kept``) and ``dst_lens`` (int32 [nseq]) receive
+    their weights and how many stayed."""
+    nseq, n = _table("table", table)
+    nd, m = _table("dst_table", dst_table)
+    if nd != nseq or acc.dim() != 3 or kept.dim() != 3:
+        raise ValueError("table and dst_table differ in sequences, or acc or kept is not "
+                         "[nseq][H][..]")
+    _scores("acc", acc, (nseq, pages.H, acc.shape[2]))
+    keep = kept.shape[2]
+    if kept.shape != (nseq, pages.H, keep) or kept.dtype is not torch.int32 or \
+            not kept.is_contiguous():
+        raise ValueError(f"kept: contiguous int32 {(nseq, pages.H, keep)} expected, got "
+                         f"{kept.dtype} {tuple(kept.shape)}")
+    _scores("acc_out", acc_out, (nseq, pages.H, keep))
+    _extents("lens", lens, nseq)
+    _extents("dst_lens", dst_lens, nseq)
+    handle = _stream_for(stream, table, lens, acc, dst_table, kept, acc_out, dst_lens, pages.blocks)
+    _check("fg_kv_evict_q4_paged",
+           lib.fg_kv_evict_q4_paged(C.byref(pages.struct()), _ptr(table), n, nseq, _ptr(lens),
+                                    _ptr(acc), acc.shape[2], keep, recent, _ptr(dst_table), m,
+                                    _ptr(kept), _ptr(acc_out), _ptr(dst_lens), handle))
 
 
 def fg_layernorm(x, gamma, beta, eps: float, y, stream=None):

@@ -84,6 +84,34 @@ typedef struct {
   int32_t H;    /* heads; d = h / H must be 64 or 128 */
 } fg_kvcache;
 
+/* The INT4 KV cache of one layer in pages, for sequences that share one pool of memory.  blocks:
+ * device [pages][H][page * 9 * d / 8] bytes; the block of one page and head holds K codes
+ * [page][d/2], K ab [page][d/64] words, V codes, V ab, with the codes and statistics of above.
+ * Which pages a sequence has stands in a page table of the call: device int32 [nseq][table_stride],
+ * position p of sequence b being position p % page of page table[b][p / page].  The host never
+ * reads it; entries of positions that a call does not touch may hold anything, and one that names
+ * no page where a call needs it is reported by fg_check_device_error() (FG_ERR_CAPACITY).
+ * table_stride * page < 2^31 - 65536; nseq <= 65535. */
+typedef struct {
+  uint8_t* blocks;
+  int32_t pages;  /* pages of the pool */
+  int32_t page;   /* positions per page: a power of two, 16 .. 1024 */
+  int32_t h;      /* hidden size */
+  int32_t H;      /* heads; d = h / H must be 64 or 128 */
+} fg_kvpages;
+
+/* Rotary positions: a row at position p turns pairs of the first `rot` channels of a head,
+ *   y0 = x0 c - x1 s,  y1 = x0 s + x1 c,  (c, s) = angles[p][j], j < rot/2,
+ * pairs (j, j + rot/2), or (2j, 2j + 1) when interleaved; every product and sum is rounded to
+ * binary32, the result to fp16. */
+typedef struct {
+  const float* angles;  /* device [positions][rot/2][2], 16-byte aligned (fg_rope_table) */
+  const int32_t* pos;   /* device [nseq]: the position of each sequence's first row */
+  int32_t positions;    /* rows of the table */
+  int32_t rot;          /* channels of a head that turn: a multiple of 16, at most d */
+  int32_t interleaved;  /* 0 or 1 */
+} fg_rope_rows;
+
 typedef struct {
   int32_t h;      /* hidden size, multiple of 256, at most 16384 */
   int32_t H;      /* heads */
@@ -210,6 +238,100 @@ int fg_kv_append_q4_ragged(const uint16_t* k_new, const uint16_t* v_new, int64_t
  * compute] */
 int fg_kv_read_q4_ragged(const fg_kvcache* kv, const int32_t* row_off, const int32_t* pos,
                          int32_t rows, uint16_t* k_out, uint16_t* v_out, int64_t row_stride,
+                         void* stream);
+
+/* ---------------------------------------------------------------------- paged cache */
+
+/* angles[p][j] = gain * (cos, sin)(p * w_j) for p < positions, j < rot/2, computed in 64 bits and
+ * rounded once.  w_j = base^(-2j/rot), stretched for contexts longer than those of `original`
+ * positions: with r = original * w_j / 2 pi turns within them, w_j stays where r >= high, is divided
+ * by `factor` where r <= low, and goes over linearly in r between; original = 0 divides every w_j.
+ * factor = 1: no stretching.  rot even; 0 <= low <= high where original > 0.  A table is made once
+ * and serves every call (and every layer). */
+int fg_rope_table(float* angles, int32_t positions, int32_t rot, double base, double factor,
+                  int32_t original, double low, double high, double gain, void* stream);
+
+/* Rotary positions of packed rows: rows row_off[b] .. row_off[b+1]-1 of x are positions
+ * rope->pos[b], rope->pos[b] + 1, .. of sequence b; every one of `heads` heads of d channels is
+ * turned, channels behind the first rot are copied.  transpose = 1 turns by the transposed matrix
+ * (s negated): the gradient of the call, given the gradient of its output, and with a gain of 1 its
+ * inverse.  x, y: device fp16, rows x_stride and y_stride elements apart (>= heads * d, multiples of
+ * 8); y may be x with the same stride; any other overlap of their rows is refused.  d in {64, 128}.
+ * Extents are checked on the device as in fg_kv_append_q4_ragged: a row whose position the table
+ * does not hold is not written.  The pages' models learn absolute positions; no counterpart. */
+int fg_rope(const uint16_t* x, int64_t x_stride, int32_t rows, int32_t heads, int32_t d,
+            const int32_t* row_off, int32_t nseq, const fg_rope_rows* rope, int32_t transpose,
+            uint16_t* y, int64_t y_stride, void* stream);
+
+/* fg_kv_append_q4_ragged into pages: rows row_off[b] .. row_off[b+1]-1 of k_new and v_new go to
+ * positions pos[b], pos[b] + 1, .. of sequence b.  rope (nullable): K is turned first, as fg_rope
+ * would, and quantised from the fp16 values that gives; rope->pos NULL means pos (they differ once
+ * a cache has been made smaller).  Two rows that name the same place of the same page are a fault of
+ * the caller (one of them is stored). */
+int fg_kv_append_q4_paged(const uint16_t* k_new, const uint16_t* v_new, int64_t row_stride,
+                          int32_t rows, const int32_t* row_off, const int32_t* pos,
+                          const fg_rope_rows* rope, const fg_kvpages* kv, const int32_t* table,
+                          int64_t table_stride, int32_t nseq, void* stream);
+
+/* fg_kv_read_q4_ragged from pages. */
+int fg_kv_read_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
+                        int32_t nseq, const int32_t* row_off, const int32_t* pos, int32_t rows,
+                        uint16_t* k_out, uint16_t* v_out, int64_t row_stride, void* stream);
+
+/* Attention of the newest tokens of every sequence over its pages, one token or many: sequence b
+ * has query rows q_off[b] .. q_off[b+1]-1 (nq of them, at most max_q) and lens[b] cached positions,
+ * those of its query rows included (append first); query row r of them is position
+ * i = lens[b] - nq + r, and
+ *   out[row][hq*d + j] = sum_t softmax_t(scale * q_row,hq . K^_hk,t) V^_hk,t,j   over the visible t
+ * (visible: as stated below for the windowed calls), hk = hq / (Hq / H), Hq a multiple of H, at
+ * most 128 times H, K^ and V^ the fp16 restorations of the codes.  A row that sees nothing gets 0.
+ * lse (nullable): device fp32 [q_rows][Hq], the logarithm of the row's sum of exp(score), -inf for
+ * a row that sees nothing.  q, out: device fp16, q_rows rows q_stride and out_stride elements apart
+ * (>= Hq*d, multiples of 8); out may be q with the same stride; any other overlap is refused.
+ * q_off: device int32 [nseq+1], not decreasing, within 0 .. q_rows; lens: device int32 [nseq], at
+ * most what a row of the table names; checked on the device (the rows of a sequence that does not
+ * fit stay as they were; those of one with a bad page hold nothing of use;
+ * fg_check_device_error() returns FG_ERR_CAPACITY).  Rows outside every sequence stay as they were.
+ * Values of positions that a row does not see never reach it, not even infinities and NaN.  ws:
+ * device scratch of at least fg_attn_paged_workspace_bytes(kv, Hq, max_q) bytes, whatever the
+ * lengths; two calls in flight at once need workspaces of their own. */
+int fg_attn_q4kv_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows, const int32_t* q_off,
+                       int32_t max_q, int32_t Hq, const fg_kvpages* kv, const int32_t* table,
+                       int64_t table_stride, const int32_t* lens, int32_t nseq, int32_t window,
+                       int32_t sinks, float scale, uint16_t* out, int64_t out_stride, float* lse,
+                       void* ws, size_t ws_bytes, void* stream);
+/* Scratch bytes of fg_attn_q4kv_paged (planned for up to 192 SMs).  Host computation only; 0 for
+ * invalid arguments. */
+size_t fg_attn_paged_workspace_bytes(const fg_kvpages* kv, int32_t Hq, int32_t max_q);
+
+/* The softmax weights that cached positions receive from given queries:
+ *   acc_out[b][hk][t] = acc[b][hk][t] + sum exp(scale * q_row,hq . K^_hk,t - lse[row][hq])
+ * over sequence b's query rows that see t and the query heads of hk, for t < lens[b]; everything
+ * else of acc_out stays as it was.  acc (nullable: zeros) and acc_out: device fp32
+ * [nseq][H][acc_stride], lens[b] <= acc_stride; acc_out may be acc.  lse: as fg_attn_q4kv_paged
+ * gives it; rows of -inf add nothing.  Sums are taken in one order whatever else runs.  The other
+ * arguments as there. */
+int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows,
+                             const int32_t* q_off, int32_t max_q, int32_t Hq, const fg_kvpages* kv,
+                             const int32_t* table, int64_t table_stride, const int32_t* lens,
+                             int32_t nseq, int32_t window, int32_t sinks, float scale,
+                             const float* lse, const float* acc, float* acc_out,
+                             int64_t acc_stride, void* stream);
+
+/* Caches of at most `keep` positions: every K/V head of sequence b keeps its last `recent`
+ * positions (<= keep) and, of the others, the keep - recent with the largest acc (equal ones: the
+ * lower position first; NaN orders above +inf), or everything when lens[b] <= keep.  What stays is
+ * moved, in order of position, to positions 0, 1, .. of the pages that dst_table names: pages of the
+ * same pool that no sequence of `table` uses (afterwards the old pages are free).  kept: device
+ * int32 [nseq][H][keep], the positions that stay, -1 behind them; acc_out: device fp32
+ * [nseq][H][keep], their acc, 0 behind them; dst_lens: device int32 [nseq], min(lens[b], keep).
+ * Heads keep different positions: a cached position no longer says when its token came, so later
+ * rows give fg_kv_append_q4_paged a rope->pos of their own.  keep <= dst_stride * page
+ * (FG_ERR_CAPACITY).  acc as in fg_attn_weights_q4_paged. */
+int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
+                         int32_t nseq, const int32_t* lens, const float* acc, int64_t acc_stride,
+                         int32_t keep, int32_t recent, const int32_t* dst_table,
+                         int64_t dst_stride, int32_t* kept, float* acc_out, int32_t* dst_lens,
                          void* stream);
 
 /* ---------------------------------------------------------------------- attention */
@@ -397,7 +519,11 @@ enum {
   FG_K_DECODE_ATTN_WINDOW = 14,  /* fg_decode_attn_q4kv_window, all its kernels: bytes */
   FG_K_PREFILL_ATTN_WINDOW = 15, /* fg_prefill_attn_window: bytes of its rows (not its flops: how
                                     many pairs are visible stands in the device arrays) */
-  FG_K_COUNT = 16
+  FG_K_ROPE = 16,                /* fg_rope: bytes */
+  FG_K_ATTN_PAGED = 17,          /* fg_attn_q4kv_paged, all its kernels: bytes */
+  FG_K_ATTN_WEIGHTS = 18,        /* fg_attn_weights_q4_paged: bytes */
+  FG_K_KV_EVICT = 19,            /* fg_kv_evict_q4_paged, both kernels: bytes */
+  FG_K_COUNT = 20
 };
 int fg_prof_enable(int on);
 int fg_prof_reset(void);

@@ -1,0 +1,57 @@
+"""Shared helpers of the paged cache's GPU tests: pools of pages, their contents and sequences."""
+import numpy as np
+import torch
+
+import fg_synth
+from oracle import quant as OQ
+
+H16 = 2.0 ** -11          # half a step of fp16, relative
+F32 = 2.0 ** -23          # one binary32 operation, rounded or truncated, relative
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def offsets(lens, first=0):
+    return np.concatenate([[first], first + np.cumsum(lens)]).astype(int).tolist()
+
+
+def tables(need, seed, spare=2, first=0):
+    """Page tables (numpy) of sequences that need so many pages, in a shuffled order, unused entries
+    bad (-7); and the pages of the pool."""
+    pages = sum(need) + spare + first
+    order = iter(np.random.default_rng(seed).permutation(pages - first) + first)
+    t = np.full((len(need), max(1, max(need, default=1))), -7, np.int32)
+    for b, n in enumerate(need):
+        t[b, :n] = [next(order) for _ in range(n)]
+    return t, pages
+
+
+def fill(fg, pages, P, H, d, seed, scale=1.0):
+    """A pool of pages of quantised normal values, and their restored values [pages][H][P][d] of K
+    and of V."""
+    pool = fg.KVPagesQ4(pages, P, H * d, H)
+    vals = []
+    for codes_t, ab_t, sd in zip(pool.parts()[0::2], pool.parts()[1::2], (0, 1)):
+        x = fg_synth.random_fp16((pages * H * P, d), seed=seed * 2 + sd, scale=scale,
+                                 offset=0.2 * scale)
+        q, a, b = OQ.quantize_g64(x)
+        codes_t.copy_(torch.from_numpy(OQ.pack_nibbles(q)).cuda().view(codes_t.shape))
+        ab = np.stack([a, b], -1).reshape(pages, H, P, d // 64, 2)
+        ab_t.copy_(torch.from_numpy(ab).cuda())
+        vals.append(OQ.dequant_g64(q, a, b).reshape(pages, H, P, d))
+    return pool, vals[0], vals[1]
+
+
+def rows_of(vals, table, b, n):
+    """Values [H][n][d] of sequence b's first n positions, from values by page."""
+    P = vals.shape[2]
+    if n == 0:
+        return np.zeros((vals.shape[1], 0, vals.shape[3]), vals.dtype)
+    x = vals[table[b, :(n + P - 1) // P]]                    # [pages][H][P][d]
+    return np.moveaxis(x, 0, 1).reshape(x.shape[1], -1, x.shape[3])[:, :n]
+
+
+def need(lens, P):
+    return [(n + P - 1) // P for n in lens]
