@@ -1,11 +1,52 @@
-// Attention of the newest tokens of every sequence over the paged 4-bit cache, and the softmax
-// weights that cached positions receive (sm_103a): plain forms, a warp per query row and head, a
-// warp per cached position.
+// Attention of the newest tokens of every sequence over the paged 4-bit cache, on the
+// 5th-generation tensor cores (sm_103a).
+//
+// Query row r of sequence b (nq rows, n cached positions) is position i = n - nq + r, and
+//   out_r,hq = sum_t softmax_t(scale * q_r,hq . k^_t) v^_t   over the t that i sees,
+// K/V head hq / G of G = Hq / H query heads each.  The rows of a product are a K/V head's tokens' G
+// heads, so that a key tile is restored once for all of them (paged_work.cuh: row tiles, blocks,
+// the order of the work, its even split into shares and the pieces of a block that a share cuts).
+//
+// A CTA owns a share.  For a block of two row tiles, chain A and chain B take one each and share
+// the key tiles; for a block of one, they hold the same rows and take the key tiles in turn, joined
+// at the end.  Per key tile of 128 positions:
+//   codes         one bulk copy per page and half (K or V: codes and statistics lie side by side)
+//                 into a ring of parts
+//   restore       four warps write the part as fp16 into the tensor core's 128B-swizzled tiles: a
+//                 nibble under fp16's exponent 2^10, q - 8 exactly, and one fused (q - 8) s + (a +
+//                 8 s) with s = (b - a) / 15 and a + 8 s rounded to fp16: within 3.1 half steps of
+//                 the group's largest magnitude M (8 s <= 1.07 M).  V's channels keep the order in
+//                 which the nibbles lie in a word (0,4,1,5,2,6,3,7), which the output undoes.
+//                 Rows behind the sequence become 0.
+//   S = Q K^T     tcgen05.mma kind::f16, fp32 in TMEM
+//   softmax       one thread per row, two passes over its 128 columns (the maximum, then P): base-2
+//                 online softmax with a lazily moved reference maximum (by more than 2^8), P =
+//                 2^(s - m + 7) rounded to fp16 over S's columns
+//   O += P V      tcgen05.mma with P from TMEM
+//   warp 0        page table lookups and bulk copies
+//   warps 1, 2    MMA issuers of chains A and B
+//   warp 3        the share's segments, handed to the others through a ring; Q by TMA
+//   warps 4-11    softmax of A and B (TMEM lanes 32 (w % 4) ..), and their output
+//   warps 12-15   restore
+// A second kernel puts cut blocks together, piece after piece in order.
+//
+// Masked positions have P = 0, but 0 times an infinity or NaN in V is NaN: rows that end with one
+// are computed again over what they see alone (attend_row).  Rows whose sum of weights is NaN have
+// their answer.
+//
+// Every wait is bounded; on timeout the CTA sets the device error word, drains its copies and MMAs
+// and frees TMEM.
 #include <math.h>
 
+#include <algorithm>
+#include <mutex>
+
+#include "attn_tc.cuh"
 #include "fg_common.cuh"
 #include "fg_internal.h"
+#include "gemm_tc.cuh"
 #include "paged.cuh"
+#include "paged_work.cuh"
 #include "q4_restore.cuh"
 #include "ragged.cuh"
 
@@ -15,23 +56,33 @@ __device__ unsigned int g_paged_attn_error = 0;
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int THREADS = 16 * 32;
+constexpr int W_MMA = 1, W_SEG = 3, W_SM = 4, W_RST = 12;
+constexpr int RST_THREADS = 128;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int BOX = 128 * 128;             // bytes of one 64-column x 128-row box
+constexpr int SEGS = 4;                    // ring of segments
+constexpr int MAX_PARTS = 12;              // ring of parts (K or V codes of a key tile)
+constexpr long long kWaitCycles = 1ll << 36;   // attend_row may keep the other warps waiting
+constexpr long long kDrainCycles = 1ll << 32;  // for copies and products in flight
+constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
+constexpr float kLag = 8.0f;               // base-2 score by which a row may pass its reference
+constexpr float kPExp = 7.0f;              // P is scaled by 2^7, as its row sum is: P <= 2^15, and
+                                           // down to 2^-21 of the reference's P normal in fp16
 
+// ---------------------------------------------------------------- extents and rows
+
+__device__ __forceinline__ bool extent_of(const PagedAttn& a, int b, PagedSeq& e) {
+  const int q0 = a.q_off[b], q1 = a.q_off[b + 1], n = a.lens[b];
+  if (q0 < 0 || q0 > q1 || q1 > a.q_rows || q1 - q0 > a.max_q || n < 0 || n > a.cache.cap())
+    return false;
+  e = PagedSeq{q0, q1 - q0, n};
+  return true;
+}
 __device__ __forceinline__ float restored(uint32_t code, uint32_t abw) {
   const float2 ab = unpack_h2(abw);
   const float s = __fdiv_rn(__fsub_rn(ab.y, ab.x), 15.0f);
   return h2f(f2h(__fadd_rn(ab.x, __fmul_rn((float)code, s))));
-}
-// Whether sequence b's extents fit; its query rows, first row and length.
-struct Extent {
-  int q0, nq, n;
-};
-__device__ __forceinline__ bool extent_of(const PagedAttn& a, int b, Extent& e) {
-  const int q0 = a.q_off[b], q1 = a.q_off[b + 1], n = a.lens[b];
-  if (q0 < 0 || q0 > q1 || q1 > a.q_rows || q1 - q0 > a.max_q || n < 0 || n > a.cache.cap())
-    return false;
-  e = Extent{q0, q1 - q0, n};
-  return true;
 }
 // The K (which 0) or V (1) row of one position and head; null for a bad page.
 template <int D>
@@ -47,70 +98,1127 @@ __device__ __forceinline__ const uint8_t* row_of(const PagedCache& c, int b, int
   *ab = reinterpret_cast<const uint32_t*>(k + ((int64_t)(D / 2) << c.lg)) + at * (D / 64);
   return k + at * (D / 2);
 }
+__device__ __forceinline__ float in_range(float y) {
+  return fabsf(y) < 66000.0f ? fminf(fmaxf(y, -65504.0f), 65504.0f) : y;
+}
 
+// One row on its own, by a whole warp, over the positions that it sees of key tiles j0 .. j1 - 1:
+// a position per lane for the scores, channels lane * D/32 .. for the values.  o: unnormalised; m,
+// l in the base-2 scale of the kernel.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attend_kernel(const PagedAttn a) {
-  __shared__ float qs[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
-  if (w >= (int64_t)a.q_rows * a.Hq) return;
-  const int row = (int)(w / a.Hq), hq = (int)(w % a.Hq), hk = hq / (a.Hq / a.cache.H);
-  const int b = sequence_of_row(a.q_off, a.cache.B, row);
-  Extent e;
-  if (b < 0) return;
-  if (!extent_of(a, b, e)) {
-    atomicOr(&g_paged_attn_error, kErrExtent);
-    return;
-  }
-  const int i = e.n - e.nq + row - e.q0;
-  const uint16_t* q = a.q + row * a.q_stride + (int64_t)hq * D;
-  for (int j = lane; j < D; j += 32) qs[warp][j] = h2f(q[j]) * a.scale;
-  __syncwarp();
+__device__ __noinline__ void attend_row(const PagedAttn& a, const PagedSeg& g, const uint16_t* q,
+                                        int i, float (&o)[D / 32], float& m, float& l) {
   constexpr int C = D / 32;
-  float m = -INFINITY, l = 0.0f, o[C] = {};
-  for (int t0 = 0; t0 <= i; t0 += 32) {
-    const int t = t0 + lane;
-    const bool vis = visible(t, i, a.window, a.sinks);
-    float s = -INFINITY;
-    const uint32_t* ab;
-    if (vis) {
-      const uint8_t* k = row_of<D>(a.cache, b, hk, t, 0, &ab);
-      s = 0.0f;
-      for (int j = 0; k && j < D / 2; ++j)
-        s += qs[warp][2 * j] * restored(k[j] & 15u, ab[j / 32]) +
-             qs[warp][2 * j + 1] * restored(k[j] >> 4, ab[j / 32]);
-    }
-    float mx = s;
-    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-    mx = fmaxf(mx, m);
-    const float ref = mx == -INFINITY ? 0.0f : mx, corr = __expf(m - ref);
-    const float p = vis ? __expf(s - ref) : 0.0f;
-    l = l * corr + p;
-    m = mx;
-    for (int c = 0; c < C; ++c) o[c] *= corr;
-    for (int u = 0; u < 32; ++u) {
-      if (!__shfl_sync(0xFFFFFFFFu, vis, u)) continue;
-      const float pu = __shfl_sync(0xFFFFFFFFu, p, u);
-      const uint8_t* v = row_of<D>(a.cache, b, hk, t0 + u, 1, &ab);
-      for (int c = 0; v && c < C; ++c) {
-        const int ch = lane * C + c;
-        o[c] += pu * restored(v[ch / 2] >> (4 * (ch & 1)) & 15u, ab[ch / 64]);
+  const int lane = threadIdx.x & 31;
+  const float sl2 = a.scale * 1.4426950408889634f;
+  m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = 0.0f;
+#pragma unroll 1
+  for (int j = g.j0; j < g.j1; ++j) {
+#pragma unroll 1
+    for (int t0 = g.kt.tile(j) * kKeyTile, e = t0 + kKeyTile; t0 < e; t0 += 32) {
+      const int t = t0 + lane;
+      const bool vis = i >= 0 && visible(t, i, a.window, a.sinks);
+      if (!__any_sync(0xFFFFFFFFu, vis)) continue;
+      float s = -INFINITY;
+      const uint32_t* ab;
+      if (vis) {
+        const uint8_t* k = row_of<D>(a.cache, g.b, g.hk, t, 0, &ab);
+        s = 0.0f;
+#pragma unroll 1
+        for (int c = 0; k && c < D / 2; ++c)
+          s += h2f(q[2 * c]) * restored(k[c] & 15u, ab[c / 32]) +
+               h2f(q[2 * c + 1]) * restored(k[c] >> 4, ab[c / 32]);
+        s *= sl2;
+      }
+      float mx = s;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+      mx = fmaxf(mx, m);
+      const float ref = mx == -INFINITY ? 0.0f : mx, corr = ex2(m - ref);
+      const float p = vis ? ex2(s - ref + kPExp) : 0.0f;
+      l = l * corr + p;
+      m = mx;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] *= corr;
+#pragma unroll 1
+      for (int u = 0; u < 32; ++u) {
+        if (!__shfl_sync(0xFFFFFFFFu, vis, u)) continue;
+        const float pu = __shfl_sync(0xFFFFFFFFu, p, u);
+        const uint8_t* v = row_of<D>(a.cache, g.b, g.hk, t0 + u, 1, &ab);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const int ch = lane * C + c;
+          if (v) o[c] += pu * restored(v[ch / 2] >> (4 * (ch & 1)) & 15u, ab[ch / 64]);
+        }
       }
     }
   }
+#pragma unroll
   for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-  uint16_t* out = a.out + row * a.out_stride + (int64_t)hq * D;
-  for (int c = 0; c < C; ++c) out[lane * C + c] = f2h(l == 0.0f ? 0.0f : o[c] / l);
-  if (a.lse && lane == 0) a.lse[(int64_t)row * a.Hq + hq] = l == 0.0f ? -INFINITY : m + logf(l);
+}
+
+// ---------------------------------------------------------------- the kernel
+
+struct PArgs {
+  PagedAttn a;
+  float scale_log2;
+  int G, tpt;
+  int parts;           // depth of the ring of parts
+  int two;             // blocks of two row tiles occur: Q_B has a buffer
+  int min_units;       // of a share
+  int slot_rows;       // rows of a partial slot
+  PagedCut* cuts;      // [grid]
+  float* partial;      // [2 * grid][slot_rows][D], then maxima and sums [2 * grid][slot_rows][2]
+};
+
+// K stages, V stages, Q_A, (Q_B,) parts; barriers and rings behind them.
+template <int D>
+struct Smem {
+  static constexpr int TILE = (D / 64) * BOX;
+  static constexpr int PART = 128 * (9 * D / 16);
+  static constexpr int K_OFF = 0, V_OFF = 2 * TILE, Q_OFF = 4 * TILE;
+  static constexpr int CTRL = 512 + SEGS * 64 + 2 * 128 * 4;      // barriers, segments, B's m and l
+  __host__ __device__ static constexpr int part_off(int two) { return Q_OFF + (1 + two) * TILE; }
+  __host__ __device__ static constexpr int ctrl_off(int two, int parts) {
+    return part_off(two) + parts * PART;
+  }
+  static constexpr int bytes(int two, int parts) { return ctrl_off(two, parts) + CTRL + 1024; }
+  static constexpr int depth(int two) {
+    int n = MAX_PARTS;
+    while (bytes(two, n) > 227 * 1024) --n;
+    return n;
+  }
+};
+static_assert(Smem<128>::depth(1) >= 3 && Smem<128>::depth(0) >= 6, "room for codes in flight");
+
+constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_QFULL = 2 * MAX_PARTS, B_QFREE = B_QFULL + 2,
+              B_KFULL = B_QFREE + 2, B_KFREE = B_KFULL + 2, B_VFULL = B_KFREE + 2,
+              B_VFREE = B_VFULL + 2, B_SFULL = B_VFREE + 2, B_PFULL = B_SFULL + 2,
+              B_ODONE = B_PFULL + 2, B_OFREE = B_ODONE + 2, B_LFULL = B_OFREE + 2,
+              B_GFULL = B_LFULL + 1, B_GFREE = B_GFULL + SEGS, B_DRAIN = B_GFREE + SEGS,
+              NBARS = B_DRAIN + 2;
+static_assert(NBARS * 8 + 16 <= 512 && sizeof(PagedSeg) <= 64, "control space");
+
+__device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      atomicOr(&g_paged_attn_error, kErrWait);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (clock64() - t0 > kDrainCycles) {
+      atomicOr(&g_paged_attn_error, kErrDrain);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y,
+                                            int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Tokens of row tile t of a block, and whether it takes part in key tile number j.
+__device__ __forceinline__ int tile_tokens(const PagedSeg& g, int t, int tpt) {
+  return g.single ? g.ntok : (t ? g.ntok - tpt : tpt);
+}
+__device__ __forceinline__ bool takes_part(const PagedSeg& g, int t, int j, int tpt, int window,
+                                           int sinks) {
+  if (g.single) return ((j - g.j0) & 1) == t;
+  const int lo = g.pos + t * tpt;
+  return span_sees(g.kt.tile(j), lo, lo + tile_tokens(g, t, tpt) - 1, window, sinks);
+}
+
+// 8 codes of a word times s plus c8 = a + 8 s, in the channels' order (K) or in the nibbles' (V).
+__device__ __forceinline__ uint32_t hadd2_u32(uint32_t x, uint32_t y) {
+  const __half2 r = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint4 restore_natural(uint32_t w, uint32_t s, uint32_t c8) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = (__byte_perm(w, 0, 0x1111 * i) & 0x00F0000Fu) | 0x64006400u;
+    // (1024 + q0, 1024 + 16 q1) -> (q0 - 8, q1 - 8)
+    o[i] = hfma2_u32(hfma2_u32(u, 0x2C003C00u, 0xD480E408u), s, c8);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 restore_permuted(uint32_t w, uint32_t s, uint32_t c8) {
+  const uint32_t w8 = w >> 8;
+  uint4 o;
+  o.x = hfma2_u32(hadd2_u32((w & 0x000F000Fu) | 0x64006400u, 0xE408E408u), s, c8);
+  o.y = hfma2_u32(hfma2_u32((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), s, c8);
+  o.z = hfma2_u32(hadd2_u32((w8 & 0x000F000Fu) | 0x64006400u, 0xE408E408u), s, c8);
+  o.w = hfma2_u32(hfma2_u32((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), s, c8);
+  return o;
+}
+
+// A part of `valid` positions from a ring stage into an fp16 tile, by the restore warps: 16 bytes
+// of codes (32 channels) per thread and turn.  Neighbouring threads hold neighbouring code bytes;
+// the upper 64 channels' threads take their words in another order, so that the 16-byte stores of 8
+// threads meet all banks.
+template <int D, bool V>
+__device__ __forceinline__ void restore_part(const uint8_t* part, uint32_t tile, int lgb, int valid,
+                                             int tid) {
+  constexpr int CH = D / 32;               // chunks of 32 channels per row
+#pragma unroll 2
+  for (int it = 0; it < 128 * CH / RST_THREADS; ++it) {
+    const int idx = it * RST_THREADS + tid, row = idx / CH, q = idx % CH;
+    const uint8_t* sub = part + (((row >> lgb) * (9 * D / 16)) << lgb);
+    const int r = row & ((1 << lgb) - 1);
+    uint4 w = *reinterpret_cast<const uint4*>(sub + r * (D / 2) + q * 16);
+    const uint32_t abw = *reinterpret_cast<const uint32_t*>(sub + ((D / 2) << lgb) + r * (D / 16) +
+                                                            (q >> 1) * 4);
+    const float2 ab = unpack_h2(abw);
+    const float s = (ab.y - ab.x) * (1.0f / 15.0f);
+    const float c = fmaf(8.0f, s, ab.x);
+    const uint32_t s2 = pack_h2(s, s), c2 = pack_h2(c, c);
+    const int flip = (q >> 1) << 1;        // words 0, 1, 2, 3, or 2, 3, 0, 1
+    if (flip) w = make_uint4(w.z, w.w, w.x, w.y);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t base = tile + (q >> 1) * BOX + row * 128;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 o = V ? restore_permuted(ww[i], s2, c2) : restore_natural(ww[i], s2, c2);
+      if (row >= valid) o = make_uint4(0, 0, 0, 0);
+      const int chunk = (q & 1) * 4 + (i ^ flip);
+      st_shared_v4(base + ((chunk ^ (row & 7)) << 4), o.x, o.y, o.z, o.w);
+    }
+  }
+}
+
+// 32 output columns in the nibbles' order -> 4 x 8 fp16 channels, times f.
+__device__ __forceinline__ uint4 pack_channels(const float* o, float f) {
+  return make_uint4(pack_h2(in_range(o[0] * f), in_range(o[2] * f)),
+                    pack_h2(in_range(o[4] * f), in_range(o[6] * f)),
+                    pack_h2(in_range(o[1] * f), in_range(o[3] * f)),
+                    pack_h2(in_range(o[5] * f), in_range(o[7] * f)));
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ PArgs pa) {
+  using L = Smem<D>;
+  constexpr int NB = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* ctrl = smem + L::ctrl_off(pa.two, pa.parts);
+  const uint32_t bar0 = smem_u32(ctrl);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + NBARS * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto seg_slot = [&](int n) { return reinterpret_cast<PagedSeg*>(ctrl + 512 + 64 * (n % SEGS)); };
+  float* ml_b = reinterpret_cast<float*>(ctrl + 512 + SEGS * 64);   // chain B's maxima and sums
+  __shared__ int64_t warp_units[THREADS / 32];
+  __shared__ int first_b;                  // the sequence of the share's first unit, and
+  __shared__ int64_t first_before;         // the units before it
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedAttn& a = pa.a;
+  const PagedShape shape{pa.tpt, a.window, a.sinks};
+  const int nseq = a.cache.B, H = a.cache.H;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < MAX_PARTS; ++i) {
+      mbar_init(bar(B_CFULL + i), 1);
+      mbar_init(bar(B_CFREE + i), 4);      // one arrival per restore warp
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_QFULL + i), 1);
+      mbar_init(bar(B_QFREE + i), 2);      // two arrivals of the issuers' per use of a buffer
+      mbar_init(bar(B_KFULL + i), 4);
+      mbar_init(bar(B_KFREE + i), 2);
+      mbar_init(bar(B_VFULL + i), 4);
+      mbar_init(bar(B_VFREE + i), 2);
+      mbar_init(bar(B_SFULL + i), 1);
+      mbar_init(bar(B_PFULL + i), 4);      // one arrival per softmax warp
+      mbar_init(bar(B_ODONE + i), 1);
+      mbar_init(bar(B_OFREE + i), 4);
+      mbar_init(bar(B_DRAIN + i), 1);
+    }
+    mbar_init(bar(B_LFULL), 4);
+    for (int i = 0; i < SEGS; ++i) {
+      mbar_init(bar(B_GFULL + i), 1);
+      mbar_init(bar(B_GFREE + i), 1 + 2 + 8 + 4);      // every other warp
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- the order of the work: its units, and where this share's begin
+  int64_t total = 0, before = 0, incl = 0, mine = 0;
+  auto scan_round = [&](int b0) {          // a sequence per thread: its units, those up to it
+    const int b = b0 + threadIdx.x;
+    mine = 0;
+    if (b < nseq) {
+      PagedSeq s;
+      if (extent_of(a, b, s))
+        mine = H * head_units(s, shape);
+      else if (blockIdx.x == 0)
+        atomicOr(&g_paged_attn_error, kErrExtent);
+    }
+    incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) warp_units[warp] = incl;
+    __syncthreads();
+    int64_t round = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+      const int64_t n = warp_units[i];
+      if (i < warp) incl += n;
+      round += n;
+    }
+    __syncthreads();
+    return round;
+  };
+  for (int b0 = 0; b0 < nseq; b0 += THREADS) total += scan_round(b0);
+  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, total / pa.min_units));
+  const Shares shares(total, n_shares);
+  const int share = blockIdx.x;
+  const bool busy = total > 0 && share < n_shares;
+  const int64_t x0 = busy ? shares.first(share) : 0, x1 = busy ? shares.first(share + 1) : 0;
+  if (busy) {
+    for (int b0 = 0; b0 < nseq; b0 += THREADS) {
+      const int64_t round = nseq > THREADS ? scan_round(b0) : total;
+      if (before + round > x0) {
+        if (before + incl > x0 && before + incl - mine <= x0) {
+          first_b = b0 + threadIdx.x;
+          first_before = before + incl - mine;
+        }
+        break;
+      }
+      before += round;
+    }
+  }
+  if (!busy && threadIdx.x == 0) pa.cuts[share].pieces = 0;
+  // rows before the first position see nothing
+  for (int b = blockIdx.x; b < nseq; b += gridDim.x) {
+    PagedSeq s;
+    if (!extent_of(a, b, s) || s.nq <= s.n) continue;
+    const int64_t words = (int64_t)a.Hq * D / 8;
+    for (int64_t i = threadIdx.x; i < (s.nq - s.n) * words; i += THREADS) {
+      const int64_t row = s.q0 + i / words;
+      reinterpret_cast<uint4*>(a.out + row * a.out_stride)[i % words] = make_uint4(0, 0, 0, 0);
+    }
+    if (a.lse)
+      for (int64_t i = threadIdx.x; i < (int64_t)(s.nq - s.n) * a.Hq; i += THREADS)
+        a.lse[(int64_t)s.q0 * a.Hq + i] = -INFINITY;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM columns: S_A 0..127, S_B 128..255, O_A 256.., O_B 256 + D..
+  auto s_col = [&](int t) { return (uint32_t)(t * KT); };
+  auto o_col = [&](int t) { return (uint32_t)(2 * KT + t * D); };
+  const int lgb = min(a.cache.lg, 7);      // positions of a page within one key tile: 2^lgb
+  auto seg_wait = [&](int n) -> bool {
+    const bool got = bwait(bar(B_GFULL + n % SEGS), (uint32_t)((n / SEGS) & 1), abort_flag);
+    return __all_sync(0xFFFFFFFFu, got);
+  };
+  auto seg_done = [&](int n) { mbar_arrive(bar(B_GFREE + n % SEGS)); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ codes
+    int np = 0;                                        // parts issued
+    bool ok = true;
+    const int subs = 128 >> lgb;
+    for (int n = 0; ok; ++n) {
+      if (!seg_wait(n)) break;
+      const PagedSeg g = *seg_slot(n);
+      __syncwarp();
+      if (lane == 0) seg_done(n);
+      if (g.b < 0) break;
+      // lane l holds the block of the page of positions l * 2^lgb .. of a key tile
+      auto lookup = [&](int j) -> int64_t {
+        const int64_t t = (int64_t)g.kt.tile(j) * kKeyTile + ((int64_t)lane << lgb);
+        return lane < subs && t < g.n ? a.cache.slot(g.b, t) : -2;
+      };
+      int64_t slot = lookup(g.j0);
+      for (int j = g.j0; j < g.j1 && ok; ++j) {
+        const int64_t at = slot;
+        if (j + 1 < g.j1) slot = lookup(j + 1);        // in flight meanwhile
+        if (at == -1) atomicOr(&g_paged_attn_error, kErrExtent);
+        const unsigned live = __ballot_sync(0xFFFFFFFFu, at >= 0);
+        for (int which = 0; which < 2; ++which, ++np) {
+          const int st = np % pa.parts;
+          if (np >= pa.parts) {
+            const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((np / pa.parts - 1) & 1),
+                                  abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, fr)) {
+              ok = false;
+              break;
+            }
+          }
+          const uint32_t bytes = (uint32_t)(9 * D / 16) << lgb;
+          if (lane == 0) {
+            // the stage was last read through the generic proxy; order that before the copies
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_expect_tx(bar(B_CFULL + st), bytes * __popc(live));
+          }
+          __syncwarp();
+          if (at >= 0) {
+            const uint32_t dst = smem_u32(smem + L::part_off(pa.two) + st * L::PART) + lane * bytes;
+            const uint8_t* src = a.cache.block(at, g.hk, D) + which * a.cache.half_bytes(D);
+            if (a.cache.lg <= 7) {
+              bulk_copy(dst, src, bytes, bar(B_CFULL + st));
+            } else {                                   // a key tile's piece of a longer page
+              const int64_t r = at & ((1 << a.cache.lg) - 1);
+              bulk_copy(dst, src + r * (D / 2), 128 * (D / 2), bar(B_CFULL + st));
+              bulk_copy(dst + 128 * (D / 2), src + ((int64_t)(D / 2) << a.cache.lg) + r * (D / 16),
+                        128 * (D / 16), bar(B_CFULL + st));
+            }
+          }
+        }
+      }
+    }
+    // every issued copy has landed before the CTA exits
+    if (lane == 0)
+      for (int i = max(0, np - pa.parts); i < np; ++i)
+        drain_wait(bar(B_CFULL + i % pa.parts), (uint32_t)((i / pa.parts) & 1));
+    __syncwarp();
+  } else if (warp < W_SEG) {
+    // ------------------------------------------------------------ MMA issuer of chain t
+    // Both chains go through the K and V stages of every key tile in order, and release each: a
+    // parity wait cannot tell a use of a stage from the next but one, so neither may fall two behind.
+    const int t = __shfl_sync(0xFFFFFFFFu, warp - W_MMA, 0);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), sbase = smem_u32(smem);
+    const uint32_t one = elect_one();
+    const uint32_t od = tm + o_col(t), scol = tm + s_col(t);
+    const uint32_t idesc_o = idesc_pv(D);
+    int g0 = 0;                                        // key tiles before the segment
+    int q_uses[2] = {0, 0}, pc = 0, uses = 0;          // Q loads; P products; segments with tiles
+    bool ok = true;
+    auto wait = [&](int b, int parity) {
+      ok = ok && __all_sync(0xFFFFFFFFu, bwait(bar(b), (uint32_t)parity, abort_flag));
+    };
+    auto commit = [&](int b) { umma_commit_if(bar(b), one); };
+    auto arrive = [&](int b) {
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    for (int n = 0; ok; ++n) {
+      if (!seg_wait(n)) break;
+      const PagedSeg g = *seg_slot(n);
+      __syncwarp();
+      if (lane == 0) seg_done(n);
+      if (g.b < 0) break;
+      const int qb = g.single ? 0 : t;                 // the chain's Q buffer
+      const uint64_t qd = smem_desc(sbase + L::Q_OFF + qb * L::TILE, 16, 1024);
+      wait(B_QFULL, q_uses[0]++ & 1);
+      if (!g.single) {
+        if (t == 1) wait(B_QFULL + 1, q_uses[1] & 1);
+        ++q_uses[1];
+      }
+      if (!ok) break;
+      auto own = [&](int j) { return takes_part(g, t, j, pa.tpt, a.window, a.sinks); };
+      auto next_own = [&](int j) {
+        while (j < g.j1 && !own(j)) ++j;
+        return __shfl_sync(0xFFFFFFFFu, j, 0);
+      };
+      // waits for the stages of key tiles seen .. j, of which all but j are the other chain's
+      int k_seen = g.j0, v_seen = g.j0;
+      auto wait_to = [&](int& seen, int j, int full, int free) {
+        for (; seen < j; ++seen) {
+          const int x = g0 + seen - g.j0;
+          wait(full + (x & 1), (x >> 1) & 1);
+          if (ok) arrive(free + (x & 1));
+        }
+        if (j < g.j1) {
+          const int x = g0 + j - g.j0;
+          wait(full + (x & 1), (x >> 1) & 1);
+          ++seen;
+        }
+      };
+      auto issue_s = [&](int j) {
+        const int st = (g0 + j - g.j0) & 1;
+        const uint64_t kd = smem_desc(sbase + L::K_OFF + st * L::TILE, 16, 1024);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
+          umma_f16_if(scol, qd + off, kd + off, kIdescS, i > 0, one);
+        }
+        commit(B_SFULL + t);
+        commit(B_KFREE + st);
+      };
+      auto issue_pv = [&](int j, uint32_t add) {
+        const int st = (g0 + j - g.j0) & 1;
+        const uint64_t vd = smem_desc(sbase + L::V_OFF + st * L::TILE, BOX, 1024);
+        umma_ts_if(od, scol, vd, idesc_o, add, one);
+#pragma unroll
+        for (int i = 1; i < KT / 16; ++i)
+          umma_ts_if(od, scol + 32 * (i >> 1) + 8 * (i & 1), vd + (uint64_t)(i * 128), idesc_o, 1u,
+                     one);
+        commit(B_VFREE + st);
+      };
+      int j = next_own(g.j0);
+      uint32_t add = 0;
+      wait_to(k_seen, j, B_KFULL, B_KFREE);
+      if (!ok) break;
+      if (j < g.j1) {
+        tc_fence_after();
+        issue_s(j);
+      }
+      while (j < g.j1) {
+        const int jn = next_own(j + 1);
+        if (jn >= g.j1) {                              // the chain's last S product of the segment
+          commit(B_QFREE + qb);
+          if (!g.single) commit(B_QFREE + qb);
+        }
+        wait_to(v_seen, j, B_VFULL, B_VFREE);
+        // the first product of a segment overwrites O_t: its last values have been read
+        if (!add && uses > 0) wait(B_OFREE + t, (uses - 1) & 1);
+        wait(B_PFULL + t, pc++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(j, add);
+        add = 1;
+        wait_to(k_seen, jn, B_KFULL, B_KFREE);
+        if (!ok) break;
+        if (jn < g.j1) {
+          // S's columns hold no P that is still to be read (the product above was issued before)
+          tc_fence_after();
+          issue_s(jn);
+        }
+        j = jn;
+      }
+      if (!ok) break;
+      if (add) {
+        commit(B_ODONE + t);
+        ++uses;
+      } else {                                         // no part in any key tile
+        arrive(B_QFREE + qb);
+        if (!g.single) arrive(B_QFREE + qb);
+      }
+      wait_to(v_seen, g.j1, B_VFULL, B_VFREE);
+      g0 += g.j1 - g.j0;
+    }
+    // the CTA frees TMEM only after every MMA issued here has completed
+    commit(B_DRAIN + t);
+    if (one) drain_wait(bar(B_DRAIN + t), 0u);
+    __syncwarp();
+  } else if (warp == W_SEG) {
+    // ------------------------------------------------------------ segments, and their Q
+    if (lane == 0) {
+      PagedWalk k;
+      k.sh = shape;
+      k.share = share;
+      k.H = H;
+      k.x0 = x0;
+      k.x1 = x1;
+      bool more = busy;
+      if (busy) {
+        PagedSeq s;
+        extent_of(a, first_b, s);
+        k.start(s, first_b, first_before);
+      }
+      PagedCut cut{};
+      // the next segment of the share (b < 0: none)
+      auto next = [&](bool first) {
+        PagedSeg g;
+        g.b = -1;
+        while (more) {
+          bool got = false;
+          if (k.at >= k.x1) {
+            more = false;
+            break;
+          }
+          const PagedBlock blk = paged_block(k.s, k.blk, shape);
+          got = k.segment(g, blk);
+          if (got && first && g.j0 > 0 && shares.share_of(k.at) == share - 1) {
+            const int64_t last = k.at + (int64_t)blk.cost * (blk.kt.count() - 1);
+            cut = PagedCut{shares.share_of(last) - share + 2, g.q0, g.ntok, g.hk, g.pos};
+          }
+          k.at += (int64_t)blk.cost * blk.kt.count();
+          if (++k.blk >= paged_blocks(k.s, shape.tpt)) {
+            k.blk = 0;
+            if (++k.hk == H) {
+              k.hk = 0;
+              do {
+                if (++k.b >= nseq) {
+                  more = false;
+                  break;
+                }
+                k.per_head = extent_of(a, k.b, k.s) ? head_units(k.s, shape) : 0;
+              } while (k.per_head == 0);
+            }
+          }
+          if (got) break;
+          g.b = -1;
+        }
+        return g;
+      };
+      int made = 0, loaded = 0, q_b = 0;               // segments; of them with Q issued; Q_B loads
+      bool ended = false;
+      long long t0 = clock64();
+      while (!ended || loaded < made) {
+        bool moved = false;
+        if (!ended && (made < SEGS || mbar_test(bar(B_GFREE + made % SEGS),
+                                                (uint32_t)((made / SEGS - 1) & 1)))) {
+          const PagedSeg g = next(made == 0);
+          *seg_slot(made) = g;
+          mbar_arrive(bar(B_GFULL + made % SEGS));
+          ended = g.b < 0;
+          if (!ended) ++made;
+          moved = true;
+        }
+        if (loaded < made) {
+          const PagedSeg* g = seg_slot(loaded);
+          const int two = !g->single;
+          if ((loaded == 0 || mbar_test(bar(B_QFREE), (uint32_t)((loaded - 1) & 1))) &&
+              (!two || q_b == 0 || mbar_test(bar(B_QFREE + 1), (uint32_t)((q_b - 1) & 1)))) {
+            for (int t = 0; t <= two; ++t) {
+              mbar_expect_tx(bar(B_QFULL + t), (uint32_t)(NB * pa.G * pa.tpt * 128));
+              for (int c = 0; c < NB; ++c)
+                tma_load_3d(smem_u32(smem + L::Q_OFF + t * L::TILE + c * BOX), &tmQ, 64 * c,
+                            g->hk * pa.G, g->q0 + t * pa.tpt, bar(B_QFULL + t));
+            }
+            ++loaded;
+            q_b += two;
+            moved = true;
+          }
+        }
+        if (moved) {
+          t0 = clock64();
+        } else if (*abort_flag || clock64() - t0 > kWaitCycles) {
+          if (!*abort_flag) atomicOr(&g_paged_attn_error, kErrWait);
+          *abort_flag = 1;
+          break;
+        }
+      }
+      if (busy) pa.cuts[share] = cut;
+      if (loaded > 0) drain_wait(bar(B_QFULL), (uint32_t)((loaded - 1) & 1));
+      if (q_b > 0) drain_wait(bar(B_QFULL + 1), (uint32_t)((q_b - 1) & 1));
+    }
+    __syncwarp();
+  } else if (warp >= W_RST) {
+    // ------------------------------------------------------------ restore
+    const int tid = threadIdx.x - W_RST * 32;
+    int np = 0;                                        // parts restored
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!seg_wait(n)) break;
+      const PagedSeg* slot = seg_slot(n);
+      const int b = slot->b, j1 = slot->j1, len = slot->n;
+      const KeyTiles kt = slot->kt;
+      int j = slot->j0;
+      __syncwarp();
+      if (lane == 0) seg_done(n);
+      if (b < 0) break;
+      for (; j < j1 && ok; ++j) {
+        const int valid = min(128, len - kt.tile(j) * kKeyTile);
+        for (int which = 0; which < 2; ++which, ++np) {
+          const int st = np % pa.parts, g = np >> 1;
+          bool got = bwait(bar(B_CFULL + st), (uint32_t)((np / pa.parts) & 1), abort_flag);
+          if (g >= 2)
+            got = got && bwait(bar((which ? B_VFREE : B_KFREE) + (g & 1)),
+                               (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            ok = false;
+            break;
+          }
+          const uint8_t* part = smem + L::part_off(pa.two) + st * L::PART;
+          const uint32_t tile = smem_u32(smem + (which ? L::V_OFF : L::K_OFF) + (g & 1) * L::TILE);
+          if (which)
+            restore_part<D, true>(part, tile, lgb, valid, tid);
+          else
+            restore_part<D, false>(part, tile, lgb, valid, tid);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(B_CFREE + st));
+            mbar_arrive(bar((which ? B_VFULL : B_KFULL) + (g & 1)));
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output of chain t
+    const int t = (warp - W_SM) >> 2;
+    const int quarter = warp & 3;                      // TMEM lanes 32 quarter ..
+    const int m = 32 * quarter + lane;                 // row within the row tile
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t srow = lane_addr + s_col(t);
+    const float sl2 = pa.scale_log2;
+    const int tok = m / pa.G, gh = m - tok * pa.G;     // the row's token in the tile, its head
+    const float* mb = ml_b;
+    const float* lb = ml_b + 128;
+    int sc = 0, uses = 0, uses_b = 0, joins = 0;       // S products, own segments, B's, joined ones
+    bool ok = true;
+    // tcgen05.ld / st are warp-collective: every branch around them is decided for the whole warp
+    for (int n = 0; ok; ++n) {
+      if (!seg_wait(n)) break;
+      const PagedSeg& g = *seg_slot(n);                // read where needed: no registers for it
+      if (g.b < 0) break;
+      const int ntok = tile_tokens(g, t, pa.tpt), pos0 = g.pos + (g.single ? 0 : t * pa.tpt);
+      const bool mine = tok < ntok && m < pa.G * pa.tpt;
+      const bool any_row = __any_sync(0xFFFFFFFFu, mine);
+      const int i = pos0 + tok;                        // the row's position
+      // (rows of no token: no score of theirs moves the reference of the warp's rows)
+      float m_ref = mine ? -INFINITY : INFINITY, l_sum = 0.0f;
+      bool some = false;                               // a key tile of the segment is the chain's
+      for (int j = g.j0; j < g.j1; ++j) {
+        if (!takes_part(g, t, j, pa.tpt, a.window, a.sinks)) continue;
+        const bool got = bwait(bar(B_SFULL + t), (uint32_t)(sc++ & 1), abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (any_row) {
+          // masked: some row does not see every key of the tile; ahead: the first row's position
+          // less the key tile's first
+          const int k0 = g.kt.tile(j) * kKeyTile, ahead = pos0 - k0;
+          const bool masked = ahead < KT - 1 || (a.window != 0 && k0 + KT > a.sinks &&
+                                                 ahead + ntok > a.window);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto max_chunk = [&](const float (&v)[32]) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], v[e], v[e + 1]);
+          };
+          float va[32], vb[32];
+          unsigned none = 0;                           // chunks that no row of the warp sees
+          if (masked) {
+            // keys that a row does not see are set to -inf, in TMEM too: pass 2 reads them there
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t vis =
+                  mine && i >= 0 ? visible_bits(k0 + 32 * c, i, a.window, a.sinks) : 0u;
+              if (!__any_sync(0xFFFFFFFFu, vis != 0u)) {
+                none |= 1u << c;
+                continue;
+              }
+              tmem_ld32(srow + 32 * c, va);
+              tmem_wait_ld_dep(va);
+              if (!__all_sync(0xFFFFFFFFu, vis == ~0u)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) va[e] = (vis >> e & 1u) ? va[e] : -INFINITY;
+                tmem_st16(srow + 32 * c, reinterpret_cast<const uint32_t*>(va));
+                tmem_st16(srow + 32 * c + 16, reinterpret_cast<const uint32_t*>(va) + 16);
+              }
+              max_chunk(va);
+            }
+            tmem_wait_st();
+          } else {
+            tmem_ld32(srow, va);
+            tmem_wait_ld_dep(va);
+            tmem_ld32(srow + 32, vb);
+            max_chunk(va);
+            tmem_wait_ld_dep(vb);
+            tmem_ld32(srow + 64, va);
+            max_chunk(vb);
+            tmem_wait_ld_dep(va);
+            tmem_ld32(srow + 96, vb);
+            max_chunk(va);
+            tmem_wait_ld_dep(vb);
+            max_chunk(vb);
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
+          if (__any_sync(0xFFFFFFFFu, mx > m_ref + kLag)) {
+            // move the reference of every row of the warp to max(m_ref, mx): O and l scale by
+            // 2^(m_ref - m_new).  O holds P V of the segment's earlier tiles: done before this S
+            const float m_new = fmaxf(m_ref, mx);
+            const float alpha = (m_ref == -INFINITY) ? 0.0f : ex2(m_ref - m_new);
+            if (some) {
+#pragma unroll 1
+              for (int c16 = 0; c16 < D / 16; ++c16) {
+                uint32_t wv[16];
+                const uint32_t oa = lane_addr + o_col(t) + (uint32_t)(16 * c16);
+                tmem_ld16(oa, wv);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  wv[e] = __float_as_uint(__uint_as_float(wv[e]) * alpha);
+                tmem_st16(oa, wv);
+              }
+              tmem_wait_st();
+            }
+            l_sum *= alpha;
+            m_ref = m_new;
+          }
+          const float ref = (m_ref == -INFINITY) ? 0.0f : m_ref;
+          const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(kPExp - ref, kPExp - ref);
+          uint64_t ls2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
+          auto p_chunk = [&](const float (&v)[32], int c) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = f2unpack(ffma2(f2pack(v[e], v[e + 1]), sl2x2, negm2));
+              const float p0 = ex2(x.x), p1 = ex2(x.y);
+              ls2[(e >> 1) & 1] = fadd2(ls2[(e >> 1) & 1], f2pack(p0, p1));
+              pw[e / 2] = pack_h2(p0, p1);
+            }
+            tmem_st16(srow + 32 * c, pw);
+          };
+          if (!masked) {
+            tmem_ld32(srow, va);                       // the last chunk is still in registers
+            p_chunk(vb, 3);
+            tmem_wait_ld_dep(va);
+            tmem_ld32(srow + 32, vb);
+            p_chunk(va, 0);
+            tmem_wait_ld_dep(vb);
+            tmem_ld32(srow + 64, va);
+            p_chunk(vb, 1);
+            tmem_wait_ld_dep(va);
+            p_chunk(va, 2);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              if (none >> c & 1u) {
+                const uint32_t zeros[16] = {};
+                tmem_st16(srow + 32 * c, zeros);
+              } else {
+                tmem_ld32(srow + 32 * c, va);
+                tmem_wait_ld_dep(va);
+                p_chunk(va, c);
+              }
+            }
+          }
+          tmem_wait_st();
+          const float2 la = f2unpack(fadd2(ls2[0], ls2[1]));
+          l_sum += la.x + la.y;
+        }
+        some = true;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL + t));
+      }
+      if (!ok) break;
+
+      // ---- the segment's rows
+      const bool b_has = g.single && g.j1 - g.j0 >= 2;  // a single block's key tiles are both's
+      if (g.single && t == 1) {
+        if (b_has) {
+          // A joins: hand it the maxima and sums, once it has taken those of the join before
+          if (uses > 0) {
+            const bool fr = bwait(bar(B_OFREE + 1), (uint32_t)((uses - 1) & 1), abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, fr)) break;
+          }
+          ml_b[m] = m_ref;
+          ml_b[128 + m] = l_sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_LFULL));
+          ++uses;
+        }
+        __syncwarp();
+        if (lane == 0) seg_done(n);
+        continue;
+      }
+      bool got = true;
+      if (some) got = bwait(bar(B_ODONE + t), (uint32_t)(uses & 1), abort_flag);
+      if (b_has) {
+        got = got && bwait(bar(B_LFULL), (uint32_t)(joins & 1), abort_flag);
+        got = got && bwait(bar(B_ODONE + 1), (uint32_t)(uses_b & 1), abort_flag);
+      }
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      tc_fence_after();
+      // O = O_A fa + O_B fb over the common maximum
+      float fa = 1.0f, fb = 0.0f, l = l_sum, mm = m_ref;
+      if (b_has) {
+        const float m2 = mb[m], l2 = lb[m];
+        mm = fmaxf(m_ref, m2);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
+        fa = ex2(m_ref - ref);
+        fb = ex2(m2 - ref);
+        l = l_sum * fa + l2 * fb;
+      }
+      if (l == 0.0f) mm = -INFINITY;
+      if (any_row) {
+        const int row = g.q0 + (g.single ? 0 : t * pa.tpt) + tok, hq = g.hk * pa.G + gh;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = a.out + (int64_t)row * a.out_stride + (int64_t)hq * D;
+        const int64_t pr = (int64_t)g.slot * pa.slot_rows + (g.single ? 0 : t * pa.tpt * pa.G) + m;
+        float* part = pa.partial + pr * D;
+        if (g.slot < 0) {
+          fa *= inv;
+          fb *= inv;
+        }
+        // x * 0 summed: NaN for an infinity or a NaN.  Those rows are computed again; where out is q
+        // they are found before anything is stored over their queries.
+        __half2 zero = __float2half2_rn(0.0f);
+        bool stores = mine;
+        const int first = g.slot < 0 && a.out == a.q ? -D / 32 : 0;
+#pragma unroll 1
+        for (int cc = first; cc < D / 32; ++cc) {
+          const int c = cc < 0 ? cc + D / 32 : cc;
+          if (first < 0 && cc == 0)
+            stores = mine && !__hisnan(__low2half(zero)) && !__hisnan(__high2half(zero));
+          float o[32];
+          if (some) {
+            tmem_ld32(lane_addr + o_col(t) + 32 * c, o);
+            tmem_wait_ld_dep(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= fa;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          }
+          if (b_has) {
+            float o2[32];
+            tmem_ld32(lane_addr + o_col(1) + 32 * c, o2);
+            tmem_wait_ld_dep(o2);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], fb, o[e]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 p = pack_channels(o + 8 * k, 1.0f);
+            const uint32_t pw[4] = {p.x, p.y, p.z, p.w};
+            if (g.slot < 0) {
+              if (stores && cc >= 0) *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = p;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                zero = __hfma2(*reinterpret_cast<const __half2*>(&pw[e]), __float2half2_rn(0.0f),
+                               zero);
+            } else {
+              const float* x = o + 8 * k;
+              if (mine) {
+                float4* dst = reinterpret_cast<float4*>(part + 32 * c + 8 * k);
+                dst[0] = make_float4(x[0], x[2], x[4], x[6]);
+                dst[1] = make_float4(x[1], x[3], x[5], x[7]);
+              }
+              float z = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) z = fmaf(x[e], 0.0f, z);
+              const __half2 hz = __float2half2_rn(z);
+              zero = __hadd2(zero, hz);
+            }
+          }
+        }
+        if (mine) {
+          if (g.slot < 0) {
+            if (a.lse)
+              a.lse[(int64_t)row * a.Hq + hq] =
+                  l == 0.0f ? -INFINITY : (mm + log2f(l) - kPExp) * 0.6931471805599453f;
+          } else {
+            float* ml = pa.partial + (int64_t)2 * gridDim.x * pa.slot_rows * D + pr * 2;
+            ml[0] = mm;
+            ml[1] = l;
+          }
+        }
+        // rows with an infinity or NaN, over what they see alone
+        unsigned redo = __ballot_sync(0xFFFFFFFFu, mine && !isnan(l) &&
+                                                       (__hisnan(__low2half(zero)) ||
+                                                        __hisnan(__high2half(zero))));
+        for (; redo; redo &= redo - 1) {
+          const int src = __ffs(redo) - 1;
+          const int rrow = __shfl_sync(0xFFFFFFFFu, row, src), rhq = __shfl_sync(0xFFFFFFFFu, hq, src);
+          const int ri = __shfl_sync(0xFFFFFFFFu, i, src);
+          const int64_t rpr = pr - lane + src;
+          float o[D / 32], rm, rl;
+          attend_row<D>(a, g, a.q + (int64_t)rrow * a.q_stride + (int64_t)rhq * D, ri, o, rm, rl);
+          const float f = rl == 0.0f ? 0.0f : 1.0f / rl;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const int ch = lane * (D / 32) + c;
+            if (g.slot < 0)
+              a.out[(int64_t)rrow * a.out_stride + (int64_t)rhq * D + ch] = f2h(in_range(o[c] * f));
+            else
+              pa.partial[rpr * D + ch] = o[c];
+          }
+          if (g.slot >= 0 && lane == 0) {
+            float* ml = pa.partial + (int64_t)2 * gridDim.x * pa.slot_rows * D + rpr * 2;
+            ml[0] = rl == 0.0f ? -INFINITY : rm;
+            ml[1] = rl;
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (some) mbar_arrive(bar(B_OFREE + t));
+        if (b_has) mbar_arrive(bar(B_OFREE + 1));
+      }
+      if (some) ++uses;
+      if (b_has) {
+        ++uses_b;
+        ++joins;
+      }
+      if (t == 0 && !g.single)                         // B's segments with key tiles
+        for (int j = g.j1 - 1; j >= g.j0; --j)
+          if (takes_part(g, 1, j, pa.tpt, a.window, a.sinks)) {
+            ++uses_b;
+            break;
+          }
+      __syncwarp();
+      if (lane == 0) seg_done(n);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// Puts cut blocks together: a warp per row, its pieces (m, l, unnormalised O) in order, 32 at a
+// time.
+constexpr int kMergeWarps = 8, kMergeSplit = 4;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PArgs pa, int ncta) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int C = D / 32;
+  const PagedCut cut = pa.cuts[blockIdx.x];
+  const int lane = threadIdx.x & 31, w = blockIdx.x;
+  if (cut.pieces == 0) return;
+  const float* ml = pa.partial + (int64_t)2 * ncta * pa.slot_rows * D;
+  for (int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); r < cut.ntok * pa.G;
+       r += gridDim.y * kMergeWarps) {
+    auto at = [&](int i) { return (int64_t)cut_slot(w, cut.pieces, i) * pa.slot_rows + r; };
+    float M = -INFINITY, L = 0.0f, o[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = 0.0f;
+    for (int i0 = 0; i0 < cut.pieces; i0 += 32) {
+      const int n = min(32, cut.pieces - i0);
+      float2 x = make_float2(-INFINITY, 0.0f);
+      if (lane < n) x = *reinterpret_cast<const float2*>(ml + 2 * at(i0 + lane));
+      float mx = x.x;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+      mx = fmaxf(mx, M);
+      const float ref = (mx == -INFINITY) ? 0.0f : mx;
+      const float corr = exp2f(M - ref);
+      const float wgt = x.y == 0.0f ? 0.0f : exp2f(x.x - ref);
+      float l = wgt * x.y;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
+      L = fmaf(L, corr, l);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] *= corr;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xFFFFFFFFu, wgt, i);
+        const float* pp = pa.partial + at(i0 + i) * D + lane * C;
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(pp + c);
+          v[c] = y.x;
+          v[c + 1] = y.y;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = wi == 0.0f ? o[c] : fmaf(wi, v[c], o[c]);
+      }
+      M = mx;
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int64_t row = cut.q0 + r / pa.G;
+    const int hq = cut.hk * pa.G + r % pa.G;
+    uint16_t* op = pa.a.out + row * pa.a.out_stride + (int64_t)hq * D + lane * C;
+#pragma unroll
+    for (int c = 0; c < C; c += 2)
+      *reinterpret_cast<uint32_t*>(op + c) =
+          pack_h2(in_range(o[c] * inv), in_range(o[c + 1] * inv));
+    if (pa.a.lse && lane == 0)
+      pa.a.lse[row * pa.a.Hq + hq] =
+          L == 0.0f ? -INFINITY : (M + log2f(L) - kPExp) * 0.6931471805599453f;
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+int tokens_per_tile(int G) { return 128 / G; }
+int slot_rows_of(int G, int max_q) {
+  const int tpt = tokens_per_tile(G);
+  return G * std::min(max_q, 2 * tpt);
+}
+size_t cut_bytes(int grid) { return (grid * sizeof(PagedCut) + 255) / 256 * 256; }
+
+// Shared memory of the kernel on the current device, set once per device.
+template <int D>
+cudaError_t prepare() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (dev < 0 || dev >= 64 || done[dev]) return cudaSuccess;
+  using L = Smem<D>;
+  e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           std::max(L::bytes(0, L::depth(0)), L::bytes(1, L::depth(1))));
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedAttn& a, void* ws, int nsm, cudaStream_t st) {
+  using L = Smem<D>;
+  cudaError_t e = prepare<D>();
+  if (e != cudaSuccess || (e = get_encode()) != cudaSuccess) return e;
+  PArgs pa;
+  pa.a = a;
+  pa.scale_log2 = a.scale * 1.4426950408889634f;
+  pa.G = a.Hq / a.cache.H;
+  pa.tpt = tokens_per_tile(pa.G);
+  pa.two = std::min(a.max_q, a.q_rows) > pa.tpt;
+  pa.parts = L::depth(pa.two);
+  pa.min_units = 1 + pa.two;
+  pa.slot_rows = slot_rows_of(pa.G, a.max_q);
+  const int grid = std::max(nsm, 1);       // one CTA per SM
+  pa.cuts = static_cast<PagedCut*>(ws);
+  pa.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + cut_bytes(grid));
+  CUtensorMap tq;
+  e = make_map_3d(&tq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.q, D, (uint64_t)a.Hq, (uint64_t)a.q_rows,
+                  2 * D, (uint64_t)a.q_stride * 2, 64, pa.G, CU_TENSOR_MAP_SWIZZLE_128B, pa.tpt);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attend_kernel<D>, dim3(grid), dim3(THREADS), L::bytes(pa.two, pa.parts), st, tq,
+                 pa);
+  if (e != cudaSuccess) return e;
+  const int split = std::min((pa.slot_rows + kMergeWarps - 1) / kMergeWarps, kMergeSplit);
+  return launch_pdl(merge_kernel<D>, dim3(grid, split), dim3(kMergeWarps * 32), 0, st, pa, grid);
 }
 
 // A warp per (sequence, K/V head, position): lanes take (row, head) pairs.
+constexpr int kWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const PagedAttn a) {
   __shared__ float ks[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.z, hk = blockIdx.y, G = a.Hq / a.cache.H;
-  Extent e;
+  PagedSeq e;
   if (!extent_of(a, b, e) || e.n > a.acc_stride) {
     if (threadIdx.x == 0) atomicOr(&g_paged_attn_error, kErrExtent);
     return;
@@ -139,14 +1247,14 @@ __global__ void __launch_bounds__(kWarps * 32) weights_kernel(const PagedAttn a)
 
 }  // namespace
 
-size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) { return 256; }
+size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
+  const int G = Hq / kv.H, d = kv.h / kv.H;
+  return cut_bytes(kMaxSms) +
+         (size_t)2 * kMaxSms * slot_rows_of(G, max_q) * (d + 2) * sizeof(float);
+}
 
 cudaError_t launch_attn_paged(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st) {
-  const int64_t warps = (int64_t)a.q_rows * a.Hq;
-  const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
-  if (d == 128) attend_kernel<128><<<grid, kWarps * 32, 0, st>>>(a);
-  else attend_kernel<64><<<grid, kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  return d == 128 ? launch_d<128>(a, ws, nsm, st) : launch_d<64>(a, ws, nsm, st);
 }
 
 cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st) {
