@@ -28,9 +28,26 @@ def tables(need, seed, spare=2, first=0):
     return t, pages
 
 
+class Values:
+    """Restored values and their groups' largest magnitudes, by page."""
+
+    def __init__(self, x, big):
+        self.x, self.big, self.shape = x, big, x.shape
+
+
+def restore_error(big):
+    """How far a value of the attention may be from its definition fp16(a + q s), s = (b - a)/15.
+
+    It computes fp16((q - 8) fp16(s) + fp16(a + 8 s)).  With M the larger of |a| and |b| and h = 2^-11
+    half a step: |q - 8| <= 8 and s <= 2 M / 15 make the rounding of s cost h 16 M / 15; a + 8 s lies
+    between a and b: h M; the result: h M (1 + 3 h) at most; the definition's own rounding: h M.  Where
+    the numbers are subnormal, half of 2^-24 each: 8 + 1 + 1 + 1 times 2^-25 < 2^-21."""
+    return H16 * 4.1 * big + 2.0 ** -21
+
+
 def fill(fg, pages, P, H, d, seed, scale=1.0):
     """A pool of pages of quantised normal values, and their restored values [pages][H][P][d] of K
-    and of V."""
+    and of V, each with the largest of its group's magnitudes M beside it (rows_of takes either)."""
     pool = fg.KVPagesQ4(pages, P, H * d, H)
     vals = []
     for codes_t, ab_t, sd in zip(pool.parts()[0::2], pool.parts()[1::2], (0, 1)):
@@ -40,12 +57,15 @@ def fill(fg, pages, P, H, d, seed, scale=1.0):
         codes_t.copy_(torch.from_numpy(OQ.pack_nibbles(q)).cuda().view(codes_t.shape))
         ab = np.stack([a, b], -1).reshape(pages, H, P, d // 64, 2)
         ab_t.copy_(torch.from_numpy(ab).cuda())
-        vals.append(OQ.dequant_g64(q, a, b).reshape(pages, H, P, d))
+        big = np.maximum(np.abs(a.astype(np.float64)), np.abs(b.astype(np.float64)))
+        vals.append(Values(OQ.dequant_g64(q, a, b).reshape(pages, H, P, d),
+                           np.repeat(big, 64, axis=1).reshape(pages, H, P, d)))
     return pool, vals[0], vals[1]
 
 
 def rows_of(vals, table, b, n):
     """Values [H][n][d] of sequence b's first n positions, from values by page."""
+    vals = getattr(vals, "x", vals)
     P = vals.shape[2]
     if n == 0:
         return np.zeros((vals.shape[1], 0, vals.shape[3]), vals.dtype)

@@ -12,7 +12,7 @@ import torch
 import fg_synth
 from oracle import paged as OP
 from oracle import quant as OQ
-from paged_util import F32, H16, fill, i32, need, offsets, rows_of, tables
+from paged_util import F32, H16, fill, i32, need, offsets, restore_error, rows_of, tables
 from parity_util import dev, host, lib
 
 pytestmark = pytest.mark.gpu
@@ -230,8 +230,8 @@ def run_attend(fg, q, q_off, Hq, pool, table, lens, scale, out=None, lse=True, m
 def check_attend(got, z, q, q_off, Hq, k, v, table, lens, scale, window=0, sinks=0):
     """Every row within what the arithmetic allows of the oracle's.
 
-    Scores: d + 40 binary32 operations on terms of size |q_j k_j|; an error ds moves a weight by a
-    factor within e^(+-2 ds).  Weights are rounded to fp16 (half a step; half of 2^-24 where they are
+    Scores: d + 40 binary32 operations on terms of size |q_j k_j|, and each k within restore_error; an
+    error ds moves a weight by a factor within e^(+-2 ds).  Values: within restore_error.  Weights are rounded to fp16 (half a step; half of 2^-24 where they are
     subnormal, at most 2^-31 of the row's largest after their scaling), the exponential adds 2^-21,
     the sums n + 64 binary32 operations; last, the output's own half step."""
     got, z = host(got).astype(np.float64), None if z is None else host(z)
@@ -249,11 +249,13 @@ def check_attend(got, z, q, q_off, Hq, k, v, table, lens, scale, window=0, sinks
             o, lse, p = OP.attend(qq, kk, vv, ok, scale)
             mag = np.einsum("rgd,td->rgt", np.abs(qq.astype(np.float64)),
                             np.abs(kk.astype(np.float64))) * scale
-            ds = np.where(ok[:, None], mag, 0).max(-1, initial=0.0) * (d + 40) * F32
+            dk, dv = (restore_error(rows_of(x.big, table, b, n)[hk]) for x in (k, v))
+            moved = np.einsum("rgd,td->rgt", np.abs(qq.astype(np.float64)), dk) * scale
+            ds = np.where(ok[:, None], mag * (d + 40) * F32 + moved, 0).max(-1, initial=0.0)
             V = p @ np.abs(vv.astype(np.float64))
             vmax = np.abs(vv.astype(np.float64)).max(0, initial=0.0)
             tol = ((np.expm1(2 * ds)[..., None] + H16 + 2.0 ** -21 + (n + 64) * F32) * V
-                   + n * 2.0 ** -31 * vmax + H16 * np.abs(o) + 2.0 ** -24)
+                   + p @ dv + n * 2.0 ** -31 * vmax + H16 * np.abs(o) + 2.0 ** -24)
             g = got[rows, hk * G * d:(hk + 1) * G * d].reshape(nq, G, d)
             err = np.abs(g - o)
             assert np.all(err <= tol), (b, hk, float((err - tol).max()), float(err.max()))
@@ -517,7 +519,7 @@ def test_generation_over_pages(fg):
     after = after.astype(np.int32)
     K, V = ([[np.zeros((0, d), np.float16) for _ in range(H)] for _ in range(2)] for _ in range(2))
     acc = torch.zeros((2, H, 320), device="cuda")
-    acc_ref = np.zeros((2, H, 320))
+    acc_ref, acc_tol = np.zeros((2, H, 320)), np.zeros((2, H, 320))
     pos, rope_pos = [0, 0], [0, 0]
 
     def step(nq, table):
@@ -552,13 +554,21 @@ def test_generation_over_pages(fg):
                 qq = qr[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d)
                 o, _, p = OP.attend(qq, K[b][hk], V[b][hk], ok, scale)
                 g = got[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d)
-                # half fp16 steps of the weights and of the output, and the scores' roundings
-                tol = 2.5 * H16 * (p @ np.abs(V[b][hk].astype(np.float64))) + 2.0 ** -12
+                # (as in check_attend, with 8 > 4.1 times a row's largest value for its groups' M)
+                dk, dv = (restore_error(2 * np.abs(x[b][hk].astype(np.float64)).max(1, keepdims=True))
+                          for x in (K, V))
+                ds = (np.abs(qq.astype(np.float64)).sum(-1) * dk.max(initial=0) * scale
+                      + 2.0 ** -12)[..., None]
+                tol = ((np.expm1(2 * ds) + 2 * H16) * (p @ np.abs(V[b][hk].astype(np.float64)))
+                       + p @ np.broadcast_to(dv, V[b][hk].shape) + H16 * np.abs(o) + 2.0 ** -20)
                 assert np.all(np.abs(g - o) <= tol)
                 acc_ref[b, hk, :n] += p.sum((0, 1))
+                # the log-sum-exp that the attention gives is within ds too
+                acc_tol[b, hk, :n] += (p * np.expm1(2 * ds)).sum((0, 1))
         for b in range(2):
             n = pos[b]
-            assert np.allclose(host(acc)[b, :, :n], acc_ref[b, :, :n], rtol=1e-4, atol=1e-5)
+            err = np.abs(host(acc)[b, :, :n] - acc_ref[b, :, :n])
+            assert np.all(err <= acc_tol[b, :, :n] + 2.0 ** -16 * acc_ref[b, :, :n])
 
     for nq in ([130, 1], [77, 90], [1, 1]):
         step(nq, table)
@@ -572,7 +582,7 @@ def test_generation_over_pages(fg):
     fg.fg_check_device_error()
     acc.zero_()
     acc[:, :, :keep] = acc_out
-    acc_ref[:] = 0.0
+    acc_ref[:] = acc_tol[:] = 0.0
     for b in range(2):
         for hk in range(H):
             at = OP.evict(old[b, hk], pos[b], keep, recent)
