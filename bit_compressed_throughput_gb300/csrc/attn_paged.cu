@@ -56,9 +56,9 @@ __device__ unsigned int g_paged_attn_error = 0;
 
 namespace {
 
-constexpr int THREADS = 16 * 32;
+constexpr int THREADS = 20 * 32;
 constexpr int W_MMA = 1, W_SEG = 3, W_SM = 4, W_RST = 12;
-constexpr int RST_THREADS = 128;
+constexpr int RST_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int BOX = 128 * 128;             // bytes of one 64-column x 128-row box
 constexpr int SEGS = 4;                    // ring of segments
@@ -202,18 +202,25 @@ constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_QFULL = 2 * MAX_PARTS, B_QFREE
               NBARS = B_DRAIN + 2;
 static_assert(NBARS * 8 + 16 <= 512 && sizeof(PagedSeg) <= 64, "control space");
 
+// A wait that ran out, or another warp's.
+__device__ __noinline__ bool gave_up(long long t0, volatile int* abort_flag) {
+  if (*abort_flag) return true;
+  if (clock64() - t0 <= kWaitCycles) return false;
+  *abort_flag = 1;
+  atomicOr(&g_paged_attn_error, kErrWait);
+  return true;
+}
+// LAZY: for warps that run ahead of the others, which need the instruction fetches more.
+template <bool LAZY = false>
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try(bar, parity)) {
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *abort_flag = 1;
-      atomicOr(&g_paged_attn_error, kErrWait);
-      return false;
-    }
+#pragma unroll 1
+  for (unsigned n = 1;; ++n) {
+    if (mbar_try(bar, parity)) return true;
+    if (LAZY) __nanosleep(200);
+    if ((n & 63u) == 0 && gave_up(t0, abort_flag)) return false;
   }
-  return true;
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -252,73 +259,108 @@ __device__ __forceinline__ bool takes_part(const PagedSeg& g, int t, int j, int 
   return span_sees(g.kt.tile(j), lo, lo + tile_tokens(g, t, tpt) - 1, window, sinks);
 }
 
-// 8 codes of a word times s plus c8 = a + 8 s, in the channels' order (K) or in the nibbles' (V).
-__device__ __forceinline__ uint32_t hadd2_u32(uint32_t x, uint32_t y) {
-  const __half2 r = __hadd2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr));
+  return r;
 }
-__device__ __forceinline__ uint4 restore_natural(uint32_t w, uint32_t s, uint32_t c8) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = (__byte_perm(w, 0, 0x1111 * i) & 0x00F0000Fu) | 0x64006400u;
-    // (1024 + q0, 1024 + 16 q1) -> (q0 - 8, q1 - 8)
-    o[i] = hfma2_u32(hfma2_u32(u, 0x2C003C00u, 0xD480E408u), s, c8);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
 }
-__device__ __forceinline__ uint4 restore_permuted(uint32_t w, uint32_t s, uint32_t c8) {
-  const uint32_t w8 = w >> 8;
-  uint4 o;
-  o.x = hfma2_u32(hadd2_u32((w & 0x000F000Fu) | 0x64006400u, 0xE408E408u), s, c8);
-  o.y = hfma2_u32(hfma2_u32((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), s, c8);
-  o.z = hfma2_u32(hadd2_u32((w8 & 0x000F000Fu) | 0x64006400u, 0xE408E408u), s, c8);
-  o.w = hfma2_u32(hfma2_u32((w8 & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u), s, c8);
-  return o;
-}
-
-// A part of `valid` positions from a ring stage into an fp16 tile, by the restore warps: 16 bytes
-// of codes (32 channels) per thread and turn.  Neighbouring threads hold neighbouring code bytes;
-// the upper 64 channels' threads take their words in another order, so that the 16-byte stores of 8
-// threads meet all banks.
-template <int D, bool V>
-__device__ __forceinline__ void restore_part(const uint8_t* part, uint32_t tile, int lgb, int valid,
-                                             int tid) {
-  constexpr int CH = D / 32;               // chunks of 32 channels per row
-#pragma unroll 2
-  for (int it = 0; it < 128 * CH / RST_THREADS; ++it) {
-    const int idx = it * RST_THREADS + tid, row = idx / CH, q = idx % CH;
-    const uint8_t* sub = part + (((row >> lgb) * (9 * D / 16)) << lgb);
-    const int r = row & ((1 << lgb) - 1);
-    uint4 w = *reinterpret_cast<const uint4*>(sub + r * (D / 2) + q * 16);
-    const uint32_t abw = *reinterpret_cast<const uint32_t*>(sub + ((D / 2) << lgb) + r * (D / 16) +
-                                                            (q >> 1) * 4);
+// Codes of a group (a, b) restored in fp16 arithmetic, two per instruction.  With z the code whose
+// value a + z s is nearest to 0, x = fp16((q - z) s1 + fp16((q - z) s2 + c)): s = s1 + s2 in two
+// fp16 numbers and c = fp16(a + z s), so that all but the last rounding are of numbers a tenth of the
+// group's largest.  It is the definition's fp16(a + q s) or, for one value in 20, its neighbour
+// (relative error 1.0e-4; with one fp16 number for s and codes counted from the middle 3.3e-4, which
+// the scores bring to 8.5e-4 in the outputs).  Restoring in binary32 takes twice the instructions
+// that pack and unpack.
+struct Group {
+  uint32_t s1, s2, c, z;                   // z: (-1024 - z, -64 - z)
+  __device__ __forceinline__ explicit Group(uint32_t abw) {
     const float2 ab = unpack_h2(abw);
     const float s = (ab.y - ab.x) * (1.0f / 15.0f);
-    const float c = fmaf(8.0f, s, ab.x);
-    const uint32_t s2 = pack_h2(s, s), c2 = pack_h2(c, c);
-    const int flip = (q >> 1) << 1;        // words 0, 1, 2, 3, or 2, 3, 0, 1
-    if (flip) w = make_uint4(w.z, w.w, w.x, w.y);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    const uint32_t base = tile + (q >> 1) * BOX + row * 128;
+    // (s = 0 and infinities: any z will do)
+    const float zf = rintf(fminf(fmaxf(__fdividef(-ab.x, s), 0.0f), 15.0f)), cf = fmaf(zf, s, ab.x);
+    s1 = pack_h2(s, s);
+    const float rest = s - unpack_h2(s1).x;
+    s2 = pack_h2(rest, rest);
+    c = pack_h2(cf, cf);
+    z = pack_h2(-1024.0f - zf, -64.0f - zf);
+  }
+  __device__ __forceinline__ uint4 restore(uint32_t w) const {
+    uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint4 o = V ? restore_permuted(ww[i], s2, c2) : restore_natural(ww[i], s2, c2);
-      if (row >= valid) o = make_uint4(0, 0, 0, 0);
-      const int chunk = (q & 1) * 4 + (i ^ flip);
-      st_shared_v4(base + ((chunk ^ (row & 7)) << 4), o.x, o.y, o.z, o.w);
+      // a byte's two nibbles under fp16's exponent of 1024: (1024 + q0, 1024 + 16 q1)
+      const uint32_t u = (__byte_perm(w, 0, 0x1111 * i) & 0x00F0000Fu) | 0x64006400u;
+      const uint32_t t = hfma2_u32(u, 0x2C003C00u, z);
+      o[i] = hfma2_u32(t, s1, hfma2_u32(t, s2, c));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
+
+// A part from a ring stage into an fp16 tile: two threads per position, 64 channels each (d = 64:
+// 32).  The upper 64 channels' threads take their words in another order, so that the 16-byte
+// stores of 8 threads meet all banks.  Positions `valid` .. are not the sequence's: 0.  (The loop
+// stays a loop: with everything unrolled, in code of their own for K, V and tails, the warps waited
+// for instructions, and a part took 2770 cycles instead of 1740.)
+template <int D>
+__device__ __forceinline__ void restore_part(uint32_t part, uint32_t tile, int lgb, int valid,
+                                             int tid) {
+  const int row = tid >> 1, h = tid & 1, r = row & ((1 << lgb) - 1);
+  const uint32_t sub = part + (((row >> lgb) * (9 * D / 16)) << lgb);
+  const uint32_t codes = sub + r * (D / 2) + h * (D / 4);
+  const uint32_t abw = ld_shared(sub + ((D / 2) << lgb) + r * (D / 16) + (D == 128 ? 4 * h : 0));
+  const Group g(row < valid ? abw : 0u);   // (0, 0): every code is 0
+  const uint32_t dst = tile + (D == 128 ? h * BOX : 0) + row * 128;
+#pragma unroll 1
+  for (int it = 0; it < D / 64; ++it) {
+    const int half = D == 128 ? it ^ h : h;
+    const uint4 w = ld_shared_v4(codes + (D == 128 ? 16 * half : 0));
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t to = dst + (((4 * half) ^ (row & 4)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 o = g.restore(ww[i]);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((i ^ (row & 3)) << 4)),
+                   "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w));
     }
   }
 }
 
-// 32 output columns in the nibbles' order -> 4 x 8 fp16 channels, times f.
-__device__ __forceinline__ uint4 pack_channels(const float* o, float f) {
-  return make_uint4(pack_h2(in_range(o[0] * f), in_range(o[2] * f)),
-                    pack_h2(in_range(o[4] * f), in_range(o[6] * f)),
-                    pack_h2(in_range(o[1] * f), in_range(o[3] * f)),
-                    pack_h2(in_range(o[5] * f), in_range(o[7] * f)));
+// 16 TMEM columns, and the wait that ties them to it; 8 columns stored.
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  tmem_ld16(taddr, r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld_dep(float (&v)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
+        "+f"(v[14]), "+f"(v[15])
+      :
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
 }
 
+// 8 output channels as fp16.
+__device__ __forceinline__ uint4 pack_channels(const float* o) {
+  return make_uint4(pack_h2(in_range(o[0]), in_range(o[1])), pack_h2(in_range(o[2]), in_range(o[3])),
+                    pack_h2(in_range(o[4]), in_range(o[5])), pack_h2(in_range(o[6]), in_range(o[7])));
+}
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
 attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ PArgs pa) {
@@ -346,14 +388,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
   if (threadIdx.x == 0) {
     for (int i = 0; i < MAX_PARTS; ++i) {
       mbar_init(bar(B_CFULL + i), 1);
-      mbar_init(bar(B_CFREE + i), 4);      // one arrival per restore warp
+      mbar_init(bar(B_CFREE + i), RST_WARPS);   // one arrival per restore warp
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_QFULL + i), 1);
       mbar_init(bar(B_QFREE + i), 2);      // two arrivals of the issuers' per use of a buffer
-      mbar_init(bar(B_KFULL + i), 4);
+      mbar_init(bar(B_KFULL + i), RST_WARPS);
       mbar_init(bar(B_KFREE + i), 2);
-      mbar_init(bar(B_VFULL + i), 4);
+      mbar_init(bar(B_VFULL + i), RST_WARPS);
       mbar_init(bar(B_VFREE + i), 2);
       mbar_init(bar(B_SFULL + i), 1);
       mbar_init(bar(B_PFULL + i), 4);      // one arrival per softmax warp
@@ -364,7 +406,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
     mbar_init(bar(B_LFULL), 4);
     for (int i = 0; i < SEGS; ++i) {
       mbar_init(bar(B_GFULL + i), 1);
-      mbar_init(bar(B_GFREE + i), 1 + 2 + 8 + 4);      // every other warp
+      mbar_init(bar(B_GFREE + i), 1 + 2 + 8 + RST_WARPS);      // every other warp
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -480,8 +522,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         for (int which = 0; which < 2; ++which, ++np) {
           const int st = np % pa.parts;
           if (np >= pa.parts) {
-            const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((np / pa.parts - 1) & 1),
-                                  abort_flag);
+            const bool fr = bwait<true>(bar(B_CFREE + st), (uint32_t)((np / pa.parts - 1) & 1),
+                                        abort_flag);
             if (!__all_sync(0xFFFFFFFFu, fr)) {
               ok = false;
               break;
@@ -716,7 +758,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         }
         if (moved) {
           t0 = clock64();
-        } else if (*abort_flag || clock64() - t0 > kWaitCycles) {
+          continue;
+        }
+        __nanosleep(400);                              // leaves the issue slots to the others
+        if (*abort_flag || clock64() - t0 > kWaitCycles) {
           if (!*abort_flag) atomicOr(&g_paged_attn_error, kErrWait);
           *abort_flag = 1;
           break;
@@ -745,20 +790,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         const int valid = min(128, len - kt.tile(j) * kKeyTile);
         for (int which = 0; which < 2; ++which, ++np) {
           const int st = np % pa.parts, g = np >> 1;
-          bool got = bwait(bar(B_CFULL + st), (uint32_t)((np / pa.parts) & 1), abort_flag);
+          bool got = bwait<true>(bar(B_CFULL + st), (uint32_t)((np / pa.parts) & 1), abort_flag);
           if (g >= 2)
-            got = got && bwait(bar((which ? B_VFREE : B_KFREE) + (g & 1)),
+            got = got && bwait<true>(bar((which ? B_VFREE : B_KFREE) + (g & 1)),
                                (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
           if (!__all_sync(0xFFFFFFFFu, got)) {
             ok = false;
             break;
           }
-          const uint8_t* part = smem + L::part_off(pa.two) + st * L::PART;
+          const uint32_t part = smem_u32(smem + L::part_off(pa.two) + st * L::PART);
           const uint32_t tile = smem_u32(smem + (which ? L::V_OFF : L::K_OFF) + (g & 1) * L::TILE);
-          if (which)
-            restore_part<D, true>(part, tile, lgb, valid, tid);
-          else
-            restore_part<D, false>(part, tile, lgb, valid, tid);
+          restore_part<D>(part, tile, lgb, valid, tid);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
@@ -807,48 +849,48 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
           const int k0 = g.kt.tile(j) * kKeyTile, ahead = pos0 - k0;
           const bool masked = ahead < KT - 1 || (a.window != 0 && k0 + KT > a.sinks &&
                                                  ahead + ntok > a.window);
+          // (16 columns at a time in loops: 32 at a time and unrolled took twice the instructions,
+          // for want of registers, and the warps waited for them)
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto max_chunk = [&](const float (&v)[32]) {
+          auto max_chunk = [&](const float (&v)[16]) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
+            for (int e = 0; e < 16; e += 2)
               m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], v[e], v[e + 1]);
           };
-          float va[32], vb[32];
+          float va[16], vb[16];
           unsigned none = 0;                           // chunks that no row of the warp sees
           if (masked) {
             // keys that a row does not see are set to -inf, in TMEM too: pass 2 reads them there
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
               const uint32_t vis =
-                  mine && i >= 0 ? visible_bits(k0 + 32 * c, i, a.window, a.sinks) : 0u;
+                  mine && i >= 0 ? visible_bits(k0 + 16 * c, i, a.window, a.sinks) & 0xFFFFu : 0u;
               if (!__any_sync(0xFFFFFFFFu, vis != 0u)) {
                 none |= 1u << c;
                 continue;
               }
-              tmem_ld32(srow + 32 * c, va);
+              tmem_ld16f(srow + 16 * c, va);
               tmem_wait_ld_dep(va);
-              if (!__all_sync(0xFFFFFFFFu, vis == ~0u)) {
+              if (!__all_sync(0xFFFFFFFFu, vis == 0xFFFFu)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) va[e] = (vis >> e & 1u) ? va[e] : -INFINITY;
-                tmem_st16(srow + 32 * c, reinterpret_cast<const uint32_t*>(va));
-                tmem_st16(srow + 32 * c + 16, reinterpret_cast<const uint32_t*>(va) + 16);
+                for (int e = 0; e < 16; ++e) va[e] = (vis >> e & 1u) ? va[e] : -INFINITY;
+                tmem_st16(srow + 16 * c, reinterpret_cast<const uint32_t*>(va));
               }
               max_chunk(va);
             }
             tmem_wait_st();
           } else {
-            tmem_ld32(srow, va);
+            tmem_ld16f(srow, va);
             tmem_wait_ld_dep(va);
-            tmem_ld32(srow + 32, vb);
-            max_chunk(va);
-            tmem_wait_ld_dep(vb);
-            tmem_ld32(srow + 64, va);
-            max_chunk(vb);
-            tmem_wait_ld_dep(va);
-            tmem_ld32(srow + 96, vb);
-            max_chunk(va);
-            tmem_wait_ld_dep(vb);
-            max_chunk(vb);
+#pragma unroll 1
+            for (int c = 0; c < 8; c += 2) {           // the next load in flight
+              tmem_ld16f(srow + 16 * c + 16, vb);
+              max_chunk(va);
+              tmem_wait_ld_dep(vb);
+              if (c < 6) tmem_ld16f(srow + 16 * c + 32, va);
+              max_chunk(vb);
+              tmem_wait_ld_dep(va);
+            }
           }
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl2;
           if (__any_sync(0xFFFFFFFFu, mx > m_ref + kLag)) {
@@ -876,36 +918,38 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
           const float ref = (m_ref == -INFINITY) ? 0.0f : m_ref;
           const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(kPExp - ref, kPExp - ref);
           uint64_t ls2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
-          auto p_chunk = [&](const float (&v)[32], int c) {
-            uint32_t pw[16];
+          // P of keys 32 c .. lies in the first 16 of their S columns
+          auto p_chunk = [&](const float (&v)[16], int c) {
+            uint32_t pw[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < 16; e += 2) {
               const float2 x = f2unpack(ffma2(f2pack(v[e], v[e + 1]), sl2x2, negm2));
               const float p0 = ex2(x.x), p1 = ex2(x.y);
               ls2[(e >> 1) & 1] = fadd2(ls2[(e >> 1) & 1], f2pack(p0, p1));
               pw[e / 2] = pack_h2(p0, p1);
             }
-            tmem_st16(srow + 32 * c, pw);
+            tmem_st8(srow + 32 * (c >> 1) + 8 * (c & 1), pw);
           };
           if (!masked) {
-            tmem_ld32(srow, va);                       // the last chunk is still in registers
-            p_chunk(vb, 3);
+            tmem_ld16f(srow, va);
             tmem_wait_ld_dep(va);
-            tmem_ld32(srow + 32, vb);
-            p_chunk(va, 0);
-            tmem_wait_ld_dep(vb);
-            tmem_ld32(srow + 64, va);
-            p_chunk(vb, 1);
-            tmem_wait_ld_dep(va);
-            p_chunk(va, 2);
+#pragma unroll 1
+            for (int c = 0; c < 8; c += 2) {
+              tmem_ld16f(srow + 16 * c + 16, vb);
+              p_chunk(va, c);
+              tmem_wait_ld_dep(vb);
+              if (c < 6) tmem_ld16f(srow + 16 * c + 32, va);
+              p_chunk(vb, c + 1);
+              tmem_wait_ld_dep(va);
+            }
           } else {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
               if (none >> c & 1u) {
-                const uint32_t zeros[16] = {};
-                tmem_st16(srow + 32 * c, zeros);
+                const uint32_t zeros[8] = {};
+                tmem_st8(srow + 32 * (c >> 1) + 8 * (c & 1), zeros);
               } else {
-                tmem_ld32(srow + 32 * c, va);
+                tmem_ld16f(srow + 16 * c, va);
                 tmem_wait_ld_dep(va);
                 p_chunk(va, c);
               }
@@ -974,52 +1018,50 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         // they are found before anything is stored over their queries.
         __half2 zero = __float2half2_rn(0.0f);
         bool stores = mine;
-        const int first = g.slot < 0 && a.out == a.q ? -D / 32 : 0;
+        const int first = g.slot < 0 && a.out == a.q ? -D / 16 : 0;
 #pragma unroll 1
-        for (int cc = first; cc < D / 32; ++cc) {
-          const int c = cc < 0 ? cc + D / 32 : cc;
+        for (int cc = first; cc < D / 16; ++cc) {
+          const int c = cc < 0 ? cc + D / 16 : cc;
           if (first < 0 && cc == 0)
             stores = mine && !__hisnan(__low2half(zero)) && !__hisnan(__high2half(zero));
-          float o[32];
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0.0f;
           if (some) {
-            tmem_ld32(lane_addr + o_col(t) + 32 * c, o);
+            tmem_ld16f(lane_addr + o_col(t) + 16 * c, o);
             tmem_wait_ld_dep(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= fa;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+            for (int e = 0; e < 16; ++e) o[e] *= fa;
           }
           if (b_has) {
-            float o2[32];
-            tmem_ld32(lane_addr + o_col(1) + 32 * c, o2);
+            float o2[16];
+            tmem_ld16f(lane_addr + o_col(1) + 16 * c, o2);
             tmem_wait_ld_dep(o2);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], fb, o[e]);
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(o2[e], fb, o[e]);
           }
+          if (g.slot < 0) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 p = pack_channels(o + 8 * k, 1.0f);
-            const uint32_t pw[4] = {p.x, p.y, p.z, p.w};
-            if (g.slot < 0) {
-              if (stores && cc >= 0) *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = p;
+            for (int k = 0; k < 2; ++k) {
+              const uint4 p = pack_channels(o + 8 * k);
+              const uint32_t pw[4] = {p.x, p.y, p.z, p.w};
+              if (stores && cc >= 0) *reinterpret_cast<uint4*>(out + 16 * c + 8 * k) = p;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 zero = __hfma2(*reinterpret_cast<const __half2*>(&pw[e]), __float2half2_rn(0.0f),
                                zero);
-            } else {
-              const float* x = o + 8 * k;
-              if (mine) {
-                float4* dst = reinterpret_cast<float4*>(part + 32 * c + 8 * k);
-                dst[0] = make_float4(x[0], x[2], x[4], x[6]);
-                dst[1] = make_float4(x[1], x[3], x[5], x[7]);
-              }
-              float z = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) z = fmaf(x[e], 0.0f, z);
-              const __half2 hz = __float2half2_rn(z);
-              zero = __hadd2(zero, hz);
             }
+          } else {
+            float z = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              if (mine)
+                *reinterpret_cast<float4*>(part + 16 * c + e) =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) z = fmaf(o[e + x], 0.0f, z);
+            }
+            zero = __hadd2(zero, __float2half2_rn(z));
           }
         }
         if (mine) {
