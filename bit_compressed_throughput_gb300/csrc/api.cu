@@ -434,6 +434,7 @@ int fg_check_device_error(void* stream) {
                   {"windowed decode attention", decode_window_read_error},
                   {"windowed prefill attention", prefill_window_read_error},
                   {"paged attention", paged_attn_read_error},
+                  {"received weights", weights_read_error},
                   {"eviction", evict_read_error}};
   constexpr int n = sizeof(families) / sizeof(families[0]);
   DeviceErrorWord words[n];

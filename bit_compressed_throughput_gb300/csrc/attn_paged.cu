@@ -46,6 +46,7 @@
 #include "fg_internal.h"
 #include "gemm_tc.cuh"
 #include "paged.cuh"
+#include "paged_tc.cuh"
 #include "paged_work.cuh"
 #include "q4_restore.cuh"
 #include "ragged.cuh"
@@ -56,29 +57,27 @@ __device__ unsigned int g_paged_attn_error = 0;
 
 namespace {
 
+using namespace paged;
+
+template <bool LAZY = false>
+__device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return bounded_wait<LAZY>(bar, parity, abort_flag, &g_paged_attn_error);
+}
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  bounded_drain(bar, parity, &g_paged_attn_error);
+}
+
 constexpr int THREADS = 20 * 32;
 constexpr int W_MMA = 1, W_SEG = 3, W_SM = 4, W_RST = 12;
 constexpr int RST_WARPS = 8;
-constexpr uint32_t TMEM_COLS = 512;
-constexpr int BOX = 128 * 128;             // bytes of one 64-column x 128-row box
 constexpr int SEGS = 4;                    // ring of segments
 constexpr int MAX_PARTS = 12;              // ring of parts (K or V codes of a key tile)
-constexpr long long kWaitCycles = 1ll << 36;   // attend_row may keep the other warps waiting
-constexpr long long kDrainCycles = 1ll << 32;  // for copies and products in flight
-constexpr unsigned int kErrWait = 1u, kErrDrain = 2u;
 constexpr float kLag = 8.0f;               // base-2 score by which a row may pass its reference
 constexpr float kPExp = 7.0f;              // P is scaled by 2^7, as its row sum is: P <= 2^15, and
                                            // down to 2^-21 of the reference's P normal in fp16
 
-// ---------------------------------------------------------------- extents and rows
+// ---------------------------------------------------------------- rows on their own
 
-__device__ __forceinline__ bool extent_of(const PagedAttn& a, int b, PagedSeq& e) {
-  const int q0 = a.q_off[b], q1 = a.q_off[b + 1], n = a.lens[b];
-  if (q0 < 0 || q0 > q1 || q1 > a.q_rows || q1 - q0 > a.max_q || n < 0 || n > a.cache.cap())
-    return false;
-  e = PagedSeq{q0, q1 - q0, n};
-  return true;
-}
 __device__ __forceinline__ float restored(uint32_t code, uint32_t abw) {
   const float2 ab = unpack_h2(abw);
   const float s = __fdiv_rn(__fsub_rn(ab.y, ab.x), 15.0f);
@@ -202,52 +201,6 @@ constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_QFULL = 2 * MAX_PARTS, B_QFREE
               NBARS = B_DRAIN + 2;
 static_assert(NBARS * 8 + 16 <= 512 && sizeof(PagedSeg) <= 64, "control space");
 
-// A wait that ran out, or another warp's.
-__device__ __noinline__ bool gave_up(long long t0, volatile int* abort_flag) {
-  if (*abort_flag) return true;
-  if (clock64() - t0 <= kWaitCycles) return false;
-  *abort_flag = 1;
-  atomicOr(&g_paged_attn_error, kErrWait);
-  return true;
-}
-// LAZY: for warps that run ahead of the others, which need the instruction fetches more.
-template <bool LAZY = false>
-__device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_test(bar, parity)) return true;
-  const long long t0 = clock64();
-#pragma unroll 1
-  for (unsigned n = 1;; ++n) {
-    if (mbar_try(bar, parity)) return true;
-    if (LAZY) __nanosleep(200);
-    if ((n & 63u) == 0 && gave_up(t0, abort_flag)) return false;
-  }
-}
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try(bar, parity)) {
-    if (clock64() - t0 > kDrainCycles) {
-      atomicOr(&g_paged_attn_error, kErrDrain);
-      return;
-    }
-  }
-}
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y,
-                                            int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-
 // Tokens of row tile t of a block, and whether it takes part in key tile number j.
 __device__ __forceinline__ int tile_tokens(const PagedSeg& g, int t, int tpt) {
   return g.single ? g.ntok : (t ? g.ntok - tpt : tpt);
@@ -259,18 +212,6 @@ __device__ __forceinline__ bool takes_part(const PagedSeg& g, int t, int j, int 
   return span_sees(g.kt.tile(j), lo, lo + tile_tokens(g, t, tpt) - 1, window, sinks);
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
-  return r;
-}
 // Codes of a group (a, b) restored in fp16 arithmetic, two per instruction.  With z the code whose
 // value a + z s is nearest to 0, x = fp16((q - z) s1 + fp16((q - z) s2 + c)): s = s1 + s2 in two
 // fp16 numbers and c = fp16(a + z s), so that all but the last rounding are of numbers a tenth of the
@@ -331,29 +272,6 @@ __device__ __forceinline__ void restore_part(uint32_t part, uint32_t tile, int l
                    "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w));
     }
   }
-}
-
-// 16 TMEM columns, and the wait that ties them to it; 8 columns stored.
-__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  tmem_ld16(taddr, r);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_ld_dep(float (&v)[16]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
-        "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]),
-        "+f"(v[14]), "+f"(v[15])
-      :
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
 }
 
 // 8 output channels as fp16.
@@ -1253,40 +1171,6 @@ cudaError_t launch_d(const PagedAttn& a, void* ws, int nsm, cudaStream_t st) {
   return launch_pdl(merge_kernel<D>, dim3(grid, split), dim3(kMergeWarps * 32), 0, st, pa, grid);
 }
 
-// A warp per (sequence, K/V head, position): lanes take (row, head) pairs.
-constexpr int kWarps = 4;
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) weights_kernel(const PagedAttn a) {
-  __shared__ float ks[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, hk = blockIdx.y, G = a.Hq / a.cache.H;
-  PagedSeq e;
-  if (!extent_of(a, b, e) || e.n > a.acc_stride) {
-    if (threadIdx.x == 0) atomicOr(&g_paged_attn_error, kErrExtent);
-    return;
-  }
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < e.n; t += (int64_t)gridDim.x * kWarps) {
-    const uint32_t* ab;
-    const uint8_t* k = row_of<D>(a.cache, b, hk, t, 0, &ab);
-    __syncwarp();
-    for (int j = lane; k && j < D; j += 32)
-      ks[warp][j] = restored(k[j / 2] >> (4 * (j & 1)) & 15u, ab[j / 64]);
-    __syncwarp();
-    float sum = 0.0f;
-    for (int64_t p = lane; p < (int64_t)e.nq * G; p += 32) {
-      const int r = (int)(p / G), hq = hk * G + (int)(p % G), i = e.n - e.nq + r;
-      if (!visible((int)t, i, a.window, a.sinks)) continue;
-      const uint16_t* q = a.q + (e.q0 + r) * a.q_stride + (int64_t)hq * D;
-      float s = 0.0f;
-      for (int j = 0; j < D; ++j) s = fmaf(h2f(q[j]), ks[warp][j], s);
-      sum += expf(s * a.scale - a.lse_in[(int64_t)(e.q0 + r) * a.Hq + hq]);
-    }
-    for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    const int64_t at = ((int64_t)b * a.cache.H + hk) * a.acc_stride + t;
-    if (lane == 0) a.acc_out[at] = (a.acc ? a.acc[at] : 0.0f) + sum;
-  }
-}
-
 }  // namespace
 
 size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
@@ -1297,13 +1181,6 @@ size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
 
 cudaError_t launch_attn_paged(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st) {
   return d == 128 ? launch_d<128>(a, ws, nsm, st) : launch_d<64>(a, ws, nsm, st);
-}
-
-cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st) {
-  const dim3 grid(64, a.cache.H, a.cache.B);
-  if (d == 128) weights_kernel<128><<<grid, kWarps * 32, 0, st>>>(a);
-  else weights_kernel<64><<<grid, kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
 }
 
 cudaError_t paged_attn_read_error(unsigned int* out) {

@@ -244,6 +244,7 @@ cudaError_t ragged_read_error(unsigned int* out);
 cudaError_t decode_window_read_error(unsigned int* out);
 cudaError_t prefill_window_read_error(unsigned int* out);
 cudaError_t paged_attn_read_error(unsigned int* out);
+cudaError_t weights_read_error(unsigned int* out);
 cudaError_t evict_read_error(unsigned int* out);
 
 // Algorithmic work of one launch (bytes for memory-bound kernels, flops for the GEMM and
