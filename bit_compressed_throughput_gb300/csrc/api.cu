@@ -434,6 +434,7 @@ int fg_check_device_error(void* stream) {
                   {"windowed decode attention", decode_window_read_error},
                   {"windowed prefill attention", prefill_window_read_error},
                   {"paged attention", paged_attn_read_error},
+                  {"paged attention of single tokens", paged_step_read_error},
                   {"received weights", weights_read_error},
                   {"eviction", evict_read_error}};
   constexpr int n = sizeof(families) / sizeof(families[0]);
@@ -932,6 +933,8 @@ static int check_paged_attn(const uint16_t* q, int64_t q_stride, int32_t q_rows,
   if (rc || (rc = check_window(window, sinks, scale))) return rc;
   if (!paged_heads_ok(*kv, Hq) || q_rows < 0 || max_q < 0 || q_rows > 0x7FFFFFFF - 65536)
     return FG_ERR_SHAPE;
+  // the streaming kernel numbers a call's tiles, and a warp's share of them
+  if ((int64_t)nseq * Hq > (1ll << 40) / (table_stride * kv->page / 16 + 2)) return FG_ERR_SHAPE;
   if (q_stride < (int64_t)Hq * (kv->h / kv->H) || q_stride % 8 != 0) return FG_ERR_SHAPE;
   if (nseq == 0) {
     *nothing_to_do = true;

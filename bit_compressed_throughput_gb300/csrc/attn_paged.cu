@@ -340,6 +340,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
   pdl_wait();
 
   // ---- the order of the work: its units, and where this share's begin
+  auto ours = [&](const PagedSeq& s) { return !(a.steps && s.nq == 1); };
   int64_t total = 0, before = 0, incl = 0, mine = 0;
   auto scan_round = [&](int b0) {          // a sequence per thread: its units, those up to it
     const int b = b0 + threadIdx.x;
@@ -347,7 +348,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
     if (b < nseq) {
       PagedSeq s;
       if (extent_of(a, b, s))
-        mine = H * head_units(s, shape);
+        mine = ours(s) ? H * head_units(s, shape) : 0;
       else if (blockIdx.x == 0)
         atomicOr(&g_paged_attn_error, kErrExtent);
     }
@@ -635,7 +636,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
                   more = false;
                   break;
                 }
-                k.per_head = extent_of(a, k.b, k.s) ? head_units(k.s, shape) : 0;
+                k.per_head = extent_of(a, k.b, k.s) && ours(k.s) ? head_units(k.s, shape) : 0;
               } while (k.per_head == 0);
             }
           }
@@ -1173,13 +1174,30 @@ cudaError_t launch_d(const PagedAttn& a, void* ws, int nsm, cudaStream_t st) {
 
 }  // namespace
 
+// Scratch of this file's kernels; that of the single tokens' follows.
+static size_t tiles_ws_bytes(int G, int d, int max_q) {
+  return (cut_bytes(kMaxSms) +
+          (size_t)2 * kMaxSms * slot_rows_of(G, max_q) * (d + 2) * sizeof(float) + 255) /
+         256 * 256;
+}
 size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
-  const int G = Hq / kv.H, d = kv.h / kv.H;
-  return cut_bytes(kMaxSms) +
-         (size_t)2 * kMaxSms * slot_rows_of(G, max_q) * (d + 2) * sizeof(float);
+  const int G = Hq / kv.H;
+  return tiles_ws_bytes(G, kv.h / kv.H, max_q) +
+         (G <= kStepHeads ? attn_paged_step_ws_bytes(kv, Hq) : 0);
 }
 
-cudaError_t launch_attn_paged(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st) {
+// Single query rows with few heads go to the streaming kernels: alone where no sequence has more, and
+// ahead of the others where several sequences may be mixed.  (16 contexts of 9000 .. 32760, 8 K/V
+// heads, 4 query heads each: 93 us there, 283 us here.)
+cudaError_t launch_attn_paged(const PagedAttn& call, int d, void* ws, int nsm, cudaStream_t st) {
+  PagedAttn a = call;
+  const int G = a.Hq / a.cache.H;
+  a.steps = G <= kStepHeads && (a.max_q == 1 || a.cache.B > 1);
+  if (a.steps) {
+    void* sws = static_cast<uint8_t*>(ws) + tiles_ws_bytes(G, d, a.max_q);
+    cudaError_t e = launch_attn_paged_step(a, d, sws, nsm, st);
+    if (e != cudaSuccess || a.max_q == 1) return e;
+  }
   return d == 128 ? launch_d<128>(a, ws, nsm, st) : launch_d<64>(a, ws, nsm, st);
 }
 

@@ -71,6 +71,7 @@ struct PagedAttn {
   int64_t q_stride;
   int32_t q_rows, max_q, Hq, window, sinks;
   float scale;
+  bool steps;                // single query rows are attn_paged_step.cu's
   uint16_t* out;             // attention
   int64_t out_stride;
   float* lse;                // [q_rows][Hq], may be null
@@ -79,6 +80,11 @@ struct PagedAttn {
   int64_t acc_stride;
 };
 size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q);
+// The same for the sequences with one query row (attn_paged_step.cu): at most kStepHeads query heads
+// per K/V head.
+constexpr int kStepHeads = 8;
+size_t attn_paged_step_ws_bytes(const fg_kvpages& kv, int32_t Hq);
+cudaError_t launch_attn_paged_step(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st);
 cudaError_t launch_attn_paged(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st);
 cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st);
 
@@ -244,6 +250,7 @@ cudaError_t ragged_read_error(unsigned int* out);
 cudaError_t decode_window_read_error(unsigned int* out);
 cudaError_t prefill_window_read_error(unsigned int* out);
 cudaError_t paged_attn_read_error(unsigned int* out);
+cudaError_t paged_step_read_error(unsigned int* out);
 cudaError_t weights_read_error(unsigned int* out);
 cudaError_t evict_read_error(unsigned int* out);
 
