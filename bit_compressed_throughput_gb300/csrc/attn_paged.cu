@@ -59,9 +59,8 @@ namespace {
 
 using namespace paged;
 
-template <bool LAZY = false>
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return bounded_wait<LAZY>(bar, parity, abort_flag, &g_paged_attn_error);
+  return bounded_wait(bar, parity, abort_flag, &g_paged_attn_error);
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   bounded_drain(bar, parity, &g_paged_attn_error);
@@ -441,7 +440,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         for (int which = 0; which < 2; ++which, ++np) {
           const int st = np % pa.parts;
           if (np >= pa.parts) {
-            const bool fr = bwait<true>(bar(B_CFREE + st), (uint32_t)((np / pa.parts - 1) & 1),
+            const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((np / pa.parts - 1) & 1),
                                         abort_flag);
             if (!__all_sync(0xFFFFFFFFu, fr)) {
               ok = false;
@@ -501,7 +500,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
       if (lane == 0) seg_done(n);
       if (g.b < 0) break;
       const int qb = g.single ? 0 : t;                 // the chain's Q buffer
-      const uint64_t qd = smem_desc(sbase + L::Q_OFF + qb * L::TILE, 16, 1024);
+      const uint64_t qd =
+          smem_desc(__shfl_sync(0xFFFFFFFFu, sbase + L::Q_OFF + qb * L::TILE, 0), 16, 1024);
       wait(B_QFULL, q_uses[0]++ & 1);
       if (!g.single) {
         if (t == 1) wait(B_QFULL + 1, q_uses[1] & 1);
@@ -528,8 +528,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         }
       };
       auto issue_s = [&](int j) {
-        const int st = (g0 + j - g.j0) & 1;
-        const uint64_t kd = smem_desc(sbase + L::K_OFF + st * L::TILE, 16, 1024);
+        const int st = __shfl_sync(0xFFFFFFFFu, (g0 + j - g.j0) & 1, 0);
+        const uint64_t kd =
+            smem_desc(__shfl_sync(0xFFFFFFFFu, sbase + L::K_OFF + st * L::TILE, 0), 16, 1024);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
@@ -539,8 +540,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         commit(B_KFREE + st);
       };
       auto issue_pv = [&](int j, uint32_t add) {
-        const int st = (g0 + j - g.j0) & 1;
-        const uint64_t vd = smem_desc(sbase + L::V_OFF + st * L::TILE, BOX, 1024);
+        const int st = __shfl_sync(0xFFFFFFFFu, (g0 + j - g.j0) & 1, 0);
+        const uint64_t vd =
+            smem_desc(__shfl_sync(0xFFFFFFFFu, sbase + L::V_OFF + st * L::TILE, 0), BOX, 1024);
         umma_ts_if(od, scol, vd, idesc_o, add, one);
 #pragma unroll
         for (int i = 1; i < KT / 16; ++i)
@@ -709,9 +711,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         const int valid = min(128, len - kt.tile(j) * kKeyTile);
         for (int which = 0; which < 2; ++which, ++np) {
           const int st = np % pa.parts, g = np >> 1;
-          bool got = bwait<true>(bar(B_CFULL + st), (uint32_t)((np / pa.parts) & 1), abort_flag);
+          bool got = bwait(bar(B_CFULL + st), (uint32_t)((np / pa.parts) & 1), abort_flag);
           if (g >= 2)
-            got = got && bwait<true>(bar((which ? B_VFREE : B_KFREE) + (g & 1)),
+            got = got && bwait(bar((which ? B_VFREE : B_KFREE) + (g & 1)),
                                (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
           if (!__all_sync(0xFFFFFFFFu, got)) {
             ok = false;

@@ -36,9 +36,8 @@ namespace {
 
 using namespace paged;
 
-template <bool LAZY = false>
 __device__ __forceinline__ bool bwait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return bounded_wait<LAZY>(bar, parity, abort_flag, &g_weights_error);
+  return bounded_wait(bar, parity, abort_flag, &g_weights_error);
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   bounded_drain(bar, parity, &g_weights_error);
@@ -201,8 +200,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   };
 #pragma unroll 1
   for (int b0 = 0; b0 < nseq; b0 += THREADS) total += scan_round(b0);
-  // (every item costs at least 2)
-  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, total / 2));
+  // (a share without an item's beginning has nothing to do)
+  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, total));
   const Shares shares(total, n_shares);
   const bool busy = total > 0 && (int)blockIdx.x < n_shares;
   const int64_t x0 = busy ? shares.first(blockIdx.x) : 0;
@@ -258,7 +257,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const unsigned live = __ballot_sync(0xFFFFFFFFu, at >= 0);
         const int st = np % wa.parts;
         if (np >= wa.parts) {
-          const bool fr = bwait<true>(bar(B_CFREE + st), (uint32_t)((np / wa.parts - 1) & 1),
+          const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((np / wa.parts - 1) & 1),
                                       abort_flag);
           if (!__all_sync(0xFFFFFFFFu, fr)) {
             ok = false;
@@ -291,7 +290,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         drain_wait(bar(B_CFULL + i % wa.parts), (uint32_t)((i / wa.parts) & 1));
     __syncwarp();
   } else if (warp == W_MMA) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer.  What the products take
+    // is the same in every lane, and comes from a shuffle so that it stays in uniform registers.
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), sbase = smem_u32(smem);
     const uint32_t one = elect_one();
     int q_made = 0, q_base = 0, cnt = 0;               // Q tiles so far; the K/V head's first; S pairs
@@ -318,19 +318,22 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const int q = resident ? q_base + r : q_made++;
         wait(B_QFULL + (q & 1), (q >> 1) & 1);
         const int cols = (min(it.nq - r * wa.tpt, wa.tpt) * wa.G + 15) & ~15;
-        const uint32_t idesc = idesc_qk(cols);
-        const uint64_t qd = smem_desc(sbase + L::Q_OFF + (q & 1) * L::TILE, 16, 1024);
+        const uint32_t idesc = __shfl_sync(0xFFFFFFFFu, idesc_qk(cols), 0);
+        const uint64_t qd =
+            smem_desc(__shfl_sync(0xFFFFFFFFu, sbase + L::Q_OFF + (q & 1) * L::TILE, 0), 16, 1024);
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
           const int s = 2 * e + (cnt & 1);
           if (cnt >= 2) wait(B_SFREE + s, ((cnt >> 1) - 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kd = smem_desc(sbase + L::K_OFF + ks[e] * L::TILE, 16, 1024);
+          const uint64_t kd = smem_desc(
+              __shfl_sync(0xFFFFFFFFu, sbase + L::K_OFF + (e ? ks[1] : ks[0]) * L::TILE, 0), 16, 1024);
+          const uint32_t sd = __shfl_sync(0xFFFFFFFFu, tm + 128 * s, 0);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint64_t off = (uint64_t)(((i >> 2) * BOX + (i & 3) * 32) >> 4);
-            umma_f16_if(tm + 128 * s, kd + off, qd + off, idesc, i > 0, one);
+            umma_f16_if(sd, kd + off, qd + off, idesc, i > 0, one);
           }
           commit(B_SFULL + s);
         }
@@ -416,11 +419,11 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             it.nq = s.nq;
             it.n = s.n;
             it.k0 = w.k0;
-            it.r0 = w.r0;
-            it.r1 = w.r1;
-            it.tiles = (int)(((int64_t)s.nq + wa.tpt - 1) / wa.tpt);
+            it.r0 = w.t0 / wa.tpt;
+            it.r1 = w.t1 > w.t0 ? (w.t1 - 1) / wa.tpt + 1 : it.r0;
+            it.tiles = s.nq > 0 ? (s.nq - 1) / wa.tpt + 1 : 0;
           }
-          at += w.cost();
+          at += weight_cost(w, shape);
           if (++i == items) {
             i = 0;
             if (++hk == H) {
@@ -442,7 +445,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         nx.keep = nx.b >= 0 && nx.b == cur.b && nx.hk == cur.hk && nx.tiles <= 2;
         cur.keep_next = nx.keep;
         if (n >= ITEMS &&
-            !bwait<true>(bar(B_IFREE + n % ITEMS), (uint32_t)((n / ITEMS - 1) & 1), abort_flag))
+            !bwait(bar(B_IFREE + n % ITEMS), (uint32_t)((n / ITEMS - 1) & 1), abort_flag))
           break;
         *item_slot(n) = cur;
         mbar_arrive(bar(B_IFULL + n % ITEMS));
@@ -465,9 +468,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll 1
       for (int e = 0; e < 2; ++e, ++np) {
         const int st = np % wa.parts, ks = np % KRING;
-        bool got = bwait<true>(bar(B_CFULL + st), (uint32_t)((np / wa.parts) & 1), abort_flag);
+        bool got = bwait(bar(B_CFULL + st), (uint32_t)((np / wa.parts) & 1), abort_flag);
         if (np >= KRING)
-          got = got && bwait<true>(bar(B_KFREE + ks), (uint32_t)((np / KRING - 1) & 1), abort_flag);
+          got = got && bwait(bar(B_KFREE + ks), (uint32_t)((np / KRING - 1) & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           ok = false;
           break;
@@ -492,32 +495,47 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const int tok = m / wa.G, gh = m - tok * wa.G;
     const uint64_t sl2x2 = f2pack(wa.scale_log2, wa.scale_log2);
     int cnt = 0;                                       // row tiles
-    bool ok = true;
+    // The log-sum-exp of row m of row tile r of an item: -inf for columns of no row.
+    auto fetch = [&](const Item& it, int r) -> float {
+      const int i = r * wa.tpt + tok;
+      if (r >= it.r1 || tok >= wa.tpt || i >= it.nq) return -INFINITY;
+      return a.lse_in[(int64_t)(it.q0 + i) * a.Hq + it.hk * wa.G + gh];
+    };
+    auto weight_at = [&](const Item& it) {
+      return ((int64_t)it.b * H + it.hk) * a.acc_stride + it.k0 + e * kKeyTile + m;
+    };
+    auto fetch_old = [&](const Item& it) -> float {
+      return a.acc && it.k0 + e * kKeyTile + m < it.n ? a.acc[weight_at(it)] : 0.0f;
+    };
+    float z_next = -INFINITY, old_next = 0.0f;         // of the next item, in flight
+    bool ok = item_wait(0);
+    if (ok && item_slot(0)->b >= 0) {
+      z_next = fetch(*item_slot(0), item_slot(0)->r0);
+      old_next = fetch_old(*item_slot(0));
+    }
     for (int n = 0; ok; ++n) {
-      if (!item_wait(n)) break;
       const Item& it = *item_slot(n);                  // read where needed: no registers for it
       if (it.b < 0) break;
       const int t = it.k0 + e * kKeyTile + m;          // the thread's position
       const bool live = t < it.n;
-      const int64_t at = ((int64_t)it.b * H + it.hk) * a.acc_stride + t;
-      const float old = live && a.acc ? a.acc[at] : 0.0f;
-      // the row's -lse / ln 2; -inf for columns of no row, and rows that see nothing (0 then)
-      auto fetch = [&](int r) -> float {
-        const int i = r * wa.tpt + tok;
-        if (r >= it.r1 || tok >= wa.tpt || i >= it.nq) return -INFINITY;
-        const float z = a.lse_in[(int64_t)(it.q0 + i) * a.Hq + it.hk * wa.G + gh];
-        return z == -INFINITY ? z : z * -1.4426950408889634f;
-      };
-      float z = fetch(it.r0);
+      float z = z_next;
+      const float old = old_next;
+      if (!item_wait(n + 1)) break;
+      const Item& nx = *item_slot(n + 1);
+      if (nx.b >= 0) {
+        z_next = fetch(nx, nx.r0);
+        old_next = fetch_old(nx);
+      }
       uint64_t sum2[2] = {f2pack(0.0f, 0.0f), f2pack(0.0f, 0.0f)};
 #pragma unroll 1
       for (int r = it.r0; r < it.r1; ++r, ++cnt) {
         const int s = cnt & 1;
         // (the buffer's last readers have arrived at the other buffer's barrier since)
-        lse[128 * s + m] = z;
+        // (-lse / ln 2; a row that sees nothing has -inf, and adds 0)
+        lse[128 * s + m] = z == -INFINITY ? z : z * -1.4426950408889634f;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_ZFULL + 2 * e + s));
-        z = fetch(r + 1);                              // in flight meanwhile
+        z = fetch(it, r + 1);                          // in flight meanwhile
         // columns c0 .. c1 - 1 are rows that see the position
         const int ntok = min(it.nq - r * wa.tpt, wa.tpt), pos0 = it.n - it.nq + r * wa.tpt;
         const int64_t first = (int64_t)t - pos0;
@@ -580,7 +598,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       if (!ok) break;
       const float2 su = f2unpack(fadd2(sum2[0], sum2[1]));
-      if (live) a.acc_out[at] = old + (su.x + su.y);
+      if (live) a.acc_out[weight_at(it)] = old + (su.x + su.y);
       item_done(n);
     }
   }

@@ -36,8 +36,6 @@ static __device__ __noinline__ bool gave_up(long long t0, volatile int* abort_fl
   atomicOr(word, kErrWait);
   return true;
 }
-// LAZY: for warps that run ahead of the others, which need the instruction fetches more.
-template <bool LAZY = false>
 __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                              unsigned int* word) {
   if (mbar_test(bar, parity)) return true;
@@ -45,7 +43,6 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
 #pragma unroll 1
   for (unsigned n = 1;; ++n) {
     if (mbar_try(bar, parity)) return true;
-    if (LAZY) __nanosleep(200);
     if ((n & 63u) == 0 && gave_up(t0, abort_flag, word)) return false;
   }
 }

@@ -133,13 +133,13 @@ struct PagedWalk {
 };
 
 // ---- the weights that positions receive: items of 256 positions of one K/V head (two key tiles), for
-// each the row tiles that see one of them.  An item costs its restoring (two units) and a unit per
-// row tile; a share owns the items that begin in it, so its sums have one owner each.
+// each the row tiles that see one of them.  An item costs as many units as tokens see it, and its
+// restoring as many as two row tiles hold; a share owns the items that begin in it, so its sums have
+// one owner each.
 constexpr int kItemKeys = 2 * kKeyTile;
 struct WeightItem {
   int k0;              // first position
-  int r0, r1;          // row tiles
-  FG_HD int cost() const { return 2 + r1 - r0; }
+  int t0, t1;          // the tokens that see one of its positions
 };
 FG_HD int weight_items(const PagedSeq& s) {
   return (int)(((int64_t)s.n + kItemKeys - 1) / kItemKeys);
@@ -147,20 +147,21 @@ FG_HD int weight_items(const PagedSeq& s) {
 FG_HD WeightItem weight_item(const PagedSeq& s, int i, const PagedShape& sh) {
   WeightItem w;
   w.k0 = i * kItemKeys;
-  const int64_t first = (int64_t)s.n - s.nq;           // position of the first token
-  const int64_t last = (s.n - w.k0 < kItemKeys ? s.n : w.k0 + kItemKeys) - 1;
-  const int64_t t0 = w.k0 > first ? w.k0 - first : 0;  // the first token that sees position k0
-  int64_t t1 = s.nq;                                   // behind the last that sees one
-  if (sh.window != 0 && w.k0 >= sh.sinks && last + sh.window - first < t1)
-    t1 = last + sh.window - first;
-  w.r0 = (int)(t0 / sh.tpt);
-  w.r1 = (int)((t1 + sh.tpt - 1) / sh.tpt);
-  if (t1 <= t0) w.r1 = w.r0;
+  const int first = s.n - s.nq;                        // position of the first token
+  const int last = (s.n - w.k0 < kItemKeys ? s.n : w.k0 + kItemKeys) - 1;
+  w.t0 = w.k0 > first ? w.k0 - first : 0;              // the first token that sees position k0
+  w.t1 = s.nq;                                         // behind the last that sees one
+  if (sh.window != 0 && w.k0 >= sh.sinks && (int64_t)last + sh.window - first < w.t1)
+    w.t1 = last + sh.window - first;
+  if (w.t1 < w.t0) w.t1 = w.t0;
   return w;
+}
+FG_HD int64_t weight_cost(const WeightItem& w, const PagedShape& sh) {
+  return 2 * sh.tpt + w.t1 - w.t0;
 }
 FG_HD int64_t weight_units(const PagedSeq& s, const PagedShape& sh) {   // of one K/V head
   int64_t u = 0;
-  for (int i = weight_items(s) - 1; i >= 0; --i) u += weight_item(s, i, sh).cost();
+  for (int i = weight_items(s) - 1; i >= 0; --i) u += weight_cost(weight_item(s, i, sh), sh);
   return u;
 }
 
