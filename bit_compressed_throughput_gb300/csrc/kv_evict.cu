@@ -1,15 +1,21 @@
 // Smaller caches: every K/V head of a sequence keeps its newest positions and the heaviest of the
 // others, moved in order into pages of their own (sm_103a).
 //
-// Selection, a CTA per (sequence, head): the weights' order keys are 32-bit numbers, and four
-// passes over them, a histogram of 8 bits each, find the key of the last one that stays and how many
-// equal ones do; a last pass lists the positions in order.  Ties go to the lower position.
-// Moving: a position's K and V codes and statistics, copied as they are.
+// Selection, a CTA per (sequence, head), or four that share its positions where such pairs are few and
+// long (they add up their counts through one another's shared memory): the weights' order keys are 32-bit numbers, and three
+// passes over them, histograms of 11, 11 and 10 bits, find the key of the last one that stays and how
+// many equal ones do.  (11 bits of a weight are its exponent and two bits more, so that the threads
+// of a warp rarely meet in one bin.)  Then every warp counts what stays of its part of the
+// positions, and lists it behind what the warps before it have.  Ties go to the lower position.
+// Moving: a position's K and V codes and statistics, copied as they are, 16 bytes a thread.
+// Bound by HBM: the weights once, 2 * 1.125 d bytes per kept position; by latency where a call has few
+// (sequence, head) pairs.
 #include <algorithm>
 
 #include "attn_q4.cuh"
 #include "fg_common.cuh"
 #include "fg_internal.h"
+#include "gemm_tc.cuh"
 #include "paged.cuh"
 #include "ragged.cuh"
 
@@ -22,35 +28,34 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
-// The block's sum of `mine`, and the sum of the threads before this one.
-__device__ __forceinline__ int block_scan(int mine, int* warp_sums, int* before) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  int total = 0, base = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i == warp) base = total;
-    total += warp_sums[i];
-  }
-  *before = base + incl - mine;
-  return total;
+constexpr int kBins = 2048;
+
+constexpr int kShare = 4;                  // CTAs of a pair of its own
+
+__device__ __forceinline__ uint32_t key_of(const float* acc, int i) {
+  return q4attn::order_key_f32(acc[i]);
+}
+// A word of the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)));
+  return v;
 }
 
+template <int CL>
 __global__ void __launch_bounds__(kThreads) select_kernel(const Evict a) {
-  __shared__ int hist[256];
-  __shared__ int warp_sums[kWarps];
+  __shared__ int hist[kBins];
+  __shared__ int2 warp_counts[kWarps];
+  __shared__ int2 totals;                  // of the CTA's positions: that stay for sure, equal ones
   __shared__ int found[2];
+  const int rank = CL == 1 ? 0 : (int)cluster_ctarank();
+  auto together = [&]() {                  // all threads of the pair's CTAs
+    if (CL == 1) __syncthreads(); else cluster_sync_all();
+  };
   pdl_launch_dependents();
   pdl_wait();
-  const int head = blockIdx.x, b = blockIdx.y, H = a.src.H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x / CL, b = blockIdx.y, H = a.src.H;
   int n = a.lens[b];
   if (n < 0 || n > a.src.cap() || n > a.acc_stride) {
     if (threadIdx.x == 0) atomicOr(&g_evict_error, kErrExtent);
@@ -61,13 +66,13 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Evict a) {
   int32_t* kept = a.kept + row * a.keep;
   float* acc_out = a.acc_out + row * a.keep;
   const int left = min(n, a.keep);
-  if (head == 0 && threadIdx.x == 0) a.dst_lens[b] = left;
-  for (int i = left + threadIdx.x; i < a.keep; i += kThreads) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.dst_lens[b] = left;
+  for (int i = left + rank * kThreads + threadIdx.x; i < a.keep; i += CL * kThreads) {
     kept[i] = -1;
     acc_out[i] = 0.0f;
   }
   if (n <= a.keep) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = rank * kThreads + threadIdx.x; i < n; i += CL * kThreads) {
       kept[i] = i;
       acc_out[i] = acc[i];
     }
@@ -75,86 +80,184 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Evict a) {
   }
   const int old = n - a.recent;            // recent <= keep < n
   int want = a.keep - a.recent;            // of the first `old`
-  // the key of the want-th largest, 8 bits at a time
+  const bool none = want == 0;
+  // the CTA's positions
+  const int share = ((n + CL - 1) / CL + 31) & ~31;
+  const int n0 = min(n, rank * share), n1 = min(n, n0 + share);
+  // the key of the want-th largest: bits 21 and up, 10 .. 20, 0 .. 9
   uint32_t prefix = 0;
-  for (int shift = 24; want > 0 && shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < old; i += kThreads) {
-      const uint32_t k = q4attn::order_key_f32(acc[i]);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[k >> shift & 255u], 1);
+  if (!none) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+      const uint32_t mask = pass == 2 ? 1023u : 2047u;
+      const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);      // bits that are settled
+      for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+      __syncthreads();
+#pragma unroll 8
+      for (int i = n0 + threadIdx.x; i < min(n1, old); i += kThreads) {
+        const uint32_t k = key_of(acc, i);
+        if (pass == 0 || (k >> above) == prefix) atomicAdd(&hist[k >> shift & mask], 1);
+      }
+      together();
+      // bins from the top, two a thread: the one in which the want-th falls
+      const int b1 = (int)mask - 2 * (int)threadIdx.x, b0 = b1 - 1;
+      int c1 = 0, c0 = 0;
+#pragma unroll
+      for (int r = 0; r < CL; ++r) {
+        if (b1 >= 0) c1 += CL == 1 ? hist[b1] : ld_cluster(&hist[b1], r);
+        if (b0 >= 0) c0 += CL == 1 ? hist[b0] : ld_cluster(&hist[b0], r);
+      }
+      int incl = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) warp_counts[warp].x = incl;
+      __syncthreads();
+      int before = incl - c0 - c1;
+      for (int i = 0; i < warp; ++i) before += warp_counts[i].x;
+      if (before < want && before + c1 >= want) {
+        found[0] = b1;
+        found[1] = before;
+      } else if (before + c1 < want && before + c1 + c0 >= want) {
+        found[0] = b0;
+        found[1] = before + c1;
+      }
+      together();                          // (the counts are read by others, too)
+      prefix = prefix << (pass == 0 ? 0 : (pass == 1 ? 11 : 10)) | (uint32_t)found[0];
+      want -= found[1];
     }
-    __syncthreads();
-    // bins from the top: the one in which the want-th falls
-    const int bin = 255 - (int)threadIdx.x;
-    int before, mine = threadIdx.x < 256 ? hist[bin] : 0;
-    block_scan(mine, warp_sums, &before);
-    if (threadIdx.x < 256 && before < want && before + mine >= want) {
-      found[0] = bin;
-      found[1] = before;
-    }
-    __syncthreads();
-    prefix = prefix << 8 | (uint32_t)found[0];
-    want -= found[1];
   }
-  // larger keys stay, and the first `want` equal ones
-  const bool none = a.keep == a.recent;
-  int at = 0, equal = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t k = i < old && !none ? q4attn::order_key_f32(acc[i]) : 0;
-    const bool same = i < old && !none && k == prefix;
-    int before;
-    const int equals = block_scan(same, warp_sums, &before);
-    const bool stays = i < n && (i >= old || (!none && (k > prefix || (same && equal + before < want))));
-    const int stay = block_scan(stays, warp_sums, &before);
+  // larger keys stay, and the first `want` equal ones; a warp has positions i0 .. i1 - 1
+  const int per = ((share + kWarps - 1) / kWarps + 31) & ~31;
+  const int i0 = min(n1, n0 + warp * per), i1 = min(n1, i0 + per);
+  int2 cnt = make_int2(0, 0);              // that stay for sure; equal ones
+#pragma unroll 4
+  for (int base = i0; base < i1; base += 32) {         // the same turns for every lane
+    const int i = base + lane;
+    const uint32_t k = i < old && i < i1 && !none ? key_of(acc, i) : 0u;
+    const bool sure = i < i1 && (i >= old || (!none && k > prefix));
+    const bool same = i < i1 && i < old && !none && k == prefix;
+    cnt.x += __popc(__ballot_sync(0xFFFFFFFFu, sure));
+    cnt.y += __popc(__ballot_sync(0xFFFFFFFFu, same));
+  }
+  __syncthreads();
+  if (lane == 0) warp_counts[warp] = cnt;
+  __syncthreads();
+  int sure_before = 0, equal = 0;
+  for (int i = 0; i < warp; ++i) {
+    sure_before += warp_counts[i].x;
+    equal += warp_counts[i].y;
+  }
+  if (CL > 1) {
+    if (threadIdx.x == kThreads - 1)
+      totals = make_int2(sure_before + cnt.x, equal + cnt.y);
+    together();
+    for (int r = 0; r < rank; ++r) {
+      sure_before += ld_cluster(&totals.x, r);
+      equal += ld_cluster(&totals.y, r);
+    }
+  }
+  int at = sure_before + min(equal, want);
+#pragma unroll 4
+  for (int base = i0; base < i1; base += 32) {         // the same turns for every lane
+    const int i = base + lane;
+    const float w = i < i1 ? acc[i] : 0.0f;
+    const uint32_t k = q4attn::order_key_f32(w);
+    const bool sure = i < i1 && (i >= old || (!none && k > prefix));
+    const bool same = i < i1 && i < old && !none && k == prefix;
+    const unsigned eq = __ballot_sync(0xFFFFFFFFu, same), below = (1u << lane) - 1u;
+    const bool stays = sure || (same && equal + __popc(eq & below) < want);
+    const unsigned st = __ballot_sync(0xFFFFFFFFu, stays);
     if (stays) {
-      kept[at + before] = i;
-      acc_out[at + before] = acc[i];
+      kept[at + __popc(st & below)] = i;
+      acc_out[at + __popc(st & below)] = w;
     }
-    at += stay;
-    equal += equals;
+    at += __popc(st);
+    equal += __popc(eq);
   }
+  if (CL > 1) together();                  // others may still read this CTA's totals
 }
 
-// A warp per kept position.
+// 16 bytes of codes a thread (2 * D / 32 threads a position: K, then V), and a statistics word of it
+// each; kMoves positions in flight.
+constexpr int kMoves = 4;
 template <int D>
 __global__ void __launch_bounds__(256) move_kernel(const Evict a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  constexpr int TPP = D / 16, PER = 256 / TPP;           // threads per position, positions a turn
+  const int u = threadIdx.x % TPP, which = u / (TPP / 2), c = u % (TPP / 2);
   const int head = blockIdx.y, b = blockIdx.z, H = a.src.H;
   const int64_t row = (int64_t)b * H + head;
   const int n = a.dst_lens[b];
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
-    const int t = a.kept[row * a.keep + i];
-    const int64_t s = a.src.slot(b, t), d = a.dst.slot(b, i);
-    if (s < 0 || d < 0) {
-      if (lane == 0) atomicOr(&g_evict_error, kErrExtent);
-      continue;
-    }
-    const int64_t sp = s & ((1 << a.src.lg) - 1), dp = d & ((1 << a.src.lg) - 1);
-    const int64_t ab = (int64_t)(D / 2) << a.src.lg;
-    for (int w = 0; w < 2; ++w) {
-      const uint8_t* f = a.src.block(s, head, D) + w * a.src.half_bytes(D);
-      uint8_t* g = a.dst.block(d, head, D) + w * a.src.half_bytes(D);
-      if (lane < D / 8)
-        reinterpret_cast<uint32_t*>(g + dp * (D / 2))[lane] =
-            reinterpret_cast<const uint32_t*>(f + sp * (D / 2))[lane];
-      if (lane < D / 64)
-        reinterpret_cast<uint32_t*>(g + ab)[dp * (D / 64) + lane] =
-            reinterpret_cast<const uint32_t*>(f + ab)[sp * (D / 64) + lane];
+  const int64_t ab = (int64_t)(D / 2) << a.src.lg, v = which * a.src.half_bytes(D);
+  const int mask = (1 << a.src.lg) - 1;
+  const int first = blockIdx.x * PER * kMoves + threadIdx.x / TPP;
+  int64_t s[kMoves], d[kMoves];
+#pragma unroll
+  for (int j = 0; j < kMoves; ++j) {
+    const int i = first + j * PER;
+    s[j] = i < n ? a.kept[row * a.keep + i] : -1;
+  }
+#pragma unroll
+  for (int j = 0; j < kMoves; ++j) {
+    const int i = first + j * PER;
+    if (i >= n) continue;
+    d[j] = a.dst.slot(b, i);
+    s[j] = a.src.slot(b, s[j]);
+    if (s[j] < 0 || d[j] < 0) {
+      if (u == 0) atomicOr(&g_evict_error, kErrExtent);
+      s[j] = -1;
     }
   }
+  uint4 x[kMoves];
+  uint32_t w[kMoves];
+#pragma unroll
+  for (int j = 0; j < kMoves; ++j)
+    if (s[j] >= 0) {
+      const uint8_t* f = a.src.block(s[j], head, D) + v;
+      const int64_t p = s[j] & mask;
+      x[j] = *reinterpret_cast<const uint4*>(f + p * (D / 2) + 16 * c);
+      if (c < D / 64) w[j] = reinterpret_cast<const uint32_t*>(f + ab)[p * (D / 64) + c];
+    }
+#pragma unroll
+  for (int j = 0; j < kMoves; ++j)
+    if (s[j] >= 0) {
+      uint8_t* g = a.dst.block(d[j], head, D) + v;
+      const int64_t p = d[j] & mask;
+      *reinterpret_cast<uint4*>(g + p * (D / 2) + 16 * c) = x[j];
+      if (c < D / 64) reinterpret_cast<uint32_t*>(g + ab)[p * (D / 64) + c] = w[j];
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const Evict& a, int d, int nsm, cudaStream_t st) {
-  cudaError_t e = launch_pdl(select_kernel, dim3(a.src.H, a.src.B), dim3(kThreads), 0, st, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kShare;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  // four CTAs where the pairs leave most SMs idle and may be long (4 sequences of 8 heads, 20001 ..
+  // 32001 positions: 52 us with one CTA each, selection and move, 43 with four; 128 pairs of 4096: 16)
+  const bool few = (int64_t)a.src.H * a.src.B * kShare <= nsm &&
+                   std::min<int64_t>(a.src.cap(), a.acc_stride) >= 4096;
+  cfg.numAttrs = few ? 2 : 1;
+  cfg.gridDim = dim3(a.src.H * (few ? kShare : 1), a.src.B);
+  cudaError_t e = few ? cudaLaunchKernelEx(&cfg, select_kernel<kShare>, a)
+                      : cudaLaunchKernelEx(&cfg, select_kernel<1>, a);
   if (e != cudaSuccess) return e;
+  const int per = 256 / (d / 16) * kMoves;
   return launch_pdl(d == 128 ? move_kernel<128> : move_kernel<64>,
-                    dim3(std::min((a.keep + 7) / 8, 64), a.src.H, a.src.B), dim3(256), 0, st, a);
+                    dim3((a.keep + per - 1) / per, a.src.H, a.src.B), dim3(256), 0, st, a);
 }
 
 cudaError_t evict_read_error(unsigned int* out) { return read_and_clear(g_evict_error, out); }

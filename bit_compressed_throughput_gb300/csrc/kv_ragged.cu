@@ -503,20 +503,26 @@ read_kernel(const RaggedArgs a, const Cache cache, uint16_t* __restrict__ k_out,
   }
 }
 
-// Heads per CTA: as many as leave the grid kCtasPerSm CTAs per SM, at most 8, so that the lookup
+// Heads per CTA: as many as leave the grid ctas_per_sm CTAs per SM, at most 8, so that the lookup
 // of a tile's rows is shared; one when there are few tiles.
-constexpr int kCtasPerSm = 16;
+constexpr int kCtasPerSm = 16, kTurnCtasPerSm = 4;
 template <typename Kernel, typename... Args>
-cudaError_t launch(Kernel* kernel, const int32_t* row_off, const int32_t* pos, int32_t rows,
-                   int64_t stride, int B, int H, int d, int nsm, cudaStream_t st, Args... args) {
+cudaError_t launch_per_sm(int ctas_per_sm, Kernel* kernel, const int32_t* row_off,
+                          const int32_t* pos, int32_t rows, int64_t stride, int B, int H, int d,
+                          int nsm, cudaStream_t st, Args... args) {
   const int per = 16 * kThreads / d;
   const int64_t tiles = ((int64_t)rows + per - 1) / per;
   const int heads =
-      (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * H / ((int64_t)nsm * kCtasPerSm)));
+      (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * H / ((int64_t)nsm * ctas_per_sm)));
   const int hblocks = (H + heads - 1) / heads;
   if (tiles * hblocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const RaggedArgs a{row_off, pos, rows, B, H, heads, hblocks, stride};
   return launch_pdl(kernel, dim3((unsigned)(tiles * hblocks)), dim3(kThreads), 0, st, a, args...);
+}
+template <typename Kernel, typename... Args>
+cudaError_t launch(Kernel* kernel, const int32_t* row_off, const int32_t* pos, int32_t rows,
+                   int64_t stride, int B, int H, int d, int nsm, cudaStream_t st, Args... args) {
+  return launch_per_sm(kCtasPerSm, kernel, row_off, pos, rows, stride, B, H, d, nsm, st, args...);
 }
 
 }  // namespace
@@ -552,8 +558,9 @@ cudaError_t launch_kv_append_paged(const uint16_t* k_new, const uint16_t* v_new,
     else
       kernel = d == 128 ? append_kernel<128, Pages, 1> : append_kernel<64, Pages, 1>;
   }
-  return launch(kernel, row_off, pos, rows, row_stride, pc.B, pc.H, d, nsm, st, k_new, v_new,
-                Pages{pc}, turn);
+  // (a CTA's angles serve all of its heads)
+  return launch_per_sm(rope ? kTurnCtasPerSm : kCtasPerSm, kernel, row_off, pos, rows, row_stride,
+                       pc.B, pc.H, d, nsm, st, k_new, v_new, Pages{pc}, turn);
 }
 
 cudaError_t launch_kv_read_paged(const PagedCache& pc, int d, const int32_t* row_off,
