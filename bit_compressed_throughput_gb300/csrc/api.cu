@@ -436,6 +436,7 @@ int fg_check_device_error(void* stream) {
                   {"paged attention", paged_attn_read_error},
                   {"paged attention of single tokens", paged_step_read_error},
                   {"received weights", weights_read_error},
+                  {"received weights of few rows", weights_step_read_error},
                   {"eviction", evict_read_error}};
   constexpr int n = sizeof(families) / sizeof(families[0]);
   DeviceErrorWord words[n];

@@ -87,6 +87,9 @@ size_t attn_paged_step_ws_bytes(const fg_kvpages& kv, int32_t Hq);
 cudaError_t launch_attn_paged_step(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st);
 cudaError_t launch_attn_paged(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st);
 cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st);
+// The same for the sequences with at most kStepRows query rows of a K/V head (attn_weights_step.cu).
+constexpr int kStepRows = 32;
+cudaError_t launch_attn_weights_step(const PagedAttn& a, int d, int nsm, cudaStream_t st);
 
 // Eviction (kv_evict.cu): src and dst are the same blocks under two page tables.
 struct Evict {
@@ -252,6 +255,7 @@ cudaError_t prefill_window_read_error(unsigned int* out);
 cudaError_t paged_attn_read_error(unsigned int* out);
 cudaError_t paged_step_read_error(unsigned int* out);
 cudaError_t weights_read_error(unsigned int* out);
+cudaError_t weights_step_read_error(unsigned int* out);
 cudaError_t evict_read_error(unsigned int* out);
 
 // Algorithmic work of one launch (bytes for memory-bound kernels, flops for the GEMM and
