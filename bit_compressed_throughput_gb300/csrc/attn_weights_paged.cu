@@ -84,6 +84,11 @@ constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_KFULL = 2 * MAX_PARTS, B_KFREE
               B_DRAIN = B_IFREE + ITEMS, NBARS = B_DRAIN + 1;
 static_assert(NBARS * 8 + 16 <= 512, "control space");
 
+// (a called function: groups with infinities or NaN are rare)
+__device__ __noinline__ uint4 restore8_any(uint32_t codes, uint32_t abw) {
+  return restore8_fp16(codes, abw);
+}
+
 // A K part into an fp16 tile: two threads per position (the loop stays a loop, so that its
 // instructions stay near).
 template <int D>
@@ -95,6 +100,8 @@ __device__ __forceinline__ void restore_k(uint32_t part, uint32_t tile, int lgb,
   const uint32_t word = ld_shared(sub + ((D / 2) << lgb) + r * (D / 16) + (D == 128 ? 4 * h : 0));
   const uint32_t abw = row < valid ? word : 0u;        // (0, 0): every code is 0
   const uint32_t dst = tile + (D == 128 ? h * BOX : 0) + row * 128;
+  const GroupFp16 g(abw);
+  const bool plain = __all_sync(0xFFFFFFFFu, g.plain);
 #pragma unroll 1
   for (int it = 0; it < D / 64; ++it) {
     const int half = D == 128 ? it ^ h : h;            // 8 threads' stores meet all banks
@@ -103,7 +110,7 @@ __device__ __forceinline__ void restore_k(uint32_t part, uint32_t tile, int lgb,
     const uint32_t to = dst + (((4 * half) ^ (row & 4)) << 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 o = restore8_fp16(ww[i], abw);
+      const uint4 o = plain ? g.restore(ww[i]) : restore8_any(ww[i], abw);
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((i ^ (row & 3)) << 4)),
                    "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w));
     }

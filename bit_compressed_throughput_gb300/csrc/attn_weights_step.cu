@@ -37,11 +37,16 @@ struct SArgs {
   int G;
 };
 
+// (a called function: groups with infinities or NaN are rare)
+__device__ __noinline__ uint4 restore8_any(uint32_t codes, uint32_t abw) {
+  return restore8_fp16(codes, abw);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(const SArgs sa) {
   constexpr int NW = D / 32;               // code words of a position in a lane
   __shared__ uint4 qf[kSets * NW * 32];    // [set][word][lane]: 8 channels of query row 8 set + gid
-  __shared__ float zs[kStepRows];          // -lse / ln 2; -inf: no row, or one that sees nothing
+  __shared__ __align__(8) float zs[kStepRows];          // -lse / ln 2; -inf: no row, or one that sees nothing
   __shared__ int64_t warp_units[kWarps];
   __shared__ int first_b;
   __shared__ int64_t first_before;
@@ -184,16 +189,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(cons
     if (x + 1 < x1) slot = lane < 2 ? slot_of(lane) : -2;
     // ---- products and sums
     float sum[2][2] = {};
+    // every row sees all of the warp's positions
+    const bool all_see = a.window == 0 && p0 + 31 <= pos0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (sl[t] < 0) continue;
       uint4 k0[NW], k1[NW];
       const uint32_t w0[4] = {kw[t][0].x, kw[t][0].y, kw[t][0].z, kw[t][0].w};
       const uint32_t w1[4] = {kw[t][1].x, kw[t][1].y, kw[t][1].z, kw[t][1].w};
+      const GroupFp16 g0(ab[t][0]), g1(ab[t][1]);
+      if (__all_sync(0xFFFFFFFFu, g0.plain && g1.plain)) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        k0[w] = restore8_fp16(w0[w], ab[t][0]);
-        k1[w] = restore8_fp16(w1[w], ab[t][1]);
+        for (int w = 0; w < NW; ++w) {
+          k0[w] = g0.restore(w0[w]);
+          k1[w] = g1.restore(w1[w]);
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          k0[w] = restore8_any(w0[w], ab[t][0]);
+          k1[w] = restore8_any(w1[w], ab[t][1]);
+        }
       }
       const int tp = p0 + 16 * t + gid;    // the lane's positions: tp and tp + 8
 #pragma unroll 1
@@ -206,14 +222,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(cons
           mma16816(c, k0[w].z, k1[w].z, k0[w].w, k1[w].w, q.z, q.w);
         }
         // c[2 r + e]: position tp + 8 r, query row 8 set + 2 tig + e
+        const float2 z = *reinterpret_cast<const float2*>(zs + 8 * set + 2 * tig);
+        if (all_see) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 8 * set + 2 * tig + e, pos = pos0 + row / G;
-          const float z = zs[row];
+          for (int r = 0; r < 2; ++r) {
+            const float y0 = ex2(fmaf(c[2 * r], sa.scale_log2, z.x));
+            const float y1 = ex2(fmaf(c[2 * r + 1], sa.scale_log2, z.y));
+            sum[t][r] += (8 * set + 2 * tig < rows ? y0 : 0.0f) +
+                         (8 * set + 2 * tig + 1 < rows ? y1 : 0.0f);
+          }
+        } else {
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            if (row < rows && visible(tp + 8 * r, pos, a.window, a.sinks))
-              sum[t][r] += ex2(fmaf(c[2 * r + e], sa.scale_log2, z));
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * set + 2 * tig + e, pos = pos0 + row / G;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (row < rows && visible(tp + 8 * r, pos, a.window, a.sinks))
+                sum[t][r] += ex2(fmaf(c[2 * r + e], sa.scale_log2, e ? z.y : z.x));
+          }
         }
       }
     }

@@ -51,4 +51,32 @@ __device__ __forceinline__ uint4 restore8_fp16(uint32_t codes, uint32_t abw) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The same with a group's constants computed once for many code words; `plain`: its statistics are
+// finite (elsewhere the words take restore8_fp16).
+struct GroupFp16 {
+  uint64_t a2, s2, c2;
+  bool plain;
+  __device__ __forceinline__ explicit GroupFp16(uint32_t abw) {
+    const float2 ab = unpack_h2(abw);
+    const float s = div15(__fsub_rn(ab.y, ab.x)), c = -8388608.0f * s;
+    a2 = q4_pack2(ab.x, ab.x);
+    s2 = q4_pack2(s, s);
+    c2 = q4_pack2(c, c);
+    plain = s < INFINITY;
+  }
+  __device__ __forceinline__ uint4 restore(uint32_t codes) const {
+    const uint32_t ev = codes & 0x0F0F0F0Fu, od = (codes >> 4) & 0x0F0F0F0Fu;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(__byte_perm(ev, 0x4B000000u, 0x7440 + i));
+      const float hi = __uint_as_float(__byte_perm(od, 0x4B000000u, 0x7440 + i));
+      float x, y;
+      q4_unpack2(q4_add2(a2, q4_fma2(q4_pack2(lo, hi), s2, c2)), x, y);
+      o[i] = pack_h2(x, y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
+
 }  // namespace fg
