@@ -1057,7 +1057,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
 
 // Puts cut blocks together: a warp per row, its pieces (m, l, unnormalised O) in order, 32 at a
 // time.
-constexpr int kMergeWarps = 8, kMergeSplit = 4;
+constexpr int kMergeWarps = 8, kMergeSplit = 16;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PArgs pa, int ncta) {
   pdl_launch_dependents();

@@ -15,7 +15,7 @@
 //   warp 2        Q row tiles by TMA, a ring of two (two or fewer stay while the K/V head does)
 //   warp 3        items
 //   warps 4-11    a key tile each four: exponentials and sums
-//   warps 12-19   K^ = fp16(a + q (b - a) / 15) exactly as defined (the sums are binary32, and errors of
+//   warps 12-15   K^ = fp16(a + q (b - a) / 15) exactly as defined (the sums are binary32, and errors of
 //                 K^ would show in them), once per item
 // What bounds it: with few rows, the bytes of K (0.5625 d per position) and restoring them; with many,
 // the exponentials, one per pair, beside 2 d multiply-adds.
@@ -43,8 +43,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   bounded_drain(bar, parity, &g_weights_error);
 }
 
-constexpr int THREADS = 20 * 32;
-constexpr int W_MMA = 1, W_Q = 2, W_ITEM = 3, W_EXP = 4, W_RST = 12, RST_WARPS = 8;
+constexpr int THREADS = 16 * 32;
+constexpr int W_MMA = 1, W_Q = 2, W_ITEM = 3, W_EXP = 4, W_RST = 12, RST_WARPS = 4;
 constexpr int ITEMS = 4, KRING = 4, MAX_PARTS = 8;
 
 struct Item {
@@ -89,30 +89,35 @@ __device__ __noinline__ uint4 restore8_any(uint32_t codes, uint32_t abw) {
   return restore8_fp16(codes, abw);
 }
 
-// A K part into an fp16 tile: two threads per position (the loop stays a loop, so that its
-// instructions stay near).
+// A K part into an fp16 tile, a thread per position.  Positions take their 16-byte pieces of codes in
+// different orders, so that 8 threads' loads, and their stores, meet all banks (the loops stay loops,
+// so that their instructions stay near).
 template <int D>
 __device__ __forceinline__ void restore_k(uint32_t part, uint32_t tile, int lgb, int valid,
-                                          int tid) {
-  const int row = tid >> 1, h = tid & 1, r = row & ((1 << lgb) - 1);
+                                          int row) {
+  const int r = row & ((1 << lgb) - 1);
   const uint32_t sub = part + (((row >> lgb) * (9 * D / 16)) << lgb);
-  const uint32_t codes = sub + r * (D / 2) + h * (D / 4);
-  const uint32_t word = ld_shared(sub + ((D / 2) << lgb) + r * (D / 16) + (D == 128 ? 4 * h : 0));
-  const uint32_t abw = row < valid ? word : 0u;        // (0, 0): every code is 0
-  const uint32_t dst = tile + (D == 128 ? h * BOX : 0) + row * 128;
-  const GroupFp16 g(abw);
-  const bool plain = __all_sync(0xFFFFFFFFu, g.plain);
+  const uint32_t codes = sub + r * (D / 2), ab = sub + ((D / 2) << lgb) + r * (D / 16);
 #pragma unroll 1
   for (int it = 0; it < D / 64; ++it) {
-    const int half = D == 128 ? it ^ h : h;            // 8 threads' stores meet all banks
-    const uint4 w = ld_shared_v4(codes + (D == 128 ? 16 * half : 0));
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    const uint32_t to = dst + (((4 * half) ^ (row & 4)) << 4);
+    const int gr = D == 128 ? it ^ (row >> 2 & 1) : 0;
+    const uint32_t word = ld_shared(ab + 4 * gr);
+    const uint32_t abw = row < valid ? word : 0u;      // (0, 0): every code is 0
+    const GroupFp16 g(abw);
+    const bool plain = __all_sync(0xFFFFFFFFu, g.plain);
+    const uint32_t dst = tile + gr * BOX + row * 128;
+#pragma unroll 1
+    for (int jt = 0; jt < 2; ++jt) {
+      const int half = jt ^ (row >> (D == 128 ? 1 : 2) & 1);
+      const uint4 w = ld_shared_v4(codes + gr * 32 + half * 16);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t to = dst + (((4 * half) ^ (row & 4)) << 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 o = plain ? g.restore(ww[i]) : restore8_any(ww[i], abw);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((i ^ (row & 3)) << 4)),
-                   "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w));
+      for (int i = 0; i < 4; ++i) {
+        const uint4 o = plain ? g.restore(ww[i]) : restore8_any(ww[i], abw);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((i ^ (row & 3)) << 4)),
+                     "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w));
+      }
     }
   }
 }
