@@ -417,7 +417,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
 
   if (warp == 0) {
     // ------------------------------------------------------------ codes
-    int np = 0;                                        // parts issued
+    int np = 0, st = 0, turn = 0;                      // parts issued; ring stage, its turn
     bool ok = true;
     const int subs = 128 >> lgb;
     for (int n = 0; ok; ++n) {
@@ -438,10 +438,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         if (at == -1) atomicOr(&g_paged_attn_error, kErrExtent);
         const unsigned live = __ballot_sync(0xFFFFFFFFu, at >= 0);
         for (int which = 0; which < 2; ++which, ++np) {
-          const int st = np % pa.parts;
-          if (np >= pa.parts) {
-            const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((np / pa.parts - 1) & 1),
-                                        abort_flag);
+          if (turn > 0) {
+            const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((turn - 1) & 1), abort_flag);
             if (!__all_sync(0xFFFFFFFFu, fr)) {
               ok = false;
               break;
@@ -465,6 +463,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
               bulk_copy(dst + 128 * (D / 2), src + ((int64_t)(D / 2) << a.cache.lg) + r * (D / 16),
                         128 * (D / 16), bar(B_CFULL + st));
             }
+          }
+          if (++st == pa.parts) {
+            st = 0;
+            ++turn;
           }
         }
       }
@@ -696,7 +698,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
   } else if (warp >= W_RST) {
     // ------------------------------------------------------------ restore
     const int tid = threadIdx.x - W_RST * 32;
-    int np = 0;                                        // parts restored
+    int st = 0, turn = 0, g2 = 0;                      // ring stage, its turn; key tiles restored
     bool ok = true;
     for (int n = 0; ok; ++n) {
       if (!seg_wait(n)) break;
@@ -709,24 +711,29 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
       if (b < 0) break;
       for (; j < j1 && ok; ++j) {
         const int valid = min(128, len - kt.tile(j) * kKeyTile);
-        for (int which = 0; which < 2; ++which, ++np) {
-          const int st = np % pa.parts, g = np >> 1;
-          bool got = bwait(bar(B_CFULL + st), (uint32_t)((np / pa.parts) & 1), abort_flag);
-          if (g >= 2)
-            got = got && bwait(bar((which ? B_VFREE : B_KFREE) + (g & 1)),
-                               (uint32_t)(((g >> 1) - 1) & 1), abort_flag);
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          bool got = bwait(bar(B_CFULL + st), (uint32_t)(turn & 1), abort_flag);
+          if (g2 >= 2)
+            got = got && bwait(bar((which ? B_VFREE : B_KFREE) + (g2 & 1)),
+                               (uint32_t)(((g2 >> 1) - 1) & 1), abort_flag);
           if (!__all_sync(0xFFFFFFFFu, got)) {
             ok = false;
             break;
           }
           const uint32_t part = smem_u32(smem + L::part_off(pa.two) + st * L::PART);
-          const uint32_t tile = smem_u32(smem + (which ? L::V_OFF : L::K_OFF) + (g & 1) * L::TILE);
+          const uint32_t tile = smem_u32(smem + (which ? L::V_OFF : L::K_OFF) + (g2 & 1) * L::TILE);
           restore_part<D>(part, tile, lgb, valid, tid);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(bar(B_CFREE + st));
-            mbar_arrive(bar((which ? B_VFULL : B_KFULL) + (g & 1)));
+            mbar_arrive(bar((which ? B_VFULL : B_KFULL) + (g2 & 1)));
+          }
+          g2 += which;
+          if (++st == pa.parts) {
+            st = 0;
+            ++turn;
           }
         }
       }

@@ -249,7 +249,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------------------ codes
-    int np = 0;
+    int np = 0, st = 0, turn = 0;                      // parts issued; ring stage, its turn
     bool ok = true;
     const int subs = 128 >> lgb;
     for (int n = 0; ok; ++n) {
@@ -268,10 +268,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const int64_t at = e ? slots[1] : slots[0];
         if (at == -1) atomicOr(&g_weights_error, kErrExtent);
         const unsigned live = __ballot_sync(0xFFFFFFFFu, at >= 0);
-        const int st = np % wa.parts;
-        if (np >= wa.parts) {
-          const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((np / wa.parts - 1) & 1),
-                                      abort_flag);
+        if (turn > 0) {
+          const bool fr = bwait(bar(B_CFREE + st), (uint32_t)((turn - 1) & 1), abort_flag);
           if (!__all_sync(0xFFFFFFFFu, fr)) {
             ok = false;
             break;
@@ -295,6 +293,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             bulk_copy(dst + 128 * (D / 2), src + ((int64_t)(D / 2) << a.cache.lg) + r * (D / 16),
                       128 * (D / 16), bar(B_CFULL + st));
           }
+        }
+        if (++st == wa.parts) {
+          st = 0;
+          ++turn;
         }
       }
     }
@@ -470,7 +472,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   } else if (warp >= W_RST) {
     // ------------------------------------------------------------ restore
     const int tid = threadIdx.x - W_RST * 32;
-    int np = 0;
+    int np = 0, st = 0, turn = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
       if (!item_wait(n)) break;
@@ -480,8 +482,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (b < 0) break;
 #pragma unroll 1
       for (int e = 0; e < 2; ++e, ++np) {
-        const int st = np % wa.parts, ks = np % KRING;
-        bool got = bwait(bar(B_CFULL + st), (uint32_t)((np / wa.parts) & 1), abort_flag);
+        const int ks = np % KRING;
+        bool got = bwait(bar(B_CFULL + st), (uint32_t)(turn & 1), abort_flag);
         if (np >= KRING)
           got = got && bwait(bar(B_KFREE + ks), (uint32_t)((np / KRING - 1) & 1), abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {
@@ -495,6 +497,10 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (lane == 0) {
           mbar_arrive(bar(B_CFREE + st));
           mbar_arrive(bar(B_KFULL + ks));
+        }
+        if (++st == wa.parts) {
+          st = 0;
+          ++turn;
         }
       }
     }
