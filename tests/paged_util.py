@@ -38,10 +38,16 @@ class Values:
 def restore_error(big):
     """How far a value of the attention may be from its definition fp16(a + q s), s = (b - a)/15.
 
-    It computes fp16((q - 8) fp16(s) + fp16(a + 8 s)).  With M the larger of |a| and |b| and h = 2^-11
-    half a step: |q - 8| <= 8 and s <= 2 M / 15 make the rounding of s cost h 16 M / 15; a + 8 s lies
-    between a and b: h M; the result: h M (1 + 3 h) at most; the definition's own rounding: h M.  Where
-    the numbers are subnormal, half of 2^-24 each: 8 + 1 + 1 + 1 times 2^-25 < 2^-21."""
+    It computes fp16((q - z) s1 + fp16((q - z) s2 + c)) with z the code whose value a + z s is nearest
+    to 0, c = fp16(a + z s), s1 = fp16(s) and s2 = fp16(s - s1).  With M the larger of |a| and |b| and
+    h = 2^-11 half a step: s <= 2 M / 15, so |(q - z) s| <= 2 M, of which s1 + s2 misses h^2 and the
+    quotient 2^-21: 2 (h^2 + 2^-21) M < h M / 300; c: h M; the inner sum, M (1 + 2 h) at most: h M (1 +
+    2 h); the result: h M (1 + 4 h); the definition's own: h M.  Together less than 4.1 h M.
+
+    Below 2^-14 half a step is 2^-25.  Where s2 is that small, s1 + s2 misses s by 2^-25: 15 times that
+    at most.  Where M is, the sums are of multiples of 2^-24, exact, and with them only the definition's
+    rounding and c's count; c is a or b, exact, where |q - z| = 15: 15 + 1 or 14 + 2 times 2^-25, which
+    is 2^-21."""
     return H16 * 4.1 * big + 2.0 ** -21
 
 
