@@ -1007,6 +1007,11 @@ int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows
   if (noop) return FG_OK;
   if ((q_rows > 0 && (!lse || !aligned4(lse))) || !acc_out || !aligned4(acc_out) || !aligned4(acc))
     return FG_ERR_ARG;
+  const int64_t acc_row = 4 * acc_stride, acc_rows = (int64_t)nseq * kv->H;
+  if (acc && acc != acc_out && acc_stride > 0 &&
+      rows_overlap(RowSet{reinterpret_cast<uint64_t>(acc), acc_rows, acc_row, acc_row},
+                   RowSet{reinterpret_cast<uint64_t>(acc_out), acc_rows, acc_row, acc_row}))
+    return FG_ERR_ARG;
   int sms = 0;
   if ((rc = check_device(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

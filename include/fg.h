@@ -284,7 +284,10 @@ int fg_kv_read_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t tabl
  * i = lens[b] - nq + r, and
  *   out[row][hq*d + j] = sum_t softmax_t(scale * q_row,hq . K^_hk,t) V^_hk,t,j   over the visible t
  * (visible: as stated below for the windowed calls), hk = hq / (Hq / H), Hq a multiple of H, at
- * most 128 times H, K^ and V^ the fp16 restorations of the codes.  A row that sees nothing gets 0.
+ * most 128 times H, nseq * Hq * (table_stride * page / 16 + 2) at most 2^40.  K^ and V^ are the
+ * codes' a + q (b - a)/15: unrounded where single tokens of up to 8 heads per K/V head are
+ * streamed, else fp16, which may be the neighbour of the rounded value.  A row that sees nothing
+ * gets 0.
  * lse (nullable): device fp32 [q_rows][Hq], the logarithm of the row's sum of exp(score), -inf for
  * a row that sees nothing.  q, out: device fp16, q_rows rows q_stride and out_stride elements apart
  * (>= Hq*d, multiples of 8); out may be q with the same stride; any other overlap is refused.
@@ -308,7 +311,8 @@ size_t fg_attn_paged_workspace_bytes(const fg_kvpages* kv, int32_t Hq, int32_t m
  *   acc_out[b][hk][t] = acc[b][hk][t] + sum exp(scale * q_row,hq . K^_hk,t - lse[row][hq])
  * over sequence b's query rows that see t and the query heads of hk, for t < lens[b]; everything
  * else of acc_out stays as it was.  acc (nullable: zeros) and acc_out: device fp32
- * [nseq][H][acc_stride], lens[b] <= acc_stride; acc_out may be acc.  lse: as fg_attn_q4kv_paged
+ * [nseq][H][acc_stride], lens[b] <= acc_stride; acc_out may be acc, and any other overlap of the
+ * two is refused.  K^: the codes restored to fp16.  lse: as fg_attn_q4kv_paged
  * gives it; rows of -inf add nothing.  Sums are taken in one order whatever else runs.  The other
  * arguments as there. */
 int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows,

@@ -153,6 +153,12 @@ def test_paged_attention_validation(fg):
     assert weights(stride=-1) == fg.FG_ERR_SHAPE
     assert weights(lse=None) == fg.FG_ERR_ARG and weights(out=None) == fg.FG_ERR_ARG
     assert weights(acc=FAKE + 1) == fg.FG_ERR_ARG
+    assert weights(acc=OUT + 64) == fg.FG_ERR_ARG            # one sum over another's
+    many = dict(nseq=65535, Hq=256, qs=1 << 15)              # 2^40 tiles of 16 positions and heads
+    assert attend(os_=1 << 15, ts=65472, n=0, **many) == fg.FG_ERR_SHAPE
+    assert attend(os_=1 << 15, ts=16384, n=0, **many) == fg.FG_ERR_WORKSPACE
+    assert weights(ts=65472, lse=None, **many) == fg.FG_ERR_SHAPE
+    assert weights(ts=16384, lse=None, **many) == fg.FG_ERR_ARG
 
 
 def test_evict_validation(fg):
