@@ -12,12 +12,9 @@
 // at the end.  Per key tile of 128 positions:
 //   codes         one bulk copy per page and half (K or V: codes and statistics lie side by side)
 //                 into a ring of parts
-//   restore       four warps write the part as fp16 into the tensor core's 128B-swizzled tiles: a
-//                 nibble under fp16's exponent 2^10, q - 8 exactly, and one fused (q - 8) s + (a +
-//                 8 s) with s = (b - a) / 15 and a + 8 s rounded to fp16: within 3.1 half steps of
-//                 the group's largest magnitude M (8 s <= 1.07 M).  V's channels keep the order in
-//                 which the nibbles lie in a word (0,4,1,5,2,6,3,7), which the output undoes.
-//                 Rows behind the sequence become 0.
+//   restore       eight warps write the part as fp16 into the tensor core's 128B-swizzled tiles (struct
+//                 Group: packed fp16 arithmetic, the definition's value or its neighbour).  Rows behind
+//                 the sequence become 0.
 //   S = Q K^T     tcgen05.mma kind::f16, fp32 in TMEM
 //   softmax       one thread per row, two passes over its 128 columns (the maximum, then P): base-2
 //                 online softmax with a lazily moved reference maximum (by more than 2^8), P =
@@ -27,8 +24,16 @@
 //   warps 1, 2    MMA issuers of chains A and B
 //   warp 3        the share's segments, handed to the others through a ring; Q by TMA
 //   warps 4-11    softmax of A and B (TMEM lanes 32 (w % 4) ..), and their output
-//   warps 12-15   restore
+//   warps 12-19   restore (four warps: 727 us for the long pieces, eight: 616 us)
 // A second kernel puts cut blocks together, piece after piece in order.
+//
+// What bounds it: per key tile of a block of two row tiles, a chain's turn of softmax (3150 cycles) and
+// the wait for its next S (2000: the two products, one behind the other, as P stands where S stood);
+// for a block of one, restoring (2 x 1290 cycles a key tile).  Two documents' pieces of 1501 .. 2048
+// tokens behind 12,001 .. 16,384 positions, 32 heads over 8, window 8192: 616 us, 0.78 PFLOP/s.
+// (S in two halves of 64 keys, so that one is computed while the other is read, costs more turns
+// than it hides: 795 us, and 382 us instead of 259 us where blocks have one row tile.  Restoring in
+// code unrolled for K, V and tails: 755 us.  Moving registers between the warps' roles: no gain.)
 //
 // Masked positions have P = 0, but 0 times an infinity or NaN in V is NaN: rows that end with one
 // are computed again over what they see alone (attend_row).  Rows whose sum of weights is NaN have
@@ -69,6 +74,11 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
 constexpr int THREADS = 20 * 32;
 constexpr int W_MMA = 1, W_SEG = 3, W_SM = 4, W_RST = 12;
 constexpr int RST_WARPS = 8;
+// A block's start and output take as long as this many units: 8 pieces of 100 .. 256 tokens behind
+// 400 .. 2000 positions, 32 heads, 119 us with 0, 95 us with 4, 94 us with 7 (a CTA took 206,000
+// cycles at most, 123,000 on average).  Not in calls of few units per CTA, whose shares would become
+// fewer.
+constexpr int kLead = 4, kLeadFrom = 16;
 constexpr int SEGS = 4;                    // ring of segments
 constexpr int MAX_PARTS = 12;              // ring of parts (K or V codes of a key tile)
 constexpr float kLag = 8.0f;               // base-2 score by which a row may pass its reference
@@ -169,7 +179,7 @@ struct PArgs {
   int min_units;       // of a share
   int slot_rows;       // rows of a partial slot
   PagedCut* cuts;      // [grid]
-  float* partial;      // [2 * grid][slot_rows][D], then maxima and sums [2 * grid][slot_rows][2]
+  float* partial;      // [2 * grid][D/4][slot_rows][4], then maxima and sums [2 * grid][slot_rows][2]
 };
 
 // K stages, V stages, Q_A, (Q_B,) parts; barriers and rings behind them.
@@ -299,7 +309,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedAttn& a = pa.a;
-  const PagedShape shape{pa.tpt, a.window, a.sinks};
+  PagedShape shape{pa.tpt, a.window, a.sinks, 0};
   const int nseq = a.cache.B, H = a.cache.H;
 
   if (threadIdx.x == 0) {
@@ -368,8 +378,16 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
     __syncthreads();
     return round;
   };
-  for (int b0 = 0; b0 < nseq; b0 += THREADS) total += scan_round(b0);
-  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, total / pa.min_units));
+  auto scan = [&]() {
+    total = 0;
+    for (int b0 = 0; b0 < nseq; b0 += THREADS) total += scan_round(b0);
+  };
+  scan();
+  if (total >= (int64_t)kLeadFrom * gridDim.x) {
+    shape.lead = kLead;
+    scan();
+  }
+  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, total / (pa.min_units + shape.lead)));
   const Shares shares(total, n_shares);
   const int share = blockIdx.x;
   const bool busy = total > 0 && share < n_shares;
@@ -627,10 +645,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
           const PagedBlock blk = paged_block(k.s, k.blk, shape);
           got = k.segment(g, blk);
           if (got && first && g.j0 > 0 && shares.share_of(k.at) == share - 1) {
-            const int64_t last = k.at + (int64_t)blk.cost * (blk.kt.count() - 1);
+            const int64_t last = k.at + blk.begin(blk.kt.count() - 1);
             cut = PagedCut{shares.share_of(last) - share + 2, g.q0, g.ntok, g.hk, g.pos};
           }
-          k.at += (int64_t)blk.cost * blk.kt.count();
+          k.at += blk.units();
           if (++k.blk >= paged_blocks(k.s, shape.tpt)) {
             k.blk = 0;
             if (++k.hk == H) {
@@ -936,8 +954,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         const int row = g.q0 + (g.single ? 0 : t * pa.tpt) + tok, hq = g.hk * pa.G + gh;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t* out = a.out + (int64_t)row * a.out_stride + (int64_t)hq * D;
-        const int64_t pr = (int64_t)g.slot * pa.slot_rows + (g.single ? 0 : t * pa.tpt * pa.G) + m;
-        float* part = pa.partial + pr * D;
+        // (4 channels of all rows side by side, so that a warp's store is one run of 512 bytes, and the
+        // merge's loads are: 169 us for a mixed batch, 172 us with a row's channels together)
+        const int in_slot = (g.single ? 0 : t * pa.tpt * pa.G) + m;
+        const int64_t pr = (int64_t)g.slot * pa.slot_rows + in_slot;
+        float* part = pa.partial + (int64_t)g.slot * pa.slot_rows * D + 4 * in_slot;
         if (g.slot < 0) {
           fa *= inv;
           fb *= inv;
@@ -984,7 +1005,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               if (mine)
-                *reinterpret_cast<float4*>(part + 16 * c + e) =
+                *reinterpret_cast<float4*>(part + (int64_t)(16 * c + e) * pa.slot_rows) =
                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
 #pragma unroll
               for (int x = 0; x < 4; ++x) z = fmaf(o[e + x], 0.0f, z);
@@ -1021,7 +1042,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
             if (g.slot < 0)
               a.out[(int64_t)rrow * a.out_stride + (int64_t)rhq * D + ch] = f2h(in_range(o[c] * f));
             else
-              pa.partial[rpr * D + ch] = o[c];
+              pa.partial[(int64_t)g.slot * pa.slot_rows * D + (int64_t)(ch & ~3) * pa.slot_rows +
+                         4 * (in_slot - lane + src) + (ch & 3)] = o[c];
           }
           if (g.slot >= 0 && lane == 0) {
             float* ml = pa.partial + (int64_t)2 * gridDim.x * pa.slot_rows * D + rpr * 2;
@@ -1062,66 +1084,60 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
   }
 }
 
-// Puts cut blocks together: a warp per row, its pieces (m, l, unnormalised O) in order, 32 at a
-// time.
+// Puts cut blocks together: a thread per row and 16 channels, its pieces (m, l, unnormalised O) in
+// order.
 constexpr int kMergeWarps = 8, kMergeSplit = 16;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PArgs pa, int ncta) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int C = D / 32;
   const PagedCut cut = pa.cuts[blockIdx.x];
-  const int lane = threadIdx.x & 31, w = blockIdx.x;
   if (cut.pieces == 0) return;
-  const float* ml = pa.partial + (int64_t)2 * ncta * pa.slot_rows * D;
-  for (int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); r < cut.ntok * pa.G;
-       r += gridDim.y * kMergeWarps) {
-    auto at = [&](int i) { return (int64_t)cut_slot(w, cut.pieces, i) * pa.slot_rows + r; };
-    float M = -INFINITY, L = 0.0f, o[C];
+  const int lane = threadIdx.x & 31, rows = cut.ntok * pa.G;
+  const int64_t slot_floats = (int64_t)pa.slot_rows * D;
+  const float* ml = pa.partial + 2 * ncta * slot_floats;
+  for (int u = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); u < (rows + 31) / 32 * (D / 16);
+       u += gridDim.y * kMergeWarps) {
+    const int r = u / (D / 16) * 32 + lane, ch = u % (D / 16) * 16;
+    if (r >= rows) continue;
+    auto slot = [&](int i) { return (int64_t)cut_slot(blockIdx.x, cut.pieces, i); };
+    auto max_sum = [&](int i) {
+      return *reinterpret_cast<const float2*>(ml + 2 * (slot(i) * pa.slot_rows + r));
+    };
+    float M = -INFINITY, L = 0.0f, o[16];
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = 0.0f;
-    for (int i0 = 0; i0 < cut.pieces; i0 += 32) {
-      const int n = min(32, cut.pieces - i0);
-      float2 x = make_float2(-INFINITY, 0.0f);
-      if (lane < n) x = *reinterpret_cast<const float2*>(ml + 2 * at(i0 + lane));
-      float mx = x.x;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-      mx = fmaxf(mx, M);
-      const float ref = (mx == -INFINITY) ? 0.0f : mx;
-      const float corr = exp2f(M - ref);
-      const float wgt = x.y == 0.0f ? 0.0f : exp2f(x.x - ref);
-      float l = wgt * x.y;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, k);
-      L = fmaf(L, corr, l);
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] *= corr;
+    for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < cut.pieces; ++i) M = fmaxf(M, max_sum(i).x);
+    const float ref = (M == -INFINITY) ? 0.0f : M;
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xFFFFFFFFu, wgt, i);
-        const float* pp = pa.partial + at(i0 + i) * D + lane * C;
-        float v[C];
+    for (int i = 0; i < cut.pieces; ++i) {
+      const float2 x = max_sum(i);
+      const float* p = pa.partial + slot(i) * slot_floats + (int64_t)ch * pa.slot_rows + 4 * r;
+      float4 v[4];
 #pragma unroll
-        for (int c = 0; c < C; c += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(pp + c);
-          v[c] = y.x;
-          v[c + 1] = y.y;
-        }
+      for (int c = 0; c < 4; ++c)
+        v[c] = *reinterpret_cast<const float4*>(p + (int64_t)(4 * c) * pa.slot_rows);
+      const float w = x.y == 0.0f ? 0.0f : exp2f(x.x - ref);
+      if (w == 0.0f) continue;
+      L = fmaf(w, x.y, L);
 #pragma unroll
-        for (int c = 0; c < C; ++c) o[c] = wi == 0.0f ? o[c] : fmaf(wi, v[c], o[c]);
+      for (int c = 0; c < 4; ++c) {
+        o[4 * c] = fmaf(w, v[c].x, o[4 * c]);
+        o[4 * c + 1] = fmaf(w, v[c].y, o[4 * c + 1]);
+        o[4 * c + 2] = fmaf(w, v[c].z, o[4 * c + 2]);
+        o[4 * c + 3] = fmaf(w, v[c].w, o[4 * c + 3]);
       }
-      M = mx;
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int64_t row = cut.q0 + r / pa.G;
     const int hq = cut.hk * pa.G + r % pa.G;
-    uint16_t* op = pa.a.out + row * pa.a.out_stride + (int64_t)hq * D + lane * C;
 #pragma unroll
-    for (int c = 0; c < C; c += 2)
-      *reinterpret_cast<uint32_t*>(op + c) =
-          pack_h2(in_range(o[c] * inv), in_range(o[c + 1] * inv));
-    if (pa.a.lse && lane == 0)
+    for (int c = 0; c < 16; ++c) o[c] *= inv;
+    uint4* op = reinterpret_cast<uint4*>(pa.a.out + row * pa.a.out_stride + (int64_t)hq * D + ch);
+    op[0] = pack_channels(o);
+    op[1] = pack_channels(o + 8);
+    if (pa.a.lse && ch == 0)
       pa.a.lse[row * pa.a.Hq + hq] =
           L == 0.0f ? -INFINITY : (M + log2f(L) - kPExp) * 0.6931471805599453f;
   }
@@ -1177,7 +1193,8 @@ cudaError_t launch_d(const PagedAttn& a, void* ws, int nsm, cudaStream_t st) {
   e = launch_pdl(attend_kernel<D>, dim3(grid), dim3(THREADS), L::bytes(pa.two, pa.parts), st, tq,
                  pa);
   if (e != cudaSuccess) return e;
-  const int split = std::min((pa.slot_rows + kMergeWarps - 1) / kMergeWarps, kMergeSplit);
+  const int units = (pa.slot_rows + 31) / 32 * (D / 16);
+  const int split = std::min((units + kMergeWarps - 1) / kMergeWarps, kMergeSplit);
   return launch_pdl(merge_kernel<D>, dim3(grid, split), dim3(kMergeWarps * 32), 0, st, pa, grid);
 }
 
@@ -1197,7 +1214,7 @@ size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
 
 // Single query rows with few heads go to the streaming kernels: alone where no sequence has more, and
 // ahead of the others where several sequences may be mixed.  (16 contexts of 9000 .. 32760, 8 K/V
-// heads, 4 query heads each: 93 us there, 283 us here.)
+// heads: 84, 93 and 171 us there with 1, 4 and 8 query heads each, 257 us here with any.)
 cudaError_t launch_attn_paged(const PagedAttn& call, int d, void* ws, int nsm, cudaStream_t st) {
   PagedAttn a = call;
   const int G = a.Hq / a.cache.H;

@@ -17,8 +17,10 @@
 //   warps 4-11    a key tile each four: exponentials and sums
 //   warps 12-15   K^ = fp16(a + q (b - a) / 15) exactly as defined (the sums are binary32, and errors of
 //                 K^ would show in them), once per item
-// What bounds it: with few rows, the bytes of K (0.5625 d per position) and restoring them; with many,
-// the exponentials, one per pair, beside 2 d multiply-adds.
+// What bounds it: with few rows, restoring K (25 instructions for every 8 codes) and its bytes (0.5625 d
+// per position); with many, the exponentials, one per pair, beside 2 d multiply-adds.  The last 64
+// tokens of 8 prompts of 8001 .. 16,001 positions, 32 query heads over 8, 196 million pairs: 93 us (126
+// us with 20 warps of 96 registers, whose exponentials took three times the instructions).
 #include <math.h>
 
 #include <algorithm>
@@ -80,8 +82,8 @@ static_assert(Smem<128>::depth() >= 2, "room for codes in flight");
 
 constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_KFULL = 2 * MAX_PARTS, B_KFREE = B_KFULL + KRING,
               B_QFULL = B_KFREE + KRING, B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2,
-              B_SFREE = B_SFULL + 4, B_ZFULL = B_SFREE + 4, B_IFULL = B_ZFULL + 4, B_IFREE = B_IFULL + ITEMS,
-              B_DRAIN = B_IFREE + ITEMS, NBARS = B_DRAIN + 1;
+              B_SFREE = B_SFULL + 4, B_ZFULL = B_SFREE + 4, B_IFULL = B_ZFULL + 4,
+              B_IFREE = B_IFULL + ITEMS, B_DRAIN = B_IFREE + ITEMS, NBARS = B_DRAIN + 1;
 static_assert(NBARS * 8 + 16 <= 512, "control space");
 
 // (a called function: groups with infinities or NaN are rare)
@@ -143,7 +145,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedAttn& a = wa.a;
-  const PagedShape shape{wa.tpt, a.window, a.sinks};
+  const PagedShape shape{wa.tpt, a.window, a.sinks, 0};
   const int nseq = a.cache.B, H = a.cache.H;
 
   if (threadIdx.x == 0) {
@@ -674,7 +676,7 @@ cudaError_t launch_d(const PagedAttn& a, int nsm, cudaStream_t st) {
 
 // Sequences with few query rows go to the streaming kernel, the others here; a call whose rows are
 // known to be few launches that alone.  (One token of 32 sequences of 2000 .. 4096 positions, 8 K/V
-// heads, 4 query heads each: 44 us there, 75 us here.)
+// heads: 36 us there with 1 to 8 query heads each and 50 us with 32, 71 us here with any.)
 cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st) {
   const cudaError_t e = launch_attn_weights_step(a, d, nsm, st);
   if (e != cudaSuccess || (int64_t)a.max_q * (a.Hq / a.cache.H) <= kStepRows) return e;

@@ -2,8 +2,8 @@
 // others, moved in order into pages of their own (sm_103a).
 //
 // Selection, a CTA per (sequence, head), or four that share its positions where such pairs are few and
-// long (they add up their counts through one another's shared memory): the weights' order keys are 32-bit numbers, and three
-// passes over them, histograms of 11, 11 and 10 bits, find the key of the last one that stays and how
+// long (they add up their counts through one another's shared memory): the weights' order keys are
+// 32-bit numbers, and three passes over them, histograms of 11, 11 and 10 bits, find the key of the last one that stays and how
 // many equal ones do.  (11 bits of a weight are its exponent and two bits more, so that the threads
 // of a warp rarely meet in one bin.)  Then every warp counts what stays of its part of the
 // positions, and lists it behind what the warps before it have.  Ties go to the lower position.

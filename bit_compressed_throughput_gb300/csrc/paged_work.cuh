@@ -5,8 +5,9 @@
 // 128 / G whole tokens, a block two row tiles (a sequence's last one, or its only one, may hold one:
 // a single block).  A block works on the 128-position key tiles that one of its tokens sees.  All
 // blocks stand in one order: sequences, K/V heads, blocks, key tiles.  A key tile of a block counts
-// one unit, of a block of two row tiles two; the units are cut evenly into shares, and a share owns
-// the key tiles that begin in it.  So every CTA has the same work whatever the lengths, and a block
+// one unit, of a block of two row tiles two, and the first one `lead` more, for what a block costs
+// beside its tiles; the units are cut evenly into shares, and a share owns the key tiles that begin
+// in it.  So every CTA has the same work whatever the lengths, and a block
 // that a cut divides is put together afterwards from its pieces, one per share.
 #pragma once
 #include <stdint.h>
@@ -19,7 +20,7 @@ struct PagedSeq {
   int q0, nq, n;       // first query row, query rows, cached positions
 };
 struct PagedShape {
-  int tpt, window, sinks;
+  int tpt, window, sinks, lead;
 };
 
 // The key tiles that tokens at positions pos .. pos + ntok - 1 see (pos may be negative).
@@ -43,8 +44,10 @@ FG_HD bool span_sees(int tile, int lo, int hi, int window, int sinks) {
 
 struct PagedBlock {
   int t0, ntok, pos;   // first token of the sequence, tokens, the first one's position
-  int cost;            // units per key tile
+  int cost, lead;      // units per key tile, and the first one's more
   KeyTiles kt;
+  FG_HD int64_t begin(int64_t j) const { return j > 0 ? lead + cost * j : 0; }  // of tile number j
+  FG_HD int64_t units() const { return kt.count() > 0 ? begin(kt.count()) : 0; }
 };
 FG_HD int paged_blocks(const PagedSeq& s, int tpt) {
   return (int)(((int64_t)s.nq + 2 * tpt - 1) / (2 * tpt));
@@ -55,16 +58,14 @@ FG_HD PagedBlock paged_block(const PagedSeq& s, int blk, const PagedShape& sh) {
   b.ntok = s.nq - b.t0 < 2 * sh.tpt ? s.nq - b.t0 : 2 * sh.tpt;
   b.pos = s.n - s.nq + b.t0;
   b.cost = b.ntok > sh.tpt ? 2 : 1;
+  b.lead = sh.lead;
   b.kt = span_tiles(b.pos, b.ntok, sh.window, sh.sinks);
   return b;
 }
 // Units of one K/V head of a sequence.
 FG_HD int64_t head_units(const PagedSeq& s, const PagedShape& sh) {
   int64_t u = 0;
-  for (int i = paged_blocks(s, sh.tpt) - 1; i >= 0; --i) {
-    const PagedBlock b = paged_block(s, i, sh);
-    u += (int64_t)b.cost * b.kt.count();
-  }
+  for (int i = paged_blocks(s, sh.tpt) - 1; i >= 0; --i) u += paged_block(s, i, sh).units();
   return u;
 }
 
@@ -109,13 +110,13 @@ struct PagedWalk {
     at = before + hk * per_head;
     blk = 0;
   }
-  FG_HD static int64_t tiles_before(int64_t x, int64_t at, int cost) {   // that begin before x
-    return x <= at ? 0 : (x - at + cost - 1) / cost;
+  FG_HD static int64_t tiles_before(int64_t x, const PagedBlock& k) {    // that begin before unit x
+    if (x <= 0) return 0;                                                // of the block
+    return x <= k.lead + k.cost ? 1 : (x - k.lead + k.cost - 1) / k.cost;
   }
   // The current block's segment (false: none in this share), without moving on.
   FG_HD bool segment(PagedSeg& g, const PagedBlock& k) const {
-    const int64_t nt = k.kt.count(), j0 = tiles_before(x0, at, k.cost),
-                  j1 = tiles_before(x1, at, k.cost);
+    const int64_t nt = k.kt.count(), j0 = tiles_before(x0 - at, k), j1 = tiles_before(x1 - at, k);
     g.j0 = (int)(j0 < nt ? j0 : nt);
     g.j1 = (int)(j1 < nt ? j1 : nt);
     if (g.j0 >= g.j1) return false;

@@ -16,14 +16,15 @@ using namespace fg;
 // a record per segment, {share, b, hk, q0, ntok, pos, j0, j1, slot, single, tiles, cut pieces, cut
 // q0} and its key tiles behind it.  Returns the records; -1: `room` is too small.
 extern "C" int h_walk(const int32_t* q_off, const int32_t* lens, int nseq, int H, int tpt, int window,
-                      int sinks, int n_shares, int32_t* out, int room) {
-  const PagedShape sh{tpt, window, sinks};
+                      int sinks, int lead, int n_shares, int32_t* out,
+                      int room) {
+  const PagedShape sh{tpt, window, sinks, lead};
   auto seq = [&](int b) { return PagedSeq{q_off[b], q_off[b + 1] - q_off[b], lens[b]}; };
   int64_t total = 0;
   for (int b = 0; b < nseq; ++b) total += H * head_units(seq(b), sh);
   if (total == 0) return 0;
-  // (as many shares as there are pairs of units at most: each then holds the start of a key tile)
-  if (n_shares > total / 2) n_shares = total < 2 ? 1 : (int)(total / 2);
+  // (so few shares that each holds the start of a key tile)
+  if (n_shares > total / (2 + lead)) n_shares = total < 2 + lead ? 1 : (int)(total / (2 + lead));
   const Shares shares(total, n_shares);
   int used = 0, recs = 0;
   for (int w = 0; w < n_shares; ++w) {
@@ -45,7 +46,7 @@ extern "C" int h_walk(const int32_t* q_off, const int32_t* lens, int nseq, int H
       if (k.segment(g, blk)) {
         int32_t cut[2] = {0, 0};
         if (first && g.j0 > 0 && shares.share_of(k.at) == w - 1) {
-          const int64_t last = k.at + (int64_t)blk.cost * (blk.kt.count() - 1);
+          const int64_t last = k.at + blk.begin(blk.kt.count() - 1);
           cut[0] = shares.share_of(last) - w + 2;
           cut[1] = g.q0;
         }
@@ -58,7 +59,7 @@ extern "C" int h_walk(const int32_t* q_off, const int32_t* lens, int nseq, int H
         for (int j = g.j0; j < g.j1; ++j) out[used++] = g.kt.tile(j);
         ++recs;
       }
-      k.at += (int64_t)blk.cost * blk.kt.count();
+      k.at += blk.units();
       if (++k.blk >= paged_blocks(k.s, tpt)) {
         k.blk = 0;
         if (++k.hk == H) {
@@ -80,7 +81,7 @@ extern "C" int h_span_sees(int tile, int lo, int hi, int window, int sinks) {
 }
 extern "C" int h_weight_item(int q0, int nq, int n, int i, int tpt, int window, int sinks,
                              int32_t* out) {
-  const WeightItem w = weight_item(PagedSeq{q0, nq, n}, i, PagedShape{tpt, window, sinks});
+  const WeightItem w = weight_item(PagedSeq{q0, nq, n}, i, PagedShape{tpt, window, sinks, 0});
   out[0] = w.k0;
   out[1] = w.t0;
   out[2] = w.t1;
@@ -98,7 +99,7 @@ def dll(tmp_path_factory):
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(src), "-o",
                     str(so)], check=True)
     dll = C.CDLL(str(so))
-    dll.h_walk.argtypes = [C.c_void_p, C.c_void_p] + [C.c_int] * 6 + [C.c_void_p, C.c_int]
+    dll.h_walk.argtypes = [C.c_void_p, C.c_void_p] + [C.c_int] * 7 + [C.c_void_p, C.c_int]
     dll.h_weight_item.argtypes = [C.c_int] * 7 + [C.c_void_p]
     return dll
 
@@ -123,12 +124,13 @@ CASES = [
 
 @pytest.mark.parametrize("lens,nq,H,tpt,window,sinks", CASES)
 @pytest.mark.parametrize("n_shares", [1, 2, 7, 152])
-def test_every_key_tile_once(dll, lens, nq, H, tpt, window, sinks, n_shares):
+@pytest.mark.parametrize("lead", [0, 4, 7])
+def test_every_key_tile_once(dll, lens, nq, H, tpt, window, sinks, n_shares, lead):
     off = np.concatenate([[3], 3 + np.cumsum(nq)]).astype(np.int32)
     ln = np.asarray(lens, np.int32)
     out = np.zeros(1 << 20, np.int32)
-    recs = dll.h_walk(off.ctypes.data, ln.ctypes.data, len(lens), H, tpt, window, sinks, n_shares,
-                      out.ctypes.data, len(out))
+    recs = dll.h_walk(off.ctypes.data, ln.ctypes.data, len(lens), H, tpt, window, sinks, lead,
+                      n_shares, out.ctypes.data, len(out))
     assert recs >= 0
     at, work, pieces, slots, cuts = 0, {}, {}, set(), {}
     for _ in range(recs):
