@@ -3,7 +3,10 @@
 // kStepHeads query heads per K/V head (attn_paged.cu has the others).
 //
 // With so few rows a key tile's restoring would cost the tensor-core kernel more than its bytes; here
-// the codes go into the products as they are, and the bytes are what counts.
+// the codes go into the products as they are, and the bytes are what counts.  The page table comes 32
+// entries at a time, a lane each, and a slot's four copies are issued by a lane each.  16 contexts of
+// 9000 .. 32,760, 8 K/V heads of 128 channels, 4 query heads each, 384 MB: 93 us, 4.1 TB/s; 84 us with
+// one query head each.
 #include "attn_decode_window.cuh"
 #include "paged.cuh"
 

@@ -176,6 +176,8 @@ __device__ __forceinline__ uint4 turn_pairs(uint4 x, const float2* cs) {
 
 // d/16 lanes per row, 16 channels each: 8 of either half of the pairs, or 8 neighbouring pairs;
 // channels behind the first `rot` are copied.  A lane's angles serve all heads that its CTA walks.
+// Bound by HBM, 4 bytes an element: 16 prompts of 300 .. 512 tokens, 64 heads of 128 channels, 214 MB:
+// 39 us, 5.5 TB/s (0.82 of the copy rate); 64 tokens: the launch, 3 us.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads)
 rope_kernel(const RaggedArgs a, const Turn turn, float sign, const uint16_t* x, uint16_t* y,
@@ -372,7 +374,9 @@ __device__ __forceinline__ uint2 quantize16(const uint4 v0, const uint4 v1, int 
 }
 
 // 4 lanes per group of 64, 16 values each: 16 * 256 / D rows per CTA.  ROPE: K is turned first (1:
-// pairs in halves, 2: neighbouring pairs), as rope_kernel does.
+// pairs in halves, 2: neighbouring pairs), as rope_kernel does.  Pairs in halves lie in other lanes,
+// whose chunks come in a second load (from L1): 48 us for 16 prompts of 300 .. 512 tokens, 32 heads,
+// 136 MB, where neighbouring pairs take 38 us and K as it is 30 us.
 template <int D, typename Cache, int ROPE>
 __global__ void __launch_bounds__(kThreads, ROPE == 0 ? 4 : 2)
 append_kernel(const RaggedArgs a, const uint16_t* __restrict__ k_new,
@@ -558,7 +562,7 @@ cudaError_t launch_kv_append_paged(const uint16_t* k_new, const uint16_t* v_new,
     else
       kernel = d == 128 ? append_kernel<128, Pages, 1> : append_kernel<64, Pages, 1>;
   }
-  // (a CTA's angles serve all of its heads)
+  // (a CTA's angles serve all of its heads: 85 us with read-back at 16 CTAs per SM, 74 us at 4)
   return launch_per_sm(rope ? kTurnCtasPerSm : kCtasPerSm, kernel, row_off, pos, rows, row_stride,
                        pc.B, pc.H, d, nsm, st, k_new, v_new, Pages{pc}, turn);
 }

@@ -216,3 +216,25 @@ def test_pool_past_32_bits(fg):
         fg.fg_check_device_error()
         got.append([host(x) for x in res + [kept, acc_out, n, back]])
     all_equal(*got)
+
+
+def test_sequences_that_share_pages(fg):
+    """A common beginning in the same pages: each sequence gets what it gets with pages of its own."""
+    d, H, G, P = 64, 2, 2, 32
+    lens, nq = [200, 170, 129], [40, 1, 3]
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 41, G)
+    t, Hq = dev(q)[:, :H * G * d], H * G
+    blocks = pool.blocks.view(pool.pages, -1)
+    for b in (1, 2):                                         # copies of sequence 0's first 128
+        blocks[table[b, :4].tolist()] = blocks[table[0, :4].tolist()]
+    shared = table.copy()
+    shared[1:, :4] = table[0, :4]
+    got = []
+    for tab in (table, shared):
+        out, z = run_attend(fg, t, q_off, Hq, pool, tab, lens, 0.125, max_q=max(nq))
+        acc = torch.zeros((3, H, 200), device="cuda")
+        fg.fg_attn_weights_q4_paged(t, i32(q_off), Hq, pool, dev(tab), i32(lens), 0.125, z, acc, acc,
+                                    max_q=max(nq))
+        fg.fg_check_device_error()
+        got.append([host(out), host(z), host(acc)])
+    all_equal(*got)
