@@ -116,6 +116,64 @@ def window_case(op, B, Hq, H, d, lens, window, reps):
     fg.fg_check_device_error()
 
 
+def paged_case(op, Hq, H, d, page, lens, new, reps, window=0, keep=0):
+    """Rotary positions, append, attention, received weights or eviction over pages: sequences of the
+    given lengths, with their newest `new` positions as query (and appended) rows."""
+    import torch
+    from bit_compressed_throughput_gb300 import fg
+    g = torch.Generator(device="cuda")
+    g.manual_seed(19)
+    B, G = len(lens), Hq // H
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    offs = lambda x: i32([0] + [sum(x[:i + 1]) for i in range(B)])
+    need = [(n + page - 1) // page for n in lens]
+    kept_pages = (keep + page - 1) // page
+    order = torch.randperm(sum(need) + B * kept_pages, generator=g, device="cuda").int()
+    table = torch.zeros((B, max(need)), dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    pages = fg.KVPagesQ4(sum(need) + B * kept_pages, page, H * d, H)
+    x = torch.randn((sum(lens), 2 * H * d), generator=g, device="cuda").half()
+    fg.fg_kv_append_q4_paged(x[:, :H * d], x[:, H * d:], offs(lens), i32([0] * B), pages, table)
+    angles = torch.empty((max(lens), d // 2, 2), device="cuda")
+    fg.fg_rope_table(angles, 1e4)
+    rows, pos = sum(new), i32([n - m for n, m in zip(lens, new)])
+    q = torch.randn((rows, Hq * d), generator=g, device="cuda").half()
+    out, lse = torch.empty_like(q), torch.empty((rows, Hq), device="cuda")
+    acc = torch.rand((B, H, max(lens)), generator=g, device="cuda")
+    ws = torch.empty(fg.fg_attn_paged_workspace_bytes(pages, Hq, max(new)), dtype=torch.uint8,
+                     device="cuda")
+    args = (q, offs(new), Hq, pages, table, i32(lens), 1.0 / math.sqrt(d))
+    attend = lambda: fg.fg_attn_q4kv_paged(*args, out, ws, max_q=max(new), window=window, lse=lse)
+    if op == "rope":
+        call = lambda: fg.fg_rope(q, d, offs(new), pos, angles, out)
+    elif op == "append":
+        call = lambda: fg.fg_kv_append_q4_paged(x[:rows, :H * d], x[:rows, H * d:], offs(new), pos,
+                                                pages, table, angles=angles)
+    elif op == "attend":
+        call = attend
+    elif op == "weights":
+        attend()
+        call = lambda: fg.fg_attn_weights_q4_paged(*args, lse, acc, acc, max_q=max(new),
+                                                   window=window)
+    else:
+        dst = order[at:].view(B, kept_pages)
+        kept = torch.empty((B, H, keep), dtype=torch.int32, device="cuda")
+        acc_out, left = torch.empty((B, H, keep), device="cuda"), i32([0] * B)
+        call = lambda: fg.fg_kv_evict_q4_paged(pages, table, i32(lens), acc, 256, dst, kept, acc_out,
+                                               left)
+    for _ in range(1 + reps):
+        call()
+    fg.fg_check_device_error()
+
+
+def between(lo, hi, n):
+    """n lengths spread evenly over lo .. hi."""
+    return [lo + (hi - lo) * i // max(1, n - 1) for i in range(n)]
+
+
 def layer_prefill_case(h, H, f, g, s, reps):
     """One decoder layer's prefill over one GPU batch (g sequences of s tokens): the layer
     restores its weights to fp16 once, then runs LN, the four projections (the CTA-pair GEMM
@@ -182,6 +240,22 @@ CASES = {
     # windowed prefill attention: long documents with grouped heads, and prompts
     "prefill-window-long": lambda r: window_case("prefill", 2, 32, 8, 128, (7001, 8191), 1024, r),
     "prefill-window-prompts": lambda r: window_case("prefill", 16, 32, 32, 128, (300, 512), 0, r),
+    "rope-prompts": lambda r: paged_case("rope", 64, 8, 128, 16, between(300, 512, 16),
+                                         between(300, 512, 16), r),
+    "append-paged": lambda r: paged_case("append", 32, 32, 128, 64, between(300, 512, 16),
+                                         between(300, 512, 16), r),
+    "attend-paged-step": lambda r: paged_case("attend", 32, 8, 128, 16, between(9000, 32760, 16),
+                                              [1] * 16, r),
+    "attend-paged-pieces": lambda r: paged_case("attend", 32, 32, 128, 32, between(400, 2000, 8),
+                                                between(100, 256, 8), r),
+    "attend-paged-long": lambda r: paged_case("attend", 32, 8, 128, 64, [12001, 16384], [1501, 2048],
+                                              r, window=8192),
+    "attn-weights-step": lambda r: paged_case("weights", 32, 8, 128, 16, between(2000, 4096, 32),
+                                              [1] * 32, r),
+    "attn-weights-recent": lambda r: paged_case("weights", 32, 8, 128, 64, between(8001, 16001, 8),
+                                                [64] * 8, r),
+    "evict-long": lambda r: paged_case("evict", 8, 8, 128, 64, between(20001, 32001, 4), [1] * 4, r,
+                                       keep=8192),
     # top-K on the full KV workload (launch lists only: 4.3 GB of cache)
     "decode-attn-topk-kv": lambda r: attn_case(512, 56, 128, 1056, r, topk=106),
 }
