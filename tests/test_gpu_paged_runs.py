@@ -177,6 +177,18 @@ def test_many_sequences(fg, nq):
     assert np.all(np.abs(got - G * np.asarray(rows)) <= 0.1 * G * np.asarray(rows))
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (300, 5)])
+def test_many_blocks(fg, window, sinks):
+    """So many key tiles that every multiprocessor has several blocks, whole ones and cut ones."""
+    d, H, G, P = 64, 32, 1, 64
+    lens, nq = [1300, 900, 1177, 640, 1290, 1, 1024, 799], [200, 300, 129, 128, 257, 1, 64, 255]
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 61, G)
+    out, z = run_attend(fg, dev(q)[:, :H * G * d], q_off, H * G, pool, table, lens, 0.125,
+                        max_q=max(nq), window=window, sinks=sinks)
+    fg.fg_check_device_error()
+    check_attend(out, z, q, q_off, H * G, k, v, table, lens, 0.125, window, sinks)
+
+
 def test_pool_past_32_bits(fg):
     """Pages whose offsets pass 2^32 bytes hold what pages at the start hold, bit for bit."""
     d, H, G, P, lens, nq = 128, 2, 2, 64, [200, 333], [70, 1]
