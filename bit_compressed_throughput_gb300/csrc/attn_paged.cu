@@ -387,7 +387,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
     shape.lead = kLead;
     scan();
   }
-  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, total / (pa.min_units + shape.lead)));
+  const int64_t most = total / (pa.min_units + shape.lead);      // so that each begins a key tile
+  const int n_shares = (int)min((int64_t)gridDim.x, max((int64_t)1, most));
   const Shares shares(total, n_shares);
   const int share = blockIdx.x;
   const bool busy = total > 0 && share < n_shares;

@@ -15,10 +15,10 @@
 //   warp 2        Q row tiles by TMA, a ring of two (two or fewer stay while the K/V head does)
 //   warp 3        items
 //   warps 4-11    a key tile each four: exponentials and sums
-//   warps 12-15   K^ = fp16(a + q (b - a) / 15) exactly as defined (the sums are binary32, and errors of
-//                 K^ would show in them), once per item
-// What bounds it: with few rows, restoring K (25 instructions for every 8 codes) and its bytes (0.5625 d
-// per position); with many, the exponentials beside it, one per pair.  The last 64 tokens of 8 prompts
+//   warps 12-15   K^ = fp16(a + q (b - a) / 15) exactly as defined (the sums are binary32, and
+//                 errors of K^ would show in them), once per item
+// What bounds it: with few rows, restoring K (25 instructions for every 8 codes) and its bytes (0.5625
+// d per position); with many, the exponentials beside it, one per pair.  The last 64 tokens of 8 prompts
 // of 8001 .. 16,001 positions, 32 query heads over 8, 196 million pairs: 93 us (126 us with 20 warps of
 // 96 registers, whose exponentials took three times the instructions); the restoring warps work 98,000
 // of 156,000 cycles, those of the exponentials 87,000.

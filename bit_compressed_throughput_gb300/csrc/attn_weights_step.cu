@@ -2,8 +2,8 @@
 // rows (at most kStepRows rows of a K/V head's query heads): a stream over the K codes and statistics
 // (sm_103a).  attn_weights_paged.cu has the sequences with more.
 //
-// The sums are those of that file: acc + sum exp(scale q . k^ - lse), with K^ = fp16(a + q (b - a) / 15)
-// exactly as defined, so they are restored before the products, in registers: mma.sync m16n8k16 with
+// The sums are those of that file: acc + sum exp(scale q . k^ - lse), with K^ = fp16(a + q (b - a) /
+// 15) exactly as defined, so they are restored before the products, in registers: mma.sync m16n8k16 with
 // 16 positions in its rows and 8 query rows in its columns.  A lane (gid, tig) holds 32 (d = 64: 16)
 // channels of positions gid and gid + 8, as the codes lie; the products' index order follows, and
 // Q's fragments are laid out for it in shared memory once per (sequence, K/V head).

@@ -3,15 +3,16 @@
 //
 // Selection, a CTA per (sequence, head), or four that share its positions where such pairs are few and
 // long (they add up their counts through one another's shared memory): the weights' order keys are
-// 32-bit numbers, and three passes over them, histograms of 11, 11 and 10 bits, find the key of the last one that stays and how
-// many equal ones do.  (11 bits of a weight are its exponent and two bits more, so that the threads
-// of a warp rarely meet in one bin.)  Then every warp counts what stays of its part of the
-// positions, and lists it behind what the warps before it have.  Ties go to the lower position.
+// 32-bit numbers, and three passes over them, histograms of 11, 11 and 10 bits, find the key of the
+// last one that stays and how many equal ones do.  (11 bits of a weight are its exponent and two bits
+// more, so that the threads of a warp rarely meet in one bin.)  Then every warp counts what stays of
+// its part of the positions, and lists it behind what the warps before it have.  Ties go to the lower
+// position.
 // Moving: a position's K and V codes and statistics, copied as they are, 16 bytes a thread.
 // Bound by HBM: the weights once, 2 * 1.125 d bytes per kept position; by latency where a call has few
 // (sequence, head) pairs.  16 sequences of 2000 .. 4096 positions cut to 1024, 8 heads, 38 MB of
-// positions read and written: 16 us; 4 of 20,001 .. 32,001 cut to 8192, 75 MB: 43 us.  (The weights held in
-// shared memory between the passes: 58 us against 52 at that stage.)
+// positions read and written: 16 us; 4 of 20,001 .. 32,001 cut to 8192, 75 MB: 43 us.  (The weights
+// held in shared memory between the passes: 58 us against 52 at that stage.)
 #include <algorithm>
 
 #include "attn_q4.cuh"

@@ -231,8 +231,8 @@ def check_attend(got, z, q, q_off, Hq, k, v, table, lens, scale, window=0, sinks
     """Every row within what the arithmetic allows of the oracle's.
 
     Scores: d + 40 binary32 operations on terms of size |q_j k_j|, and each k within restore_error; an
-    error ds moves a weight by a factor within e^(+-2 ds).  Values: within restore_error.  Weights are rounded to fp16 (half a step; half of 2^-24 where they are
-    subnormal, at most 2^-31 of the row's largest after their scaling), the exponential adds 2^-21,
+    error ds moves a weight by a factor within e^(+-2 ds).  Values: within restore_error.  Weights are
+    rounded to fp16 (half a step; half of 2^-24 where they are subnormal, at most 2^-31 of the row's largest after their scaling), the exponential adds 2^-21,
     the sums n + 64 binary32 operations; last, the output's own half step."""
     got, z = host(got).astype(np.float64), None if z is None else host(z)
     H, d = k.shape[1], k.shape[3]
