@@ -24,13 +24,13 @@
 //   warps 1, 2    MMA issuers of chains A and B
 //   warp 3        the share's segments, handed to the others through a ring; Q by TMA
 //   warps 4-11    softmax of A and B (TMEM lanes 32 (w % 4) ..), and their output
-//   warps 12-19   restore (four warps: 727 us for the long pieces, eight: 616 us)
+//   warps 12-19   restore (four warps: 727 us for the long pieces, eight: 646 us)
 // A second kernel puts cut blocks together, piece after piece in order.
 //
 // What bounds it: per key tile of a block of two row tiles, a chain's turn of softmax (3150 cycles) and
 // the wait for its next S (2000: the two products, one behind the other, as P stands where S stood);
 // for a block of one, restoring (2 x 1290 cycles a key tile).  Two documents' pieces of 1501 .. 2048
-// tokens behind 12,001 .. 16,384 positions, 32 heads over 8, window 8192: 616 us, 0.78 PFLOP/s.
+// tokens behind 12,001 .. 16,384 positions, 32 heads over 8, window 8192: 619 us, 0.77 PFLOP/s.
 // (S in two halves of 64 keys, so that one is computed while the other is read, costs more turns
 // than it hides: 795 us, and 382 us instead of 259 us where blocks have one row tile.  Restoring in
 // code unrolled for K, V and tails: 755 us.  Moving registers between the warps' roles: no gain.)
