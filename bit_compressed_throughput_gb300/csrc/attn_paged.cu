@@ -24,7 +24,7 @@
 //   warps 1, 2    MMA issuers of chains A and B
 //   warp 3        the share's segments, handed to the others through a ring; Q by TMA
 //   warps 4-11    softmax of A and B (TMEM lanes 32 (w % 4) ..), and their output
-//   warps 12-19   restore (four warps: 727 us for the long pieces, eight: 646 us)
+//   warps 12-19   restore
 // A second kernel puts cut blocks together, piece after piece in order.
 //
 // What bounds it: per key tile of a block of two row tiles, a chain's turn of softmax (3150 cycles) and
