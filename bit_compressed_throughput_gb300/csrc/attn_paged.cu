@@ -319,7 +319,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_QFULL + i), 1);
-      mbar_init(bar(B_QFREE + i), 2);      // two arrivals of the issuers' per use of a buffer
+      mbar_init(bar(B_QFREE + i), 2);      // two arrivals of the issuers' (q_given_*)
       mbar_init(bar(B_KFULL + i), RST_WARPS);
       mbar_init(bar(B_KFREE + i), 2);
       mbar_init(bar(B_VFULL + i), RST_WARPS);
@@ -529,6 +529,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         ++q_uses[1];
       }
       if (!ok) break;
+      if (q_given_at_once(t, g.single)) arrive(B_QFREE);
+      const int q_given = q_given_after_use(t, g.single);
       auto own = [&](int j) { return takes_part(g, t, j, pa.tpt, a.window, a.sinks); };
       auto next_own = [&](int j) {
         while (j < g.j1 && !own(j)) ++j;
@@ -583,7 +585,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         const int jn = next_own(j + 1);
         if (jn >= g.j1) {                              // the chain's last S product of the segment
           commit(B_QFREE + qb);
-          if (!g.single) commit(B_QFREE + qb);
+          if (q_given == 2) commit(B_QFREE + qb);
         }
         wait_to(v_seen, j, B_VFULL, B_VFREE);
         // the first product of a segment overwrites O_t: its last values have been read
@@ -608,7 +610,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
         ++uses;
       } else {                                         // no part in any key tile
         arrive(B_QFREE + qb);
-        if (!g.single) arrive(B_QFREE + qb);
+        if (q_given == 2) arrive(B_QFREE + qb);
       }
       wait_to(v_seen, g.j1, B_VFULL, B_VFREE);
       g0 += g.j1 - g.j0;
