@@ -1121,8 +1121,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const PArgs pa,
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         v[c] = *reinterpret_cast<const float4*>(p + (int64_t)(4 * c) * pa.slot_rows);
-      const float w = x.y == 0.0f ? 0.0f : exp2f(x.x - ref);
-      if (w == 0.0f) continue;
+      const float w = exp2f(x.x - ref);    // 0 * NaN where a piece is NaN: as in a block that is not cut
       L = fmaf(w, x.y, L);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {

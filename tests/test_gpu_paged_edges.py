@@ -45,3 +45,32 @@ def test_blocks_of_two_row_tiles_before_blocks_of_one(fg, G):
     # (rows computed on their own take their sums in another order)
     assert np.all(np.abs(a - c) <= 4 * H16 * np.abs(c) + 2.0 ** -10 * np.abs(c).max())
     assert not np.isfinite(out[sees]).all(axis=1).any()
+
+
+@pytest.mark.parametrize("n,nq,bad", [(897, 3, 896), (900, 3, 898), (897, 1, 896), (900, 1, 898)])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("G", [1, 9])
+def test_pieces_of_cut_blocks_keep_their_nan(fg, n, nq, bad, which, G):
+    """A long row's key tiles go to many multiprocessors.  A NaN in K that is all that a row sees of the
+    last tile, or that stands among keys whose weights are 0 beside the others', makes the row and its
+    log-sum-exp NaN; one in V makes the row NaN.  Rows before it do not show it."""
+    d, P = 64, 16
+    table, pool, k, v, q_off, q = paged_case(fg, d, 1, P, [n], [nq], 5, G)
+    t = torch.ones((len(q), G * d), dtype=torch.float16, device="cuda")
+    for p in range(896, n):                                  # scores 800 below 0
+        pool.parts()[1][table[0, p // P], 0, p % P] = -100.0
+    args = (t, q_off, G, pool, table, [n], 0.125)
+    clean, zc = run_attend(fg, *args, max_q=nq)
+    pool.parts()[1 + 2 * which][table[0, bad // P], 0, bad % P] = float("nan")
+    out, z = run_attend(fg, *args, max_q=nq)
+    fg.fg_check_device_error()
+    first = q_off[1] - (n - bad)                             # the first row that sees it
+    out, z, clean, zc = (host(x)[q_off[0]:q_off[1]] for x in (out, z, clean, zc))
+    first = max(0, first - q_off[0])
+    assert np.isfinite(clean).all() and np.isfinite(zc).all()
+    assert np.isnan(out[first:]).all()
+    assert np.isnan(z[first:]).all() if which == 0 else np.array_equal(z[first:], zc[first:])
+    # (rows computed on their own take their sums in another order)
+    a, c = out[:first].astype(np.float64), clean[:first].astype(np.float64)
+    assert np.all(np.abs(a - c) <= 4 * H16 * np.abs(c) + 2.0 ** -10 * np.abs(c).max(initial=0))
+    assert np.isfinite(z[:first]).all()
