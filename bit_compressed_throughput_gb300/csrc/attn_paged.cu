@@ -12,9 +12,8 @@
 // at the end.  Per key tile of 128 positions:
 //   codes         one bulk copy per page and half (K or V: codes and statistics lie side by side)
 //                 into a ring of parts
-//   restore       eight warps write the part as fp16 into the tensor core's 128B-swizzled tiles (struct
-//                 Group: packed fp16 arithmetic, the definition's value or its neighbour).  Rows behind
-//                 the sequence become 0.
+//   restore       eight warps write the part as fp16 into the tensor core's 128B-swizzled tiles,
+//                 fp16(a + q (b - a) / 15) exactly as defined.  Rows behind the sequence become 0.
 //   S = Q K^T     tcgen05.mma kind::f16, fp32 in TMEM
 //   softmax       one thread per row, two passes over its 128 columns (the maximum, then P): base-2
 //                 online softmax with a lazily moved reference maximum (by more than 2^8), P =
@@ -27,10 +26,10 @@
 //   warps 12-19   restore
 // A second kernel puts cut blocks together, piece after piece in order.
 //
-// What bounds it: per key tile of a block of two row tiles, a chain's turn of softmax (3150 cycles) and
-// the wait for its next S (2000: the two products, one behind the other, as P stands where S stood);
-// for a block of one, restoring (2 x 1290 cycles a key tile).  Two documents' pieces of 1501 .. 2048
-// tokens behind 12,001 .. 16,384 positions, 32 heads over 8, window 8192: 619 us, 0.77 PFLOP/s.
+// What bounds it: per key tile of a block of two row tiles, a chain's turn of softmax (3430 cycles) and
+// the wait for its next S (1930: the two products, one behind the other, as P stands where S stood);
+// for a block of one, restoring (2 x 1370 cycles a key tile).  Two documents' pieces of 1501 .. 2048
+// tokens behind 12,001 .. 16,384 positions, 32 heads over 8, window 8192: 647 us, 0.74 PFLOP/s.
 // (S in two halves of 64 keys, so that one is computed while the other is read, costs more turns
 // than it hides: 795 us, and 382 us instead of 259 us where blocks have one row tile.  Restoring in
 // code unrolled for K, V and tails: 755 us.  Moving registers between the warps' roles: no gain.)
@@ -75,9 +74,9 @@ constexpr int THREADS = 20 * 32;
 constexpr int W_MMA = 1, W_SEG = 3, W_SM = 4, W_RST = 12;
 constexpr int RST_WARPS = 8;
 // A block's start and output take as long as this many units: 8 pieces of 100 .. 256 tokens behind
-// 400 .. 2000 positions, 32 heads, 119 us with 0, 95 us with 4, 94 us with 7 (a CTA took 206,000
-// cycles at most, 123,000 on average).  Not in calls of few units per CTA, whose shares would become
-// fewer.
+// 400 .. 2000 positions, 32 heads, 119 us with 0, 95 us with 4, 94 us with 7 when a CTA took 206,000
+// cycles at most, 123,000 on average; now 99 us with 4.  Not in calls of few units per CTA, whose
+// shares would become fewer.
 constexpr int kLead = 4, kLeadFrom = 16;
 constexpr int SEGS = 4;                    // ring of segments
 constexpr int MAX_PARTS = 12;              // ring of parts (K or V codes of a key tile)
@@ -221,44 +220,18 @@ __device__ __forceinline__ bool takes_part(const PagedSeg& g, int t, int j, int 
   return span_sees(g.kt.tile(j), lo, lo + tile_tokens(g, t, tpt) - 1, window, sinks);
 }
 
-// Codes of a group (a, b) restored in fp16 arithmetic, two per instruction.  With z the code whose
-// value a + z s is nearest to 0, x = fp16((q - z) s1 + fp16((q - z) s2 + c)): s = s1 + s2 in two
-// fp16 numbers and c = fp16(a + z s), so that all but the last rounding are of numbers a tenth of the
-// group's largest.  It is the definition's fp16(a + q s) or, for one value in 20, its neighbour
-// (relative error 1.0e-4; with one fp16 number for s and codes counted from the middle 3.3e-4, which
-// the scores bring to 8.5e-4 in the outputs).  Restoring in binary32 takes twice the instructions
-// that pack and unpack.
-struct Group {
-  uint32_t s1, s2, c, z;                   // z: (-1024 - z, -64 - z)
-  __device__ __forceinline__ explicit Group(uint32_t abw) {
-    const float2 ab = unpack_h2(abw);
-    const float s = (ab.y - ab.x) * (1.0f / 15.0f);
-    // (s = 0 and infinities: any z will do)
-    const float zf = rintf(fminf(fmaxf(__fdividef(-ab.x, s), 0.0f), 15.0f)), cf = fmaf(zf, s, ab.x);
-    s1 = pack_h2(s, s);
-    const float rest = s - unpack_h2(s1).x;
-    s2 = pack_h2(rest, rest);
-    c = pack_h2(cf, cf);
-    z = pack_h2(-1024.0f - zf, -64.0f - zf);
-  }
-  __device__ __forceinline__ uint4 restore(uint32_t w) const {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // a byte's two nibbles under fp16's exponent of 1024: (1024 + q0, 1024 + 16 q1)
-      const uint32_t u = (__byte_perm(w, 0, 0x1111 * i) & 0x00F0000Fu) | 0x64006400u;
-      const uint32_t t = hfma2_u32(u, 0x2C003C00u, z);
-      o[i] = hfma2_u32(t, s1, hfma2_u32(t, s2, c));
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-  }
-};
+// (a called function: groups with infinities or NaN are rare)
+__device__ __noinline__ uint4 restore8_any(uint32_t codes, uint32_t abw) {
+  return restore8_fp16(codes, abw);
+}
 
 // A part from a ring stage into an fp16 tile: two threads per position, 64 channels each (d = 64:
-// 32).  The upper 64 channels' threads take their words in another order, so that the 16-byte
-// stores of 8 threads meet all banks.  Positions `valid` .. are not the sequence's: 0.  (The loop
-// stays a loop: with everything unrolled, in code of their own for K, V and tails, the warps waited
-// for instructions, and a part took 2770 cycles instead of 1740.)
+// 32), in binary32, two values per instruction.  (In fp16 arithmetic, with s = (b - a) / 15 as a sum of
+// two fp16 numbers, 614 us instead of 647 for the long pieces above, but neighbours of the defined
+// values, and up to 5 steps off where s is near fp16's smallest numbers.)
+// The upper 64 channels' threads take their words in another order, so that the 16-byte stores of 8
+// threads meet all banks.  Positions `valid` .. are not the sequence's: 0.  (The loop stays a loop, for
+// K, V and tails alike, so that its instructions stay near.)
 template <int D>
 __device__ __forceinline__ void restore_part(uint32_t part, uint32_t tile, int lgb, int valid,
                                              int tid) {
@@ -266,7 +239,9 @@ __device__ __forceinline__ void restore_part(uint32_t part, uint32_t tile, int l
   const uint32_t sub = part + (((row >> lgb) * (9 * D / 16)) << lgb);
   const uint32_t codes = sub + r * (D / 2) + h * (D / 4);
   const uint32_t abw = ld_shared(sub + ((D / 2) << lgb) + r * (D / 16) + (D == 128 ? 4 * h : 0));
-  const Group g(row < valid ? abw : 0u);   // (0, 0): every code is 0
+  const uint32_t stats = row < valid ? abw : 0u;       // (0, 0): every code is 0
+  const GroupFp16 g(stats);
+  const bool plain = __all_sync(0xFFFFFFFFu, g.plain);
   const uint32_t dst = tile + (D == 128 ? h * BOX : 0) + row * 128;
 #pragma unroll 1
   for (int it = 0; it < D / 64; ++it) {
@@ -276,7 +251,7 @@ __device__ __forceinline__ void restore_part(uint32_t part, uint32_t tile, int l
     const uint32_t to = dst + (((4 * half) ^ (row & 4)) << 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 o = g.restore(ww[i]);
+      const uint4 o = plain ? g.restore(ww[i]) : restore8_any(ww[i], stats);
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((i ^ (row & 3)) << 4)),
                    "r"(o.x), "r"(o.y), "r"(o.z), "r"(o.w));
     }
@@ -1216,7 +1191,7 @@ size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
 
 // Single query rows with few heads go to the streaming kernels: alone where no sequence has more, and
 // ahead of the others where several sequences may be mixed.  (16 contexts of 9000 .. 32760, 8 K/V
-// heads: 84, 93 and 171 us there with 1, 4 and 8 query heads each, 257 us here with any.)
+// heads: 84, 93 and 171 us there with 1, 4 and 8 query heads each, 292 us here with any.)
 cudaError_t launch_attn_paged(const PagedAttn& call, int d, void* ws, int nsm, cudaStream_t st) {
   PagedAttn a = call;
   const int G = a.Hq / a.cache.H;

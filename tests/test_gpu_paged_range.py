@@ -1,0 +1,91 @@
+"""Attention over pages over the range of what the 4-bit format holds: K^ and V^ of pieces are the
+format's values bit for bit, and small and large groups lose nothing that the arithmetic does not say."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fg_synth
+from oracle import paged as OP
+from paged_util import F32, H16, rows_of
+from parity_util import dev, host, lib
+from test_gpu_paged import paged_case, run_attend
+
+pytestmark = pytest.mark.gpu
+
+SCALES = [1e-6, 1e-5, 1e-4, 1e-2, 1.0, 4000.0]
+
+
+@pytest.fixture(scope="module")
+def fg():
+    return lib()
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("d,G,P", [(64, 1, 16), (128, 4, 64), (64, 9, 256)])
+def test_pieces_take_the_formats_values(fg, scale, d, G, P):
+    """A window of one position: a row's output is that position's V^, its weight 1 (2^7 before the sum,
+    2^7, divides it), and with a query of one channel its log-sum-exp is that of K^."""
+    n, H = 300, 2
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, [n], [n], 3 + d, G, scale=scale)
+    q[:] = 0
+    ch = (np.arange(n)[:, None] * 7 + np.arange(H * G)[None]) % d
+    rows = np.arange(n)[:, None]
+    q[q_off[0] + rows, np.arange(H * G) * d + ch] = 1.0
+    a = 1.0 / scale
+    out, z = run_attend(fg, dev(q)[:, :H * G * d], q_off, H * G, pool, table, [n], a, window=1)
+    fg.fg_check_device_error()
+    live = slice(q_off[0], q_off[1])
+    got, z = host(out)[live].reshape(n, H, G, d), host(z)[live].astype(np.float64)
+    assert np.array_equal(got, np.broadcast_to(
+        np.moveaxis(rows_of(v, table, 0, n), 0, 1)[:, :, None], got.shape))
+    kk = rows_of(k, table, 0, n).astype(np.float64)                    # [H][n][d]
+    want = a * kk[np.arange(H * G) // G, rows, ch]
+    # seven binary32 roundings (the scale, twice, the score, its shifts by 7 and back, log2, ln 2) of
+    # numbers of |want| / ln 2 + 7 at most, half a step each, log2 one; times 2
+    assert np.all(np.abs(z - want) <= 16 * 2.0 ** -24 * (np.abs(want) * 1.5 + 7))
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("d,H,G,P,lens,nq,window,sinks", [
+    (128, 2, 1, 16, [300], [200], 0, 0),
+    (64, 1, 4, 64, [900], [33], 0, 0),
+    (128, 1, 12, 32, [700], [9], 300, 5),
+    (128, 2, 1, 16, [300, 5, 1111], [1, 1, 1], 0, 0),
+    (64, 1, 2, 32, [2000], [1], 500, 4),
+    (128, 2, 4, 64, [130, 900], [1, 1], 0, 0),
+    (64, 1, 7, 16, [700, 77], [1, 1], 0, 0),
+])
+def test_attention_over_the_range_of_values(fg, scale, d, H, G, P, lens, nq, window, sinks):
+    """As check_attend's bound, without an error of K^ and V^ in pieces.  Single tokens take them
+    unrounded: half a step of fp16 (2^-25 where it is subnormal) from the rounded ones, and with more
+    than two heads the remainder of a weight's rounding counts at the codes' middle: 7.5 (b - a)/15 is
+    at most the larger of |a| and |b|."""
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 5 + d + G, G, scale=scale)
+    a = 1.0 / (math.sqrt(d) * scale)
+    single = max(nq) == 1 and G <= 8
+    out, z = run_attend(fg, dev(q)[:, :H * G * d], q_off, H * G, pool, table, lens, a, max_q=max(nq),
+                        window=window, sinks=sinks)
+    fg.fg_check_device_error()
+    got, z = host(out).astype(np.float64), host(z)
+    for b, n in enumerate(lens):
+        r = slice(q_off[b], q_off[b + 1])
+        ok = OP.seen(n - nq[b], nq[b], n, window, sinks)
+        for hk in range(H):
+            kk, vv = (rows_of(x, table, b, n)[hk].astype(np.float64) for x in (k, v))
+            qq = q[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d)
+            o, lse, p = OP.attend(qq, kk, vv, ok, a)
+            aq = np.abs(qq.astype(np.float64))
+            dk, dv = (H16 * np.abs(x) + 2.0 ** -25 if single else np.zeros_like(x) for x in (kk, vv))
+            if single and G > 2:
+                dv = dv + H16 * rows_of(v.big, table, b, n)[hk]
+            moved = np.einsum("rgd,td->rgt", aq, np.abs(kk) * (d + 40) * F32 + dk) * a
+            ds = np.where(ok[:, None], moved, 0).max(-1)
+            V = p @ np.abs(vv)
+            tol = ((np.expm1(2 * ds)[..., None] + H16 + 2.0 ** -21 + (n + 64) * F32) * V + p @ dv
+                   + n * 2.0 ** -31 * np.abs(vv).max(0) + H16 * np.abs(o) + 2.0 ** -25)
+            err = np.abs(got[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d) - o)
+            assert np.all(err <= tol), (b, hk, float((err / tol).max()))
+            zt = 2 * ds + 2.0 ** -20 + (n + 64) * F32 + np.abs(lse) * 4 * F32
+            assert np.all(np.abs(z[r, hk * G:(hk + 1) * G] - lse) <= zt), (b, hk)
