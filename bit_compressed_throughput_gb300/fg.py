@@ -235,7 +235,8 @@ class KVPagesQ4:
     """One layer's 4-bit KV cache in pages of ``page`` positions (a power of two, 16 .. 1024):
     ``blocks`` uint8 [pages][H][page*9*d/8], per page and head K codes [page][d/2], K statistics
     [page][d/64] (int32), V codes, V statistics.  Which pages a sequence has is the caller's
-    affair: calls take a page table, int32 [nseq][n] on the device."""
+    affair: calls take a page table, int32 [nseq][n] on the device.  ``blocks`` may be replaced (a
+    grown or moved pool); the other attributes follow from it and ``d``."""
 
     def __init__(self, pages: int, page: int, h: int, H: int, device="cuda"):
         self._set(torch.zeros((pages, H, page * 9 * (h // H) // 8), dtype=torch.uint8,
@@ -255,12 +256,20 @@ class KVPagesQ4:
                 not blocks.is_contiguous() or blocks.shape[2] % (9 * d // 8):
             raise ValueError(f"blocks: contiguous uint8 [pages][H][page*9*d/8] expected, got "
                              f"{blocks.dtype} {tuple(blocks.shape)} for d = {d}")
-        self.blocks, self.d = blocks, d
-        self.pages, self.H = blocks.shape[0], blocks.shape[1]
-        self.page, self.h = blocks.shape[2] * 8 // (9 * d), self.H * d
-        if self.page < 16 or self.page > 1024 or self.page & (self.page - 1):
-            raise ValueError(f"pages of {self.page} positions: a power of two, 16 .. 1024, expected")
-        self._struct = fg_kvpages(_ptr(blocks), self.pages, self.page, self.h, self.H)
+        (pages, H), page = blocks.shape[:2], blocks.shape[2] * 8 // (9 * d)
+        if page < 16 or page > 1024 or page & (page - 1):
+            raise ValueError(f"pages of {page} positions: a power of two, 16 .. 1024, expected")
+        self.__dict__.update(blocks=blocks, d=d, pages=pages, H=H, page=page, h=H * d,
+                             _ptr=_ptr(blocks), _numel=blocks.numel(),
+                             _struct=fg_kvpages(_ptr(blocks), pages, page, H * d, H))
+
+    def __setattr__(self, name, value):
+        if name in ("d", "H", "h", "page", "pages"):
+            raise AttributeError(f"{name} follows from the blocks: set those")
+        if name == "blocks":
+            self._set(value, self.d)
+        else:
+            object.__setattr__(self, name, value)
 
     def parts(self):
         """Views of the blocks: K codes [pages][H][page][d/2] and statistics [..][page][d/64] (fp16
@@ -274,6 +283,9 @@ class KVPagesQ4:
         return out
 
     def struct(self) -> fg_kvpages:
+        t = self.blocks
+        if t.data_ptr() != self._ptr or t.numel() != self._numel:    # resized in place
+            self._set(t, self.d)
         return self._struct
 
 
