@@ -35,8 +35,10 @@ constexpr int kBins = 2048;
 
 constexpr int kShare = 4;                  // CTAs of a pair of its own
 
-__device__ __forceinline__ uint32_t key_of(const float* acc, int i) {
-  return q4attn::order_key_f32(acc[i]);
+// Keys of equal weights are equal: -0 takes +0's, and every NaN the largest.
+__device__ __forceinline__ uint32_t key_of(float w) {
+  const uint32_t k = q4attn::order_key_f32(w);
+  return isnan(w) ? 0xFFFFFFFFu : (k == 0x7FFFFFFFu ? 0x80000000u : k);
 }
 // A word of the shared memory of CTA `rank` of the cluster.
 __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Evict a) {
       __syncthreads();
 #pragma unroll 8
       for (int i = n0 + threadIdx.x; i < min(n1, old); i += kThreads) {
-        const uint32_t k = key_of(acc, i);
+        const uint32_t k = key_of(acc[i]);
         if (pass == 0 || (k >> above) == prefix) atomicAdd(&hist[k >> shift & mask], 1);
       }
       together();
@@ -140,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Evict a) {
 #pragma unroll 4
   for (int base = i0; base < i1; base += 32) {         // the same turns for every lane
     const int i = base + lane;
-    const uint32_t k = i < old && i < i1 && !none ? key_of(acc, i) : 0u;
+    const uint32_t k = i < old && i < i1 && !none ? key_of(acc[i]) : 0u;
     const bool sure = i < i1 && (i >= old || (!none && k > prefix));
     const bool same = i < i1 && i < old && !none && k == prefix;
     cnt.x += __popc(__ballot_sync(0xFFFFFFFFu, sure));
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Evict a) {
   for (int base = i0; base < i1; base += 32) {         // the same turns for every lane
     const int i = base + lane;
     const float w = i < i1 ? acc[i] : 0.0f;
-    const uint32_t k = q4attn::order_key_f32(w);
+    const uint32_t k = key_of(w);
     const bool sure = i < i1 && (i >= old || (!none && k > prefix));
     const bool same = i < i1 && i < old && !none && k == prefix;
     const unsigned eq = __ballot_sync(0xFFFFFFFFu, same), below = (1u << lane) - 1u;

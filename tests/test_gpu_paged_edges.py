@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from paged_util import H16
+from oracle import paged as OP
+from paged_util import H16, fill, i32, need, tables
 from parity_util import dev, host, lib
 from test_gpu_paged import check_attend, paged_case, run_attend
 
@@ -74,3 +75,41 @@ def test_pieces_of_cut_blocks_keep_their_nan(fg, n, nq, bad, which, G):
     a, c = out[:first].astype(np.float64), clean[:first].astype(np.float64)
     assert np.all(np.abs(a - c) <= 4 * H16 * np.abs(c) + 2.0 ** -10 * np.abs(c).max(initial=0))
     assert np.isfinite(z[:first]).all()
+
+
+@pytest.mark.parametrize("H,lens,keep,recent", [(2, [2, 40, 200], 20, 4), (2, [2], 1, 0),
+                                                (1, [6000], 900, 33), (3, [64, 5000, 17], 30, 0)])
+@pytest.mark.parametrize("kind", ["zeros", "nan"])
+def test_eviction_order_of_zeros_and_nan(fg, H, lens, keep, recent, kind):
+    """Zeros of both signs are equal, NaN of either sign and any payload lie above +inf and are equal:
+    among equal ones the lower positions stay.  The weights are handed on as they are."""
+    d, P = 64, 16
+    both = need(lens, P) + [(keep + P - 1) // P] * len(lens)
+    all_tables, pages = tables(both, seed=keep)
+    src = np.ascontiguousarray(all_tables[:len(lens)])
+    dst = np.ascontiguousarray(all_tables[len(lens):, :both[-1]])
+    pool, _, _ = fill(fg, pages, P, H, d, 4)
+    rng = np.random.default_rng(keep + H)
+    pick = {"zeros": [0x80000000, 0, 0x80000001, 0x00000001, 0xBF800000],
+            "nan": [0x7FC00000, 0xFFC00000, 0xFFFFFFFF, 0x7F800001, 0x7F800000, 0xFF800000, 0x3F800000,
+                    0x7F7FFFFF]}[kind]
+    bits = rng.choice(np.array(pick, np.uint32), (len(lens), H, max(lens) + 3))
+    if kind == "nan":                                        # few NaN, so that the last to stay varies
+        bits[rng.random(bits.shape) < 0.9] = 0x3F000000
+    bits[0, :, :2] = [0x80000000, 0] if kind == "zeros" else [0x7F800000, 0xFFC00000]
+    acc = bits.view(np.float32)
+    kept = torch.full((len(lens), H, keep), 99, dtype=torch.int32, device="cuda")
+    acc_out = torch.full((len(lens), H, keep), 7.0, device="cuda")
+    dst_lens = torch.full((len(lens),), 99, dtype=torch.int32, device="cuda")
+    fg.fg_kv_evict_q4_paged(pool, dev(src), i32(lens), dev(bits.view(np.int32)).view(torch.float32),
+                            recent, dev(dst), kept, acc_out, dst_lens)
+    fg.fg_check_device_error()
+    with np.errstate(invalid="ignore"):
+        wide = acc.astype(np.float64)
+    order = np.where(np.isnan(acc), np.inf, np.where(np.isposinf(acc), 1e300, wide))
+    got = host(acc_out.view(torch.int32)).view(np.uint32)
+    for b, n in enumerate(lens):
+        for h in range(H):
+            at = OP.evict(order[b, h], n, keep, recent)
+            assert np.array_equal(host(kept)[b, h, :len(at)], at), (b, h)
+            assert np.array_equal(got[b, h, :len(at)], bits[b, h, at]), (b, h)
