@@ -796,6 +796,10 @@ static int check_rope(const fg_rope_rows* r, int d) {
     return FG_ERR_ARG;
   return FG_OK;
 }
+// An array of so many bytes, for rows_overlap.
+static RowSet array_at(const void* p, int64_t bytes) {
+  return RowSet{reinterpret_cast<uint64_t>(p), p && bytes > 0 ? 1 : 0, bytes, bytes};
+}
 static RopeRows rope_rows(const fg_rope_rows& r) {
   return RopeRows{r.angles, r.pos, r.positions, r.rot, r.interleaved != 0};
 }
@@ -961,9 +965,13 @@ int fg_attn_q4kv_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows, cons
   if (out_stride < width || out_stride % 8 != 0) return FG_ERR_SHAPE;
   if (noop || q_rows == 0 || max_q == 0) return FG_OK;
   if (!out || !aligned16(out) || !aligned4(lse)) return FG_ERR_ARG;
+  const RowSet q_at = fp16_rows(q, q_rows, q_stride, width);
+  const RowSet out_at = fp16_rows(out, q_rows, out_stride, width);
+  const RowSet lse_at = array_at(lse, 4ll * q_rows * Hq);
   if (!(out == q && (q_stride == out_stride || q_rows == 1)) &&      // in place
-      rows_overlap(fp16_rows(q, q_rows, q_stride, width), fp16_rows(out, q_rows, out_stride, width)))
+      rows_overlap(q_at, out_at))
     return FG_ERR_ARG;
+  if (rows_overlap(lse_at, q_at) || rows_overlap(lse_at, out_at)) return FG_ERR_ARG;
   const size_t need = fg_attn_paged_workspace_bytes(kv, Hq, max_q);
   if (ws_bytes < need || (need > 0 && (!ws || !aligned16(ws)))) return FG_ERR_WORKSPACE;
   int sms = 0;
@@ -1007,10 +1015,11 @@ int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows
   if (noop) return FG_OK;
   if ((q_rows > 0 && (!lse || !aligned4(lse))) || !acc_out || !aligned4(acc_out) || !aligned4(acc))
     return FG_ERR_ARG;
-  const int64_t acc_row = 4 * acc_stride, acc_rows = (int64_t)nseq * kv->H;
-  if (acc && acc != acc_out && acc_stride > 0 &&
-      rows_overlap(RowSet{reinterpret_cast<uint64_t>(acc), acc_rows, acc_row, acc_row},
-                   RowSet{reinterpret_cast<uint64_t>(acc_out), acc_rows, acc_row, acc_row}))
+  const int64_t acc_bytes = 4 * acc_stride * nseq * kv->H;
+  const RowSet acc_at = array_at(acc_out, acc_bytes);
+  if ((acc != acc_out && rows_overlap(acc_at, array_at(acc, acc_bytes))) ||
+      rows_overlap(acc_at, array_at(lse, 4ll * q_rows * Hq)) ||
+      rows_overlap(acc_at, fp16_rows(q, q_rows, q_stride, (int64_t)Hq * (kv->h / kv->H))))
     return FG_ERR_ARG;
   int sms = 0;
   if ((rc = check_device(&sms))) return rc;
@@ -1052,13 +1061,19 @@ int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t tab
   if (nseq == 0) return FG_OK;
   if (!pages_ok(kv, table) || !dst_table || !aligned4(dst_table) || !lens || !aligned4(lens) ||
       !acc || !aligned4(acc) || !kept || !aligned4(kept) || !acc_out || !aligned4(acc_out) ||
-      !dst_lens || !aligned4(dst_lens) || dst_lens == lens || dst_table == table)
+      !dst_lens || !aligned4(dst_lens) || dst_table == table)
     return FG_ERR_ARG;
-  const RowSet out{reinterpret_cast<uint64_t>(acc_out), (int64_t)nseq * kv->H, 4ll * keep,
-                   4ll * keep};
-  if (acc_stride > 0 &&
-      rows_overlap(out, RowSet{reinterpret_cast<uint64_t>(acc), (int64_t)nseq * kv->H,
-                               4 * acc_stride, 4 * acc_stride}))
+  const int64_t heads = (int64_t)nseq * kv->H;
+  const RowSet outs[] = {array_at(kept, 4 * heads * keep), array_at(acc_out, 4 * heads * keep),
+                         array_at(dst_lens, 4ll * nseq)};
+  const RowSet ins[] = {array_at(acc, 4 * heads * acc_stride), array_at(lens, 4ll * nseq),
+                        array_at(table, 4 * table_stride * nseq),
+                        array_at(dst_table, 4 * dst_stride * nseq)};
+  for (const RowSet& o : outs)
+    for (const RowSet& i : ins)
+      if (rows_overlap(o, i)) return FG_ERR_ARG;
+  if (rows_overlap(outs[0], outs[1]) || rows_overlap(outs[0], outs[2]) ||
+      rows_overlap(outs[1], outs[2]))
     return FG_ERR_ARG;
   int sms = 0;
   if ((rc = check_device(&sms))) return rc;

@@ -290,7 +290,8 @@ int fg_kv_read_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t tabl
  * A row that sees nothing gets 0.
  * lse (nullable): device fp32 [q_rows][Hq], the logarithm of the row's sum of exp(score), -inf for
  * a row that sees nothing.  q, out: device fp16, q_rows rows q_stride and out_stride elements apart
- * (>= Hq*d, multiples of 8); out may be q with the same stride; any other overlap is refused.
+ * (>= Hq*d, multiples of 8); out may be q with the same stride; any other overlap of q, out and lse
+ * is refused.
  * q_off: device int32 [nseq+1], not decreasing, within 0 .. q_rows; lens: device int32 [nseq], at
  * most what a row of the table names; checked on the device (the rows of a sequence that does not
  * fit stay as they were; those of one with a bad page hold nothing of use;
@@ -311,8 +312,8 @@ size_t fg_attn_paged_workspace_bytes(const fg_kvpages* kv, int32_t Hq, int32_t m
  *   acc_out[b][hk][t] = acc[b][hk][t] + sum exp(scale * q_row,hq . K^_hk,t - lse[row][hq])
  * over sequence b's query rows that see t and the query heads of hk, for t < lens[b]; everything
  * else of acc_out stays as it was.  acc (nullable: zeros) and acc_out: device fp32
- * [nseq][H][acc_stride], lens[b] <= acc_stride; acc_out may be acc, and any other overlap of the
- * two is refused.  K^: the codes restored to fp16.  lse: as fg_attn_q4kv_paged
+ * [nseq][H][acc_stride], lens[b] <= acc_stride; acc_out may be acc, and any other overlap of it with
+ * acc, lse or q is refused.  K^: the codes restored to fp16.  lse: as fg_attn_q4kv_paged
  * gives it; rows of -inf add nothing.  Sums are taken in one order whatever else runs.  The other
  * arguments as there. */
 int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows,
@@ -331,7 +332,8 @@ int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows
  * [nseq][H][keep], their acc, 0 behind them; dst_lens: device int32 [nseq], min(lens[b], keep).
  * Heads keep different positions: a cached position no longer says when its token came, so later
  * rows give fg_kv_append_q4_paged a rope->pos of their own.  keep <= dst_stride * page
- * (FG_ERR_CAPACITY).  acc as in fg_attn_weights_q4_paged. */
+ * (FG_ERR_CAPACITY).  acc as in fg_attn_weights_q4_paged.  kept, acc_out and dst_lens may overlap
+ * neither one another nor acc, lens and the tables. */
 int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
                          int32_t nseq, const int32_t* lens, const float* acc, int64_t acc_stride,
                          int32_t keep, int32_t recent, const int32_t* dst_table,
