@@ -19,9 +19,10 @@
 //                 errors of K^ would show in them), once per item
 // What bounds it: with few rows, restoring K (25 instructions for every 8 codes) and its bytes (0.5625
 // d per position); with many, the exponentials beside it, one per pair.  The last 64 tokens of 8 prompts
-// of 8001 .. 16,001 positions, 32 query heads over 8, 196 million pairs: 93 us (126 us with 20 warps of
-// 96 registers, whose exponentials took three times the instructions); the restoring warps work 98,000
-// of 156,000 cycles, those of the exponentials 87,000.
+// of 8001 .. 16,001 positions, 32 query heads over 8, 196 million pairs: 95 us (126 us with 20 warps of
+// 96 registers, whose exponentials took three times the instructions; 3 us are the test for rows of
+// log-sum-exp -inf with infinities or NaN in their scores); the restoring warps work 98,000 of 160,000
+// cycles.
 #include <math.h>
 
 #include <algorithm>
@@ -86,6 +87,13 @@ constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_KFULL = 2 * MAX_PARTS, B_KFREE
               B_SFREE = B_SFULL + 4, B_ZFULL = B_SFREE + 4, B_IFULL = B_ZFULL + 4,
               B_IFREE = B_IFULL + ITEMS, B_DRAIN = B_IFREE + ITEMS, NBARS = B_DRAIN + 1;
 static_assert(NBARS * 8 + 16 <= 512, "control space");
+
+// Columns of a row tile that a position adds up: all; those that see it; of those, the ones whose row has
+// a log-sum-exp.
+enum { kAll, kSome, kHeard };
+template <int N>
+using Columns = std::integral_constant<int, N>;
+constexpr float kSilent = -0x1.fffffep127f;
 
 // (a called function: groups with infinities or NaN are rare)
 __device__ __noinline__ uint4 restore8_any(uint32_t codes, uint32_t abw) {
@@ -553,8 +561,8 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       for (int r = it.r0; r < it.r1; ++r, ++cnt) {
         const int s = cnt & 1;
         // (the buffer's last readers have arrived at the other buffer's barrier since)
-        // (-lse / ln 2; a row that sees nothing has -inf, and adds 0)
-        lse[128 * s + m] = z == -INFINITY ? z : z * -1.4426950408889634f;
+        // (-lse / ln 2; for a row of -inf, which adds nothing, a number that leaves 0 of finite scores)
+        lse[128 * s + m] = z == -INFINITY ? kSilent : z * -1.4426950408889634f;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_ZFULL + 2 * e + s));
         z = fetch(it, r + 1);                          // in flight meanwhile
@@ -574,14 +582,20 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc_fence_after();
         const uint32_t srow = lane_addr + 128 * (2 * e + s);
         const float* zr = lse + 128 * s;
-        auto chunk = [&](const float (&v)[32], int c, auto masked) {
+        auto chunk = [&](const float (&v)[32], int c, auto columns) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             const float4 z4 = *reinterpret_cast<const float4*>(zr + 32 * c + i);
             const float2 x = f2unpack(ffma2(f2pack(v[i], v[i + 1]), sl2x2, f2pack(z4.x, z4.y)));
             const float2 y = f2unpack(ffma2(f2pack(v[i + 2], v[i + 3]), sl2x2, f2pack(z4.z, z4.w)));
             float p[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
-            if (decltype(masked)::value) {
+            if (decltype(columns)::value == kHeard) {
+              p[0] = z4.x != kSilent ? p[0] : 0.0f;
+              p[1] = z4.y != kSilent ? p[1] : 0.0f;
+              p[2] = z4.z != kSilent ? p[2] : 0.0f;
+              p[3] = z4.w != kSilent ? p[3] : 0.0f;
+            }
+            if (decltype(columns)::value != kAll) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int col = 32 * c + i + k;
@@ -593,26 +607,37 @@ weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
         };
         float va[32], vb[32];
+        const uint64_t before[2] = {sum2[0], sum2[1]};
+        auto some = [&](auto columns) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            if (!__any_sync(0xFFFFFFFFu, c0 < 32 * c + 32 && c1 > 32 * c && c1 > c0)) continue;
+            tmem_ld32(srow + 32 * c, va);
+            tmem_wait_ld_dep(va);
+            chunk(va, c, columns);
+          }
+        };
         if (__all_sync(0xFFFFFFFFu, c0 == 0 && c1 == 128)) {
           tmem_ld32(srow, va);
           tmem_wait_ld_dep(va);
 #pragma unroll 1
           for (int c = 0; c < 4; c += 2) {             // the next load in flight
             tmem_ld32(srow + 32 * c + 32, vb);
-            chunk(va, c, std::false_type{});
+            chunk(va, c, Columns<kAll>{});
             tmem_wait_ld_dep(vb);
             if (c == 0) tmem_ld32(srow + 64, va);
-            chunk(vb, c + 1, std::false_type{});
+            chunk(vb, c + 1, Columns<kAll>{});
             tmem_wait_ld_dep(va);
           }
         } else {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            if (!__any_sync(0xFFFFFFFFu, c0 < 32 * c + 32 && c1 > 32 * c && c1 > c0)) continue;
-            tmem_ld32(srow + 32 * c, va);
-            tmem_wait_ld_dep(va);
-            chunk(va, c, std::true_type{});
-          }
+          some(Columns<kSome>{});
+        }
+        // an infinity or NaN in Q or K: again, without what rows of -inf made of it
+        const float2 now = f2unpack(fadd2(sum2[0], sum2[1]));
+        if (__any_sync(0xFFFFFFFFu, !(now.x + now.y < INFINITY))) {
+          sum2[0] = before[0];
+          sum2[1] = before[1];
+          some(Columns<kHeard>{});
         }
         tc_fence_before();
         __syncwarp();

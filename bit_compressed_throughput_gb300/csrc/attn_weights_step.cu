@@ -64,7 +64,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(const SArgs sa) {
   constexpr int NW = D / 32;               // code words of a position in a lane
   __shared__ uint4 qf[kSets * NW * 32];    // [set][word][lane]: 8 channels of query row 8 set + gid
-  // -lse / ln 2 of the query rows; -inf: no row, or one that sees nothing
+  // -lse / ln 2 of the query rows; +inf: no row, or one that adds nothing
   __shared__ __align__(8) float zs[kStepRows];
   // two blocks of the warps' 32 positions: codes, then statistics
   constexpr int CODES = 16 * (D / 2), STATS = 16 * (D / 16);      // bytes of 16 positions
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(cons
         const int row = threadIdx.x;
         float z = -INFINITY;
         if (row < rows) z = a.lse_in[(int64_t)(s.q0 + row / G) * a.Hq + hk * G + row % G];
-        zs[row] = z == -INFINITY ? z : z * -1.4426950408889634f;
+        zs[row] = z * -1.4426950408889634f;
       }
       __syncthreads();
     }
@@ -283,8 +283,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(cons
             for (int r = 0; r < 2; ++r) {
               const float y0 = ex2(fmaf(c[2 * r], sa.scale_log2, z.x));
               const float y1 = ex2(fmaf(c[2 * r + 1], sa.scale_log2, z.y));
-              sum[r] += (8 * set + 2 * tig < rows ? y0 : 0.0f) +
-                      (8 * set + 2 * tig + 1 < rows ? y1 : 0.0f);
+              sum[r] += (z.x != INFINITY ? y0 : 0.0f) + (z.y != INFINITY ? y1 : 0.0f);
             }
           } else {
 #pragma unroll
@@ -292,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weights_step_kernel(cons
               const int row = 8 * set + 2 * tig + e, pos = pos0 + row / G;
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                if (row < rows && visible(tp + 8 * r, pos, a.window, a.sinks))
+                if ((e ? z.y : z.x) != INFINITY && visible(tp + 8 * r, pos, a.window, a.sinks))
                   sum[r] += ex2(fmaf(c[2 * r + e], sa.scale_log2, e ? z.y : z.x));
             }
           }

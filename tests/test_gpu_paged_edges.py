@@ -113,3 +113,38 @@ def test_eviction_order_of_zeros_and_nan(fg, H, lens, keep, recent, kind):
             at = OP.evict(order[b, h], n, keep, recent)
             assert np.array_equal(host(kept)[b, h, :len(at)], at), (b, h)
             assert np.array_equal(got[b, h, :len(at)], bits[b, h, at]), (b, h)
+
+
+@pytest.mark.parametrize("d,H,G,lens,nq", [
+    (64, 2, 1, [700, 300], [128, 200]),                      # whole row tiles that all see the first keys
+    (128, 1, 4, [600, 257], [64, 33]),
+    (64, 1, 7, [500], [40]),                                 # 126 rows a tile
+    (128, 2, 2, [700, 40], [8, 1]),                          # few rows: streamed
+    (64, 1, 32, [513], [1]),
+])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 60000.0])
+def test_rows_without_a_log_sum_exp_add_nothing(fg, d, H, G, lens, nq, bad):
+    """A row whose log-sum-exp is -inf hands out no weight, whatever its query is; one whose is +inf hands
+    out 0 to every finite score."""
+    P, Hq, scale = 32, H * G, 1.0 / math.sqrt(d)
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 31 + d, G)
+    t = dev(q)[:, :Hq * d].contiguous()
+    _, z = run_attend(fg, t, q_off, Hq, pool, table, lens, scale, max_q=max(nq))
+    rng = np.random.default_rng(3)
+    silent = torch.from_numpy(rng.random(tuple(z.shape)) < 0.2).cuda()
+    silent[q_off[0]] = True
+    silent[q_off[0], 0] = False
+
+    def weights(rows, lse):
+        acc = torch.zeros((len(lens), H, max(lens)), device="cuda")
+        fg.fg_attn_weights_q4_paged(rows.reshape(t.shape), i32(q_off), Hq, pool, dev(table), i32(lens),
+                                    scale, lse, None, acc, max_q=max(nq))
+        fg.fg_check_device_error()
+        return host(acc)
+
+    heads = t.view(len(q), Hq, d)
+    none = z.masked_fill(silent, -float("inf"))
+    want = weights(heads.masked_fill(silent[..., None], 0.0), none)
+    assert np.isfinite(want).all() and want.any()
+    assert np.array_equal(weights(heads.masked_fill(silent[..., None], bad), none), want)
+    assert np.array_equal(weights(heads, z.masked_fill(silent, float("inf"))), want)
