@@ -624,7 +624,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ P
           got = k.segment(g, blk);
           if (got && first && g.j0 > 0 && shares.share_of(k.at) == share - 1) {
             const int64_t last = k.at + blk.begin(blk.kt.count() - 1);
-            cut = PagedCut{shares.share_of(last) - share + 2, g.q0, g.ntok, g.hk, g.pos};
+            cut = PagedCut{shares.share_of(last) - share + 2, g.q0, g.ntok, g.hk};
           }
           k.at += blk.units();
           if (++k.blk >= paged_blocks(k.s, shape.tpt)) {

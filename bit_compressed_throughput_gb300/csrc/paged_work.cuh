@@ -83,7 +83,7 @@ struct PagedSeg {
 // before holds (at its end) the block's first key tile.
 struct PagedCut {
   int pieces;          // 0: nothing
-  int q0, ntok, hk, pos;
+  int q0, ntok, hk;
 };
 // Partial slots: 2 share + 1 for a segment whose block goes on in the next share, 2 share for one
 // that ends a block.  Piece i of a cut at share w:
