@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged as OP
-from paged_util import H16, fill, i32, need, tables
+from paged_util import F32, H16, fill, i32, need, rows_of, tables
 from parity_util import dev, host, lib
 from test_gpu_paged import check_attend, paged_case, run_attend
 
@@ -148,3 +148,42 @@ def test_rows_without_a_log_sum_exp_add_nothing(fg, d, H, G, lens, nq, bad):
     assert np.isfinite(want).all() and want.any()
     assert np.array_equal(weights(heads.masked_fill(silent[..., None], bad), none), want)
     assert np.array_equal(weights(heads, z.masked_fill(silent, float("inf"))), want)
+
+
+@pytest.mark.parametrize("d,H,G,lens,nq,window,sinks", [
+    (64, 1, 2, [700, 300, 5], [128, 40, 5], 0, 0),           # pieces, and many rows
+    (128, 2, 4, [600, 257], [3, 8], 0, 0),                   # pieces, and few rows
+    (128, 1, 7, [500, 90], [40, 20], 64, 3),
+    (64, 2, 1, [900, 1, 77, 0], [1, 1, 1, 0], 0, 0),         # single tokens
+    (128, 1, 8, [2000, 300], [1, 1], 500, 4),
+    (64, 1, 12, [300, 40], [1, 1], 0, 0),                    # single tokens of many heads
+])
+def test_every_row_hands_out_a_weight_of_one(fg, d, H, G, lens, nq, window, sinks):
+    """The received weights with the log-sum-exp that the attention gave: each row and head hands out 1.
+    Either call's scores miss theirs by d + 40 binary32 operations on sum |q_j k_j| at most; the
+    log-sum-exp and the exponential as in check_attend and test_weights.  Streamed single tokens take K^
+    unrounded, half a step of fp16 from the value that the weights take."""
+    P, Hq, scale = 32, H * G, 1.0 / math.sqrt(d)
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 83 + d, G)
+    t, kw = dev(q)[:, :Hq * d], dict(window=window, sinks=sinks, max_q=max(nq))
+    _, z = run_attend(fg, t, q_off, Hq, pool, table, lens, scale, **kw)
+    acc = torch.full((len(lens), H, max(lens)), 9.0, device="cuda")
+    fg.fg_attn_weights_q4_paged(t, i32(q_off), Hq, pool, dev(table), i32(lens), scale, z, None, acc, **kw)
+    fg.fg_check_device_error()
+    streamed = G <= 8 and max(nq) == 1
+    for b, n in enumerate(lens):
+        if nq[b] == 0:
+            continue
+        ok = OP.seen(n - nq[b], nq[b], n, window, sinks)
+        for hk in range(H):
+            kk = rows_of(k, table, b, n)[hk].astype(np.float64)
+            qq = q[q_off[b]:q_off[b + 1], hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d)
+            mag = np.einsum("rgd,td->rgt", np.abs(qq.astype(np.float64)), np.abs(kk)) * scale
+            mag = np.where(ok[:, None], mag, 0).max(-1)
+            _, lse, _ = OP.attend(qq, kk, kk, ok, scale)
+            off = 2 * mag * (d + 40) * F32 + np.abs(lse) * 8 * F32 + (n + 64) * F32 + 2.0 ** -20 \
+                + 2.0 ** -21 + (mag * H16 + 2.0 ** -20 if streamed else 0)
+            got = host(acc)[b, hk, :n].astype(np.float64).sum()
+            want = ok.any(1).sum() * G
+            tol = np.expm1(off).sum() + want * (nq[b] * G + 8) * F32
+            assert abs(got - want) <= tol, (b, hk, got, want, tol)
