@@ -11,7 +11,7 @@ namespace {
 using namespace decode_window;
 
 struct Regions {
-  static constexpr bool kLse = false;
+  static constexpr bool kLse = false, kRestored = false;
   fg_kvcache kv;
   const int32_t* lens;
   int B, H;
@@ -34,7 +34,7 @@ struct Regions {
   }
   template <int D>
   __device__ __forceinline__ void copy(Run& r, int tiles, uint32_t slot, uint32_t bar) const {
-    using R = Ring<D>;
+    using R = Ring<D, false>;
     constexpr int NG = D / 64;
     const uint32_t rows = tiles * kTilePos;            // whole tiles: never past cap
     if ((threadIdx.x & 31) == 0) {
@@ -53,8 +53,8 @@ struct Regions {
 }  // namespace
 
 size_t decode_attn_window_ws_bytes(const fg_kvcache& kv, int32_t Hq) {
-  const int G = Hq / kv.H, heads = set_heads(G);
-  return workspace_bytes((int64_t)kv.B * kv.H * ((G + heads - 1) / heads), kv.cap, heads,
+  const int G = Hq / kv.H, heads = set_heads(G, false);
+  return workspace_bytes<false>((int64_t)kv.B * kv.H * ((G + heads - 1) / heads), kv.cap, heads,
                          kv.h / kv.H, kMaxSms);
 }
 
@@ -62,7 +62,7 @@ cudaError_t launch_decode_attn_window(const uint16_t* q, int64_t q_stride, int32
                                       const fg_kvcache& kv, const int32_t* lens, int32_t window,
                                       int32_t sinks, float scale, uint16_t* out,
                                       int64_t out_stride, void* ws, int nsm, cudaStream_t st) {
-  const int G = Hq / kv.H, heads = set_heads(G);
+  const int G = Hq / kv.H, heads = set_heads(G, false);
   Args a;
   a.q = q;
   a.out = out;

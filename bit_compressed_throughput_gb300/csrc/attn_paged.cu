@@ -1191,7 +1191,7 @@ size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
 
 // Single query rows with few heads go to the streaming kernels: alone where no sequence has more, and
 // ahead of the others where several sequences may be mixed.  (16 contexts of 9000 .. 32760, 8 K/V
-// heads: 84, 93 and 171 us there with 1, 4 and 8 query heads each, 292 us here with any.)
+// heads: 163 to 169 us there with 1 to 8 query heads each, 292 us here with any.)
 cudaError_t launch_attn_paged(const PagedAttn& call, int d, void* ws, int nsm, cudaStream_t st) {
   PagedAttn a = call;
   const int G = a.Hq / a.cache.H;

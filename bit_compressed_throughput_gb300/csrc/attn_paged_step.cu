@@ -2,11 +2,19 @@
 // attn_decode_window.cuh, for the sequences of a call that have one query row and at most
 // kStepHeads query heads per K/V head (attn_paged.cu has the others).
 //
-// With so few rows a key tile's restoring would cost the tensor-core kernel more than its bytes; here
-// the codes go into the products as they are, and the bytes are what counts.  The page table comes 32
-// entries at a time, a lane each, and a slot's four copies are issued by a lane each.  16 contexts of
-// 9000 .. 32,760, 8 K/V heads of 128 channels, 4 query heads each, 384 MB: 93 us, 4.1 TB/s; 84 us with
-// one query head each.
+// With so few rows most of a row tile of the tensor-core kernel would be empty; here up to 8 heads are
+// the columns of mma.sync products over values restored in registers, to the fp16 numbers that the
+// tensor-core kernel restores, too: a position counts the same for a token and for a piece.  The page
+// table comes 32 entries at a time, a lane each, and a slot's copies are issued by a lane each.
+//
+// Bound by instructions: 1450 for 32 positions of 128 channels, about 900 of them exact restoring, issued
+// in 66% of the cycles (as many again go to the two-register operands of packed arithmetic).  16 contexts
+// of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB: 163 us with 1 query head each, 166 us with 4,
+// 169 us with 8, 2.3 TB/s.  (Products over the codes as they are, weights times (b - a) / 15, took 84, 93
+// and 171 us, but K and V are not rounded to fp16 then: relative error 3.7e-4 .. 4.8e-4 of the outputs,
+// now 2.5e-4 .. 2.9e-4, 2.1e-4 of it their own rounding.  One fused multiply-add per value instead of the
+// format's two roundings: 5% faster, neighbours.  16 warps of 128 registers: 174 us with slots of 2
+// tiles.)
 #include "attn_decode_window.cuh"
 #include "paged.cuh"
 
@@ -19,7 +27,7 @@ namespace {
 using namespace decode_window;
 
 struct Pages {
-  static constexpr bool kLse = true;
+  static constexpr bool kLse = true, kRestored = true;
   PagedCache pc;
   const int32_t *q_off, *lens;
   int q_rows, max_q;
@@ -52,49 +60,46 @@ struct Pages {
     r.pos = pos;
     load(r);
   }
-  // A lane per copy: K codes, V codes, K and V statistics of each tile, or of both where they lie in
-  // one page.
+  // A lane per copy: K codes, V codes, K and V statistics of the slot's tiles, those of one page at once.
   template <int D>
   __device__ __forceinline__ void copy(Run& r, int tiles, uint32_t slot, uint32_t bar) const {
-    using R = Ring<D>;
-    const int lane = threadIdx.x & 31;
+    using R = Ring<D, true>;
+    const int lane = threadIdx.x & 31, tile = lane >> 2, kind = lane & 3;  // 0, 1: codes of K, V
     if (((r.pos + (tiles - 1) * kTilePos) >> pc.lg) - r.page0 >= 32) load(r);
-    const int page = r.pos >> pc.lg, second = (r.pos + kTilePos) >> pc.lg;
-    const int32_t e0 = __shfl_sync(0xFFFFFFFFu, r.entry, page - r.page0);
-    const int32_t e1 = __shfl_sync(0xFFFFFFFFu, r.entry, tiles > 1 ? second - r.page0 : 0);
-    const bool ok0 = e0 >= 0 && e0 < pc.pages;
-    const bool ok1 = tiles > 1 && e1 >= 0 && e1 < pc.pages;
-    const bool joined = tiles > 1 && second == page;
-    if (lane == 0 && !(ok0 && (ok1 || tiles == 1))) atomicOr(&g_paged_step_error, kErrExtent);
-    // the slot was last read through the generic proxy; order that before the copies
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (lane == 0) mbar_expect_tx(bar, (ok0 + ok1) * kTilePos * 2 * (R::ROW_CODE + R::ROW_AB));
+    const int pos = r.pos + min(tile, tiles - 1) * kTilePos;
+    const int32_t e = __shfl_sync(0xFFFFFFFFu, r.entry, (pos >> pc.lg) - r.page0);
+    const bool ok = tile < tiles && e >= 0 && e < pc.pages;
+    const unsigned oks = __ballot_sync(0xFFFFFFFFu, ok);
+    if (lane == 0) {
+      if (__popc(oks) != 4 * tiles) atomicOr(&g_paged_step_error, kErrExtent);
+      // the slot was last read through the generic proxy; order that before the copies
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_expect_tx(bar, __popc(oks) * (kTilePos / 2) * (R::ROW_CODE + R::ROW_AB));
+    }
     __syncwarp();
-    const int tile = lane >> 2, kind = lane & 3;       // kind: 0, 1 codes of K, V; 2, 3 statistics
-    if (lane < 8 && (tile ? ok1 && !joined : ok0)) {
-      const int32_t e = tile ? e1 : e0;
-      const int64_t p = (r.pos + tile * kTilePos) & ((1 << pc.lg) - 1);
+    const int in_page = pos & ((1 << pc.lg) - 1);
+    if (ok && (tile == 0 || in_page == 0)) {           // the first of its page
       const uint8_t* src = pc.block((int64_t)e << pc.lg, r.hk, D) + (kind & 1) * pc.half_bytes(D);
-      const uint32_t rows = joined ? 2 * kTilePos : kTilePos;
+      const uint32_t rows = min((tiles - tile) * kTilePos, (1 << pc.lg) - in_page);
       if (kind < 2)
         bulk_copy(slot + (kind ? R::V_OFF : 0) + tile * kTilePos * R::ROW_CODE,
-                  src + p * R::ROW_CODE, rows * R::ROW_CODE, bar);
+                  src + in_page * R::ROW_CODE, rows * R::ROW_CODE, bar);
       else
         bulk_copy(slot + (kind == 3 ? R::VAB_OFF : R::KAB_OFF) + tile * kTilePos * R::ROW_AB,
-                  src + ((int64_t)R::ROW_CODE << pc.lg) + p * R::ROW_AB, rows * R::ROW_AB, bar);
+                  src + ((int64_t)R::ROW_CODE << pc.lg) + in_page * R::ROW_AB, rows * R::ROW_AB, bar);
     }
     r.pos += tiles * kTilePos;
   }
 };
 
-int sets_of(int G) { return (G + set_heads(G) - 1) / set_heads(G); }
+int sets_of(int G) { return (G + set_heads(G, true) - 1) / set_heads(G, true); }
 
 }  // namespace
 
 size_t attn_paged_step_ws_bytes(const fg_kvpages& kv, int32_t Hq) {
   const int G = Hq / kv.H;
   // any number of sequences, of any length: as many shares as the largest grid has warps
-  return workspace_bytes(1 << 20, 1 << 20, set_heads(G), kv.h / kv.H, kMaxSms);
+  return workspace_bytes<true>(1 << 20, 1 << 20, set_heads(G, true), kv.h / kv.H, kMaxSms);
 }
 
 cudaError_t launch_attn_paged_step(const PagedAttn& a, int d, void* ws, int nsm, cudaStream_t st) {

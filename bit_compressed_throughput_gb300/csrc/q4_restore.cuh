@@ -79,4 +79,43 @@ struct GroupFp16 {
   }
 };
 
+// Two positions' values side by side: a word whose halves hold four codes of either position, as a
+// transposition of 8 positions' code words leaves them, gives four pairs (of channel i: both positions).
+static __device__ __noinline__ uint4 restore_pairs_exact(uint32_t codes, uint32_t ab0, uint32_t ab1) {
+  const float2 x = unpack_h2(ab0), y = unpack_h2(ab1);
+  const float sx = __fdiv_rn(__fsub_rn(x.y, x.x), 15.0f), sy = __fdiv_rn(__fsub_rn(y.y, y.x), 15.0f);
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_h2(__fadd_rn(x.x, __fmul_rn((float)((codes >> (4 * i)) & 0xFu), sx)),
+                   __fadd_rn(y.x, __fmul_rn((float)((codes >> (16 + 4 * i)) & 0xFu), sy)));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+struct PairsFp16 {
+  uint64_t a2, s2, c2;
+  bool plain;                              // the statistics are finite
+  __device__ __forceinline__ PairsFp16(uint32_t ab0, uint32_t ab1) {
+    const float2 x = unpack_h2(ab0), y = unpack_h2(ab1);
+    const float sx = div15(__fsub_rn(x.y, x.x)), sy = div15(__fsub_rn(y.y, y.x));
+    a2 = q4_pack2(x.x, y.x);
+    s2 = q4_pack2(sx, sy);
+    c2 = q4_pack2(-8388608.0f * sx, -8388608.0f * sy);
+    plain = sx < INFINITY && sy < INFINITY;
+  }
+  __device__ __forceinline__ uint4 restore(uint32_t codes) const {
+    const uint32_t ev = codes & 0x0F0F0F0Fu, od = (codes >> 4) & 0x0F0F0F0Fu;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i & 1 ? od : ev;
+      const float lo = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + (i >> 1)));
+      const float hi = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442 + (i >> 1)));
+      float x, y;
+      q4_unpack2(q4_add2(a2, q4_fma2(q4_pack2(lo, hi), s2, c2)), x, y);
+      o[i] = pack_h2(x, y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
+
 }  // namespace fg

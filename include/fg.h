@@ -285,9 +285,7 @@ int fg_kv_read_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t tabl
  *   out[row][hq*d + j] = sum_t softmax_t(scale * q_row,hq . K^_hk,t) V^_hk,t,j   over the visible t
  * (visible: as stated below for the windowed calls), hk = hq / (Hq / H), Hq a multiple of H, at
  * most 128 times H, nseq * Hq * (table_stride * page / 16 + 2) at most 2^40.  K^ and V^ are the
- * codes' a + q (b - a)/15: unrounded where single tokens of up to 8 heads per K/V head are streamed
- * (max_q is 1, or there are several sequences), else the fp16 values that fg_kv_read_q4_paged gives.
- * A row that sees nothing gets 0.
+ * fp16 values that fg_kv_read_q4_paged gives.  A row that sees nothing gets 0.
  * lse (nullable): device fp32 [q_rows][Hq], the logarithm of the row's sum of exp(score), -inf for
  * a row that sees nothing.  q, out: device fp16, q_rows rows q_stride and out_stride elements apart
  * (>= Hq*d, multiples of 8); out may be q with the same stride; any other overlap of q, out and lse

@@ -161,8 +161,7 @@ def test_rows_without_a_log_sum_exp_add_nothing(fg, d, H, G, lens, nq, bad):
 def test_every_row_hands_out_a_weight_of_one(fg, d, H, G, lens, nq, window, sinks):
     """The received weights with the log-sum-exp that the attention gave: each row and head hands out 1.
     Either call's scores miss theirs by d + 40 binary32 operations on sum |q_j k_j| at most; the
-    log-sum-exp and the exponential as in check_attend and test_weights.  Streamed single tokens take K^
-    unrounded, half a step of fp16 from the value that the weights take."""
+    log-sum-exp and the exponential as in check_attend and test_weights."""
     P, Hq, scale = 32, H * G, 1.0 / math.sqrt(d)
     table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 83 + d, G)
     t, kw = dev(q)[:, :Hq * d], dict(window=window, sinks=sinks, max_q=max(nq))
@@ -170,7 +169,6 @@ def test_every_row_hands_out_a_weight_of_one(fg, d, H, G, lens, nq, window, sink
     acc = torch.full((len(lens), H, max(lens)), 9.0, device="cuda")
     fg.fg_attn_weights_q4_paged(t, i32(q_off), Hq, pool, dev(table), i32(lens), scale, z, None, acc, **kw)
     fg.fg_check_device_error()
-    streamed = G <= 8 and max(nq) == 1
     for b, n in enumerate(lens):
         if nq[b] == 0:
             continue
@@ -182,7 +180,7 @@ def test_every_row_hands_out_a_weight_of_one(fg, d, H, G, lens, nq, window, sink
             mag = np.where(ok[:, None], mag, 0).max(-1)
             _, lse, _ = OP.attend(qq, kk, kk, ok, scale)
             off = 2 * mag * (d + 40) * F32 + np.abs(lse) * 8 * F32 + (n + 64) * F32 + 2.0 ** -20 \
-                + 2.0 ** -21 + (mag * H16 + 2.0 ** -20 if streamed else 0)
+                + 2.0 ** -21
             got = host(acc)[b, hk, :n].astype(np.float64).sum()
             want = ok.any(1).sum() * G
             tol = np.expm1(off).sum() + want * (nq[b] * G + 8) * F32

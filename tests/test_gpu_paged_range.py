@@ -1,14 +1,14 @@
-"""Attention over pages over the range of what the 4-bit format holds: K^ and V^ of pieces are the
-format's values bit for bit, and small and large groups lose nothing that the arithmetic does not say."""
+"""Attention over pages over the range of what the 4-bit format holds: K^ and V^ are the format's values
+bit for bit, and small and large groups lose nothing that the arithmetic does not say."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
-import fg_synth
 from oracle import paged as OP
-from paged_util import F32, H16, rows_of
+from oracle import quant as OQ
+from paged_util import F32, H16, offsets, rows_of
 from parity_util import dev, host, lib
 from test_gpu_paged import paged_case, run_attend
 
@@ -22,19 +22,28 @@ def fg():
     return lib()
 
 
+def batch(n, single):
+    """Every position of one page table row as a query: a prompt of n, or n single tokens that share its
+    pages."""
+    return (list(range(1, n + 1)), [1] * n) if single else ([n], [n])
+
+
 @pytest.mark.parametrize("scale", SCALES)
-@pytest.mark.parametrize("d,G,P", [(64, 1, 16), (128, 4, 64), (64, 9, 256)])
-def test_pieces_take_the_formats_values(fg, scale, d, G, P):
+@pytest.mark.parametrize("d,G,P", [(64, 1, 16), (128, 4, 64), (64, 9, 256), (128, 7, 32)])
+@pytest.mark.parametrize("single", [False, True])
+def test_attention_takes_the_formats_values(fg, scale, d, G, P, single):
     """A window of one position: a row's output is that position's V^, its weight 1 (2^7 before the sum,
     2^7, divides it), and with a query of one channel its log-sum-exp is that of K^."""
     n, H = 300, 2
     table, pool, k, v, q_off, q = paged_case(fg, d, H, P, [n], [n], 3 + d, G, scale=scale)
+    lens, nq = batch(n, single)
     q[:] = 0
     ch = (np.arange(n)[:, None] * 7 + np.arange(H * G)[None]) % d
     rows = np.arange(n)[:, None]
     q[q_off[0] + rows, np.arange(H * G) * d + ch] = 1.0
     a = 1.0 / scale
-    out, z = run_attend(fg, dev(q)[:, :H * G * d], q_off, H * G, pool, table, [n], a, window=1)
+    out, z = run_attend(fg, dev(q)[:, :H * G * d], offsets(nq, q_off[0]), H * G, pool,
+                        np.repeat(table, len(nq), 0), lens, a, window=1, max_q=max(nq))
     fg.fg_check_device_error()
     live = slice(q_off[0], q_off[1])
     got, z = host(out)[live].reshape(n, H, G, d), host(z)[live].astype(np.float64)
@@ -42,9 +51,35 @@ def test_pieces_take_the_formats_values(fg, scale, d, G, P):
         np.moveaxis(rows_of(v, table, 0, n), 0, 1)[:, :, None], got.shape))
     kk = rows_of(k, table, 0, n).astype(np.float64)                    # [H][n][d]
     want = a * kk[np.arange(H * G) // G, rows, ch]
-    # seven binary32 roundings (the scale, twice, the score, its shifts by 7 and back, log2, ln 2) of
-    # numbers of |want| / ln 2 + 7 at most, half a step each, log2 one; times 2
+    # nine binary32 roundings (the scale, twice, the score, its shifts by 7 and by the maximum and back,
+    # log2, ln 2) of numbers of |want| / ln 2 + 7 at most, half a step each, the exponential and log2
+    # one or two: 16 halves
     assert np.all(np.abs(z - want) <= 16 * 2.0 ** -24 * (np.abs(want) * 1.5 + 7))
+
+
+@pytest.mark.parametrize("d,G,P", [(64, 1, 16), (128, 4, 64), (64, 9, 256), (128, 8, 32)])
+@pytest.mark.parametrize("single", [False, True])
+def test_infinite_statistics(fg, d, G, P, single):
+    """Infinities and NaN of V^ where the format has them (codes of 0 among them), and in no other row."""
+    n, H = 200, 1
+    table, pool, k, v, q_off, q = paged_case(fg, d, H, P, [n], [n], 9 + d, G)
+    lens, nq = batch(n, single)
+    codes, ab = (host(x).copy() for x in pool.parts()[2:])
+    at = np.arange(0, n, 7)
+    for i, p in enumerate(at):
+        word = [(1.0, np.inf), (-np.inf, 2.0), (np.nan, 1.0), (0.5, np.nan), (-np.inf, np.inf)][i % 5]
+        ab[table[0, p // P], 0, p % P, i % (d // 64)] = word
+    pool.parts()[3].copy_(torch.from_numpy(ab))
+    with np.errstate(invalid="ignore"):
+        c = np.stack([codes & 15, codes >> 4], -1).reshape(-1, d)
+        vals = OQ.dequant_g64(c, *(ab.reshape(-1, d // 64, 2)[..., i] for i in (0, 1)))
+    want = rows_of(vals.reshape(ab.shape[0], H, P, d), table, 0, n)[0]
+    out, _ = run_attend(fg, dev(q)[:, :G * d], offsets(nq, q_off[0]), G, pool,
+                        np.repeat(table, len(nq), 0), lens, 0.125, window=1, max_q=max(nq))
+    fg.fg_check_device_error()
+    got = host(out)[q_off[0]:q_off[1]].reshape(n, G, d)
+    assert not np.isfinite(want[at]).all(1).any() and np.isposinf(want).any()
+    assert np.array_equal(got, np.broadcast_to(want[:, None], got.shape), equal_nan=True)
 
 
 @pytest.mark.parametrize("scale", SCALES)
@@ -58,13 +93,9 @@ def test_pieces_take_the_formats_values(fg, scale, d, G, P):
     (64, 1, 7, 16, [700, 77], [1, 1], 0, 0),
 ])
 def test_attention_over_the_range_of_values(fg, scale, d, H, G, P, lens, nq, window, sinks):
-    """As check_attend's bound, without an error of K^ and V^ in pieces.  Single tokens take them
-    unrounded: half a step of fp16 (2^-25 where it is subnormal) from the rounded ones, and with more
-    than two heads the remainder of a weight's rounding counts at the codes' middle: 7.5 (b - a)/15 is
-    at most the larger of |a| and |b|."""
+    """As check_attend's bound, without an error of K^ and V^."""
     table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 5 + d + G, G, scale=scale)
     a = 1.0 / (math.sqrt(d) * scale)
-    single = max(nq) == 1 and G <= 8
     out, z = run_attend(fg, dev(q)[:, :H * G * d], q_off, H * G, pool, table, lens, a, max_q=max(nq),
                         window=window, sinks=sinks)
     fg.fg_check_device_error()
@@ -77,13 +108,10 @@ def test_attention_over_the_range_of_values(fg, scale, d, H, G, P, lens, nq, win
             qq = q[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d)
             o, lse, p = OP.attend(qq, kk, vv, ok, a)
             aq = np.abs(qq.astype(np.float64))
-            dk, dv = (H16 * np.abs(x) + 2.0 ** -25 if single else np.zeros_like(x) for x in (kk, vv))
-            if single and G > 2:
-                dv = dv + H16 * rows_of(v.big, table, b, n)[hk]
-            moved = np.einsum("rgd,td->rgt", aq, np.abs(kk) * (d + 40) * F32 + dk) * a
+            moved = np.einsum("rgd,td->rgt", aq, np.abs(kk) * (d + 40) * F32) * a
             ds = np.where(ok[:, None], moved, 0).max(-1)
             V = p @ np.abs(vv)
-            tol = ((np.expm1(2 * ds)[..., None] + H16 + 2.0 ** -21 + (n + 64) * F32) * V + p @ dv
+            tol = ((np.expm1(2 * ds)[..., None] + H16 + 2.0 ** -21 + (n + 64) * F32) * V
                    + n * 2.0 ** -31 * np.abs(vv).max(0) + H16 * np.abs(o) + 2.0 ** -25)
             err = np.abs(got[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d) - o)
             assert np.all(err <= tol), (b, hk, float((err / tol).max()))
