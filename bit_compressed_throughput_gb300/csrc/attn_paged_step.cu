@@ -8,9 +8,8 @@
 // table comes 32 entries at a time, a lane each, and a slot's copies are issued by a lane each.
 //
 // Bound by instructions: 1450 for 32 positions of 128 channels, about 900 of them exact restoring, issued
-// in 66% of the cycles (as many again go to the two-register operands of packed arithmetic).  16 contexts
-// of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB: 163 us with 1 query head each, 166 us with 4,
-// 169 us with 8, 2.3 TB/s.  (Products over the codes as they are, weights times (b - a) / 15, took 84, 93
+// in 66% of the cycles.  16 contexts of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB: 163 us with 1
+// query head each, 166 us with 4, 169 us with 8, 2.3 TB/s.  (Products over the codes as they are, weights times (b - a) / 15, took 84, 93
 // and 171 us, but K and V are not rounded to fp16 then: relative error 3.7e-4 .. 4.8e-4 of the outputs,
 // now 2.5e-4 .. 2.9e-4, 2.1e-4 of it their own rounding.  One fused multiply-add per value instead of the
 // format's two roundings: 5% faster, neighbours.  16 warps of 128 registers: 174 us with slots of 2

@@ -21,8 +21,8 @@
 // d per position); with many, the exponentials beside it, one per pair.  The last 64 tokens of 8 prompts
 // of 8001 .. 16,001 positions, 32 query heads over 8, 196 million pairs: 95 us (126 us with 20 warps of
 // 96 registers, whose exponentials took three times the instructions; 3 us are the test for rows of
-// log-sum-exp -inf with infinities or NaN in their scores); the restoring warps work 98,000 of 160,000
-// cycles.
+// log-sum-exp -inf with infinities or NaN in their scores); the restoring warps work 98,000 cycles of a
+// CTA's time.
 #include <math.h>
 
 #include <algorithm>

@@ -10,7 +10,7 @@
 //
 // Work: blocks of 256 positions of one K/V head in one order, cut evenly among the CTAs; a warp takes
 // 32 positions of a block, and copies those of the next one into shared memory meanwhile.
-// Bound by instructions: 25 for every 8 codes of exact restoring are 400 of the 1000 that a warp takes
+// Bound by instructions: 25 for every 8 codes of exact restoring are 400 of the 1150 that a warp takes
 // for 32 positions of 128 channels, the turns, copies and sums around them the rest; then by HBM
 // (0.5625 d bytes a position).  One token of 32 sequences of 2000 .. 4096 positions, 8 K/V heads, 4
 // query heads each, 62 MB: 36 us, 1.7 TB/s (39 us with the codes loaded into registers as they are
