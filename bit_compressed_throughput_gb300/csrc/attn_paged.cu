@@ -34,6 +34,7 @@
 // than it hides: 795 us, and 382 us instead of 259 us where blocks have one row tile.  Restoring in
 // code unrolled for K, V and tails: 755 us.  Moving registers between the warps' roles: no gain.)
 //
+// The products' additions truncate: 65,536 positions in one share, of values of one sign, lose 2e-4.
 // Masked positions have P = 0, but 0 times an infinity or NaN in V is NaN: rows that end with one
 // are computed again over what they see alone (attend_row).  Rows whose sum of weights is NaN have
 // their answer.

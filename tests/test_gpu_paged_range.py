@@ -8,7 +8,7 @@ import torch
 
 from oracle import paged as OP
 from oracle import quant as OQ
-from paged_util import F32, H16, offsets, rows_of
+from paged_util import F32, H16, i32, offsets, rows_of
 from parity_util import dev, host, lib
 from test_gpu_paged import paged_case, run_attend
 
@@ -117,3 +117,40 @@ def test_attention_over_the_range_of_values(fg, scale, d, H, G, P, lens, nq, win
             assert np.all(err <= tol), (b, hk, float((err / tol).max()))
             zt = 2 * ds + 2.0 ** -20 + (n + 64) * F32 + np.abs(lse) * 4 * F32
             assert np.all(np.abs(z[r, hk * G:(hk + 1) * G] - lse) <= zt), (b, hk)
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4)])
+def test_sums_do_not_lose_with_the_length(fg, d, G):
+    """65,536 positions of values around 2 that one warp adds up: the outputs' errors have no common
+    direction.  A rounding of an output is half a step at most, either way; 1500 of them that agree in
+    no direction lie within 0.17 half steps on average (Hoeffding's bound, one in 10^9), and the weights'
+    errors, of 65,536 each, within less; 128 truncated additions before a sum is moved lose 2^-23 of it
+    each, and 32 rounded ones 2^-24: together less than 0.3 half steps."""
+    H, P, n = 8, 64, 65536
+    warps = 16 if d == 64 else 12
+    B = torch.cuda.get_device_properties(0).multi_processor_count * warps // H
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(d)
+    pool = fg.KVPagesQ4(n // P, P, H * d, H)
+    for codes, ab, mid in zip(pool.parts()[0::2], pool.parts()[1::2], (0.0, 2.0)):
+        codes.copy_(torch.randint(0, 256, codes.shape, generator=gen, device="cuda", dtype=torch.uint8))
+        half = 1.0 + torch.rand(ab.shape[:-1], generator=gen, device="cuda")
+        ab.copy_(torch.stack((mid - half, mid + half), -1))
+    order = torch.randperm(n // P, generator=gen, device="cuda").int()
+    table = order.expand(B, -1).contiguous()
+    q = torch.randn((B, H * G * d), generator=gen, device="cuda").half()
+    scale = 1.0 / math.sqrt(d)
+    out, z = run_attend(fg, q, list(range(B + 1)), H * G, pool, host(table), [n] * B, scale, max_q=1)
+    fg.fg_check_device_error()
+    at = i32([0, n]), i32([0])
+    kv = torch.empty((n, 2 * H * d), dtype=torch.float16, device="cuda")
+    fg.fg_kv_read_q4_paged(pool, table[:1].contiguous(), *at, kv[:, :H * d], kv[:, H * d:])
+    k, v = (x.double().view(n, H, d).transpose(0, 1) for x in (kv[:, :H * d], kv[:, H * d:]))
+    rel = []
+    for b in (0, B // 2, B - 1):
+        s = q[b].double().view(H, G, d) @ k.mT * scale
+        o = torch.softmax(s, -1) @ v
+        rel.append(((out[b].double().view(H, G, d) - o) / o.abs()).flatten())
+        assert (torch.logsumexp(s, -1).flatten() - z[b]).abs().max() <= 2.0 ** -16
+    rel = torch.cat(rel)
+    assert rel.abs().max() <= 4 * H16 and rel.mean().abs() <= 0.3 * H16
