@@ -800,6 +800,11 @@ static int check_rope(const fg_rope_rows* r, int d) {
 static RowSet array_at(const void* p, int64_t bytes) {
   return RowSet{reinterpret_cast<uint64_t>(p), p && bytes > 0 ? 1 : 0, bytes, bytes};
 }
+// The same of 32-bit words, a row per (sequence, head) side by side (all of them may pass 64 bits).
+constexpr int64_t kMaxAccStride = 1ll << 60;
+static RowSet words_at(const void* p, int64_t rows, int64_t words) {
+  return RowSet{reinterpret_cast<uint64_t>(p), p && words > 0 ? rows : 0, 4 * words, 4 * words};
+}
 static RopeRows rope_rows(const fg_rope_rows& r) {
   return RopeRows{r.angles, r.pos, r.positions, r.rot, r.interleaved != 0};
 }
@@ -1011,13 +1016,13 @@ int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows
   int rc = check_paged_attn(q, q_stride, q_rows, q_off, max_q, Hq, kv, table, table_stride, lens,
                             nseq, window, sinks, scale, &noop);
   if (rc) return rc;
-  if (acc_stride < 0) return FG_ERR_SHAPE;
+  if (acc_stride < 0 || acc_stride >= kMaxAccStride) return FG_ERR_SHAPE;
   if (noop) return FG_OK;
   if ((q_rows > 0 && (!lse || !aligned4(lse))) || !acc_out || !aligned4(acc_out) || !aligned4(acc))
     return FG_ERR_ARG;
-  const int64_t acc_bytes = 4 * acc_stride * nseq * kv->H;
-  const RowSet acc_at = array_at(acc_out, acc_bytes);
-  if ((acc != acc_out && rows_overlap(acc_at, array_at(acc, acc_bytes))) ||
+  const int64_t sums = (int64_t)nseq * kv->H;
+  const RowSet acc_at = words_at(acc_out, sums, acc_stride);
+  if ((acc != acc_out && rows_overlap(acc_at, words_at(acc, sums, acc_stride))) ||
       rows_overlap(acc_at, array_at(lse, 4ll * q_rows * Hq)) ||
       rows_overlap(acc_at, fp16_rows(q, q_rows, q_stride, (int64_t)Hq * (kv->h / kv->H))))
     return FG_ERR_ARG;
@@ -1056,7 +1061,9 @@ int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t tab
                          void* stream) {
   int rc = check_pages(kv, nseq, table_stride);
   if (rc || (rc = check_pages(kv, nseq, dst_stride))) return rc;
-  if (keep <= 0 || recent < 0 || recent > keep || acc_stride < 0) return FG_ERR_SHAPE;
+  if (keep <= 0 || recent < 0 || recent > keep || acc_stride < 0 ||
+      acc_stride >= kMaxAccStride)
+    return FG_ERR_SHAPE;
   if (keep > dst_stride * kv->page) return FG_ERR_CAPACITY;
   if (nseq == 0) return FG_OK;
   if (!pages_ok(kv, table) || !dst_table || !aligned4(dst_table) || !lens || !aligned4(lens) ||
@@ -1064,9 +1071,9 @@ int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t tab
       !dst_lens || !aligned4(dst_lens) || dst_table == table)
     return FG_ERR_ARG;
   const int64_t heads = (int64_t)nseq * kv->H;
-  const RowSet outs[] = {array_at(kept, 4 * heads * keep), array_at(acc_out, 4 * heads * keep),
+  const RowSet outs[] = {words_at(kept, heads, keep), words_at(acc_out, heads, keep),
                          array_at(dst_lens, 4ll * nseq)};
-  const RowSet ins[] = {array_at(acc, 4 * heads * acc_stride), array_at(lens, 4ll * nseq),
+  const RowSet ins[] = {words_at(acc, heads, acc_stride), array_at(lens, 4ll * nseq),
                         array_at(table, 4 * table_stride * nseq),
                         array_at(dst_table, 4 * dst_stride * nseq)};
   for (const RowSet& o : outs)

@@ -59,3 +59,27 @@ def test_evict(fg):
                dict(kept=0xA0000), dict(acc_out=0xB0000 + 28), dict(dl=0xB0000 + 28),
                dict(dl=0xA0000 - 4)):
         assert call(**kw) == fg.FG_ERR_ARG, kw
+
+
+def test_extents_past_64_bits(fg):
+    """Strides whose product with the sequences and heads passes 64 bits still cover what lies in them."""
+    kv = fg.fg_kvpages(0x1000000, 8, 32, 256, 2)
+    for stride in (1 << 46, 1 << 47, (1 << 60) - 1):
+
+        def weights(acc, lse):
+            return fg.lib.fg_attn_weights_q4_paged(Q, 512, 8, FAR, 4, 4, C.byref(kv), FAR, 4, FAR, 65535, 0,
+                                                   0, 0.1, lse, acc, OUT, stride, None)
+
+        assert weights(None, 0x7000000000) == fg.FG_ERR_ARG, hex(stride)
+        assert weights(0x7000000000, LSE) == fg.FG_ERR_ARG, hex(stride)
+
+        def evict(kept):
+            return fg.lib.fg_kv_evict_q4_paged(C.byref(kv), 0x9000, 4, 2, 0xB000, OUT, stride, 32, 8,
+                                               0xA000, 4, kept, 0x8000, 0x6000, None)
+
+        assert evict(0x7000000000) == fg.FG_ERR_ARG, hex(stride)
+    # rows that no address space holds
+    assert fg.lib.fg_attn_weights_q4_paged(Q, 512, 8, FAR, 4, 4, C.byref(kv), FAR, 4, FAR, 2, 0, 0, 0.1, LSE,
+                                           ACC, OUT, 1 << 61, None) == fg.FG_ERR_SHAPE
+    assert fg.lib.fg_kv_evict_q4_paged(C.byref(kv), 0x9000, 4, 2, 0xB000, OUT, 1 << 61, 32, 8, 0xA000, 4,
+                                       0x7000, 0x8000, 0x6000, None) == fg.FG_ERR_SHAPE
