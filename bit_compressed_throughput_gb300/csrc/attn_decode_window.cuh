@@ -10,12 +10,12 @@
 //   sum_t p_t a_t,
 // so the products run on mma.sync m16n8k16 over the codes (exact fp16 subnormals, attn_q4.cuh) with
 // fp32 sums.  The work is bound by reading the visible part of the cache once.  k^ and v^ are not
-// rounded to fp16 then; where a cache asks for the format's rounded values (kRestored: the pages, whose
-// values the tensor-core kernels restore, too), they are restored before the products (RestoredSums),
-// and the work is bound by the instructions for that.
+// rounded to fp16 then; where a cache asks for the format's rounded values (kRestored: the pages,
+// whose values the tensor-core kernels restore, too), they are restored before the products
+// (RestoredSums), and the work is bound by the instructions for that.
 //
-// Columns over codes: the 8 columns of a product are (part, query head, group) with NP parts of HEADS = 4 / NP
-// query heads of one K/V head (for d = 64 the second column of a group pair repeats the first), so
+// Columns, over codes: the 8 columns of a product are (part, query head, group) with NP parts of HEADS
+// = 4 / NP query heads of one K/V head (for d = 64 the second column of a group pair repeats the first), so
 // lane (gid, tig) ends up with scores of head tig % HEADS.  A slot of 32 positions has four
 // 8-row halves of tiles; part tig / HEADS takes 4 / NP of them, so the softmax and the statistics
 // of a position are computed once per head: with one head per K/V head (NP = 4) a lane has one
@@ -32,8 +32,9 @@
 // depend on the order in which warps run.
 //
 // Memory pipeline, as in the dense decode attention: per warp a ring of slots (2 tiles of K and V
-// codes and statistics; 4 where they are restored), filled by bulk async copies that run ahead across row sets.  Every wait is
-// bounded; on timeout the warp sets the device error word, drains its copies and stops.
+// codes and statistics; 4 where they are restored), filled by bulk async copies that run ahead across
+// row sets.  Every wait is bounded; on timeout the warp sets the device error word, drains its copies
+// and stops.
 //
 // Measured (GB300, HBM copy 6.78 TB/s; calls one after another, bytes of the visible 4-bit K/V):
 //   128 sequences x 56 heads, 512 .. 1055 positions: 135 us, 0.89 of the copy rate.
@@ -97,8 +98,9 @@ __device__ __forceinline__ float to_scale(float t) {
 // KB = 17 MB, 2.4 us of its rate); with twice as much the SMs advance less evenly and the last ones
 // finish later (128 sequences of 784 positions, 56 heads: 173 us with 16 warps x 3 slots, 152 us
 // with 12 x 2; 64-channel heads, whose slots are half as large, 72 us with 16 x 3, 81 us with 12 x
-// 2).  Restored values take longer than their bytes, and slots of 4 tiles halve what a slot costs beside
-// them (16 contexts of 9000 .. 32760, 8 K/V heads: 173 us with 2 tiles, 166 us with 4).
+// 2).  Restored values take longer than their bytes, and slots of 4 tiles halve what a slot costs
+// beside them (16 contexts of 9000 .. 32760, 8 K/V heads: 173 us with 2 tiles, 166 us with 4 at that
+// stage).
 template <int D, bool RESTORED>
 struct Ring {
   static constexpr int WARPS = (D == 128) ? 12 : 16, DEPTH = (D == 128) ? 2 : 3;
@@ -268,8 +270,8 @@ __device__ __forceinline__ void load_q(const uint16_t* q_heads, int heads, int l
     f.Q[g] = __shfl_sync(0xFFFFFFFFu, qsum, 8 * (tig % HEADS) + 2 * g) * scale_log2;
 }
 
-// What a warp keeps of a row set while it goes through its positions, in products over the codes as they
-// are: queries, softmax, the values' sums.
+// What a warp keeps of a row set while it goes through its positions, in products over the codes as
+// they are: queries, softmax, the values' sums.
 template <int D, int HEADS>
 struct CodeSums {
   using R = Ring<D, false>;
@@ -589,7 +591,8 @@ struct RestoredSums {
       float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       {
         const uint8_t* k = slot + (row0 + gid) * R::ROW_CODE + tig * 4 * NW;
-        const uint8_t* ab = slot + R::KAB_OFF + (row0 + gid) * R::ROW_AB + (D == 128 ? 4 * (tig >> 1) : 0);
+        const uint8_t* ab = slot + R::KAB_OFF + (row0 + gid) * R::ROW_AB +
+                            (D == 128 ? 4 * (tig >> 1) : 0);
         uint32_t w0[NW], w1[NW], ab0[1], ab1[1];
         load_words<NW>(k, w0);
         load_words<NW>(k + 8 * R::ROW_CODE, w1);

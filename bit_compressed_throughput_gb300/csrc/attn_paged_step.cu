@@ -2,18 +2,18 @@
 // attn_decode_window.cuh, for the sequences of a call that have one query row and at most
 // kStepHeads query heads per K/V head (attn_paged.cu has the others).
 //
-// With so few rows most of a row tile of the tensor-core kernel would be empty; here up to 8 heads are
-// the columns of mma.sync products over values restored in registers, to the fp16 numbers that the
-// tensor-core kernel restores, too: a position counts the same for a token and for a piece.  The page
-// table comes 32 entries at a time, a lane each, and a slot's copies are issued by a lane each.
+// With so few rows most of a row tile of the tensor-core kernel would be empty; here up to 8 heads
+// are the columns of mma.sync products over values restored in registers, to the fp16 numbers that
+// the tensor-core kernel restores, too: a position counts the same for a token and for a piece.  The
+// page table comes 32 entries at a time, a lane each, and a slot's copies are issued by a lane each.
 //
-// Bound by instructions: 1450 for 32 positions of 128 channels, about 900 of them exact restoring, issued
-// in 66% of the cycles.  16 contexts of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB: 163 us with 1
-// query head each, 166 us with 4, 169 us with 8, 2.3 TB/s.  (Products over the codes as they are, weights times (b - a) / 15, took 84, 93
-// and 171 us, but K and V are not rounded to fp16 then: relative error 3.7e-4 .. 4.8e-4 of the outputs,
-// now 2.5e-4 .. 2.9e-4, 2.1e-4 of it their own rounding.  One fused multiply-add per value instead of the
-// format's two roundings: 5% faster, neighbours.  16 warps of 128 registers: 174 us with slots of 2
-// tiles.)
+// Bound by instructions: 1500 for 32 positions of 128 channels, about 900 of them exact restoring,
+// issued in 67% of the cycles.  16 contexts of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB:
+// 170 us with 1 or 4 query heads each, 174 us with 8, 2.3 TB/s.  (Products over the codes as they are,
+// weights times (b - a) / 15, took 84, 93 and 171 us, but K and V are not rounded to fp16 then:
+// relative error of the outputs 3.7e-4 .. 4.8e-4, now 2.5e-4 .. 2.9e-4, 2.1e-4 of it their own
+// rounding.  One fused multiply-add per value instead of the format's two roundings: 5% faster,
+// neighbours.  16 warps of 128 registers gained nothing.)
 #include "attn_decode_window.cuh"
 #include "paged.cuh"
 
@@ -59,7 +59,8 @@ struct Pages {
     r.pos = pos;
     load(r);
   }
-  // A lane per copy: K codes, V codes, K and V statistics of the slot's tiles, those of one page at once.
+  // A lane per copy: K codes, V codes, K and V statistics of the slot's tiles, those of one page at
+  // once.
   template <int D>
   __device__ __forceinline__ void copy(Run& r, int tiles, uint32_t slot, uint32_t bar) const {
     using R = Ring<D, true>;

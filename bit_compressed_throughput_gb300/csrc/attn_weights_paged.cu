@@ -88,8 +88,8 @@ constexpr int B_CFULL = 0, B_CFREE = MAX_PARTS, B_KFULL = 2 * MAX_PARTS, B_KFREE
               B_IFREE = B_IFULL + ITEMS, B_DRAIN = B_IFREE + ITEMS, NBARS = B_DRAIN + 1;
 static_assert(NBARS * 8 + 16 <= 512, "control space");
 
-// Columns of a row tile that a position adds up: all; those that see it; of those, the ones whose row has
-// a log-sum-exp.
+// Columns of a row tile that a position adds up: all; those that see it; of those, the ones whose row
+// has a log-sum-exp.
 enum { kAll, kSome, kHeard };
 template <int N>
 using Columns = std::integral_constant<int, N>;
@@ -702,7 +702,7 @@ cudaError_t launch_d(const PagedAttn& a, int nsm, cudaStream_t st) {
 
 // Sequences with few query rows go to the streaming kernel, the others here; a call whose rows are
 // known to be few launches that alone.  (One token of 32 sequences of 2000 .. 4096 positions, 8 K/V
-// heads: 36 us there with 1 to 8 query heads each and 50 us with 32, 71 us here with any.)
+// heads: 36 us there with 1 to 8 query heads each and 50 us with 32, 72 us here with any.)
 cudaError_t launch_attn_weights_paged(const PagedAttn& a, int d, int nsm, cudaStream_t st) {
   const cudaError_t e = launch_attn_weights_step(a, d, nsm, st);
   if (e != cudaSuccess || (int64_t)a.max_q * (a.Hq / a.cache.H) <= kStepRows) return e;

@@ -92,14 +92,13 @@ FG_HD int cut_slot(int w, int pieces, int i) {
 }
 
 // ---- Q buffers.  Chain 0 multiplies buffer 0, chain 1 buffer 1, or 0 too where a block has one row
-// tile; both wait for buffer 0 in every segment.  A buffer's use ends with two arrivals at its barrier.
-// Where a block has two row tiles one of buffer 0's is chain 1's, behind its wait: else the next
-// segment's rows could come while chain 1 has not passed that wait, which a parity cannot tell from the
-// phase before.
-FG_HD int q_given_at_once(int chain, bool single) { return chain == 1 && !single ? 1 : 0; }  // of buffer 0
-FG_HD int q_given_after_use(int chain, bool single) {           // of the buffer that the chain multiplies
-  return chain == 1 && !single ? 2 : 1;
-}
+// tile; both wait for buffer 0 in every segment.  A buffer's use ends with two arrivals at its
+// barrier.  Where a block has two row tiles one of buffer 0's is chain 1's, behind its wait: else the
+// next segment's rows could come while chain 1 has not passed that wait, which a parity cannot tell
+// from the phase before.  Arrivals at buffer 0's barrier behind the wait; at the barrier of the buffer
+// that the chain multiplies, after its last product:
+FG_HD int q_given_at_once(int chain, bool single) { return chain == 1 && !single ? 1 : 0; }
+FG_HD int q_given_after_use(int chain, bool single) { return chain == 1 && !single ? 2 : 1; }
 
 // Walks the segments of share [x0, x1) of the order.
 struct PagedWalk {

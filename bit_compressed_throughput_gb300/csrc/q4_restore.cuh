@@ -80,7 +80,8 @@ struct GroupFp16 {
 };
 
 // Two positions' values side by side: a word whose halves hold four codes of either position, as a
-// transposition of 8 positions' code words leaves them, gives four pairs (of channel i: both positions).
+// transposition of 8 positions' code words leaves them, gives four pairs (of channel i: both
+// positions).
 static __device__ __noinline__ uint4 restore_pairs_exact(uint32_t codes, uint32_t ab0, uint32_t ab1) {
   const float2 x = unpack_h2(ab0), y = unpack_h2(ab1);
   const float sx = __fdiv_rn(__fsub_rn(x.y, x.x), 15.0f), sy = __fdiv_rn(__fsub_rn(y.y, y.x), 15.0f);

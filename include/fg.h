@@ -329,8 +329,8 @@ int fg_attn_weights_q4_paged(const uint16_t* q, int64_t q_stride, int32_t q_rows
  * int32 [nseq][H][keep], the positions that stay, -1 behind them; acc_out: device fp32
  * [nseq][H][keep], their acc, 0 behind them; dst_lens: device int32 [nseq], min(lens[b], keep).
  * Heads keep different positions: a cached position no longer says when its token came, so later
- * rows give fg_kv_append_q4_paged a rope->pos of their own, and window and sinks of the attention count
- * cached positions, the ones that stayed, from then on.  keep <= dst_stride * page
+ * rows give fg_kv_append_q4_paged a rope->pos of their own, and the attention's window and sinks
+ * count cached positions, the ones that stayed, from then on.  keep <= dst_stride * page
  * (FG_ERR_CAPACITY).  acc as in fg_attn_weights_q4_paged.  kept, acc_out and dst_lens may overlap
  * neither one another nor acc, lens and the tables. */
 int fg_kv_evict_q4_paged(const fg_kvpages* kv, const int32_t* table, int64_t table_stride,
