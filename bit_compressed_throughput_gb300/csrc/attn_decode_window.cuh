@@ -540,8 +540,10 @@ struct CodeSums {
 // the rows of K Q^T and the columns of V^T P^T, up to 8 query heads the columns of both.  A lane (gid,
 // tig) has the scores of positions gid and gid + 8 of a tile for heads 2 tig and 2 tig + 1; of the
 // values it restores, for positions 2 tig, 2 tig + 1 (and 8 behind), the channels that a transposition
-// of the code words gives row gid.  Weights are rounded to fp16 once, after a scaling by 2^7 that lets
-// the reference maximum lag by 2^8 and keeps them normal down to 2^-21 of the largest.
+// of the code words gives row gid.  Weights are scaled by 2^7, which lets the reference maximum lag by
+// 2^8, and go into the products as two fp16 terms, so that their rounding does not show in the outputs
+// (relative error 2.9e-4, and up to 3.2e-4 where few weights count, with one; 2.1e-4, that of the
+// outputs' own rounding, with both; 5% of the time).
 template <int D, int HEADS>
 struct RestoredSums {
   using R = Ring<D, true>;
@@ -554,7 +556,7 @@ struct RestoredSums {
   float m[2], l[2], acc[2 * NW][4];        // heads 2 tig, 2 tig + 1
   // The products' additions truncate: sums of values of one sign lose 4e-4 over 65536 positions.  So
   // every kFlush slots they move to sums of binary32 additions, in local memory (volatile: with all in
-  // registers some are spilled, and 16 contexts of 9000 .. 32760 take 185 us, 171 us as it is, 166 us
+  // registers some are spilled, and 16 contexts of 9000 .. 32760 took 185 us, 171 us as it is, 166 us
   // without), relative to the maximum m_far.
   volatile float far[2 * NW][4];
   float m_far[2];
@@ -646,7 +648,7 @@ struct RestoredSums {
         }
       }
       // ---- weights
-      uint32_t b[2];
+      uint32_t b[2], rest[2];
       {
         const float z0 = kPExp - (m[0] == -INFINITY ? 0.0f : m[0]);
         const float z1 = kPExp - (m[1] == -INFINITY ? 0.0f : m[1]);
@@ -655,7 +657,10 @@ struct RestoredSums {
           const float p0 = ex2(fmaf(c[2 * r], sl2, z0)), p1 = ex2(fmaf(c[2 * r + 1], sl2, z1));
           l[0] += p0;
           l[1] += p1;
-          b[r] = movtrans(pack_h2(p0, p1));
+          const uint32_t h = pack_h2(p0, p1);
+          const float2 x = unpack_h2(h);
+          b[r] = movtrans(h);
+          rest[r] = movtrans(pack_h2(p0 - x.x, p1 - x.y));
         }
       }
       // ---- values
@@ -698,6 +703,10 @@ struct RestoredSums {
           const int u = 2 * (w + i);
           mma16816(acc[u], x[i].x, x[i].y, y[i].x, y[i].y, b[0], b[1]);
           mma16816(acc[u + 1], x[i].z, x[i].w, y[i].z, y[i].w, b[0], b[1]);
+          if (plain) {                     // (0 or less times an infinity: NaN)
+            mma16816(acc[u], x[i].x, x[i].y, y[i].x, y[i].y, rest[0], rest[1]);
+            mma16816(acc[u + 1], x[i].z, x[i].w, y[i].z, y[i].w, rest[0], rest[1]);
+          }
         }
       }
     }

@@ -1192,7 +1192,7 @@ size_t attn_paged_ws_bytes(const fg_kvpages& kv, int32_t Hq, int32_t max_q) {
 
 // Single query rows with few heads go to the streaming kernels: alone where no sequence has more, and
 // ahead of the others where several sequences may be mixed.  (16 contexts of 9000 .. 32760, 8 K/V
-// heads: 170 to 174 us there with 1 to 8 query heads each, 290 us here with any.)
+// heads: 178 to 182 us there with 1 to 8 query heads each, 290 us here with any.)
 cudaError_t launch_attn_paged(const PagedAttn& call, int d, void* ws, int nsm, cudaStream_t st) {
   PagedAttn a = call;
   const int G = a.Hq / a.cache.H;

@@ -7,13 +7,12 @@
 // the tensor-core kernel restores, too: a position counts the same for a token and for a piece.  The
 // page table comes 32 entries at a time, a lane each, and a slot's copies are issued by a lane each.
 //
-// Bound by instructions: 1500 for 32 positions of 128 channels, about 900 of them exact restoring,
-// issued in 67% of the cycles.  16 contexts of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB:
-// 170 us with 1 or 4 query heads each, 174 us with 8, 2.3 TB/s.  (Products over the codes as they are,
-// weights times (b - a) / 15, took 84, 93 and 171 us, but K and V are not rounded to fp16 then:
-// relative error of the outputs 3.7e-4 .. 4.8e-4, now 2.5e-4 .. 2.9e-4, 2.1e-4 of it their own
-// rounding.  One fused multiply-add per value instead of the format's two roundings: 5% faster,
-// neighbours.  16 warps of 128 registers gained nothing.)
+// Bound by instructions: 1570 for 32 positions of 128 channels, about 900 of them exact restoring.  16
+// contexts of 9000 .. 32,760, 8 K/V heads of 128 channels, 384 MB: 178 us with 1 or 4 query heads each,
+// 182 us with 8, 2.2 TB/s.  (Products over the codes as they are, weights times (b - a) / 15, took 84,
+// 93 and 171 us, but K and V are not rounded to fp16 then: relative error of the outputs 3.7e-4 ..
+// 4.8e-4, now 2.1e-4, their own rounding.  One fused multiply-add per value instead of the format's two
+// roundings: 5% faster, neighbours.  16 warps of 128 registers gained nothing.)
 #include "attn_decode_window.cuh"
 #include "paged.cuh"
 

@@ -93,7 +93,8 @@ def test_infinite_statistics(fg, d, G, P, single):
     (64, 1, 7, 16, [700, 77], [1, 1], 0, 0),
 ])
 def test_attention_over_the_range_of_values(fg, scale, d, H, G, P, lens, nq, window, sinks):
-    """As check_attend's bound, without an error of K^ and V^."""
+    """As check_attend's bound, without an error of K^ and V^.  The weights of streamed single tokens are
+    two fp16 terms: 2^-22 of a weight."""
     table, pool, k, v, q_off, q = paged_case(fg, d, H, P, lens, nq, 5 + d + G, G, scale=scale)
     a = 1.0 / (math.sqrt(d) * scale)
     out, z = run_attend(fg, dev(q)[:, :H * G * d], q_off, H * G, pool, table, lens, a, max_q=max(nq),
@@ -111,7 +112,8 @@ def test_attention_over_the_range_of_values(fg, scale, d, H, G, P, lens, nq, win
             moved = np.einsum("rgd,td->rgt", aq, np.abs(kk) * (d + 40) * F32) * a
             ds = np.where(ok[:, None], moved, 0).max(-1)
             V = p @ np.abs(vv)
-            tol = ((np.expm1(2 * ds)[..., None] + H16 + 2.0 ** -21 + (n + 64) * F32) * V
+            rounded = 2.0 ** -22 if max(nq) == 1 and G <= 8 else H16
+            tol = ((np.expm1(2 * ds)[..., None] + rounded + 2.0 ** -21 + (n + 64) * F32) * V
                    + n * 2.0 ** -31 * np.abs(vv).max(0) + H16 * np.abs(o) + 2.0 ** -25)
             err = np.abs(got[r, hk * G * d:(hk + 1) * G * d].reshape(nq[b], G, d) - o)
             assert np.all(err <= tol), (b, hk, float((err / tol).max()))
